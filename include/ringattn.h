@@ -332,6 +332,116 @@ int ringattn_merge(float* o_run, float* lse_run, const float* o_part, const floa
                    long long rows, int d, ra_stream_t stream);
 
 /*
+ * The paged K/V cache: ringattn_cache_append, ringattn_cache_read, ringattn_fwd_paged.
+ *
+ * What follows a prompt that the ring has prefilled: its K and V are kept in pages of a pool,
+ * new tokens (the next chunk of a prompt, or one token of every sequence) append theirs and
+ * attend over what is kept.  These entry points have no chunk map and no alignment of lengths:
+ * a sequence has any length from 0 up, and the batch is ragged.
+ *
+ * Pool: k, v are [n_pages, Hkv, page_size, d], bf16 (dtype 0) or e4m3 (dtype 1, one byte an
+ *   element); page p starts k_page_stride (v_page_stride) elements after page p - 1, the rest is
+ *   contiguous.  An e4m3 pool has one fp32 scale a row: k_scale, v_scale [n_pages, Hkv,
+ *   page_size], pages k_scale_page_stride (v_scale_page_stride) apart; a row's value is code *
+ *   scale.  ringattn_cache_append writes scales that are powers of two, which every reader
+ *   applies exactly; with other positive scales the reader's products round to bf16.  The NaN
+ *   codes 0x7f and 0xff are not used (a row that has no scale, because it held an infinity
+ *   or a NaN, is zeros with the scale NaN, and reads as NaN); what they read as in a pool
+ *   written by other means is unspecified.
+ * Batch: `batch` sequences share arrays of `total` token rows.  cu [batch + 1] int32, device,
+ *   not decreasing, cu[0] = 0: sequence b has rows [cu[b], cu[b+1]), n_b of them (0 is
+ *   allowed).  kv_len [batch] int32, device: its length WITH those rows, so that its row t is
+ *   position kv_len[b] - n_b + t.  block_table [batch, max_pages] int32, device, rows
+ *   table_stride apart: entry i is the page of positions [i * page_size, (i+1) * page_size);
+ *   entries behind the last position are not used and may hold anything.
+ * Rows at and behind cu[batch] belong to no sequence (a padded batch): nothing is written for
+ * them.  Row 0 of a sequence may come before position 0 (kv_len[b] < n_b): such a row is not
+ * stored (append), reads as zeros (read), or sees no key (out = 0, lse = -inf).
+ * The arrays on the device are not checked on the host.  A length outside [0, max_pages *
+ * page_size], a cu outside [0, total], and a page outside [0, n_pages) never lead to an
+ * access outside the tensors: lengths and rows are clamped, a row that would go to such a
+ * page is dropped, and one that would come from it reads as zeros.
+ * No two (sequence, position) pairs that one append writes may have the same page and row.
+ * Requirements: d in {64, 128}; page_size a multiple of 16, at most 65536; batch at most
+ * RINGATTN_PAGED_MAX_BATCH; max_pages * page_size at most 2^30; k and v 16-byte aligned and
+ * their page strides multiples of 16 bytes, at least Hkv * page_size * d; scale page strides at
+ * least Hkv * page_size; the other arrays 4-byte aligned.  total = 0 is valid: nothing to do.
+ * The struct is read during the call only; it is host memory, what it points to is device
+ * memory.
+ */
+#define RINGATTN_PAGED_MAX_BATCH 4096
+typedef struct {
+    void* k;
+    void* v;
+    float* k_scale; /* NULL when dtype is 0 */
+    float* v_scale;
+    const int* block_table;
+    const int* cu;
+    const int* kv_len;
+    long long k_page_stride, v_page_stride;             /* elements */
+    long long k_scale_page_stride, v_scale_page_stride; /* elements */
+    long long table_stride;                             /* entries */
+    int n_pages, page_size, Hkv, d, dtype, batch, max_pages, total;
+} ra_paged_kv;
+
+/*
+ * ringattn_cache_append -- write the K and V rows of new tokens to their places.
+ * k_new, v_new: [total, Hkv, d] bf16, elements of a row adjacent; tokens and heads
+ *     *_token_stride and *_head_stride elements apart (multiples of 8, at least d, below 2^32;
+ *     a slice of a fused projection, or head-major rows).  16-byte aligned.
+ * bf16 pool: a copy.  e4m3 pool, per row x of d elements:
+ *     scale = 2^e, e = max(-120, the least e with max|x| <= 448 * 2^e); code = x / scale rounded
+ *     to the nearest e4m3 number, ties to even.
+ *     An element's error is at most 2^-4 of it, or 2^(e-10) where that is more.
+ * total * Hkv below 2^31 (else RA_ERR_UNSUPPORTED).  Other rows of the pool are left as they
+ * were.
+ */
+int ringattn_cache_append(const void* k_new, const void* v_new, long long k_token_stride,
+                          long long k_head_stride, long long v_token_stride, long long v_head_stride,
+                          const ra_paged_kv* kv, ra_stream_t stream);
+
+/*
+ * ringattn_cache_read -- the rows of the batch (the last n_b positions of every sequence) as
+ * bf16, head-major and in natural order: k_out, v_out [Hkv, total, d], 16-byte aligned.  With
+ * one sequence and n_b = kv_len[b] these are ringattn_fwd_natural's k and v.  A bf16 pool is
+ * copied; an e4m3 pool's code * scale is exact for the scales that ringattn_cache_append writes
+ * (beyond 1.9375 * 2^127, where the code may round up to 2^128, it is an infinity).
+ * total * Hkv below 2^31 (else RA_ERR_UNSUPPORTED).
+ */
+int ringattn_cache_read(const ra_paged_kv* kv, void* k_out, void* v_out, ra_stream_t stream);
+
+/*
+ * ringattn_fwd_paged -- attention of the batch's rows over their sequences' kept keys:
+ * q [total, Hq, d] bf16 (strides as k_new's), out [total, Hq, d] bf16 (out_f32 = 0) or fp32
+ * (1), lse [total, Hq] fp32, natural log; token and head strides in elements, out rows
+ * adjacent elements (out strides as k_new's; lse strides at least 1).  Row t of sequence b, at position
+ * i = kv_len[b] - n_b + t, sees the keys j < kv_len[b] with
+ *     causal = 1:  j <= i, and with window > 0 also (j > i - window or j < sinks)
+ *     causal = 0:  all of them (window must be 0).
+ * kv head h / (Hq / Hkv); no 1/sqrt(d) scale.  The keys must have been appended, the new
+ * tokens' own among them.  A row that sees no key gets out = 0, lse = -inf.  What a row does
+ * not see does not touch it, infinities and NaN in K or V included.  (out, lse) of calls over
+ * disjoint keys combine with ringattn_merge when out is fp32.
+ * max_q: at least the largest n_b (host knowledge: it picks the kernel and bounds the work; rows
+ *     of a sequence at and behind max_q are not written).
+ * Sums, maxima and the running output are fp32; the probabilities are rounded to 16 bits for
+ * their product with V.
+ * workspace: DEVICE, at least ringattn_paged_workspace_bytes(total, batch, Hq, Hkv, d, max_q)
+ *     bytes, 256-byte aligned; its contents do not matter before or after.  Calls that may
+ *     overlap on the GPU, captured ones among them, need one each.
+ * Requires Hq % Hkv == 0, Hq / Hkv <= 128, total * Hq below 2^31 (else RA_ERR_UNSUPPORTED),
+ * 16-byte aligned q and out.
+ */
+int ringattn_fwd_paged(const void* q, long long q_token_stride, long long q_head_stride, const ra_paged_kv* kv,
+                       void* out, long long out_token_stride, long long out_head_stride, int out_f32,
+                       float* lse, long long lse_token_stride, long long lse_head_stride, int Hq, int max_q,
+                       int causal, int window, int sinks, void* workspace, long long workspace_bytes,
+                       ra_stream_t stream);
+
+/* ringattn_paged_workspace_bytes -- host only.  See ringattn_fwd_paged. */
+int ringattn_paged_workspace_bytes(int total, int batch, int Hq, int Hkv, int d, int max_q, long long* bytes);
+
+/*
  * ringattn_permute -- move rows between natural and rank-major order.
  * src, dst: [H, S, row_bytes] bytes, distinct buffers.  inverse = 0: natural ->
  * rank-major; 1: rank-major -> natural.  row_bytes >= 1 (2*d for bf16 Q/K/V, 4*d

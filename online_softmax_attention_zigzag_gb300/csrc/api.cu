@@ -14,6 +14,7 @@
 
 #include "ringattn.h"
 #include "internal.h"
+#include "paged.h"
 
 namespace {
 
@@ -608,6 +609,62 @@ int bwd_bf16(const void* q, const void* k, const void* v, const float* out, cons
     return ra::launch_attn_bwd(p, out, dout, tq, tk, tv, tdo, dev->sms, stream) == 0 ? RA_OK : RA_ERR_CUDA;
 }
 
+// ------------------------------------------------------------------ paged cache
+// Strides of a [token, head, d] tensor: rows start on 16 bytes, and offsets stay in 64 bits.
+bool row_strides_ok(long long token, long long head, int d) {
+    constexpr long long kMax = 1LL << 32;
+    return token >= d && head >= d && token % 8 == 0 && head % 8 == 0 && token < kMax && head < kMax;
+}
+
+// Checks that concern the pool and the batch alone.
+int make_paged(const ra_paged_kv* a, ra::PagedKV* kv) {
+    if (!a || a->n_pages < 1 || a->page_size < 1 || a->Hkv < 1 || a->d < 1 || a->batch < 1 || a->max_pages < 1 ||
+        a->total < 0 || (a->dtype != 0 && a->dtype != 1))
+        return RA_ERR_INVALID_ARG;
+    if (!a->k || !a->v || a->k == a->v || !a->block_table || !a->cu || !a->kv_len || !aligned16(a->k) || !aligned16(a->v))
+        return RA_ERR_INVALID_ARG;
+    if (((reinterpret_cast<uintptr_t>(a->block_table) | reinterpret_cast<uintptr_t>(a->cu) |
+          reinterpret_cast<uintptr_t>(a->kv_len) | reinterpret_cast<uintptr_t>(a->k_scale) |
+          reinterpret_cast<uintptr_t>(a->v_scale)) & 3u) != 0)
+        return RA_ERR_INVALID_ARG;
+    const bool scaled = a->dtype == 1;
+    if (scaled != (a->k_scale != nullptr) || scaled != (a->v_scale != nullptr)) return RA_ERR_INVALID_ARG;
+    if (a->d != 64 && a->d != 128) return RA_ERR_UNSUPPORTED;
+    if (a->page_size % 16 != 0 || a->page_size > 65536 || a->batch > RINGATTN_PAGED_MAX_BATCH) return RA_ERR_UNSUPPORTED;
+    if (static_cast<long long>(a->max_pages) * a->page_size > (1LL << 30)) return RA_ERR_UNSUPPORTED;
+    const long long rows = static_cast<long long>(a->Hkv) * a->page_size;  // of one page
+    if (rows > (1LL << 30)) return RA_ERR_UNSUPPORTED;
+    const int unit = scaled ? 16 : 8;  // elements of 16 bytes
+    constexpr long long kMaxStride = 1LL << 36;
+    if (a->k_page_stride < rows * a->d || a->v_page_stride < rows * a->d || a->k_page_stride % unit != 0 ||
+        a->v_page_stride % unit != 0 || a->table_stride < a->max_pages)
+        return RA_ERR_INVALID_ARG;
+    if (scaled && (a->k_scale_page_stride < rows || a->v_scale_page_stride < rows)) return RA_ERR_INVALID_ARG;
+    if (a->k_page_stride > kMaxStride || a->v_page_stride > kMaxStride) return RA_ERR_UNSUPPORTED;
+    kv->k = a->k;
+    kv->v = a->v;
+    kv->k_scale = a->k_scale;
+    kv->v_scale = a->v_scale;
+    kv->k_ps = a->k_page_stride;
+    kv->v_ps = a->v_page_stride;
+    kv->ks_ps = a->k_scale_page_stride;
+    kv->vs_ps = a->v_scale_page_stride;
+    kv->table = a->block_table;
+    kv->cu = a->cu;
+    kv->len = a->kv_len;
+    kv->table_stride = a->table_stride;
+    kv->n_pages = a->n_pages;
+    kv->page = a->page_size;
+    kv->hkv = a->Hkv;
+    kv->d = a->d;
+    kv->e4m3 = a->dtype;
+    kv->batch = a->batch;
+    kv->max_pages = a->max_pages;
+    kv->total = a->total;
+    kv->by_page = ra::make_fastdiv(static_cast<unsigned>(a->page_size));
+    return RA_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -688,6 +745,98 @@ int ringattn_permute(const void* src, void* dst, int S, int H, int row_bytes, in
     if (st != RA_OK) return st;
     return ra::launch_permute(src, dst, S, H, row_bytes, c, layout, inverse, dev->err,
                               reinterpret_cast<cudaStream_t>(stream));
+}
+
+int ringattn_cache_append(const void* k_new, const void* v_new, long long k_token_stride, long long k_head_stride,
+                          long long v_token_stride, long long v_head_stride, const ra_paged_kv* kv,
+                          ra_stream_t stream) {
+    NvtxRange nvtx("ringattn_cache_append");
+    ra::PagedCopyParams p = {};
+    int st = make_paged(kv, &p.kv);
+    if (st != RA_OK || p.kv.total == 0) return st;
+    if (!k_new || !v_new || !aligned16(k_new) || !aligned16(v_new)) return RA_ERR_INVALID_ARG;
+    if (!row_strides_ok(k_token_stride, k_head_stride, p.kv.d) || !row_strides_ok(v_token_stride, v_head_stride, p.kv.d))
+        return RA_ERR_INVALID_ARG;
+    if (static_cast<long long>(p.kv.total) * p.kv.hkv > INT_MAX) return RA_ERR_UNSUPPORTED;
+    DeviceInfo* dev = nullptr;
+    if ((st = device_info(&dev)) != RA_OK) return st;
+    p.k_in = k_new;
+    p.v_in = v_new;
+    p.k_ts = k_token_stride;
+    p.k_hs = k_head_stride;
+    p.v_ts = v_token_stride;
+    p.v_hs = v_head_stride;
+    p.by_heads = ra::make_fastdiv(static_cast<unsigned>(p.kv.hkv));
+    return ra::launch_cache_append(p, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int ringattn_cache_read(const ra_paged_kv* kv, void* k_out, void* v_out, ra_stream_t stream) {
+    NvtxRange nvtx("ringattn_cache_read");
+    ra::PagedCopyParams p = {};
+    int st = make_paged(kv, &p.kv);
+    if (st != RA_OK || p.kv.total == 0) return st;
+    if (!k_out || !v_out || !aligned16(k_out) || !aligned16(v_out)) return RA_ERR_INVALID_ARG;
+    if (static_cast<long long>(p.kv.total) * p.kv.hkv > INT_MAX) return RA_ERR_UNSUPPORTED;
+    DeviceInfo* dev = nullptr;
+    if ((st = device_info(&dev)) != RA_OK) return st;
+    p.k_out = k_out;
+    p.v_out = v_out;
+    p.by_heads = ra::make_fastdiv(static_cast<unsigned>(p.kv.total));
+    return ra::launch_cache_read(p, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int ringattn_paged_workspace_bytes(int total, int batch, int Hq, int Hkv, int d, int max_q, long long* bytes) {
+    if (!bytes || total < 0 || batch < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || d < 1 || max_q < 1)
+        return RA_ERR_INVALID_ARG;
+    *bytes = 256;
+    return RA_OK;
+}
+
+int ringattn_fwd_paged(const void* q, long long q_token_stride, long long q_head_stride, const ra_paged_kv* kv,
+                       void* out, long long out_token_stride, long long out_head_stride, int out_f32, float* lse,
+                       long long lse_token_stride, long long lse_head_stride, int Hq, int max_q, int causal,
+                       int window, int sinks, void* workspace, long long workspace_bytes, ra_stream_t stream) {
+    NvtxRange nvtx("ringattn_fwd_paged");
+    ra::PagedAttnParams p = {};
+    int st = make_paged(kv, &p.kv);
+    if (st != RA_OK) return st;
+    if (Hq < 1 || Hq % p.kv.hkv != 0 || max_q < 1) return RA_ERR_INVALID_ARG;
+    if ((causal != 0 && causal != 1) || (out_f32 != 0 && out_f32 != 1)) return RA_ERR_INVALID_ARG;
+    if (window < 0 || sinks < 0 || (window > 0 && causal == 0)) return RA_ERR_INVALID_ARG;
+    if (p.kv.total == 0) return RA_OK;
+    if (!q || !out || !lse || !workspace || !aligned16(q) || !aligned16(out)) return RA_ERR_INVALID_ARG;
+    if ((reinterpret_cast<uintptr_t>(lse) & 3u) != 0 || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+        return RA_ERR_INVALID_ARG;
+    if (!row_strides_ok(q_token_stride, q_head_stride, p.kv.d) || !row_strides_ok(out_token_stride, out_head_stride, p.kv.d))
+        return RA_ERR_INVALID_ARG;
+    if (lse_token_stride < 1 || lse_head_stride < 1) return RA_ERR_INVALID_ARG;
+    long long need = 0;
+    if ((st = ringattn_paged_workspace_bytes(p.kv.total, p.kv.batch, Hq, p.kv.hkv, p.kv.d, max_q, &need)) != RA_OK)
+        return st;
+    if (workspace_bytes < need) return RA_ERR_INVALID_ARG;
+    p.g = Hq / p.kv.hkv;
+    if (p.g > 128 || static_cast<long long>(p.kv.total) * Hq > INT_MAX) return RA_ERR_UNSUPPORTED;
+    DeviceInfo* dev = nullptr;
+    if ((st = device_info(&dev)) != RA_OK) return st;
+    p.q = q;
+    p.out = out;
+    p.lse = lse;
+    p.q_ts = q_token_stride;
+    p.q_hs = q_head_stride;
+    p.o_ts = out_token_stride;
+    p.o_hs = out_head_stride;
+    p.l_ts = lse_token_stride;
+    p.l_hs = lse_head_stride;
+    p.hq = Hq;
+    p.max_q = max_q < p.kv.total ? max_q : p.kv.total;
+    p.causal = causal;
+    p.window = window;
+    p.sinks = sinks;
+    p.out_f32 = out_f32;
+    p.workspace = workspace;
+    p.err = dev->err;
+    p.timeout_ns = wait_timeout_ns();
+    return ra::launch_paged_attn(p, reinterpret_cast<cudaStream_t>(stream));
 }
 
 int ringattn_rank_work(int S, int c, int causal, int layout, int tile, long long* units, long long* pairs,

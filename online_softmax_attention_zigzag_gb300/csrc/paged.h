@@ -1,0 +1,96 @@
+// paged.h -- parameter block, launchers and index arithmetic of the paged K/V cache
+// (ringattn_cache_append, ringattn_cache_read, ringattn_fwd_paged).
+#pragma once
+#include <cstdint>
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "fastdiv.h"
+
+namespace ra {
+
+constexpr int kPagedMaxBatch = 4096;  // RINGATTN_PAGED_MAX_BATCH
+
+// The cache and the batch that uses it (ra_paged_kv, checked).  Strides are in elements.
+struct PagedKV {
+    void* k;
+    void* v;
+    float* k_scale;  // null for bf16
+    float* v_scale;
+    long long k_ps, v_ps, ks_ps, vs_ps;  // from page to page
+    const int* table;                    // [batch, max_pages], rows table_stride apart
+    const int* cu;                       // [batch + 1]
+    const int* len;                      // [batch]
+    long long table_stride;
+    int n_pages, page, hkv, d, e4m3, batch, max_pages;
+    int total;       // rows of the caller's token tensors
+    FastDiv by_page;
+};
+
+struct PagedCopyParams {  // append: token-major rows in; read: [Hkv, total, d] out
+    PagedKV kv;
+    const void* k_in;
+    const void* v_in;
+    long long k_ts, k_hs, v_ts, v_hs;  // token and head strides of k_in, v_in
+    void* k_out;
+    void* v_out;
+    FastDiv by_heads;  // append: Hkv; read: total
+};
+
+struct PagedAttnParams {
+    PagedKV kv;
+    const void* q;
+    void* out;
+    float* lse;
+    long long q_ts, q_hs, o_ts, o_hs, l_ts, l_hs;
+    int hq, g, max_q, causal, window, sinks, out_f32;
+    void* workspace;
+    int* err;
+    unsigned long long timeout_ns;
+};
+
+int launch_cache_append(const PagedCopyParams& p, cudaStream_t stream);
+int launch_cache_read(const PagedCopyParams& p, cudaStream_t stream);
+int launch_paged_attn(const PagedAttnParams& p, cudaStream_t stream);
+
+#ifdef __CUDACC__
+// One sequence of the batch: rows [q0, q0 + T) of the token tensors, row t at position
+// base + t, L positions in all.  Whatever the device arrays hold, the rows lie inside the
+// tensors and the positions inside the block table.
+struct PagedSeq {
+    int q0, T, L, base;
+};
+
+__device__ __forceinline__ PagedSeq paged_seq(const PagedKV& kv, int b) {
+    PagedSeq s;
+    s.q0 = min(max(__ldg(kv.cu + b), 0), kv.total);
+    s.T = min(max(__ldg(kv.cu + b + 1), s.q0), kv.total) - s.q0;
+    s.L = min(max(__ldg(kv.len + b), 0), kv.max_pages * kv.page);
+    s.base = s.L - s.T;
+    return s;
+}
+
+// Page of position pos (0 <= pos < max_pages * page) of sequence b; -1 when the table's entry
+// is no page of the pool.
+__device__ __forceinline__ int paged_page(const PagedKV& kv, int b, int pos, int& row) {
+    const int i = static_cast<int>(fdiv(static_cast<unsigned>(pos), kv.by_page));
+    row = pos - i * kv.page;
+    const int pg = __ldg(kv.table + b * kv.table_stride + i);
+    return (pg >= 0 && pg < kv.n_pages) ? pg : -1;
+}
+
+// The sequence whose rows hold row t (cu[b] <= t < cu[b + 1]), -1 if none does.  cu may be in
+// shared memory.
+__device__ __forceinline__ int paged_find(const int* cu, int batch, int t) {
+    if (t < cu[0] || t >= cu[batch]) return -1;
+    int lo = 0, hi = batch;  // cu[lo] <= t < cu[hi]
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (cu[mid] <= t) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
+#endif
+
+}  // namespace ra

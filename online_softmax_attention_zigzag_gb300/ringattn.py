@@ -36,10 +36,15 @@ EXPORTS = (
     "ringattn_fwd_rank", "ringattn_fwd_docmask", "ringattn_fwd_docmask_noalloc",
     "ringattn_fwd_host", "ringattn_host_workspace_bytes", "ringattn_relayout", "ringattn_ulysses_fwd",
     "ringattn_bwd", "ringattn_bwd_natural",
+    "ringattn_cache_append", "ringattn_cache_read", "ringattn_fwd_paged", "ringattn_paged_workspace_bytes",
 )
 
 # Longest sequence ringattn_fwd_docmask_noalloc takes (its static scratch, int32 [S]).
 DOCMASK_NOALLOC_MAX_S = 262144
+
+
+# Most sequences of one paged call.
+PAGED_MAX_BATCH = 4096
 
 
 class RingAttnError(RuntimeError):
@@ -52,6 +57,14 @@ _lib = None
 
 _P, _I, _LL = ctypes.c_void_p, ctypes.c_int, ctypes.c_longlong
 _ATTN = [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I]
+
+
+class _PagedKV(ctypes.Structure):
+    """ra_paged_kv: the pool and the batch of a paged call."""
+    _fields_ = [(n, _P) for n in ("k", "v", "k_scale", "v_scale", "block_table", "cu", "kv_len")] + \
+               [(n, _LL) for n in ("k_page_stride", "v_page_stride", "k_scale_page_stride", "v_scale_page_stride",
+                                   "table_stride")] + \
+               [(n, _I) for n in ("n_pages", "page_size", "Hkv", "d", "dtype", "batch", "max_pages", "total")]
 
 
 def lib() -> ctypes.CDLL:
@@ -80,6 +93,10 @@ def lib() -> ctypes.CDLL:
             "ringattn_fwd_hop_f32": _ATTN + [_I, _I, _P],
             "ringattn_merge": [_P, _P, _P, _P, _LL, _I, _P],
             "ringattn_permute": [_P, _P, _I, _I, _I, _I, _I, _I, _P],
+            "ringattn_cache_append": [_P, _P, _LL, _LL, _LL, _LL, _P, _P],
+            "ringattn_cache_read": [_P, _P, _P, _P],
+            "ringattn_fwd_paged": [_P, _LL, _LL, _P, _P, _LL, _LL, _I, _P, _LL, _LL, _I, _I, _I, _I, _I, _P, _LL, _P],
+            "ringattn_paged_workspace_bytes": [_I, _I, _I, _I, _I, _I, _P],
             "ringattn_rank_work": [_I, _I, _I, _I, _I, _P, _P, _P],
             "ringattn_sync_status": [_P],
             "ringattn_selftest_timeout": [_LL, _P],
@@ -321,6 +338,135 @@ def permute(src, dst, *, c, layout, inverse, stream=None) -> None:
     _check("ringattn_permute", lib().ringattn_permute(
         _dev(src, "src"), _dev(dst, "dst"), S, H, row_bytes, c, layout, int(inverse),
         ctypes.c_void_p(_stream(stream))))
+
+
+def _strided(t: torch.Tensor, name: str, dtype, dev: int, dim: int) -> int:
+    """Address of a CUDA tensor whose strides go along to the library; its last axis is
+    contiguous."""
+    if not isinstance(t, torch.Tensor) or t.get_device() < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, but the current device is cuda:{dev}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != dim:
+        raise ValueError(f"{name} must have {dim} axes, got {t.dim()}")
+    if t.stride(-1) != 1 and t.shape[-1] > 1:
+        raise ValueError(f"{name}'s last axis must be contiguous")
+    return t.data_ptr()
+
+
+def _step(t: torch.Tensor, axis: int) -> int:
+    """Stride of an axis; of an axis of one entry, whose stride means nothing, that of a
+    contiguous tensor."""
+    if t.shape[axis] > 1:
+        return t.stride(axis)
+    n = 1
+    for size in t.shape[axis + 1:]:
+        n *= size
+    return max(1, n)
+
+
+def _paged(k_cache, v_cache, k_scale, v_scale, block_table, cu, kv_len, total: int, dev: int) -> _PagedKV:
+    """The library's description of a paged cache and the batch that uses it."""
+    e4m3 = k_cache.dtype == torch.float8_e4m3fn
+    dtype = torch.float8_e4m3fn if e4m3 else torch.bfloat16
+    a = _PagedKV()
+    a.k = _strided(k_cache, "k_cache", dtype, dev, 4)
+    a.v = _strided(v_cache, "v_cache", dtype, dev, 4)
+    shape = k_cache.shape
+    n, h, page, d = shape
+    if v_cache.shape != shape:
+        raise ValueError("k_cache and v_cache must have the same shape [n_pages, Hkv, page_size, d]")
+    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        if (h > 1 and t.stride(1) != page * d) or (page > 1 and t.stride(2) != d):
+            raise ValueError(f"each page of {name} must be contiguous")
+    a.k_page_stride, a.v_page_stride = _step(k_cache, 0), _step(v_cache, 0)
+    if (k_scale is not None) != e4m3 or (v_scale is not None) != e4m3:
+        raise ValueError("an e4m3 cache has k_scale and v_scale, a bf16 cache has none")
+    if e4m3:
+        for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+            p = _strided(t, name, torch.float32, dev, 3)
+            if t.shape != shape[:3]:
+                raise ValueError(f"{name} must be [n_pages, Hkv, page_size]")
+            if h > 1 and t.stride(1) != page:
+                raise ValueError(f"each page of {name} must be contiguous")
+            setattr(a, name, p)
+        a.k_scale_page_stride, a.v_scale_page_stride = _step(k_scale, 0), _step(v_scale, 0)
+    a.block_table = _strided(block_table, "block_table", torch.int32, dev, 2)
+    a.cu = _strided(cu, "cu", torch.int32, dev, 1)
+    a.kv_len = _strided(kv_len, "kv_len", torch.int32, dev, 1)
+    batch, a.max_pages = block_table.shape
+    if cu.shape[0] != batch + 1 or kv_len.shape[0] != batch:
+        raise ValueError("block_table must be [batch, max_pages], cu [batch + 1] and kv_len [batch]")
+    a.table_stride = _step(block_table, 0)
+    a.n_pages, a.Hkv, a.page_size, a.d = n, h, page, d
+    a.dtype, a.batch, a.total = int(e4m3), batch, total
+    return a
+
+
+def cache_append(k_new, v_new, k_cache, v_cache, block_table, cu, kv_len, *, k_scale=None, v_scale=None,
+                 stream=None) -> None:
+    """ringattn_cache_append: store the rows of new tokens, k_new and v_new [total, Hkv, d] bf16
+    (any token and head strides), at their positions in the pages of k_cache and v_cache
+    [n_pages, Hkv, page_size, d], bf16 or float8_e4m3fn (then with k_scale, v_scale [n_pages, Hkv,
+    page_size] fp32).  block_table [batch, max_pages], cu [batch + 1] and kv_len [batch] are
+    int32; kv_len counts the new tokens."""
+    dev = torch.cuda.current_device()
+    kp, vp = _strided(k_new, "k_new", torch.bfloat16, dev, 3), _strided(v_new, "v_new", torch.bfloat16, dev, 3)
+    total = k_new.shape[0]
+    a = _paged(k_cache, v_cache, k_scale, v_scale, block_table, cu, kv_len, total, dev)
+    if tuple(k_new.shape) != (total, a.Hkv, a.d) or v_new.shape != k_new.shape:
+        raise ValueError("k_new and v_new must be [total, Hkv, d] with the cache's Hkv and d")
+    _check("ringattn_cache_append", lib().ringattn_cache_append(
+        kp, vp, _step(k_new, 0), _step(k_new, 1), _step(v_new, 0), _step(v_new, 1), ctypes.byref(a), _stream(stream)))
+
+
+def cache_read(k_cache, v_cache, k_out, v_out, block_table, cu, kv_len, *, k_scale=None, v_scale=None,
+               stream=None) -> None:
+    """ringattn_cache_read: the last cu[b+1] - cu[b] positions of every sequence as bf16 rows,
+    head-major: k_out, v_out [Hkv, total, d], contiguous.  The cache as for :func:`cache_append`."""
+    dev = torch.cuda.current_device()
+    kp, vp = _strided(k_out, "k_out", torch.bfloat16, dev, 3), _strided(v_out, "v_out", torch.bfloat16, dev, 3)
+    total = k_out.shape[1]
+    a = _paged(k_cache, v_cache, k_scale, v_scale, block_table, cu, kv_len, total, dev)
+    if tuple(k_out.shape) != (a.Hkv, total, a.d) or v_out.shape != k_out.shape:
+        raise ValueError("k_out and v_out must be [Hkv, total, d] with the cache's Hkv and d")
+    if not (k_out.is_contiguous() and v_out.is_contiguous()):
+        raise ValueError("k_out and v_out must be contiguous")
+    _check("ringattn_cache_read", lib().ringattn_cache_read(ctypes.byref(a), kp, vp, _stream(stream)))
+
+
+def paged_workspace_bytes(total: int, batch: int, Hq: int, Hkv: int, d: int, max_q: int) -> int:
+    """ringattn_paged_workspace_bytes (host only)."""
+    n = ctypes.c_longlong(0)
+    _check("ringattn_paged_workspace_bytes", lib().ringattn_paged_workspace_bytes(
+        total, batch, Hq, Hkv, d, max_q, ctypes.byref(n)))
+    return n.value
+
+
+def fwd_paged(q, k_cache, v_cache, out, lse, block_table, cu, kv_len, workspace, *, max_q, causal=1, window=0,
+              sinks=0, k_scale=None, v_scale=None, stream=None) -> None:
+    """ringattn_fwd_paged: attention of q [total, Hq, d] bf16 (any token and head strides) over the
+    cached keys of its sequences -> out [total, Hq, d] bf16 or fp32, lse [total, Hq] fp32 (any
+    strides).  With window > 0 a row at position i sees j in (i - window, i] and the first
+    ``sinks`` positions.  max_q: at least the most rows of one sequence; workspace: a CUDA uint8
+    tensor of at least :func:`paged_workspace_bytes`.  The cache as for :func:`cache_append`."""
+    dev = torch.cuda.current_device()
+    f32 = out.dtype == torch.float32
+    qp = _strided(q, "q", torch.bfloat16, dev, 3)
+    op = _strided(out, "out", torch.float32 if f32 else torch.bfloat16, dev, 3)
+    total, Hq, d = q.shape
+    a = _paged(k_cache, v_cache, k_scale, v_scale, block_table, cu, kv_len, total, dev)
+    if d != a.d or out.shape != q.shape:
+        raise ValueError("q and out must be [total, Hq, d] with the cache's d")
+    if not isinstance(lse, torch.Tensor) or lse.get_device() != dev or lse.dtype != torch.float32 or \
+            tuple(lse.shape) != (total, Hq):
+        raise ValueError("lse must be a fp32 [total, Hq] tensor on the current device")
+    wp = _strided(workspace, "workspace", torch.uint8, dev, 1)
+    _check("ringattn_fwd_paged", lib().ringattn_fwd_paged(
+        qp, _step(q, 0), _step(q, 1), ctypes.byref(a), op, _step(out, 0), _step(out, 1), int(f32), lse.data_ptr(),
+        _step(lse, 0), _step(lse, 1), Hq, max_q, int(causal), window, sinks, wp, workspace.shape[0], _stream(stream)))
 
 
 def rank_work(S: int, c: int, causal: int, layout: int, tile: int = 128):

@@ -31,6 +31,8 @@ numpy).  Each function names the passage it follows:
   rank's heads in between ("Ring Attention and Ulysses shard a sequence two
   different ways...", section "Ulysses: an all-to-all relayout instead of a
   rotation").
+* :mod:`oracle.paged` -- a paged K/V cache (bf16 or e4m3 rows) and the attention
+  of a sequence's last rows over it.
 * :mod:`oracle.backward` -- the exact gradient of that attention with respect
   to q, k and v, and the ring's backward (KV blocks travel with their dK, dV
   accumulators); the pages give only the forward, so the gradient is the
