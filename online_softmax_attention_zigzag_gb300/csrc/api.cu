@@ -11,6 +11,7 @@
 #include <cstdint>
 #include <cstdlib>
 #include <mutex>
+#include <numeric>
 
 #include "ringattn.h"
 #include "internal.h"
@@ -616,6 +617,44 @@ bool row_strides_ok(long long token, long long head, int d) {
     return token >= d && head >= d && token % 8 == 0 && head % 8 == 0 && token < kMax && head < kMax;
 }
 
+// One pool tensor as [n_pages, Hkv * page_size, d], boxes of box_rows rows of one page x 128 bytes
+// (64 where a row has only 64), swizzled as wide; a page index outside the pool reads zeros.
+int encode_pool(CUtensorMap* map, const void* base, long long page_stride, const ra::PagedKV& kv, int box_rows) {
+    const int es = kv.e4m3 ? 1 : 2, cols = kv.e4m3 ? kv.d : 64;
+    cuuint64_t dims[3] = {static_cast<cuuint64_t>(kv.d), static_cast<cuuint64_t>(kv.hkv) * kv.page,
+                          static_cast<cuuint64_t>(kv.n_pages)};
+    cuuint64_t strides[2] = {static_cast<cuuint64_t>(kv.d) * es, static_cast<cuuint64_t>(page_stride) * es};
+    cuuint32_t box[3] = {static_cast<cuuint32_t>(cols), static_cast<cuuint32_t>(box_rows), 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    CUresult r = g_encode(map, kv.e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+                          const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          cols * es == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? RA_OK : RA_ERR_CUDA;
+}
+
+// The scales of a pool tensor as [n_pages, Hkv * page_size], boxes of box_rows.
+int encode_scales(CUtensorMap* map, const float* base, long long page_stride, const ra::PagedKV& kv, int box_rows) {
+    cuuint64_t dims[2] = {static_cast<cuuint64_t>(kv.hkv) * kv.page, static_cast<cuuint64_t>(kv.n_pages)};
+    cuuint64_t strides[1] = {static_cast<cuuint64_t>(page_stride) * 4};
+    cuuint32_t box[2] = {static_cast<cuuint32_t>(box_rows), 1};
+    cuuint32_t estr[2] = {1, 1};
+    CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, const_cast<float*>(base), dims, strides, box, estr,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? RA_OK : RA_ERR_CUDA;
+}
+
+int encode_paged(const ra::PagedAttnParams& p, ra::PagedMaps* m) {
+    const ra::PagedKV& kv = p.kv;
+    int st;
+    if ((st = encode_pool(&m->k, kv.k, kv.k_ps, kv, p.box_rows)) != RA_OK) return st;
+    if ((st = encode_pool(&m->v, kv.v, kv.v_ps, kv, p.box_rows)) != RA_OK) return st;
+    if (!kv.e4m3) return RA_OK;
+    if ((st = encode_scales(&m->ks, kv.k_scale, kv.ks_ps, kv, p.box_rows)) != RA_OK) return st;
+    return encode_scales(&m->vs, kv.v_scale, kv.vs_ps, kv, p.box_rows);
+}
+
 // Checks that concern the pool and the batch alone.
 int make_paged(const ra_paged_kv* a, ra::PagedKV* kv) {
     if (!a || a->n_pages < 1 || a->page_size < 1 || a->Hkv < 1 || a->d < 1 || a->batch < 1 || a->max_pages < 1 ||
@@ -624,8 +663,7 @@ int make_paged(const ra_paged_kv* a, ra::PagedKV* kv) {
     if (!a->k || !a->v || a->k == a->v || !a->block_table || !a->cu || !a->kv_len || !aligned16(a->k) || !aligned16(a->v))
         return RA_ERR_INVALID_ARG;
     if (((reinterpret_cast<uintptr_t>(a->block_table) | reinterpret_cast<uintptr_t>(a->cu) |
-          reinterpret_cast<uintptr_t>(a->kv_len) | reinterpret_cast<uintptr_t>(a->k_scale) |
-          reinterpret_cast<uintptr_t>(a->v_scale)) & 3u) != 0)
+          reinterpret_cast<uintptr_t>(a->kv_len)) & 3u) != 0)
         return RA_ERR_INVALID_ARG;
     const bool scaled = a->dtype == 1;
     if (scaled != (a->k_scale != nullptr) || scaled != (a->v_scale != nullptr)) return RA_ERR_INVALID_ARG;
@@ -639,8 +677,13 @@ int make_paged(const ra_paged_kv* a, ra::PagedKV* kv) {
     if (a->k_page_stride < rows * a->d || a->v_page_stride < rows * a->d || a->k_page_stride % unit != 0 ||
         a->v_page_stride % unit != 0 || a->table_stride < a->max_pages)
         return RA_ERR_INVALID_ARG;
-    if (scaled && (a->k_scale_page_stride < rows || a->v_scale_page_stride < rows)) return RA_ERR_INVALID_ARG;
+    if (scaled && (!aligned16(a->k_scale) || !aligned16(a->v_scale) || a->k_scale_page_stride < rows ||
+                   a->v_scale_page_stride < rows || a->k_scale_page_stride % 4 != 0 || a->v_scale_page_stride % 4 != 0))
+        return RA_ERR_INVALID_ARG;
     if (a->k_page_stride > kMaxStride || a->v_page_stride > kMaxStride) return RA_ERR_UNSUPPORTED;
+    // tiles of 128 keys over all sequences are counted in 32 bits
+    if ((static_cast<long long>(a->max_pages) * a->page_size / ra::kPagedTile + 1) * a->batch > INT_MAX)
+        return RA_ERR_UNSUPPORTED;
     kv->k = a->k;
     kv->v = a->v;
     kv->k_scale = a->k_scale;
@@ -788,7 +831,7 @@ int ringattn_cache_read(const ra_paged_kv* kv, void* k_out, void* v_out, ra_stre
 int ringattn_paged_workspace_bytes(int total, int batch, int Hq, int Hkv, int d, int max_q, long long* bytes) {
     if (!bytes || total < 0 || batch < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || d < 1 || max_q < 1)
         return RA_ERR_INVALID_ARG;
-    *bytes = 256;
+    *bytes = (2LL * ra::kPagedMaxShares * static_cast<long long>(sizeof(ra::PagedPartial)) + 255) / 256 * 256;
     return RA_OK;
 }
 
@@ -836,7 +879,13 @@ int ringattn_fwd_paged(const void* q, long long q_token_stride, long long q_head
     p.workspace = workspace;
     p.err = dev->err;
     p.timeout_ns = wait_timeout_ns();
-    return ra::launch_paged_attn(p, reinterpret_cast<cudaStream_t>(stream));
+    cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+    if (static_cast<long long>(p.max_q) * p.g > ra::kPagedFewRows) return ra::launch_paged_attn(p, cs);
+    p.box_rows = std::gcd(p.kv.page, ra::kPagedTile);
+    ra::PagedMaps maps = {};
+    if ((st = get_encoder()) != RA_OK || (st = encode_paged(p, &maps)) != RA_OK) return st;
+    const int shares = dev->sms < ra::kPagedMaxShares ? dev->sms : ra::kPagedMaxShares;
+    return ra::launch_paged_decode(p, maps, shares, cs);
 }
 
 int ringattn_rank_work(int S, int c, int causal, int layout, int tile, long long* units, long long* pairs,

@@ -9,7 +9,18 @@
 
 namespace ra {
 
-constexpr int kPagedMaxBatch = 4096;  // RINGATTN_PAGED_MAX_BATCH
+constexpr int kPagedTile = 128;       // keys of a tile
+constexpr int kPagedMaxD = 128;
+constexpr int kPagedMaxShares = 160;  // most blocks of an attention kernel
+constexpr int kPagedFewRows = 16;     // rows of one sequence and KV head that the few-row kernel takes
+
+// What a block of the few-row kernel leaves of a (sequence, KV head) pair that other blocks
+// share: row r's sum of p v with weights 2^(x - m), and sum of p with weights 2^(x - ms).
+struct PagedPartial {
+    int b, h, begins, pad;  // b < 0: none; begins: the pair's first tile is in it
+    float m[kPagedFewRows], ms[kPagedFewRows], l[kPagedFewRows];
+    float o[kPagedFewRows * kPagedMaxD];
+};
 
 // The cache and the batch that uses it (ra_paged_kv, checked).  Strides are in elements.
 struct PagedKV {
@@ -44,14 +55,22 @@ struct PagedAttnParams {
     float* lse;
     long long q_ts, q_hs, o_ts, o_hs, l_ts, l_hs;
     int hq, g, max_q, causal, window, sinks, out_f32;
+    int box_rows;  // gcd(page, 128): rows of a TMA box, all on one page
     void* workspace;
     int* err;
     unsigned long long timeout_ns;
 };
 
+struct PagedMaps {  // of the pool; ks and vs only for e4m3
+    CUtensorMap k, v, ks, vs;
+};
+
 int launch_cache_append(const PagedCopyParams& p, cudaStream_t stream);
 int launch_cache_read(const PagedCopyParams& p, cudaStream_t stream);
 int launch_paged_attn(const PagedAttnParams& p, cudaStream_t stream);
+// max_q * g <= kPagedFewRows; `shares` blocks (at most kPagedMaxShares), the workspace 2 * shares
+// PagedPartial
+int launch_paged_decode(const PagedAttnParams& p, const PagedMaps& m, int shares, cudaStream_t stream);
 
 #ifdef __CUDACC__
 // One sequence of the batch: rows [q0, q0 + T) of the token tensors, row t at position
@@ -90,6 +109,21 @@ __device__ __forceinline__ int paged_find(const int* cu, int batch, int t) {
         else hi = mid;
     }
     return lo;
+}
+
+// Four elements of an output row, times inv, in the caller's type.
+__device__ __forceinline__ void paged_store4(const PagedAttnParams& p, int tok, int head, int d, const float (&x)[4],
+                                             float inv) {
+    const long long at = tok * p.o_ts + head * p.o_hs + d;
+    if (p.out_f32) {
+        *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) =
+            make_float4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
+    } else {
+        uint2 w;
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w.x) : "f"(x[1] * inv), "f"(x[0] * inv));
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w.y) : "f"(x[3] * inv), "f"(x[2] * inv));
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at) = w;
+    }
 }
 #endif
 

@@ -1,0 +1,749 @@
+// paged_decode.cu -- attention of few rows over a paged K/V cache: the rows of one sequence and KV
+// head (n_b tokens times g query heads) fill at most one 16-row matrix tile.
+//
+//     s_j = q . k_j,  out = sum_j 2^(c s_j - m) v_j / l,  l = sum_j 2^(c s_j - m),  c = log2 e
+// Every K and V row is read once for at most 16 query rows: 16 * 4 * d FLOP for 4 * d bytes (2 * d
+// in 8 bits), so HBM bounds it by far and everything else only has to keep out of the way:
+//   * one persistent block an SM; the tiles of 128 keys of all (sequence, KV head) pairs, in one
+//     line, are dealt out in equal contiguous shares, so that one long context or a thousand
+//     short ones load every SM alike.  A pair whose tiles lie in several shares leaves
+//     partial results (O, m, l) in the workspace, which a second small kernel joins; a share
+//     has at most two of these (its first and its last pair), so the workspace does not grow
+//     with the lengths.
+//   * one warp streams K and V tiles through a ring of shared-memory slots with TMA, box by box
+//     as the pages come (a box is gcd(page, 128) rows of one page), and runs on into the next
+//     pair while the others finish the last.
+//   * eight warps compute, 16 keys of every tile each, with mma.sync (16 rows are an eighth
+//     of a tcgen05 tile, and S and P stay in registers between the two products).  Each keeps its own
+//     running max, sum and output; they meet once a pair.
+// bf16 cache: P goes into its product as two bf16 halves (p = hi + lo, 16 significant bits): the
+// second product costs nothing here, the loads take longer.
+// e4m3 cache: codes become fp16 (one instruction for two, exact), q is brought to fp16's range by
+// a power of two per row (elements below 2^-28 of the row's largest lose bits), the K scale
+// multiplies the score, and the V scale enters the exponent: with v_j = 2^(a_j) u_j,
+//     p'_j = 2^(c s_j + a_j - m),  out = 2^m sum p'_j u_j / (2^ms l),  l = sum 2^(c s_j - ms)
+// where m is the running max of c s_j + a_j and ms that of c s_j.  So p' fits fp16 whatever the
+// scales are and keeps 11 bits down to 2^-20 of the largest contribution, and l loses nothing.
+#include <cuda_bf16.h>
+
+#include "paged.h"
+#include "ptx_paged.cuh"
+
+namespace ra {
+namespace {
+
+constexpr int kTile = kPagedTile;         // keys of a tile
+constexpr int kWarps = 8;                 // computing warps
+constexpr int kThreads = (kWarps + 1) * 32;
+constexpr int kRows = 16;
+constexpr int kBar = 1;                   // named barrier of the computing warps
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.69314718055994531f;
+constexpr float kRescale = 8.0f;          // the running max moves when it is exceeded by more (log2)
+constexpr float kF16Up = 6.0f;            // p' is kept 2^6 times larger: at most 2^(8 + 6 + 1) in fp16
+
+template <int D, bool E4M3>
+struct Cfg {
+    static constexpr int kSlotBytes = kTile * D * (E4M3 ? 1 : 2);
+    static constexpr int kSlots = (D == 128 && !E4M3) ? 5 : 8;
+    static constexpr int kPad = E4M3 ? 16 : 8;  // floats; keeps the fragments' stores off each other's banks
+    static constexpr int kOStride = D + kPad;
+    static constexpr int kScaleBytes = 1024;  // of a slot: boxes start 128 bytes apart at least, as TMA wants
+    static constexpr int kScaleOff = kSlots * kSlotBytes;
+    static constexpr int kOOff = kScaleOff + (E4M3 ? kSlots * kScaleBytes : 0);
+    static constexpr int kMlOff = kOOff + kWarps * 8 * kOStride * 4;  // m, ms, l of every warp and row
+    static constexpr int kPreOff = kMlOff + 3 * kWarps * kRows * 4;
+    static constexpr int kFixedBytes = kPreOff + 1024;  // and 4 * (batch + 1) for the shares
+};
+
+// The key tiles of a sequence that some row sees: tiles [0, ns) hold the sinks, tiles from lo on the
+// window (or everything).  At least one tile where there are rows, so that every row is
+// written.
+struct Tiles {
+    int ns, lo, n;
+};
+__device__ __forceinline__ Tiles key_tiles(const PagedAttnParams& p, const PagedSeq& s) {
+    Tiles t;
+    const int first = p.window > 0 ? max(0, s.base - p.window + 1) : 0;
+    const int hi = (s.L + kTile - 1) / kTile;
+    t.lo = min(first / kTile, hi);
+    t.ns = p.window > 0 ? min((min(p.sinks, s.L) + kTile - 1) / kTile, t.lo) : 0;
+    t.n = s.T > 0 ? max(1, t.ns + hi - t.lo) : 0;
+    return t;
+}
+
+// One block's part of one (sequence, head) pair: tiles [ta, tb) of its n.
+struct Part {
+    int b, h, ta, tb, n;
+};
+
+// Shares of the tiles, found by every block for itself: pre[b] = tiles of the sequences before b
+// (of one head).  Returns their sum.
+__device__ int share_tiles(const PagedAttnParams& p, int* pre, int* scratch) {
+    const int B = p.kv.batch, lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+    int base = 0;
+    for (int b0 = 0; b0 < B; b0 += kThreads) {
+        const int b = b0 + threadIdx.x;
+        const int n = b < B ? key_tiles(p, paged_seq(p.kv, b)).n : 0;
+        int x = n;
+#pragma unroll
+        for (int o = 1; o < 32; o *= 2) {
+            const int y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += y;
+        }
+        if (lane == 31) scratch[warp] = x;
+        __syncthreads();
+        int before = base, all = 0;
+        for (int w = 0; w <= kWarps; ++w) {
+            const int y = scratch[w];
+            if (w < warp) before += y;
+            all += y;
+        }
+        if (b < B) pre[b] = before + x - n;
+        base += all;
+        __syncthreads();
+    }
+    if (threadIdx.x == 0) pre[B] = base;
+    __syncthreads();
+    return base;
+}
+
+// Walks the parts of this block's share [w0, w1): f(part) until it returns false.
+template <class F>
+__device__ __forceinline__ void for_each_part(const PagedAttnParams& p, const int* pre, long long w0, long long w1,
+                                              F&& f) {
+    if (w0 >= w1) return;
+    const int H = p.kv.hkv;
+    int lo = 0, hi = p.kv.batch;  // pre[lo] * H <= w0 < pre[hi] * H
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (static_cast<long long>(pre[mid]) * H <= w0) lo = mid;
+        else hi = mid;
+    }
+    Part q;
+    q.b = lo;
+    q.n = pre[lo + 1] - pre[lo];
+    const long long in = w0 - static_cast<long long>(pre[lo]) * H;
+    q.h = static_cast<int>(in / q.n);
+    q.ta = static_cast<int>(in - static_cast<long long>(q.h) * q.n);
+    long long w = w0;
+    while (true) {
+        q.tb = static_cast<int>(min(static_cast<long long>(q.n), q.ta + (w1 - w)));
+        if (!f(q)) return;
+        w += q.tb - q.ta;
+        if (w >= w1) return;
+        q.ta = 0;
+        if (++q.h == H) {
+            q.h = 0;
+            do ++q.b; while (pre[q.b + 1] == pre[q.b]);
+            q.n = pre[q.b + 1] - pre[q.b];
+        }
+    }
+}
+
+// ------------------------------------------------------------------ the loading warp
+template <int D, bool E4M3>
+__device__ void load_role(const PagedAttnParams& p, const CUtensorMap* tk, const CUtensorMap* tv,
+                          const CUtensorMap* tks, const CUtensorMap* tvs, uint32_t ring, uint32_t scales, uint64_t* full,
+                          uint64_t* empty, const int* pre, long long w0, long long w1, const WaitCtl& wc) {
+    using C = Cfg<D, E4M3>;
+    const PagedKV& kv = p.kv;
+    const int lane = threadIdx.x & 31;
+    const int rows = p.box_rows;          // of a box; a lane loads one
+    const int boxes = kTile / rows;       // at most 8: pages are multiples of 16 rows
+    const uint64_t policy = make_policy_evict_first();
+    constexpr uint32_t kBytes = C::kSlotBytes + (E4M3 ? kTile * 4 : 0);
+    uint32_t it = 0;
+    bool ok = true;
+    for_each_part(p, pre, w0, w1, [&](const Part& q) -> bool {
+        const PagedSeq s = paged_seq(kv, q.b);
+        const Tiles kt = key_tiles(p, s);
+        int page = -1, row = 0;
+        auto look = [&](int t) {  // the page of this lane's box of tile t; no page behind the last key
+            const int pos = (t < kt.ns ? t : kt.lo + t - kt.ns) * kTile + lane * rows;
+            page = -1;
+            row = 0;
+            if (lane < boxes && pos < s.L) page = paged_page(kv, q.b, pos, row);
+        };
+        look(q.ta);
+        for (int t = q.ta; t < q.tb; ++t) {
+            const int pg = page, y = q.h * kv.page + row;
+            if (t + 1 < q.tb) look(t + 1);
+#pragma unroll
+            for (int half = 0; half < 2; ++half, ++it) {
+                const uint32_t slot = it % C::kSlots;
+                ok = __all_sync(0xffffffffu, mbar_wait(&empty[slot], ((it / C::kSlots) & 1u) ^ 1u, wc, 20));
+                if (!ok) return false;
+                if (lane == 0) mbar_arrive_expect_tx(&full[slot], kBytes);
+                __syncwarp();
+                if (lane < boxes) {
+                    const CUtensorMap* map = half ? tv : tk;
+                    const uint32_t dst = ring + slot * C::kSlotBytes;
+                    if constexpr (E4M3) {
+                        tma_load_3d(dst + lane * rows * D, map, &full[slot], 0, y, pg, policy);
+                        tma_load_2d(scales + slot * C::kScaleBytes + lane * max(rows * 4, 128), half ? tvs : tks, &full[slot], y, pg,
+                                    policy);
+                    } else {
+#pragma unroll
+                        for (int x = 0; x < D / 64; ++x)
+                            tma_load_3d(dst + x * kTile * 128 + lane * rows * 128, map, &full[slot], x * 64, y, pg, policy);
+                    }
+                }
+            }
+        }
+        return true;
+    });
+    if (!ok && lane == 0) {  // let the copies in flight land before the block ends
+        for (uint32_t s = 0; s < (uint32_t)C::kSlots && s < it; ++s) {
+            const uint32_t last = it - 1 - ((it - 1 - s) % C::kSlots);
+            drain_wait(&full[s], (last / C::kSlots) & 1u, wc.timeout_ns);
+        }
+    }
+}
+
+// ------------------------------------------------------------------ the computing warps
+// Byte offset of the 16-byte chunk `c` of key row r in a tile as TMA stored it (128-byte swizzle;
+// 64-byte for rows of 64 bytes).
+template <int D, bool E4M3>
+__device__ __forceinline__ uint32_t chunk_at(int r, int c) {
+    if constexpr (!E4M3) return (c >> 3) * (kTile * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+    else if constexpr (D == 128) return r * 128 + ((c ^ (r & 7)) << 4);
+    else return r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+}
+
+// Weight of a partial result with running max m when the joint one is M.  All -inf: nothing was
+// seen (sums are 0), or only scores that are no numbers, which have to come through.
+__device__ __forceinline__ float weight(float m, float M) {
+    return m == -INFINITY ? (M == -INFINITY ? 1.f : 0.f) : ex2(m - M);
+}
+__device__ __forceinline__ float add_weighted(float sum, float w, float x) {
+    return (w == 0.f && x == x) ? sum : fmaf(w, x, sum);
+}
+// What turns sum p' u into out.
+template <bool E4M3>
+__device__ __forceinline__ float out_factor(float M, float Ms, float L) {
+    if (L == 0.f) return 0.f;
+    return (E4M3 && M != -INFINITY) ? ex2(M - kF16Up - Ms) / L : 1.f / L;
+}
+
+__device__ __forceinline__ float bf16_add_nonfinite(float acc, uint16_t bits) {
+    return (bits & 0x7f80u) == 0x7f80u ? acc + __uint_as_float(static_cast<uint32_t>(bits) << 16) : acc;
+}
+
+template <int D, bool E4M3>
+__device__ void compute_role(const PagedAttnParams& p, uint8_t* smem, uint64_t* full, uint64_t* empty, const int* pre,
+                             long long w0, long long w1, const WaitCtl& wc) {
+    using C = Cfg<D, E4M3>;
+    const PagedKV& kv = p.kv;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31, c4 = lane & 3, r8 = lane >> 2;
+    const uint32_t ring = smem_u32(smem);
+    float* so = reinterpret_cast<float*>(smem + C::kOOff);
+    float* sm = reinterpret_cast<float*>(smem + C::kMlOff);
+    float* sms = sm + kWarps * kRows;
+    float* sl = sms + kWarps * kRows;
+    // this warp's scales in a slot (boxes of 16 rows lie 128 bytes apart)
+    const float* scales = reinterpret_cast<const float*>(smem + C::kScaleOff) + (p.box_rows == 16 ? 32 : 16) * warp + 2 * c4;
+    PagedPartial* parts = static_cast<PagedPartial*>(p.workspace);
+    uint32_t it = 0;
+    bool ok = true;
+    int first = 1;
+    for_each_part(p, pre, w0, w1, [&](const Part& q) -> bool {
+        const PagedSeq s = paged_seq(kv, q.b);
+        const Tiles kt = key_tiles(p, s);
+        const int T = min(s.T, p.max_q), R = T * p.g;
+        const bool two = R > 8;
+        // this thread's rows r8 and r8 + 8: their q as matrix operands, and the keys they see
+        uint32_t qa[D / 16][4];
+        float cs[2] = {kLog2e, kLog2e};
+        int hi[2], lo[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const int r = r8 + 8 * x, t = r / p.g;
+            const int i = s.base + t;
+            hi[x] = p.causal ? i + 1 : s.L;
+            lo[x] = p.window > 0 ? i - p.window + 1 : 0;
+            const uint16_t* src = static_cast<const uint16_t*>(p.q) + (s.q0 + t) * p.q_ts + (q.h * p.g + r - t * p.g) * p.q_hs;
+            const bool live = r < R;
+            if constexpr (E4M3) {
+                uint2 w[D / 16];
+                uint32_t m = 0;
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) {
+                    w[k] = live ? __ldg(reinterpret_cast<const uint2*>(src + 16 * k + 4 * c4)) : make_uint2(0, 0);
+                    m = __vmaxu2(m, __vmaxu2(w[k].x & 0x7fff7fffu, w[k].y & 0x7fff7fffu));
+                }
+                m = max(m & 0xffffu, m >> 16);
+                m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+                m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+                // largest element in [2^13, 2^14): exponent field m >> 7 becomes 127 + 13
+                const int e = min(max(static_cast<int>(m >> 7), 16), 254);
+                const float up = __uint_as_float(static_cast<uint32_t>(127 + 13 + 127 - e) << 23);
+                cs[x] = kLog2e * __uint_as_float(static_cast<uint32_t>(e - 13) << 23);
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) {
+                    qa[k][x] = pack_f16x2(__uint_as_float(w[k].x << 16) * up, __uint_as_float(w[k].x & 0xffff0000u) * up);
+                    qa[k][2 + x] = pack_f16x2(__uint_as_float(w[k].y << 16) * up, __uint_as_float(w[k].y & 0xffff0000u) * up);
+                }
+            } else {
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) {
+                    qa[k][x] = live ? __ldg(reinterpret_cast<const uint32_t*>(src + 16 * k + 2 * c4)) : 0u;
+                    qa[k][2 + x] = live ? __ldg(reinterpret_cast<const uint32_t*>(src + 16 * k + 8 + 2 * c4)) : 0u;
+                }
+            }
+        }
+        float o[D / 8][4];
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
+        float m[2] = {-INFINITY, -INFINITY}, ms[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+        bool bad_v = false;  // a value that is no number, in a tile that not every row sees whole
+        const int see_lo = s.base + T - p.window;  // the window of the last row begins here
+        for (int t = q.ta; t < q.tb; ++t) {
+            const int j0 = (t < kt.ns ? t : kt.lo + t - kt.ns) * kTile;
+            // does every row see every key of the tile?
+            const bool whole = j0 + kTile <= (p.causal ? s.base + 1 : s.L) &&
+                               (p.window == 0 || j0 >= see_lo || j0 + kTile <= p.sinks);
+            // ---- S = Q K^T
+            uint32_t slot = it % C::kSlots;
+            ok = __all_sync(0xffffffffu, mbar_wait(&full[slot], (it / C::kSlots) & 1u, wc));
+            if (!ok) break;
+            float sc[2][4] = {};
+            uint32_t base = ring + slot * C::kSlotBytes;
+            if constexpr (E4M3) {
+                // matrices: keys 0-7 and 8-15 of chunk 2 x, then of chunk 2 x + 1
+                const int kr = warp * 16 + (lane & 15);
+#pragma unroll
+                for (int x = 0; x < D / 32; ++x) {
+                    uint32_t b[4];
+                    ldmatrix4(b, base + chunk_at<D, E4M3>(kr, 2 * x + (lane >> 4)));
+#pragma unroll
+                    for (int y = 0; y < 2; ++y)
+#pragma unroll
+                        for (int nt = 0; nt < 2; ++nt)
+                            mma16816<true>(sc[nt], qa[2 * x + y], e4m3x2_f16x2(b[2 * y + nt] & 0xffffu), e4m3x2_f16x2(b[2 * y + nt] >> 16));
+                }
+            } else {
+                // matrices: keys 0-7 of chunks 2 k and 2 k + 1, then keys 8-15
+                const int kr = warp * 16 + (lane & 7) + ((lane >> 4) << 3);
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) {
+                    uint32_t b[4];
+                    ldmatrix4(b, base + chunk_at<D, E4M3>(kr, 2 * k + ((lane >> 3) & 1)));
+                    mma16816<false>(sc[0], qa[k], b[0], b[1]);
+                    mma16816<false>(sc[1], qa[k], b[2], b[3]);
+                }
+            }
+            float2 ks[2], vs[2];
+            const int kc = warp * 16 + 2 * c4;  // keys kc, kc + 1, kc + 8, kc + 9 of the tile
+            if constexpr (E4M3) {
+                const float* f = scales + slot * (C::kScaleBytes / 4);
+                ks[0] = *reinterpret_cast<const float2*>(f);
+                ks[1] = *reinterpret_cast<const float2*>(f + 8);
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&empty[slot]);
+            ++it;
+            slot = it % C::kSlots;
+            ok = __all_sync(0xffffffffu, mbar_wait(&full[slot], (it / C::kSlots) & 1u, wc));
+            if (!ok) break;
+            base = ring + slot * C::kSlotBytes;
+            if constexpr (E4M3) {
+                const float* f = scales + slot * (C::kScaleBytes / 4);
+                vs[0] = *reinterpret_cast<const float2*>(f);
+                vs[1] = *reinterpret_cast<const float2*>(f + 8);
+            }
+            // ---- scores in log2 units, masked
+            float va[4], vm[4];  // e4m3: V scale = 2^va * vm with vm in [1, 2)
+#pragma unroll
+            for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    if constexpr (E4M3) {
+                        const float k1 = e ? ks[nt].y : ks[nt].x;
+                        const uint32_t vb = __float_as_uint(e ? vs[nt].y : vs[nt].x);
+                        // a scale that is no number makes the row no number; exponent 0 is a scale of 0 (a row
+                        // of zeros, from a page that is none)
+                        const int a = static_cast<int>((vb >> 23) & 0xffu);
+                        va[2 * nt + e] = a == 255 ? __uint_as_float(0x7fc00000u) : static_cast<float>(a - 127);
+                        vm[2 * nt + e] = __uint_as_float((vb & 0x7fffffu) | 0x3f800000u);
+                        sc[nt][e] *= k1 * cs[0];
+                        sc[nt][2 + e] *= k1 * cs[1];
+                    } else {
+                        sc[nt][e] *= kLog2e;
+                        sc[nt][2 + e] *= kLog2e;
+                    }
+                }
+            if (!whole) {
+#pragma unroll
+                for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int j = j0 + kc + 8 * nt + (e & 1), x = e >> 1;
+                        const bool see = j < hi[x] && (p.window == 0 || j >= lo[x] || j < p.sinks);
+                        if (!see) sc[nt][e] = -INFINITY;
+                    }
+            }
+            // ---- e4m3: l with a max of each lane's own, then the V scales join the scores
+            if constexpr (E4M3) {
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    if (x == 1 && !two) break;
+                    const float mx = fmaxf(fmaxf(sc[0][2 * x], sc[0][2 * x + 1]), fmaxf(sc[1][2 * x], sc[1][2 * x + 1]));
+                    if (mx > ms[x] + kRescale || (ms[x] == -INFINITY && mx > ms[x])) {
+                        l[x] *= ex2(ms[x] - mx);
+                        ms[x] = mx;
+                    }
+                    const float nm = ms[x] == -INFINITY ? 0.f : -ms[x];
+                    l[x] += (ex2(sc[0][2 * x] + nm) + ex2(sc[0][2 * x + 1] + nm)) + (ex2(sc[1][2 * x] + nm) + ex2(sc[1][2 * x + 1] + nm));
+#pragma unroll
+                    for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)  // (a masked score stays -inf whatever the scale)
+                            if (sc[nt][2 * x + e] != -INFINITY) sc[nt][2 * x + e] += va[2 * nt + e];
+                }
+            }
+            // ---- running max of the row (shared by the four lanes that hold it), p, sums
+            float mx[2];
+#pragma unroll
+            for (int x = 0; x < 2; ++x) mx[x] = fmaxf(fmaxf(sc[0][2 * x], sc[0][2 * x + 1]), fmaxf(sc[1][2 * x], sc[1][2 * x + 1]));
+            mx[0] = fmaxf(mx[0], __shfl_xor_sync(0xffffffffu, mx[0], 1));
+            mx[0] = fmaxf(mx[0], __shfl_xor_sync(0xffffffffu, mx[0], 2));
+            if (two) {
+                mx[1] = fmaxf(mx[1], __shfl_xor_sync(0xffffffffu, mx[1], 1));
+                mx[1] = fmaxf(mx[1], __shfl_xor_sync(0xffffffffu, mx[1], 2));
+            }
+            const bool up0 = mx[0] > m[0] + kRescale || (m[0] == -INFINITY && mx[0] > m[0]);
+            const bool up1 = two && (mx[1] > m[1] + kRescale || (m[1] == -INFINITY && mx[1] > m[1]));
+            if (__any_sync(0xffffffffu, up0 || up1)) {
+                const float f0 = up0 ? ex2(m[0] - mx[0]) : 1.f, f1 = up1 ? ex2(m[1] - mx[1]) : 1.f;
+                if (up0) m[0] = mx[0];
+                if (up1) m[1] = mx[1];
+                if (!E4M3) {
+                    l[0] *= f0;
+                    l[1] *= f1;
+                }
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i) {
+                    o[i][0] *= f0;
+                    o[i][1] *= f0;
+                    o[i][2] *= f1;
+                    o[i][3] *= f1;
+                }
+            }
+            const float up = E4M3 ? kF16Up : 0.f;
+            const float nm[2] = {up - (m[0] == -INFINITY ? 0.f : m[0]), up - (m[1] == -INFINITY ? 0.f : m[1])};
+            uint32_t pa[4], pb[4];
+#pragma unroll
+            for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    pa[2 * nt + x] = pb[2 * nt + x] = 0u;
+                    if (x == 1 && !two) break;
+                    const float a = ex2(sc[nt][2 * x] + nm[x]), b = ex2(sc[nt][2 * x + 1] + nm[x]);
+                    if constexpr (E4M3) {
+                        pa[2 * nt + x] = pack_f16x2(a * vm[2 * nt], b * vm[2 * nt + 1]);
+                    } else {
+                        l[x] += a + b;
+                        const uint32_t h = pack_bf16x2(a, b);
+                        pa[2 * nt + x] = h;
+                        pb[2 * nt + x] = pack_bf16x2(a - __uint_as_float(h << 16), b - __uint_as_float(h & 0xffff0000u));
+                    }
+                }
+            // ---- O += P V; values of keys that no row sees count as zero, whatever they hold
+            uint32_t keep[2] = {0xffffffffu, 0xffffffffu};  // of the key pairs kc, kc + 1 and kc + 8, kc + 9
+            if (!whole) {
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const int j = j0 + kc + 8 * x;
+                    const int wlo = p.window > 0 ? s.base - p.window + 1 : 0;
+                    const bool a = j < s.L && (j >= wlo || j < p.sinks);
+                    const bool b = j + 1 < s.L && (j + 1 >= wlo || j + 1 < p.sinks);
+                    keep[x] = (a ? 0xffffu : 0u) | (b ? 0xffff0000u : 0u);
+                }
+            }
+            const int vr = warp * 16 + (lane & 15);  // matrices: keys 0-7 and 8-15 of a chunk, then of the next
+#pragma unroll
+            for (int x = 0; x < (E4M3 ? D / 32 : D / 16); ++x) {
+                uint32_t b[4];
+                ldmatrix4_t(b, base + chunk_at<D, E4M3>(vr, 2 * x + (lane >> 4)));
+                if (!whole) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) b[e] &= keep[e & 1];
+                    if (!E4M3 && T > 1) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const uint32_t b0 = (b[e] & 0x7f80u) == 0x7f80u ? 0xffffu : 0u;
+                            const uint32_t b1 = (b[e] & 0x7f800000u) == 0x7f800000u ? 0xffff0000u : 0u;
+                            if (b0 | b1) bad_v = true;
+                            b[e] &= ~(b0 | b1);
+                        }
+                    }
+                }
+                if constexpr (E4M3) {
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {  // chunk 2 x + y: columns of even and of odd elements
+                        const uint32_t ev = __byte_perm(b[2 * y], b[2 * y + 1], 0x6420), od = __byte_perm(b[2 * y], b[2 * y + 1], 0x7531);
+                        mma16816<true>(o[4 * x + 2 * y], pa, e4m3x2_f16x2(ev & 0xffffu), e4m3x2_f16x2(ev >> 16));
+                        mma16816<true>(o[4 * x + 2 * y + 1], pa, e4m3x2_f16x2(od & 0xffffu), e4m3x2_f16x2(od >> 16));
+                    }
+                } else {
+                    mma16816<false>(o[2 * x], pa, b[0], b[1]);
+                    mma16816<false>(o[2 * x + 1], pa, b[2], b[3]);
+                    mma16816<false>(o[2 * x], pb, b[0], b[1]);
+                    mma16816<false>(o[2 * x + 1], pb, b[2], b[3]);
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&empty[slot]);
+            ++it;
+        }
+        // ---- the warps' results meet: rows 0-7, then rows 8-15
+        const bool cut = q.ta > 0 || q.tb < q.n;
+        const int slot_i = 2 * blockIdx.x + (first ? 0 : 1);
+        PagedPartial* part = parts + slot_i;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            if constexpr (E4M3) {  // the lanes' sums to one max
+                float top = fmaxf(ms[x], __shfl_xor_sync(0xffffffffu, ms[x], 1));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                if (ms[x] != -INFINITY) l[x] *= ex2(ms[x] - top);
+                ms[x] = top;
+            } else {
+                ms[x] = m[x];
+            }
+            l[x] += __shfl_xor_sync(0xffffffffu, l[x], 1);
+            l[x] += __shfl_xor_sync(0xffffffffu, l[x], 2);
+            if (c4 == 0) {
+                sm[warp * kRows + r8 + 8 * x] = m[x];
+                sms[warp * kRows + r8 + 8 * x] = ms[x];
+                sl[warp * kRows + r8 + 8 * x] = l[x];
+            }
+        }
+        for (int x = 0; x < (two ? 2 : 1); ++x) {
+            float* dst = so + (warp * 8 + r8) * C::kOStride;
+#pragma unroll
+            for (int i = 0; i < D / 8; i += 2) {
+                const float a0 = x ? o[i][2] : o[i][0], a1 = x ? o[i][3] : o[i][1];
+                const float b0 = x ? o[i + 1][2] : o[i + 1][0], b1 = x ? o[i + 1][3] : o[i + 1][1];
+                if constexpr (E4M3) {
+                    *reinterpret_cast<float4*>(dst + 8 * i + 4 * c4) = make_float4(a0, b0, a1, b1);
+                } else {
+                    *reinterpret_cast<float2*>(dst + 8 * i + 2 * c4) = make_float2(a0, a1);
+                    *reinterpret_cast<float2*>(dst + 8 * i + 8 + 2 * c4) = make_float2(b0, b1);
+                }
+            }
+            // (a warp that gave up still comes here, so that none waits for it)
+            ok = named_bar_and(kBar, kWarps * 32, ok);
+            const bool any_bad = !named_bar_and(kBar, kWarps * 32, !bad_v);
+            if (!ok) return false;
+            const int tid = threadIdx.x, row8 = tid / 32, r = row8 + 8 * x;
+            if (r < R) {
+                float M = -INFINITY, Ms = -INFINITY;
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) {
+                    M = fmaxf(M, sm[w * kRows + r]);
+                    Ms = fmaxf(Ms, sms[w * kRows + r]);
+                }
+                float f[kWarps], L = 0.f;
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) {
+                    f[w] = weight(sm[w * kRows + r], M);
+                    L = add_weighted(L, weight(sms[w * kRows + r], Ms), sl[w * kRows + r]);
+                }
+                const int t = r / p.g, head = q.h * p.g + r - t * p.g, tok = s.q0 + t;
+                for (int d = 4 * lane; d < D; d += 128) {
+                    float acc[4] = {};
+#pragma unroll
+                    for (int w = 0; w < kWarps; ++w) {
+                        const float4 v = *reinterpret_cast<const float4*>(so + (w * 8 + row8) * C::kOStride + d);
+                        acc[0] = fmaf(f[w], v.x, acc[0]);
+                        acc[1] = fmaf(f[w], v.y, acc[1]);
+                        acc[2] = fmaf(f[w], v.z, acc[2]);
+                        acc[3] = fmaf(f[w], v.w, acc[3]);
+                    }
+                    if (!E4M3 && any_bad) {  // values that are no numbers, of the keys this row sees
+                        const int i = s.base + t, rhi = p.causal ? i + 1 : s.L, rlo = p.window > 0 ? i - p.window + 1 : 0;
+                        for (int tt = q.ta; tt < q.tb; ++tt) {
+                            const int j0 = (tt < kt.ns ? tt : kt.lo + tt - kt.ns) * kTile;
+                            if (j0 + kTile <= (p.causal ? s.base + 1 : s.L) && (p.window == 0 || j0 >= see_lo || j0 + kTile <= p.sinks))
+                                continue;  // its values went into the product as they are
+                            for (int j = j0; j < min(j0 + kTile, rhi); ++j) {
+                                if (p.window > 0 && j < rlo && j >= p.sinks) continue;
+                                int row;
+                                const int pg = paged_page(kv, q.b, j, row);
+                                if (pg < 0) continue;
+                                const uint16_t* v = static_cast<const uint16_t*>(kv.v) + pg * kv.v_ps + (static_cast<long long>(q.h) * kv.page + row) * D + d;
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) acc[e] = bf16_add_nonfinite(acc[e], v[e]);
+                            }
+                        }
+                    }
+                    if (cut) {
+                        *reinterpret_cast<float4*>(&part->o[r * kPagedMaxD + d]) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+                    } else {
+                        paged_store4(p, tok, head, d, acc, out_factor<E4M3>(M, Ms, L));
+                    }
+                }
+                if (lane == 0) {
+                    if (cut) {
+                        part->m[r] = M;
+                        part->ms[r] = Ms;
+                        part->l[r] = L;
+                    } else {
+                        p.lse[tok * p.l_ts + head * p.l_hs] = L == 0.f ? -INFINITY : (Ms + log2f(L)) * kLn2;
+                    }
+                }
+            }
+            named_bar_sync(kBar, kWarps * 32);  // the buffers are free again
+        }
+        if (threadIdx.x == 0) {
+            if (cut) {
+                part->b = q.b;
+                part->h = q.h;
+                part->begins = q.ta == 0;
+            } else {
+                part->b = -1;
+            }
+        }
+        first = 0;
+        return true;
+    });
+}
+
+template <int D, bool E4M3>
+__global__ void __launch_bounds__(kThreads, 1)
+    paged_decode_kernel(const __grid_constant__ PagedAttnParams p, const __grid_constant__ CUtensorMap tk,
+                        const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tks,
+                        const __grid_constant__ CUtensorMap tvs) {
+    using C = Cfg<D, E4M3>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    __shared__ __align__(8) uint64_t full[C::kSlots];
+    __shared__ __align__(8) uint64_t empty[C::kSlots];
+    __shared__ int scratch[kWarps + 1];
+    __shared__ int abort_flag;
+    int* pre = reinterpret_cast<int*>(smem + C::kPreOff);
+    launch_dependents();
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < C::kSlots; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], kWarps);
+        }
+        abort_flag = 0;
+        fence_mbar_init();
+    }
+    const long long W = static_cast<long long>(share_tiles(p, pre, scratch)) * p.kv.hkv;
+    // the first W % grid blocks take one tile more: blocks without any are the last ones
+    const long long each = W / gridDim.x, more = W % gridDim.x, x = blockIdx.x;
+    const long long w0 = x * each + min(x, more), w1 = w0 + each + (x < more ? 1 : 0);
+    PagedPartial* parts = static_cast<PagedPartial*>(p.workspace) + 2 * blockIdx.x;
+    if (threadIdx.x < 2) parts[threadIdx.x].b = -1;  // until a cut pair says otherwise
+    __syncthreads();
+    const WaitCtl wc{&abort_flag, p.err, p.timeout_ns};
+    if (threadIdx.x / 32 == kWarps)
+        load_role<D, E4M3>(p, &tk, &tv, &tks, &tvs, smem_u32(smem), smem_u32(smem) + C::kScaleOff, full, empty, pre, w0, w1, wc);
+    else
+        compute_role<D, E4M3>(p, smem, full, empty, pre, w0, w1, wc);
+}
+
+// Joins the parts of pairs that were cut.  Block (x, r): if a pair begins in block x of the first
+// kernel and goes on in block x + 1, row r of that pair.
+template <int D, bool E4M3>
+__global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__ PagedAttnParams p, int shares) {
+    constexpr int kSub = 8;
+    __shared__ float so[kSub][D], sl[kSub];
+    __shared__ int hdr[2 * kPagedMaxShares][2];  // pair (sequence and head, -1: none), and whether it begins there
+    wait_primary();
+    const PagedPartial* parts = static_cast<const PagedPartial*>(p.workspace);
+    for (int i = threadIdx.x; i < 2 * shares; i += 256) {
+        const int b = parts[i].b;
+        hdr[i][0] = b < 0 ? -1 : b * p.kv.hkv + parts[i].h;
+        hdr[i][1] = b < 0 ? 0 : parts[i].begins;
+    }
+    __syncthreads();
+    const int x = blockIdx.x, r = blockIdx.y;
+    // the pair of x that begins in x and goes on: its last cut part
+    const int i0 = hdr[2 * x + 1][0] >= 0 ? 2 * x + 1 : 2 * x;
+    const int pair = hdr[i0][0];
+    if (pair < 0 || !hdr[i0][1]) return;
+    int x1 = x + 1;  // parts: i0, then the first of every block up to x1
+    while (x1 < shares && hdr[2 * x1][0] == pair && !hdr[2 * x1][1]) ++x1;
+    const int b = pair / p.kv.hkv, h = pair - b * p.kv.hkv;
+    const PagedSeq s = paged_seq(p.kv, b);
+    const int t = r / p.g;
+    if (t >= min(s.T, p.max_q)) return;
+    const int n = x1 - x, warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+    float M = -INFINITY, Ms = -INFINITY;
+    for (int k = lane; k < n; k += 32) {
+        const PagedPartial* q = parts + (k == 0 ? i0 : 2 * (x + k));
+        M = fmaxf(M, q->m[r]);
+        Ms = fmaxf(Ms, q->ms[r]);
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+        Ms = fmaxf(Ms, __shfl_xor_sync(0xffffffffu, Ms, o));
+    }
+    float l = 0.f, acc[4] = {};
+#pragma unroll 4
+    for (int k = warp; k < n; k += kSub) {
+        const PagedPartial* q = parts + (k == 0 ? i0 : 2 * (x + k));
+        const float f = weight(q->m[r], M);
+        l = add_weighted(l, weight(q->ms[r], Ms), q->l[r]);
+        if (4 * lane < D) {
+            const float4 v = *reinterpret_cast<const float4*>(&q->o[r * kPagedMaxD + 4 * lane]);
+            acc[0] = fmaf(f, v.x, acc[0]);
+            acc[1] = fmaf(f, v.y, acc[1]);
+            acc[2] = fmaf(f, v.z, acc[2]);
+            acc[3] = fmaf(f, v.w, acc[3]);
+        }
+    }
+    if (4 * lane < D) *reinterpret_cast<float4*>(&so[warp][4 * lane]) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+    if (lane == 0) sl[warp] = l;
+    __syncthreads();
+    if (warp != 0) return;
+    l = 0.f;
+#pragma unroll
+    for (int w = 0; w < kSub; ++w) l += sl[w];
+    const int head = h * p.g + r - t * p.g, tok = s.q0 + t;
+    if (4 * lane < D) {
+        float v[4] = {};
+#pragma unroll
+        for (int w = 0; w < kSub; ++w)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] += so[w][4 * lane + e];
+        paged_store4(p, tok, head, 4 * lane, v, out_factor<E4M3>(M, Ms, l));
+    }
+    if (lane == 0) p.lse[tok * p.l_ts + head * p.l_hs] = l == 0.f ? -INFINITY : (Ms + log2f(l)) * kLn2;
+}
+
+template <int D, bool E4M3>
+int launch_t(const PagedAttnParams& p, const PagedMaps& m, int shares, cudaStream_t stream) {
+    using C = Cfg<D, E4M3>;
+    auto kern = paged_decode_kernel<D, E4M3>;
+    const int bytes = C::kFixedBytes + 4 * (p.kv.batch + 1);
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return -4;
+    kern<<<shares, kThreads, bytes, stream>>>(p, m.k, m.v, m.ks, m.vs);
+    if (cudaGetLastError() != cudaSuccess) return -4;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(shares, p.max_q * p.g);
+    cfg.blockDim = dim3(256);
+    cfg.stream = stream;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, paged_join_kernel<D, E4M3>, p, shares) == cudaSuccess ? 0 : -4;
+}
+
+}  // namespace
+
+int launch_paged_decode(const PagedAttnParams& p, const PagedMaps& m, int shares, cudaStream_t stream) {
+    if (p.kv.d == 128) return p.kv.e4m3 ? launch_t<128, true>(p, m, shares, stream) : launch_t<128, false>(p, m, shares, stream);
+    return p.kv.e4m3 ? launch_t<64, true>(p, m, shares, stream) : launch_t<64, false>(p, m, shares, stream);
+}
+
+}  // namespace ra
