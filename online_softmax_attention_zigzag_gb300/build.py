@@ -25,7 +25,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libringattn.so")
 LIB_CHECK = os.path.join(PKG, "libringattn_check.so")  # -DRA_CHECK: index checks in the kernels
 SOURCES = ["api.cu", "attn_bf16.cu", "attn_f32.cu", "permute_merge.cu", "ulysses.cu", "attn_bwd.cu",
-           "paged_cache.cu", "paged_attn.cu", "paged_decode.cu"]
+           "paged_cache.cu", "paged_decode.cu", "paged_chunk.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-I", INCLUDE, "-I", CSRC]

@@ -1,6 +1,6 @@
 // api.cu -- the C ABI of libringattn.so (declared in include/ringattn.h): argument
 // validation, device checks, TMA descriptors, work geometry and kernel launches.
-// Host code only; the compute is in attn_bf16.cu, attn_f32.cu and permute_merge.cu.
+// Host code only; the compute is in the other files.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
@@ -645,11 +645,49 @@ int encode_scales(CUtensorMap* map, const float* base, long long page_stride, co
     return r == CUDA_SUCCESS ? RA_OK : RA_ERR_CUDA;
 }
 
+// Rows of a sequence and KV head decide the kernel: up to 16 the few-row one, which 16-row matrix
+// instructions serve; a chunk item fills 256 rows and does 17 at the cost of 128, which the loads
+// still hide.
+bool paged_few(int total, int g, int max_q) {
+    return static_cast<long long>(max_q < total ? max_q : total) * g <= ra::kPagedFewRows;
+}
+
+// Bytes of the workspace: two partial results a block, and for chunks the list of items (a
+// 64-bit count an item, an index a sequence).
+long long paged_workspace(int total, int batch, int g, int max_q, ra::PagedAttnParams* p) {
+    long long n = 2LL * ra::kPagedMaxShares;
+    if (paged_few(total, g, max_q)) {
+        n *= sizeof(ra::PagedPartial);
+    } else {
+        n *= sizeof(ra::PagedChunkPartial);
+        const int unit = g <= 128 ? 128 / g : 1;
+        const long long pairs = total / (2 * unit) + batch;
+        if (p) {
+            p->unit_tokens = unit;
+            p->max_pairs = static_cast<int>(pairs);
+            p->plan_off = n;
+        }
+        n += 8 * (pairs + 1) + 4LL * (batch + 1);
+    }
+    return (n + 255) / 256 * 256;
+}
+
 int encode_paged(const ra::PagedAttnParams& p, ra::PagedMaps* m) {
     const ra::PagedKV& kv = p.kv;
     int st;
     if ((st = encode_pool(&m->k, kv.k, kv.k_ps, kv, p.box_rows)) != RA_OK) return st;
     if ((st = encode_pool(&m->v, kv.v, kv.v_ps, kv, p.box_rows)) != RA_OK) return st;
+    if (p.unit_tokens > 0) {  // q as [total, Hq, d], boxes of a unit's tokens x the heads of a KV head x 64
+        cuuint64_t dims[3] = {static_cast<cuuint64_t>(kv.d), static_cast<cuuint64_t>(p.hq), static_cast<cuuint64_t>(kv.total)};
+        cuuint64_t strides[2] = {static_cast<cuuint64_t>(p.q_hs) * 2, static_cast<cuuint64_t>(p.q_ts) * 2};
+        cuuint32_t box[3] = {64, static_cast<cuuint32_t>(p.g), static_cast<cuuint32_t>(p.unit_tokens)};
+        cuuint32_t estr[3] = {1, 1, 1};
+        return g_encode(&m->q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(p.q), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+                   ? RA_OK
+                   : RA_ERR_CUDA;
+    }
     if (!kv.e4m3) return RA_OK;
     if ((st = encode_scales(&m->ks, kv.k_scale, kv.ks_ps, kv, p.box_rows)) != RA_OK) return st;
     return encode_scales(&m->vs, kv.v_scale, kv.vs_ps, kv, p.box_rows);
@@ -831,7 +869,7 @@ int ringattn_cache_read(const ra_paged_kv* kv, void* k_out, void* v_out, ra_stre
 int ringattn_paged_workspace_bytes(int total, int batch, int Hq, int Hkv, int d, int max_q, long long* bytes) {
     if (!bytes || total < 0 || batch < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || d < 1 || max_q < 1)
         return RA_ERR_INVALID_ARG;
-    *bytes = (2LL * ra::kPagedMaxShares * static_cast<long long>(sizeof(ra::PagedPartial)) + 255) / 256 * 256;
+    *bytes = paged_workspace(total, batch, Hq / Hkv, max_q, nullptr);
     return RA_OK;
 }
 
@@ -853,12 +891,9 @@ int ringattn_fwd_paged(const void* q, long long q_token_stride, long long q_head
     if (!row_strides_ok(q_token_stride, q_head_stride, p.kv.d) || !row_strides_ok(out_token_stride, out_head_stride, p.kv.d))
         return RA_ERR_INVALID_ARG;
     if (lse_token_stride < 1 || lse_head_stride < 1) return RA_ERR_INVALID_ARG;
-    long long need = 0;
-    if ((st = ringattn_paged_workspace_bytes(p.kv.total, p.kv.batch, Hq, p.kv.hkv, p.kv.d, max_q, &need)) != RA_OK)
-        return st;
-    if (workspace_bytes < need) return RA_ERR_INVALID_ARG;
     p.g = Hq / p.kv.hkv;
     if (p.g > 128 || static_cast<long long>(p.kv.total) * Hq > INT_MAX) return RA_ERR_UNSUPPORTED;
+    if (workspace_bytes < paged_workspace(p.kv.total, p.kv.batch, p.g, max_q, &p)) return RA_ERR_INVALID_ARG;
     DeviceInfo* dev = nullptr;
     if ((st = device_info(&dev)) != RA_OK) return st;
     p.q = q;
@@ -880,12 +915,12 @@ int ringattn_fwd_paged(const void* q, long long q_token_stride, long long q_head
     p.err = dev->err;
     p.timeout_ns = wait_timeout_ns();
     cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-    if (static_cast<long long>(p.max_q) * p.g > ra::kPagedFewRows) return ra::launch_paged_attn(p, cs);
     p.box_rows = std::gcd(p.kv.page, ra::kPagedTile);
     ra::PagedMaps maps = {};
     if ((st = get_encoder()) != RA_OK || (st = encode_paged(p, &maps)) != RA_OK) return st;
     const int shares = dev->sms < ra::kPagedMaxShares ? dev->sms : ra::kPagedMaxShares;
-    return ra::launch_paged_decode(p, maps, shares, cs);
+    return paged_few(p.kv.total, p.g, max_q) ? ra::launch_paged_decode(p, maps, shares, cs)
+                                             : ra::launch_paged_chunk(p, maps, shares, cs);
 }
 
 int ringattn_rank_work(int S, int c, int causal, int layout, int tile, long long* units, long long* pairs,

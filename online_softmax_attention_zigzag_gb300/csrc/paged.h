@@ -38,6 +38,14 @@ struct PagedKV {
     FastDiv by_page;
 };
 
+// The same of an item (two units of 128 rows) of the chunk kernel: l sums the exact p, lr the p as
+// rounded for the product with V.
+struct PagedChunkPartial {
+    int b, pair, h, begins;
+    float m[2 * 128], l[2 * 128], lr[2 * 128];
+    float o[2 * 128 * kPagedMaxD];
+};
+
 struct PagedCopyParams {  // append: token-major rows in; read: [Hkv, total, d] out
     PagedKV kv;
     const void* k_in;
@@ -55,22 +63,27 @@ struct PagedAttnParams {
     float* lse;
     long long q_ts, q_hs, o_ts, o_hs, l_ts, l_hs;
     int hq, g, max_q, causal, window, sinks, out_f32;
+    // chunk kernel: tokens of a unit (128 / g), most items of one head, and where the list of
+    // items lies in the workspace (behind the partial results)
+    int unit_tokens, max_pairs;
+    long long plan_off;
     int box_rows;  // gcd(page, 128): rows of a TMA box, all on one page
     void* workspace;
     int* err;
     unsigned long long timeout_ns;
 };
 
-struct PagedMaps {  // of the pool; ks and vs only for e4m3
-    CUtensorMap k, v, ks, vs;
+struct PagedMaps {  // of the pool; ks and vs (few rows) only for e4m3; q for chunks
+    CUtensorMap k, v, ks, vs, q;
 };
 
 int launch_cache_append(const PagedCopyParams& p, cudaStream_t stream);
 int launch_cache_read(const PagedCopyParams& p, cudaStream_t stream);
-int launch_paged_attn(const PagedAttnParams& p, cudaStream_t stream);
 // max_q * g <= kPagedFewRows; `shares` blocks (at most kPagedMaxShares), the workspace 2 * shares
 // PagedPartial
 int launch_paged_decode(const PagedAttnParams& p, const PagedMaps& m, int shares, cudaStream_t stream);
+// any number of rows, g <= 128; the workspace 2 * shares PagedChunkPartial and the list of items
+int launch_paged_chunk(const PagedAttnParams& p, const PagedMaps& m, int shares, cudaStream_t stream);
 
 #ifdef __CUDACC__
 // One sequence of the batch: rows [q0, q0 + T) of the token tensors, row t at position
@@ -111,6 +124,18 @@ __device__ __forceinline__ int paged_find(const int* cu, int batch, int t) {
     return lo;
 }
 
+// Weight of a partial result with running max m when the joint one is M.  All -inf: nothing was
+// seen (sums are 0), or only scores that are no numbers, which have to come through.
+__device__ __forceinline__ float paged_weight(float m, float M) {
+    if (m == -INFINITY) return M == -INFINITY ? 1.f : 0.f;
+    float w;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(w) : "f"(m - M));
+    return w;
+}
+__device__ __forceinline__ float paged_add_weighted(float sum, float w, float x) {
+    return (w == 0.f && x == x) ? sum : fmaf(w, x, sum);
+}
+
 // Four elements of an output row, times inv, in the caller's type.
 __device__ __forceinline__ void paged_store4(const PagedAttnParams& p, int tok, int head, int d, const float (&x)[4],
                                              float inv) {
@@ -123,6 +148,27 @@ __device__ __forceinline__ void paged_store4(const PagedAttnParams& p, int tok, 
         asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w.x) : "f"(x[1] * inv), "f"(x[0] * inv));
         asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w.y) : "f"(x[3] * inv), "f"(x[2] * inv));
         *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at) = w;
+    }
+}
+// A whole output row, times inv: 16-byte stores (rows start on 16 bytes).
+template <int D>
+__device__ __forceinline__ void paged_store_row(const PagedAttnParams& p, int tok, int head, const float (&o)[D], float inv) {
+    const long long at = tok * p.o_ts + head * p.o_hs;
+    if (p.out_f32) {
+        float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.out) + at);
+#pragma unroll
+        for (int i = 0; i < D / 4; ++i)
+            dst[i] = make_float4(o[4 * i] * inv, o[4 * i + 1] * inv, o[4 * i + 2] * inv, o[4 * i + 3] * inv);
+    } else {
+        uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + at);
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[e]) : "f"(o[8 * i + 2 * e + 1] * inv), "f"(o[8 * i + 2 * e] * inv));
+            dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
     }
 }
 #endif

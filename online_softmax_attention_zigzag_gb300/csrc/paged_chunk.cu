@@ -1,0 +1,950 @@
+// paged_chunk.cu -- attention of a chunk of new tokens over a paged K/V cache on the tcgen05 tensor
+// cores: more rows of a sequence and KV head than the few-row kernel takes.
+//
+// The mathematics is the ring kernel's (one online softmax over tiles of 128 keys, the running
+// max moved only when it is exceeded by 2^8, out = sum of bf16(p) v / sum of bf16(p), lse from the
+// unrounded p).  What differs:
+//   * rows: a unit is 128 / g tokens times the g query heads of a KV head, so that grouped heads
+//     share every K/V tile inside one matrix tile; an item is two units.
+//   * keys: tiles come page by page, a TMA box is gcd(page, 128) rows of one page; a tile is read
+//     when some row of the item sees a key of it (sinks first, then the window up to the last
+//     row's position).
+//   * work: the key tiles of all (sequence, head, pair of units) items in one line are dealt to
+//     the blocks in equal contiguous shares; an item that lies in several shares leaves
+//     partial results that a join kernel combines.  Every SM then ends within one tile of
+//     the others, whatever the lengths are, at the price of 2 * 132 KB of partial results a
+//     block, about two tiles' time.  The list of items is made on the device by a one-block
+//     kernel, because the lengths are there.
+//   * values: a row of P is 0 where a key is hidden, but 0 * NaN is NaN, so tiles that not every
+//     row sees whole have their V looked over before the product: rows that nobody sees
+//     become zeros, and infinities and NaN become zeros that the rows that do see them add at
+//     the end.
+//   * e4m3: four warps expand codes into the bf16 tiles: exponent and mantissa bits moved into
+//     place are the value times 2^-120, exact for subnormal codes too, and one packed
+//     multiplication by 2^120 * scale finishes it, exact for scales that are powers of two.
+//
+// Warps: 0-7 softmax (four a unit), 8 and 9 issue the units' MMAs, 10 loads, 11 (bf16) looks
+// values over; e4m3: 12-15 expand and look over.  TMEM as in the ring kernel: S_x at
+// [128 x, 128 x + 128), P_x over the upper half of S_x, O_x at 256 + D x.
+#include <cuda_bf16.h>
+
+#include "paged.h"
+#include "ptx_paged.cuh"
+
+namespace ra {
+namespace {
+
+constexpr int kTile = kPagedTile;
+constexpr int kMmaWarp = 8, kLoadWarp = 10, kExpandWarp = 12;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.69314718055994531f;
+constexpr float kRescaleLog2 = 8.0f;
+constexpr int kPoison = 8;  // marks of the last parts, in turn: part k's holds k + 1 if it needs care
+
+template <int D, bool E4M3>
+struct Cfg {
+    static constexpr int kThreads = E4M3 ? 512 : 384;
+    static constexpr int kTileBytes = kTile * D * 2;  // a bf16 tile
+    static constexpr int kBoxBytes = kTile * 128;     // 64 columns of it
+    static constexpr int kBoxes = D / 64;
+    static constexpr int kRawBytes = kTile * D;       // an e4m3 tile as it comes
+    static constexpr int kStageBytes = 2 * kTileBytes;  // V of one tile and K of the next
+    static constexpr int kStages = D == 128 ? 2 : 4;
+    static constexpr int kRaw = E4M3 ? (D == 128 ? 2 : 4) : 0;
+    static constexpr int kKVOff = 2 * kTileBytes;
+    static constexpr int kRawOff = kKVOff + kStages * kStageBytes;
+    static constexpr int kSmemBytes = kRawOff + kRaw * kRawBytes + 1024;
+    static constexpr uint32_t kTmemCols = 512;
+    static constexpr uint32_t kOCol = 256;
+};
+
+struct Bars {
+    uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_done[2], o_free[2], drain[2];
+    uint64_t kv_full[4], kv_empty[4];
+    uint64_t fixed[2];                // bf16: a tile's values have been looked over
+    uint64_t raw_full[4], raw_empty[4];  // e4m3
+};
+struct Shared {
+    Bars b;
+    uint32_t tmem;
+    int abort_flag;
+    uint32_t turn;
+    int poison[kPoison];
+};
+
+// ------------------------------------------------------------------ items
+// Pair `pair` of units of sequence b: tokens [ta, tb) of it, key tiles [0, ns) and from lo on.
+struct Chunk {
+    int b, pair;
+    PagedSeq s;
+    int ta, tb;   // tokens of the item
+    int hi;       // keys at and behind hi are seen by no row
+    int first;    // nor are keys below first that are no sinks
+    int ns, lo, n;
+    __device__ __forceinline__ int key(int t) const { return (t < ns ? t : lo + t - ns) * kTile; }
+};
+
+__device__ __forceinline__ Chunk make_chunk(const PagedAttnParams& p, int b, int pair) {
+    Chunk c;
+    c.b = b;
+    c.pair = pair;
+    c.s = paged_seq(p.kv, b);
+    const int tt = 2 * p.unit_tokens;
+    c.ta = pair * tt;
+    c.tb = min(min(c.s.T, p.max_q), c.ta + tt);
+    c.hi = p.causal ? min(c.s.L, max(0, c.s.base + c.tb)) : c.s.L;
+    c.first = p.window > 0 ? max(0, c.s.base + c.ta - p.window + 1) : 0;
+    const int hi = (c.hi + kTile - 1) / kTile;
+    c.lo = min(c.first / kTile, hi);
+    c.ns = p.window > 0 ? min((min(p.sinks, c.hi) + kTile - 1) / kTile, c.lo) : 0;
+    c.n = max(1, c.ns + hi - c.lo);
+    return c;
+}
+
+// Does every row of the item see every key of the tile at j0?
+__device__ __forceinline__ bool whole_tile(const PagedAttnParams& p, const Chunk& c, int j0) {
+    return j0 + kTile <= (p.causal ? c.s.base + c.ta + 1 : c.s.L) &&
+           (p.window == 0 || j0 >= c.s.base + c.tb - p.window || j0 + kTile <= p.sinks);
+}
+
+__device__ __forceinline__ int pairs_of(const PagedAttnParams& p, int b) {
+    const int tt = 2 * p.unit_tokens;
+    return (min(paged_seq(p.kv, b).T, p.max_q) + tt - 1) / tt;
+}
+
+// The list of items: base[b] = pairs of the sequences before b; pre[e] = tiles of the pairs before
+// pair e (of one head).
+struct Plan {
+    long long* pre;
+    int* base;
+};
+__device__ __forceinline__ Plan plan_at(const PagedAttnParams& p) {
+    Plan x;
+    x.pre = reinterpret_cast<long long*>(static_cast<uint8_t*>(p.workspace) + p.plan_off);
+    x.base = reinterpret_cast<int*>(x.pre + p.max_pairs + 1);
+    return x;
+}
+
+constexpr int kPlanThreads = 1024;
+
+// Exclusive sum over the block; `all` receives the total.
+__device__ __forceinline__ long long block_scan(long long x, long long* scratch, long long& all) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+    long long y = x;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+        const long long z = __shfl_up_sync(0xffffffffu, y, o);
+        if (lane >= o) y += z;
+    }
+    if (lane == 31) scratch[warp] = y;
+    __syncthreads();
+    long long w = scratch[lane], v = w;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+        const long long z = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += z;
+    }
+    all = __shfl_sync(0xffffffffu, v, 31);
+    const long long before = __shfl_sync(0xffffffffu, v - w, warp);
+    __syncthreads();
+    return before + y - x;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const __grid_constant__ PagedAttnParams p) {
+    __shared__ long long scratch[32];
+    launch_dependents();
+    const Plan plan = plan_at(p);
+    const int B = p.kv.batch;
+    long long sum = 0, all;
+    for (int b0 = 0; b0 < B; b0 += kPlanThreads) {
+        const int b = b0 + threadIdx.x;
+        const long long at = block_scan(b < B ? pairs_of(p, b) : 0, scratch, all);
+        // (a cu that decreases could list more than there is room for)
+        if (b < B) plan.base[b] = static_cast<int>(min(sum + at, static_cast<long long>(p.max_pairs)));
+        sum += all;
+    }
+    const int E = static_cast<int>(min(sum, static_cast<long long>(p.max_pairs)));
+    if (threadIdx.x == 0) plan.base[B] = E;
+    __syncthreads();
+    sum = 0;
+    for (int e0 = 0; e0 < E; e0 += kPlanThreads) {
+        const int e = e0 + threadIdx.x;
+        int n = 0;
+        if (e < E) {
+            int lo = 0, hi = B;  // base[lo] <= e < base[hi]
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (plan.base[mid] <= e) lo = mid;
+                else hi = mid;
+            }
+            n = make_chunk(p, lo, e - plan.base[lo]).n;
+        }
+        const long long at = block_scan(n, scratch, all);
+        if (e < E) plan.pre[e] = sum + at;
+        sum += all;
+    }
+    if (threadIdx.x == 0) plan.pre[E] = sum;
+}
+
+// Tiles [ta, tb) of an item, for KV head h.
+struct Part {
+    Chunk c;
+    int h, ta, tb;
+    int k;  // its number in this block's share
+};
+
+// Walks the parts of this block's share: f(part) until it returns false.
+template <class F>
+__device__ __forceinline__ void for_each_part(const PagedAttnParams& p, F&& f) {
+    const Plan plan = plan_at(p);
+    const int B = p.kv.batch, H = p.kv.hkv;
+    const int E = plan.base[B];
+    const long long W = plan.pre[E] * H;
+    // the first W % grid blocks take one tile more: blocks without any are the last ones
+    const long long each = W / gridDim.x, more = W % gridDim.x, x = blockIdx.x;
+    long long w = x * each + min(x, more);
+    const long long w1 = w + each + (x < more ? 1 : 0);
+    if (w >= w1) return;
+    int lo = 0, hi = B;  // the sequence: pre[base[lo]] * H <= w < pre[base[hi]] * H
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (plan.pre[plan.base[mid]] * H <= w) lo = mid;
+        else hi = mid;
+    }
+    int b = lo, e0 = plan.base[b], e1 = plan.base[b + 1];
+    const long long off = plan.pre[e0], per = plan.pre[e1] - off;  // tiles of one head
+    Part q;
+    q.h = static_cast<int>((w - off * H) / per);
+    const long long in = w - off * H - q.h * per + off;
+    lo = e0;
+    hi = e1;  // the pair: pre[lo] <= in < pre[hi]
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (plan.pre[mid] <= in) lo = mid;
+        else hi = mid;
+    }
+    int e = lo;
+    q.ta = static_cast<int>(in - plan.pre[e]);
+    q.k = 0;
+    while (true) {
+        q.c = make_chunk(p, b, e - e0);
+        q.tb = static_cast<int>(min(static_cast<long long>(q.c.n), q.ta + (w1 - w)));
+        if (!f(q)) return;
+        w += q.tb - q.ta;
+        if (w >= w1) return;
+        q.ta = 0;
+        ++q.k;
+        if (++e == e1) {
+            e = e0;
+            if (++q.h == H) {
+                q.h = 0;
+                do {
+                    ++b;
+                    e0 = e1;
+                    e1 = plan.base[b + 1];
+                } while (e1 == e0);
+                e = e0;
+            }
+        }
+    }
+}
+
+// Units of an item: the second is there when its first token is.
+__device__ __forceinline__ int units_of(const PagedAttnParams& p, const Chunk& c) {
+    return c.ta + p.unit_tokens < c.tb ? 2 : 1;
+}
+
+// ------------------------------------------------------------------ the loading warp
+// Stages of a part of n tiles: K(0); V(j-1) with K(j); V(n-1).  V at the stage's base, K a tile
+// above it.  e4m3: the tiles go one by one into the raw ring, in the same order.
+template <int D, bool E4M3>
+__device__ void load_role(const PagedAttnParams& p, const CUtensorMap* tq, const CUtensorMap* tk, const CUtensorMap* tv,
+                          uint32_t smem, Bars& b, const WaitCtl& wc) {
+    using C = Cfg<D, E4M3>;
+    const PagedKV& kv = p.kv;
+    const int lane = threadIdx.x & 31;
+    const int rows = p.box_rows, boxes = kTile / rows;
+    const uint32_t q_bytes = static_cast<uint32_t>(p.unit_tokens * p.g) * 128u * C::kBoxes;
+    const uint64_t keep = make_policy_evict_last(), stream = make_policy_evict_first();
+    uint32_t st = 0, qit[2] = {0, 0};
+    bool ok = true;
+    for_each_part(p, [&](const Part& q) -> bool {
+        const int nx = units_of(p, q.c);
+        for (int x = 0; x < nx; ++x) {
+            ok = __all_sync(0xffffffffu, mbar_wait(&b.q_empty[x], (qit[x] & 1u) ^ 1u, wc, 32));
+            if (!ok) return false;
+            ++qit[x];
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&b.q_full[x], q_bytes);
+                for (int i = 0; i < C::kBoxes; ++i)
+                    tma_load_3d(smem + x * C::kTileBytes + i * C::kBoxBytes, tq, &b.q_full[x], i * 64, q.h * p.g,
+                                q.c.s.q0 + q.c.ta + x * p.unit_tokens, stream);
+            }
+            __syncwarp();
+        }
+        // K and V are read again by the sequence's other pairs, if it has any
+        const uint64_t policy = q.c.s.T > 2 * p.unit_tokens ? keep : stream;
+        int page = -1, row = 0, prev_page = -1, prev_y = 0;
+        auto look = [&](int t) {  // the page of this lane's box; no page behind the last key
+            const int pos = q.c.key(t) + lane * rows;
+            page = -1;
+            row = 0;
+            if (lane < boxes && pos < q.c.hi) page = paged_page(kv, q.c.b, pos, row);
+        };
+        look(q.ta);
+        for (int t = q.ta; t <= q.tb; ++t) {
+            const int pg = page, y = q.h * kv.page + row;
+            if (t + 1 < q.tb) look(t + 1);
+            const bool has_v = t > q.ta, has_k = t < q.tb;
+            if constexpr (E4M3) {
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {  // V(t - 1), then K(t)
+                    if (half ? !has_k : !has_v) continue;
+                    const uint32_t slot = st % C::kRaw;
+                    ok = __all_sync(0xffffffffu, mbar_wait(&b.raw_empty[slot], ((st / C::kRaw) & 1u) ^ 1u, wc, 32));
+                    if (!ok) return false;
+                    ++st;
+                    if (lane == 0) mbar_arrive_expect_tx(&b.raw_full[slot], C::kRawBytes);
+                    __syncwarp();
+                    if (lane < boxes)
+                        tma_load_3d(smem + C::kRawOff + slot * C::kRawBytes + lane * rows * D, half ? tk : tv, &b.raw_full[slot], 0,
+                                    half ? y : prev_y, half ? pg : prev_page, policy);
+                }
+            } else {
+                const uint32_t slot = st % C::kStages;
+                ok = __all_sync(0xffffffffu, mbar_wait(&b.kv_empty[slot], ((st / C::kStages) & 1u) ^ 1u, wc, 32));
+                if (!ok) return false;
+                ++st;
+                if (lane == 0) mbar_arrive_expect_tx(&b.kv_full[slot], (has_v && has_k) ? C::kStageBytes : C::kTileBytes);
+                __syncwarp();
+                if (lane < boxes) {
+                    const uint32_t dst = smem + C::kKVOff + slot * C::kStageBytes + lane * rows * 128;
+#pragma unroll
+                    for (int i = 0; i < C::kBoxes; ++i) {
+                        if (has_v) tma_load_3d(dst + i * C::kBoxBytes, tv, &b.kv_full[slot], i * 64, prev_y, prev_page, policy);
+                        if (has_k)
+                            tma_load_3d(dst + C::kTileBytes + i * C::kBoxBytes, tk, &b.kv_full[slot], i * 64, y, pg, policy);
+                    }
+                }
+            }
+            prev_page = pg;
+            prev_y = y;
+        }
+        return true;
+    });
+    if (!ok && lane == 0) {  // let the copies in flight land before the block ends
+        constexpr uint32_t kN = E4M3 ? C::kRaw : C::kStages;
+        uint64_t* full = E4M3 ? b.raw_full : b.kv_full;
+        for (uint32_t s = 0; s < kN && s < st; ++s) {
+            const uint32_t last = st - 1 - ((st - 1 - s) % kN);
+            drain_wait(&full[s], (last / kN) & 1u, wc.timeout_ns);
+        }
+        for (int x = 0; x < 2; ++x)
+            if (qit[x] > 0) drain_wait(&b.q_full[x], (qit[x] - 1) & 1u, wc.timeout_ns);
+    }
+}
+
+// ------------------------------------------------------------------ values that must not spread
+__device__ __forceinline__ bool key_used(const PagedAttnParams& p, const Chunk& c, int j) {
+    return j < c.hi && (j >= c.first || j < p.sinks);
+}
+__device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// bf16: one warp passes every stage; V tiles that not every row sees whole are cleaned in place.
+template <int D>
+__device__ void fix_role(const PagedAttnParams& p, uint8_t* smem, Bars& b, volatile int* poison, const WaitCtl& wc) {
+    using C = Cfg<D, false>;
+    const int lane = threadIdx.x & 31;
+    uint32_t st = 0, nf = 0;
+    for_each_part(p, [&](const Part& q) -> bool {
+        for (int t = q.ta; t <= q.tb; ++t, ++st) {
+            const uint32_t slot = st % C::kStages;
+            if (!mbar_wait_w(&b.kv_full[slot], (st / C::kStages) & 1u, wc)) return false;
+            const int j0 = t > q.ta ? q.c.key(t - 1) : 0;
+            if (t > q.ta && !whole_tile(p, q.c, j0)) {
+                uint8_t* v = smem + C::kKVOff + slot * C::kStageBytes;
+                bool bad = false;
+                // lane l and its three neighbours take a row of 128 bytes, two chunks each; the swizzle
+                // permutes chunks inside a row only
+                for (int r = lane / 4; r < kTile; r += 8) {
+                    const bool used = key_used(p, q.c, j0 + r);
+#pragma unroll
+                    for (int i = 0; i < 2 * C::kBoxes; ++i) {
+                        uint4* w = reinterpret_cast<uint4*>(v + (i >> 1) * C::kBoxBytes + r * 128) + (lane & 3) + 4 * (i & 1);
+                        uint4 x = *w;
+                        uint32_t* y = reinterpret_cast<uint32_t*>(&x);
+                        bool change = !used;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const uint32_t m = ((y[e] & 0x7f80u) == 0x7f80u ? 0xffffu : 0u) |
+                                               ((y[e] & 0x7f800000u) == 0x7f800000u ? 0xffff0000u : 0u);
+                            if (used && m) bad = change = true;
+                            y[e] = used ? y[e] & ~m : 0u;
+                        }
+                        if (change) *w = x;
+                    }
+                }
+                if (bad) poison[q.k % kPoison] = q.k + 1;
+                fence_async_shared();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&b.fixed[nf % 2]);
+                ++nf;
+            }
+            if (lane == 0) mbar_arrive(&b.kv_empty[slot]);
+        }
+        return true;
+    });
+}
+
+// e4m3: 128 threads, a row each, expand every tile into its bf16 stage.
+template <int D>
+__device__ void expand_role(const PagedAttnParams& p, uint8_t* smem, Bars& b, volatile int* poison, const WaitCtl& wc) {
+    using C = Cfg<D, true>;
+    const PagedKV& kv = p.kv;
+    const int r = threadIdx.x - kExpandWarp * 32;
+    uint32_t st = 0, raw = 0;
+    auto expand = [&](uint8_t* dst, float scale, bool zero) -> bool {
+        const uint32_t slot = raw % C::kRaw;
+        if (!mbar_wait_w(&b.raw_full[slot], (raw / C::kRaw) & 1u, wc)) return false;
+        ++raw;
+        const uint8_t* src = smem + C::kRawOff + slot * C::kRawBytes + r * D;
+        const int sw = D == 128 ? (r & 7) : ((r >> 1) & 3);
+        uint4 x[D / 16];
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) x[c] = *reinterpret_cast<const uint4*>(src + ((c ^ sw) << 4));
+        // 2^120 * scale, in two factors where it is no bf16 number
+        const bool big = scale > 128.f;
+        const float f1 = big ? 0x1p120f : scale * 0x1p120f;
+        __nv_bfloat162 m1 = __float2bfloat162_rn(f1), m2 = __float2bfloat162_rn(big ? scale : 1.f);
+        const bool any_big = __any_sync(0xffffffffu, big);
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) {
+            const uint32_t w[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
+            uint32_t y[8];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const uint32_t a = __byte_perm(w[i], 0, e ? 0x3424 : 0x1404);  // a code in each high byte
+                    const uint32_t v = ((a >> 4) & 0x07f007f0u) | (a & 0x80008000u);
+                    __nv_bfloat162 z = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&v), m1);
+                    if (any_big) z = __hmul2(z, m2);
+                    y[2 * i + e] = zero ? 0u : *reinterpret_cast<const uint32_t*>(&z);
+                }
+            uint8_t* d = dst + (c >> 2) * C::kBoxBytes + r * 128;
+            *reinterpret_cast<uint4*>(d + (((2 * c) & 7) ^ (r & 7)) * 16) = make_uint4(y[0], y[1], y[2], y[3]);
+            *reinterpret_cast<uint4*>(d + (((2 * c + 1) & 7) ^ (r & 7)) * 16) = make_uint4(y[4], y[5], y[6], y[7]);
+        }
+        // Only now, when every loaded code has been used: an arrival right behind the loads let the
+        // next tile's copy overtake them (seen as wrong values in the chunks loaded last).
+        mbar_arrive(&b.raw_empty[slot]);
+        return true;
+    };
+    for_each_part(p, [&](const Part& q) -> bool {
+        // this row's scales, a tile ahead
+        float ks = 0.f, vs = 0.f;
+        auto look = [&](int t) {
+            const int pos = q.c.key(t) + r;
+            int row = 0;
+            const int pg = pos < q.c.hi ? paged_page(kv, q.c.b, pos, row) : -1;
+            const long long at = static_cast<long long>(q.h) * kv.page + row;
+            ks = pg >= 0 ? __ldg(kv.k_scale + pg * kv.ks_ps + at) : 0.f;
+            vs = pg >= 0 ? __ldg(kv.v_scale + pg * kv.vs_ps + at) : 0.f;
+        };
+        look(q.ta);
+        float prev_vs = 0.f;
+        for (int t = q.ta; t <= q.tb; ++t, ++st) {
+            const float k1 = ks, v1 = prev_vs;
+            prev_vs = vs;
+            if (t + 1 < q.tb) look(t + 1);
+            const uint32_t slot = st % C::kStages;
+            if (!mbar_wait_w(&b.kv_empty[slot], ((st / C::kStages) & 1u) ^ 1u, wc)) return false;
+            uint8_t* stage = smem + C::kKVOff + slot * C::kStageBytes;
+            if (t > q.ta) {
+                bool zero = false;
+                const int j0 = q.c.key(t - 1);
+                if (!whole_tile(p, q.c, j0)) {
+                    zero = !key_used(p, q.c, j0 + r);
+                    if (!zero && !(fabsf(v1) < INFINITY)) {
+                        zero = true;
+                        poison[q.k % kPoison] = q.k + 1;
+                    }
+                }
+                if (!expand(stage, v1, zero)) return false;
+            }
+            if (t < q.tb && !expand(stage + C::kTileBytes, k1, false)) return false;
+            fence_async_shared();
+            mbar_arrive(&b.kv_full[slot]);
+        }
+        return true;
+    });
+}
+
+// ------------------------------------------------------------------ MMA issuers
+__device__ __forceinline__ uint32_t sdesc_lo(uint32_t smem_addr, uint32_t lbo) {
+    return ((smem_addr >> 4) & 0x3FFFu) | (((lbo >> 4) & 0x3FFFu) << 16);
+}
+constexpr uint32_t kSdescHi = (1024u >> 4) | (1u << 14) | (2u << 29);  // sbo 1024 B, version 1, 128 B swizzle
+
+// S = Q K^T: K slice kk lies (kk / 4) boxes and (kk % 4) * 32 bytes in.
+template <int D>
+__device__ __forceinline__ void issue_s(uint32_t d_tmem, uint32_t q_base, uint32_t k_base) {
+    constexpr uint32_t idesc = idesc_bf16(kTile, kTile, 0);
+    const uint32_t qlo = sdesc_lo(q_base, 16), klo = sdesc_lo(k_base, 16);
+#pragma unroll
+    for (int kk = 0; kk < D / 16; ++kk) {
+        const uint32_t off = (kk / 4) * (kTile * 128 >> 4) + (kk % 4) * (32 >> 4);
+        asm volatile(
+            "{\n\t.reg .b64 da, db;\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "mov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %5};\n\telect.sync _|e, 0xffffffff;\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d_tmem),
+            "r"(qlo + off), "r"(klo + off), "r"(idesc), "r"(kk > 0 ? 1u : 0u), "r"(kSdescHi)
+            : "memory");
+    }
+}
+// O += P V, P from tensor memory.
+template <int D>
+__device__ __forceinline__ void issue_pv(uint32_t d_tmem, uint32_t p_tmem, uint32_t v_base, bool accumulate) {
+    constexpr uint32_t idesc = idesc_bf16(kTile, D, 1);
+    const uint32_t vlo = sdesc_lo(v_base, kTile * 128);
+    const uint32_t acc = accumulate ? 1u : 0u;
+#pragma unroll
+    for (int kk = 0; kk < kTile / 16; ++kk) {
+        asm volatile(
+            "{\n\t.reg .b64 db;\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "mov.b64 db, {%2, %5};\n\telect.sync _|e, 0xffffffff;\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(d_tmem),
+            "r"(p_tmem + kk * 8), "r"(vlo + ((kk * 16 * 128) >> 4)), "r"(idesc), "r"(kk > 0 ? 1u : acc),
+            "r"(kSdescHi)
+            : "memory");
+    }
+}
+
+__device__ __forceinline__ bool wait_turn(volatile uint32_t* turn, uint32_t mine, const WaitCtl& wc) {
+    if (*turn == mine) return true;
+    const uint64_t t0 = globaltimer_ns();
+    for (uint32_t i = 1;; ++i) {
+        if (*turn == mine) return true;
+        if ((i & 255u) == 0u) {
+            if (*wc.abort_flag) return false;
+            if (globaltimer_ns() - t0 > wc.timeout_ns) {
+                raise_abort(wc, reinterpret_cast<uint64_t*>(const_cast<uint32_t*>(turn)));
+                return false;
+            }
+        }
+    }
+}
+
+// The issuer of unit x.  The two take turns batch by batch (`turn` counts the batches issued), so
+// that the tensor pipe sees each unit's batch whole while one issuer's waits overlap the
+// other's batch.  Every stage is released once by each of them.
+template <int D, bool E4M3>
+__device__ void mma_role(const PagedAttnParams& p, int x, uint32_t smem, Bars& b, uint32_t tmem, volatile uint32_t* turn,
+                         const WaitCtl& wc) {
+    using C = Cfg<D, E4M3>;
+    const uint32_t q_base = smem + x * C::kTileBytes, kv_base = smem + C::kKVOff;
+    const uint32_t s_tmem = tmem + x * kTile, o_tmem = tmem + C::kOCol + x * D;
+    uint32_t st = 0, qit = 0, pit = 0, seq = 0, nf = 0;
+    bool ok = true;
+    for_each_part(p, [&](const Part& q) -> bool {
+        ok = false;
+        const int n = q.tb - q.ta, nx = units_of(p, q.c);
+        auto wait_stage = [&](uint32_t& slot, uint32_t& base) -> bool {
+            slot = st % C::kStages;
+            base = kv_base + slot * C::kStageBytes;
+            const bool r = mbar_wait_w(&b.kv_full[slot], (st / C::kStages) & 1u, wc);
+            ++st;
+            return r;
+        };
+        uint32_t slot, base;
+        if (x >= nx) {  // no second unit: pass every stage
+            for (int i = 0; i <= n; ++i) {
+                if (!wait_stage(slot, base)) return false;
+                if ((threadIdx.x & 31) == 0) mbar_arrive(&b.kv_empty[slot]);
+                if (!E4M3 && i > 0 && !whole_tile(p, q.c, q.c.key(q.ta + i - 1))) ++nf;
+            }
+            seq += 1 + n;
+            ok = true;
+            return true;
+        }
+        // batches: S(0) of unit x is seq + x, tile j of unit x is seq + nx (j + 1) + x
+        if (!mbar_wait_w(&b.q_full[x], qit & 1u, wc)) return false;
+        if (!wait_stage(slot, base)) return false;
+        if (!__all_sync(0xffffffffu, wait_turn(turn, seq + x, wc))) return false;
+        tc_fence_after();
+        issue_s<D>(s_tmem, q_base, base + C::kTileBytes);
+        mma_commit_e(&b.s_full[x]);
+        *turn = seq + x + 1;
+        mma_commit_e(&b.kv_empty[slot]);
+        if (n == 1) mma_commit_e(&b.q_empty[x]);
+        for (int j = 0; j < n; ++j) {
+            if (!wait_stage(slot, base)) return false;  // V(j) and, unless j is the last, K(j + 1)
+            if (!E4M3 && !whole_tile(p, q.c, q.c.key(q.ta + j))) {
+                if (!mbar_wait_w(&b.fixed[nf % 2], (nf / 2) & 1u, wc)) return false;
+                ++nf;
+            }
+            const uint32_t mine = seq + nx * (j + 1) + x;
+            if (!__all_sync(0xffffffffu, wait_turn(turn, mine, wc))) return false;
+            if (j == 0 && !mbar_wait_w(&b.o_free[x], (qit & 1u) ^ 1u, wc)) return false;
+            if (!mbar_wait_w(&b.p_full[x], pit & 1u, wc)) return false;
+            ++pit;
+            tc_fence_after();
+            issue_pv<D>(o_tmem, s_tmem + 64, base, j > 0);
+            if (j + 1 < n) {
+                issue_s<D>(s_tmem, q_base, base + C::kTileBytes);
+                mma_commit_e(&b.s_full[x]);
+            } else {
+                mma_commit_e(&b.o_done[x]);
+            }
+            *turn = mine + 1;
+            mma_commit_e(&b.kv_empty[slot]);
+            if (j + 2 == n) mma_commit_e(&b.q_empty[x]);
+        }
+        seq += nx * (n + 1);
+        ++qit;
+        ok = true;
+        return true;
+    });
+    if (!ok) {  // every MMA this warp issued must finish before TMEM is released
+        mma_commit_e(&b.drain[x]);
+        drain_wait(&b.drain[x], 0, wc.timeout_ns);
+    }
+}
+
+// ------------------------------------------------------------------ softmax
+template <int D, bool E4M3>
+__device__ void softmax_role(const PagedAttnParams& p, int x, Bars& b, uint32_t tmem, const volatile int* poison,
+                             const WaitCtl& wc) {
+    using C = Cfg<D, E4M3>;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int row = (warp & 3) * 32 + lane;
+    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t s_tmem = tmem + lane_off + x * kTile;
+    const uint32_t p_tmem = s_tmem + 64;
+    const uint32_t o_tmem = tmem + lane_off + C::kOCol + x * D;
+    const int tok_in = row / p.g;
+    uint32_t sit = 0, iit = 0;
+    auto wait = [&](uint64_t* bar, uint32_t parity) -> bool { return __all_sync(0xffffffffu, mbar_wait(bar, parity, wc)); };
+    for_each_part(p, [&](const Part& q) -> bool {
+        if (x >= units_of(p, q.c)) return true;
+        const int t_row = q.c.ta + x * p.unit_tokens + tok_in;  // the row's token; none if not below tb
+        const int pos = q.c.s.base + t_row;
+        // keys this row sees: below hi, and from lo on or below the sinks
+        const int hi = p.causal ? min(pos + 1, q.c.s.L) : q.c.s.L;
+        const int lo = p.window > 0 ? pos - p.window + 1 : 0;
+        // the rows of the unit all see a tile that lies in [., u_hi) and from u_lo on
+        const int t0 = q.c.ta + x * p.unit_tokens, t1 = min(t0 + p.unit_tokens, q.c.tb);
+        const int u_hi = p.causal ? q.c.s.base + t0 + 1 : q.c.s.L;
+        const int u_lo = p.window > 0 ? q.c.s.base + t1 - p.window : 0;
+        float m = -INFINITY, l = 0.f, lr = 0.f;
+        for (int t = q.ta; t < q.tb; ++t) {
+            const int j0 = q.c.key(t);
+            if (!wait(&b.s_full[x], sit & 1u)) return false;
+            ++sit;
+            tc_fence_after();
+            float s[kTile];
+            float pm0, pm1, pm2, pm3;
+            {
+                uint32_t r0[32], r1[32], r2[32], r3[32];
+                tmem_ld32_max(s_tmem + 0, r0, pm0);
+                tmem_ld32_max(s_tmem + 32, r1, pm1);
+                tmem_ld32_max(s_tmem + 64, r2, pm2);
+                tmem_ld32_max(s_tmem + 96, r3, pm3);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    s[i] = __uint_as_float(r0[i]);
+                    s[32 + i] = __uint_as_float(r1[i]);
+                    s[64 + i] = __uint_as_float(r2[i]);
+                    s[96 + i] = __uint_as_float(r3[i]);
+                }
+            }
+            float mx = fmaxf(fmaxf(pm0, pm1), fmaxf(pm2, pm3));
+            if (j0 + kTile > u_hi || (j0 < u_lo && j0 + kTile > p.sinks)) {
+                const int h = hi - j0, w = lo - j0, k = p.window > 0 ? p.sinks - j0 : 0;
+#pragma unroll
+                for (int i = 0; i < kTile; ++i) s[i] = (i >= h || (i < w && i >= k)) ? -INFINITY : s[i];
+                float c[8];
+#pragma unroll
+                for (int a = 0; a < 8; ++a) c[a] = fmaxf(s[2 * a], s[2 * a + 1]);
+#pragma unroll
+                for (int i = 16; i < kTile; i += 16)
+#pragma unroll
+                    for (int a = 0; a < 8; ++a) c[a] = fmax3(c[a], s[i + 2 * a], s[i + 2 * a + 1]);
+                mx = fmaxf(fmax3(c[0], c[1], c[2]), fmax3(c[3], c[4], fmax3(c[5], c[6], c[7])));
+            }
+            const float m_new = fmaxf(m, mx * kLog2e);
+            float f = 1.f;
+            bool need = false;
+            if (t == q.ta) {
+                m = m_new;
+            } else if (m_new > m + kRescaleLog2 || (m == -INFINITY && m_new > m)) {
+                need = true;
+                f = ex2(m - m_new);
+                l *= f;
+                lr *= f;
+                m = m_new;
+            }
+            const float nmu = (m == -INFINITY) ? 0.f : -m;
+            float se[2] = {}, sr[2] = {};
+#pragma unroll
+            for (int qq = 0; qq < 4; ++qq) {
+                uint32_t pk[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    float t0, t1;
+                    ffma2(t0, t1, s[qq * 32 + 2 * i], s[qq * 32 + 2 * i + 1], kLog2e, kLog2e, nmu, nmu);
+                    const float a = ex2(t0), c2 = ex2(t1);
+                    fadd2(se[0], se[1], se[0], se[1], a, c2);
+                    pk[i] = pack_bf16x2(a, c2);
+                    add_bf16x2_f32(sr[0], sr[1], pk[i]);
+                }
+                tmem_st16(p_tmem + qq * 16, pk);  // every score is in registers: P may overwrite S's upper half
+            }
+            // O is stable here: the commit that signalled this S covered the previous P V, and the
+            // next one waits for this tile's arrivals
+            if (__any_sync(0xffffffffu, need)) {
+#pragma unroll
+                for (int cc = 0; cc < D; cc += 32) {
+                    uint32_t o0[32];
+                    tmem_ld32(o_tmem + cc, o0);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) o0[i] = __float_as_uint(__uint_as_float(o0[i]) * f);
+                    tmem_st32(o_tmem + cc, o0);
+                }
+            }
+            l += se[0] + se[1];
+            lr += sr[0] + sr[1];
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(&b.p_full[x]);
+        }
+        if (!wait(&b.o_done[x], iit & 1u)) return false;
+        ++iit;
+        tc_fence_after();
+        float o[D];
+#pragma unroll
+        for (int cc = 0; cc < D; cc += 32) {
+            uint32_t r[32];
+            tmem_ld32(o_tmem + cc, r);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[cc + i] = __uint_as_float(r[i]);
+        }
+        tmem_wait_ld();
+        tc_fence_before();
+        mbar_arrive(&b.o_free[x]);
+        const bool cut = q.ta > 0 || q.tb < q.c.n;
+        const bool live = row < p.unit_tokens * p.g && t_row < q.c.tb;
+        if (live && poison[q.k % kPoison] == q.k + 1) {  // values that are no numbers, of the keys this row sees
+            for (int t = q.ta; t < q.tb; ++t) {
+                const int j0 = q.c.key(t);
+                if (whole_tile(p, q.c, j0)) continue;  // its values went into the product as they are
+                for (int j = j0; j < min(j0 + kTile, hi); ++j) {
+                    if (j < lo && j >= p.sinks) continue;
+                    int r;
+                    const int pg = paged_page(p.kv, q.c.b, j, r);
+                    if (pg < 0) continue;
+                    const long long at = static_cast<long long>(q.h) * p.kv.page + r;
+                    if constexpr (E4M3) {
+                        if (fabsf(__ldg(p.kv.v_scale + pg * p.kv.vs_ps + at)) < INFINITY) continue;
+#pragma unroll
+                        for (int i = 0; i < D; ++i) o[i] = __uint_as_float(0x7fc00000u);
+                    } else {
+                        const uint32_t* v = reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(p.kv.v) + pg * p.kv.v_ps + at * D);
+#pragma unroll
+                        for (int i = 0; i < D / 2; ++i) {
+                            const uint32_t y = __ldg(v + i);
+                            if ((y & 0x7f80u) == 0x7f80u) o[2 * i] += __uint_as_float(y << 16);
+                            if ((y & 0x7f800000u) == 0x7f800000u) o[2 * i + 1] += __uint_as_float(y & 0xffff0000u);
+                        }
+                    }
+                }
+            }
+        }
+        if (cut) {
+            PagedChunkPartial* part = static_cast<PagedChunkPartial*>(p.workspace) + 2 * blockIdx.x + (q.k ? 1 : 0);
+            const int r2 = x * kTile + row;
+            if (live) {
+                float* dst = part->o + r2 * kPagedMaxD;
+#pragma unroll
+                for (int i = 0; i < D; i += 4)
+                    *reinterpret_cast<float4*>(dst + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                part->m[r2] = m;
+                part->l[r2] = l;
+                part->lr[r2] = lr;
+            }
+            if (x == 0 && row == 0) {
+                part->b = q.c.b;
+                part->pair = q.c.pair;
+                part->h = q.h;
+                part->begins = q.ta == 0;
+            }
+        } else {
+            if (live) {
+                const float inv = lr == 0.f ? 0.f : 1.f / lr;
+                const int tok = q.c.s.q0 + t_row, head = q.h * p.g + row - tok_in * p.g;
+                paged_store_row<D>(p, tok, head, o, inv);
+                p.lse[tok * p.l_ts + head * p.l_hs] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+            }
+        }
+        return true;
+    });
+}
+
+template <int D, bool E4M3>
+__global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
+    paged_chunk_kernel(const __grid_constant__ PagedAttnParams p, const __grid_constant__ CUtensorMap tq,
+                       const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv) {
+    using C = Cfg<D, E4M3>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    __shared__ __align__(8) Shared sh;
+    Bars& b = sh.b;
+    const int warp = threadIdx.x / 32;
+    if (threadIdx.x == 0) {
+        for (int x = 0; x < 2; ++x) {
+            mbar_init(&b.q_full[x], 1);
+            mbar_init(&b.q_empty[x], 1);
+            mbar_init(&b.s_full[x], 1);
+            mbar_init(&b.p_full[x], 128);
+            mbar_init(&b.o_done[x], 1);
+            mbar_init(&b.o_free[x], 128);
+            mbar_init(&b.drain[x], 1);
+            mbar_init(&b.fixed[x], 1);
+        }
+        for (int s = 0; s < 4; ++s) {
+            mbar_init(&b.kv_full[s], E4M3 ? 128 : 1);
+            mbar_init(&b.kv_empty[s], E4M3 ? 2 : 3);  // both issuers, and the warp that looks values over
+            mbar_init(&b.raw_full[s], 1);
+            mbar_init(&b.raw_empty[s], 128);
+        }
+        sh.abort_flag = 0;
+        sh.turn = 0;
+        for (int i = 0; i < kPoison; ++i) sh.poison[i] = 0;
+        fence_mbar_init();
+    }
+    if (warp == kMmaWarp) {
+        tmem_alloc(&sh.tmem, C::kTmemCols);
+        tmem_relinquish();
+    }
+    launch_dependents();
+    wait_primary();  // the list of items
+    if (threadIdx.x < 2) (static_cast<PagedChunkPartial*>(p.workspace) + 2 * blockIdx.x + threadIdx.x)->b = -1;
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sh.tmem;
+    const WaitCtl wc{&sh.abort_flag, p.err, p.timeout_ns};
+    if (warp < 8) {
+        // e4m3: 512 threads start with 128 registers each; 256 * 168 + 256 * 88 is the same sum
+        if constexpr (E4M3) asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
+        softmax_role<D, E4M3>(p, warp / 4, b, tmem, sh.poison, wc);
+    } else {
+        if constexpr (E4M3) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+        if (warp == kMmaWarp || warp == kMmaWarp + 1) {
+            mma_role<D, E4M3>(p, warp - kMmaWarp, smem_u32(smem), b, tmem, &sh.turn, wc);
+        } else if (warp == kLoadWarp) {
+            load_role<D, E4M3>(p, &tq, &tk, &tv, smem_u32(smem), b, wc);
+        } else if constexpr (E4M3) {
+            if (warp >= kExpandWarp) expand_role<D>(p, smem, b, sh.poison, wc);
+        } else {
+            fix_role<D>(p, smem, b, sh.poison, wc);
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == kMmaWarp) tmem_dealloc(tmem, C::kTmemCols);
+}
+
+// Joins the parts of items that were cut: a warp takes one row of an item that begins in block x of
+// the first kernel and goes on in the next ones.
+constexpr int kJoinRows = 8;
+template <int D>
+__global__ void __launch_bounds__(kJoinRows * 32) paged_chunk_join_kernel(const __grid_constant__ PagedAttnParams p, int shares) {
+    wait_primary();
+    const PagedChunkPartial* parts = static_cast<const PagedChunkPartial*>(p.workspace);
+    const int x = blockIdx.x, lane = threadIdx.x & 31;
+    const PagedChunkPartial* p0 = parts + 2 * x + (parts[2 * x + 1].b >= 0 ? 1 : 0);
+    const int b = p0->b, pair = p0->pair, h = p0->h;
+    if (b < 0 || !p0->begins) return;
+    const Chunk c = make_chunk(p, b, pair);
+    const int r = blockIdx.y * kJoinRows + threadIdx.x / 32;  // row of the two units
+    const int unit = r / kTile, ru = r - unit * kTile, t = c.ta + unit * p.unit_tokens + ru / p.g;
+    if (ru >= p.unit_tokens * p.g || t >= c.tb) return;
+    int n = 1;  // parts: p0, then the first ones of the blocks up to x + n - 1
+    while (x + n < shares) {
+        const int y = x + n + lane;
+        const PagedChunkPartial* q = parts + 2 * y;
+        const bool on = y < shares && q->b == b && q->pair == pair && q->h == h && !q->begins;
+        const uint32_t v = __ballot_sync(0xffffffffu, on);
+        n += v == 0xffffffffu ? 32 : __ffs(~v) - 1;
+        if (v != 0xffffffffu) break;
+    }
+    float M = -INFINITY;
+    for (int k = lane; k < n; k += 32) M = fmaxf(M, (k ? parts + 2 * (x + k) : p0)->m[r]);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    float l = 0.f, lr = 0.f, acc[4] = {};
+#pragma unroll 4
+    for (int k = 0; k < n; ++k) {
+        const PagedChunkPartial* q = k ? parts + 2 * (x + k) : p0;
+        const float f = paged_weight(q->m[r], M);
+        l = paged_add_weighted(l, f, q->l[r]);
+        lr = paged_add_weighted(lr, f, q->lr[r]);
+        if (4 * lane < D) {
+            const float4 v = *reinterpret_cast<const float4*>(&q->o[r * kPagedMaxD + 4 * lane]);
+            acc[0] = paged_add_weighted(acc[0], f, v.x);
+            acc[1] = paged_add_weighted(acc[1], f, v.y);
+            acc[2] = paged_add_weighted(acc[2], f, v.z);
+            acc[3] = paged_add_weighted(acc[3], f, v.w);
+        }
+    }
+    const int tok = c.s.q0 + t, head = h * p.g + ru % p.g;
+    if (4 * lane < D) paged_store4(p, tok, head, 4 * lane, acc, lr == 0.f ? 0.f : 1.f / lr);
+    if (lane == 0) p.lse[tok * p.l_ts + head * p.l_hs] = l == 0.f ? -INFINITY : (M + log2f(l)) * kLn2;
+}
+
+template <class... Args>
+cudaError_t launch_dependent(void (*kern)(Args...), dim3 grid, int threads, int smem, cudaStream_t stream, Args... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+template <int D, bool E4M3>
+int launch_t(const PagedAttnParams& p, const PagedMaps& m, int shares, cudaStream_t stream) {
+    using C = Cfg<D, E4M3>;
+    auto kern = paged_chunk_kernel<D, E4M3>;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes) != cudaSuccess) return -4;
+    if constexpr (E4M3) {  // the register split adds up only if the block starts with 128 a thread
+        cudaFuncAttributes a;
+        if (cudaFuncGetAttributes(&a, kern) != cudaSuccess || a.numRegs != 128) return -4;
+    }
+    paged_plan_kernel<<<1, kPlanThreads, 0, stream>>>(p);
+    if (cudaGetLastError() != cudaSuccess) return -4;
+    if (launch_dependent(kern, dim3(shares), C::kThreads, C::kSmemBytes, stream, p, m.q, m.k, m.v) != cudaSuccess) return -4;
+    return launch_dependent(paged_chunk_join_kernel<D>, dim3(shares, 2 * kTile / kJoinRows), kJoinRows * 32, 0, stream, p, shares) ==
+                   cudaSuccess
+               ? 0
+               : -4;
+}
+
+}  // namespace
+
+int launch_paged_chunk(const PagedAttnParams& p, const PagedMaps& m, int shares, cudaStream_t stream) {
+    if (p.kv.d == 128) return p.kv.e4m3 ? launch_t<128, true>(p, m, shares, stream) : launch_t<128, false>(p, m, shares, stream);
+    return p.kv.e4m3 ? launch_t<64, true>(p, m, shares, stream) : launch_t<64, false>(p, m, shares, stream);
+}
+
+}  // namespace ra

@@ -211,14 +211,6 @@ __device__ __forceinline__ uint32_t chunk_at(int r, int c) {
     else return r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
 }
 
-// Weight of a partial result with running max m when the joint one is M.  All -inf: nothing was
-// seen (sums are 0), or only scores that are no numbers, which have to come through.
-__device__ __forceinline__ float weight(float m, float M) {
-    return m == -INFINITY ? (M == -INFINITY ? 1.f : 0.f) : ex2(m - M);
-}
-__device__ __forceinline__ float add_weighted(float sum, float w, float x) {
-    return (w == 0.f && x == x) ? sum : fmaf(w, x, sum);
-}
 // What turns sum p' u into out.
 template <bool E4M3>
 __device__ __forceinline__ float out_factor(float M, float Ms, float L) {
@@ -342,6 +334,17 @@ __device__ void compute_role(const PagedAttnParams& p, uint8_t* smem, uint64_t* 
                 ks[0] = *reinterpret_cast<const float2*>(f);
                 ks[1] = *reinterpret_cast<const float2*>(f + 8);
             }
+            if constexpr (E4M3) {
+#pragma unroll
+                for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float k1 = e ? ks[nt].y : ks[nt].x;
+                        sc[nt][e] *= k1 * cs[0];
+                        sc[nt][2 + e] *= k1 * cs[1];
+                    }
+            }
+            // (a slot is handed back when what was loaded from it has been used)
             __syncwarp();
             if (lane == 0) mbar_arrive(&empty[slot]);
             ++it;
@@ -361,15 +364,12 @@ __device__ void compute_role(const PagedAttnParams& p, uint8_t* smem, uint64_t* 
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     if constexpr (E4M3) {
-                        const float k1 = e ? ks[nt].y : ks[nt].x;
                         const uint32_t vb = __float_as_uint(e ? vs[nt].y : vs[nt].x);
                         // a scale that is no number makes the row no number; exponent 0 is a scale of 0 (a row
                         // of zeros, from a page that is none)
                         const int a = static_cast<int>((vb >> 23) & 0xffu);
                         va[2 * nt + e] = a == 255 ? __uint_as_float(0x7fc00000u) : static_cast<float>(a - 127);
                         vm[2 * nt + e] = __uint_as_float((vb & 0x7fffffu) | 0x3f800000u);
-                        sc[nt][e] *= k1 * cs[0];
-                        sc[nt][2 + e] *= k1 * cs[1];
                     } else {
                         sc[nt][e] *= kLog2e;
                         sc[nt][2 + e] *= kLog2e;
@@ -549,8 +549,8 @@ __device__ void compute_role(const PagedAttnParams& p, uint8_t* smem, uint64_t* 
                 float f[kWarps], L = 0.f;
 #pragma unroll
                 for (int w = 0; w < kWarps; ++w) {
-                    f[w] = weight(sm[w * kRows + r], M);
-                    L = add_weighted(L, weight(sms[w * kRows + r], Ms), sl[w * kRows + r]);
+                    f[w] = paged_weight(sm[w * kRows + r], M);
+                    L = paged_add_weighted(L, paged_weight(sms[w * kRows + r], Ms), sl[w * kRows + r]);
                 }
                 const int t = r / p.g, head = q.h * p.g + r - t * p.g, tok = s.q0 + t;
                 for (int d = 4 * lane; d < D; d += 128) {
@@ -603,8 +603,6 @@ __device__ void compute_role(const PagedAttnParams& p, uint8_t* smem, uint64_t* 
                 part->b = q.b;
                 part->h = q.h;
                 part->begins = q.ta == 0;
-            } else {
-                part->b = -1;
             }
         }
         first = 0;
@@ -690,8 +688,8 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__
 #pragma unroll 4
     for (int k = warp; k < n; k += kSub) {
         const PagedPartial* q = parts + (k == 0 ? i0 : 2 * (x + k));
-        const float f = weight(q->m[r], M);
-        l = add_weighted(l, weight(q->ms[r], Ms), q->l[r]);
+        const float f = paged_weight(q->m[r], M);
+        l = paged_add_weighted(l, paged_weight(q->ms[r], Ms), q->l[r]);
         if (4 * lane < D) {
             const float4 v = *reinterpret_cast<const float4*>(&q->o[r * kPagedMaxD + 4 * lane]);
             acc[0] = fmaf(f, v.x, acc[0]);
