@@ -5,10 +5,25 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
+
 #include "fastdiv.h"
 
 namespace ra {
 
+// Sets a kernel up once a device (at most 64 of them, as everywhere): f() returns whether it worked.
+template <class F>
+bool once_a_device(std::atomic<unsigned long long>& done, F&& f) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    const unsigned long long bit = 1ull << (dev & 63);
+    if (done.load(std::memory_order_acquire) & bit) return true;
+    if (!f()) return false;
+    done.fetch_or(bit, std::memory_order_release);
+    return true;
+}
+
+constexpr int kPagedMaxBatch = 4096;  // RINGATTN_PAGED_MAX_BATCH
 constexpr int kPagedTile = 128;       // keys of a tile
 constexpr int kPagedMaxD = 128;
 constexpr int kPagedMaxShares = 160;  // most blocks of an attention kernel
@@ -111,6 +126,16 @@ __device__ __forceinline__ int paged_page(const PagedKV& kv, int b, int pos, int
     return (pg >= 0 && pg < kv.n_pages) ? pg : -1;
 }
 
+// The same in two steps, for loops that load the table's entry well before they need it.
+__device__ __forceinline__ int paged_entry(const PagedKV& kv, int b, int pos, int& row) {
+    const int i = static_cast<int>(fdiv(static_cast<unsigned>(pos), kv.by_page));
+    row = pos - i * kv.page;
+    return __ldg(kv.table + b * kv.table_stride + i);
+}
+__device__ __forceinline__ int paged_checked(const PagedKV& kv, int entry) {
+    return (entry >= 0 && entry < kv.n_pages) ? entry : -1;
+}
+
 // The sequence whose rows hold row t (cu[b] <= t < cu[b + 1]), -1 if none does.  cu may be in
 // shared memory.
 __device__ __forceinline__ int paged_find(const int* cu, int batch, int t) {
@@ -150,19 +175,20 @@ __device__ __forceinline__ void paged_store4(const PagedAttnParams& p, int tok, 
         *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at) = w;
     }
 }
-// A whole output row, times inv: 16-byte stores (rows start on 16 bytes).
-template <int D>
-__device__ __forceinline__ void paged_store_row(const PagedAttnParams& p, int tok, int head, const float (&o)[D], float inv) {
-    const long long at = tok * p.o_ts + head * p.o_hs;
+// N columns of an output row, times inv: 16-byte stores (rows start on 16 bytes).
+template <int N>
+__device__ __forceinline__ void paged_store_cols(const PagedAttnParams& p, int tok, int head, int col, const float (&o)[N],
+                                                 float inv) {
+    const long long at = tok * p.o_ts + head * p.o_hs + col;
     if (p.out_f32) {
         float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.out) + at);
 #pragma unroll
-        for (int i = 0; i < D / 4; ++i)
+        for (int i = 0; i < N / 4; ++i)
             dst[i] = make_float4(o[4 * i] * inv, o[4 * i + 1] * inv, o[4 * i + 2] * inv, o[4 * i + 3] * inv);
     } else {
         uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + at);
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
+        for (int i = 0; i < N / 8; ++i) {
             uint32_t w[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e)

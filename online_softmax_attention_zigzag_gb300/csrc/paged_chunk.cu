@@ -19,12 +19,12 @@
 //     row sees whole have their V looked over before the product: rows that nobody sees
 //     become zeros, and infinities and NaN become zeros that the rows that do see them add at
 //     the end.
-//   * e4m3: four warps expand codes into the bf16 tiles: exponent and mantissa bits moved into
+//   * e4m3: eight warps expand codes into the bf16 tiles: exponent and mantissa bits moved into
 //     place are the value times 2^-120, exact for subnormal codes too, and one packed
 //     multiplication by 2^120 * scale finishes it, exact for scales that are powers of two.
 //
 // Warps: 0-7 softmax (four a unit), 8 and 9 issue the units' MMAs, 10 loads, 11 (bf16) looks
-// values over; e4m3: 12-15 expand and look over.  TMEM as in the ring kernel: S_x at
+// values over; e4m3: 12-19 expand and look over.  TMEM as in the ring kernel: S_x at
 // [128 x, 128 x + 128), P_x over the upper half of S_x, O_x at 256 + D x.
 #include <cuda_bf16.h>
 
@@ -43,7 +43,7 @@ constexpr int kPoison = 8;  // marks of the last parts, in turn: part k's holds 
 
 template <int D, bool E4M3>
 struct Cfg {
-    static constexpr int kThreads = E4M3 ? 512 : 384;
+    static constexpr int kThreads = E4M3 ? 640 : 384;
     static constexpr int kTileBytes = kTile * D * 2;  // a bf16 tile
     static constexpr int kBoxBytes = kTile * 128;     // 64 columns of it
     static constexpr int kBoxes = D / 64;
@@ -84,11 +84,11 @@ struct Chunk {
     __device__ __forceinline__ int key(int t) const { return (t < ns ? t : lo + t - ns) * kTile; }
 };
 
-__device__ __forceinline__ Chunk make_chunk(const PagedAttnParams& p, int b, int pair) {
+__device__ __forceinline__ Chunk make_chunk(const PagedAttnParams& p, int b, int pair, const PagedSeq& s) {
     Chunk c;
     c.b = b;
     c.pair = pair;
-    c.s = paged_seq(p.kv, b);
+    c.s = s;
     const int tt = 2 * p.unit_tokens;
     c.ta = pair * tt;
     c.tb = min(min(c.s.T, p.max_q), c.ta + tt);
@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const __grid_c
                 if (plan.base[mid] <= e) lo = mid;
                 else hi = mid;
             }
-            n = make_chunk(p, lo, e - plan.base[lo]).n;
+            n = make_chunk(p, lo, e - plan.base[lo], paged_seq(p.kv, lo)).n;
         }
         const long long at = block_scan(n, scratch, all);
         if (e < E) plan.pre[e] = sum + at;
@@ -226,8 +226,9 @@ __device__ __forceinline__ void for_each_part(const PagedAttnParams& p, F&& f) {
     int e = lo;
     q.ta = static_cast<int>(in - plan.pre[e]);
     q.k = 0;
+    PagedSeq s = paged_seq(p.kv, b);
     while (true) {
-        q.c = make_chunk(p, b, e - e0);
+        q.c = make_chunk(p, b, e - e0, s);
         q.tb = static_cast<int>(min(static_cast<long long>(q.c.n), q.ta + (w1 - w)));
         if (!f(q)) return;
         w += q.tb - q.ta;
@@ -244,6 +245,7 @@ __device__ __forceinline__ void for_each_part(const PagedAttnParams& p, F&& f) {
                     e1 = plan.base[b + 1];
                 } while (e1 == e0);
                 e = e0;
+                s = paged_seq(p.kv, b);
             }
         }
     }
@@ -284,16 +286,18 @@ __device__ void load_role(const PagedAttnParams& p, const CUtensorMap* tq, const
         }
         // K and V are read again by the sequence's other pairs, if it has any
         const uint64_t policy = q.c.s.T > 2 * p.unit_tokens ? keep : stream;
-        int page = -1, row = 0, prev_page = -1, prev_y = 0;
-        auto look = [&](int t) {  // the page of this lane's box; no page behind the last key
+        // the page of this lane's box, asked for a tile ahead and looked at only when it is needed: a load
+        // waited for here would hold up the copies
+        int entry = -1, row = 0, prev_page = -1, prev_y = 0;
+        auto look = [&](int t) {  // no page behind the last key
             const int pos = q.c.key(t) + lane * rows;
-            page = -1;
+            entry = -1;
             row = 0;
-            if (lane < boxes && pos < q.c.hi) page = paged_page(kv, q.c.b, pos, row);
+            if (lane < boxes && pos < q.c.hi) entry = paged_entry(kv, q.c.b, pos, row);
         };
         look(q.ta);
         for (int t = q.ta; t <= q.tb; ++t) {
-            const int pg = page, y = q.h * kv.page + row;
+            const int pg = paged_checked(kv, entry), y = q.h * kv.page + row;
             if (t + 1 < q.tb) look(t + 1);
             const bool has_v = t > q.ta, has_k = t < q.tb;
             if constexpr (E4M3) {
@@ -396,44 +400,46 @@ __device__ void fix_role(const PagedAttnParams& p, uint8_t* smem, Bars& b, volat
     });
 }
 
-// e4m3: 128 threads, a row each, expand every tile into its bf16 stage.
+// e4m3: 256 threads, half a row each, expand every tile into its bf16 stage.
 template <int D>
-__device__ void expand_role(const PagedAttnParams& p, uint8_t* smem, Bars& b, volatile int* poison, const WaitCtl& wc) {
+__device__ void expand_role(const PagedAttnParams& p, uint32_t smem, Bars& b, volatile int* poison, const WaitCtl& wc) {
     using C = Cfg<D, true>;
     const PagedKV& kv = p.kv;
-    const int r = threadIdx.x - kExpandWarp * 32;
+    const int r = threadIdx.x & (kTile - 1);
+    const int c0 = threadIdx.x >= kExpandWarp * 32 + kTile ? D / 32 : 0;  // first chunk of this half
     uint32_t st = 0, raw = 0;
-    auto expand = [&](uint8_t* dst, float scale, bool zero) -> bool {
+    const uint32_t row_at = r * 128, sw = r & 7;
+    auto expand = [&](uint32_t dst, float scale, bool zero) -> bool {
         const uint32_t slot = raw % C::kRaw;
         if (!mbar_wait_w(&b.raw_full[slot], (raw / C::kRaw) & 1u, wc)) return false;
         ++raw;
-        const uint8_t* src = smem + C::kRawOff + slot * C::kRawBytes + r * D;
-        const int sw = D == 128 ? (r & 7) : ((r >> 1) & 3);
-        uint4 x[D / 16];
-#pragma unroll
-        for (int c = 0; c < D / 16; ++c) x[c] = *reinterpret_cast<const uint4*>(src + ((c ^ sw) << 4));
-        // 2^120 * scale, in two factors where it is no bf16 number
+        const uint32_t src = smem + C::kRawOff + slot * C::kRawBytes + r * D;
+        const uint32_t src_sw = D == 128 ? sw : ((r >> 1) & 3);
+        // 2^120 * scale, in two factors where it is no bf16 number; 0 where the row counts as zeros
+        // (a scale that is no number is kept out of the product there)
         const bool big = scale > 128.f;
-        const float f1 = big ? 0x1p120f : scale * 0x1p120f;
-        __nv_bfloat162 m1 = __float2bfloat162_rn(f1), m2 = __float2bfloat162_rn(big ? scale : 1.f);
+        const __nv_bfloat162 m1 = __float2bfloat162_rn(zero ? 0.f : big ? 0x1p120f : scale * 0x1p120f);
+        const __nv_bfloat162 m2 = __float2bfloat162_rn(big && !zero ? scale : 1.f);
         const bool any_big = __any_sync(0xffffffffu, big);
+        uint4 next = lds128(src + ((c0 ^ src_sw) << 4));
 #pragma unroll
-        for (int c = 0; c < D / 16; ++c) {
-            const uint32_t w[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
+        for (int i2 = 0; i2 < D / 32; ++i2) {
+            const int c = c0 + i2;
+            const uint4 x = next;
+            if (i2 + 1 < D / 32) next = lds128(src + (((c + 1) ^ src_sw) << 4));
+            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
             uint32_t y[8];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const uint32_t a = __byte_perm(w[i], 0, e ? 0x3424 : 0x1404);  // a code in each high byte
-                    const uint32_t v = ((a >> 4) & 0x07f007f0u) | (a & 0x80008000u);
-                    __nv_bfloat162 z = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&v), m1);
-                    if (any_big) z = __hmul2(z, m2);
-                    y[2 * i + e] = zero ? 0u : *reinterpret_cast<const uint32_t*>(&z);
-                }
-            uint8_t* d = dst + (c >> 2) * C::kBoxBytes + r * 128;
-            *reinterpret_cast<uint4*>(d + (((2 * c) & 7) ^ (r & 7)) * 16) = make_uint4(y[0], y[1], y[2], y[3]);
-            *reinterpret_cast<uint4*>(d + (((2 * c + 1) & 7) ^ (r & 7)) * 16) = make_uint4(y[4], y[5], y[6], y[7]);
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t a = __byte_perm(w[i >> 1], 0, i & 1 ? 0x3424 : 0x1404);  // a code in each high byte
+                const uint32_t v = ((a >> 4) & 0x07f007f0u) | (a & 0x80008000u);
+                __nv_bfloat162 z = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&v), m1);
+                if (any_big) z = __hmul2(z, m2);
+                y[i] = *reinterpret_cast<const uint32_t*>(&z);
+            }
+            const uint32_t d = dst + (c >> 2) * C::kBoxBytes + row_at;
+            sts128(d + ((((2 * c) & 7) ^ sw) << 4), y[0], y[1], y[2], y[3]);
+            sts128(d + ((((2 * c + 1) & 7) ^ sw) << 4), y[4], y[5], y[6], y[7]);
         }
         // Only now, when every loaded code has been used: an arrival right behind the loads let the
         // next tile's copy overtake them (seen as wrong values in the chunks loaded last).
@@ -441,25 +447,32 @@ __device__ void expand_role(const PagedAttnParams& p, uint8_t* smem, Bars& b, vo
         return true;
     };
     for_each_part(p, [&](const Part& q) -> bool {
-        // this row's scales, a tile ahead
+        // this row's page two tiles ahead, and its scales one: neither load is waited for at once
         float ks = 0.f, vs = 0.f;
+        int entry = -1, row = 0;
         auto look = [&](int t) {
             const int pos = q.c.key(t) + r;
-            int row = 0;
-            const int pg = pos < q.c.hi ? paged_page(kv, q.c.b, pos, row) : -1;
+            entry = -1;
+            if (t < q.tb && pos < q.c.hi) entry = paged_entry(kv, q.c.b, pos, row);
+        };
+        auto fetch = [&]() {
+            const int pg = paged_checked(kv, entry);
             const long long at = static_cast<long long>(q.h) * kv.page + row;
             ks = pg >= 0 ? __ldg(kv.k_scale + pg * kv.ks_ps + at) : 0.f;
             vs = pg >= 0 ? __ldg(kv.v_scale + pg * kv.vs_ps + at) : 0.f;
         };
         look(q.ta);
+        fetch();
+        look(q.ta + 1);
         float prev_vs = 0.f;
         for (int t = q.ta; t <= q.tb; ++t, ++st) {
             const float k1 = ks, v1 = prev_vs;
             prev_vs = vs;
-            if (t + 1 < q.tb) look(t + 1);
+            fetch();
+            look(t + 2);
             const uint32_t slot = st % C::kStages;
             if (!mbar_wait_w(&b.kv_empty[slot], ((st / C::kStages) & 1u) ^ 1u, wc)) return false;
-            uint8_t* stage = smem + C::kKVOff + slot * C::kStageBytes;
+            const uint32_t stage = smem + C::kKVOff + slot * C::kStageBytes;
             if (t > q.ta) {
                 bool zero = false;
                 const int j0 = q.c.key(t - 1);
@@ -612,6 +625,44 @@ __device__ void mma_role(const PagedAttnParams& p, int x, uint32_t smem, Bars& b
 }
 
 // ------------------------------------------------------------------ softmax
+// Bits [0, n) set, n clamped to 0 .. 32.
+__device__ __forceinline__ uint32_t low_bits(int n) {
+    return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
+}
+// Which of 32 keys a row sees: below hi, and from lo on or below the sinks (all relative to them).
+__device__ __forceinline__ uint32_t seen_bits(int hi, int lo, int sinks) {
+    return low_bits(hi) & (~low_bits(lo) | low_bits(sinks));
+}
+
+// Values that are no numbers, of the keys a row sees in the part's tiles that were looked over:
+// columns [cc, cc + 32) of the row's sum.  (Those of other tiles went into the product.)
+template <bool E4M3, int D>
+__device__ __noinline__ void add_sick(const PagedAttnParams& p, const Chunk& c, int h, int ta, int tb, int hi, int lo,
+                                      int cc, float (&o)[32]) {
+    for (int t = ta; t < tb; ++t) {
+        const int j0 = c.key(t);
+        if (whole_tile(p, c, j0)) continue;
+        for (int j = j0; j < min(j0 + kTile, hi); ++j) {
+            if (j < lo && j >= p.sinks) continue;
+            int r;
+            const int pg = paged_page(p.kv, c.b, j, r);
+            if (pg < 0) continue;
+            const long long at = static_cast<long long>(h) * p.kv.page + r;
+            if constexpr (E4M3) {
+                if (fabsf(__ldg(p.kv.v_scale + pg * p.kv.vs_ps + at)) < INFINITY) continue;
+                for (int i = 0; i < 32; ++i) o[i] = __uint_as_float(0x7fc00000u);
+            } else {
+                const uint32_t* v = reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(p.kv.v) + pg * p.kv.v_ps + at * D + cc);
+                for (int i = 0; i < 16; ++i) {
+                    const uint32_t y = __ldg(v + i);
+                    if ((y & 0x7f80u) == 0x7f80u) o[2 * i] += __uint_as_float(y << 16);
+                    if ((y & 0x7f800000u) == 0x7f800000u) o[2 * i + 1] += __uint_as_float(y & 0xffff0000u);
+                }
+            }
+        }
+    }
+}
+
 template <int D, bool E4M3>
 __device__ void softmax_role(const PagedAttnParams& p, int x, Bars& b, uint32_t tmem, const volatile int* poison,
                              const WaitCtl& wc) {
@@ -642,6 +693,22 @@ __device__ void softmax_role(const PagedAttnParams& p, int x, Bars& b, uint32_t 
             if (!wait(&b.s_full[x], sit & 1u)) return false;
             ++sit;
             tc_fence_after();
+            // A tile that not every row of the unit sees whole is masked in place, 32 columns at a time
+            // in a rolled loop: it is rare, and as straight code over 128 registers it ran at the speed
+            // of instruction fetches (9 us a tile).
+            if (j0 + kTile > u_hi || (j0 < u_lo && j0 + kTile > p.sinks)) {
+#pragma unroll 1
+                for (int cc = 0; cc < kTile; cc += 32) {
+                    const uint32_t see = seen_bits(hi - j0 - cc, lo - j0 - cc, p.window > 0 ? p.sinks - j0 - cc : 0);
+                    uint32_t r[32];
+                    tmem_ld32(s_tmem + cc, r);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) r[i] = (see & (1u << i)) ? r[i] : 0xff800000u;
+                    tmem_st32(s_tmem + cc, r);
+                }
+                tmem_wait_st();
+            }
             float s[kTile];
             float pm0, pm1, pm2, pm3;
             {
@@ -659,20 +726,7 @@ __device__ void softmax_role(const PagedAttnParams& p, int x, Bars& b, uint32_t 
                     s[96 + i] = __uint_as_float(r3[i]);
                 }
             }
-            float mx = fmaxf(fmaxf(pm0, pm1), fmaxf(pm2, pm3));
-            if (j0 + kTile > u_hi || (j0 < u_lo && j0 + kTile > p.sinks)) {
-                const int h = hi - j0, w = lo - j0, k = p.window > 0 ? p.sinks - j0 : 0;
-#pragma unroll
-                for (int i = 0; i < kTile; ++i) s[i] = (i >= h || (i < w && i >= k)) ? -INFINITY : s[i];
-                float c[8];
-#pragma unroll
-                for (int a = 0; a < 8; ++a) c[a] = fmaxf(s[2 * a], s[2 * a + 1]);
-#pragma unroll
-                for (int i = 16; i < kTile; i += 16)
-#pragma unroll
-                    for (int a = 0; a < 8; ++a) c[a] = fmax3(c[a], s[i + 2 * a], s[i + 2 * a + 1]);
-                mx = fmaxf(fmax3(c[0], c[1], c[2]), fmax3(c[3], c[4], fmax3(c[5], c[6], c[7])));
-            }
+            const float mx = fmaxf(fmaxf(pm0, pm1), fmaxf(pm2, pm3));
             const float m_new = fmaxf(m, mx * kLog2e);
             float f = 1.f;
             bool need = false;
@@ -723,53 +777,48 @@ __device__ void softmax_role(const PagedAttnParams& p, int x, Bars& b, uint32_t 
         if (!wait(&b.o_done[x], iit & 1u)) return false;
         ++iit;
         tc_fence_after();
-        float o[D];
-#pragma unroll
-        for (int cc = 0; cc < D; cc += 32) {
-            uint32_t r[32];
-            tmem_ld32(o_tmem + cc, r);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) o[cc + i] = __uint_as_float(r[i]);
-        }
-        tmem_wait_ld();
-        tc_fence_before();
-        mbar_arrive(&b.o_free[x]);
         const bool cut = q.ta > 0 || q.tb < q.c.n;
         const bool live = row < p.unit_tokens * p.g && t_row < q.c.tb;
-        if (live && poison[q.k % kPoison] == q.k + 1) {  // values that are no numbers, of the keys this row sees
-            for (int t = q.ta; t < q.tb; ++t) {
-                const int j0 = q.c.key(t);
-                if (whole_tile(p, q.c, j0)) continue;  // its values went into the product as they are
-                for (int j = j0; j < min(j0 + kTile, hi); ++j) {
-                    if (j < lo && j >= p.sinks) continue;
-                    int r;
-                    const int pg = paged_page(p.kv, q.c.b, j, r);
-                    if (pg < 0) continue;
-                    const long long at = static_cast<long long>(q.h) * p.kv.page + r;
-                    if constexpr (E4M3) {
-                        if (fabsf(__ldg(p.kv.v_scale + pg * p.kv.vs_ps + at)) < INFINITY) continue;
+        const bool sick = poison[q.k % kPoison] == q.k + 1;
+        const float inv = lr == 0.f ? 0.f : 1.f / lr;
+        const int tok = q.c.s.q0 + t_row, head = q.h * p.g + row - tok_in * p.g;
+        PagedChunkPartial* part = static_cast<PagedChunkPartial*>(p.workspace) + 2 * blockIdx.x + (q.k ? 1 : 0);
+        const int r2 = x * kTile + row;
+        // (rolled, as the mask: a quarter of the code to fetch once an item)
+#pragma unroll 1
+        for (int cc = 0; cc < D; cc += 32) {
+            float o[32];
+            {
+                uint32_t r[32];
+                tmem_ld32(o_tmem + cc, r);
+                tmem_wait_ld();
 #pragma unroll
-                        for (int i = 0; i < D; ++i) o[i] = __uint_as_float(0x7fc00000u);
-                    } else {
-                        const uint32_t* v = reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(p.kv.v) + pg * p.kv.v_ps + at * D);
+                for (int i = 0; i < 32; ++i) o[i] = __uint_as_float(r[i]);
+            }
+            if (cc + 32 == D) {
+                tc_fence_before();
+                mbar_arrive(&b.o_free[x]);
+            }
+            if (!live) continue;
+            if (sick) {  // (copies, so that only this rare call keeps anything in memory)
+                const Chunk c = q.c;
+                float o2[32];
 #pragma unroll
-                        for (int i = 0; i < D / 2; ++i) {
-                            const uint32_t y = __ldg(v + i);
-                            if ((y & 0x7f80u) == 0x7f80u) o[2 * i] += __uint_as_float(y << 16);
-                            if ((y & 0x7f800000u) == 0x7f800000u) o[2 * i + 1] += __uint_as_float(y & 0xffff0000u);
-                        }
-                    }
-                }
+                for (int i = 0; i < 32; ++i) o2[i] = o[i];
+                add_sick<E4M3, D>(p, c, q.h, q.ta, q.tb, hi, lo, cc, o2);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) o[i] = o2[i];
+            }
+            if (cut) {
+                float4* dst = reinterpret_cast<float4*>(part->o + r2 * kPagedMaxD + cc);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+            } else {
+                paged_store_cols<32>(p, tok, head, cc, o, inv);
             }
         }
         if (cut) {
-            PagedChunkPartial* part = static_cast<PagedChunkPartial*>(p.workspace) + 2 * blockIdx.x + (q.k ? 1 : 0);
-            const int r2 = x * kTile + row;
             if (live) {
-                float* dst = part->o + r2 * kPagedMaxD;
-#pragma unroll
-                for (int i = 0; i < D; i += 4)
-                    *reinterpret_cast<float4*>(dst + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
                 part->m[r2] = m;
                 part->l[r2] = l;
                 part->lr[r2] = lr;
@@ -780,13 +829,8 @@ __device__ void softmax_role(const PagedAttnParams& p, int x, Bars& b, uint32_t 
                 part->h = q.h;
                 part->begins = q.ta == 0;
             }
-        } else {
-            if (live) {
-                const float inv = lr == 0.f ? 0.f : 1.f / lr;
-                const int tok = q.c.s.q0 + t_row, head = q.h * p.g + row - tok_in * p.g;
-                paged_store_row<D>(p, tok, head, o, inv);
-                p.lse[tok * p.l_ts + head * p.l_hs] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
-            }
+        } else if (live) {
+            p.lse[tok * p.l_ts + head * p.l_hs] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
         }
         return true;
     });
@@ -814,10 +858,10 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
             mbar_init(&b.fixed[x], 1);
         }
         for (int s = 0; s < 4; ++s) {
-            mbar_init(&b.kv_full[s], E4M3 ? 128 : 1);
+            mbar_init(&b.kv_full[s], E4M3 ? 256 : 1);
             mbar_init(&b.kv_empty[s], E4M3 ? 2 : 3);  // both issuers, and the warp that looks values over
             mbar_init(&b.raw_full[s], 1);
-            mbar_init(&b.raw_empty[s], 128);
+            mbar_init(&b.raw_empty[s], 256);
         }
         sh.abort_flag = 0;
         sh.turn = 0;
@@ -837,17 +881,17 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
     const uint32_t tmem = sh.tmem;
     const WaitCtl wc{&sh.abort_flag, p.err, p.timeout_ns};
     if (warp < 8) {
-        // e4m3: 512 threads start with 128 registers each; 256 * 168 + 256 * 88 is the same sum
+        // e4m3: 640 threads start with 96 registers each; 256 * 168 + 384 * 48 is the same sum
         if constexpr (E4M3) asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
         softmax_role<D, E4M3>(p, warp / 4, b, tmem, sh.poison, wc);
     } else {
-        if constexpr (E4M3) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+        if constexpr (E4M3) asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
         if (warp == kMmaWarp || warp == kMmaWarp + 1) {
             mma_role<D, E4M3>(p, warp - kMmaWarp, smem_u32(smem), b, tmem, &sh.turn, wc);
         } else if (warp == kLoadWarp) {
             load_role<D, E4M3>(p, &tq, &tk, &tv, smem_u32(smem), b, wc);
         } else if constexpr (E4M3) {
-            if (warp >= kExpandWarp) expand_role<D>(p, smem, b, sh.poison, wc);
+            if (warp >= kExpandWarp) expand_role<D>(p, smem_u32(smem), b, sh.poison, wc);
         } else {
             fix_role<D>(p, smem, b, sh.poison, wc);
         }
@@ -870,7 +914,7 @@ __global__ void __launch_bounds__(kJoinRows * 32) paged_chunk_join_kernel(const 
     const PagedChunkPartial* p0 = parts + 2 * x + (parts[2 * x + 1].b >= 0 ? 1 : 0);
     const int b = p0->b, pair = p0->pair, h = p0->h;
     if (b < 0 || !p0->begins) return;
-    const Chunk c = make_chunk(p, b, pair);
+    const Chunk c = make_chunk(p, b, pair, paged_seq(p.kv, b));
     const int r = blockIdx.y * kJoinRows + threadIdx.x / 32;  // row of the two units
     const int unit = r / kTile, ru = r - unit * kTile, t = c.ta + unit * p.unit_tokens + ru / p.g;
     if (ru >= p.unit_tokens * p.g || t >= c.tb) return;
@@ -926,11 +970,15 @@ template <int D, bool E4M3>
 int launch_t(const PagedAttnParams& p, const PagedMaps& m, int shares, cudaStream_t stream) {
     using C = Cfg<D, E4M3>;
     auto kern = paged_chunk_kernel<D, E4M3>;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes) != cudaSuccess) return -4;
-    if constexpr (E4M3) {  // the register split adds up only if the block starts with 128 a thread
-        cudaFuncAttributes a;
-        if (cudaFuncGetAttributes(&a, kern) != cudaSuccess || a.numRegs != 128) return -4;
-    }
+    static std::atomic<unsigned long long> ready{0};
+    if (!once_a_device(ready, [&] {
+            if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes) != cudaSuccess) return false;
+            if (!E4M3) return true;
+            // the register split adds up only if the block starts with 96 a thread
+            cudaFuncAttributes a;
+            return cudaFuncGetAttributes(&a, kern) == cudaSuccess && a.numRegs == 96;
+        }))
+        return -4;
     paged_plan_kernel<<<1, kPlanThreads, 0, stream>>>(p);
     if (cudaGetLastError() != cudaSuccess) return -4;
     if (launch_dependent(kern, dim3(shares), C::kThreads, C::kSmemBytes, stream, p, m.q, m.k, m.v) != cudaSuccess) return -4;

@@ -158,16 +158,17 @@ __device__ void load_role(const PagedAttnParams& p, const CUtensorMap* tk, const
     for_each_part(p, pre, w0, w1, [&](const Part& q) -> bool {
         const PagedSeq s = paged_seq(kv, q.b);
         const Tiles kt = key_tiles(p, s);
-        int page = -1, row = 0;
-        auto look = [&](int t) {  // the page of this lane's box of tile t; no page behind the last key
+        // the page of this lane's box, asked for a tile ahead and looked at only when it is needed
+        int entry = -1, row = 0;
+        auto look = [&](int t) {  // no page behind the last key
             const int pos = (t < kt.ns ? t : kt.lo + t - kt.ns) * kTile + lane * rows;
-            page = -1;
+            entry = -1;
             row = 0;
-            if (lane < boxes && pos < s.L) page = paged_page(kv, q.b, pos, row);
+            if (lane < boxes && pos < s.L) entry = paged_entry(kv, q.b, pos, row);
         };
         look(q.ta);
         for (int t = q.ta; t < q.tb; ++t) {
-            const int pg = page, y = q.h * kv.page + row;
+            const int pg = paged_checked(kv, entry), y = q.h * kv.page + row;
             if (t + 1 < q.tb) look(t + 1);
 #pragma unroll
             for (int half = 0; half < 2; ++half, ++it) {
@@ -722,7 +723,12 @@ int launch_t(const PagedAttnParams& p, const PagedMaps& m, int shares, cudaStrea
     using C = Cfg<D, E4M3>;
     auto kern = paged_decode_kernel<D, E4M3>;
     const int bytes = C::kFixedBytes + 4 * (p.kv.batch + 1);
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return -4;
+    static std::atomic<unsigned long long> ready{0};
+    if (!once_a_device(ready, [&] {
+            return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                        C::kFixedBytes + 4 * (kPagedMaxBatch + 1)) == cudaSuccess;
+        }))
+        return -4;
     kern<<<shares, kThreads, bytes, stream>>>(p, m.k, m.v, m.ks, m.vs);
     if (cudaGetLastError() != cudaSuccess) return -4;
     cudaLaunchConfig_t cfg = {};

@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import numpy as np
 import torch
@@ -356,53 +357,71 @@ def _strided(t: torch.Tensor, name: str, dtype, dev: int, dim: int) -> int:
     return t.data_ptr()
 
 
-def _step(t: torch.Tensor, axis: int) -> int:
-    """Stride of an axis; of an axis of one entry, whose stride means nothing, that of a
-    contiguous tensor."""
-    if t.shape[axis] > 1:
-        return t.stride(axis)
-    n = 1
-    for size in t.shape[axis + 1:]:
-        n *= size
-    return max(1, n)
+def _rows(t: torch.Tensor, name: str, dtype, dev: int):
+    """(address, first stride, second stride) of a [n, m, d] tensor.  The stride of an axis of one
+    entry means nothing: it becomes that of a contiguous tensor."""
+    shape = t.shape
+    if t.dtype is not dtype or t.get_device() != dev or len(shape) != 3:
+        _strided(t, name, dtype, dev, 3)
+    n, m, d = shape
+    s0, s1, s2 = t.stride()
+    if s2 != 1:
+        _strided(t, name, dtype, dev, 3)
+    return t.data_ptr(), (s0 if n > 1 else max(1, m * d)), (s1 if m > 1 else max(1, d))
 
 
-def _paged(k_cache, v_cache, k_scale, v_scale, block_table, cu, kv_len, total: int, dev: int) -> _PagedKV:
-    """The library's description of a paged cache and the batch that uses it."""
-    e4m3 = k_cache.dtype == torch.float8_e4m3fn
+# ra_paged_kv's fields in order: pointers, 64-bit strides, 32-bit sizes
+_pack_paged = struct.Struct("7P5q8i").pack
+
+
+def _paged(k_cache, v_cache, k_scale, v_scale, block_table, cu, kv_len, total: int, dev: int):
+    """(Hkv, d, ra_paged_kv as bytes): the library's description of a paged cache and the batch
+    that uses it.  These calls run once a layer and token: what is right passes a few combined
+    tests, and only what is not goes on to the one that says why."""
+    e4m3 = k_cache.dtype is torch.float8_e4m3fn
     dtype = torch.float8_e4m3fn if e4m3 else torch.bfloat16
-    a = _PagedKV()
-    a.k = _strided(k_cache, "k_cache", dtype, dev, 4)
-    a.v = _strided(v_cache, "v_cache", dtype, dev, 4)
+    i32 = torch.int32
     shape = k_cache.shape
-    n, h, page, d = shape
-    if v_cache.shape != shape:
+    if not (k_cache.get_device() == v_cache.get_device() == block_table.get_device() == cu.get_device()
+            == kv_len.get_device() == dev and k_cache.dtype is dtype and v_cache.dtype is dtype
+            and block_table.dtype is i32 and cu.dtype is i32 and kv_len.dtype is i32
+            and len(shape) == 4 and v_cache.shape == shape and block_table.dim() == 2):
+        for t, name, dt, dim in ((k_cache, "k_cache", dtype, 4), (v_cache, "v_cache", dtype, 4),
+                                 (block_table, "block_table", i32, 2), (cu, "cu", i32, 1), (kv_len, "kv_len", i32, 1)):
+            _strided(t, name, dt, dev, dim)
         raise ValueError("k_cache and v_cache must have the same shape [n_pages, Hkv, page_size, d]")
-    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        if (h > 1 and t.stride(1) != page * d) or (page > 1 and t.stride(2) != d):
-            raise ValueError(f"each page of {name} must be contiguous")
-    a.k_page_stride, a.v_page_stride = _step(k_cache, 0), _step(v_cache, 0)
+    n, h, page, d = shape
+    rows = h * page
+    k0, k1, k2, k3 = k_cache.stride()
+    v0, v1, v2, v3 = v_cache.stride()
+    pd = page * d
+    if k3 != 1 or v3 != 1 or (h > 1 and (k1 != pd or v1 != pd)) or (page > 1 and (k2 != d or v2 != d)):
+        raise ValueError("each page of k_cache and v_cache must be contiguous")
     if (k_scale is not None) != e4m3 or (v_scale is not None) != e4m3:
         raise ValueError("an e4m3 cache has k_scale and v_scale, a bf16 cache has none")
+    ksp = vsp = ks0 = vs0 = 0
     if e4m3:
-        for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-            p = _strided(t, name, torch.float32, dev, 3)
-            if t.shape != shape[:3]:
-                raise ValueError(f"{name} must be [n_pages, Hkv, page_size]")
-            if h > 1 and t.stride(1) != page:
-                raise ValueError(f"each page of {name} must be contiguous")
-            setattr(a, name, p)
-        a.k_scale_page_stride, a.v_scale_page_stride = _step(k_scale, 0), _step(v_scale, 0)
-    a.block_table = _strided(block_table, "block_table", torch.int32, dev, 2)
-    a.cu = _strided(cu, "cu", torch.int32, dev, 1)
-    a.kv_len = _strided(kv_len, "kv_len", torch.int32, dev, 1)
-    batch, a.max_pages = block_table.shape
-    if cu.shape[0] != batch + 1 or kv_len.shape[0] != batch:
+        want = (n, h, page)
+        if k_scale.shape != want or v_scale.shape != want:
+            raise ValueError("k_scale and v_scale must be [n_pages, Hkv, page_size]")
+        (ksp, ks0, ks1), (vsp, vs0, vs1) = (_rows(k_scale, "k_scale", torch.float32, dev),
+                                            _rows(v_scale, "v_scale", torch.float32, dev))
+        if ks1 != page or vs1 != page:
+            raise ValueError("each page of k_scale and v_scale must be contiguous")
+    batch, max_pages = block_table.shape
+    t0, t1 = block_table.stride()
+    if cu.shape != (batch + 1,) or kv_len.shape != (batch,):
         raise ValueError("block_table must be [batch, max_pages], cu [batch + 1] and kv_len [batch]")
-    a.table_stride = _step(block_table, 0)
-    a.n_pages, a.Hkv, a.page_size, a.d = n, h, page, d
-    a.dtype, a.batch, a.total = int(e4m3), batch, total
-    return a
+    if (t1 != 1 and max_pages > 1) or not cu.is_contiguous() or not kv_len.is_contiguous():
+        raise ValueError("cu, kv_len and the rows of block_table must be contiguous")
+    return h, d, _pack_paged(k_cache.data_ptr(), v_cache.data_ptr(), ksp, vsp, block_table.data_ptr(), cu.data_ptr(),
+                             kv_len.data_ptr(), k0 if n > 1 else rows * d, v0 if n > 1 else rows * d, ks0, vs0,
+                             t0 if batch > 1 else max_pages, n, page, h, d, e4m3, batch, max_pages, total)
+
+
+def _raw_stream(stream, dev: int) -> int:
+    """As :func:`_stream`, without making a Stream object for the current one."""
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
 
 
 def cache_append(k_new, v_new, k_cache, v_cache, block_table, cu, kv_len, *, k_scale=None, v_scale=None,
@@ -413,13 +432,14 @@ def cache_append(k_new, v_new, k_cache, v_cache, block_table, cu, kv_len, *, k_s
     page_size] fp32).  block_table [batch, max_pages], cu [batch + 1] and kv_len [batch] are
     int32; kv_len counts the new tokens."""
     dev = torch.cuda.current_device()
-    kp, vp = _strided(k_new, "k_new", torch.bfloat16, dev, 3), _strided(v_new, "v_new", torch.bfloat16, dev, 3)
+    kp, k0, k1 = _rows(k_new, "k_new", torch.bfloat16, dev)
+    vp, v0, v1 = _rows(v_new, "v_new", torch.bfloat16, dev)
     total = k_new.shape[0]
-    a = _paged(k_cache, v_cache, k_scale, v_scale, block_table, cu, kv_len, total, dev)
-    if tuple(k_new.shape) != (total, a.Hkv, a.d) or v_new.shape != k_new.shape:
+    h, d, kv = _paged(k_cache, v_cache, k_scale, v_scale, block_table, cu, kv_len, total, dev)
+    if k_new.shape != (total, h, d) or v_new.shape != (total, h, d):
         raise ValueError("k_new and v_new must be [total, Hkv, d] with the cache's Hkv and d")
-    _check("ringattn_cache_append", lib().ringattn_cache_append(
-        kp, vp, _step(k_new, 0), _step(k_new, 1), _step(v_new, 0), _step(v_new, 1), ctypes.byref(a), _stream(stream)))
+    _check("ringattn_cache_append", (_lib or lib()).ringattn_cache_append(kp, vp, k0, k1, v0, v1, kv,
+                                                                          _raw_stream(stream, dev)))
 
 
 def cache_read(k_cache, v_cache, k_out, v_out, block_table, cu, kv_len, *, k_scale=None, v_scale=None,
@@ -429,12 +449,12 @@ def cache_read(k_cache, v_cache, k_out, v_out, block_table, cu, kv_len, *, k_sca
     dev = torch.cuda.current_device()
     kp, vp = _strided(k_out, "k_out", torch.bfloat16, dev, 3), _strided(v_out, "v_out", torch.bfloat16, dev, 3)
     total = k_out.shape[1]
-    a = _paged(k_cache, v_cache, k_scale, v_scale, block_table, cu, kv_len, total, dev)
-    if tuple(k_out.shape) != (a.Hkv, total, a.d) or v_out.shape != k_out.shape:
+    h, d, kv = _paged(k_cache, v_cache, k_scale, v_scale, block_table, cu, kv_len, total, dev)
+    if k_out.shape != (h, total, d) or v_out.shape != (h, total, d):
         raise ValueError("k_out and v_out must be [Hkv, total, d] with the cache's Hkv and d")
     if not (k_out.is_contiguous() and v_out.is_contiguous()):
         raise ValueError("k_out and v_out must be contiguous")
-    _check("ringattn_cache_read", lib().ringattn_cache_read(ctypes.byref(a), kp, vp, _stream(stream)))
+    _check("ringattn_cache_read", (_lib or lib()).ringattn_cache_read(kv, kp, vp, _raw_stream(stream, dev)))
 
 
 def paged_workspace_bytes(total: int, batch: int, Hq: int, Hkv: int, d: int, max_q: int) -> int:
@@ -453,20 +473,21 @@ def fwd_paged(q, k_cache, v_cache, out, lse, block_table, cu, kv_len, workspace,
     ``sinks`` positions.  max_q: at least the most rows of one sequence; workspace: a CUDA uint8
     tensor of at least :func:`paged_workspace_bytes`.  The cache as for :func:`cache_append`."""
     dev = torch.cuda.current_device()
-    f32 = out.dtype == torch.float32
-    qp = _strided(q, "q", torch.bfloat16, dev, 3)
-    op = _strided(out, "out", torch.float32 if f32 else torch.bfloat16, dev, 3)
+    f32 = out.dtype is torch.float32
+    qp, q0, q1 = _rows(q, "q", torch.bfloat16, dev)
+    op, o0, o1 = _rows(out, "out", torch.float32 if f32 else torch.bfloat16, dev)
     total, Hq, d = q.shape
-    a = _paged(k_cache, v_cache, k_scale, v_scale, block_table, cu, kv_len, total, dev)
-    if d != a.d or out.shape != q.shape:
+    _, kd, kv = _paged(k_cache, v_cache, k_scale, v_scale, block_table, cu, kv_len, total, dev)
+    if d != kd or out.shape != q.shape:
         raise ValueError("q and out must be [total, Hq, d] with the cache's d")
-    if not isinstance(lse, torch.Tensor) or lse.get_device() != dev or lse.dtype != torch.float32 or \
-            tuple(lse.shape) != (total, Hq):
+    if lse.get_device() != dev or lse.dtype is not torch.float32 or lse.shape != (total, Hq):
         raise ValueError("lse must be a fp32 [total, Hq] tensor on the current device")
-    wp = _strided(workspace, "workspace", torch.uint8, dev, 1)
-    _check("ringattn_fwd_paged", lib().ringattn_fwd_paged(
-        qp, _step(q, 0), _step(q, 1), ctypes.byref(a), op, _step(out, 0), _step(out, 1), int(f32), lse.data_ptr(),
-        _step(lse, 0), _step(lse, 1), Hq, max_q, int(causal), window, sinks, wp, workspace.shape[0], _stream(stream)))
+    l0, l1 = lse.stride()
+    if workspace.dtype is not torch.uint8 or workspace.get_device() != dev or workspace.stride() != (1,):
+        _strided(workspace, "workspace", torch.uint8, dev, 1)
+    _check("ringattn_fwd_paged", (_lib or lib()).ringattn_fwd_paged(
+        qp, q0, q1, kv, op, o0, o1, f32, lse.data_ptr(), l0 if total > 1 else max(1, Hq), l1 if Hq > 1 else 1, Hq, max_q,
+        causal, window, sinks, workspace.data_ptr(), workspace.shape[0], _raw_stream(stream, dev)))
 
 
 def rank_work(S: int, c: int, causal: int, layout: int, tile: int = 128):

@@ -173,6 +173,8 @@ def test_header_and_binding_agree(ra):
     fields = re.search(r"typedef struct \{(.*?)\} ra_paged_kv;", hdr, re.S).group(1)
     names = [n for decl in re.sub(r"/\*.*?\*/", "", fields, flags=re.S).split(";") for n in re.findall(r"(\w+)\s*(?:,|$)", decl.strip())]
     assert names == [n for n, _ in ra._PagedKV._fields_]
+    import struct
+    assert struct.calcsize("7P5q8i") == ctypes.sizeof(ra._PagedKV)  # the order that the binding packs
 
 
 # ------------------------------------------------------------------ refusals of the binding
@@ -181,7 +183,7 @@ def host(ra, monkeypatch):
     """CPU tensors stand for the device's: the checks run, the library refuses or is not reached."""
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
     monkeypatch.setattr(torch.Tensor, "get_device", lambda self: 0)
-    monkeypatch.setattr(ra, "_stream", lambda s: 0)
+    monkeypatch.setattr(ra, "_raw_stream", lambda s, dev: 0)
     return ra
 
 
