@@ -58,7 +58,7 @@ struct PagedKV {
 struct PagedChunkPartial {
     int b, pair, h, begins;
     float m[2 * 128], l[2 * 128], lr[2 * 128];
-    float o[2 * 128 * kPagedMaxD];
+    float4 o[kPagedMaxD / 4 * 2 * 128];  // [group of 4 columns][row]
 };
 
 struct PagedCopyParams {  // append: token-major rows in; read: [Hkv, total, d] out
@@ -173,28 +173,6 @@ __device__ __forceinline__ void paged_store4(const PagedAttnParams& p, int tok, 
         asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w.x) : "f"(x[1] * inv), "f"(x[0] * inv));
         asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w.y) : "f"(x[3] * inv), "f"(x[2] * inv));
         *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at) = w;
-    }
-}
-// N columns of an output row, times inv: 16-byte stores (rows start on 16 bytes).
-template <int N>
-__device__ __forceinline__ void paged_store_cols(const PagedAttnParams& p, int tok, int head, int col, const float (&o)[N],
-                                                 float inv) {
-    const long long at = tok * p.o_ts + head * p.o_hs + col;
-    if (p.out_f32) {
-        float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.out) + at);
-#pragma unroll
-        for (int i = 0; i < N / 4; ++i)
-            dst[i] = make_float4(o[4 * i] * inv, o[4 * i + 1] * inv, o[4 * i + 2] * inv, o[4 * i + 3] * inv);
-    } else {
-        uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + at);
-#pragma unroll
-        for (int i = 0; i < N / 8; ++i) {
-            uint32_t w[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[e]) : "f"(o[8 * i + 2 * e + 1] * inv), "f"(o[8 * i + 2 * e] * inv));
-            dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
-        }
     }
 }
 #endif

@@ -354,9 +354,14 @@ __device__ __forceinline__ bool key_used(const PagedAttnParams& p, const Chunk& 
 }
 __device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
+// A pair of bf16 with infinities and NaN as zeros.
+__device__ __forceinline__ uint32_t finite2(uint32_t y) {
+    return y & ~(((y & 0x7f80u) == 0x7f80u ? 0xffffu : 0u) | ((y & 0x7f800000u) == 0x7f800000u ? 0xffff0000u : 0u));
+}
+
 // bf16: one warp passes every stage; V tiles that not every row sees whole are cleaned in place.
 template <int D>
-__device__ void fix_role(const PagedAttnParams& p, uint8_t* smem, Bars& b, volatile int* poison, const WaitCtl& wc) {
+__device__ void fix_role(const PagedAttnParams& p, uint32_t smem, Bars& b, volatile int* poison, const WaitCtl& wc) {
     using C = Cfg<D, false>;
     const int lane = threadIdx.x & 31;
     uint32_t st = 0, nf = 0;
@@ -366,26 +371,34 @@ __device__ void fix_role(const PagedAttnParams& p, uint8_t* smem, Bars& b, volat
             if (!mbar_wait_w(&b.kv_full[slot], (st / C::kStages) & 1u, wc)) return false;
             const int j0 = t > q.ta ? q.c.key(t - 1) : 0;
             if (t > q.ta && !whole_tile(p, q.c, j0)) {
-                uint8_t* v = smem + C::kKVOff + slot * C::kStageBytes;
+                const uint32_t v = smem + C::kKVOff + slot * C::kStageBytes + lane * 16;
                 bool bad = false;
-                // lane l and its three neighbours take a row of 128 bytes, two chunks each; the swizzle
-                // permutes chunks inside a row only
-                for (int r = lane / 4; r < kTile; r += 8) {
-                    const bool used = key_used(p, q.c, j0 + r);
+                // eight lanes a row of 128 bytes, so four rows a load; eight loads in flight.  (The
+                // swizzle permutes chunks inside a row only.)
+#pragma unroll 1
+                for (int i = 0; i < C::kBoxes * 4; ++i) {
+                    const uint32_t at = v + (i >> 2) * C::kBoxBytes + (i & 3) * (32 * 128);
+                    const int r = (i & 3) * 32 + lane / 8;  // and r + 4, ... r + 28
+                    uint4 x[8];
+                    uint32_t top = 0, drop = 0;
 #pragma unroll
-                    for (int i = 0; i < 2 * C::kBoxes; ++i) {
-                        uint4* w = reinterpret_cast<uint4*>(v + (i >> 1) * C::kBoxBytes + r * 128) + (lane & 3) + 4 * (i & 1);
-                        uint4 x = *w;
-                        uint32_t* y = reinterpret_cast<uint32_t*>(&x);
-                        bool change = !used;
+                    for (int e = 0; e < 8; ++e) x[e] = lds128(at + e * 512);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const uint32_t m = ((y[e] & 0x7f80u) == 0x7f80u ? 0xffffu : 0u) |
-                                               ((y[e] & 0x7f800000u) == 0x7f800000u ? 0xffff0000u : 0u);
-                            if (used && m) bad = change = true;
-                            y[e] = used ? y[e] & ~m : 0u;
+                    for (int e = 0; e < 8; ++e) {
+                        const uint32_t m = __vmaxu2(__vmaxu2(x[e].x & 0x7fff7fffu, x[e].y & 0x7fff7fffu),
+                                                    __vmaxu2(x[e].z & 0x7fff7fffu, x[e].w & 0x7fff7fffu));
+                        if (key_used(p, q.c, j0 + r + 4 * e)) top = __vmaxu2(top, m);
+                        else drop |= 1u << e;
+                    }
+                    const bool sick = max(top & 0xffffu, top >> 16) >= 0x7f80u;
+                    if (drop || sick) {
+                        bad |= sick;
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const uint32_t keep = (drop >> e) & 1u ? 0u : 0xffffffffu;
+                            sts128(at + e * 512, finite2(x[e].x) & keep, finite2(x[e].y) & keep, finite2(x[e].z) & keep,
+                                   finite2(x[e].w) & keep);
                         }
-                        if (change) *w = x;
                     }
                 }
                 if (bad) poison[q.k % kPoison] = q.k + 1;
@@ -634,6 +647,34 @@ __device__ __forceinline__ uint32_t seen_bits(int hi, int lo, int sinks) {
     return low_bits(hi) & (~low_bits(lo) | low_bits(sinks));
 }
 
+// Each lane has 64 bytes (w) for an address of its own (16-byte aligned).  Four neighbouring lanes
+// exchange 16-byte pieces first, so that one store instruction writes eight whole 64-byte runs and
+// not 32 pieces of 16 bytes in 32 lines.  `on`: whether the lane's bytes are wanted.
+__device__ __forceinline__ void store_quads(void* dst, uint32_t (&w)[16], bool on) {
+    const int c = threadIdx.x & 3;
+    // 4 x 4 transposition of pieces among the four lanes: piece j of lane i to piece i of lane j
+#pragma unroll
+    for (int step = 1; step < 4; step *= 2)
+#pragma unroll
+        for (int a = 0; a < 4; ++a)
+            if (!(a & step)) {
+                const bool up = (c & step) != 0;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const uint32_t give = up ? w[4 * a + e] : w[4 * (a | step) + e];
+                    const uint32_t got = __shfl_xor_sync(0xffffffffu, give, step);
+                    if (up) w[4 * a + e] = got;
+                    else w[4 * (a | step) + e] = got;
+                }
+            }
+    const unsigned long long mine = on ? reinterpret_cast<unsigned long long>(dst) : 0ull;
+#pragma unroll
+    for (int a = 0; a < 4; ++a) {  // now piece a is this lane's quarter of lane a's bytes
+        const unsigned long long at = __shfl_sync(0xffffffffu, mine, (threadIdx.x & 28) + a);
+        if (at) *(reinterpret_cast<uint4*>(at) + c) = make_uint4(w[4 * a], w[4 * a + 1], w[4 * a + 2], w[4 * a + 3]);
+    }
+}
+
 // Values that are no numbers, of the keys a row sees in the part's tiles that were looked over:
 // columns [cc, cc + 32) of the row's sum.  (Those of other tiles went into the product.)
 template <bool E4M3, int D>
@@ -799,8 +840,7 @@ __device__ void softmax_role(const PagedAttnParams& p, int x, Bars& b, uint32_t 
                 tc_fence_before();
                 mbar_arrive(&b.o_free[x]);
             }
-            if (!live) continue;
-            if (sick) {  // (copies, so that only this rare call keeps anything in memory)
+            if (sick && live) {  // (copies, so that only this rare call keeps anything in memory)
                 const Chunk c = q.c;
                 float o2[32];
 #pragma unroll
@@ -809,12 +849,27 @@ __device__ void softmax_role(const PagedAttnParams& p, int x, Bars& b, uint32_t 
 #pragma unroll
                 for (int i = 0; i < 32; ++i) o[i] = o2[i];
             }
-            if (cut) {
-                float4* dst = reinterpret_cast<float4*>(part->o + r2 * kPagedMaxD + cc);
+            if (cut && live) {
+                float4* dst = part->o + (cc / 4) * (2 * kTile) + r2;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-            } else {
-                paged_store_cols<32>(p, tok, head, cc, o, inv);
+                for (int i = 0; i < 8; ++i) dst[i * (2 * kTile)] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+            }
+            if (!cut) {
+                if (p.out_f32) {
+                    float* dst = static_cast<float*>(p.out) + tok * p.o_ts + head * p.o_hs + cc;
+#pragma unroll
+                    for (int h2 = 0; h2 < 2; ++h2) {
+                        uint32_t w[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(o[16 * h2 + i] * inv);
+                        store_quads(dst + 16 * h2, w, live);
+                    }
+                } else {
+                    uint32_t w[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) w[i] = pack_bf16x2(o[2 * i] * inv, o[2 * i + 1] * inv);
+                    store_quads(static_cast<uint16_t*>(p.out) + tok * p.o_ts + head * p.o_hs + cc, w, live);
+                }
             }
         }
         if (cut) {
@@ -893,7 +948,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
         } else if constexpr (E4M3) {
             if (warp >= kExpandWarp) expand_role<D>(p, smem_u32(smem), b, sh.poison, wc);
         } else {
-            fix_role<D>(p, smem, b, sh.poison, wc);
+            fix_role<D>(p, smem_u32(smem), b, sh.poison, wc);
         }
     }
     __syncwarp();
@@ -903,11 +958,11 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
     if (warp == kMmaWarp) tmem_dealloc(tmem, C::kTmemCols);
 }
 
-// Joins the parts of items that were cut: a warp takes one row of an item that begins in block x of
-// the first kernel and goes on in the next ones.
+// Joins the parts of items that were cut: block (x, y) takes rows [8 y, 8 y + 8) of the item that
+// begins in block x of the first kernel and goes on in the next ones, a thread 4 columns of a row.
 constexpr int kJoinRows = 8;
 template <int D>
-__global__ void __launch_bounds__(kJoinRows * 32) paged_chunk_join_kernel(const __grid_constant__ PagedAttnParams p, int shares) {
+__global__ void __launch_bounds__(kJoinRows * D / 4) paged_chunk_join_kernel(const __grid_constant__ PagedAttnParams p, int shares) {
     wait_primary();
     const PagedChunkPartial* parts = static_cast<const PagedChunkPartial*>(p.workspace);
     const int x = blockIdx.x, lane = threadIdx.x & 31;
@@ -915,9 +970,6 @@ __global__ void __launch_bounds__(kJoinRows * 32) paged_chunk_join_kernel(const 
     const int b = p0->b, pair = p0->pair, h = p0->h;
     if (b < 0 || !p0->begins) return;
     const Chunk c = make_chunk(p, b, pair, paged_seq(p.kv, b));
-    const int r = blockIdx.y * kJoinRows + threadIdx.x / 32;  // row of the two units
-    const int unit = r / kTile, ru = r - unit * kTile, t = c.ta + unit * p.unit_tokens + ru / p.g;
-    if (ru >= p.unit_tokens * p.g || t >= c.tb) return;
     int n = 1;  // parts: p0, then the first ones of the blocks up to x + n - 1
     while (x + n < shares) {
         const int y = x + n + lane;
@@ -927,28 +979,29 @@ __global__ void __launch_bounds__(kJoinRows * 32) paged_chunk_join_kernel(const 
         n += v == 0xffffffffu ? 32 : __ffs(~v) - 1;
         if (v != 0xffffffffu) break;
     }
+    const int r = blockIdx.y * kJoinRows + threadIdx.x % kJoinRows;  // row of the two units
+    const int col = threadIdx.x / kJoinRows;                         // group of 4 columns
+    const int unit = r / kTile, ru = r - unit * kTile, t = c.ta + unit * p.unit_tokens + ru / p.g;
+    if (ru >= p.unit_tokens * p.g || t >= c.tb) return;
     float M = -INFINITY;
-    for (int k = lane; k < n; k += 32) M = fmaxf(M, (k ? parts + 2 * (x + k) : p0)->m[r]);
-#pragma unroll
-    for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+#pragma unroll 4
+    for (int k = 0; k < n; ++k) M = fmaxf(M, (k ? parts + 2 * (x + k) : p0)->m[r]);
     float l = 0.f, lr = 0.f, acc[4] = {};
 #pragma unroll 4
     for (int k = 0; k < n; ++k) {
         const PagedChunkPartial* q = k ? parts + 2 * (x + k) : p0;
         const float f = paged_weight(q->m[r], M);
+        const float4 v = q->o[col * (2 * kTile) + r];
         l = paged_add_weighted(l, f, q->l[r]);
         lr = paged_add_weighted(lr, f, q->lr[r]);
-        if (4 * lane < D) {
-            const float4 v = *reinterpret_cast<const float4*>(&q->o[r * kPagedMaxD + 4 * lane]);
-            acc[0] = paged_add_weighted(acc[0], f, v.x);
-            acc[1] = paged_add_weighted(acc[1], f, v.y);
-            acc[2] = paged_add_weighted(acc[2], f, v.z);
-            acc[3] = paged_add_weighted(acc[3], f, v.w);
-        }
+        acc[0] = paged_add_weighted(acc[0], f, v.x);
+        acc[1] = paged_add_weighted(acc[1], f, v.y);
+        acc[2] = paged_add_weighted(acc[2], f, v.z);
+        acc[3] = paged_add_weighted(acc[3], f, v.w);
     }
     const int tok = c.s.q0 + t, head = h * p.g + ru % p.g;
-    if (4 * lane < D) paged_store4(p, tok, head, 4 * lane, acc, lr == 0.f ? 0.f : 1.f / lr);
-    if (lane == 0) p.lse[tok * p.l_ts + head * p.l_hs] = l == 0.f ? -INFINITY : (M + log2f(l)) * kLn2;
+    paged_store4(p, tok, head, 4 * col, acc, lr == 0.f ? 0.f : 1.f / lr);
+    if (col == 0) p.lse[tok * p.l_ts + head * p.l_hs] = l == 0.f ? -INFINITY : (M + log2f(l)) * kLn2;
 }
 
 template <class... Args>
@@ -982,7 +1035,8 @@ int launch_t(const PagedAttnParams& p, const PagedMaps& m, int shares, cudaStrea
     paged_plan_kernel<<<1, kPlanThreads, 0, stream>>>(p);
     if (cudaGetLastError() != cudaSuccess) return -4;
     if (launch_dependent(kern, dim3(shares), C::kThreads, C::kSmemBytes, stream, p, m.q, m.k, m.v) != cudaSuccess) return -4;
-    return launch_dependent(paged_chunk_join_kernel<D>, dim3(shares, 2 * kTile / kJoinRows), kJoinRows * 32, 0, stream, p, shares) ==
+    return launch_dependent(paged_chunk_join_kernel<D>, dim3(shares, 2 * kTile / kJoinRows), kJoinRows * D / 4, 0, stream, p,
+                            shares) ==
                    cudaSuccess
                ? 0
                : -4;
