@@ -847,8 +847,7 @@ int ringattn_cache_append(const void* k_new, const void* v_new, long long k_toke
     p.k_hs = k_head_stride;
     p.v_ts = v_token_stride;
     p.v_hs = v_head_stride;
-    p.by_heads = ra::make_fastdiv(static_cast<unsigned>(p.kv.hkv));
-    return ra::launch_cache_append(p, reinterpret_cast<cudaStream_t>(stream));
+    return ra::launch_cache_append(p, dev->sms, reinterpret_cast<cudaStream_t>(stream));
 }
 
 int ringattn_cache_read(const ra_paged_kv* kv, void* k_out, void* v_out, ra_stream_t stream) {
@@ -862,8 +861,7 @@ int ringattn_cache_read(const ra_paged_kv* kv, void* k_out, void* v_out, ra_stre
     if ((st = device_info(&dev)) != RA_OK) return st;
     p.k_out = k_out;
     p.v_out = v_out;
-    p.by_heads = ra::make_fastdiv(static_cast<unsigned>(p.kv.total));
-    return ra::launch_cache_read(p, reinterpret_cast<cudaStream_t>(stream));
+    return ra::launch_cache_read(p, dev->sms, reinterpret_cast<cudaStream_t>(stream));
 }
 
 int ringattn_paged_workspace_bytes(int total, int batch, int Hq, int Hkv, int d, int max_q, long long* bytes) {

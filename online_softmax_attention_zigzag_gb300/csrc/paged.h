@@ -68,7 +68,8 @@ struct PagedCopyParams {  // append: token-major rows in; read: [Hkv, total, d] 
     long long k_ts, k_hs, v_ts, v_hs;  // token and head strides of k_in, v_in
     void* k_out;
     void* v_out;
-    FastDiv by_heads;  // append: Hkv; read: total
+    int tokens;  // of a block (set by the launcher, with the two divisions)
+    FastDiv by_heads, by_tokens;
 };
 
 struct PagedAttnParams {
@@ -92,8 +93,8 @@ struct PagedMaps {  // of the pool; ks and vs (few rows) only for e4m3; q for ch
     CUtensorMap k, v, ks, vs, q;
 };
 
-int launch_cache_append(const PagedCopyParams& p, cudaStream_t stream);
-int launch_cache_read(const PagedCopyParams& p, cudaStream_t stream);
+int launch_cache_append(const PagedCopyParams& p, int sms, cudaStream_t stream);
+int launch_cache_read(const PagedCopyParams& p, int sms, cudaStream_t stream);
 // max_q * g <= kPagedFewRows; `shares` blocks (at most kPagedMaxShares), the workspace 2 * shares
 // PagedPartial
 int launch_paged_decode(const PagedAttnParams& p, const PagedMaps& m, int shares, cudaStream_t stream);
