@@ -13,9 +13,9 @@
 //   * one warp streams K and V tiles through a ring of shared-memory slots with TMA, box by box
 //     as the pages come (a box is gcd(page, 128) rows of one page), and runs on into the next
 //     pair while the others finish the last.
-//   * eight warps compute, 16 keys of every tile each, with mma.sync (16 rows are an eighth
-//     of a tcgen05 tile, and S and P stay in registers between the two products).  Each keeps its own
-//     running max, sum and output; they meet once a pair.
+//   * eight warps compute, 16 keys of every tile each (e4m3: twelve, 32 of every third tile), with mma.sync
+//     (16 rows are an eighth of a tcgen05 tile, and S and P stay in registers between the two
+//     products).  Each keeps its own running max, sum and output; they meet once a pair.
 // bf16 cache: P goes into its product as two bf16 halves (p = hi + lo, 16 significant bits): the
 // second product costs nothing here, the loads take longer.
 // e4m3 cache: codes become fp16 (one instruction for two, exact), q is brought to fp16's range by
@@ -33,8 +33,6 @@ namespace ra {
 namespace {
 
 constexpr int kTile = kPagedTile;         // keys of a tile
-constexpr int kWarps = 8;                 // computing warps
-constexpr int kThreads = (kWarps + 1) * 32;
 constexpr int kRows = 16;
 constexpr int kBar = 1;                   // named barrier of the computing warps
 constexpr float kLog2e = 1.4426950408889634f;
@@ -46,6 +44,14 @@ template <int D, bool E4M3>
 struct Cfg {
     static constexpr int kSlotBytes = kTile * D * (E4M3 ? 1 : 2);
     static constexpr int kSlots = (D == 128 && !E4M3) ? 5 : 8;
+    // In 8 bits a tile arrives in half the time, and what a warp does for it is a chain of
+    // latencies (barrier, S, max, exponentials, P V): three groups of four warps then take tiles in
+    // turn, so that each has three times as long for a tile and 32 keys of it to overlap.
+    static constexpr int kGroups = E4M3 ? 3 : 1;
+    static constexpr int kWarps = E4M3 ? 12 : 8;       // that compute
+    static constexpr int kThreads = E4M3 ? 512 : 288;  // and the loading warp (e4m3: of four, which give registers away)
+    static constexpr int kGroupWarps = kWarps / kGroups;
+    static constexpr int kKeys = kTile / kGroupWarps;  // of a tile, for a warp
     static constexpr int kPad = E4M3 ? 16 : 8;  // floats; keeps the fragments' stores off each other's banks
     static constexpr int kOStride = D + kPad;
     static constexpr int kScaleBytes = 1024;  // of a slot: boxes start 128 bytes apart at least, as TMA wants
@@ -79,6 +85,7 @@ struct Part {
 
 // Shares of the tiles, found by every block for itself: pre[b] = tiles of the sequences before b
 // (of one head).  Returns their sum.
+template <int kThreads>
 __device__ int share_tiles(const PagedAttnParams& p, int* pre, int* scratch) {
     const int B = p.kv.batch, lane = threadIdx.x & 31, warp = threadIdx.x / 32;
     int base = 0;
@@ -94,7 +101,7 @@ __device__ int share_tiles(const PagedAttnParams& p, int* pre, int* scratch) {
         if (lane == 31) scratch[warp] = x;
         __syncthreads();
         int before = base, all = 0;
-        for (int w = 0; w <= kWarps; ++w) {
+        for (int w = 0; w < kThreads / 32; ++w) {
             const int y = scratch[w];
             if (w < warp) before += y;
             all += y;
@@ -158,6 +165,12 @@ __device__ void load_role(const PagedAttnParams& p, const CUtensorMap* tk, const
     for_each_part(p, pre, w0, w1, [&](const Part& q) -> bool {
         const PagedSeq s = paged_seq(kv, q.b);
         const Tiles kt = key_tiles(p, s);
+        // q on its way to L1 for the warps that compute, who come here later
+        for (int i = lane; i < min(s.T, p.max_q) * p.g * (D / 32); i += 32) {
+            const int r = i / (D / 32), t = r / p.g;
+            const uint16_t* src = static_cast<const uint16_t*>(p.q) + (s.q0 + t) * p.q_ts + (q.h * p.g + r - t * p.g) * p.q_hs;
+            asm volatile("prefetch.global.L1 [%0];" ::"l"(src + (i % (D / 32)) * 32));
+        }
         // the page of this lane's box, asked for a tile ahead and looked at only when it is needed
         int entry = -1, row = 0;
         auto look = [&](int t) {  // no page behind the last key
@@ -219,6 +232,16 @@ __device__ __forceinline__ float out_factor(float M, float Ms, float L) {
     return (E4M3 && M != -INFINITY) ? ex2(M - kF16Up - Ms) / L : 1.f / L;
 }
 
+// Largest of this lane's scores of its row r8 + 8 x.
+template <int NB>
+__device__ __forceinline__ float lane_max(const float (&sc)[NB][2][4], int x) {
+    float m = -INFINITY;
+#pragma unroll
+    for (int n = 0; n < NB; ++n)
+        m = fmaxf(m, fmaxf(fmaxf(sc[n][0][2 * x], sc[n][0][2 * x + 1]), fmaxf(sc[n][1][2 * x], sc[n][1][2 * x + 1])));
+    return m;
+}
+
 __device__ __forceinline__ float bf16_add_nonfinite(float acc, uint16_t bits) {
     return (bits & 0x7f80u) == 0x7f80u ? acc + __uint_as_float(static_cast<uint32_t>(bits) << 16) : acc;
 }
@@ -227,6 +250,7 @@ template <int D, bool E4M3>
 __device__ void compute_role(const PagedAttnParams& p, uint8_t* smem, uint64_t* full, uint64_t* empty, const int* pre,
                              long long w0, long long w1, const WaitCtl& wc) {
     using C = Cfg<D, E4M3>;
+    constexpr int kWarps = C::kWarps;
     const PagedKV& kv = p.kv;
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31, c4 = lane & 3, r8 = lane >> 2;
     const uint32_t ring = smem_u32(smem);
@@ -234,10 +258,13 @@ __device__ void compute_role(const PagedAttnParams& p, uint8_t* smem, uint64_t* 
     float* sm = reinterpret_cast<float*>(smem + C::kMlOff);
     float* sms = sm + kWarps * kRows;
     float* sl = sms + kWarps * kRows;
-    // this warp's scales in a slot (boxes of 16 rows lie 128 bytes apart)
-    const float* scales = reinterpret_cast<const float*>(smem + C::kScaleOff) + (p.box_rows == 16 ? 32 : 16) * warp + 2 * c4;
+    const int grp = warp / C::kGroupWarps, key0 = (warp % C::kGroupWarps) * C::kKeys;  // this warp's keys of a tile
+    constexpr int NB = C::kKeys / 16;
+    // its scales in a slot: 16 keys lie 16 floats apart (boxes of 16 rows 32, 128 bytes)
+    const int step16 = p.box_rows == 16 ? 32 : 16;
+    const float* scales = reinterpret_cast<const float*>(smem + C::kScaleOff) + step16 * (key0 / 16) + 2 * c4;
     PagedPartial* parts = static_cast<PagedPartial*>(p.workspace);
-    uint32_t it = 0;
+    uint32_t tiles = 0;  // of the parts before
     bool ok = true;
     int first = 1;
     for_each_part(p, pre, w0, w1, [&](const Part& q) -> bool {
@@ -293,8 +320,9 @@ __device__ void compute_role(const PagedAttnParams& p, uint8_t* smem, uint64_t* 
         float m[2] = {-INFINITY, -INFINITY}, ms[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
         bool bad_v = false;  // a value that is no number, in a tile that not every row sees whole
         const int see_lo = s.base + T - p.window;  // the window of the last row begins here
-        for (int t = q.ta; t < q.tb; ++t) {
+        for (int t = q.ta + (grp + C::kGroups - tiles % C::kGroups) % C::kGroups; t < q.tb; t += C::kGroups) {
             const int j0 = (t < kt.ns ? t : kt.lo + t - kt.ns) * kTile;
+            uint32_t it = 2 * (tiles + t - q.ta);  // the ring's number of this K tile; V is the next
             // does every row see every key of the tile?
             const bool whole = j0 + kTile <= (p.causal ? s.base + 1 : s.L) &&
                                (p.window == 0 || j0 >= see_lo || j0 + kTile <= p.sinks);
@@ -302,113 +330,117 @@ __device__ void compute_role(const PagedAttnParams& p, uint8_t* smem, uint64_t* 
             uint32_t slot = it % C::kSlots;
             ok = __all_sync(0xffffffffu, mbar_wait(&full[slot], (it / C::kSlots) & 1u, wc));
             if (!ok) break;
-            float sc[2][4] = {};
+            float sc[NB][2][4] = {};
             uint32_t base = ring + slot * C::kSlotBytes;
             if constexpr (E4M3) {
                 // matrices: keys 0-7 and 8-15 of chunk 2 x, then of chunk 2 x + 1
-                const int kr = warp * 16 + (lane & 15);
 #pragma unroll
-                for (int x = 0; x < D / 32; ++x) {
-                    uint32_t b[4];
-                    ldmatrix4(b, base + chunk_at<D, E4M3>(kr, 2 * x + (lane >> 4)));
+                for (int x = 0; x < D / 32; ++x)
 #pragma unroll
-                    for (int y = 0; y < 2; ++y)
+                    for (int n = 0; n < NB; ++n) {
+                        uint32_t b[4];
+                        ldmatrix4(b, base + chunk_at<D, E4M3>(key0 + 16 * n + (lane & 15), 2 * x + (lane >> 4)));
 #pragma unroll
-                        for (int nt = 0; nt < 2; ++nt)
-                            mma16816<true>(sc[nt], qa[2 * x + y], e4m3x2_f16x2(b[2 * y + nt] & 0xffffu), e4m3x2_f16x2(b[2 * y + nt] >> 16));
-                }
+                        for (int y = 0; y < 2; ++y)
+#pragma unroll
+                            for (int nt = 0; nt < 2; ++nt)
+                                mma16816<true>(sc[n][nt], qa[2 * x + y], e4m3x2_f16x2(b[2 * y + nt] & 0xffffu),
+                                               e4m3x2_f16x2(b[2 * y + nt] >> 16));
+                    }
+                const float* f = scales + slot * (C::kScaleBytes / 4);
+#pragma unroll
+                for (int n = 0; n < NB; ++n)
+#pragma unroll
+                    for (int nt = 0; nt < 2; ++nt) {
+                        const float2 k1 = *reinterpret_cast<const float2*>(f + step16 * n + 8 * nt);
+                        sc[n][nt][0] *= k1.x * cs[0];
+                        sc[n][nt][1] *= k1.y * cs[0];
+                        sc[n][nt][2] *= k1.x * cs[1];
+                        sc[n][nt][3] *= k1.y * cs[1];
+                    }
             } else {
                 // matrices: keys 0-7 of chunks 2 k and 2 k + 1, then keys 8-15
-                const int kr = warp * 16 + (lane & 7) + ((lane >> 4) << 3);
 #pragma unroll
-                for (int k = 0; k < D / 16; ++k) {
-                    uint32_t b[4];
-                    ldmatrix4(b, base + chunk_at<D, E4M3>(kr, 2 * k + ((lane >> 3) & 1)));
-                    mma16816<false>(sc[0], qa[k], b[0], b[1]);
-                    mma16816<false>(sc[1], qa[k], b[2], b[3]);
-                }
-            }
-            float2 ks[2], vs[2];
-            const int kc = warp * 16 + 2 * c4;  // keys kc, kc + 1, kc + 8, kc + 9 of the tile
-            if constexpr (E4M3) {
-                const float* f = scales + slot * (C::kScaleBytes / 4);
-                ks[0] = *reinterpret_cast<const float2*>(f);
-                ks[1] = *reinterpret_cast<const float2*>(f + 8);
-            }
-            if constexpr (E4M3) {
+                for (int k = 0; k < D / 16; ++k)
 #pragma unroll
-                for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const float k1 = e ? ks[nt].y : ks[nt].x;
-                        sc[nt][e] *= k1 * cs[0];
-                        sc[nt][2 + e] *= k1 * cs[1];
+                    for (int n = 0; n < NB; ++n) {
+                        uint32_t b[4];
+                        ldmatrix4(b, base + chunk_at<D, E4M3>(key0 + 16 * n + (lane & 7) + ((lane >> 4) << 3), 2 * k + ((lane >> 3) & 1)));
+                        mma16816<false>(sc[n][0], qa[k], b[0], b[1]);
+                        mma16816<false>(sc[n][1], qa[k], b[2], b[3]);
                     }
+#pragma unroll
+                for (int n = 0; n < NB; ++n)
+#pragma unroll
+                    for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) sc[n][nt][e] *= kLog2e;
             }
             // (a slot is handed back when what was loaded from it has been used)
             __syncwarp();
             if (lane == 0) mbar_arrive(&empty[slot]);
             ++it;
             slot = it % C::kSlots;
-            ok = __all_sync(0xffffffffu, mbar_wait(&full[slot], (it / C::kSlots) & 1u, wc));
-            if (!ok) break;
             base = ring + slot * C::kSlotBytes;
-            if constexpr (E4M3) {
-                const float* f = scales + slot * (C::kScaleBytes / 4);
-                vs[0] = *reinterpret_cast<const float2*>(f);
-                vs[1] = *reinterpret_cast<const float2*>(f + 8);
-            }
-            // ---- scores in log2 units, masked
-            float va[4], vm[4];  // e4m3: V scale = 2^va * vm with vm in [1, 2)
-#pragma unroll
-            for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    if constexpr (E4M3) {
-                        const uint32_t vb = __float_as_uint(e ? vs[nt].y : vs[nt].x);
-                        // a scale that is no number makes the row no number; exponent 0 is a scale of 0 (a row
-                        // of zeros, from a page that is none)
-                        const int a = static_cast<int>((vb >> 23) & 0xffu);
-                        va[2 * nt + e] = a == 255 ? __uint_as_float(0x7fc00000u) : static_cast<float>(a - 127);
-                        vm[2 * nt + e] = __uint_as_float((vb & 0x7fffffu) | 0x3f800000u);
-                    } else {
-                        sc[nt][e] *= kLog2e;
-                        sc[nt][2 + e] *= kLog2e;
-                    }
-                }
+            const int jc = j0 + key0 + 2 * c4;  // this thread's keys: jc + 16 n + 8 nt and the one behind
             if (!whole) {
 #pragma unroll
-                for (int nt = 0; nt < 2; ++nt)
+                for (int n = 0; n < NB; ++n)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int j = j0 + kc + 8 * nt + (e & 1), x = e >> 1;
-                        const bool see = j < hi[x] && (p.window == 0 || j >= lo[x] || j < p.sinks);
-                        if (!see) sc[nt][e] = -INFINITY;
-                    }
+                    for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int j = jc + 16 * n + 8 * nt + (e & 1), x = e >> 1;
+                            const bool see = j < hi[x] && (p.window == 0 || j >= lo[x] || j < p.sinks);
+                            if (!see) sc[n][nt][e] = -INFINITY;
+                        }
             }
-            // ---- e4m3: l with a max of each lane's own, then the V scales join the scores
+            // ---- e4m3: l, with a running max of each lane's own
             if constexpr (E4M3) {
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
                     if (x == 1 && !two) break;
-                    const float mx = fmaxf(fmaxf(sc[0][2 * x], sc[0][2 * x + 1]), fmaxf(sc[1][2 * x], sc[1][2 * x + 1]));
+                    const float mx = lane_max(sc, x);
                     if (mx > ms[x] + kRescale || (ms[x] == -INFINITY && mx > ms[x])) {
                         l[x] *= ex2(ms[x] - mx);
                         ms[x] = mx;
                     }
                     const float nm = ms[x] == -INFINITY ? 0.f : -ms[x];
-                    l[x] += (ex2(sc[0][2 * x] + nm) + ex2(sc[0][2 * x + 1] + nm)) + (ex2(sc[1][2 * x] + nm) + ex2(sc[1][2 * x + 1] + nm));
+                    float sum = 0.f;
 #pragma unroll
-                    for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e)  // (a masked score stays -inf whatever the scale)
-                            if (sc[nt][2 * x + e] != -INFINITY) sc[nt][2 * x + e] += va[2 * nt + e];
+                    for (int n = 0; n < NB; ++n)
+                        sum += (ex2(sc[n][0][2 * x] + nm) + ex2(sc[n][0][2 * x + 1] + nm)) +
+                               (ex2(sc[n][1][2 * x] + nm) + ex2(sc[n][1][2 * x + 1] + nm));
+                    l[x] += sum;
                 }
             }
-            // ---- running max of the row (shared by the four lanes that hold it), p, sums
-            float mx[2];
+            ok = __all_sync(0xffffffffu, mbar_wait(&full[slot], (it / C::kSlots) & 1u, wc));
+            if (!ok) break;
+            // ---- e4m3: the V scales 2^a vm, vm in [1, 2), join the scores
+            float vm[NB][4];
+            if constexpr (E4M3) {
+                const float* f = scales + slot * (C::kScaleBytes / 4);
 #pragma unroll
-            for (int x = 0; x < 2; ++x) mx[x] = fmaxf(fmaxf(sc[0][2 * x], sc[0][2 * x + 1]), fmaxf(sc[1][2 * x], sc[1][2 * x + 1]));
+                for (int n = 0; n < NB; ++n)
+#pragma unroll
+                    for (int nt = 0; nt < 2; ++nt) {
+                        const float2 v1 = *reinterpret_cast<const float2*>(f + step16 * n + 8 * nt);
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const uint32_t vb = __float_as_uint(e ? v1.y : v1.x);
+                            // a scale that is no number makes the row no number; exponent 0 is a scale of 0
+                            // (a row of zeros, from a page that is none)
+                            const int a = static_cast<int>((vb >> 23) & 0xffu);
+                            const float va = a == 255 ? __uint_as_float(0x7fc00000u) : static_cast<float>(a - 127);
+                            vm[n][2 * nt + e] = __uint_as_float((vb & 0x7fffffu) | 0x3f800000u);
+#pragma unroll
+                            for (int x = 0; x < 2; ++x)  // (a masked score stays -inf whatever the scale)
+                                if (sc[n][nt][2 * x + e] != -INFINITY) sc[n][nt][2 * x + e] += va;
+                        }
+                    }
+            }
+            // ---- running max of the row (shared by the four lanes that hold it), p, sums
+            float mx[2] = {lane_max(sc, 0), lane_max(sc, 1)};
             mx[0] = fmaxf(mx[0], __shfl_xor_sync(0xffffffffu, mx[0], 1));
             mx[0] = fmaxf(mx[0], __shfl_xor_sync(0xffffffffu, mx[0], 2));
             if (two) {
@@ -435,71 +467,77 @@ __device__ void compute_role(const PagedAttnParams& p, uint8_t* smem, uint64_t* 
             }
             const float up = E4M3 ? kF16Up : 0.f;
             const float nm[2] = {up - (m[0] == -INFINITY ? 0.f : m[0]), up - (m[1] == -INFINITY ? 0.f : m[1])};
-            uint32_t pa[4], pb[4];
+            uint32_t pa[NB][4], pb[NB][4];
 #pragma unroll
-            for (int nt = 0; nt < 2; ++nt)
+            for (int n = 0; n < NB; ++n)
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    pa[2 * nt + x] = pb[2 * nt + x] = 0u;
-                    if (x == 1 && !two) break;
-                    const float a = ex2(sc[nt][2 * x] + nm[x]), b = ex2(sc[nt][2 * x + 1] + nm[x]);
-                    if constexpr (E4M3) {
-                        pa[2 * nt + x] = pack_f16x2(a * vm[2 * nt], b * vm[2 * nt + 1]);
-                    } else {
-                        l[x] += a + b;
-                        const uint32_t h = pack_bf16x2(a, b);
-                        pa[2 * nt + x] = h;
-                        pb[2 * nt + x] = pack_bf16x2(a - __uint_as_float(h << 16), b - __uint_as_float(h & 0xffff0000u));
-                    }
-                }
-            // ---- O += P V; values of keys that no row sees count as zero, whatever they hold
-            uint32_t keep[2] = {0xffffffffu, 0xffffffffu};  // of the key pairs kc, kc + 1 and kc + 8, kc + 9
-            if (!whole) {
+                for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const int j = j0 + kc + 8 * x;
-                    const int wlo = p.window > 0 ? s.base - p.window + 1 : 0;
-                    const bool a = j < s.L && (j >= wlo || j < p.sinks);
-                    const bool b = j + 1 < s.L && (j + 1 >= wlo || j + 1 < p.sinks);
-                    keep[x] = (a ? 0xffffu : 0u) | (b ? 0xffff0000u : 0u);
-                }
-            }
-            const int vr = warp * 16 + (lane & 15);  // matrices: keys 0-7 and 8-15 of a chunk, then of the next
-#pragma unroll
-            for (int x = 0; x < (E4M3 ? D / 32 : D / 16); ++x) {
-                uint32_t b[4];
-                ldmatrix4_t(b, base + chunk_at<D, E4M3>(vr, 2 * x + (lane >> 4)));
-                if (!whole) {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) b[e] &= keep[e & 1];
-                    if (!E4M3 && T > 1) {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const uint32_t b0 = (b[e] & 0x7f80u) == 0x7f80u ? 0xffffu : 0u;
-                            const uint32_t b1 = (b[e] & 0x7f800000u) == 0x7f800000u ? 0xffff0000u : 0u;
-                            if (b0 | b1) bad_v = true;
-                            b[e] &= ~(b0 | b1);
+                    for (int x = 0; x < 2; ++x) {
+                        pa[n][2 * nt + x] = pb[n][2 * nt + x] = 0u;
+                        if (x == 1 && !two) break;
+                        const float a = ex2(sc[n][nt][2 * x] + nm[x]), b = ex2(sc[n][nt][2 * x + 1] + nm[x]);
+                        if constexpr (E4M3) {
+                            pa[n][2 * nt + x] = pack_f16x2(a * vm[n][2 * nt], b * vm[n][2 * nt + 1]);
+                        } else {
+                            l[x] += a + b;
+                            const uint32_t h = pack_bf16x2(a, b);
+                            pa[n][2 * nt + x] = h;
+                            pb[n][2 * nt + x] = pack_bf16x2(a - __uint_as_float(h << 16), b - __uint_as_float(h & 0xffff0000u));
                         }
                     }
-                }
-                if constexpr (E4M3) {
+            // ---- O += P V; values of keys that no row sees count as zero, whatever they hold
+            uint32_t keep[NB][2];  // of the key pairs jc + 16 n and jc + 16 n + 8
 #pragma unroll
-                    for (int y = 0; y < 2; ++y) {  // chunk 2 x + y: columns of even and of odd elements
-                        const uint32_t ev = __byte_perm(b[2 * y], b[2 * y + 1], 0x6420), od = __byte_perm(b[2 * y], b[2 * y + 1], 0x7531);
-                        mma16816<true>(o[4 * x + 2 * y], pa, e4m3x2_f16x2(ev & 0xffffu), e4m3x2_f16x2(ev >> 16));
-                        mma16816<true>(o[4 * x + 2 * y + 1], pa, e4m3x2_f16x2(od & 0xffffu), e4m3x2_f16x2(od >> 16));
+            for (int n = 0; n < NB; ++n)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    keep[n][x] = 0xffffffffu;
+                    if (!whole) {
+                        const int j = jc + 16 * n + 8 * x;
+                        const int wlo = p.window > 0 ? s.base - p.window + 1 : 0;
+                        const bool a = j < s.L && (j >= wlo || j < p.sinks);
+                        const bool b = j + 1 < s.L && (j + 1 >= wlo || j + 1 < p.sinks);
+                        keep[n][x] = (a ? 0xffffu : 0u) | (b ? 0xffff0000u : 0u);
                     }
-                } else {
-                    mma16816<false>(o[2 * x], pa, b[0], b[1]);
-                    mma16816<false>(o[2 * x + 1], pa, b[2], b[3]);
-                    mma16816<false>(o[2 * x], pb, b[0], b[1]);
-                    mma16816<false>(o[2 * x + 1], pb, b[2], b[3]);
                 }
-            }
+#pragma unroll
+            for (int x = 0; x < (E4M3 ? D / 32 : D / 16); ++x)
+#pragma unroll
+                for (int n = 0; n < NB; ++n) {
+                    uint32_t b[4];  // matrices: keys 0-7 and 8-15 of a chunk, then of the next
+                    ldmatrix4_t(b, base + chunk_at<D, E4M3>(key0 + 16 * n + (lane & 15), 2 * x + (lane >> 4)));
+                    if (!whole) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) b[e] &= keep[n][e & 1];
+                        if (!E4M3 && T > 1) {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const uint32_t b0 = (b[e] & 0x7f80u) == 0x7f80u ? 0xffffu : 0u;
+                                const uint32_t b1 = (b[e] & 0x7f800000u) == 0x7f800000u ? 0xffff0000u : 0u;
+                                if (b0 | b1) bad_v = true;
+                                b[e] &= ~(b0 | b1);
+                            }
+                        }
+                    }
+                    if constexpr (E4M3) {
+#pragma unroll
+                        for (int y = 0; y < 2; ++y) {  // chunk 2 x + y: columns of even and of odd elements
+                            const uint32_t ev = __byte_perm(b[2 * y], b[2 * y + 1], 0x6420), od = __byte_perm(b[2 * y], b[2 * y + 1], 0x7531);
+                            mma16816<true>(o[4 * x + 2 * y], pa[n], e4m3x2_f16x2(ev & 0xffffu), e4m3x2_f16x2(ev >> 16));
+                            mma16816<true>(o[4 * x + 2 * y + 1], pa[n], e4m3x2_f16x2(od & 0xffffu), e4m3x2_f16x2(od >> 16));
+                        }
+                    } else {
+                        mma16816<false>(o[2 * x], pa[n], b[0], b[1]);
+                        mma16816<false>(o[2 * x + 1], pa[n], b[2], b[3]);
+                        mma16816<false>(o[2 * x], pb[n], b[0], b[1]);
+                        mma16816<false>(o[2 * x + 1], pb[n], b[2], b[3]);
+                    }
+                }
             __syncwarp();
             if (lane == 0) mbar_arrive(&empty[slot]);
-            ++it;
         }
+        tiles += q.tb - q.ta;
         // ---- the warps' results meet: rows 0-7, then rows 8-15
         const bool cut = q.ta > 0 || q.tb < q.n;
         const int slot_i = 2 * blockIdx.x + (first ? 0 : 1);
@@ -539,8 +577,8 @@ __device__ void compute_role(const PagedAttnParams& p, uint8_t* smem, uint64_t* 
             ok = named_bar_and(kBar, kWarps * 32, ok);
             const bool any_bad = !named_bar_and(kBar, kWarps * 32, !bad_v);
             if (!ok) return false;
-            const int tid = threadIdx.x, row8 = tid / 32, r = row8 + 8 * x;
-            if (r < R) {
+            const int row8 = warp, r = row8 + 8 * x;
+            if (row8 < 8 && r < R) {
                 float M = -INFINITY, Ms = -INFINITY;
 #pragma unroll
                 for (int w = 0; w < kWarps; ++w) {
@@ -612,7 +650,7 @@ __device__ void compute_role(const PagedAttnParams& p, uint8_t* smem, uint64_t* 
 }
 
 template <int D, bool E4M3>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
     paged_decode_kernel(const __grid_constant__ PagedAttnParams p, const __grid_constant__ CUtensorMap tk,
                         const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tks,
                         const __grid_constant__ CUtensorMap tvs) {
@@ -621,19 +659,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     __shared__ __align__(8) uint64_t full[C::kSlots];
     __shared__ __align__(8) uint64_t empty[C::kSlots];
-    __shared__ int scratch[kWarps + 1];
+    __shared__ int scratch[C::kThreads / 32];
     __shared__ int abort_flag;
     int* pre = reinterpret_cast<int*>(smem + C::kPreOff);
     launch_dependents();
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::kSlots; ++s) {
             mbar_init(&full[s], 1);
-            mbar_init(&empty[s], kWarps);
+            mbar_init(&empty[s], C::kGroupWarps);
         }
         abort_flag = 0;
         fence_mbar_init();
     }
-    const long long W = static_cast<long long>(share_tiles(p, pre, scratch)) * p.kv.hkv;
+    const long long W = static_cast<long long>(share_tiles<C::kThreads>(p, pre, scratch)) * p.kv.hkv;
     // the first W % grid blocks take one tile more: blocks without any are the last ones
     const long long each = W / gridDim.x, more = W % gridDim.x, x = blockIdx.x;
     const long long w0 = x * each + min(x, more), w1 = w0 + each + (x < more ? 1 : 0);
@@ -641,10 +679,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x < 2) parts[threadIdx.x].b = -1;  // until a cut pair says otherwise
     __syncthreads();
     const WaitCtl wc{&abort_flag, p.err, p.timeout_ns};
-    if (threadIdx.x / 32 == kWarps)
-        load_role<D, E4M3>(p, &tk, &tv, &tks, &tvs, smem_u32(smem), smem_u32(smem) + C::kScaleOff, full, empty, pre, w0, w1, wc);
-    else
+    // e4m3: 512 threads start with 128 registers each; 384 * 152 + 128 * 56 is the same sum
+    if (threadIdx.x / 32 >= C::kWarps) {
+        if constexpr (E4M3) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        if (threadIdx.x / 32 == C::kWarps)
+            load_role<D, E4M3>(p, &tk, &tv, &tks, &tvs, smem_u32(smem), smem_u32(smem) + C::kScaleOff, full, empty, pre, w0, w1, wc);
+    } else {
+        if constexpr (E4M3) asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
         compute_role<D, E4M3>(p, smem, full, empty, pre, w0, w1, wc);
+    }
 }
 
 // Joins the parts of pairs that were cut.  Block (x, r): if a pair begins in block x of the first
@@ -725,11 +768,16 @@ int launch_t(const PagedAttnParams& p, const PagedMaps& m, int shares, cudaStrea
     const int bytes = C::kFixedBytes + 4 * (p.kv.batch + 1);
     static std::atomic<unsigned long long> ready{0};
     if (!once_a_device(ready, [&] {
-            return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                        C::kFixedBytes + 4 * (kPagedMaxBatch + 1)) == cudaSuccess;
+            if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     C::kFixedBytes + 4 * (kPagedMaxBatch + 1)) != cudaSuccess)
+                return false;
+            if (!E4M3) return true;
+            // the register split adds up only if the block starts with 128 a thread
+            cudaFuncAttributes a;
+            return cudaFuncGetAttributes(&a, kern) == cudaSuccess && a.numRegs == 128;
         }))
         return -4;
-    kern<<<shares, kThreads, bytes, stream>>>(p, m.k, m.v, m.ks, m.vs);
+    kern<<<shares, C::kThreads, bytes, stream>>>(p, m.k, m.v, m.ks, m.vs);
     if (cudaGetLastError() != cudaSuccess) return -4;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(shares, p.max_q * p.g);
