@@ -13,9 +13,16 @@
 //   * one warp streams K and V tiles through a ring of shared-memory slots with TMA, box by box
 //     as the pages come (a box is gcd(page, 128) rows of one page), and runs on into the next
 //     pair while the others finish the last.
-//   * eight warps compute, 16 keys of every tile each (e4m3: twelve, 32 of every third tile), with mma.sync
-//     (16 rows are an eighth of a tcgen05 tile, and S and P stay in registers between the two
-//     products).  Each keeps its own running max, sum and output; they meet once a pair.
+//   * eight warps compute, 16 keys of every tile each, with mma.sync: 8 rows are a sixteenth of a
+//     tcgen05 tile, and S and P stay in registers between the two products.  Both products are
+//     transposed, S^T = K Q^T and O^T = V^T P^T, so that the keys and the elements fill the 16 rows of
+//     the instruction and the query rows its 8 columns: up to 8 rows, the usual case, then
+//     cost half the instructions and registers of S = Q K^T.  Each warp keeps its own
+//     running max, sum and output; they meet once a pair.  In 8 bits a tile arrives in half the
+//     time, and what a warp does for it is a chain of latencies (barrier, S, max, exponentials, P
+//     V): groups of warps then take tiles in turn, so that a warp has more keys of a tile to
+//     overlap and more time for it: four groups of two warps, 64 keys each, for up to 8 rows, two
+//     groups of four, 32 keys each, above.
 // bf16 cache: P goes into its product as two bf16 halves (p = hi + lo, 16 significant bits): the
 // second product costs nothing here, the loads take longer.
 // e4m3 cache: codes become fp16 (one instruction for two, exact), q is brought to fp16's range by
@@ -40,20 +47,21 @@ constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kRescale = 8.0f;          // the running max moves when it is exceeded by more (log2)
 constexpr float kF16Up = 6.0f;            // p' is kept 2^6 times larger: at most 2^(8 + 6 + 1) in fp16
 
-template <int D, bool E4M3>
+// NT: 8 query rows each
+template <int D, bool E4M3, int NT>
 struct Cfg {
     static constexpr int kSlotBytes = kTile * D * (E4M3 ? 1 : 2);
     static constexpr int kSlots = (D == 128 && !E4M3) ? 5 : 8;
-    // In 8 bits a tile arrives in half the time, and what a warp does for it is a chain of
-    // latencies (barrier, S, max, exponentials, P V): three groups of four warps then take tiles in
-    // turn, so that each has three times as long for a tile and 32 keys of it to overlap.
-    static constexpr int kGroups = E4M3 ? 3 : 1;
-    static constexpr int kWarps = E4M3 ? 12 : 8;       // that compute
-    static constexpr int kThreads = E4M3 ? 512 : 288;  // and the loading warp (e4m3: of four, which give registers away)
+    static constexpr int kWarps = 8;                   // that compute
+    static constexpr int kThreads = kWarps * 32 + 32;  // and the loading warp
+    static constexpr int kGroups = E4M3 ? (NT == 1 ? 4 : 2) : 1;
     static constexpr int kGroupWarps = kWarps / kGroups;
+    // A slot's tiles must all be one group's: waits go by a barrier's parity, and a group that met a slot
+    // of another's could be two tiles ahead of it (copies need not end in order) and take the
+    // parity of the tile before last for its own.
+    static_assert(kGroups == 1 || (kSlots % 2 == 0 && (kSlots / 2) % kGroups == 0), "a slot pair a group");
     static constexpr int kKeys = kTile / kGroupWarps;  // of a tile, for a warp
-    static constexpr int kPad = E4M3 ? 16 : 8;  // floats; keeps the fragments' stores off each other's banks
-    static constexpr int kOStride = D + kPad;
+    static constexpr int kOStride = D + 4;             // keeps the fragments' stores off each other's banks
     static constexpr int kScaleBytes = 1024;  // of a slot: boxes start 128 bytes apart at least, as TMA wants
     static constexpr int kScaleOff = kSlots * kSlotBytes;
     static constexpr int kOOff = kScaleOff + (E4M3 ? kSlots * kScaleBytes : 0);
@@ -149,11 +157,11 @@ __device__ __forceinline__ void for_each_part(const PagedAttnParams& p, const in
 }
 
 // ------------------------------------------------------------------ the loading warp
-template <int D, bool E4M3>
+template <int D, bool E4M3, int NT>
 __device__ void load_role(const PagedAttnParams& p, const CUtensorMap* tk, const CUtensorMap* tv,
                           const CUtensorMap* tks, const CUtensorMap* tvs, uint32_t ring, uint32_t scales, uint64_t* full,
                           uint64_t* empty, const int* pre, long long w0, long long w1, const WaitCtl& wc) {
-    using C = Cfg<D, E4M3>;
+    using C = Cfg<D, E4M3, NT>;
     const PagedKV& kv = p.kv;
     const int lane = threadIdx.x & 31;
     const int rows = p.box_rows;          // of a box; a lane loads one
@@ -232,13 +240,12 @@ __device__ __forceinline__ float out_factor(float M, float Ms, float L) {
     return (E4M3 && M != -INFINITY) ? ex2(M - kF16Up - Ms) / L : 1.f / L;
 }
 
-// Largest of this lane's scores of its row r8 + 8 x.
-template <int NB>
-__device__ __forceinline__ float lane_max(const float (&sc)[NB][2][4], int x) {
-    float m = -INFINITY;
+// Largest of this lane's scores of its row e of row group x.
+template <int NB, int NT>
+__device__ __forceinline__ float lane_max(const float (&sc)[NB][NT][4], int x, int e) {
+    float m = fmaxf(sc[0][x][e], sc[0][x][2 + e]);
 #pragma unroll
-    for (int n = 0; n < NB; ++n)
-        m = fmaxf(m, fmaxf(fmaxf(sc[n][0][2 * x], sc[n][0][2 * x + 1]), fmaxf(sc[n][1][2 * x], sc[n][1][2 * x + 1])));
+    for (int n = 1; n < NB; ++n) m = fmaxf(m, fmaxf(sc[n][x][e], sc[n][x][2 + e]));
     return m;
 }
 
@@ -246,11 +253,11 @@ __device__ __forceinline__ float bf16_add_nonfinite(float acc, uint16_t bits) {
     return (bits & 0x7f80u) == 0x7f80u ? acc + __uint_as_float(static_cast<uint32_t>(bits) << 16) : acc;
 }
 
-template <int D, bool E4M3>
+template <int D, bool E4M3, int NT>
 __device__ void compute_role(const PagedAttnParams& p, uint8_t* smem, uint64_t* full, uint64_t* empty, const int* pre,
                              long long w0, long long w1, const WaitCtl& wc) {
-    using C = Cfg<D, E4M3>;
-    constexpr int kWarps = C::kWarps;
+    using C = Cfg<D, E4M3, NT>;
+    constexpr int kWarps = C::kWarps, NB = C::kKeys / 16;
     const PagedKV& kv = p.kv;
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31, c4 = lane & 3, r8 = lane >> 2;
     const uint32_t ring = smem_u32(smem);
@@ -259,10 +266,9 @@ __device__ void compute_role(const PagedAttnParams& p, uint8_t* smem, uint64_t* 
     float* sms = sm + kWarps * kRows;
     float* sl = sms + kWarps * kRows;
     const int grp = warp / C::kGroupWarps, key0 = (warp % C::kGroupWarps) * C::kKeys;  // this warp's keys of a tile
-    constexpr int NB = C::kKeys / 16;
     // its scales in a slot: 16 keys lie 16 floats apart (boxes of 16 rows 32, 128 bytes)
     const int step16 = p.box_rows == 16 ? 32 : 16;
-    const float* scales = reinterpret_cast<const float*>(smem + C::kScaleOff) + step16 * (key0 / 16) + 2 * c4;
+    const float* scales = reinterpret_cast<const float*>(smem + C::kScaleOff) + step16 * (key0 / 16) + r8;
     PagedPartial* parts = static_cast<PagedPartial*>(p.workspace);
     uint32_t tiles = 0;  // of the parts before
     bool ok = true;
@@ -271,17 +277,13 @@ __device__ void compute_role(const PagedAttnParams& p, uint8_t* smem, uint64_t* 
         const PagedSeq s = paged_seq(kv, q.b);
         const Tiles kt = key_tiles(p, s);
         const int T = min(s.T, p.max_q), R = T * p.g;
-        const bool two = R > 8;
-        // this thread's rows r8 and r8 + 8: their q as matrix operands, and the keys they see
-        uint32_t qa[D / 16][4];
-        float cs[2] = {kLog2e, kLog2e};
-        int hi[2], lo[2];
+        // q as the B operand: this lane has elements of row 8 x + r8
+        uint32_t qb[NT][D / 16][2];
+        float cs[NT][2];        // e4m3: log2 e times what row 8 x + 2 c4 + e was scaled down by
+        int hi[NT][2], lo[NT][2];  // the keys that row sees: below hi, from lo on or sinks
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            const int r = r8 + 8 * x, t = r / p.g;
-            const int i = s.base + t;
-            hi[x] = p.causal ? i + 1 : s.L;
-            lo[x] = p.window > 0 ? i - p.window + 1 : 0;
+        for (int x = 0; x < NT; ++x) {
+            const int r = 8 * x + r8, t = r / p.g;
             const uint16_t* src = static_cast<const uint16_t*>(p.q) + (s.q0 + t) * p.q_ts + (q.h * p.g + r - t * p.g) * p.q_hs;
             const bool live = r < R;
             if constexpr (E4M3) {
@@ -298,26 +300,43 @@ __device__ void compute_role(const PagedAttnParams& p, uint8_t* smem, uint64_t* 
                 // largest element in [2^13, 2^14): exponent field m >> 7 becomes 127 + 13
                 const int e = min(max(static_cast<int>(m >> 7), 16), 254);
                 const float up = __uint_as_float(static_cast<uint32_t>(127 + 13 + 127 - e) << 23);
-                cs[x] = kLog2e * __uint_as_float(static_cast<uint32_t>(e - 13) << 23);
+                const float down = kLog2e * __uint_as_float(static_cast<uint32_t>(e - 13) << 23);
+                cs[x][0] = __shfl_sync(0xffffffffu, down, 8 * c4);
+                cs[x][1] = __shfl_sync(0xffffffffu, down, 8 * c4 + 4);
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k) {
-                    qa[k][x] = pack_f16x2(__uint_as_float(w[k].x << 16) * up, __uint_as_float(w[k].x & 0xffff0000u) * up);
-                    qa[k][2 + x] = pack_f16x2(__uint_as_float(w[k].y << 16) * up, __uint_as_float(w[k].y & 0xffff0000u) * up);
+                    qb[x][k][0] = pack_f16x2(__uint_as_float(w[k].x << 16) * up, __uint_as_float(w[k].x & 0xffff0000u) * up);
+                    qb[x][k][1] = pack_f16x2(__uint_as_float(w[k].y << 16) * up, __uint_as_float(w[k].y & 0xffff0000u) * up);
                 }
             } else {
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k) {
-                    qa[k][x] = live ? __ldg(reinterpret_cast<const uint32_t*>(src + 16 * k + 2 * c4)) : 0u;
-                    qa[k][2 + x] = live ? __ldg(reinterpret_cast<const uint32_t*>(src + 16 * k + 8 + 2 * c4)) : 0u;
+                    qb[x][k][0] = live ? __ldg(reinterpret_cast<const uint32_t*>(src + 16 * k + 2 * c4)) : 0u;
+                    qb[x][k][1] = live ? __ldg(reinterpret_cast<const uint32_t*>(src + 16 * k + 8 + 2 * c4)) : 0u;
                 }
             }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int i = s.base + (8 * x + 2 * c4 + e) / p.g;
+                hi[x][e] = p.causal ? i + 1 : s.L;
+                lo[x][e] = p.window > 0 ? i - p.window + 1 : 0;
+            }
         }
-        float o[D / 8][4];
+        float o[D / 16][NT][4];
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i)
+        for (int i = 0; i < D / 16; ++i)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
-        float m[2] = {-INFINITY, -INFINITY}, ms[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+            for (int x = 0; x < NT; ++x)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[i][x][e] = 0.f;
+        float m[NT][2], ms[NT][2], l[NT][2];
+#pragma unroll
+        for (int x = 0; x < NT; ++x)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                m[x][e] = ms[x][e] = -INFINITY;
+                l[x][e] = 0.f;
+            }
         bool bad_v = false;  // a value that is no number, in a tile that not every row sees whole
         const int see_lo = s.base + T - p.window;  // the window of the last row begins here
         for (int t = q.ta + (grp + C::kGroups - tiles % C::kGroups) % C::kGroups; t < q.tb; t += C::kGroups) {
@@ -326,14 +345,14 @@ __device__ void compute_role(const PagedAttnParams& p, uint8_t* smem, uint64_t* 
             // does every row see every key of the tile?
             const bool whole = j0 + kTile <= (p.causal ? s.base + 1 : s.L) &&
                                (p.window == 0 || j0 >= see_lo || j0 + kTile <= p.sinks);
-            // ---- S = Q K^T
+            // ---- S^T = K Q^T: element e is key r8 + 8 (e / 2) of the 16, row 2 c4 + e % 2 of the 8
             uint32_t slot = it % C::kSlots;
             ok = __all_sync(0xffffffffu, mbar_wait(&full[slot], (it / C::kSlots) & 1u, wc));
             if (!ok) break;
-            float sc[NB][2][4] = {};
+            float sc[NB][NT][4] = {};
             uint32_t base = ring + slot * C::kSlotBytes;
+            // matrices: keys 0-7 and 8-15 of a 16-byte chunk, then of the next chunk
             if constexpr (E4M3) {
-                // matrices: keys 0-7 and 8-15 of chunk 2 x, then of chunk 2 x + 1
 #pragma unroll
                 for (int x = 0; x < D / 32; ++x)
 #pragma unroll
@@ -341,40 +360,41 @@ __device__ void compute_role(const PagedAttnParams& p, uint8_t* smem, uint64_t* 
                         uint32_t b[4];
                         ldmatrix4(b, base + chunk_at<D, E4M3>(key0 + 16 * n + (lane & 15), 2 * x + (lane >> 4)));
 #pragma unroll
-                        for (int y = 0; y < 2; ++y)
+                        for (int y = 0; y < 2; ++y) {
+                            const uint32_t a[4] = {e4m3x2_f16x2(b[2 * y] & 0xffffu), e4m3x2_f16x2(b[2 * y + 1] & 0xffffu),
+                                                   e4m3x2_f16x2(b[2 * y] >> 16), e4m3x2_f16x2(b[2 * y + 1] >> 16)};
 #pragma unroll
-                            for (int nt = 0; nt < 2; ++nt)
-                                mma16816<true>(sc[n][nt], qa[2 * x + y], e4m3x2_f16x2(b[2 * y + nt] & 0xffffu),
-                                               e4m3x2_f16x2(b[2 * y + nt] >> 16));
+                            for (int z = 0; z < NT; ++z) mma16816<true>(sc[n][z], a, qb[z][2 * x + y][0], qb[z][2 * x + y][1]);
+                        }
                     }
                 const float* f = scales + slot * (C::kScaleBytes / 4);
 #pragma unroll
-                for (int n = 0; n < NB; ++n)
+                for (int n = 0; n < NB; ++n) {
+                    const float k0 = f[step16 * n], k1 = f[step16 * n + 8];
 #pragma unroll
-                    for (int nt = 0; nt < 2; ++nt) {
-                        const float2 k1 = *reinterpret_cast<const float2*>(f + step16 * n + 8 * nt);
-                        sc[n][nt][0] *= k1.x * cs[0];
-                        sc[n][nt][1] *= k1.y * cs[0];
-                        sc[n][nt][2] *= k1.x * cs[1];
-                        sc[n][nt][3] *= k1.y * cs[1];
+                    for (int z = 0; z < NT; ++z) {
+                        sc[n][z][0] *= k0 * cs[z][0];
+                        sc[n][z][1] *= k0 * cs[z][1];
+                        sc[n][z][2] *= k1 * cs[z][0];
+                        sc[n][z][3] *= k1 * cs[z][1];
                     }
+                }
             } else {
-                // matrices: keys 0-7 of chunks 2 k and 2 k + 1, then keys 8-15
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k)
 #pragma unroll
                     for (int n = 0; n < NB; ++n) {
-                        uint32_t b[4];
-                        ldmatrix4(b, base + chunk_at<D, E4M3>(key0 + 16 * n + (lane & 7) + ((lane >> 4) << 3), 2 * k + ((lane >> 3) & 1)));
-                        mma16816<false>(sc[n][0], qa[k], b[0], b[1]);
-                        mma16816<false>(sc[n][1], qa[k], b[2], b[3]);
+                        uint32_t a[4];
+                        ldmatrix4(a, base + chunk_at<D, E4M3>(key0 + 16 * n + (lane & 15), 2 * k + (lane >> 4)));
+#pragma unroll
+                        for (int z = 0; z < NT; ++z) mma16816<false>(sc[n][z], a, qb[z][k][0], qb[z][k][1]);
                     }
 #pragma unroll
                 for (int n = 0; n < NB; ++n)
 #pragma unroll
-                    for (int nt = 0; nt < 2; ++nt)
+                    for (int z = 0; z < NT; ++z)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) sc[n][nt][e] *= kLog2e;
+                        for (int e = 0; e < 4; ++e) sc[n][z][e] *= kLog2e;
             }
             // (a slot is handed back when what was loaded from it has been used)
             __syncwarp();
@@ -382,158 +402,168 @@ __device__ void compute_role(const PagedAttnParams& p, uint8_t* smem, uint64_t* 
             ++it;
             slot = it % C::kSlots;
             base = ring + slot * C::kSlotBytes;
-            const int jc = j0 + key0 + 2 * c4;  // this thread's keys: jc + 16 n + 8 nt and the one behind
+            const int jk = j0 + key0;  // the warp's first key
             if (!whole) {
 #pragma unroll
                 for (int n = 0; n < NB; ++n)
 #pragma unroll
-                    for (int nt = 0; nt < 2; ++nt)
+                    for (int z = 0; z < NT; ++z)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            const int j = jc + 16 * n + 8 * nt + (e & 1), x = e >> 1;
-                            const bool see = j < hi[x] && (p.window == 0 || j >= lo[x] || j < p.sinks);
-                            if (!see) sc[n][nt][e] = -INFINITY;
+                            const int j = jk + 16 * n + r8 + 8 * (e >> 1);
+                            const bool see = j < hi[z][e & 1] && (p.window == 0 || j >= lo[z][e & 1] || j < p.sinks);
+                            if (!see) sc[n][z][e] = -INFINITY;
                         }
             }
             // ---- e4m3: l, with a running max of each lane's own
             if constexpr (E4M3) {
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    if (x == 1 && !two) break;
-                    const float mx = lane_max(sc, x);
-                    if (mx > ms[x] + kRescale || (ms[x] == -INFINITY && mx > ms[x])) {
-                        l[x] *= ex2(ms[x] - mx);
-                        ms[x] = mx;
-                    }
-                    const float nm = ms[x] == -INFINITY ? 0.f : -ms[x];
-                    float sum = 0.f;
+                for (int z = 0; z < NT; ++z)
 #pragma unroll
-                    for (int n = 0; n < NB; ++n)
-                        sum += (ex2(sc[n][0][2 * x] + nm) + ex2(sc[n][0][2 * x + 1] + nm)) +
-                               (ex2(sc[n][1][2 * x] + nm) + ex2(sc[n][1][2 * x + 1] + nm));
-                    l[x] += sum;
-                }
+                    for (int e = 0; e < 2; ++e) {
+                        const float mx = lane_max(sc, z, e);
+                        if (mx > ms[z][e] + kRescale || (ms[z][e] == -INFINITY && mx > ms[z][e])) {
+                            l[z][e] *= ex2(ms[z][e] - mx);
+                            ms[z][e] = mx;
+                        }
+                        const float nm = ms[z][e] == -INFINITY ? 0.f : -ms[z][e];
+#pragma unroll
+                        for (int n = 0; n < NB; ++n) l[z][e] += ex2(sc[n][z][e] + nm) + ex2(sc[n][z][2 + e] + nm);
+                    }
             }
             ok = __all_sync(0xffffffffu, mbar_wait(&full[slot], (it / C::kSlots) & 1u, wc));
             if (!ok) break;
-            // ---- e4m3: the V scales 2^a vm, vm in [1, 2), join the scores
-            float vm[NB][4];
+            // ---- e4m3: the V scales join the scores as exponents.  (No number stays none; log2 0 = -inf,
+            // for the zeros of a page that is none.)
             if constexpr (E4M3) {
                 const float* f = scales + slot * (C::kScaleBytes / 4);
 #pragma unroll
+                for (int n = 0; n < NB; ++n) {
+                    const float v0 = lg2(f[step16 * n]), v1 = lg2(f[step16 * n + 8]);
+#pragma unroll
+                    for (int z = 0; z < NT; ++z)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float y = sc[n][z][e] + (e < 2 ? v0 : v1);
+                            sc[n][z][e] = whole || sc[n][z][e] != -INFINITY ? y : -INFINITY;  // masked stays masked
+                        }
+                }
+            }
+            // ---- running max of the row (shared by the eight lanes that hold it), p, sums
+            bool raise = false;
+            float mx[NT][2];
+#pragma unroll
+            for (int z = 0; z < NT; ++z)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float y = lane_max(sc, z, e);
+                    y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 4));
+                    y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 8));
+                    mx[z][e] = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 16));
+                    raise |= mx[z][e] > m[z][e] + kRescale || (m[z][e] == -INFINITY && mx[z][e] > m[z][e]);
+                }
+            if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+                for (int z = 0; z < NT; ++z)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const bool up = mx[z][e] > m[z][e];  // (any rise will do once one is due)
+                        const float f = up ? ex2(m[z][e] - mx[z][e]) : 1.f;
+                        if (up) m[z][e] = mx[z][e];
+                        if (!E4M3) l[z][e] *= f;
+#pragma unroll
+                        for (int i = 0; i < D / 16; ++i) {
+                            o[i][z][e] *= f;
+                            o[i][z][2 + e] *= f;
+                        }
+                    }
+            }
+            // P^T as the B operand: pairs of rows become pairs of keys
+            uint32_t pa[NB][NT][2], pb[NB][NT][2];
+#pragma unroll
+            for (int z = 0; z < NT; ++z) {
+                const float n0 = (E4M3 ? kF16Up : 0.f) - (m[z][0] == -INFINITY ? 0.f : m[z][0]);
+                const float n1 = (E4M3 ? kF16Up : 0.f) - (m[z][1] == -INFINITY ? 0.f : m[z][1]);
+#pragma unroll
                 for (int n = 0; n < NB; ++n)
 #pragma unroll
-                    for (int nt = 0; nt < 2; ++nt) {
-                        const float2 v1 = *reinterpret_cast<const float2*>(f + step16 * n + 8 * nt);
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const uint32_t vb = __float_as_uint(e ? v1.y : v1.x);
-                            // a scale that is no number makes the row no number; exponent 0 is a scale of 0
-                            // (a row of zeros, from a page that is none)
-                            const int a = static_cast<int>((vb >> 23) & 0xffu);
-                            const float va = a == 255 ? __uint_as_float(0x7fc00000u) : static_cast<float>(a - 127);
-                            vm[n][2 * nt + e] = __uint_as_float((vb & 0x7fffffu) | 0x3f800000u);
-#pragma unroll
-                            for (int x = 0; x < 2; ++x)  // (a masked score stays -inf whatever the scale)
-                                if (sc[n][nt][2 * x + e] != -INFINITY) sc[n][nt][2 * x + e] += va;
-                        }
-                    }
-            }
-            // ---- running max of the row (shared by the four lanes that hold it), p, sums
-            float mx[2] = {lane_max(sc, 0), lane_max(sc, 1)};
-            mx[0] = fmaxf(mx[0], __shfl_xor_sync(0xffffffffu, mx[0], 1));
-            mx[0] = fmaxf(mx[0], __shfl_xor_sync(0xffffffffu, mx[0], 2));
-            if (two) {
-                mx[1] = fmaxf(mx[1], __shfl_xor_sync(0xffffffffu, mx[1], 1));
-                mx[1] = fmaxf(mx[1], __shfl_xor_sync(0xffffffffu, mx[1], 2));
-            }
-            const bool up0 = mx[0] > m[0] + kRescale || (m[0] == -INFINITY && mx[0] > m[0]);
-            const bool up1 = two && (mx[1] > m[1] + kRescale || (m[1] == -INFINITY && mx[1] > m[1]));
-            if (__any_sync(0xffffffffu, up0 || up1)) {
-                const float f0 = up0 ? ex2(m[0] - mx[0]) : 1.f, f1 = up1 ? ex2(m[1] - mx[1]) : 1.f;
-                if (up0) m[0] = mx[0];
-                if (up1) m[1] = mx[1];
-                if (!E4M3) {
-                    l[0] *= f0;
-                    l[1] *= f1;
-                }
-#pragma unroll
-                for (int i = 0; i < D / 8; ++i) {
-                    o[i][0] *= f0;
-                    o[i][1] *= f0;
-                    o[i][2] *= f1;
-                    o[i][3] *= f1;
-                }
-            }
-            const float up = E4M3 ? kF16Up : 0.f;
-            const float nm[2] = {up - (m[0] == -INFINITY ? 0.f : m[0]), up - (m[1] == -INFINITY ? 0.f : m[1])};
-            uint32_t pa[NB][4], pb[NB][4];
-#pragma unroll
-            for (int n = 0; n < NB; ++n)
-#pragma unroll
-                for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        pa[n][2 * nt + x] = pb[n][2 * nt + x] = 0u;
-                        if (x == 1 && !two) break;
-                        const float a = ex2(sc[n][nt][2 * x] + nm[x]), b = ex2(sc[n][nt][2 * x + 1] + nm[x]);
+                    for (int h = 0; h < 2; ++h) {
+                        const float a = ex2(sc[n][z][2 * h] + n0), b = ex2(sc[n][z][2 * h + 1] + n1);
                         if constexpr (E4M3) {
-                            pa[n][2 * nt + x] = pack_f16x2(a * vm[n][2 * nt], b * vm[n][2 * nt + 1]);
+                            pa[n][z][h] = transpose8(pack_f16x2(a, b));
                         } else {
-                            l[x] += a + b;
-                            const uint32_t h = pack_bf16x2(a, b);
-                            pa[n][2 * nt + x] = h;
-                            pb[n][2 * nt + x] = pack_bf16x2(a - __uint_as_float(h << 16), b - __uint_as_float(h & 0xffff0000u));
+                            l[z][0] += a;
+                            l[z][1] += b;
+                            const uint32_t w = pack_bf16x2(a, b);
+                            pa[n][z][h] = transpose8(w);
+                            pb[n][z][h] = transpose8(pack_bf16x2(a - __uint_as_float(w << 16), b - __uint_as_float(w & 0xffff0000u)));
                         }
                     }
-            // ---- O += P V; values of keys that no row sees count as zero, whatever they hold
-            uint32_t keep[NB][2];  // of the key pairs jc + 16 n and jc + 16 n + 8
+            }
+            // ---- O^T += V^T P^T; values of keys that no row sees count as zero, whatever they hold
+            uint32_t keep[NB][2];  // of the key pairs 2 c4 of the first and of the second 8
 #pragma unroll
             for (int n = 0; n < NB; ++n)
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    keep[n][x] = 0xffffffffu;
+                for (int h = 0; h < 2; ++h) {
+                    keep[n][h] = 0xffffffffu;
                     if (!whole) {
-                        const int j = jc + 16 * n + 8 * x;
+                        const int j = jk + 16 * n + 8 * h + 2 * c4;
                         const int wlo = p.window > 0 ? s.base - p.window + 1 : 0;
                         const bool a = j < s.L && (j >= wlo || j < p.sinks);
                         const bool b = j + 1 < s.L && (j + 1 >= wlo || j + 1 < p.sinks);
-                        keep[n][x] = (a ? 0xffffu : 0u) | (b ? 0xffff0000u : 0u);
+                        keep[n][h] = (a ? 0xffffu : 0u) | (b ? 0xffff0000u : 0u);
                     }
                 }
+            if constexpr (E4M3) {
+                // matrices: keys 0-7 and 8-15 of a chunk of 16 elements, then of the next; the operand's rows
+                // 0-7 are a chunk's even elements, 8-15 its odd ones
 #pragma unroll
-            for (int x = 0; x < (E4M3 ? D / 32 : D / 16); ++x)
+                for (int x = 0; x < D / 32; ++x)
 #pragma unroll
-                for (int n = 0; n < NB; ++n) {
-                    uint32_t b[4];  // matrices: keys 0-7 and 8-15 of a chunk, then of the next
-                    ldmatrix4_t(b, base + chunk_at<D, E4M3>(key0 + 16 * n + (lane & 15), 2 * x + (lane >> 4)));
-                    if (!whole) {
+                    for (int n = 0; n < NB; ++n) {
+                        uint32_t b[4];
+                        ldmatrix4_t(b, base + chunk_at<D, E4M3>(key0 + 16 * n + (lane & 15), 2 * x + (lane >> 4)));
+                        if (!whole) {
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) b[e] &= keep[n][e & 1];
-                        if (!E4M3 && T > 1) {
+                            for (int e = 0; e < 4; ++e) b[e] &= keep[n][e & 1];
+                        }
+#pragma unroll
+                        for (int y = 0; y < 2; ++y) {
+                            const uint32_t u = __byte_perm(b[2 * y], 0, 0x3120), v = __byte_perm(b[2 * y + 1], 0, 0x3120);
+                            const uint32_t a[4] = {e4m3x2_f16x2(u & 0xffffu), e4m3x2_f16x2(u >> 16), e4m3x2_f16x2(v & 0xffffu),
+                                                   e4m3x2_f16x2(v >> 16)};
+#pragma unroll
+                            for (int z = 0; z < NT; ++z) mma16816<true>(o[2 * x + y][z], a, pa[n][z][0], pa[n][z][1]);
+                        }
+                    }
+            } else {
+                // matrices: elements 0-7 and 8-15 of 16 for keys 0-7, then for keys 8-15
+#pragma unroll
+                for (int x = 0; x < D / 16; ++x)
+#pragma unroll
+                    for (int n = 0; n < NB; ++n) {
+                        uint32_t a[4];
+                        ldmatrix4_t(a, base + chunk_at<D, E4M3>(key0 + 16 * n + (lane & 7) + ((lane >> 4) << 3), 2 * x + ((lane >> 3) & 1)));
+                        if (!whole) {
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
-                                const uint32_t b0 = (b[e] & 0x7f80u) == 0x7f80u ? 0xffffu : 0u;
-                                const uint32_t b1 = (b[e] & 0x7f800000u) == 0x7f800000u ? 0xffff0000u : 0u;
-                                if (b0 | b1) bad_v = true;
-                                b[e] &= ~(b0 | b1);
+                                a[e] &= keep[n][e >> 1];
+                                if (T > 1) {
+                                    const uint32_t bad = ((a[e] & 0x7f80u) == 0x7f80u ? 0xffffu : 0u) |
+                                                         ((a[e] & 0x7f800000u) == 0x7f800000u ? 0xffff0000u : 0u);
+                                    if (bad) bad_v = true;
+                                    a[e] &= ~bad;
+                                }
                             }
                         }
-                    }
-                    if constexpr (E4M3) {
 #pragma unroll
-                        for (int y = 0; y < 2; ++y) {  // chunk 2 x + y: columns of even and of odd elements
-                            const uint32_t ev = __byte_perm(b[2 * y], b[2 * y + 1], 0x6420), od = __byte_perm(b[2 * y], b[2 * y + 1], 0x7531);
-                            mma16816<true>(o[4 * x + 2 * y], pa[n], e4m3x2_f16x2(ev & 0xffffu), e4m3x2_f16x2(ev >> 16));
-                            mma16816<true>(o[4 * x + 2 * y + 1], pa[n], e4m3x2_f16x2(od & 0xffffu), e4m3x2_f16x2(od >> 16));
+                        for (int z = 0; z < NT; ++z) {
+                            mma16816<false>(o[x][z], a, pa[n][z][0], pa[n][z][1]);
+                            mma16816<false>(o[x][z], a, pb[n][z][0], pb[n][z][1]);
                         }
-                    } else {
-                        mma16816<false>(o[2 * x], pa[n], b[0], b[1]);
-                        mma16816<false>(o[2 * x + 1], pa[n], b[2], b[3]);
-                        mma16816<false>(o[2 * x], pb[n], b[0], b[1]);
-                        mma16816<false>(o[2 * x + 1], pb[n], b[2], b[3]);
                     }
-                }
+            }
             __syncwarp();
             if (lane == 0) mbar_arrive(&empty[slot]);
         }
@@ -543,36 +573,41 @@ __device__ void compute_role(const PagedAttnParams& p, uint8_t* smem, uint64_t* 
         const int slot_i = 2 * blockIdx.x + (first ? 0 : 1);
         PagedPartial* part = parts + slot_i;
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            if constexpr (E4M3) {  // the lanes' sums to one max
-                float top = fmaxf(ms[x], __shfl_xor_sync(0xffffffffu, ms[x], 1));
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                if (ms[x] != -INFINITY) l[x] *= ex2(ms[x] - top);
-                ms[x] = top;
-            } else {
-                ms[x] = m[x];
-            }
-            l[x] += __shfl_xor_sync(0xffffffffu, l[x], 1);
-            l[x] += __shfl_xor_sync(0xffffffffu, l[x], 2);
-            if (c4 == 0) {
-                sm[warp * kRows + r8 + 8 * x] = m[x];
-                sms[warp * kRows + r8 + 8 * x] = ms[x];
-                sl[warp * kRows + r8 + 8 * x] = l[x];
-            }
-        }
-        for (int x = 0; x < (two ? 2 : 1); ++x) {
-            float* dst = so + (warp * 8 + r8) * C::kOStride;
+        for (int x = 0; x < NT; ++x)
 #pragma unroll
-            for (int i = 0; i < D / 8; i += 2) {
-                const float a0 = x ? o[i][2] : o[i][0], a1 = x ? o[i][3] : o[i][1];
-                const float b0 = x ? o[i + 1][2] : o[i + 1][0], b1 = x ? o[i + 1][3] : o[i + 1][1];
-                if constexpr (E4M3) {
-                    *reinterpret_cast<float4*>(dst + 8 * i + 4 * c4) = make_float4(a0, b0, a1, b1);
+            for (int e = 0; e < 2; ++e) {
+                if constexpr (E4M3) {  // the lanes' sums to one max
+                    float top = fmaxf(ms[x][e], __shfl_xor_sync(0xffffffffu, ms[x][e], 4));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+                    if (ms[x][e] != -INFINITY) l[x][e] *= ex2(ms[x][e] - top);
+                    ms[x][e] = top;
                 } else {
-                    *reinterpret_cast<float2*>(dst + 8 * i + 2 * c4) = make_float2(a0, a1);
-                    *reinterpret_cast<float2*>(dst + 8 * i + 8 + 2 * c4) = make_float2(b0, b1);
+                    ms[x][e] = m[x][e];
+                }
+                l[x][e] += __shfl_xor_sync(0xffffffffu, l[x][e], 4);
+                l[x][e] += __shfl_xor_sync(0xffffffffu, l[x][e], 8);
+                l[x][e] += __shfl_xor_sync(0xffffffffu, l[x][e], 16);
+                if (r8 == 0) {
+                    sm[warp * kRows + 8 * x + 2 * c4 + e] = m[x][e];
+                    sms[warp * kRows + 8 * x + 2 * c4 + e] = ms[x][e];
+                    sl[warp * kRows + 8 * x + 2 * c4 + e] = l[x][e];
                 }
             }
+#pragma unroll
+        for (int x = 0; x < NT; ++x) {
+            float* dst = so + (warp * 8 + 2 * c4) * C::kOStride;
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    if constexpr (E4M3) {
+                        *reinterpret_cast<float2*>(dst + e * C::kOStride + 16 * i + 2 * r8) = make_float2(o[i][x][e], o[i][x][2 + e]);
+                    } else {
+                        dst[e * C::kOStride + 16 * i + r8] = o[i][x][e];
+                        dst[e * C::kOStride + 16 * i + 8 + r8] = o[i][x][2 + e];
+                    }
+                }
             // (a warp that gave up still comes here, so that none waits for it)
             ok = named_bar_and(kBar, kWarps * 32, ok);
             const bool any_bad = !named_bar_and(kBar, kWarps * 32, !bad_v);
@@ -649,12 +684,12 @@ __device__ void compute_role(const PagedAttnParams& p, uint8_t* smem, uint64_t* 
     });
 }
 
-template <int D, bool E4M3>
-__global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
+template <int D, bool E4M3, int NT>
+__global__ void __launch_bounds__(Cfg<D, E4M3, NT>::kThreads, 1)
     paged_decode_kernel(const __grid_constant__ PagedAttnParams p, const __grid_constant__ CUtensorMap tk,
                         const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tks,
                         const __grid_constant__ CUtensorMap tvs) {
-    using C = Cfg<D, E4M3>;
+    using C = Cfg<D, E4M3, NT>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     __shared__ __align__(8) uint64_t full[C::kSlots];
@@ -679,15 +714,10 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
     if (threadIdx.x < 2) parts[threadIdx.x].b = -1;  // until a cut pair says otherwise
     __syncthreads();
     const WaitCtl wc{&abort_flag, p.err, p.timeout_ns};
-    // e4m3: 512 threads start with 128 registers each; 384 * 152 + 128 * 56 is the same sum
-    if (threadIdx.x / 32 >= C::kWarps) {
-        if constexpr (E4M3) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-        if (threadIdx.x / 32 == C::kWarps)
-            load_role<D, E4M3>(p, &tk, &tv, &tks, &tvs, smem_u32(smem), smem_u32(smem) + C::kScaleOff, full, empty, pre, w0, w1, wc);
-    } else {
-        if constexpr (E4M3) asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
-        compute_role<D, E4M3>(p, smem, full, empty, pre, w0, w1, wc);
-    }
+    if (threadIdx.x / 32 == C::kWarps)
+        load_role<D, E4M3, NT>(p, &tk, &tv, &tks, &tvs, smem_u32(smem), smem_u32(smem) + C::kScaleOff, full, empty, pre, w0, w1, wc);
+    else
+        compute_role<D, E4M3, NT>(p, smem, full, empty, pre, w0, w1, wc);
 }
 
 // Joins the parts of pairs that were cut.  Block (x, r): if a pair begins in block x of the first
@@ -761,20 +791,15 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__
     if (lane == 0) p.lse[tok * p.l_ts + head * p.l_hs] = l == 0.f ? -INFINITY : (Ms + log2f(l)) * kLn2;
 }
 
-template <int D, bool E4M3>
+template <int D, bool E4M3, int NT>
 int launch_t(const PagedAttnParams& p, const PagedMaps& m, int shares, cudaStream_t stream) {
-    using C = Cfg<D, E4M3>;
-    auto kern = paged_decode_kernel<D, E4M3>;
+    using C = Cfg<D, E4M3, NT>;
+    auto kern = paged_decode_kernel<D, E4M3, NT>;
     const int bytes = C::kFixedBytes + 4 * (p.kv.batch + 1);
     static std::atomic<unsigned long long> ready{0};
     if (!once_a_device(ready, [&] {
-            if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     C::kFixedBytes + 4 * (kPagedMaxBatch + 1)) != cudaSuccess)
-                return false;
-            if (!E4M3) return true;
-            // the register split adds up only if the block starts with 128 a thread
-            cudaFuncAttributes a;
-            return cudaFuncGetAttributes(&a, kern) == cudaSuccess && a.numRegs == 128;
+            return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                        C::kFixedBytes + 4 * (kPagedMaxBatch + 1)) == cudaSuccess;
         }))
         return -4;
     kern<<<shares, C::kThreads, bytes, stream>>>(p, m.k, m.v, m.ks, m.vs);
@@ -794,8 +819,13 @@ int launch_t(const PagedAttnParams& p, const PagedMaps& m, int shares, cudaStrea
 }  // namespace
 
 int launch_paged_decode(const PagedAttnParams& p, const PagedMaps& m, int shares, cudaStream_t stream) {
-    if (p.kv.d == 128) return p.kv.e4m3 ? launch_t<128, true>(p, m, shares, stream) : launch_t<128, false>(p, m, shares, stream);
-    return p.kv.e4m3 ? launch_t<64, true>(p, m, shares, stream) : launch_t<64, false>(p, m, shares, stream);
+    const bool one = p.max_q * p.g <= 8;
+    if (p.kv.d == 128) {
+        if (p.kv.e4m3) return one ? launch_t<128, true, 1>(p, m, shares, stream) : launch_t<128, true, 2>(p, m, shares, stream);
+        return one ? launch_t<128, false, 1>(p, m, shares, stream) : launch_t<128, false, 2>(p, m, shares, stream);
+    }
+    if (p.kv.e4m3) return one ? launch_t<64, true, 1>(p, m, shares, stream) : launch_t<64, true, 2>(p, m, shares, stream);
+    return one ? launch_t<64, false, 1>(p, m, shares, stream) : launch_t<64, false, 2>(p, m, shares, stream);
 }
 
 }  // namespace ra
