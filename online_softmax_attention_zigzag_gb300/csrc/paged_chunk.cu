@@ -39,6 +39,8 @@ constexpr int kMmaWarp = 8, kLoadWarp = 10, kExpandWarp = 12;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kRescaleLog2 = 8.0f;
+constexpr int kPBar = 1;                   // named barriers kPBar + x: unit x's P is written
+constexpr int kPBarThreads = 4 * 32 + 32;  // its softmax warps and its issuer
 constexpr int kPoison = 8;  // marks of the last parts, in turn: part k's holds k + 1 if it needs care
 
 template <int D, bool E4M3>
@@ -59,7 +61,7 @@ struct Cfg {
 };
 
 struct Bars {
-    uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_done[2], o_free[2], drain[2];
+    uint64_t q_full[2], q_empty[2], s_full[2], o_done[2], o_free[2], drain[2];
     uint64_t kv_full[4], kv_empty[4];
     uint64_t fixed[2];                // bf16: a tile's values have been looked over
     uint64_t raw_full[4], raw_empty[4];  // e4m3
@@ -570,7 +572,7 @@ __device__ void mma_role(const PagedAttnParams& p, int x, uint32_t smem, Bars& b
     using C = Cfg<D, E4M3>;
     const uint32_t q_base = smem + x * C::kTileBytes, kv_base = smem + C::kKVOff;
     const uint32_t s_tmem = tmem + x * kTile, o_tmem = tmem + C::kOCol + x * D;
-    uint32_t st = 0, qit = 0, pit = 0, seq = 0, nf = 0;
+    uint32_t st = 0, qit = 0, seq = 0, nf = 0;
     bool ok = true;
     for_each_part(p, [&](const Part& q) -> bool {
         ok = false;
@@ -612,8 +614,11 @@ __device__ void mma_role(const PagedAttnParams& p, int x, uint32_t smem, Bars& b
             const uint32_t mine = seq + nx * (j + 1) + x;
             if (!__all_sync(0xffffffffu, wait_turn(turn, mine, wc))) return false;
             if (j == 0 && !mbar_wait_w(&b.o_free[x], (qit & 1u) ^ 1u, wc)) return false;
-            if (!mbar_wait_w(&b.p_full[x], pit & 1u, wc)) return false;
-            ++pit;
+            // P on a hardware named barrier, which releases the issuer as the last softmax warp arrives,
+            // sooner than an mbarrier's wake.  It cannot time out: it is entered only while no role has
+            // given up, after S(j) was queued, and the softmax warps arrive for every tile whose S they see.
+            if (__any_sync(0xffffffffu, *wc.abort_flag != 0)) return false;
+            named_bar_sync(kPBar + x, kPBarThreads);
             tc_fence_after();
             issue_pv<D>(o_tmem, s_tmem + 64, base, j > 0);
             if (j + 1 < n) {
@@ -716,7 +721,12 @@ __device__ void softmax_role(const PagedAttnParams& p, int x, Bars& b, uint32_t 
     const uint32_t o_tmem = tmem + lane_off + C::kOCol + x * D;
     const int tok_in = row / p.g;
     uint32_t sit = 0, iit = 0;
-    auto wait = [&](uint64_t* bar, uint32_t parity) -> bool { return __all_sync(0xffffffffu, mbar_wait(bar, parity, wc)); };
+    // The issuer waits for P where it cannot give up, so these warps hold on to every S that it queued:
+    // their waits end with the barrier or with their own time limit (a second at least, far above
+    // what a queued MMA takes), never because another role has given up.
+    auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+        return __all_sync(0xffffffffu, mbar_wait_noabort(bar, parity, wc));
+    };
     for_each_part(p, [&](const Part& q) -> bool {
         if (x >= units_of(p, q.c)) return true;
         const int t_row = q.c.ta + x * p.unit_tokens + tok_in;  // the row's token; none if not below tb
@@ -813,7 +823,7 @@ __device__ void softmax_role(const PagedAttnParams& p, int x, Bars& b, uint32_t 
             lr += sr[0] + sr[1];
             tmem_wait_st();
             tc_fence_before();
-            mbar_arrive(&b.p_full[x]);
+            named_bar_arrive(kPBar + x, kPBarThreads);
         }
         if (!wait(&b.o_done[x], iit & 1u)) return false;
         ++iit;
@@ -906,7 +916,6 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
             mbar_init(&b.q_full[x], 1);
             mbar_init(&b.q_empty[x], 1);
             mbar_init(&b.s_full[x], 1);
-            mbar_init(&b.p_full[x], 128);
             mbar_init(&b.o_done[x], 1);
             mbar_init(&b.o_free[x], 128);
             mbar_init(&b.drain[x], 1);
