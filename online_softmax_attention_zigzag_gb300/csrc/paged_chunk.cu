@@ -23,8 +23,8 @@
 //     place are the value times 2^-120, exact for subnormal codes too, and one packed
 //     multiplication by 2^120 * scale finishes it, exact for scales that are powers of two.
 //
-// Warps: 0-7 softmax (four a unit), 8 and 9 issue the units' MMAs, 10 loads, 11 (bf16) looks
-// values over; e4m3: 12-19 expand and look over.  TMEM as in the ring kernel: S_x at
+// Warps: 0-7 softmax (four a unit), 8 and 9 issue the units' MMAs, 10 loads; bf16: 12-15 look values
+// over; e4m3: 12-19 expand and look over.  TMEM as in the ring kernel: S_x at
 // [128 x, 128 x + 128), P_x over the upper half of S_x, O_x at 256 + D x.
 #include <cuda_bf16.h>
 
@@ -45,7 +45,10 @@ constexpr int kPoison = 8;  // marks of the last parts, in turn: part k's holds 
 
 template <int D, bool E4M3>
 struct Cfg {
-    static constexpr int kThreads = E4M3 ? 640 : 384;
+    static constexpr int kThreads = E4M3 ? 640 : 512;
+    // registers: what the softmax warps take and what the others keep, of what all start with
+    static constexpr int kStartRegs = E4M3 ? 96 : 128, kSoftmaxRegs = 168, kOtherRegs = E4M3 ? 48 : 88;
+    static_assert(256 * kSoftmaxRegs + (kThreads - 256) * kOtherRegs <= kThreads * kStartRegs, "register split");
     static constexpr int kTileBytes = kTile * D * 2;  // a bf16 tile
     static constexpr int kBoxBytes = kTile * 128;     // 64 columns of it
     static constexpr int kBoxes = D / 64;
@@ -60,10 +63,20 @@ struct Cfg {
     static constexpr uint32_t kOCol = 256;
 };
 
+constexpr int kFixes = 8;  // more than the stages there are
+
+// A V tile that not every row sees whole: where it lies and which of its keys are used.
+struct Fix {
+    int slot, parity;  // stage and parity of its load; slot < 0: no more requests
+    int k, j0, hi, first;
+};
+
 struct Bars {
     uint64_t q_full[2], q_empty[2], s_full[2], o_done[2], o_free[2], drain[2];
     uint64_t kv_full[4], kv_empty[4];
-    uint64_t fixed[2];                // bf16: a tile's values have been looked over
+    // bf16: the loader asks for a V tile to be looked over (fix_req, its particulars in Shared::fix), the
+    // issuers wait for it (fixed).  Requests are numbered; at most kStages are open at a time, one a stage.
+    uint64_t fix_req[kFixes], fixed[kFixes];
     uint64_t raw_full[4], raw_empty[4];  // e4m3
 };
 struct Shared {
@@ -72,6 +85,7 @@ struct Shared {
     int abort_flag;
     uint32_t turn;
     int poison[kPoison];
+    Fix fix[kFixes];
 };
 
 // ------------------------------------------------------------------ items
@@ -263,15 +277,25 @@ __device__ __forceinline__ int units_of(const PagedAttnParams& p, const Chunk& c
 // above it.  e4m3: the tiles go one by one into the raw ring, in the same order.
 template <int D, bool E4M3>
 __device__ void load_role(const PagedAttnParams& p, const CUtensorMap* tq, const CUtensorMap* tk, const CUtensorMap* tv,
-                          uint32_t smem, Bars& b, const WaitCtl& wc) {
+                          uint32_t smem, Bars& b, volatile Fix* fix, const WaitCtl& wc) {
     using C = Cfg<D, E4M3>;
     const PagedKV& kv = p.kv;
     const int lane = threadIdx.x & 31;
     const int rows = p.box_rows, boxes = kTile / rows;
     const uint32_t q_bytes = static_cast<uint32_t>(p.unit_tokens * p.g) * 128u * C::kBoxes;
     const uint64_t keep = make_policy_evict_last(), stream = make_policy_evict_first();
-    uint32_t st = 0, qit[2] = {0, 0};
+    uint32_t st = 0, qit[2] = {0, 0}, nf = 0;
     bool ok = true;
+    auto ask = [&](int slot, int parity, int k, int j0, int hi, int first) {  // (one lane)
+        volatile Fix& f = fix[nf % kFixes];
+        f.slot = slot;
+        f.parity = parity;
+        f.k = k;
+        f.j0 = j0;
+        f.hi = hi;
+        f.first = first;
+        mbar_arrive(&b.fix_req[nf % kFixes]);
+    };
     for_each_part(p, [&](const Part& q) -> bool {
         const int nx = units_of(p, q.c);
         for (int x = 0; x < nx; ++x) {
@@ -332,12 +356,17 @@ __device__ void load_role(const PagedAttnParams& p, const CUtensorMap* tq, const
                             tma_load_3d(dst + C::kTileBytes + i * C::kBoxBytes, tk, &b.kv_full[slot], i * 64, y, pg, policy);
                     }
                 }
+                if (has_v && !whole_tile(p, q.c, q.c.key(t - 1))) {
+                    if (lane == 0) ask(slot, ((st - 1) / C::kStages) & 1u, q.k, q.c.key(t - 1), q.c.hi, q.c.first);
+                    ++nf;
+                }
             }
             prev_page = pg;
             prev_y = y;
         }
         return true;
     });
+    if (!E4M3 && ok && lane == 0) ask(-1, 0, 0, 0, 0, 0);
     if (!ok && lane == 0) {  // let the copies in flight land before the block ends
         constexpr uint32_t kN = E4M3 ? C::kRaw : C::kStages;
         uint64_t* full = E4M3 ? b.raw_full : b.kv_full;
@@ -351,8 +380,8 @@ __device__ void load_role(const PagedAttnParams& p, const CUtensorMap* tq, const
 }
 
 // ------------------------------------------------------------------ values that must not spread
-__device__ __forceinline__ bool key_used(const PagedAttnParams& p, const Chunk& c, int j) {
-    return j < c.hi && (j >= c.first || j < p.sinks);
+__device__ __forceinline__ bool key_used(int j, int hi, int first, int sinks) {
+    return j < hi && (j >= first || j < sinks);
 }
 __device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
@@ -361,58 +390,55 @@ __device__ __forceinline__ uint32_t finite2(uint32_t y) {
     return y & ~(((y & 0x7f80u) == 0x7f80u ? 0xffffu : 0u) | ((y & 0x7f800000u) == 0x7f800000u ? 0xffff0000u : 0u));
 }
 
-// bf16: one warp passes every stage; V tiles that not every row sees whole are cleaned in place.
+// bf16: four warps, 32 keys each, clean the V tiles that they are asked to, in place.  (One warp took
+// longer than a tile's other work, and the product waited.)
 template <int D>
-__device__ void fix_role(const PagedAttnParams& p, uint32_t smem, Bars& b, volatile int* poison, const WaitCtl& wc) {
+__device__ void fix_role(const PagedAttnParams& p, uint32_t smem, Bars& b, const volatile Fix* fix, volatile int* poison,
+                         const WaitCtl& wc) {
     using C = Cfg<D, false>;
-    const int lane = threadIdx.x & 31;
-    uint32_t st = 0, nf = 0;
-    for_each_part(p, [&](const Part& q) -> bool {
-        for (int t = q.ta; t <= q.tb; ++t, ++st) {
-            const uint32_t slot = st % C::kStages;
-            if (!mbar_wait_w(&b.kv_full[slot], (st / C::kStages) & 1u, wc)) return false;
-            const int j0 = t > q.ta ? q.c.key(t - 1) : 0;
-            if (t > q.ta && !whole_tile(p, q.c, j0)) {
-                const uint32_t v = smem + C::kKVOff + slot * C::kStageBytes + lane * 16;
-                bool bad = false;
-                // eight lanes a row of 128 bytes, so four rows a load; eight loads in flight.  (The
-                // swizzle permutes chunks inside a row only.)
+    const int lane = threadIdx.x & 31, quarter = threadIdx.x / 32 - kExpandWarp;
+    for (uint32_t nf = 0;; ++nf) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&b.fix_req[nf % kFixes], (nf / kFixes) & 1u, wc, 64))) return;
+        const volatile Fix& f = fix[nf % kFixes];
+        const int slot = f.slot, j0 = f.j0, hi = f.hi, first = f.first, k = f.k;
+        if (slot < 0) return;
+        // (the stage stays as it is until the issuers have had this tile, so its parity says enough)
+        if (!mbar_wait_w(&b.kv_full[slot], f.parity, wc)) return;
+        const uint32_t v = smem + C::kKVOff + slot * C::kStageBytes + lane * 16;
+        bool bad = false;
+        // eight lanes a row of 128 bytes, so four rows a load; eight loads in flight.  (The
+        // swizzle permutes chunks inside a row only.)
 #pragma unroll 1
-                for (int i = 0; i < C::kBoxes * 4; ++i) {
-                    const uint32_t at = v + (i >> 2) * C::kBoxBytes + (i & 3) * (32 * 128);
-                    const int r = (i & 3) * 32 + lane / 8;  // and r + 4, ... r + 28
-                    uint4 x[8];
-                    uint32_t top = 0, drop = 0;
+        for (int i = 0; i < C::kBoxes; ++i) {
+            const uint32_t at = v + i * C::kBoxBytes + quarter * (32 * 128);
+            const int r = quarter * 32 + lane / 8;  // and r + 4, ... r + 28
+            uint4 x[8];
+            uint32_t top = 0, drop = 0;
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) x[e] = lds128(at + e * 512);
+            for (int e = 0; e < 8; ++e) x[e] = lds128(at + e * 512);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const uint32_t m = __vmaxu2(__vmaxu2(x[e].x & 0x7fff7fffu, x[e].y & 0x7fff7fffu),
-                                                    __vmaxu2(x[e].z & 0x7fff7fffu, x[e].w & 0x7fff7fffu));
-                        if (key_used(p, q.c, j0 + r + 4 * e)) top = __vmaxu2(top, m);
-                        else drop |= 1u << e;
-                    }
-                    const bool sick = max(top & 0xffffu, top >> 16) >= 0x7f80u;
-                    if (drop || sick) {
-                        bad |= sick;
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const uint32_t keep = (drop >> e) & 1u ? 0u : 0xffffffffu;
-                            sts128(at + e * 512, finite2(x[e].x) & keep, finite2(x[e].y) & keep, finite2(x[e].z) & keep,
-                                   finite2(x[e].w) & keep);
-                        }
-                    }
-                }
-                if (bad) poison[q.k % kPoison] = q.k + 1;
-                fence_async_shared();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&b.fixed[nf % 2]);
-                ++nf;
+            for (int e = 0; e < 8; ++e) {
+                const uint32_t m = __vmaxu2(__vmaxu2(x[e].x & 0x7fff7fffu, x[e].y & 0x7fff7fffu),
+                                            __vmaxu2(x[e].z & 0x7fff7fffu, x[e].w & 0x7fff7fffu));
+                if (key_used(j0 + r + 4 * e, hi, first, p.sinks)) top = __vmaxu2(top, m);
+                else drop |= 1u << e;
             }
-            if (lane == 0) mbar_arrive(&b.kv_empty[slot]);
+            const bool sick = max(top & 0xffffu, top >> 16) >= 0x7f80u;
+            if (drop || sick) {
+                bad |= sick;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const uint32_t keep = (drop >> e) & 1u ? 0u : 0xffffffffu;
+                    sts128(at + e * 512, finite2(x[e].x) & keep, finite2(x[e].y) & keep, finite2(x[e].z) & keep,
+                           finite2(x[e].w) & keep);
+                }
+            }
         }
-        return true;
-    });
+        if (bad) poison[k % kPoison] = k + 1;
+        fence_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&b.fixed[nf % kFixes]);
+    }
 }
 
 // e4m3: 256 threads, half a row each, expand every tile into its bf16 stage.
@@ -492,7 +518,7 @@ __device__ void expand_role(const PagedAttnParams& p, uint32_t smem, Bars& b, vo
                 bool zero = false;
                 const int j0 = q.c.key(t - 1);
                 if (!whole_tile(p, q.c, j0)) {
-                    zero = !key_used(p, q.c, j0 + r);
+                    zero = !key_used(j0 + r, q.c.hi, q.c.first, p.sinks);
                     if (!zero && !(fabsf(v1) < INFINITY)) {
                         zero = true;
                         poison[q.k % kPoison] = q.k + 1;
@@ -608,7 +634,7 @@ __device__ void mma_role(const PagedAttnParams& p, int x, uint32_t smem, Bars& b
         for (int j = 0; j < n; ++j) {
             if (!wait_stage(slot, base)) return false;  // V(j) and, unless j is the last, K(j + 1)
             if (!E4M3 && !whole_tile(p, q.c, q.c.key(q.ta + j))) {
-                if (!mbar_wait_w(&b.fixed[nf % 2], (nf / 2) & 1u, wc)) return false;
+                if (!mbar_wait_w(&b.fixed[nf % kFixes], (nf / kFixes) & 1u, wc)) return false;
                 ++nf;
             }
             const uint32_t mine = seq + nx * (j + 1) + x;
@@ -919,13 +945,16 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
             mbar_init(&b.o_done[x], 1);
             mbar_init(&b.o_free[x], 128);
             mbar_init(&b.drain[x], 1);
-            mbar_init(&b.fixed[x], 1);
         }
         for (int s = 0; s < 4; ++s) {
             mbar_init(&b.kv_full[s], E4M3 ? 256 : 1);
-            mbar_init(&b.kv_empty[s], E4M3 ? 2 : 3);  // both issuers, and the warp that looks values over
+            mbar_init(&b.kv_empty[s], 2);  // both issuers
             mbar_init(&b.raw_full[s], 1);
             mbar_init(&b.raw_empty[s], 256);
+        }
+        for (int s = 0; s < kFixes; ++s) {
+            mbar_init(&b.fix_req[s], 1);
+            mbar_init(&b.fixed[s], 4);
         }
         sh.abort_flag = 0;
         sh.turn = 0;
@@ -945,19 +974,17 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
     const uint32_t tmem = sh.tmem;
     const WaitCtl wc{&sh.abort_flag, p.err, p.timeout_ns};
     if (warp < 8) {
-        // e4m3: 640 threads start with 96 registers each; 256 * 168 + 384 * 48 is the same sum
-        if constexpr (E4M3) asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSoftmaxRegs));
         softmax_role<D, E4M3>(p, warp / 4, b, tmem, sh.poison, wc);
     } else {
-        if constexpr (E4M3) asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
         if (warp == kMmaWarp || warp == kMmaWarp + 1) {
             mma_role<D, E4M3>(p, warp - kMmaWarp, smem_u32(smem), b, tmem, &sh.turn, wc);
         } else if (warp == kLoadWarp) {
-            load_role<D, E4M3>(p, &tq, &tk, &tv, smem_u32(smem), b, wc);
-        } else if constexpr (E4M3) {
-            if (warp >= kExpandWarp) expand_role<D>(p, smem_u32(smem), b, sh.poison, wc);
-        } else {
-            fix_role<D>(p, smem_u32(smem), b, sh.poison, wc);
+            load_role<D, E4M3>(p, &tq, &tk, &tv, smem_u32(smem), b, sh.fix, wc);
+        } else if (warp >= kExpandWarp) {
+            if constexpr (E4M3) expand_role<D>(p, smem_u32(smem), b, sh.poison, wc);
+            else fix_role<D>(p, smem_u32(smem), b, sh.fix, sh.poison, wc);
         }
     }
     __syncwarp();
@@ -1035,10 +1062,9 @@ int launch_t(const PagedAttnParams& p, const PagedMaps& m, int shares, cudaStrea
     static std::atomic<unsigned long long> ready{0};
     if (!once_a_device(ready, [&] {
             if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes) != cudaSuccess) return false;
-            if (!E4M3) return true;
-            // the register split adds up only if the block starts with 96 a thread
+            // the register split adds up only if the block starts with as many as it counts on
             cudaFuncAttributes a;
-            return cudaFuncGetAttributes(&a, kern) == cudaSuccess && a.numRegs == 96;
+            return cudaFuncGetAttributes(&a, kern) == cudaSuccess && a.numRegs == C::kStartRegs;
         }))
         return -4;
     paged_plan_kernel<<<1, kPlanThreads, 0, stream>>>(p);
