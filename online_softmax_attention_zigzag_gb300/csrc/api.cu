@@ -653,7 +653,7 @@ bool paged_few(int total, int g, int max_q) {
 }
 
 // Bytes of the workspace: two partial results a block, and for chunks the list of items (a
-// 64-bit count an item, an index a sequence).
+// 64-bit count a pair of units and a block, an index a sequence).
 long long paged_workspace(int total, int batch, int g, int max_q, ra::PagedAttnParams* p) {
     long long n = 2LL * ra::kPagedMaxShares;
     if (paged_few(total, g, max_q)) {
@@ -667,7 +667,7 @@ long long paged_workspace(int total, int batch, int g, int max_q, ra::PagedAttnP
             p->max_pairs = static_cast<int>(pairs);
             p->plan_off = n;
         }
-        n += 8 * (pairs + 1) + 4LL * (batch + 1);
+        n += 8 * (pairs + 1) + 8LL * (ra::kPagedMaxShares + 1) + 4 + 4LL * (batch + 1);
     }
     return (n + 255) / 256 * 256;
 }

@@ -9,12 +9,14 @@
 //   * keys: tiles come page by page, a TMA box is gcd(page, 128) rows of one page; a tile is read
 //     when some row of the item sees a key of it (sinks first, then the window up to the last
 //     row's position).
-//   * work: the key tiles of all (sequence, head, pair of units) items in one line are dealt to
-//     the blocks in equal contiguous shares; an item that lies in several shares leaves
-//     partial results that a join kernel combines.  Every SM then ends within one tile of
-//     the others, whatever the lengths are, at the price of 2 * 132 KB of partial results a
-//     block, about two tiles' time.  The list of items is made on the device by a one-block
-//     kernel, because the lengths are there.
+//   * work: items (sequence, KV head, pair of units) are dealt out whole, one round of blocks after
+//     the other, so that the blocks work on one or two heads at a time and their K and V stay in L2, as
+//     long as no block gets more than an equal share of all tiles; the tiles of the items
+//     that are left, in one line, then fill every block up to its share.  An item that lies in several
+//     blocks' fillings leaves partial results that a join kernel combines.  Every SM ends
+//     within one tile of the others, whatever the lengths are, at the price of at most 2 * 132 KB of
+//     partial results a block, about two tiles' time.  The list is made on the device by a
+//     one-block kernel, because the lengths are there.
 //   * values: a row of P is 0 where a key is hidden, but 0 * NaN is NaN, so tiles that not every
 //     row sees whole have their V looked over before the product: rows that nobody sees
 //     become zeros, and infinities and NaN become zeros that the rows that do see them add at
@@ -129,16 +131,46 @@ __device__ __forceinline__ int pairs_of(const PagedAttnParams& p, int b) {
 }
 
 // The list of items: base[b] = pairs of the sequences before b; pre[e] = tiles of the pairs before
-// pair e (of one head).
+// pair e (of one head).  Items are numbered by sequence, then head, then pair; the first rounds *
+// grid are whole, one a block and round; block x takes tiles [fill[x], fill[x + 1]) of the rest.
 struct Plan {
     long long* pre;
+    long long* fill;
     int* base;
+    int* rounds;
 };
 __device__ __forceinline__ Plan plan_at(const PagedAttnParams& p) {
     Plan x;
     x.pre = reinterpret_cast<long long*>(static_cast<uint8_t*>(p.workspace) + p.plan_off);
-    x.base = reinterpret_cast<int*>(x.pre + p.max_pairs + 1);
+    x.fill = x.pre + p.max_pairs + 1;
+    x.rounds = reinterpret_cast<int*>(x.fill + kPagedMaxShares + 1);
+    x.base = x.rounds + 1;
     return x;
+}
+
+// Sequence, head and pair of item i.
+struct Item {
+    int b, h, e;
+};
+__device__ __forceinline__ Item find_item(const Plan& plan, int B, int H, long long i) {
+    int lo = 0, hi = B;  // base[lo] * H <= i < base[hi] * H
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (static_cast<long long>(plan.base[mid]) * H <= i) lo = mid;
+        else hi = mid;
+    }
+    const int first = plan.base[lo], pairs = plan.base[lo + 1] - first;
+    const long long in = i - static_cast<long long>(first) * H;
+    Item it;
+    it.b = lo;
+    it.h = static_cast<int>(in / pairs);
+    it.e = first + static_cast<int>(in - static_cast<long long>(it.h) * pairs);
+    return it;
+}
+// Tiles before item `it`, all heads counted.
+__device__ __forceinline__ long long tiles_before(const Plan& plan, int H, const Item& it) {
+    const int e0 = plan.base[it.b], e1 = plan.base[it.b + 1];
+    return plan.pre[e0] * H + (plan.pre[e1] - plan.pre[e0]) * it.h + plan.pre[it.e] - plan.pre[e0];
 }
 
 constexpr int kPlanThreads = 1024;
@@ -166,7 +198,7 @@ __device__ __forceinline__ long long block_scan(long long x, long long* scratch,
     return before + y - x;
 }
 
-__global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const __grid_constant__ PagedAttnParams p) {
+__global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const __grid_constant__ PagedAttnParams p, int grid) {
     __shared__ long long scratch[32];
     launch_dependents();
     const Plan plan = plan_at(p);
@@ -200,68 +232,105 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const __grid_c
         sum += all;
     }
     if (threadIdx.x == 0) plan.pre[E] = sum;
+    __syncthreads();
+    // whole rounds, while every block's stay within an equal share
+    const int H = p.kv.hkv, x = threadIdx.x;
+    const long long W = sum * H, N = static_cast<long long>(E) * H, each = W / grid;
+    long long load = 0;
+    int rounds = 0;
+    for (long long i = x; (rounds + 1LL) * grid <= N; i += grid, ++rounds) {
+        long long more = 0;
+        if (x < grid) {
+            const Item it = find_item(plan, B, H, i);
+            more = plan.pre[it.e + 1] - plan.pre[it.e];
+        }
+        if (__syncthreads_or(load + more > each)) break;
+        load += more;
+    }
+    const long long cap = x < grid ? each + (x < W % grid ? 1 : 0) - load : 0;
+    const long long at = block_scan(cap, scratch, all);
+    if (x < grid) plan.fill[x] = at;
+    if (x == 0) {
+        plan.fill[grid] = all;
+        plan.rounds[0] = rounds;
+    }
 }
 
 // Tiles [ta, tb) of an item, for KV head h.
 struct Part {
     Chunk c;
     int h, ta, tb;
-    int k;  // its number in this block's share
+    int k;     // its number among this block's parts
+    int slot;  // where its partial results go if it is cut: 0, or 1 behind the first of the filling
 };
 
-// Walks the parts of this block's share: f(part) until it returns false.
+// Walks this block's parts: f(part) until it returns false.
 template <class F>
 __device__ __forceinline__ void for_each_part(const PagedAttnParams& p, F&& f) {
     const Plan plan = plan_at(p);
     const int B = p.kv.batch, H = p.kv.hkv;
-    const int E = plan.base[B];
-    const long long W = plan.pre[E] * H;
-    // the first W % grid blocks take one tile more: blocks without any are the last ones
-    const long long each = W / gridDim.x, more = W % gridDim.x, x = blockIdx.x;
-    long long w = x * each + min(x, more);
-    const long long w1 = w + each + (x < more ? 1 : 0);
-    if (w >= w1) return;
-    int lo = 0, hi = B;  // the sequence: pre[base[lo]] * H <= w < pre[base[hi]] * H
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (plan.pre[plan.base[mid]] * H <= w) lo = mid;
-        else hi = mid;
-    }
-    int b = lo, e0 = plan.base[b], e1 = plan.base[b + 1];
-    const long long off = plan.pre[e0], per = plan.pre[e1] - off;  // tiles of one head
+    const int E = plan.base[B], rounds = plan.rounds[0];
+    long long w = plan.fill[blockIdx.x];
+    const long long w1 = plan.fill[blockIdx.x + 1];
     Part q;
-    q.h = static_cast<int>((w - off * H) / per);
-    const long long in = w - off * H - q.h * per + off;
-    lo = e0;
-    hi = e1;  // the pair: pre[lo] <= in < pre[hi]
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (plan.pre[mid] <= in) lo = mid;
-        else hi = mid;
-    }
-    int e = lo;
-    q.ta = static_cast<int>(in - plan.pre[e]);
     q.k = 0;
-    PagedSeq s = paged_seq(p.kv, b);
-    while (true) {
-        q.c = make_chunk(p, b, e - e0, s);
-        q.tb = static_cast<int>(min(static_cast<long long>(q.c.n), q.ta + (w1 - w)));
-        if (!f(q)) return;
-        w += q.tb - q.ta;
-        if (w >= w1) return;
-        q.ta = 0;
-        ++q.k;
-        if (++e == e1) {
-            e = e0;
-            if (++q.h == H) {
-                q.h = 0;
-                do {
-                    ++b;
-                    e0 = e1;
-                    e1 = plan.base[b + 1];
-                } while (e1 == e0);
-                e = e0;
+    q.slot = 0;
+    int b = -1;
+    PagedSeq s;
+    for (int round = 0;; ++round) {
+        // a whole item, or the first of the filling, which is found by its tile
+        Item it;
+        long long skip = 0;
+        if (round < rounds) {
+            it = find_item(plan, B, H, static_cast<long long>(round) * gridDim.x + blockIdx.x);
+        } else {
+            if (w >= w1) return;
+            const long long N = static_cast<long long>(E) * H, i0 = static_cast<long long>(rounds) * gridDim.x;
+            const long long t = w + (i0 < N ? tiles_before(plan, H, find_item(plan, B, H, i0)) : 0);
+            int lo = 0, hi = B;  // the sequence: pre[base[lo]] * H <= t < pre[base[hi]] * H
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (plan.pre[plan.base[mid]] * H <= t) lo = mid;
+                else hi = mid;
+            }
+            it.b = lo;
+            const int e0 = plan.base[lo], e1 = plan.base[lo + 1];
+            const long long off = plan.pre[e0], per = plan.pre[e1] - off;  // tiles of one head
+            it.h = static_cast<int>((t - off * H) / per);
+            const long long in = t - off * H - it.h * per + off;
+            lo = e0;
+            hi = e1;  // the pair: pre[lo] <= in < pre[hi]
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (plan.pre[mid] <= in) lo = mid;
+                else hi = mid;
+            }
+            it.e = lo;
+            skip = in - plan.pre[lo];
+        }
+        while (true) {
+            if (it.b != b) {
+                b = it.b;
                 s = paged_seq(p.kv, b);
+            }
+            q.c = make_chunk(p, b, it.e - plan.base[b], s);
+            q.h = it.h;
+            q.ta = static_cast<int>(skip);
+            q.tb = round < rounds ? q.c.n : static_cast<int>(min(static_cast<long long>(q.c.n), q.ta + (w1 - w)));
+            if (!f(q)) return;
+            ++q.k;
+            if (round < rounds) break;
+            w += q.tb - q.ta;
+            if (w >= w1) return;
+            q.slot = 1;
+            skip = 0;
+            if (++it.e == plan.base[it.b + 1]) {
+                it.e = plan.base[it.b];
+                if (++it.h == H) {
+                    it.h = 0;
+                    do ++it.b; while (plan.base[it.b + 1] == plan.base[it.b]);
+                    it.e = plan.base[it.b];
+                }
             }
         }
     }
@@ -398,7 +467,7 @@ __device__ void fix_role(const PagedAttnParams& p, uint32_t smem, Bars& b, const
     using C = Cfg<D, false>;
     const int lane = threadIdx.x & 31, quarter = threadIdx.x / 32 - kExpandWarp;
     for (uint32_t nf = 0;; ++nf) {
-        if (!__all_sync(0xffffffffu, mbar_wait(&b.fix_req[nf % kFixes], (nf / kFixes) & 1u, wc, 64))) return;
+        if (!__all_sync(0xffffffffu, mbar_wait_idle(&b.fix_req[nf % kFixes], (nf / kFixes) & 1u, wc, 20000))) return;
         const volatile Fix& f = fix[nf % kFixes];
         const int slot = f.slot, j0 = f.j0, hi = f.hi, first = f.first, k = f.k;
         if (slot < 0) return;
@@ -859,7 +928,7 @@ __device__ void softmax_role(const PagedAttnParams& p, int x, Bars& b, uint32_t 
         const bool sick = poison[q.k % kPoison] == q.k + 1;
         const float inv = lr == 0.f ? 0.f : 1.f / lr;
         const int tok = q.c.s.q0 + t_row, head = q.h * p.g + row - tok_in * p.g;
-        PagedChunkPartial* part = static_cast<PagedChunkPartial*>(p.workspace) + 2 * blockIdx.x + (q.k ? 1 : 0);
+        PagedChunkPartial* part = static_cast<PagedChunkPartial*>(p.workspace) + 2 * blockIdx.x + q.slot;
         const int r2 = x * kTile + row;
         // (rolled, as the mask: a quarter of the code to fetch once an item)
 #pragma unroll 1
@@ -967,7 +1036,11 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
     }
     launch_dependents();
     wait_primary();  // the list of items
-    if (threadIdx.x < 2) (static_cast<PagedChunkPartial*>(p.workspace) + 2 * blockIdx.x + threadIdx.x)->b = -1;
+    if (threadIdx.x < 2) {  // no partial results yet; and a block without a filling is no link between two
+        const Plan plan = plan_at(p);
+        const bool none = threadIdx.x == 0 && plan.fill[blockIdx.x] == plan.fill[blockIdx.x + 1];
+        (static_cast<PagedChunkPartial*>(p.workspace) + 2 * blockIdx.x + threadIdx.x)->b = none ? -2 : -1;
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -1006,11 +1079,11 @@ __global__ void __launch_bounds__(kJoinRows * D / 4) paged_chunk_join_kernel(con
     const int b = p0->b, pair = p0->pair, h = p0->h;
     if (b < 0 || !p0->begins) return;
     const Chunk c = make_chunk(p, b, pair, paged_seq(p.kv, b));
-    int n = 1;  // parts: p0, then the first ones of the blocks up to x + n - 1
+    int n = 1;  // parts: p0, then the first ones of the blocks up to x + n - 1 (that have a filling)
     while (x + n < shares) {
         const int y = x + n + lane;
         const PagedChunkPartial* q = parts + 2 * y;
-        const bool on = y < shares && q->b == b && q->pair == pair && q->h == h && !q->begins;
+        const bool on = y < shares && (q->b == -2 || (q->b == b && q->pair == pair && q->h == h && !q->begins));
         const uint32_t v = __ballot_sync(0xffffffffu, on);
         n += v == 0xffffffffu ? 32 : __ffs(~v) - 1;
         if (v != 0xffffffffu) break;
@@ -1021,11 +1094,15 @@ __global__ void __launch_bounds__(kJoinRows * D / 4) paged_chunk_join_kernel(con
     if (ru >= p.unit_tokens * p.g || t >= c.tb) return;
     float M = -INFINITY;
 #pragma unroll 4
-    for (int k = 0; k < n; ++k) M = fmaxf(M, (k ? parts + 2 * (x + k) : p0)->m[r]);
+    for (int k = 0; k < n; ++k) {
+        const PagedChunkPartial* q = k ? parts + 2 * (x + k) : p0;
+        if (q->b >= 0) M = fmaxf(M, q->m[r]);
+    }
     float l = 0.f, lr = 0.f, acc[4] = {};
 #pragma unroll 4
     for (int k = 0; k < n; ++k) {
         const PagedChunkPartial* q = k ? parts + 2 * (x + k) : p0;
+        if (q->b < 0) continue;
         const float f = paged_weight(q->m[r], M);
         const float4 v = q->o[col * (2 * kTile) + r];
         l = paged_add_weighted(l, f, q->l[r]);
@@ -1067,7 +1144,7 @@ int launch_t(const PagedAttnParams& p, const PagedMaps& m, int shares, cudaStrea
             return cudaFuncGetAttributes(&a, kern) == cudaSuccess && a.numRegs == C::kStartRegs;
         }))
         return -4;
-    paged_plan_kernel<<<1, kPlanThreads, 0, stream>>>(p);
+    paged_plan_kernel<<<1, kPlanThreads, 0, stream>>>(p, shares);
     if (cudaGetLastError() != cudaSuccess) return -4;
     if (launch_dependent(kern, dim3(shares), C::kThreads, C::kSmemBytes, stream, p, m.q, m.k, m.v) != cudaSuccess) return -4;
     return launch_dependent(paged_chunk_join_kernel<D>, dim3(shares, 2 * kTile / kJoinRows), kJoinRows * D / 4, 0, stream, p,

@@ -82,6 +82,26 @@ __device__ __forceinline__ float lg2(float x) {
     return y;
 }
 
+// As mbar_wait, for a waiter that is seldom needed: the thread is suspended for up to `hint_ns` at a
+// time, so that it takes no issue slots (and power) from the others meanwhile.
+__device__ __forceinline__ bool mbar_wait_idle(uint64_t* bar, uint32_t parity, const WaitCtl& w, uint32_t hint_ns) {
+    const uint64_t t0 = globaltimer_ns();
+    while (true) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(smem_u32(bar)), "r"(parity), "r"(hint_ns)
+            : "memory");
+        if (ok) return true;
+        if (*w.abort_flag) return false;
+        if (globaltimer_ns() - t0 > w.timeout_ns) {
+            raise_abort(w, bar);
+            return false;
+        }
+    }
+}
+
 // The dependent launch may begin (it still waits for this grid's end before it reads anything).
 __device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 // Wait for the end of the grid this launch depends on, its writes visible.
