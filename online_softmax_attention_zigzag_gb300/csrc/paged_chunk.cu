@@ -25,8 +25,8 @@
 //     place are the value times 2^-120, exact for subnormal codes too, and one packed
 //     multiplication by 2^120 * scale finishes it, exact for scales that are powers of two.
 //
-// Warps: 0-7 softmax (four a unit), 8 and 9 issue the units' MMAs, 10 loads; bf16: 12-15 look values
-// over; e4m3: 12-19 expand and look over.  TMEM as in the ring kernel: S_x at
+// Warps: 0-7 softmax (four a unit), 8 and 9 issue the units' MMAs, 10 loads, 11 lists the block's
+// parts; bf16: 12-15 look values over; e4m3: 12-19 expand and look over.  TMEM as in the ring kernel: S_x at
 // [128 x, 128 x + 128), P_x over the upper half of S_x, O_x at 256 + D x.
 #include <cuda_bf16.h>
 
@@ -37,7 +37,7 @@ namespace ra {
 namespace {
 
 constexpr int kTile = kPagedTile;
-constexpr int kMmaWarp = 8, kLoadWarp = 10, kExpandWarp = 12;
+constexpr int kMmaWarp = 8, kLoadWarp = 10, kListWarp = 11, kExpandWarp = 12;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kRescaleLog2 = 8.0f;
@@ -66,6 +66,7 @@ struct Cfg {
 };
 
 constexpr int kFixes = 8;  // more than the stages there are
+constexpr int kParts = 4;  // parts listed ahead
 
 // A V tile that not every row sees whole: where it lies and which of its keys are used.
 struct Fix {
@@ -80,16 +81,8 @@ struct Bars {
     // issuers wait for it (fixed).  Requests are numbered; at most kStages are open at a time, one a stage.
     uint64_t fix_req[kFixes], fixed[kFixes];
     uint64_t raw_full[4], raw_empty[4];  // e4m3
+    uint64_t part_full[kParts], part_empty[kParts];
 };
-struct Shared {
-    Bars b;
-    uint32_t tmem;
-    int abort_flag;
-    uint32_t turn;
-    int poison[kPoison];
-    Fix fix[kFixes];
-};
-
 // ------------------------------------------------------------------ items
 // Pair `pair` of units of sequence b: tokens [ta, tb) of it, key tiles [0, ns) and from lo on.
 struct Chunk {
@@ -264,6 +257,16 @@ struct Part {
     int slot;  // where its partial results go if it is cut: 0, or 1 behind the first of the filling
 };
 
+struct Shared {
+    Bars b;
+    uint32_t tmem;
+    int abort_flag;
+    uint32_t turn;
+    int poison[kPoison];
+    Fix fix[kFixes];
+    Part part[kParts];
+};
+
 // Walks this block's parts: f(part) until it returns false.
 template <class F>
 __device__ __forceinline__ void for_each_part(const PagedAttnParams& p, F&& f) {
@@ -336,6 +339,40 @@ __device__ __forceinline__ void for_each_part(const PagedAttnParams& p, F&& f) {
     }
 }
 
+// One warp walks the block's parts and lists them for the others, a few ahead: the walk's searches and
+// loads are then in nobody's way, and the registers that it takes in nobody's count.
+__device__ void list_role(const PagedAttnParams& p, Bars& b, Part* ring, const WaitCtl& wc) {
+    uint32_t k = 0;
+    bool ok = true;
+    auto put = [&](const Part& q) {
+        ok = __all_sync(0xffffffffu, mbar_wait_idle(&b.part_empty[k % kParts], ((k / kParts) & 1u) ^ 1u, wc, 20000));
+        if (!ok) return false;
+        if ((threadIdx.x & 31) == 0) {
+            ring[k % kParts] = q;
+            mbar_arrive(&b.part_full[k % kParts]);
+        }
+        ++k;
+        return true;
+    };
+    for_each_part(p, put);
+    Part end = {};
+    if (ok) put(end);  // tb = 0: no more
+}
+
+// Takes the listed parts in order: f(part) until it returns false; false when it or a wait did.  Run by
+// whole warps; `wait` is the role's way of waiting.
+template <class Wait, class F>
+__device__ __forceinline__ bool take_parts(Bars& b, const Part* ring, Wait&& wait, F&& f) {
+    for (uint32_t k = 0;; ++k) {
+        if (!wait(&b.part_full[k % kParts], (k / kParts) & 1u)) return false;
+        const Part q = ring[k % kParts];
+        if (q.tb == 0) return true;
+        if (!f(q)) return false;
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) mbar_arrive(&b.part_empty[k % kParts]);
+    }
+}
+
 // Units of an item: the second is there when its first token is.
 __device__ __forceinline__ int units_of(const PagedAttnParams& p, const Chunk& c) {
     return c.ta + p.unit_tokens < c.tb ? 2 : 1;
@@ -346,7 +383,7 @@ __device__ __forceinline__ int units_of(const PagedAttnParams& p, const Chunk& c
 // above it.  e4m3: the tiles go one by one into the raw ring, in the same order.
 template <int D, bool E4M3>
 __device__ void load_role(const PagedAttnParams& p, const CUtensorMap* tq, const CUtensorMap* tk, const CUtensorMap* tv,
-                          uint32_t smem, Bars& b, volatile Fix* fix, const WaitCtl& wc) {
+                          uint32_t smem, Bars& b, volatile Fix* fix, const Part* parts, const WaitCtl& wc) {
     using C = Cfg<D, E4M3>;
     const PagedKV& kv = p.kv;
     const int lane = threadIdx.x & 31;
@@ -365,7 +402,8 @@ __device__ void load_role(const PagedAttnParams& p, const CUtensorMap* tq, const
         f.first = first;
         mbar_arrive(&b.fix_req[nf % kFixes]);
     };
-    for_each_part(p, [&](const Part& q) -> bool {
+    auto wait_part = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait(bar, parity, wc, 32)); };
+    ok = take_parts(b, parts, wait_part, [&](const Part& q) -> bool {
         const int nx = units_of(p, q.c);
         for (int x = 0; x < nx; ++x) {
             ok = __all_sync(0xffffffffu, mbar_wait(&b.q_empty[x], (qit[x] & 1u) ^ 1u, wc, 32));
@@ -512,7 +550,8 @@ __device__ void fix_role(const PagedAttnParams& p, uint32_t smem, Bars& b, const
 
 // e4m3: 256 threads, half a row each, expand every tile into its bf16 stage.
 template <int D>
-__device__ void expand_role(const PagedAttnParams& p, uint32_t smem, Bars& b, volatile int* poison, const WaitCtl& wc) {
+__device__ void expand_role(const PagedAttnParams& p, uint32_t smem, Bars& b, const Part* parts, volatile int* poison,
+                            const WaitCtl& wc) {
     using C = Cfg<D, true>;
     const PagedKV& kv = p.kv;
     const int r = threadIdx.x & (kTile - 1);
@@ -556,7 +595,7 @@ __device__ void expand_role(const PagedAttnParams& p, uint32_t smem, Bars& b, vo
         mbar_arrive(&b.raw_empty[slot]);
         return true;
     };
-    for_each_part(p, [&](const Part& q) -> bool {
+    take_parts(b, parts, [&](uint64_t* bar, uint32_t parity) { return mbar_wait_w(bar, parity, wc); }, [&](const Part& q) -> bool {
         // this row's page two tiles ahead, and its scales one: neither load is waited for at once
         float ks = 0.f, vs = 0.f;
         int entry = -1, row = 0;
@@ -662,15 +701,14 @@ __device__ __forceinline__ bool wait_turn(volatile uint32_t* turn, uint32_t mine
 // that the tensor pipe sees each unit's batch whole while one issuer's waits overlap the
 // other's batch.  Every stage is released once by each of them.
 template <int D, bool E4M3>
-__device__ void mma_role(const PagedAttnParams& p, int x, uint32_t smem, Bars& b, uint32_t tmem, volatile uint32_t* turn,
-                         const WaitCtl& wc) {
+__device__ void mma_role(const PagedAttnParams& p, int x, uint32_t smem, Bars& b, const Part* parts, uint32_t tmem,
+                         volatile uint32_t* turn, const WaitCtl& wc) {
     using C = Cfg<D, E4M3>;
     const uint32_t q_base = smem + x * C::kTileBytes, kv_base = smem + C::kKVOff;
     const uint32_t s_tmem = tmem + x * kTile, o_tmem = tmem + C::kOCol + x * D;
     uint32_t st = 0, qit = 0, seq = 0, nf = 0;
-    bool ok = true;
-    for_each_part(p, [&](const Part& q) -> bool {
-        ok = false;
+    auto wait_part = [&](uint64_t* bar, uint32_t parity) { return mbar_wait_w(bar, parity, wc); };
+    const bool ok = take_parts(b, parts, wait_part, [&](const Part& q) -> bool {
         const int n = q.tb - q.ta, nx = units_of(p, q.c);
         auto wait_stage = [&](uint32_t& slot, uint32_t& base) -> bool {
             slot = st % C::kStages;
@@ -687,7 +725,6 @@ __device__ void mma_role(const PagedAttnParams& p, int x, uint32_t smem, Bars& b
                 if (!E4M3 && i > 0 && !whole_tile(p, q.c, q.c.key(q.ta + i - 1))) ++nf;
             }
             seq += 1 + n;
-            ok = true;
             return true;
         }
         // batches: S(0) of unit x is seq + x, tile j of unit x is seq + nx (j + 1) + x
@@ -728,7 +765,6 @@ __device__ void mma_role(const PagedAttnParams& p, int x, uint32_t smem, Bars& b
         }
         seq += nx * (n + 1);
         ++qit;
-        ok = true;
         return true;
     });
     if (!ok) {  // every MMA this warp issued must finish before TMEM is released
@@ -805,8 +841,8 @@ __device__ __noinline__ void add_sick(const PagedAttnParams& p, const Chunk& c, 
 }
 
 template <int D, bool E4M3>
-__device__ void softmax_role(const PagedAttnParams& p, int x, Bars& b, uint32_t tmem, const volatile int* poison,
-                             const WaitCtl& wc) {
+__device__ void softmax_role(const PagedAttnParams& p, int x, Bars& b, const Part* parts, uint32_t tmem,
+                             const volatile int* poison, const WaitCtl& wc) {
     using C = Cfg<D, E4M3>;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int row = (warp & 3) * 32 + lane;
@@ -822,7 +858,7 @@ __device__ void softmax_role(const PagedAttnParams& p, int x, Bars& b, uint32_t 
     auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
         return __all_sync(0xffffffffu, mbar_wait_noabort(bar, parity, wc));
     };
-    for_each_part(p, [&](const Part& q) -> bool {
+    take_parts(b, parts, wait, [&](const Part& q) -> bool {
         if (x >= units_of(p, q.c)) return true;
         const int t_row = q.c.ta + x * p.unit_tokens + tok_in;  // the row's token; none if not below tb
         const int pos = q.c.s.base + t_row;
@@ -1021,6 +1057,10 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
             mbar_init(&b.raw_full[s], 1);
             mbar_init(&b.raw_empty[s], 256);
         }
+        for (int s = 0; s < kParts; ++s) {
+            mbar_init(&b.part_full[s], 1);
+            mbar_init(&b.part_empty[s], E4M3 ? 19 : 11);  // softmax warps, issuers, loader, expanding warps
+        }
         for (int s = 0; s < kFixes; ++s) {
             mbar_init(&b.fix_req[s], 1);
             mbar_init(&b.fixed[s], 4);
@@ -1048,15 +1088,17 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
     const WaitCtl wc{&sh.abort_flag, p.err, p.timeout_ns};
     if (warp < 8) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSoftmaxRegs));
-        softmax_role<D, E4M3>(p, warp / 4, b, tmem, sh.poison, wc);
+        softmax_role<D, E4M3>(p, warp / 4, b, sh.part, tmem, sh.poison, wc);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
         if (warp == kMmaWarp || warp == kMmaWarp + 1) {
-            mma_role<D, E4M3>(p, warp - kMmaWarp, smem_u32(smem), b, tmem, &sh.turn, wc);
+            mma_role<D, E4M3>(p, warp - kMmaWarp, smem_u32(smem), b, sh.part, tmem, &sh.turn, wc);
         } else if (warp == kLoadWarp) {
-            load_role<D, E4M3>(p, &tq, &tk, &tv, smem_u32(smem), b, sh.fix, wc);
-        } else if (warp >= kExpandWarp) {
-            if constexpr (E4M3) expand_role<D>(p, smem_u32(smem), b, sh.poison, wc);
+            load_role<D, E4M3>(p, &tq, &tk, &tv, smem_u32(smem), b, sh.fix, sh.part, wc);
+        } else if (warp == kListWarp) {
+            list_role(p, b, sh.part, wc);
+        } else {
+            if constexpr (E4M3) expand_role<D>(p, smem_u32(smem), b, sh.part, sh.poison, wc);
             else fix_role<D>(p, smem_u32(smem), b, sh.fix, sh.poison, wc);
         }
     }
