@@ -661,9 +661,11 @@ long long paged_workspace(int total, int batch, int g, int max_q, ra::PagedAttnP
     } else {
         n *= sizeof(ra::PagedChunkPartial);
         const int unit = g <= 128 ? 128 / g : 1;
-        const long long pairs = total / (2 * unit) + batch;
+        const int item = (max_q < total ? max_q : total) <= unit ? unit : 2 * unit;
+        const long long pairs = total / item + batch;
         if (p) {
             p->unit_tokens = unit;
+            p->item_tokens = item;
             p->max_pairs = static_cast<int>(pairs);
             p->plan_off = n;
         }

@@ -25,6 +25,12 @@
 //     place are the value times 2^-120, exact for subnormal codes too, and one packed
 //     multiplication by 2^120 * scale finishes it, exact for scales that are powers of two.
 //
+//   * calls whose items all have one unit (at most 128 rows a sequence and KV head) have no partner
+//     whose softmax would overlap its products: the scores then alternate between the two units' S
+//     columns, S(j + 2) is issued behind P V(j), and the softmax goes from tile to tile without
+//     waiting for either; half the warps have nothing to do, and the other unit's Q makes room for
+//     e4m3 tiles on their way.
+//
 // Warps: 0-7 softmax (four a unit), 8 and 9 issue the units' MMAs, 10 loads, 11 lists the block's
 // parts; bf16: 12-15 look values over; e4m3: 12-19 expand and look over.  TMEM as in the ring kernel: S_x at
 // [128 x, 128 x + 128), P_x over the upper half of S_x, O_x at 256 + D x.
@@ -45,7 +51,8 @@ constexpr int kPBar = 1;                   // named barriers kPBar + x: unit x's
 constexpr int kPBarThreads = 4 * 32 + 32;  // its softmax warps and its issuer
 constexpr int kPoison = 8;  // marks of the last parts, in turn: part k's holds k + 1 if it needs care
 
-template <int D, bool E4M3>
+// ALONE: every item has one unit
+template <int D, bool E4M3, bool ALONE>
 struct Cfg {
     static constexpr int kThreads = E4M3 ? 640 : 512;
     // registers: what the softmax warps take and what the others keep, of what all start with
@@ -57,8 +64,9 @@ struct Cfg {
     static constexpr int kRawBytes = kTile * D;       // an e4m3 tile as it comes
     static constexpr int kStageBytes = 2 * kTileBytes;  // V of one tile and K of the next
     static constexpr int kStages = D == 128 ? 2 : 4;
-    static constexpr int kRaw = E4M3 ? (D == 128 ? 2 : 4) : 0;
-    static constexpr int kKVOff = 2 * kTileBytes;
+    // e4m3 tiles on their way: what memory is left (one unit alone leaves the other's Q)
+    static constexpr int kRaw = E4M3 ? (D == 128 ? (ALONE ? 4 : 2) : 8) : 0;
+    static constexpr int kKVOff = (ALONE ? 1 : 2) * kTileBytes;
     static constexpr int kRawOff = kKVOff + kStages * kStageBytes;
     static constexpr int kSmemBytes = kRawOff + kRaw * kRawBytes + 1024;
     static constexpr uint32_t kTmemCols = 512;
@@ -76,11 +84,12 @@ struct Fix {
 
 struct Bars {
     uint64_t q_full[2], q_empty[2], s_full[2], o_done[2], o_free[2], drain[2];
+    uint64_t pv_done;  // one unit alone: P V of a tile is in O
     uint64_t kv_full[4], kv_empty[4];
     // bf16: the loader asks for a V tile to be looked over (fix_req, its particulars in Shared::fix), the
     // issuers wait for it (fixed).  Requests are numbered; at most kStages are open at a time, one a stage.
     uint64_t fix_req[kFixes], fixed[kFixes];
-    uint64_t raw_full[4], raw_empty[4];  // e4m3
+    uint64_t raw_full[8], raw_empty[8];  // e4m3
     uint64_t part_full[kParts], part_empty[kParts];
 };
 // ------------------------------------------------------------------ items
@@ -100,7 +109,7 @@ __device__ __forceinline__ Chunk make_chunk(const PagedAttnParams& p, int b, int
     c.b = b;
     c.pair = pair;
     c.s = s;
-    const int tt = 2 * p.unit_tokens;
+    const int tt = p.item_tokens;
     c.ta = pair * tt;
     c.tb = min(min(c.s.T, p.max_q), c.ta + tt);
     c.hi = p.causal ? min(c.s.L, max(0, c.s.base + c.tb)) : c.s.L;
@@ -119,7 +128,7 @@ __device__ __forceinline__ bool whole_tile(const PagedAttnParams& p, const Chunk
 }
 
 __device__ __forceinline__ int pairs_of(const PagedAttnParams& p, int b) {
-    const int tt = 2 * p.unit_tokens;
+    const int tt = p.item_tokens;
     return (min(paged_seq(p.kv, b).T, p.max_q) + tt - 1) / tt;
 }
 
@@ -374,17 +383,25 @@ __device__ __forceinline__ bool take_parts(Bars& b, const Part* ring, Wait&& wai
 }
 
 // Units of an item: the second is there when its first token is.
+template <bool ALONE>
 __device__ __forceinline__ int units_of(const PagedAttnParams& p, const Chunk& c) {
+    if (ALONE) return 1;
     return c.ta + p.unit_tokens < c.tb ? 2 : 1;
 }
 
+// How many tiles K runs ahead of V: a part's stages hold V(i - ahead) and K(i), what there is of them.
+template <bool ALONE>
+__device__ __forceinline__ int ahead_of(const Part& q) {
+    return ALONE && q.tb - q.ta >= 2 ? 2 : 1;
+}
+
 // ------------------------------------------------------------------ the loading warp
-// Stages of a part of n tiles: K(0); V(j-1) with K(j); V(n-1).  V at the stage's base, K a tile
-// above it.  e4m3: the tiles go one by one into the raw ring, in the same order.
-template <int D, bool E4M3>
+// V at a stage's base, K a tile above it.  e4m3: the tiles go one by one into the raw ring, in
+// the same order.
+template <int D, bool E4M3, bool ALONE>
 __device__ void load_role(const PagedAttnParams& p, const CUtensorMap* tq, const CUtensorMap* tk, const CUtensorMap* tv,
                           uint32_t smem, Bars& b, volatile Fix* fix, const Part* parts, const WaitCtl& wc) {
-    using C = Cfg<D, E4M3>;
+    using C = Cfg<D, E4M3, ALONE>;
     const PagedKV& kv = p.kv;
     const int lane = threadIdx.x & 31;
     const int rows = p.box_rows, boxes = kTile / rows;
@@ -404,7 +421,7 @@ __device__ void load_role(const PagedAttnParams& p, const CUtensorMap* tq, const
     };
     auto wait_part = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait(bar, parity, wc, 32)); };
     ok = take_parts(b, parts, wait_part, [&](const Part& q) -> bool {
-        const int nx = units_of(p, q.c);
+        const int nx = units_of<ALONE>(p, q.c);
         for (int x = 0; x < nx; ++x) {
             ok = __all_sync(0xffffffffu, mbar_wait(&b.q_empty[x], (qit[x] & 1u) ^ 1u, wc, 32));
             if (!ok) return false;
@@ -418,10 +435,11 @@ __device__ void load_role(const PagedAttnParams& p, const CUtensorMap* tq, const
             __syncwarp();
         }
         // K and V are read again by the sequence's other pairs, if it has any
-        const uint64_t policy = q.c.s.T > 2 * p.unit_tokens ? keep : stream;
+        const uint64_t policy = q.c.s.T > p.item_tokens ? keep : stream;
         // the page of this lane's box, asked for a tile ahead and looked at only when it is needed: a load
         // waited for here would hold up the copies
-        int entry = -1, row = 0, prev_page = -1, prev_y = 0;
+        const int ahead = ahead_of<ALONE>(q);
+        int entry = -1, row = 0, v_page = -1, v_y = 0, prev_page = -1, prev_y = 0;
         auto look = [&](int t) {  // no page behind the last key
             const int pos = q.c.key(t) + lane * rows;
             entry = -1;
@@ -429,13 +447,17 @@ __device__ void load_role(const PagedAttnParams& p, const CUtensorMap* tq, const
             if (lane < boxes && pos < q.c.hi) entry = paged_entry(kv, q.c.b, pos, row);
         };
         look(q.ta);
-        for (int t = q.ta; t <= q.tb; ++t) {
+        for (int t = q.ta; t < q.tb + ahead; ++t) {
             const int pg = paged_checked(kv, entry), y = q.h * kv.page + row;
             if (t + 1 < q.tb) look(t + 1);
-            const bool has_v = t > q.ta, has_k = t < q.tb;
+            const bool has_v = t >= q.ta + ahead, has_k = t < q.tb;
+            if (ahead == 1) {
+                v_page = prev_page;
+                v_y = prev_y;
+            }
             if constexpr (E4M3) {
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {  // V(t - 1), then K(t)
+                for (int half = 0; half < 2; ++half) {  // V, then K
                     if (half ? !has_k : !has_v) continue;
                     const uint32_t slot = st % C::kRaw;
                     ok = __all_sync(0xffffffffu, mbar_wait(&b.raw_empty[slot], ((st / C::kRaw) & 1u) ^ 1u, wc, 32));
@@ -445,7 +467,7 @@ __device__ void load_role(const PagedAttnParams& p, const CUtensorMap* tq, const
                     __syncwarp();
                     if (lane < boxes)
                         tma_load_3d(smem + C::kRawOff + slot * C::kRawBytes + lane * rows * D, half ? tk : tv, &b.raw_full[slot], 0,
-                                    half ? y : prev_y, half ? pg : prev_page, policy);
+                                    half ? y : v_y, half ? pg : v_page, policy);
                 }
             } else {
                 const uint32_t slot = st % C::kStages;
@@ -458,16 +480,18 @@ __device__ void load_role(const PagedAttnParams& p, const CUtensorMap* tq, const
                     const uint32_t dst = smem + C::kKVOff + slot * C::kStageBytes + lane * rows * 128;
 #pragma unroll
                     for (int i = 0; i < C::kBoxes; ++i) {
-                        if (has_v) tma_load_3d(dst + i * C::kBoxBytes, tv, &b.kv_full[slot], i * 64, prev_y, prev_page, policy);
+                        if (has_v) tma_load_3d(dst + i * C::kBoxBytes, tv, &b.kv_full[slot], i * 64, v_y, v_page, policy);
                         if (has_k)
                             tma_load_3d(dst + C::kTileBytes + i * C::kBoxBytes, tk, &b.kv_full[slot], i * 64, y, pg, policy);
                     }
                 }
-                if (has_v && !whole_tile(p, q.c, q.c.key(t - 1))) {
-                    if (lane == 0) ask(slot, ((st - 1) / C::kStages) & 1u, q.k, q.c.key(t - 1), q.c.hi, q.c.first);
+                if (has_v && !whole_tile(p, q.c, q.c.key(t - ahead))) {
+                    if (lane == 0) ask(slot, ((st - 1) / C::kStages) & 1u, q.k, q.c.key(t - ahead), q.c.hi, q.c.first);
                     ++nf;
                 }
             }
+            v_page = prev_page;
+            v_y = prev_y;
             prev_page = pg;
             prev_y = y;
         }
@@ -499,10 +523,10 @@ __device__ __forceinline__ uint32_t finite2(uint32_t y) {
 
 // bf16: four warps, 32 keys each, clean the V tiles that they are asked to, in place.  (One warp took
 // longer than a tile's other work, and the product waited.)
-template <int D>
+template <int D, bool ALONE>
 __device__ void fix_role(const PagedAttnParams& p, uint32_t smem, Bars& b, const volatile Fix* fix, volatile int* poison,
                          const WaitCtl& wc) {
-    using C = Cfg<D, false>;
+    using C = Cfg<D, false, ALONE>;
     const int lane = threadIdx.x & 31, quarter = threadIdx.x / 32 - kExpandWarp;
     for (uint32_t nf = 0;; ++nf) {
         if (!__all_sync(0xffffffffu, mbar_wait_idle(&b.fix_req[nf % kFixes], (nf / kFixes) & 1u, wc, 20000))) return;
@@ -549,10 +573,10 @@ __device__ void fix_role(const PagedAttnParams& p, uint32_t smem, Bars& b, const
 }
 
 // e4m3: 256 threads, half a row each, expand every tile into its bf16 stage.
-template <int D>
+template <int D, bool ALONE>
 __device__ void expand_role(const PagedAttnParams& p, uint32_t smem, Bars& b, const Part* parts, volatile int* poison,
                             const WaitCtl& wc) {
-    using C = Cfg<D, true>;
+    using C = Cfg<D, true, ALONE>;
     const PagedKV& kv = p.kv;
     const int r = threadIdx.x & (kTile - 1);
     const int c0 = threadIdx.x >= kExpandWarp * 32 + kTile ? D / 32 : 0;  // first chunk of this half
@@ -613,18 +637,20 @@ __device__ void expand_role(const PagedAttnParams& p, uint32_t smem, Bars& b, co
         look(q.ta);
         fetch();
         look(q.ta + 1);
-        float prev_vs = 0.f;
-        for (int t = q.ta; t <= q.tb; ++t, ++st) {
-            const float k1 = ks, v1 = prev_vs;
-            prev_vs = vs;
+        const int ahead = ahead_of<ALONE>(q);
+        float vs1 = 0.f, vs2 = 0.f;  // V scales of one and two tiles ago
+        for (int t = q.ta; t < q.tb + ahead; ++t, ++st) {
+            const float k1 = ks, v1 = ahead == 1 ? vs1 : vs2;
+            vs2 = vs1;
+            vs1 = vs;
             fetch();
             look(t + 2);
             const uint32_t slot = st % C::kStages;
             if (!mbar_wait_w(&b.kv_empty[slot], ((st / C::kStages) & 1u) ^ 1u, wc)) return false;
             const uint32_t stage = smem + C::kKVOff + slot * C::kStageBytes;
-            if (t > q.ta) {
+            if (t >= q.ta + ahead) {
                 bool zero = false;
-                const int j0 = q.c.key(t - 1);
+                const int j0 = q.c.key(t - ahead);
                 if (!whole_tile(p, q.c, j0)) {
                     zero = !key_used(j0 + r, q.c.hi, q.c.first, p.sinks);
                     if (!zero && !(fabsf(v1) < INFINITY)) {
@@ -699,17 +725,17 @@ __device__ __forceinline__ bool wait_turn(volatile uint32_t* turn, uint32_t mine
 
 // The issuer of unit x.  The two take turns batch by batch (`turn` counts the batches issued), so
 // that the tensor pipe sees each unit's batch whole while one issuer's waits overlap the
-// other's batch.  Every stage is released once by each of them.
-template <int D, bool E4M3>
+// other's batch.  Every stage is released once by each of them.  (One unit alone: one issuer.)
+template <int D, bool E4M3, bool ALONE>
 __device__ void mma_role(const PagedAttnParams& p, int x, uint32_t smem, Bars& b, const Part* parts, uint32_t tmem,
                          volatile uint32_t* turn, const WaitCtl& wc) {
-    using C = Cfg<D, E4M3>;
+    using C = Cfg<D, E4M3, ALONE>;
     const uint32_t q_base = smem + x * C::kTileBytes, kv_base = smem + C::kKVOff;
-    const uint32_t s_tmem = tmem + x * kTile, o_tmem = tmem + C::kOCol + x * D;
+    const uint32_t o_tmem = tmem + C::kOCol + x * D;
     uint32_t st = 0, qit = 0, seq = 0, nf = 0;
     auto wait_part = [&](uint64_t* bar, uint32_t parity) { return mbar_wait_w(bar, parity, wc); };
     const bool ok = take_parts(b, parts, wait_part, [&](const Part& q) -> bool {
-        const int n = q.tb - q.ta, nx = units_of(p, q.c);
+        const int n = q.tb - q.ta, nx = units_of<ALONE>(p, q.c);
         auto wait_stage = [&](uint32_t& slot, uint32_t& base) -> bool {
             slot = st % C::kStages;
             base = kv_base + slot * C::kStageBytes;
@@ -718,31 +744,37 @@ __device__ void mma_role(const PagedAttnParams& p, int x, uint32_t smem, Bars& b
             return r;
         };
         uint32_t slot, base;
+        const int ahead = ahead_of<ALONE>(q);
         if (x >= nx) {  // no second unit: pass every stage
-            for (int i = 0; i <= n; ++i) {
+            for (int i = 0; i < n + ahead; ++i) {
                 if (!wait_stage(slot, base)) return false;
                 if ((threadIdx.x & 31) == 0) mbar_arrive(&b.kv_empty[slot]);
-                if (!E4M3 && i > 0 && !whole_tile(p, q.c, q.c.key(q.ta + i - 1))) ++nf;
+                if (!E4M3 && i >= ahead && !whole_tile(p, q.c, q.c.key(q.ta + i - ahead))) ++nf;
             }
-            seq += 1 + n;
+            seq += n + ahead;
             return true;
         }
-        // batches: S(0) of unit x is seq + x, tile j of unit x is seq + nx (j + 1) + x
+        // batches: the first scores' of unit x are seq + x (and, one unit ahead by two, seq + 1), tile j's
+        // seq + nx j + x behind them
         if (!mbar_wait_w(&b.q_full[x], qit & 1u, wc)) return false;
-        if (!wait_stage(slot, base)) return false;
-        if (!__all_sync(0xffffffffu, wait_turn(turn, seq + x, wc))) return false;
-        tc_fence_after();
-        issue_s<D>(s_tmem, q_base, base + C::kTileBytes);
-        mma_commit_e(&b.s_full[x]);
-        *turn = seq + x + 1;
-        mma_commit_e(&b.kv_empty[slot]);
-        if (n == 1) mma_commit_e(&b.q_empty[x]);
+        for (int i = 0; i < ahead; ++i) {
+            if (!wait_stage(slot, base)) return false;
+            if (!__all_sync(0xffffffffu, wait_turn(turn, seq + x, wc))) return false;
+            tc_fence_after();
+            issue_s<D>(tmem + (x + i) * kTile, q_base, base + C::kTileBytes);
+            mma_commit_e(&b.s_full[x + i]);
+            if (i + 1 < ahead) ++seq;
+            *turn = seq + x + (i + 1 < ahead ? 0 : 1);
+            mma_commit_e(&b.kv_empty[slot]);
+            if (i + 1 == n) mma_commit_e(&b.q_empty[x]);
+        }
         for (int j = 0; j < n; ++j) {
-            if (!wait_stage(slot, base)) return false;  // V(j) and, unless j is the last, K(j + 1)
+            if (!wait_stage(slot, base)) return false;  // V(j) and, unless there is none, K(j + ahead)
             if (!E4M3 && !whole_tile(p, q.c, q.c.key(q.ta + j))) {
                 if (!mbar_wait_w(&b.fixed[nf % kFixes], (nf / kFixes) & 1u, wc)) return false;
                 ++nf;
             }
+            const int y = ahead == 2 ? (j & 1) : x;  // whose S columns tile j's scores are in
             const uint32_t mine = seq + nx * (j + 1) + x;
             if (!__all_sync(0xffffffffu, wait_turn(turn, mine, wc))) return false;
             if (j == 0 && !mbar_wait_w(&b.o_free[x], (qit & 1u) ^ 1u, wc)) return false;
@@ -750,18 +782,18 @@ __device__ void mma_role(const PagedAttnParams& p, int x, uint32_t smem, Bars& b
             // sooner than an mbarrier's wake.  It cannot time out: it is entered only while no role has
             // given up, after S(j) was queued, and the softmax warps arrive for every tile whose S they see.
             if (__any_sync(0xffffffffu, *wc.abort_flag != 0)) return false;
-            named_bar_sync(kPBar + x, kPBarThreads);
+            named_bar_sync(kPBar + y, kPBarThreads);
             tc_fence_after();
-            issue_pv<D>(o_tmem, s_tmem + 64, base, j > 0);
-            if (j + 1 < n) {
-                issue_s<D>(s_tmem, q_base, base + C::kTileBytes);
-                mma_commit_e(&b.s_full[x]);
-            } else {
-                mma_commit_e(&b.o_done[x]);
+            issue_pv<D>(o_tmem, tmem + y * kTile + 64, base, j > 0);
+            if (ALONE) mma_commit_e(&b.pv_done);
+            if (j + ahead < n) {
+                issue_s<D>(tmem + y * kTile, q_base, base + C::kTileBytes);
+                mma_commit_e(&b.s_full[y]);
             }
+            if (j + 1 == n) mma_commit_e(&b.o_done[x]);
             *turn = mine + 1;
             mma_commit_e(&b.kv_empty[slot]);
-            if (j + 2 == n) mma_commit_e(&b.q_empty[x]);
+            if (j + ahead + 1 == n) mma_commit_e(&b.q_empty[x]);
         }
         seq += nx * (n + 1);
         ++qit;
@@ -840,18 +872,16 @@ __device__ __noinline__ void add_sick(const PagedAttnParams& p, const Chunk& c, 
     }
 }
 
-template <int D, bool E4M3>
+template <int D, bool E4M3, bool ALONE>
 __device__ void softmax_role(const PagedAttnParams& p, int x, Bars& b, const Part* parts, uint32_t tmem,
                              const volatile int* poison, const WaitCtl& wc) {
-    using C = Cfg<D, E4M3>;
+    using C = Cfg<D, E4M3, ALONE>;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int row = (warp & 3) * 32 + lane;
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t s_tmem = tmem + lane_off + x * kTile;
-    const uint32_t p_tmem = s_tmem + 64;
     const uint32_t o_tmem = tmem + lane_off + C::kOCol + x * D;
     const int tok_in = row / p.g;
-    uint32_t sit = 0, iit = 0;
+    uint32_t sit[2] = {0, 0}, pvs = 0, iit = 0;  // uses of s_full (one unit alone: of both) and pv_done; items
     // The issuer waits for P where it cannot give up, so these warps hold on to every S that it queued:
     // their waits end with the barrier or with their own time limit (a second at least, far above
     // what a queued MMA takes), never because another role has given up.
@@ -859,7 +889,8 @@ __device__ void softmax_role(const PagedAttnParams& p, int x, Bars& b, const Par
         return __all_sync(0xffffffffu, mbar_wait_noabort(bar, parity, wc));
     };
     take_parts(b, parts, wait, [&](const Part& q) -> bool {
-        if (x >= units_of(p, q.c)) return true;
+        if (x >= units_of<ALONE>(p, q.c)) return true;
+        const bool two = ahead_of<ALONE>(q) == 2;  // scores in both units' S columns in turn
         const int t_row = q.c.ta + x * p.unit_tokens + tok_in;  // the row's token; none if not below tb
         const int pos = q.c.s.base + t_row;
         // keys this row sees: below hi, and from lo on or below the sinks
@@ -872,8 +903,11 @@ __device__ void softmax_role(const PagedAttnParams& p, int x, Bars& b, const Par
         float m = -INFINITY, l = 0.f, lr = 0.f;
         for (int t = q.ta; t < q.tb; ++t) {
             const int j0 = q.c.key(t);
-            if (!wait(&b.s_full[x], sit & 1u)) return false;
-            ++sit;
+            const int y = ALONE ? (two ? (t - q.ta) & 1 : 0) : x;
+            const uint32_t s_tmem = tmem + lane_off + y * kTile, p_tmem = s_tmem + 64;
+            if (!wait(&b.s_full[y], (ALONE && y ? sit[1] : sit[0]) & 1u)) return false;
+            if (ALONE && y) ++sit[1];
+            else ++sit[0];
             tc_fence_after();
             // A tile that not every row of the unit sees whole is masked in place, 32 columns at a time
             // in a rolled loop: it is rare, and as straight code over 128 registers it ran at the speed
@@ -937,9 +971,13 @@ __device__ void softmax_role(const PagedAttnParams& p, int x, Bars& b, const Par
                 }
                 tmem_st16(p_tmem + qq * 16, pk);  // every score is in registers: P may overwrite S's upper half
             }
-            // O is stable here: the commit that signalled this S covered the previous P V, and the
-            // next one waits for this tile's arrivals
+            // O is stable here: the commit that signalled this S covered the previous P V (one unit alone:
+            // only the one before it), and the next one waits for this tile's arrivals
             if (__any_sync(0xffffffffu, need)) {
+                if (ALONE) {  // tile t is the part's (t - ta)th; its predecessor's P V is use pvs + t - ta - 1
+                    if (!wait(&b.pv_done, (pvs + (t - q.ta) - 1) & 1u)) return false;
+                    tc_fence_after();
+                }
 #pragma unroll
                 for (int cc = 0; cc < D; cc += 32) {
                     uint32_t o0[32];
@@ -954,8 +992,9 @@ __device__ void softmax_role(const PagedAttnParams& p, int x, Bars& b, const Par
             lr += sr[0] + sr[1];
             tmem_wait_st();
             tc_fence_before();
-            named_bar_arrive(kPBar + x, kPBarThreads);
+            named_bar_arrive(kPBar + y, kPBarThreads);
         }
+        pvs += q.tb - q.ta;
         if (!wait(&b.o_done[x], iit & 1u)) return false;
         ++iit;
         tc_fence_after();
@@ -1032,11 +1071,11 @@ __device__ void softmax_role(const PagedAttnParams& p, int x, Bars& b, const Par
     });
 }
 
-template <int D, bool E4M3>
-__global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
+template <int D, bool E4M3, bool ALONE>
+__global__ void __launch_bounds__(Cfg<D, E4M3, ALONE>::kThreads, 1)
     paged_chunk_kernel(const __grid_constant__ PagedAttnParams p, const __grid_constant__ CUtensorMap tq,
                        const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv) {
-    using C = Cfg<D, E4M3>;
+    using C = Cfg<D, E4M3, ALONE>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     __shared__ __align__(8) Shared sh;
@@ -1053,13 +1092,16 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
         }
         for (int s = 0; s < 4; ++s) {
             mbar_init(&b.kv_full[s], E4M3 ? 256 : 1);
-            mbar_init(&b.kv_empty[s], 2);  // both issuers
+            mbar_init(&b.kv_empty[s], ALONE ? 1 : 2);  // the issuers
+        }
+        for (int s = 0; s < 8; ++s) {
             mbar_init(&b.raw_full[s], 1);
             mbar_init(&b.raw_empty[s], 256);
         }
+        mbar_init(&b.pv_done, 1);
         for (int s = 0; s < kParts; ++s) {
             mbar_init(&b.part_full[s], 1);
-            mbar_init(&b.part_empty[s], E4M3 ? 19 : 11);  // softmax warps, issuers, loader, expanding warps
+            mbar_init(&b.part_empty[s], (ALONE ? 6 : 11) + (E4M3 ? 8 : 0));  // softmax warps, issuers, loader, expanding warps
         }
         for (int s = 0; s < kFixes; ++s) {
             mbar_init(&b.fix_req[s], 1);
@@ -1088,18 +1130,19 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
     const WaitCtl wc{&sh.abort_flag, p.err, p.timeout_ns};
     if (warp < 8) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSoftmaxRegs));
-        softmax_role<D, E4M3>(p, warp / 4, b, sh.part, tmem, sh.poison, wc);
+        if (!ALONE || warp < 4) softmax_role<D, E4M3, ALONE>(p, warp / 4, b, sh.part, tmem, sh.poison, wc);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
         if (warp == kMmaWarp || warp == kMmaWarp + 1) {
-            mma_role<D, E4M3>(p, warp - kMmaWarp, smem_u32(smem), b, sh.part, tmem, &sh.turn, wc);
+            if (!ALONE || warp == kMmaWarp)
+                mma_role<D, E4M3, ALONE>(p, warp - kMmaWarp, smem_u32(smem), b, sh.part, tmem, &sh.turn, wc);
         } else if (warp == kLoadWarp) {
-            load_role<D, E4M3>(p, &tq, &tk, &tv, smem_u32(smem), b, sh.fix, sh.part, wc);
+            load_role<D, E4M3, ALONE>(p, &tq, &tk, &tv, smem_u32(smem), b, sh.fix, sh.part, wc);
         } else if (warp == kListWarp) {
             list_role(p, b, sh.part, wc);
         } else {
-            if constexpr (E4M3) expand_role<D>(p, smem_u32(smem), b, sh.part, sh.poison, wc);
-            else fix_role<D>(p, smem_u32(smem), b, sh.fix, sh.poison, wc);
+            if constexpr (E4M3) expand_role<D, ALONE>(p, smem_u32(smem), b, sh.part, sh.poison, wc);
+            else fix_role<D, ALONE>(p, smem_u32(smem), b, sh.fix, sh.poison, wc);
         }
     }
     __syncwarp();
@@ -1174,10 +1217,10 @@ cudaError_t launch_dependent(void (*kern)(Args...), dim3 grid, int threads, int 
     return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
-template <int D, bool E4M3>
+template <int D, bool E4M3, bool ALONE>
 int launch_t(const PagedAttnParams& p, const PagedMaps& m, int shares, cudaStream_t stream) {
-    using C = Cfg<D, E4M3>;
-    auto kern = paged_chunk_kernel<D, E4M3>;
+    using C = Cfg<D, E4M3, ALONE>;
+    auto kern = paged_chunk_kernel<D, E4M3, ALONE>;
     static std::atomic<unsigned long long> ready{0};
     if (!once_a_device(ready, [&] {
             if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes) != cudaSuccess) return false;
@@ -1199,8 +1242,14 @@ int launch_t(const PagedAttnParams& p, const PagedMaps& m, int shares, cudaStrea
 }  // namespace
 
 int launch_paged_chunk(const PagedAttnParams& p, const PagedMaps& m, int shares, cudaStream_t stream) {
-    if (p.kv.d == 128) return p.kv.e4m3 ? launch_t<128, true>(p, m, shares, stream) : launch_t<128, false>(p, m, shares, stream);
-    return p.kv.e4m3 ? launch_t<64, true>(p, m, shares, stream) : launch_t<64, false>(p, m, shares, stream);
+    // (item_tokens: api.cu gave items one unit when no sequence has more than a unit's tokens)
+    const bool alone = p.item_tokens == p.unit_tokens;
+    if (p.kv.d == 128) {
+        if (p.kv.e4m3) return alone ? launch_t<128, true, true>(p, m, shares, stream) : launch_t<128, true, false>(p, m, shares, stream);
+        return alone ? launch_t<128, false, true>(p, m, shares, stream) : launch_t<128, false, false>(p, m, shares, stream);
+    }
+    if (p.kv.e4m3) return alone ? launch_t<64, true, true>(p, m, shares, stream) : launch_t<64, true, false>(p, m, shares, stream);
+    return alone ? launch_t<64, false, true>(p, m, shares, stream) : launch_t<64, false, false>(p, m, shares, stream);
 }
 
 }  // namespace ra
