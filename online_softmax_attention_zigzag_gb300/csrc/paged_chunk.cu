@@ -572,6 +572,14 @@ __device__ void fix_role(const PagedAttnParams& p, uint32_t smem, Bars& b, const
     }
 }
 
+// Two of a word's four bytes (the upper two if `upper`) as the low bytes of halves, each sign-extended.
+__device__ __forceinline__ uint32_t spread_signed(uint32_t w, bool upper) {
+    uint32_t a;
+    if (upper) asm("prmt.b32 %0, %1, 0, 0xb3a2;" : "=r"(a) : "r"(w));
+    else asm("prmt.b32 %0, %1, 0, 0x9180;" : "=r"(a) : "r"(w));
+    return a;
+}
+
 // e4m3: 256 threads, half a row each, expand every tile into its bf16 stage.
 template <int D, bool ALONE>
 __device__ void expand_role(const PagedAttnParams& p, uint32_t smem, Bars& b, const Part* parts, volatile int* poison,
@@ -604,8 +612,10 @@ __device__ void expand_role(const PagedAttnParams& p, uint32_t smem, Bars& b, co
             uint32_t y[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const uint32_t a = __byte_perm(w[i >> 1], 0, i & 1 ? 0x3424 : 0x1404);  // a code in each high byte
-                const uint32_t v = ((a >> 4) & 0x07f007f0u) | (a & 0x80008000u);
+                // a code in each low byte with its sign all over the byte above: 4 bits up, the sign and the
+                // rest are where bf16 has them (one operation less than moving them apart, of five: the
+                // chunk of 1024 tokens of 16k took 464 us, 416 now)
+                const uint32_t v = (spread_signed(w[i >> 1], i & 1) << 4) & 0x87f087f0u;
                 __nv_bfloat162 z = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&v), m1);
                 if (any_big) z = __hmul2(z, m2);
                 y[i] = *reinterpret_cast<const uint32_t*>(&z);
@@ -643,8 +653,6 @@ __device__ void expand_role(const PagedAttnParams& p, uint32_t smem, Bars& b, co
             const float k1 = ks, v1 = ahead == 1 ? vs1 : vs2;
             vs2 = vs1;
             vs1 = vs;
-            fetch();
-            look(t + 2);
             const uint32_t slot = st % C::kStages;
             if (!mbar_wait_w(&b.kv_empty[slot], ((st / C::kStages) & 1u) ^ 1u, wc)) return false;
             const uint32_t stage = smem + C::kKVOff + slot * C::kStageBytes;
@@ -660,6 +668,8 @@ __device__ void expand_role(const PagedAttnParams& p, uint32_t smem, Bars& b, co
                 }
                 if (!expand(stage, v1, zero)) return false;
             }
+            fetch();
+            look(t + 2);
             if (t < q.tb && !expand(stage + C::kTileBytes, k1, false)) return false;
             fence_async_shared();
             mbar_arrive(&b.kv_full[slot]);
