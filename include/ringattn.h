@@ -363,7 +363,7 @@ int ringattn_merge(float* o_run, float* lse_run, const float* o_part, const floa
  * page is dropped, and one that would come from it reads as zeros.
  * No two (sequence, position) pairs that one append writes may have the same page and row.
  * Requirements: d in {64, 128}; page_size a multiple of 16, at most 65536; batch at most
- * RINGATTN_PAGED_MAX_BATCH; max_pages * page_size at most 2^30; k and v 16-byte aligned and
+ * RINGATTN_PAGED_MAX_BATCH; max_pages * page_size and total at most 2^30; k and v 16-byte aligned and
  * their page strides multiples of 16 bytes, at least Hkv * page_size * d, at most 2^36; the
  * scales 16-byte aligned, their page strides multiples of 4, at least Hkv * page_size; the
  * other arrays 4-byte aligned; batch * (max_pages * page_size / 128 + 1) below 2^31.  total = 0 is valid: nothing to do.

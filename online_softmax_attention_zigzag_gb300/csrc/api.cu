@@ -7,6 +7,7 @@
 
 #include <nvtx3/nvToolsExt.h>
 
+#include <algorithm>
 #include <climits>
 #include <cstdint>
 #include <cstdlib>
@@ -709,7 +710,8 @@ int make_paged(const ra_paged_kv* a, ra::PagedKV* kv) {
     if (scaled != (a->k_scale != nullptr) || scaled != (a->v_scale != nullptr)) return RA_ERR_INVALID_ARG;
     if (a->d != 64 && a->d != 128) return RA_ERR_UNSUPPORTED;
     if (a->page_size % 16 != 0 || a->page_size > 65536 || a->batch > RINGATTN_PAGED_MAX_BATCH) return RA_ERR_UNSUPPORTED;
-    if (static_cast<long long>(a->max_pages) * a->page_size > (1LL << 30)) return RA_ERR_UNSUPPORTED;
+    // positions, and differences of two of them, are 32-bit numbers
+    if (static_cast<long long>(a->max_pages) * a->page_size > (1LL << 30) || a->total > (1 << 30)) return RA_ERR_UNSUPPORTED;
     const long long rows = static_cast<long long>(a->Hkv) * a->page_size;  // of one page
     if (rows > (1LL << 30)) return RA_ERR_UNSUPPORTED;
     const int unit = scaled ? 16 : 8;  // elements of 16 bytes
@@ -908,8 +910,8 @@ int ringattn_fwd_paged(const void* q, long long q_token_stride, long long q_head
     p.hq = Hq;
     p.max_q = max_q < p.kv.total ? max_q : p.kv.total;
     p.causal = causal;
-    p.window = window;
-    p.sinks = sinks;
+    p.window = std::min(window, 1 << 30);  // (no position is larger)
+    p.sinks = std::min(sinks, 1 << 30);
     p.out_f32 = out_f32;
     p.workspace = workspace;
     p.err = dev->err;

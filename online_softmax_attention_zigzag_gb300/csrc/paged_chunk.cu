@@ -350,11 +350,11 @@ __device__ __forceinline__ void for_each_part(const PagedAttnParams& p, F&& f) {
 
 // One warp walks the block's parts and lists them for the others, a few ahead: the walk's searches and
 // loads are then in nobody's way, and the registers that it takes in nobody's count.
-__device__ void list_role(const PagedAttnParams& p, Bars& b, Part* ring, const WaitCtl& wc) {
+__device__ void list_role(const PagedAttnParams& p, Bars& b, Part* ring, const volatile uint32_t* turn, const WaitCtl& wc) {
     uint32_t k = 0;
     bool ok = true;
     auto put = [&](const Part& q) {
-        ok = __all_sync(0xffffffffu, mbar_wait_idle(&b.part_empty[k % kParts], ((k / kParts) & 1u) ^ 1u, wc, 20000));
+        ok = __all_sync(0xffffffffu, mbar_wait_idle(&b.part_empty[k % kParts], ((k / kParts) & 1u) ^ 1u, wc, 20000, turn));
         if (!ok) return false;
         if ((threadIdx.x & 31) == 0) {
             ring[k % kParts] = q;
@@ -525,11 +525,11 @@ __device__ __forceinline__ uint32_t finite2(uint32_t y) {
 // longer than a tile's other work, and the product waited.)
 template <int D, bool ALONE>
 __device__ void fix_role(const PagedAttnParams& p, uint32_t smem, Bars& b, const volatile Fix* fix, volatile int* poison,
-                         const WaitCtl& wc) {
+                         const volatile uint32_t* turn, const WaitCtl& wc) {
     using C = Cfg<D, false, ALONE>;
     const int lane = threadIdx.x & 31, quarter = threadIdx.x / 32 - kExpandWarp;
     for (uint32_t nf = 0;; ++nf) {
-        if (!__all_sync(0xffffffffu, mbar_wait_idle(&b.fix_req[nf % kFixes], (nf / kFixes) & 1u, wc, 20000))) return;
+        if (!__all_sync(0xffffffffu, mbar_wait_idle(&b.fix_req[nf % kFixes], (nf / kFixes) & 1u, wc, 20000, turn))) return;
         const volatile Fix& f = fix[nf % kFixes];
         const int slot = f.slot, j0 = f.j0, hi = f.hi, first = f.first, k = f.k;
         if (slot < 0) return;
@@ -882,6 +882,58 @@ __device__ __noinline__ void add_sick(const PagedAttnParams& p, const Chunk& c, 
     }
 }
 
+// The tensor cores add to O with truncation, a step of up to 2^-23 of it for every 16 keys and always
+// towards zero, so a million keys in one sum lost 0.4 % (of equal weights and positive values).  So O is
+// moved to memory every kFold tiles of a part and added up there, rounded to nearest; 64k keys
+// lose less than 1e-4.  The place is the block's second partial result, which nothing else needs before the
+// part that ends there, thread x's row being its row x; it has the scale of the m beside it.
+constexpr int kFold = 512;
+__device__ __forceinline__ float fold_factor(float before, float m) { return before == m ? 1.f : ex2(before - m); }
+__device__ __forceinline__ PagedChunkPartial* fold_place(void* workspace) {
+    return static_cast<PagedChunkPartial*>(workspace) + 2 * blockIdx.x + 1;
+}
+template <int D>
+__device__ __noinline__ void fold_o(void* workspace, uint32_t o_tmem, float m, bool first) {
+    PagedChunkPartial* to = fold_place(workspace);
+    const int r2 = threadIdx.x;
+    const float f = first ? 0.f : fold_factor(to->m[r2], m);
+    to->m[r2] = m;
+#pragma unroll 1
+    for (int cc = 0; cc < D; cc += 32) {
+        uint32_t o[32];
+        tmem_ld32(o_tmem + cc, o);
+        tmem_wait_ld();
+        float4* at = to->o + (cc / 4) * (2 * kTile) + r2;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            float4 y = first ? make_float4(0.f, 0.f, 0.f, 0.f) : at[i * (2 * kTile)];
+            y.x = __fmaf_rn(y.x, f, __uint_as_float(o[4 * i]));
+            y.y = __fmaf_rn(y.y, f, __uint_as_float(o[4 * i + 1]));
+            y.z = __fmaf_rn(y.z, f, __uint_as_float(o[4 * i + 2]));
+            y.w = __fmaf_rn(y.w, f, __uint_as_float(o[4 * i + 3]));
+            at[i * (2 * kTile)] = y;
+        }
+#pragma unroll
+        for (int i = 0; i < 32; ++i) o[i] = 0u;
+        tmem_st32(o_tmem + cc, o);
+    }
+}
+
+__device__ __forceinline__ void unfold_o(void* workspace, int cc, float m, float (&o)[32]) {
+    const PagedChunkPartial* from = fold_place(workspace);
+    const int r2 = threadIdx.x;
+    const float f = fold_factor(from->m[r2], m);
+    const float4* at = from->o + (cc / 4) * (2 * kTile) + r2;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float4 y = at[i * (2 * kTile)];
+        o[4 * i] = __fmaf_rn(y.x, f, o[4 * i]);
+        o[4 * i + 1] = __fmaf_rn(y.y, f, o[4 * i + 1]);
+        o[4 * i + 2] = __fmaf_rn(y.z, f, o[4 * i + 2]);
+        o[4 * i + 3] = __fmaf_rn(y.w, f, o[4 * i + 3]);
+    }
+}
+
 template <int D, bool E4M3, bool ALONE>
 __device__ void softmax_role(const PagedAttnParams& p, int x, Bars& b, const Part* parts, uint32_t tmem,
                              const volatile int* poison, const WaitCtl& wc) {
@@ -983,19 +1035,26 @@ __device__ void softmax_role(const PagedAttnParams& p, int x, Bars& b, const Par
             }
             // O is stable here: the commit that signalled this S covered the previous P V (one unit alone:
             // only the one before it), and the next one waits for this tile's arrivals
-            if (__any_sync(0xffffffffu, need)) {
+            const bool fold = t > q.ta && (t - q.ta) % kFold == 0, rescale = __any_sync(0xffffffffu, need);
+            if (rescale || fold) {
                 if (ALONE) {  // tile t is the part's (t - ta)th; its predecessor's P V is use pvs + t - ta - 1
                     if (!wait(&b.pv_done, (pvs + (t - q.ta) - 1) & 1u)) return false;
                     tc_fence_after();
                 }
+                if (rescale) {
 #pragma unroll
-                for (int cc = 0; cc < D; cc += 32) {
-                    uint32_t o0[32];
-                    tmem_ld32(o_tmem + cc, o0);
-                    tmem_wait_ld();
+                    for (int cc = 0; cc < D; cc += 32) {
+                        uint32_t o0[32];
+                        tmem_ld32(o_tmem + cc, o0);
+                        tmem_wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) o0[i] = __float_as_uint(__uint_as_float(o0[i]) * f);
-                    tmem_st32(o_tmem + cc, o0);
+                        for (int i = 0; i < 32; ++i) o0[i] = __float_as_uint(__uint_as_float(o0[i]) * f);
+                        tmem_st32(o_tmem + cc, o0);
+                    }
+                }
+                if (fold) {
+                    tmem_wait_st();
+                    fold_o<D>(p.workspace, o_tmem, m, t - q.ta == kFold);
                 }
             }
             l += se[0] + se[1];
@@ -1030,6 +1089,7 @@ __device__ void softmax_role(const PagedAttnParams& p, int x, Bars& b, const Par
                 tc_fence_before();
                 mbar_arrive(&b.o_free[x]);
             }
+            if (q.tb - q.ta > kFold) unfold_o(p.workspace, cc, m, o);
             if (sick && live) {  // (copies, so that only this rare call keeps anything in memory)
                 const Chunk c = q.c;
                 float o2[32];
@@ -1149,10 +1209,10 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, ALONE>::kThreads, 1)
         } else if (warp == kLoadWarp) {
             load_role<D, E4M3, ALONE>(p, &tq, &tk, &tv, smem_u32(smem), b, sh.fix, sh.part, wc);
         } else if (warp == kListWarp) {
-            list_role(p, b, sh.part, wc);
+            list_role(p, b, sh.part, &sh.turn, wc);
         } else {
             if constexpr (E4M3) expand_role<D, ALONE>(p, smem_u32(smem), b, sh.part, sh.poison, wc);
-            else fix_role<D, ALONE>(p, smem_u32(smem), b, sh.fix, sh.poison, wc);
+            else fix_role<D, ALONE>(p, smem_u32(smem), b, sh.fix, sh.poison, &sh.turn, wc);
         }
     }
     __syncwarp();

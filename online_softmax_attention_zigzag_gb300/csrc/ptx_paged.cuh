@@ -83,9 +83,12 @@ __device__ __forceinline__ float lg2(float x) {
 }
 
 // As mbar_wait, for a waiter that is seldom needed: the thread is suspended for up to `hint_ns` at a
-// time, so that it takes no issue slots (and power) from the others meanwhile.
-__device__ __forceinline__ bool mbar_wait_idle(uint64_t* bar, uint32_t parity, const WaitCtl& w, uint32_t hint_ns) {
-    const uint64_t t0 = globaltimer_ns();
+// time, so that it takes no issue slots (and power) from the others meanwhile.  It may have nothing to do
+// for as long as the kernel runs, so its limit counts from the last change of `alive`, which others advance.
+__device__ __forceinline__ bool mbar_wait_idle(uint64_t* bar, uint32_t parity, const WaitCtl& w, uint32_t hint_ns,
+                                               const volatile uint32_t* alive) {
+    uint64_t t0 = globaltimer_ns();
+    uint32_t seen = *alive;
     while (true) {
         uint32_t ok;
         asm volatile(
@@ -96,8 +99,12 @@ __device__ __forceinline__ bool mbar_wait_idle(uint64_t* bar, uint32_t parity, c
         if (ok) return true;
         if (*w.abort_flag) return false;
         if (globaltimer_ns() - t0 > w.timeout_ns) {
-            raise_abort(w, bar);
-            return false;
+            if (*alive == seen) {
+                raise_abort(w, bar);
+                return false;
+            }
+            seen = *alive;
+            t0 = globaltimer_ns();
         }
     }
 }

@@ -1,5 +1,7 @@
 """The paged K/V cache on the GPU against the float64 oracle: ringattn_cache_append,
 ringattn_cache_read and ringattn_fwd_paged, through the C ABI."""
+import math
+
 import numpy as np
 import pytest
 import torch
@@ -509,3 +511,83 @@ def test_partial_results_merge(ra):
         ra.merge(o, l, o2, l2)
         assert ra.sync_status() == ra.RA_OK
         _check_all(B, q, o, l)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("n,L", [(3, 200), (60, 333), (60, 20), (3, 1)])
+def test_largest_window_and_sinks(ra, e4m3, n, L):
+    """A window (and sinks) of the type's largest value sees what no window sees, in rows before position 0 too."""
+    hq, hkv, d = 4, 2, 128
+    B = Batch([(n, L), (1, 300)], hkv=hkv, d=d, page=32, e4m3=e4m3, device=dev(), seed=71)
+    q = _randn((B.total, hq, d), 72, d ** -0.5).to(dev())
+    plain = _attend(ra, B, q, torch.float32)
+    for window, sinks in ((2 ** 31 - 1, 0), (2 ** 31 - 1, 2 ** 31 - 1), (1, 2 ** 31 - 1)):
+        o, l = _attend(ra, B, q, torch.float32, window=window, sinks=sinks)
+        assert ra.sync_status() == ra.RA_OK
+        assert torch.equal(o, plain[0]) and torch.equal(l, plain[1])
+
+
+def test_call_longer_than_the_wait_limit(ra):
+    """4.5e15 operations, more than two seconds at any rate this GPU has, over 2^30 keys (one page again and
+    again): warps that have nothing to look over all that while must not take it for a hang.
+    Scores are 0 and V is 0.5, so every sum is exact: out = 0.5, lse = log 2^30."""
+    n, d, page = 8192, 128, 65536
+    k = torch.randn((1, 1, page, d), device=dev()).to(torch.bfloat16)
+    v = torch.full((1, 1, page, d), 0.5, device=dev(), dtype=torch.bfloat16)
+    table = torch.zeros((1, 2 ** 30 // page), dtype=torch.int32, device=dev())
+    cu = torch.tensor([0, n], dtype=torch.int32, device=dev())
+    ln = torch.tensor([2 ** 30], dtype=torch.int32, device=dev())
+    q = torch.zeros((n, 1, d), dtype=torch.bfloat16, device=dev())
+    out, lse = torch.empty((n, 1, d), device=dev()), torch.empty((n, 1), device=dev())
+    ws = torch.empty(ra.paged_workspace_bytes(n, 1, 1, 1, d, n), dtype=torch.uint8, device=dev())
+    ra.fwd_paged(q, k, v, out, lse, table, cu, ln, ws, max_q=n, causal=0)
+    assert ra.sync_status() == ra.RA_OK
+    # (fp32: a few half steps of the quotient, and of a logarithm of 20.8)
+    assert (out - 0.5).abs().max().item() <= 4 * 2.0 ** -24
+    assert (lse - 30 * math.log(2)).abs().max().item() <= 4 * 2.0 ** -24 * 32
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_sums_over_a_million_keys(ra, e4m3):
+    """Equal weights and positive values over 2^20 keys (one page 16 times) in one block's hands.
+
+    The tensor cores may truncate: a step of 2^-23 of the sum so far for every 16 keys, so half that of the
+    whole sum on average.  Of 64k keys at a time that is 4096 / 2 steps; a few more for adding the 16
+    sums and for the quotient."""
+    n, L, d, page = 256 * torch.cuda.get_device_properties(0).multi_processor_count, 2 ** 20, 128, 65536
+    dt = torch.float8_e4m3fn if e4m3 else torch.bfloat16
+    g = torch.Generator(device=dev()).manual_seed(81)
+    v = (torch.rand((1, 1, page, d), device=dev(), generator=g) + 0.1).to(dt)
+    k = torch.randn((1, 1, page, d), device=dev(), generator=g).to(dt)
+    one = torch.ones((1, 1, page), device=dev()) if e4m3 else None
+    table = torch.zeros((1, L // page), dtype=torch.int32, device=dev())
+    cu = torch.tensor([0, n], dtype=torch.int32, device=dev())
+    ln = torch.tensor([L], dtype=torch.int32, device=dev())
+    q = torch.zeros((n, 1, d), dtype=torch.bfloat16, device=dev())
+    out, lse = torch.empty((n, 1, d), device=dev()), torch.empty((n, 1), device=dev())
+    ws = torch.empty(ra.paged_workspace_bytes(n, 1, 1, 1, d, n), dtype=torch.uint8, device=dev())
+    ra.fwd_paged(q, k, v, out, lse, table, cu, ln, ws, max_q=n, causal=0, k_scale=one, v_scale=one)
+    assert ra.sync_status() == ra.RA_OK
+    want = v.double().mean(2)[0, 0]
+    assert (out[:, 0].double() / want - 1).abs().max().item() <= (4096 / 2 + 32) * 2.0 ** -23
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("n", [20, 40])  # one unit of rows, and two
+def test_long_items_whose_maximum_grows(ra, e4m3, n):
+    """An item of 1040 tiles a block (the same pages for all), with scores that grow along the keys."""
+    hq, d, L, nb = 4, 128, 133000, torch.cuda.get_device_properties(0).multi_processor_count
+    B = Batch([(n, L)], hkv=1, d=d, page=512, e4m3=e4m3, device=dev(), seed=82, fill=False)
+    B.k[0] = (B.k[0].float() * (0.5 + 3.5 * torch.arange(L)[:, None, None] / L)).to(torch.bfloat16)
+    B.fill()
+    q = _randn((nb * n, hq, d), 83, d ** -0.5)
+    out, lse = torch.empty((nb * n, hq, d), device=dev()), torch.empty((nb * n, hq), device=dev())
+    cu = torch.arange(0, nb * n + 1, n, dtype=torch.int32, device=dev())
+    ws = torch.empty(ra.paged_workspace_bytes(nb * n, nb, hq, 1, d, n), dtype=torch.uint8, device=dev())
+    ra.fwd_paged(q.to(dev()), B.k_cache, B.v_cache, out, lse, B.dtable.expand(nb, -1).contiguous(), cu, B.dlen.expand(nb).contiguous(),
+                 ws, max_q=n, **B.kw())
+    assert ra.sync_status() == ra.RA_OK
+    for b in (0, nb - 1):
+        rows = slice(b * n, (b + 1) * n)
+        ref = opaged.attention(q[rows].double().numpy(), *B.kept(0))
+        check(out[rows], lse[rows], ref, d, False, f"sequence {b}")

@@ -133,6 +133,14 @@ def test_too_many_rows(ra):
     assert L.ringattn_fwd_paged(F, 512, 128, ctypes.byref(a), F, 512, 128, 0, F, 4, 1, 4, 1, 1, 0, 0, F, 1 << 40, 0) == -2
 
 
+def test_more_rows_than_positions(ra):
+    L, a = ra.lib(), _kv(ra, total=2 ** 30 + 1, Hkv=1)  # (one head: no other limit says no)
+    r = ctypes.byref(a)
+    assert L.ringattn_cache_append(F, F, 256, 128, 256, 128, r, 0) == -2
+    assert L.ringattn_cache_read(r, F, F, 0) == -2
+    assert L.ringattn_fwd_paged(F, 512, 128, r, F, 512, 128, 0, F, 1, 1, 1, 1, 1, 0, 0, F, 1 << 40, 0) == -2
+
+
 def test_read_refuses_outputs(ra):
     L, a = ra.lib(), _kv(ra)
     for k, v in ((0, F), (F, 0), (F + 4, F), (F, F + 8)):
