@@ -580,6 +580,11 @@ __device__ __forceinline__ uint32_t spread_signed(uint32_t w, bool upper) {
     return a;
 }
 
+__device__ __forceinline__ uint32_t times(uint32_t x, __nv_bfloat162 m) {
+    const __nv_bfloat162 z = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&x), m);
+    return *reinterpret_cast<const uint32_t*>(&z);
+}
+
 // e4m3: 256 threads, half a row each, expand every tile into its bf16 stage.
 template <int D, bool ALONE>
 __device__ void expand_role(const PagedAttnParams& p, uint32_t smem, Bars& b, const Part* parts, volatile int* poison,
@@ -600,8 +605,6 @@ __device__ void expand_role(const PagedAttnParams& p, uint32_t smem, Bars& b, co
         // (a scale that is no number is kept out of the product there)
         const bool big = scale > 128.f;
         const __nv_bfloat162 m1 = __float2bfloat162_rn(zero ? 0.f : big ? 0x1p120f : scale * 0x1p120f);
-        const __nv_bfloat162 m2 = __float2bfloat162_rn(big && !zero ? scale : 1.f);
-        const bool any_big = __any_sync(0xffffffffu, big);
         uint4 next = lds128(src + ((c0 ^ src_sw) << 4));
 #pragma unroll
         for (int i2 = 0; i2 < D / 32; ++i2) {
@@ -616,13 +619,21 @@ __device__ void expand_role(const PagedAttnParams& p, uint32_t smem, Bars& b, co
                 // rest are where bf16 has them (one operation less than moving them apart, of five: the
                 // chunk of 1024 tokens of 16k took 464 us, 416 now)
                 const uint32_t v = (spread_signed(w[i >> 1], i & 1) << 4) & 0x87f087f0u;
-                __nv_bfloat162 z = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&v), m1);
-                if (any_big) z = __hmul2(z, m2);
+                const __nv_bfloat162 z = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&v), m1);
                 y[i] = *reinterpret_cast<const uint32_t*>(&z);
             }
             const uint32_t d = dst + (c >> 2) * C::kBoxBytes + row_at;
             sts128(d + ((((2 * c) & 7) ^ sw) << 4), y[0], y[1], y[2], y[3]);
             sts128(d + ((((2 * c + 1) & 7) ^ sw) << 4), y[4], y[5], y[6], y[7]);
+        }
+        if (big && !zero) {  // (a pass of its own: a second factor for every pair cost 8 % of the whole kernel's time)
+            const __nv_bfloat162 m2 = __float2bfloat162_rn(scale);
+#pragma unroll 1
+            for (int c = 2 * c0; c < 2 * c0 + D / 16; ++c) {
+                const uint32_t d = dst + (c >> 3) * C::kBoxBytes + row_at + (((c & 7) ^ sw) << 4);
+                const uint4 x = lds128(d);
+                sts128(d, times(x.x, m2), times(x.y, m2), times(x.z, m2), times(x.w, m2));
+            }
         }
         // Only now, when every loaded code has been used: an arrival right behind the loads let the
         // next tile's copy overtake them (seen as wrong values in the chunks loaded last).
@@ -825,6 +836,24 @@ __device__ __forceinline__ uint32_t seen_bits(int hi, int lo, int sinks) {
     return low_bits(hi) & (~low_bits(lo) | low_bits(sinks));
 }
 
+// Hides what this row does not see of a tile: its scores from hi on, and those below lo that are not
+// below sinks.  In place, 32 columns at a time in a rolled loop and not inlined: it is rare, and as
+// straight code over 128 registers it ran at the speed of instruction fetches (9 us a tile).
+__device__ __noinline__ void mask_scores(uint32_t s_tmem, int hi, int lo, int sinks) {
+#pragma unroll 1
+    for (int cc = 0; cc < kTile; cc += 32) {
+        const uint32_t see = seen_bits(hi - cc, lo - cc, sinks - cc);
+        if (__all_sync(0xffffffffu, see == 0xffffffffu)) continue;
+        uint32_t r[32];
+        tmem_ld32(s_tmem + cc, r);
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 32; ++i) r[i] = (see & (1u << i)) ? r[i] : 0xff800000u;
+        tmem_st32(s_tmem + cc, r);
+    }
+    tmem_wait_st();
+}
+
 // Each lane has 64 bytes (w) for an address of its own (16-byte aligned).  Four neighbouring lanes
 // exchange 16-byte pieces first, so that one store instruction writes eight whole 64-byte runs and
 // not 32 pieces of 16 bytes in 32 lines.  `on`: whether the lane's bytes are wanted.
@@ -880,6 +909,22 @@ __device__ __noinline__ void add_sick(const PagedAttnParams& p, const Chunk& c, 
             }
         }
     }
+}
+
+// This row's O times f.  (Rolled and not inlined, as mask_scores: rare, and the less code the warps of all
+// roles run through, the fewer wait for instructions.)
+template <int D>
+__device__ __noinline__ void scale_o(uint32_t o_tmem, float f) {
+#pragma unroll 1
+    for (int cc = 0; cc < D; cc += 32) {
+        uint32_t o[32];
+        tmem_ld32(o_tmem + cc, o);
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+        tmem_st32(o_tmem + cc, o);
+    }
+    tmem_wait_st();
 }
 
 // The tensor cores add to O with truncation, a step of up to 2^-23 of it for every 16 keys and always
@@ -971,22 +1016,8 @@ __device__ void softmax_role(const PagedAttnParams& p, int x, Bars& b, const Par
             if (ALONE && y) ++sit[1];
             else ++sit[0];
             tc_fence_after();
-            // A tile that not every row of the unit sees whole is masked in place, 32 columns at a time
-            // in a rolled loop: it is rare, and as straight code over 128 registers it ran at the speed
-            // of instruction fetches (9 us a tile).
-            if (j0 + kTile > u_hi || (j0 < u_lo && j0 + kTile > p.sinks)) {
-#pragma unroll 1
-                for (int cc = 0; cc < kTile; cc += 32) {
-                    const uint32_t see = seen_bits(hi - j0 - cc, lo - j0 - cc, p.window > 0 ? p.sinks - j0 - cc : 0);
-                    uint32_t r[32];
-                    tmem_ld32(s_tmem + cc, r);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) r[i] = (see & (1u << i)) ? r[i] : 0xff800000u;
-                    tmem_st32(s_tmem + cc, r);
-                }
-                tmem_wait_st();
-            }
+            if (j0 + kTile > u_hi || (j0 < u_lo && j0 + kTile > p.sinks))  // not every row of the unit sees it whole
+                mask_scores(s_tmem, hi - j0, lo - j0, p.window > 0 ? p.sinks - j0 : 0);
             float s[kTile];
             float pm0, pm1, pm2, pm3;
             {
@@ -1041,21 +1072,8 @@ __device__ void softmax_role(const PagedAttnParams& p, int x, Bars& b, const Par
                     if (!wait(&b.pv_done, (pvs + (t - q.ta) - 1) & 1u)) return false;
                     tc_fence_after();
                 }
-                if (rescale) {
-#pragma unroll
-                    for (int cc = 0; cc < D; cc += 32) {
-                        uint32_t o0[32];
-                        tmem_ld32(o_tmem + cc, o0);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) o0[i] = __float_as_uint(__uint_as_float(o0[i]) * f);
-                        tmem_st32(o_tmem + cc, o0);
-                    }
-                }
-                if (fold) {
-                    tmem_wait_st();
-                    fold_o<D>(p.workspace, o_tmem, m, t - q.ta == kFold);
-                }
+                if (rescale) scale_o<D>(o_tmem, f);
+                if (fold) fold_o<D>(p.workspace, o_tmem, m, t - q.ta == kFold);
             }
             l += se[0] + se[1];
             lr += sr[0] + sr[1];
