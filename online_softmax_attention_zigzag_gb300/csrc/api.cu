@@ -913,6 +913,8 @@ int ringattn_fwd_paged(const void* q, long long q_token_stride, long long q_head
     p.window = std::min(window, 1 << 30);  // (no position is larger)
     p.sinks = std::min(sinks, 1 << 30);
     p.out_f32 = out_f32;
+    const long long es = out_f32 ? 4 : 2;
+    p.out_wide = ((reinterpret_cast<uintptr_t>(out) | out_token_stride * es | out_head_stride * es) & 31) == 0;
     p.workspace = workspace;
     p.err = dev->err;
     p.timeout_ns = wait_timeout_ns();

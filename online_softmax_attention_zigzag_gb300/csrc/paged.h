@@ -79,6 +79,7 @@ struct PagedAttnParams {
     float* lse;
     long long q_ts, q_hs, o_ts, o_hs, l_ts, l_hs;
     int hq, g, max_q, causal, window, sinks, out_f32;
+    bool out_wide;  // rows of out are 32-byte aligned
     // chunk kernel: tokens of a unit (128 / g) and of an item (one unit or two), most items of one
     // head, and where the list of items lies in the workspace (behind the partial results)
     int unit_tokens, item_tokens, max_pairs;

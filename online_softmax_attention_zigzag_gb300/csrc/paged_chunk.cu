@@ -43,7 +43,7 @@ namespace ra {
 namespace {
 
 constexpr int kTile = kPagedTile;
-constexpr int kMmaWarp = 8, kLoadWarp = 10, kListWarp = 11, kExpandWarp = 12;
+constexpr int kMmaWarp = 8, kLoadWarp = 10, kExpandWarp = 12;  // (11 lists)
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kRescaleLog2 = 8.0f;
@@ -55,9 +55,11 @@ constexpr int kPoison = 8;  // marks of the last parts, in turn: part k's holds 
 template <int D, bool E4M3, bool ALONE>
 struct Cfg {
     static constexpr int kThreads = E4M3 ? 640 : 512;
-    // registers: what the softmax warps take and what the others keep, of what all start with
-    static constexpr int kStartRegs = E4M3 ? 96 : 128, kSoftmaxRegs = 168, kOtherRegs = E4M3 ? 48 : 88;
-    static_assert(256 * kSoftmaxRegs + (kThreads - 256) * kOtherRegs <= kThreads * kStartRegs, "register split");
+    // registers: what the softmax warps take, what the next four keep and what those behind them (that
+    // expand or look over) do, of what all start with
+    static constexpr int kStartRegs = E4M3 ? 96 : 128, kSoftmaxRegs = 168, kOtherRegs = E4M3 ? 64 : 88,
+                         kExpandRegs = E4M3 ? 40 : 88;
+    static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs + (kThreads - 384) * kExpandRegs <= kThreads * kStartRegs, "register split");
     static constexpr int kTileBytes = kTile * D * 2;  // a bf16 tile
     static constexpr int kBoxBytes = kTile * 128;     // 64 columns of it
     static constexpr int kBoxes = D / 64;
@@ -854,31 +856,17 @@ __device__ __noinline__ void mask_scores(uint32_t s_tmem, int hi, int lo, int si
     tmem_wait_st();
 }
 
-// Each lane has 64 bytes (w) for an address of its own (16-byte aligned).  Four neighbouring lanes
-// exchange 16-byte pieces first, so that one store instruction writes eight whole 64-byte runs and
-// not 32 pieces of 16 bytes in 32 lines.  `on`: whether the lane's bytes are wanted.
-__device__ __forceinline__ void store_quads(void* dst, uint32_t (&w)[16], bool on) {
-    const int c = threadIdx.x & 3;
-    // 4 x 4 transposition of pieces among the four lanes: piece j of lane i to piece i of lane j
+// 64 bytes of a row (16-byte aligned; `wide`: 32-byte).  A lane has a row to itself: stores of 32 bytes fill
+// whole sectors of their lines without an exchange between lanes, which took longer than it saved.
+__device__ __forceinline__ void store_row(void* dst, const uint32_t (&w)[16], bool wide) {
+    if (wide) {
 #pragma unroll
-    for (int step = 1; step < 4; step *= 2)
+        for (int i = 0; i < 16; i += 8)
+            stg256(static_cast<uint32_t*>(dst) + i, w[i], w[i + 1], w[i + 2], w[i + 3], w[i + 4], w[i + 5], w[i + 6], w[i + 7]);
+    } else {
 #pragma unroll
-        for (int a = 0; a < 4; ++a)
-            if (!(a & step)) {
-                const bool up = (c & step) != 0;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const uint32_t give = up ? w[4 * a + e] : w[4 * (a | step) + e];
-                    const uint32_t got = __shfl_xor_sync(0xffffffffu, give, step);
-                    if (up) w[4 * a + e] = got;
-                    else w[4 * (a | step) + e] = got;
-                }
-            }
-    const unsigned long long mine = on ? reinterpret_cast<unsigned long long>(dst) : 0ull;
-#pragma unroll
-    for (int a = 0; a < 4; ++a) {  // now piece a is this lane's quarter of lane a's bytes
-        const unsigned long long at = __shfl_sync(0xffffffffu, mine, (threadIdx.x & 28) + a);
-        if (at) *(reinterpret_cast<uint4*>(at) + c) = make_uint4(w[4 * a], w[4 * a + 1], w[4 * a + 2], w[4 * a + 3]);
+        for (int i = 0; i < 16; i += 4)
+            *reinterpret_cast<uint4*>(static_cast<uint32_t*>(dst) + i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
     }
 }
 
@@ -1092,7 +1080,27 @@ __device__ void softmax_role(const PagedAttnParams& p, int x, Bars& b, const Par
         const int tok = q.c.s.q0 + t_row, head = q.h * p.g + row - tok_in * p.g;
         PagedChunkPartial* part = static_cast<PagedChunkPartial*>(p.workspace) + 2 * blockIdx.x + q.slot;
         const int r2 = x * kTile + row;
-        // (rolled, as the mask: a quarter of the code to fetch once an item)
+        if (!cut && !sick && !p.out_f32 && q.tb - q.ta <= kFold) {  // the usual end, with all loads in flight at once
+            uint32_t o[D / 32][32];
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) tmem_ld32(o_tmem + c * 32, o[c]);
+            tmem_wait_ld();
+            tc_fence_before();
+            mbar_arrive(&b.o_free[x]);
+            if (live) {
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t w[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        w[i] = pack_bf16x2(__uint_as_float(o[c][2 * i]) * inv, __uint_as_float(o[c][2 * i + 1]) * inv);
+                    store_row(static_cast<uint16_t*>(p.out) + tok * p.o_ts + head * p.o_hs + c * 32, w, p.out_wide);
+                }
+                p.lse[tok * p.l_ts + head * p.l_hs] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+            }
+            return true;
+        }
+        // (rolled, as the mask: a quarter of the code to fetch)
 #pragma unroll 1
         for (int cc = 0; cc < D; cc += 32) {
             float o[32];
@@ -1130,13 +1138,13 @@ __device__ void softmax_role(const PagedAttnParams& p, int x, Bars& b, const Par
                         uint32_t w[16];
 #pragma unroll
                         for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(o[16 * h2 + i] * inv);
-                        store_quads(dst + 16 * h2, w, live);
+                        if (live) store_row(dst + 16 * h2, w, p.out_wide);
                     }
                 } else {
                     uint32_t w[16];
 #pragma unroll
                     for (int i = 0; i < 16; ++i) w[i] = pack_bf16x2(o[2 * i] * inv, o[2 * i + 1] * inv);
-                    store_quads(static_cast<uint16_t*>(p.out) + tok * p.o_ts + head * p.o_hs + cc, w, live);
+                    if (live) store_row(static_cast<uint16_t*>(p.out) + tok * p.o_ts + head * p.o_hs + cc, w, p.out_wide);
                 }
             }
         }
@@ -1219,6 +1227,10 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, ALONE>::kThreads, 1)
     if (warp < 8) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSoftmaxRegs));
         if (!ALONE || warp < 4) softmax_role<D, E4M3, ALONE>(p, warp / 4, b, sh.part, tmem, sh.poison, wc);
+    } else if (warp >= kExpandWarp) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kExpandRegs));
+        if constexpr (E4M3) expand_role<D, ALONE>(p, smem_u32(smem), b, sh.part, sh.poison, wc);
+        else fix_role<D, ALONE>(p, smem_u32(smem), b, sh.fix, sh.poison, &sh.turn, wc);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
         if (warp == kMmaWarp || warp == kMmaWarp + 1) {
@@ -1226,11 +1238,8 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, ALONE>::kThreads, 1)
                 mma_role<D, E4M3, ALONE>(p, warp - kMmaWarp, smem_u32(smem), b, sh.part, tmem, &sh.turn, wc);
         } else if (warp == kLoadWarp) {
             load_role<D, E4M3, ALONE>(p, &tq, &tk, &tv, smem_u32(smem), b, sh.fix, sh.part, wc);
-        } else if (warp == kListWarp) {
-            list_role(p, b, sh.part, &sh.turn, wc);
         } else {
-            if constexpr (E4M3) expand_role<D, ALONE>(p, smem_u32(smem), b, sh.part, sh.poison, wc);
-            else fix_role<D, ALONE>(p, smem_u32(smem), b, sh.fix, sh.poison, &sh.turn, wc);
+            list_role(p, b, sh.part, &sh.turn, wc);
         }
     }
     __syncwarp();

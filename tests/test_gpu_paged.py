@@ -591,3 +591,23 @@ def test_long_items_whose_maximum_grows(ra, e4m3, n):
         rows = slice(b * n, (b + 1) * n)
         ref = opaged.attention(q[rows].double().numpy(), *B.kept(0))
         check(out[rows], lse[rows], ref, d, False, f"sequence {b}")
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("d", [64, 128])
+def test_outputs_on_16_byte_boundaries(ra, e4m3, out_dtype, d):
+    """out rows that are 16-byte and not 32-byte aligned, in one unit of rows and in two; what lies between them stays."""
+    hq, hkv, gap, step = 4, 1, 8, 16 // out_dtype.itemsize  # (strides are multiples of 8 elements in both types)
+    for n in (25, 70):
+        B = Batch([(n, 300), (3, 90)], hkv=hkv, d=d, page=16, e4m3=e4m3, device=dev(), seed=91)
+        q = _randn((B.total, hq, d), 92, d ** -0.5).to(dev())
+        buf = torch.full((B.total * hq * (d + gap) + step,), float("nan"), dtype=out_dtype, device=dev())
+        out = buf[step:].view(B.total, hq, d + gap)[:, :, :d]
+        assert out.data_ptr() % 32 == 16
+        lse = torch.full((B.total, hq), float("nan"), device=dev())
+        ws = torch.empty(ra.paged_workspace_bytes(B.total, 2, hq, hkv, d, n), dtype=torch.uint8, device=dev())
+        ra.fwd_paged(q, B.k_cache, B.v_cache, out, lse, *B.args(), ws, max_q=n, **B.kw())
+        assert ra.sync_status() == ra.RA_OK
+        _check_all(B, q, out, lse)
+        assert torch.isnan(buf[step:].view(B.total, hq, d + gap)[:, :, d:]).all() and torch.isnan(buf[:step]).all()
