@@ -65,8 +65,13 @@ struct Cfg {
     static constexpr int kScaleBytes = 1024;  // of a slot: boxes start 128 bytes apart at least, as TMA wants
     static constexpr int kScaleOff = kSlots * kSlotBytes;
     static constexpr int kOOff = kScaleOff + (E4M3 ? kSlots * kScaleBytes : 0);
-    static constexpr int kMlOff = kOOff + kWarps * 8 * kOStride * 4;  // m, ms, l of every warp and row
-    static constexpr int kPreOff = kMlOff + 3 * kWarps * kRows * 4;
+    // Groups of warps end a part at different times: they go on with the next one and join this one behind their
+    // first tile of that (4096-key windows of 192 sequences in 8 bits: 301 us without, 280 with).
+    // One group ends together, and for 16 rows there are no registers (two tokens of 8 heads: 123 us, 143 with).
+    static constexpr bool kLater = kGroups > 1 && NT == 1;
+    // the warps' results meet in a buffer of 8 rows a warp, rows 0-7 and then rows 8-15
+    static constexpr int kMlOff = kOOff + kWarps * 8 * kOStride * 4;  // m, ms, l of every warp and row; bad values
+    static constexpr int kPreOff = kMlOff + (3 * kWarps * kRows + kWarps) * 4;
     static constexpr int kFixedBytes = kPreOff + 1024;  // and 4 * (batch + 1) for the shares
 };
 
@@ -253,9 +258,92 @@ __device__ __forceinline__ float bf16_add_nonfinite(float acc, uint16_t bits) {
     return (bits & 0x7f80u) == 0x7f80u ? acc + __uint_as_float(static_cast<uint32_t>(bits) << 16) : acc;
 }
 
+// Joins the warps' results for part q: warp w row 8 round + w of the pair.  Into the outputs, or, if others have tiles of the pair too, into the workspace.
 template <int D, bool E4M3, int NT>
-__device__ void compute_role(const PagedAttnParams& p, uint8_t* smem, uint64_t* full, uint64_t* empty, const int* pre,
-                             long long w0, long long w1, const WaitCtl& wc) {
+__device__ __forceinline__ void join_rows(const PagedAttnParams& p, const uint8_t* smem, Part q, int slot, int round) {
+    using C = Cfg<D, E4M3, NT>;
+    constexpr int kWarps = C::kWarps;
+    const PagedKV& kv = p.kv;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+    const float* so = reinterpret_cast<const float*>(smem + C::kOOff);
+    const float* sm = reinterpret_cast<const float*>(smem + C::kMlOff);
+    const float* sms = sm + kWarps * kRows;
+    const float* sl = sms + kWarps * kRows;
+    const int* sbad = reinterpret_cast<const int*>(sl + kWarps * kRows);
+    const PagedSeq s = paged_seq(kv, q.b);
+    const int T = min(s.T, p.max_q), R = T * p.g;
+    const bool cut = q.ta > 0 || q.tb < q.n;
+    PagedPartial* part = static_cast<PagedPartial*>(p.workspace) + slot;
+    if (cut && warp == 0 && lane == 0) {
+        part->b = q.b;
+        part->h = q.h;
+        part->begins = q.ta == 0;
+    }
+    static_assert(kWarps == 8, "a row a warp");
+    const int r = warp + 8 * round;
+    if (r < R) {
+        float M = -INFINITY, Ms = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            M = fmaxf(M, sm[w * kRows + r]);
+            Ms = fmaxf(Ms, sms[w * kRows + r]);
+        }
+        float f[kWarps], L = 0.f;
+        bool any_bad = false;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            f[w] = paged_weight(sm[w * kRows + r], M);
+            L = paged_add_weighted(L, paged_weight(sms[w * kRows + r], Ms), sl[w * kRows + r]);
+            any_bad |= sbad[w] != 0;
+        }
+        const int t = r / p.g, head = q.h * p.g + r - t * p.g, tok = s.q0 + t;
+        for (int d = 4 * lane; d < D; d += 128) {
+            float acc[4] = {};
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                const float4 v = *reinterpret_cast<const float4*>(so + (w * 8 + warp) * C::kOStride + d);
+                acc[0] = fmaf(f[w], v.x, acc[0]);
+                acc[1] = fmaf(f[w], v.y, acc[1]);
+                acc[2] = fmaf(f[w], v.z, acc[2]);
+                acc[3] = fmaf(f[w], v.w, acc[3]);
+            }
+            if (!E4M3 && any_bad) {  // values that are no numbers, of the keys this row sees
+                const Tiles kt = key_tiles(p, s);
+                const int see_lo = s.base + T - p.window;
+                const int i = s.base + t, rhi = p.causal ? i + 1 : s.L, rlo = p.window > 0 ? i - p.window + 1 : 0;
+                for (int tt = q.ta; tt < q.tb; ++tt) {
+                    const int j0 = (tt < kt.ns ? tt : kt.lo + tt - kt.ns) * kTile;
+                    if (j0 + kTile <= (p.causal ? s.base + 1 : s.L) && (p.window == 0 || j0 >= see_lo || j0 + kTile <= p.sinks))
+                        continue;  // its values went into the product as they are
+                    for (int j = j0; j < min(j0 + kTile, rhi); ++j) {
+                        if (p.window > 0 && j < rlo && j >= p.sinks) continue;
+                        int in;
+                        const int pg = paged_page(kv, q.b, j, in);
+                        if (pg < 0) continue;
+                        const uint16_t* v = static_cast<const uint16_t*>(kv.v) + pg * kv.v_ps + (static_cast<long long>(q.h) * kv.page + in) * D + d;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) acc[e] = bf16_add_nonfinite(acc[e], v[e]);
+                    }
+                }
+            }
+            if (cut) *reinterpret_cast<float4*>(&part->o[r * kPagedMaxD + d]) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+            else paged_store4(p, tok, head, d, acc, out_factor<E4M3>(M, Ms, L));
+        }
+        if (lane == 0) {
+            if (cut) {
+                part->m[r] = M;
+                part->ms[r] = Ms;
+                part->l[r] = L;
+            } else {
+                p.lse[tok * p.l_ts + head * p.l_hs] = L == 0.f ? -INFINITY : (Ms + log2f(L)) * kLn2;
+            }
+        }
+    }
+}
+
+template <int D, bool E4M3, int NT>
+__device__ void compute_role(const PagedAttnParams& p, uint8_t* smem, uint64_t* full, uint64_t* empty, uint64_t* ready,
+                             uint64_t* freed, const int* pre, long long w0, long long w1, const WaitCtl& wc) {
     using C = Cfg<D, E4M3, NT>;
     constexpr int kWarps = C::kWarps, NB = C::kKeys / 16;
     const PagedKV& kv = p.kv;
@@ -265,14 +353,31 @@ __device__ void compute_role(const PagedAttnParams& p, uint8_t* smem, uint64_t* 
     float* sm = reinterpret_cast<float*>(smem + C::kMlOff);
     float* sms = sm + kWarps * kRows;
     float* sl = sms + kWarps * kRows;
+    int* sbad = reinterpret_cast<int*>(sl + kWarps * kRows);
     const int grp = warp / C::kGroupWarps, key0 = (warp % C::kGroupWarps) * C::kKeys;  // this warp's keys of a tile
     // its scales in a slot: 16 keys lie 16 floats apart (boxes of 16 rows 32, 128 bytes)
     const int step16 = p.box_rows == 16 ? 32 : 16;
     const float* scales = reinterpret_cast<const float*>(smem + C::kScaleOff) + step16 * (key0 / 16) + r8;
-    PagedPartial* parts = static_cast<PagedPartial*>(p.workspace);
     uint32_t tiles = 0;  // of the parts before
     bool ok = true;
-    int first = 1;
+    uint32_t sets = 0;   // kLater: results that this warp has put into the buffer
+    Part due = {};       // kLater: the part that the last of them is of, if it has not been joined yet (n > 0)
+    int place = 2 * blockIdx.x;  // for a part that is cut: the first one's, then the others'
+    // Waits for the other warps' results of part q and joins this warp's rows of them.
+    auto join = [&](const Part& q, int round) -> bool {
+        // (not later: a warp that gave up still comes here, so that none waits for it)
+        if (C::kLater ? !__all_sync(0xffffffffu, mbar_wait(ready, (sets - 1) & 1u, wc)) : !named_bar_and(kBar, kWarps * 32, ok))
+            return false;
+        join_rows<D, E4M3, NT>(p, smem, q, place, round);
+        if (round == NT - 1) place = 2 * blockIdx.x + 1;
+        if (C::kLater) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(freed);
+        } else {
+            named_bar_sync(kBar, kWarps * 32);  // the buffer is free again
+        }
+        return true;
+    };
     for_each_part(p, pre, w0, w1, [&](const Part& q) -> bool {
         const PagedSeq s = paged_seq(kv, q.b);
         const Tiles kt = key_tiles(p, s);
@@ -339,7 +444,14 @@ __device__ void compute_role(const PagedAttnParams& p, uint8_t* smem, uint64_t* 
             }
         bool bad_v = false;  // a value that is no number, in a tile that not every row sees whole
         const int see_lo = s.base + T - p.window;  // the window of the last row begins here
-        for (int t = q.ta + (grp + C::kGroups - tiles % C::kGroups) % C::kGroups; t < q.tb; t += C::kGroups) {
+        bool one = false;  // a tile of this part is done
+        for (int t = q.ta + (grp + C::kGroups - tiles % C::kGroups) % C::kGroups;; t += C::kGroups) {
+            if (C::kLater && due.n > 0 && (one || t >= q.tb)) {
+                if (!(ok = join(due, 0))) break;
+                due.n = 0;
+            }
+            if (t >= q.tb) break;
+            one = true;
             const int j0 = (t < kt.ns ? t : kt.lo + t - kt.ns) * kTile;
             uint32_t it = 2 * (tiles + t - q.ta);  // the ring's number of this K tile; V is the next
             // does every row see every key of the tile?
@@ -568,10 +680,8 @@ __device__ void compute_role(const PagedAttnParams& p, uint8_t* smem, uint64_t* 
             if (lane == 0) mbar_arrive(&empty[slot]);
         }
         tiles += q.tb - q.ta;
-        // ---- the warps' results meet: rows 0-7, then rows 8-15
-        const bool cut = q.ta > 0 || q.tb < q.n;
-        const int slot_i = 2 * blockIdx.x + (first ? 0 : 1);
-        PagedPartial* part = parts + slot_i;
+        if (C::kLater && !ok) return false;
+        // ---- the warp's results into the buffer, once nobody reads the ones before any more
 #pragma unroll
         for (int x = 0; x < NT; ++x)
 #pragma unroll
@@ -588,12 +698,20 @@ __device__ void compute_role(const PagedAttnParams& p, uint8_t* smem, uint64_t* 
                 l[x][e] += __shfl_xor_sync(0xffffffffu, l[x][e], 4);
                 l[x][e] += __shfl_xor_sync(0xffffffffu, l[x][e], 8);
                 l[x][e] += __shfl_xor_sync(0xffffffffu, l[x][e], 16);
+                if (C::kLater && x == 0 && e == 0 && sets > 0) {
+                    ok = __all_sync(0xffffffffu, mbar_wait(freed, (sets - 1) & 1u, wc));
+                    if (!ok) break;
+                }
                 if (r8 == 0) {
                     sm[warp * kRows + 8 * x + 2 * c4 + e] = m[x][e];
                     sms[warp * kRows + 8 * x + 2 * c4 + e] = ms[x][e];
                     sl[warp * kRows + 8 * x + 2 * c4 + e] = l[x][e];
                 }
             }
+        if (C::kLater && !ok) return false;
+        if (lane == 0) sbad[warp] = 0;
+        __syncwarp();
+        if (bad_v) sbad[warp] = 1;
 #pragma unroll
         for (int x = 0; x < NT; ++x) {
             float* dst = so + (warp * 8 + 2 * c4) * C::kOStride;
@@ -608,80 +726,18 @@ __device__ void compute_role(const PagedAttnParams& p, uint8_t* smem, uint64_t* 
                         dst[e * C::kOStride + 16 * i + 8 + r8] = o[i][x][2 + e];
                     }
                 }
-            // (a warp that gave up still comes here, so that none waits for it)
-            ok = named_bar_and(kBar, kWarps * 32, ok);
-            const bool any_bad = !named_bar_and(kBar, kWarps * 32, !bad_v);
-            if (!ok) return false;
-            const int row8 = warp, r = row8 + 8 * x;
-            if (row8 < 8 && r < R) {
-                float M = -INFINITY, Ms = -INFINITY;
-#pragma unroll
-                for (int w = 0; w < kWarps; ++w) {
-                    M = fmaxf(M, sm[w * kRows + r]);
-                    Ms = fmaxf(Ms, sms[w * kRows + r]);
-                }
-                float f[kWarps], L = 0.f;
-#pragma unroll
-                for (int w = 0; w < kWarps; ++w) {
-                    f[w] = paged_weight(sm[w * kRows + r], M);
-                    L = paged_add_weighted(L, paged_weight(sms[w * kRows + r], Ms), sl[w * kRows + r]);
-                }
-                const int t = r / p.g, head = q.h * p.g + r - t * p.g, tok = s.q0 + t;
-                for (int d = 4 * lane; d < D; d += 128) {
-                    float acc[4] = {};
-#pragma unroll
-                    for (int w = 0; w < kWarps; ++w) {
-                        const float4 v = *reinterpret_cast<const float4*>(so + (w * 8 + row8) * C::kOStride + d);
-                        acc[0] = fmaf(f[w], v.x, acc[0]);
-                        acc[1] = fmaf(f[w], v.y, acc[1]);
-                        acc[2] = fmaf(f[w], v.z, acc[2]);
-                        acc[3] = fmaf(f[w], v.w, acc[3]);
-                    }
-                    if (!E4M3 && any_bad) {  // values that are no numbers, of the keys this row sees
-                        const int i = s.base + t, rhi = p.causal ? i + 1 : s.L, rlo = p.window > 0 ? i - p.window + 1 : 0;
-                        for (int tt = q.ta; tt < q.tb; ++tt) {
-                            const int j0 = (tt < kt.ns ? tt : kt.lo + tt - kt.ns) * kTile;
-                            if (j0 + kTile <= (p.causal ? s.base + 1 : s.L) && (p.window == 0 || j0 >= see_lo || j0 + kTile <= p.sinks))
-                                continue;  // its values went into the product as they are
-                            for (int j = j0; j < min(j0 + kTile, rhi); ++j) {
-                                if (p.window > 0 && j < rlo && j >= p.sinks) continue;
-                                int row;
-                                const int pg = paged_page(kv, q.b, j, row);
-                                if (pg < 0) continue;
-                                const uint16_t* v = static_cast<const uint16_t*>(kv.v) + pg * kv.v_ps + (static_cast<long long>(q.h) * kv.page + row) * D + d;
-#pragma unroll
-                                for (int e = 0; e < 4; ++e) acc[e] = bf16_add_nonfinite(acc[e], v[e]);
-                            }
-                        }
-                    }
-                    if (cut) {
-                        *reinterpret_cast<float4*>(&part->o[r * kPagedMaxD + d]) = make_float4(acc[0], acc[1], acc[2], acc[3]);
-                    } else {
-                        paged_store4(p, tok, head, d, acc, out_factor<E4M3>(M, Ms, L));
-                    }
-                }
-                if (lane == 0) {
-                    if (cut) {
-                        part->m[r] = M;
-                        part->ms[r] = Ms;
-                        part->l[r] = L;
-                    } else {
-                        p.lse[tok * p.l_ts + head * p.l_hs] = L == 0.f ? -INFINITY : (Ms + log2f(L)) * kLn2;
-                    }
-                }
-            }
-            named_bar_sync(kBar, kWarps * 32);  // the buffers are free again
-        }
-        if (threadIdx.x == 0) {
-            if (cut) {
-                part->b = q.b;
-                part->h = q.h;
-                part->begins = q.ta == 0;
+            if (C::kLater) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(ready);
+                ++sets;
+            } else if (!(ok = join(q, x))) {
+                return false;
             }
         }
-        first = 0;
+        if (C::kLater) due = q;
         return true;
     });
+    if (C::kLater && ok && due.n > 0) join(due, 0);
 }
 
 template <int D, bool E4M3, int NT>
@@ -694,6 +750,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, NT>::kThreads, 1)
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     __shared__ __align__(8) uint64_t full[C::kSlots];
     __shared__ __align__(8) uint64_t empty[C::kSlots];
+    __shared__ __align__(8) uint64_t ready, freed;  // the warps' results: all in the buffer, all joined
     __shared__ int scratch[C::kThreads / 32];
     __shared__ int abort_flag;
     int* pre = reinterpret_cast<int*>(smem + C::kPreOff);
@@ -703,6 +760,8 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, NT>::kThreads, 1)
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], C::kGroupWarps);
         }
+        mbar_init(&ready, C::kWarps);
+        mbar_init(&freed, C::kWarps);
         abort_flag = 0;
         fence_mbar_init();
     }
@@ -717,7 +776,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, NT>::kThreads, 1)
     if (threadIdx.x / 32 == C::kWarps)
         load_role<D, E4M3, NT>(p, &tk, &tv, &tks, &tvs, smem_u32(smem), smem_u32(smem) + C::kScaleOff, full, empty, pre, w0, w1, wc);
     else
-        compute_role<D, E4M3, NT>(p, smem, full, empty, pre, w0, w1, wc);
+        compute_role<D, E4M3, NT>(p, smem, full, empty, &ready, &freed, pre, w0, w1, wc);
 }
 
 // Joins the parts of pairs that were cut.  Block (x, r): if a pair begins in block x of the first
