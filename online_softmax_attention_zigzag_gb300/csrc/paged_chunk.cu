@@ -251,7 +251,13 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const __grid_c
         if (__syncthreads_or(load + more > each)) break;
         load += more;
     }
-    const long long cap = x < grid ? each + (x < W % grid ? 1 : 0) - load : 0;
+    // A few items in all blocks: a tile less for each block is a part more for the join, which reads an item's
+    // parts one after the other, a quarter of a tile's time each.  Shares of s tiles of T cost
+    // s + T / (4 s), least where s = sqrt(T / 4).  (2 items of 118 tiles: 57 us in equal shares, 38 so;
+    // one of 470: 77 us and 65.)
+    const long long least = N > 0 ? static_cast<long long>(sqrtf(static_cast<float>(W / N) * 0.25f)) : 0;
+    long long cap = 0;
+    if (x < grid) cap = each >= least ? each + (x < W % grid ? 1 : 0) - load : max(0ll, min(least, W - least * x));
     const long long at = block_scan(cap, scratch, all);
     if (x < grid) plan.fill[x] = at;
     if (x == 0) {
@@ -1250,13 +1256,17 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, ALONE>::kThreads, 1)
 }
 
 // Joins the parts of items that were cut: block (x, y) takes rows [8 y, 8 y + 8) of the item that
-// begins in block x of the first kernel and goes on in the next ones, a thread 4 columns of a row.
+// begins in block x of the first kernel and goes on in the next ones, a thread 4 columns of a row.  The
+// weights of all parts come first, the threads side by side: an item may lie in all blocks, and
+// with one look at a part after the other its 76 parts took 40 us, 20 so.
 constexpr int kJoinRows = 8;
 template <int D>
 __global__ void __launch_bounds__(kJoinRows * D / 4) paged_chunk_join_kernel(const __grid_constant__ PagedAttnParams p, int shares) {
+    constexpr int kThreads = kJoinRows * D / 4, kLanes = kThreads / kJoinRows, kWarps = kThreads / 32;
+    __shared__ float weight[kPagedMaxShares][kJoinRows], red[kWarps][kJoinRows];
     wait_primary();
     const PagedChunkPartial* parts = static_cast<const PagedChunkPartial*>(p.workspace);
-    const int x = blockIdx.x, lane = threadIdx.x & 31;
+    const int x = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x / 32;
     const PagedChunkPartial* p0 = parts + 2 * x + (parts[2 * x + 1].b >= 0 ? 1 : 0);
     const int b = p0->b, pair = p0->pair, h = p0->h;
     if (b < 0 || !p0->begins) return;
@@ -1270,22 +1280,29 @@ __global__ void __launch_bounds__(kJoinRows * D / 4) paged_chunk_join_kernel(con
         n += v == 0xffffffffu ? 32 : __ffs(~v) - 1;
         if (v != 0xffffffffu) break;
     }
-    const int r = blockIdx.y * kJoinRows + threadIdx.x % kJoinRows;  // row of the two units
-    const int col = threadIdx.x / kJoinRows;                         // group of 4 columns
-    const int unit = r / kTile, ru = r - unit * kTile, t = c.ta + unit * p.unit_tokens + ru / p.g;
-    if (ru >= p.unit_tokens * p.g || t >= c.tb) return;
+    const int r0 = blockIdx.y * kJoinRows, row8 = threadIdx.x % kJoinRows, r = r0 + row8;  // row of the two units
+    const int col = threadIdx.x / kJoinRows;                                               // group of 4 columns
+    const int unit = r0 / kTile, ru = r - unit * kTile, rows = p.unit_tokens * p.g;
+    if (r0 - unit * kTile >= rows || c.ta + unit * p.unit_tokens + (r0 - unit * kTile) / p.g >= c.tb) return;
+    auto part = [&](int k) { return k ? parts + 2 * (x + k) : p0; };
     float M = -INFINITY;
-#pragma unroll 4
-    for (int k = 0; k < n; ++k) {
-        const PagedChunkPartial* q = k ? parts + 2 * (x + k) : p0;
-        if (q->b >= 0) M = fmaxf(M, q->m[r]);
+    for (int k = col; k < n; k += kLanes) {
+        const float m = part(k)->b >= 0 ? part(k)->m[r] : NAN;  // (a block without a filling left nothing)
+        weight[k][row8] = m;
+        M = fmaxf(M, m);
     }
+    M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, 8));
+    M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, 16));
+    if (lane < kJoinRows) red[warp][lane] = M;
+    __syncthreads();
+    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, red[w][row8]);
     float l = 0.f, lr = 0.f, acc[4] = {};
-#pragma unroll 4
+#pragma unroll 8
     for (int k = 0; k < n; ++k) {
-        const PagedChunkPartial* q = k ? parts + 2 * (x + k) : p0;
-        if (q->b < 0) continue;
-        const float f = paged_weight(q->m[r], M);
+        const float m = weight[k][row8];
+        if (m != m) continue;
+        const PagedChunkPartial* q = part(k);
+        const float f = paged_weight(m, M);
         const float4 v = q->o[col * (2 * kTile) + r];
         l = paged_add_weighted(l, f, q->l[r]);
         lr = paged_add_weighted(lr, f, q->lr[r]);
@@ -1294,6 +1311,8 @@ __global__ void __launch_bounds__(kJoinRows * D / 4) paged_chunk_join_kernel(con
         acc[2] = paged_add_weighted(acc[2], f, v.z);
         acc[3] = paged_add_weighted(acc[3], f, v.w);
     }
+    const int t = c.ta + unit * p.unit_tokens + ru / p.g;
+    if (ru >= rows || t >= c.tb) return;
     const int tok = c.s.q0 + t, head = h * p.g + ru % p.g;
     paged_store4(p, tok, head, 4 * col, acc, lr == 0.f ? 0.f : 1.f / lr);
     if (col == 0) p.lse[tok * p.l_ts + head * p.l_hs] = l == 0.f ? -INFINITY : (M + log2f(l)) * kLn2;
