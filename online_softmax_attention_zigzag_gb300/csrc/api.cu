@@ -634,18 +634,6 @@ int encode_pool(CUtensorMap* map, const void* base, long long page_stride, const
     return r == CUDA_SUCCESS ? RA_OK : RA_ERR_CUDA;
 }
 
-// The scales of a pool tensor as [n_pages, Hkv * page_size], boxes of box_rows.
-int encode_scales(CUtensorMap* map, const float* base, long long page_stride, const ra::PagedKV& kv, int box_rows) {
-    cuuint64_t dims[2] = {static_cast<cuuint64_t>(kv.hkv) * kv.page, static_cast<cuuint64_t>(kv.n_pages)};
-    cuuint64_t strides[1] = {static_cast<cuuint64_t>(page_stride) * 4};
-    cuuint32_t box[2] = {static_cast<cuuint32_t>(box_rows), 1};
-    cuuint32_t estr[2] = {1, 1};
-    CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, const_cast<float*>(base), dims, strides, box, estr,
-                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS ? RA_OK : RA_ERR_CUDA;
-}
-
 // Rows of a sequence and KV head decide the kernel: up to 16 the few-row one, which 16-row matrix
 // instructions serve; a chunk item fills 256 rows and does 17 at the cost of 128, which the loads
 // still hide.
@@ -691,9 +679,7 @@ int encode_paged(const ra::PagedAttnParams& p, ra::PagedMaps* m) {
                    ? RA_OK
                    : RA_ERR_CUDA;
     }
-    if (!kv.e4m3) return RA_OK;
-    if ((st = encode_scales(&m->ks, kv.k_scale, kv.ks_ps, kv, p.box_rows)) != RA_OK) return st;
-    return encode_scales(&m->vs, kv.v_scale, kv.vs_ps, kv, p.box_rows);
+    return RA_OK;
 }
 
 // Checks that concern the pool and the batch alone.

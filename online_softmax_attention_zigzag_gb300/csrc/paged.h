@@ -90,8 +90,8 @@ struct PagedAttnParams {
     unsigned long long timeout_ns;
 };
 
-struct PagedMaps {  // of the pool; ks and vs (few rows) only for e4m3; q for chunks
-    CUtensorMap k, v, ks, vs, q;
+struct PagedMaps {  // of the pool; q for chunks
+    CUtensorMap k, v, q;
 };
 
 int launch_cache_append(const PagedCopyParams& p, int sms, cudaStream_t stream);

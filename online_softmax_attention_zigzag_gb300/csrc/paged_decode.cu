@@ -53,16 +53,19 @@ struct Cfg {
     static constexpr int kSlotBytes = kTile * D * (E4M3 ? 1 : 2);
     static constexpr int kSlots = (D == 128 && !E4M3) ? 5 : 8;
     static constexpr int kWarps = 8;                   // that compute
-    static constexpr int kThreads = kWarps * 32 + 32;  // and the loading warp
+    // and those that load: in 8 bits one K and one V, which have more copies to issue for the same bytes
+    static constexpr int kLoaders = E4M3 ? 2 : 1;
+    static constexpr int kThreads = (kWarps + kLoaders) * 32;
     static constexpr int kGroups = E4M3 ? (NT == 1 ? 4 : 2) : 1;
     static constexpr int kGroupWarps = kWarps / kGroups;
     // A slot's tiles must all be one group's: waits go by a barrier's parity, and a group that met a slot
     // of another's could be two tiles ahead of it (copies need not end in order) and take the
     // parity of the tile before last for its own.
     static_assert(kGroups == 1 || (kSlots % 2 == 0 && (kSlots / 2) % kGroups == 0), "a slot pair a group");
+    static_assert(kLoaders == 1 || kSlots % 2 == 0, "every slot one loader's");
     static constexpr int kKeys = kTile / kGroupWarps;  // of a tile, for a warp
     static constexpr int kOStride = D + 4;             // keeps the fragments' stores off each other's banks
-    static constexpr int kScaleBytes = 1024;  // of a slot: boxes start 128 bytes apart at least, as TMA wants
+    static constexpr int kScaleBytes = kTile * 4;  // of a slot
     static constexpr int kScaleOff = kSlots * kSlotBytes;
     static constexpr int kOOff = kScaleOff + (E4M3 ? kSlots * kScaleBytes : 0);
     // Groups of warps end a part at different times: they go on with the next one and join this one behind their
@@ -163,23 +166,22 @@ __device__ __forceinline__ void for_each_part(const PagedAttnParams& p, const in
 
 // ------------------------------------------------------------------ the loading warp
 template <int D, bool E4M3, int NT>
-__device__ void load_role(const PagedAttnParams& p, const CUtensorMap* tk, const CUtensorMap* tv,
-                          const CUtensorMap* tks, const CUtensorMap* tvs, uint32_t ring, uint32_t scales, uint64_t* full,
-                          uint64_t* empty, const int* pre, long long w0, long long w1, const WaitCtl& wc) {
+__device__ void load_role(const PagedAttnParams& p, const CUtensorMap* tk, const CUtensorMap* tv, uint32_t ring,
+                          uint32_t scales, uint64_t* full, uint64_t* empty, const int* pre, long long w0, long long w1, const WaitCtl& wc) {
     using C = Cfg<D, E4M3, NT>;
     const PagedKV& kv = p.kv;
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31, mine = threadIdx.x / 32 - C::kWarps;
     const int rows = p.box_rows;          // of a box; a lane loads one
     const int boxes = kTile / rows;       // at most 8: pages are multiples of 16 rows
     const uint64_t policy = make_policy_evict_first();
-    constexpr uint32_t kBytes = C::kSlotBytes + (E4M3 ? kTile * 4 : 0);
+    const int log_rows = 31 - __clz(rows);
     uint32_t it = 0;
     bool ok = true;
     for_each_part(p, pre, w0, w1, [&](const Part& q) -> bool {
         const PagedSeq s = paged_seq(kv, q.b);
         const Tiles kt = key_tiles(p, s);
         // q on its way to L1 for the warps that compute, who come here later
-        for (int i = lane; i < min(s.T, p.max_q) * p.g * (D / 32); i += 32) {
+        for (int i = lane; mine == 0 && i < min(s.T, p.max_q) * p.g * (D / 32); i += 32) {
             const int r = i / (D / 32), t = r / p.g;
             const uint16_t* src = static_cast<const uint16_t*>(p.q) + (s.q0 + t) * p.q_ts + (q.h * p.g + r - t * p.g) * p.q_hs;
             asm volatile("prefetch.global.L1 [%0];" ::"l"(src + (i % (D / 32)) * 32));
@@ -198,23 +200,30 @@ __device__ void load_role(const PagedAttnParams& p, const CUtensorMap* tk, const
             if (t + 1 < q.tb) look(t + 1);
 #pragma unroll
             for (int half = 0; half < 2; ++half, ++it) {
+                if (C::kLoaders == 2 && half != mine) continue;
                 const uint32_t slot = it % C::kSlots;
                 ok = __all_sync(0xffffffffu, mbar_wait(&empty[slot], ((it / C::kSlots) & 1u) ^ 1u, wc, 20));
                 if (!ok) return false;
-                if (lane == 0) mbar_arrive_expect_tx(&full[slot], kBytes);
+                if (lane == 0) mbar_arrive_expect_tx(&full[slot], C::kSlotBytes);
                 __syncwarp();
                 if (lane < boxes) {
                     const CUtensorMap* map = half ? tv : tk;
                     const uint32_t dst = ring + slot * C::kSlotBytes;
                     if constexpr (E4M3) {
                         tma_load_3d(dst + lane * rows * D, map, &full[slot], 0, y, pg, policy);
-                        tma_load_2d(scales + slot * C::kScaleBytes + lane * max(rows * 4, 128), half ? tvs : tks, &full[slot], y, pg,
-                                    policy);
                     } else {
 #pragma unroll
                         for (int x = 0; x < D / 64; ++x)
                             tma_load_3d(dst + x * kTile * 128 + lane * rows * 128, map, &full[slot], x * 64, y, pg, policy);
                     }
+                }
+                if constexpr (E4M3) {  // four rows' scales a lane: TMA boxes take 45 ns each, and pages of 16 rows have 8
+                    const int of = __shfl_sync(0xffffffffu, pg, (4 * lane) >> log_rows);
+                    const int at = __shfl_sync(0xffffffffu, y, (4 * lane) >> log_rows) + ((4 * lane) & (rows - 1));
+                    const float* src = half ? kv.v_scale : kv.k_scale;
+                    copy16_async(scales + slot * C::kScaleBytes + lane * 16, of >= 0 ? src + of * (half ? kv.vs_ps : kv.ks_ps) + at : src,
+                                 of >= 0);
+                    copies_arrive(&full[slot]);
                 }
             }
         }
@@ -223,6 +232,7 @@ __device__ void load_role(const PagedAttnParams& p, const CUtensorMap* tk, const
     if (!ok && lane == 0) {  // let the copies in flight land before the block ends
         for (uint32_t s = 0; s < (uint32_t)C::kSlots && s < it; ++s) {
             const uint32_t last = it - 1 - ((it - 1 - s) % C::kSlots);
+            if (C::kLoaders == 2 && (last & 1u) != static_cast<uint32_t>(mine)) continue;
             drain_wait(&full[s], (last / C::kSlots) & 1u, wc.timeout_ns);
         }
     }
@@ -355,9 +365,7 @@ __device__ void compute_role(const PagedAttnParams& p, uint8_t* smem, uint64_t* 
     float* sl = sms + kWarps * kRows;
     int* sbad = reinterpret_cast<int*>(sl + kWarps * kRows);
     const int grp = warp / C::kGroupWarps, key0 = (warp % C::kGroupWarps) * C::kKeys;  // this warp's keys of a tile
-    // its scales in a slot: 16 keys lie 16 floats apart (boxes of 16 rows 32, 128 bytes)
-    const int step16 = p.box_rows == 16 ? 32 : 16;
-    const float* scales = reinterpret_cast<const float*>(smem + C::kScaleOff) + step16 * (key0 / 16) + r8;
+    const float* scales = reinterpret_cast<const float*>(smem + C::kScaleOff) + key0 + r8;  // its scales in a slot
     uint32_t tiles = 0;  // of the parts before
     bool ok = true;
     uint32_t sets = 0;   // kLater: results that this warp has put into the buffer
@@ -482,7 +490,7 @@ __device__ void compute_role(const PagedAttnParams& p, uint8_t* smem, uint64_t* 
                 const float* f = scales + slot * (C::kScaleBytes / 4);
 #pragma unroll
                 for (int n = 0; n < NB; ++n) {
-                    const float k0 = f[step16 * n], k1 = f[step16 * n + 8];
+                    const float k0 = f[16 * n], k1 = f[16 * n + 8];
 #pragma unroll
                     for (int z = 0; z < NT; ++z) {
                         sc[n][z][0] *= k0 * cs[z][0];
@@ -551,7 +559,7 @@ __device__ void compute_role(const PagedAttnParams& p, uint8_t* smem, uint64_t* 
                 const float* f = scales + slot * (C::kScaleBytes / 4);
 #pragma unroll
                 for (int n = 0; n < NB; ++n) {
-                    const float v0 = lg2(f[step16 * n]), v1 = lg2(f[step16 * n + 8]);
+                    const float v0 = lg2(f[16 * n]), v1 = lg2(f[16 * n + 8]);
 #pragma unroll
                     for (int z = 0; z < NT; ++z)
 #pragma unroll
@@ -743,8 +751,7 @@ __device__ void compute_role(const PagedAttnParams& p, uint8_t* smem, uint64_t* 
 template <int D, bool E4M3, int NT>
 __global__ void __launch_bounds__(Cfg<D, E4M3, NT>::kThreads, 1)
     paged_decode_kernel(const __grid_constant__ PagedAttnParams p, const __grid_constant__ CUtensorMap tk,
-                        const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tks,
-                        const __grid_constant__ CUtensorMap tvs) {
+                        const __grid_constant__ CUtensorMap tv) {
     using C = Cfg<D, E4M3, NT>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -757,7 +764,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, NT>::kThreads, 1)
     launch_dependents();
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::kSlots; ++s) {
-            mbar_init(&full[s], 1);
+            mbar_init(&full[s], E4M3 ? 1 + 32 : 1);  // the tile's bytes, and every lane's scales
             mbar_init(&empty[s], C::kGroupWarps);
         }
         mbar_init(&ready, C::kWarps);
@@ -773,8 +780,8 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, NT>::kThreads, 1)
     if (threadIdx.x < 2) parts[threadIdx.x].b = -1;  // until a cut pair says otherwise
     __syncthreads();
     const WaitCtl wc{&abort_flag, p.err, p.timeout_ns};
-    if (threadIdx.x / 32 == C::kWarps)
-        load_role<D, E4M3, NT>(p, &tk, &tv, &tks, &tvs, smem_u32(smem), smem_u32(smem) + C::kScaleOff, full, empty, pre, w0, w1, wc);
+    if (threadIdx.x / 32 >= C::kWarps)
+        load_role<D, E4M3, NT>(p, &tk, &tv, smem_u32(smem), smem_u32(smem) + C::kScaleOff, full, empty, pre, w0, w1, wc);
     else
         compute_role<D, E4M3, NT>(p, smem, full, empty, &ready, &freed, pre, w0, w1, wc);
 }
@@ -861,7 +868,7 @@ int launch_t(const PagedAttnParams& p, const PagedMaps& m, int shares, cudaStrea
                                         C::kFixedBytes + 4 * (kPagedMaxBatch + 1)) == cudaSuccess;
         }))
         return -4;
-    kern<<<shares, C::kThreads, bytes, stream>>>(p, m.k, m.v, m.ks, m.vs);
+    kern<<<shares, C::kThreads, bytes, stream>>>(p, m.k, m.v);
     if (cudaGetLastError() != cudaSuccess) return -4;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(shares, p.max_q * p.g);
