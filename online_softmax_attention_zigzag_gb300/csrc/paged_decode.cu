@@ -18,11 +18,13 @@
 //     transposed, S^T = K Q^T and O^T = V^T P^T, so that the keys and the elements fill the 16 rows of
 //     the instruction and the query rows its 8 columns: up to 8 rows, the usual case, then
 //     cost half the instructions and registers of S = Q K^T.  Each warp keeps its own
-//     running max, sum and output; they meet once a pair.  In 8 bits a tile arrives in half the
-//     time, and what a warp does for it is a chain of latencies (barrier, S, max, exponentials, P
-//     V): groups of warps then take tiles in turn, so that a warp has more keys of a tile to
-//     overlap and more time for it: four groups of two warps, 64 keys each, for up to 8 rows, two
-//     groups of four, 32 keys each, above.
+//     running max, sum and output; they meet once a pair.  Where a tile arrives in half the time or
+//     less (8 bits, or 64 elements), what a warp does for it is a chain of latencies (barrier, S, max,
+//     exponentials, P V) that takes longer: groups of warps then take tiles in turn, so that a warp
+//     has more keys of a tile to overlap and more time for it.  In 8 bits four groups of two warps,
+//     64 keys each (two tokens of 8 heads: 122 us with two groups, 115 with four); bf16 of 64 elements
+//     two groups of four (193 us without, 165 with two, 169 with four).  bf16 of 128 has slots for no two
+//     groups but at four slots instead of five: 64 x 16k keys 324 -> 318 us, 512 short ones 173 -> 214 us.
 // bf16 cache: P goes into its product as two bf16 halves (p = hi + lo, 16 significant bits): the
 // second product costs nothing here, the loads take longer.
 // e4m3 cache: codes become fp16 (one instruction for two, exact), q is brought to fp16's range by
@@ -53,10 +55,11 @@ struct Cfg {
     static constexpr int kSlotBytes = kTile * D * (E4M3 ? 1 : 2);
     static constexpr int kSlots = (D == 128 && !E4M3) ? 5 : 8;
     static constexpr int kWarps = 8;                   // that compute
-    // and those that load: in 8 bits one K and one V, which have more copies to issue for the same bytes
-    static constexpr int kLoaders = E4M3 ? 2 : 1;
+    // and those that load, one K and one V: small pages and small rows have many copies to issue for their bytes
+    // (e4m3, pages of 16 rows: 313 us with one warp, 183 with two).  With five slots a slot would change hands.
+    static constexpr int kLoaders = kSlots % 2 == 0 ? 2 : 1;
     static constexpr int kThreads = (kWarps + kLoaders) * 32;
-    static constexpr int kGroups = E4M3 ? (NT == 1 ? 4 : 2) : 1;
+    static constexpr int kGroups = E4M3 ? 4 : D == 64 ? 2 : 1;
     static constexpr int kGroupWarps = kWarps / kGroups;
     // A slot's tiles must all be one group's: waits go by a barrier's parity, and a group that met a slot
     // of another's could be two tiles ahead of it (copies need not end in order) and take the
