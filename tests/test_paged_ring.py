@@ -1,4 +1,4 @@
-"""The few-row paged kernel's ring of tiles, as a model (no GPU): one loader fills slots with copies
+"""The few-row paged kernel's ring of tiles, as a model (no GPU): loaders fill slots with copies
 that may end out of order, groups of warps take tiles in turn, and both sides wait on mbarriers by
 the parity of a phase, as the kernel does.  A wait by parity is right only for a waiter that is at
 most one phase ahead; the model raises where a warp takes a slot that does not hold its tile, where
@@ -34,23 +34,22 @@ class Bar:
         return (self.phase & 1) != parity
 
 
-def run(slots, groups, warps, tiles, seed):
+def run(slots, groups, warps, tiles, seed, loaders=1):
     r = random.Random(seed)
     full, empty = [Bar(1) for _ in range(slots)], [Bar(warps) for _ in range(slots)]
     holds = [None] * slots
-    events, state = [], dict(t=0.0, n=0, it=0, taken=0)
+    events, state = [], dict(t=0.0, n=0, taken=0)
 
     def after(dt, f):
         state["n"] += 1
         heapq.heappush(events, (state["t"] + dt, state["n"], f))
 
-    def loader():
-        it = state["it"]
-        if it == 2 * tiles:
+    def loader(it):
+        if it >= 2 * tiles:
             return
         s = it % slots
         if not empty[s].done(((it // slots) & 1) ^ 1):
-            return after(0.05, loader)
+            return after(0.05, lambda: loader(it))
         full[s].arrive(1)
         holds[s] = None
 
@@ -59,8 +58,7 @@ def run(slots, groups, warps, tiles, seed):
             full[s].complete(1)
 
         after(1 + r.random() * (8 if r.random() < 0.05 else 0.5), landed)  # now and then a late one
-        state["it"] += 1
-        after(0.02, loader)
+        after(r.random() * 0.04, lambda: loader(it + loaders))
 
     def warp(tile, half, step):
         if tile >= tiles:
@@ -81,7 +79,8 @@ def run(slots, groups, warps, tiles, seed):
 
         after(r.random() * step, release)
 
-    after(0, loader)
+    for w in range(loaders):  # two: one has the K tiles, one the V tiles
+        after(0, lambda w=w: loader(w))
     for g in range(groups):
         for _ in range(warps):
             after(0, lambda g=g: warp(g, 0, 0.5 * groups))
@@ -91,13 +90,12 @@ def run(slots, groups, warps, tiles, seed):
     return state["taken"]
 
 
-# (slots, groups, warps of a group) of the kernel's variants: bf16 with d = 128 and d = 64, e4m3 with up
-# to 8 rows and with more
-@pytest.mark.parametrize("slots,groups,warps", [(5, 1, 8), (8, 1, 8), (8, 4, 2), (8, 2, 4)])
-def test_every_tile_is_taken_whole_and_once(slots, groups, warps):
+# (slots, groups, warps of a group, loaders) of the kernel's variants: bf16 with d = 128 and with d = 64, e4m3
+@pytest.mark.parametrize("slots,groups,warps,loaders", [(5, 1, 8, 1), (8, 2, 4, 2), (8, 4, 2, 2)])
+def test_every_tile_is_taken_whole_and_once(slots, groups, warps, loaders):
     for seed in range(25):
         for tiles in (1, 2, 3, 7, 150):
-            assert run(slots, groups, warps, tiles, seed) == 2 * tiles * warps
+            assert run(slots, groups, warps, tiles, seed, loaders) == 2 * tiles * warps
 
 
 def test_groups_that_share_slots_would_not_do():
