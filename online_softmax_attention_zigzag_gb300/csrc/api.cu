@@ -646,7 +646,7 @@ bool paged_few(int total, int g, int max_q) {
 long long paged_workspace(int total, int batch, int g, int max_q, ra::PagedAttnParams* p) {
     long long n = 2LL * ra::kPagedMaxShares;
     if (paged_few(total, g, max_q)) {
-        n *= sizeof(ra::PagedPartial);
+        n *= ra::kPagedMaxGroups * sizeof(ra::PagedPartial);
     } else {
         n *= sizeof(ra::PagedChunkPartial);
         const int unit = g <= 128 ? 128 / g : 1;

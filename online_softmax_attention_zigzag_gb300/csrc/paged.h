@@ -27,10 +27,11 @@ constexpr int kPagedMaxBatch = 4096;  // RINGATTN_PAGED_MAX_BATCH
 constexpr int kPagedTile = 128;       // keys of a tile
 constexpr int kPagedMaxD = 128;
 constexpr int kPagedMaxShares = 160;  // most blocks of an attention kernel
+constexpr int kPagedMaxGroups = 4;    // of a few-row block, with a share each
 constexpr int kPagedFewRows = 16;     // rows of one sequence and KV head that the few-row kernel takes
 
-// What a block of the few-row kernel leaves of a (sequence, KV head) pair that other blocks
-// share: row r's sum of p v with weights 2^(x - m), and sum of p with weights 2^(x - ms).
+// What a share of the few-row kernel's work leaves of a (sequence, KV head) pair that others have tiles
+// of too: row r's sum of p v with weights 2^(x - m), and sum of p with weights 2^(x - ms).
 struct PagedPartial {
     int b, h, begins, pad;  // b < 0: none; begins: the pair's first tile is in it
     float m[kPagedFewRows], ms[kPagedFewRows], l[kPagedFewRows];
@@ -96,9 +97,9 @@ struct PagedMaps {  // of the pool; q for chunks
 
 int launch_cache_append(const PagedCopyParams& p, int sms, cudaStream_t stream);
 int launch_cache_read(const PagedCopyParams& p, int sms, cudaStream_t stream);
-// max_q * g <= kPagedFewRows; `shares` blocks (at most kPagedMaxShares), the workspace 2 * shares
-// PagedPartial
-int launch_paged_decode(const PagedAttnParams& p, const PagedMaps& m, int shares, cudaStream_t stream);
+// max_q * g <= kPagedFewRows; `blocks` at most kPagedMaxShares, the workspace 2 * kPagedMaxGroups
+// PagedPartial for each
+int launch_paged_decode(const PagedAttnParams& p, const PagedMaps& m, int blocks, cudaStream_t stream);
 // any number of rows, g <= 128; the workspace 2 * shares PagedChunkPartial and the list of items
 int launch_paged_chunk(const PagedAttnParams& p, const PagedMaps& m, int shares, cudaStream_t stream);
 

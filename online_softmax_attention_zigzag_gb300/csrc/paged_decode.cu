@@ -4,27 +4,31 @@
 //     s_j = q . k_j,  out = sum_j 2^(c s_j - m) v_j / l,  l = sum_j 2^(c s_j - m),  c = log2 e
 // Every K and V row is read once for at most 16 query rows: 16 * 4 * d FLOP for 4 * d bytes (2 * d
 // in 8 bits), so HBM bounds it by far and everything else only has to keep out of the way:
-//   * one persistent block an SM; the tiles of 128 keys of all (sequence, KV head) pairs, in one
-//     line, are dealt out in equal contiguous shares, so that one long context or a thousand
+//   * one persistent block an SM, of two or four groups of warps that have nothing to do with each other;
+//     the tiles of 128 keys of all (sequence, KV head) pairs, in one line, are dealt out to the
+//     groups in equal contiguous shares, so that one long context or a thousand
 //     short ones load every SM alike.  A pair whose tiles lie in several shares leaves
 //     partial results (O, m, l) in the workspace, which a second small kernel joins; a share
 //     has at most two of these (its first and its last pair), so the workspace does not grow
 //     with the lengths.
-//   * one warp streams K and V tiles through a ring of shared-memory slots with TMA, box by box
-//     as the pages come (a box is gcd(page, 128) rows of one page), and runs on into the next
-//     pair while the others finish the last.
-//   * eight warps compute, 16 keys of every tile each, with mma.sync: 8 rows are a sixteenth of a
-//     tcgen05 tile, and S and P stay in registers between the two products.  Both products are
-//     transposed, S^T = K Q^T and O^T = V^T P^T, so that the keys and the elements fill the 16 rows of
-//     the instruction and the query rows its 8 columns: up to 8 rows, the usual case, then
-//     cost half the instructions and registers of S = Q K^T.  Each warp keeps its own
-//     running max, sum and output; they meet once a pair.  Where a tile arrives in half the time or
-//     less (8 bits, or 64 elements), what a warp does for it is a chain of latencies (barrier, S, max,
-//     exponentials, P V) that takes longer: groups of warps then take tiles in turn, so that a warp
-//     has more keys of a tile to overlap and more time for it.  In 8 bits four groups of two warps,
-//     64 keys each (two tokens of 8 heads: 122 us with two groups, 115 with four); bf16 of 64 elements
-//     two groups of four (193 us without, 165 with two, 169 with four).  bf16 of 128 has slots for no two
-//     groups but at four slots instead of five: 64 x 16k keys 324 -> 318 us, 512 short ones 173 -> 214 us.
+//   * a group's loading warp streams K and V tiles through its slots of shared memory with TMA, box
+//     by box as the pages come (a box is gcd(page, 128) rows of one page), and runs on into the
+//     next pair while the others finish the last.
+//   * a group's two or four other warps compute, 64 or 32 keys of every tile each, with mma.sync: 8 rows
+//     are a sixteenth of a tcgen05 tile, and S and P stay in registers between the two products.
+//     Both products are transposed, S^T = K Q^T and O^T = V^T P^T, so that the keys and the elements
+//     fill the 16 rows of the instruction and the query rows its 8 columns: up to 8 rows, the usual
+//     case, then cost half the instructions and registers of S = Q K^T.  Each warp keeps its own
+//     running max, sum and output; they meet once a pair.
+// What a tile takes is a chain of latencies (copy, barrier, S, max, exponentials, P V), and so is what
+// a pair takes (q, the meeting, the output): groups hide them behind one another.  One group of eight
+// warps with the same 128 KB of slots, and four that took one line's tiles in turn, were slower:
+//     64 x 16k keys of 8 heads, bf16             323 us, now 310 (6.6 TB/s)
+//     8 x 128k keys, e4m3                        293 us, now 288 (6.8 TB/s)
+//     48 windows of 4096 of 3k - 32k keys, e4m3   78 us, now  75
+//     512 x 20 - 300 keys, e4m3                  181 us, now  76; bf16 173 and 125
+//     32 x 16k keys of d = 64, e4m3              129 us, now 103; bf16 165 and 160 (6.6 TB/s)
+//     one sequence of 777 keys                  13.0 us, now 11.4
 // bf16 cache: P goes into its product as two bf16 halves (p = hi + lo, 16 significant bits): the
 // second product costs nothing here, the loads take longer.
 // e4m3 cache: codes become fp16 (one instruction for two, exact), q is brought to fp16's range by
@@ -53,28 +57,18 @@ constexpr float kF16Up = 6.0f;            // p' is kept 2^6 times larger: at mos
 template <int D, bool E4M3, int NT>
 struct Cfg {
     static constexpr int kSlotBytes = kTile * D * (E4M3 ? 1 : 2);
-    static constexpr int kSlots = (D == 128 && !E4M3) ? 5 : 8;
-    static constexpr int kWarps = 8;                   // that compute
-    // and those that load, one K and one V: small pages and small rows have many copies to issue for their bytes
-    // (e4m3, pages of 16 rows: 313 us with one warp, 183 with two).  With five slots a slot would change hands.
-    static constexpr int kLoaders = kSlots % 2 == 0 ? 2 : 1;
-    static constexpr int kThreads = (kWarps + kLoaders) * 32;
-    static constexpr int kGroups = E4M3 ? 4 : D == 64 ? 2 : 1;
+    static constexpr int kGroups = E4M3 ? 4 : 2;
+    static constexpr int kDepth = D == 128 ? 1 : 2;        // tiles of a group in shared memory: 128 KB in all
+    static constexpr int kGroupSlots = 2 * kDepth;         // a K and a V tile each
+    static constexpr int kSlots = kGroups * kGroupSlots;
+    static constexpr int kWarps = 8;                             // that compute
+    static constexpr int kThreads = (kWarps + kGroups) * 32;     // and one that loads for every group
     static constexpr int kGroupWarps = kWarps / kGroups;
-    // A slot's tiles must all be one group's: waits go by a barrier's parity, and a group that met a slot
-    // of another's could be two tiles ahead of it (copies need not end in order) and take the
-    // parity of the tile before last for its own.
-    static_assert(kGroups == 1 || (kSlots % 2 == 0 && (kSlots / 2) % kGroups == 0), "a slot pair a group");
-    static_assert(kLoaders == 1 || kSlots % 2 == 0, "every slot one loader's");
     static constexpr int kKeys = kTile / kGroupWarps;  // of a tile, for a warp
     static constexpr int kOStride = D + 4;             // keeps the fragments' stores off each other's banks
     static constexpr int kScaleBytes = kTile * 4;  // of a slot
     static constexpr int kScaleOff = kSlots * kSlotBytes;
     static constexpr int kOOff = kScaleOff + (E4M3 ? kSlots * kScaleBytes : 0);
-    // Groups of warps end a part at different times: they go on with the next one and join this one behind their
-    // first tile of that (4096-key windows of 192 sequences in 8 bits: 301 us without, 280 with).
-    // One group ends together, and for 16 rows there are no registers (two tokens of 8 heads: 123 us, 143 with).
-    static constexpr bool kLater = kGroups > 1 && NT == 1;
     // the warps' results meet in a buffer of 8 rows a warp, rows 0-7 and then rows 8-15
     static constexpr int kMlOff = kOOff + kWarps * 8 * kOStride * 4;  // m, ms, l of every warp and row; bad values
     static constexpr int kPreOff = kMlOff + (3 * kWarps * kRows + kWarps) * 4;
@@ -97,7 +91,7 @@ __device__ __forceinline__ Tiles key_tiles(const PagedAttnParams& p, const Paged
     return t;
 }
 
-// One block's part of one (sequence, head) pair: tiles [ta, tb) of its n.
+// One share's part of one (sequence, head) pair: tiles [ta, tb) of its n.
 struct Part {
     int b, h, ta, tb, n;
 };
@@ -134,7 +128,7 @@ __device__ int share_tiles(const PagedAttnParams& p, int* pre, int* scratch) {
     return base;
 }
 
-// Walks the parts of this block's share [w0, w1): f(part) until it returns false.
+// Walks the parts of a share [w0, w1): f(part) until it returns false.
 template <class F>
 __device__ __forceinline__ void for_each_part(const PagedAttnParams& p, const int* pre, long long w0, long long w1,
                                               F&& f) {
@@ -173,18 +167,19 @@ __device__ void load_role(const PagedAttnParams& p, const CUtensorMap* tk, const
                           uint32_t scales, uint64_t* full, uint64_t* empty, const int* pre, long long w0, long long w1, const WaitCtl& wc) {
     using C = Cfg<D, E4M3, NT>;
     const PagedKV& kv = p.kv;
-    const int lane = threadIdx.x & 31, mine = threadIdx.x / 32 - C::kWarps;
+    const int lane = threadIdx.x & 31;
     const int rows = p.box_rows;          // of a box; a lane loads one
     const int boxes = kTile / rows;       // at most 8: pages are multiples of 16 rows
     const uint64_t policy = make_policy_evict_first();
     const int log_rows = 31 - __clz(rows);
-    uint32_t it = 0;
+    uint32_t n = 0;  // tiles so far
+    int half = 0;
     bool ok = true;
     for_each_part(p, pre, w0, w1, [&](const Part& q) -> bool {
         const PagedSeq s = paged_seq(kv, q.b);
         const Tiles kt = key_tiles(p, s);
         // q on its way to L1 for the warps that compute, who come here later
-        for (int i = lane; mine == 0 && i < min(s.T, p.max_q) * p.g * (D / 32); i += 32) {
+        for (int i = lane; i < min(s.T, p.max_q) * p.g * (D / 32); i += 32) {
             const int r = i / (D / 32), t = r / p.g;
             const uint16_t* src = static_cast<const uint16_t*>(p.q) + (s.q0 + t) * p.q_ts + (q.h * p.g + r - t * p.g) * p.q_hs;
             asm volatile("prefetch.global.L1 [%0];" ::"l"(src + (i % (D / 32)) * 32));
@@ -198,14 +193,13 @@ __device__ void load_role(const PagedAttnParams& p, const CUtensorMap* tk, const
             if (lane < boxes && pos < s.L) entry = paged_entry(kv, q.b, pos, row);
         };
         look(q.ta);
-        for (int t = q.ta; t < q.tb; ++t) {
+        for (int t = q.ta; t < q.tb; ++t, ++n) {
             const int pg = paged_checked(kv, entry), y = q.h * kv.page + row;
             if (t + 1 < q.tb) look(t + 1);
 #pragma unroll
-            for (int half = 0; half < 2; ++half, ++it) {
-                if (C::kLoaders == 2 && half != mine) continue;
-                const uint32_t slot = it % C::kSlots;
-                ok = __all_sync(0xffffffffu, mbar_wait(&empty[slot], ((it / C::kSlots) & 1u) ^ 1u, wc, 20));
+            for (half = 0; half < 2; ++half) {  // K, then V
+                const uint32_t slot = n % C::kDepth * 2 + half;
+                ok = __all_sync(0xffffffffu, mbar_wait(&empty[slot], ((n / C::kDepth) & 1u) ^ 1u, wc, 20));
                 if (!ok) return false;
                 if (lane == 0) mbar_arrive_expect_tx(&full[slot], C::kSlotBytes);
                 __syncwarp();
@@ -233,11 +227,9 @@ __device__ void load_role(const PagedAttnParams& p, const CUtensorMap* tk, const
         return true;
     });
     if (!ok && lane == 0) {  // let the copies in flight land before the block ends
-        for (uint32_t s = 0; s < (uint32_t)C::kSlots && s < it; ++s) {
-            const uint32_t last = it - 1 - ((it - 1 - s) % C::kSlots);
-            if (C::kLoaders == 2 && (last & 1u) != static_cast<uint32_t>(mine)) continue;
-            drain_wait(&full[s], (last / C::kSlots) & 1u, wc.timeout_ns);
-        }
+        const uint32_t all = 2 * n + half;  // tiles asked for, K and V
+        for (uint32_t i = all > C::kGroupSlots ? all - C::kGroupSlots : 0; i < all; ++i)
+            drain_wait(&full[i % C::kGroupSlots], (i / C::kGroupSlots) & 1u, wc.timeout_ns);
     }
 }
 
@@ -271,18 +263,19 @@ __device__ __forceinline__ float bf16_add_nonfinite(float acc, uint16_t bits) {
     return (bits & 0x7f80u) == 0x7f80u ? acc + __uint_as_float(static_cast<uint32_t>(bits) << 16) : acc;
 }
 
-// Joins the warps' results for part q: warp w row 8 round + w of the pair.  Into the outputs, or, if others have tiles of the pair too, into the workspace.
+// Joins the group's warps' results for part q: rows 8 round .. + 8 of the pair, in turn.  Into the
+// outputs, or, if others have tiles of the pair too, into the workspace.
 template <int D, bool E4M3, int NT>
 __device__ __forceinline__ void join_rows(const PagedAttnParams& p, const uint8_t* smem, Part q, int slot, int round) {
     using C = Cfg<D, E4M3, NT>;
-    constexpr int kWarps = C::kWarps;
+    constexpr int kWarps = C::kGroupWarps;
     const PagedKV& kv = p.kv;
-    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
-    const float* so = reinterpret_cast<const float*>(smem + C::kOOff);
-    const float* sm = reinterpret_cast<const float*>(smem + C::kMlOff);
-    const float* sms = sm + kWarps * kRows;
-    const float* sl = sms + kWarps * kRows;
-    const int* sbad = reinterpret_cast<const int*>(sl + kWarps * kRows);
+    const int warp = threadIdx.x / 32 % kWarps, lane = threadIdx.x & 31, w0 = threadIdx.x / 32 - warp;
+    const float* so = reinterpret_cast<const float*>(smem + C::kOOff) + w0 * 8 * C::kOStride;
+    const float* sm = reinterpret_cast<const float*>(smem + C::kMlOff) + w0 * kRows;
+    const float* sms = sm + C::kWarps * kRows;
+    const float* sl = sms + C::kWarps * kRows;
+    const int* sbad = reinterpret_cast<const int*>(smem + C::kMlOff) + 3 * C::kWarps * kRows + w0;
     const PagedSeq s = paged_seq(kv, q.b);
     const int T = min(s.T, p.max_q), R = T * p.g;
     const bool cut = q.ta > 0 || q.tb < q.n;
@@ -292,9 +285,9 @@ __device__ __forceinline__ void join_rows(const PagedAttnParams& p, const uint8_
         part->h = q.h;
         part->begins = q.ta == 0;
     }
-    static_assert(kWarps == 8, "a row a warp");
-    const int r = warp + 8 * round;
-    if (r < R) {
+    for (int row8 = warp; row8 < 8; row8 += kWarps) {
+        const int r = row8 + 8 * round;
+        if (r >= R) break;
         float M = -INFINITY, Ms = -INFINITY;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
@@ -314,7 +307,7 @@ __device__ __forceinline__ void join_rows(const PagedAttnParams& p, const uint8_
             float acc[4] = {};
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) {
-                const float4 v = *reinterpret_cast<const float4*>(so + (w * 8 + warp) * C::kOStride + d);
+                const float4 v = *reinterpret_cast<const float4*>(so + (w * 8 + row8) * C::kOStride + d);
                 acc[0] = fmaf(f[w], v.x, acc[0]);
                 acc[1] = fmaf(f[w], v.y, acc[1]);
                 acc[2] = fmaf(f[w], v.z, acc[2]);
@@ -355,40 +348,23 @@ __device__ __forceinline__ void join_rows(const PagedAttnParams& p, const uint8_
 }
 
 template <int D, bool E4M3, int NT>
-__device__ void compute_role(const PagedAttnParams& p, uint8_t* smem, uint64_t* full, uint64_t* empty, uint64_t* ready,
-                             uint64_t* freed, const int* pre, long long w0, long long w1, const WaitCtl& wc) {
+__device__ void compute_role(const PagedAttnParams& p, uint8_t* smem, uint64_t* full, uint64_t* empty, const int* pre,
+                             int share, long long w0, long long w1, const WaitCtl& wc) {
     using C = Cfg<D, E4M3, NT>;
     constexpr int kWarps = C::kWarps, NB = C::kKeys / 16;
     const PagedKV& kv = p.kv;
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31, c4 = lane & 3, r8 = lane >> 2;
-    const uint32_t ring = smem_u32(smem);
+    const int grp = warp / C::kGroupWarps, key0 = (warp % C::kGroupWarps) * C::kKeys;  // this warp's keys of a tile
+    const uint32_t ring = smem_u32(smem) + grp * C::kGroupSlots * C::kSlotBytes;
     float* so = reinterpret_cast<float*>(smem + C::kOOff);
     float* sm = reinterpret_cast<float*>(smem + C::kMlOff);
     float* sms = sm + kWarps * kRows;
     float* sl = sms + kWarps * kRows;
     int* sbad = reinterpret_cast<int*>(sl + kWarps * kRows);
-    const int grp = warp / C::kGroupWarps, key0 = (warp % C::kGroupWarps) * C::kKeys;  // this warp's keys of a tile
-    const float* scales = reinterpret_cast<const float*>(smem + C::kScaleOff) + key0 + r8;  // its scales in a slot
-    uint32_t tiles = 0;  // of the parts before
+    const float* scales = reinterpret_cast<const float*>(smem + C::kScaleOff + grp * C::kGroupSlots * C::kScaleBytes) + key0 + r8;  // its
+    uint32_t done = 0;  // tiles so far
     bool ok = true;
-    uint32_t sets = 0;   // kLater: results that this warp has put into the buffer
-    Part due = {};       // kLater: the part that the last of them is of, if it has not been joined yet (n > 0)
-    int place = 2 * blockIdx.x;  // for a part that is cut: the first one's, then the others'
-    // Waits for the other warps' results of part q and joins this warp's rows of them.
-    auto join = [&](const Part& q, int round) -> bool {
-        // (not later: a warp that gave up still comes here, so that none waits for it)
-        if (C::kLater ? !__all_sync(0xffffffffu, mbar_wait(ready, (sets - 1) & 1u, wc)) : !named_bar_and(kBar, kWarps * 32, ok))
-            return false;
-        join_rows<D, E4M3, NT>(p, smem, q, place, round);
-        if (round == NT - 1) place = 2 * blockIdx.x + 1;
-        if (C::kLater) {
-            __syncwarp();
-            if (lane == 0) mbar_arrive(freed);
-        } else {
-            named_bar_sync(kBar, kWarps * 32);  // the buffer is free again
-        }
-        return true;
-    };
+    int place = 2 * share;  // for a part that is cut: the first one's, then the others'
     for_each_part(p, pre, w0, w1, [&](const Part& q) -> bool {
         const PagedSeq s = paged_seq(kv, q.b);
         const Tiles kt = key_tiles(p, s);
@@ -455,22 +431,14 @@ __device__ void compute_role(const PagedAttnParams& p, uint8_t* smem, uint64_t* 
             }
         bool bad_v = false;  // a value that is no number, in a tile that not every row sees whole
         const int see_lo = s.base + T - p.window;  // the window of the last row begins here
-        bool one = false;  // a tile of this part is done
-        for (int t = q.ta + (grp + C::kGroups - tiles % C::kGroups) % C::kGroups;; t += C::kGroups) {
-            if (C::kLater && due.n > 0 && (one || t >= q.tb)) {
-                if (!(ok = join(due, 0))) break;
-                due.n = 0;
-            }
-            if (t >= q.tb) break;
-            one = true;
+        for (int t = q.ta; t < q.tb; ++t, ++done) {
             const int j0 = (t < kt.ns ? t : kt.lo + t - kt.ns) * kTile;
-            uint32_t it = 2 * (tiles + t - q.ta);  // the ring's number of this K tile; V is the next
             // does every row see every key of the tile?
             const bool whole = j0 + kTile <= (p.causal ? s.base + 1 : s.L) &&
                                (p.window == 0 || j0 >= see_lo || j0 + kTile <= p.sinks);
             // ---- S^T = K Q^T: element e is key r8 + 8 (e / 2) of the 16, row 2 c4 + e % 2 of the 8
-            uint32_t slot = it % C::kSlots;
-            ok = __all_sync(0xffffffffu, mbar_wait(&full[slot], (it / C::kSlots) & 1u, wc));
+            const uint32_t slot = done % C::kDepth * 2, parity = (done / C::kDepth) & 1u;  // K's, V's is the next
+            ok = __all_sync(0xffffffffu, mbar_wait(&full[slot], parity, wc));
             if (!ok) break;
             float sc[NB][NT][4] = {};
             uint32_t base = ring + slot * C::kSlotBytes;
@@ -490,7 +458,7 @@ __device__ void compute_role(const PagedAttnParams& p, uint8_t* smem, uint64_t* 
                             for (int z = 0; z < NT; ++z) mma16816<true>(sc[n][z], a, qb[z][2 * x + y][0], qb[z][2 * x + y][1]);
                         }
                     }
-                const float* f = scales + slot * (C::kScaleBytes / 4);
+                const float* f = scales + slot * kTile;
 #pragma unroll
                 for (int n = 0; n < NB; ++n) {
                     const float k0 = f[16 * n], k1 = f[16 * n + 8];
@@ -522,9 +490,7 @@ __device__ void compute_role(const PagedAttnParams& p, uint8_t* smem, uint64_t* 
             // (a slot is handed back when what was loaded from it has been used)
             __syncwarp();
             if (lane == 0) mbar_arrive(&empty[slot]);
-            ++it;
-            slot = it % C::kSlots;
-            base = ring + slot * C::kSlotBytes;
+            base += C::kSlotBytes;
             const int jk = j0 + key0;  // the warp's first key
             if (!whole) {
 #pragma unroll
@@ -554,12 +520,12 @@ __device__ void compute_role(const PagedAttnParams& p, uint8_t* smem, uint64_t* 
                         for (int n = 0; n < NB; ++n) l[z][e] += ex2(sc[n][z][e] + nm) + ex2(sc[n][z][2 + e] + nm);
                     }
             }
-            ok = __all_sync(0xffffffffu, mbar_wait(&full[slot], (it / C::kSlots) & 1u, wc));
+            ok = __all_sync(0xffffffffu, mbar_wait(&full[slot + 1], parity, wc));
             if (!ok) break;
             // ---- e4m3: the V scales join the scores as exponents.  (No number stays none; log2 0 = -inf,
             // for the zeros of a page that is none.)
             if constexpr (E4M3) {
-                const float* f = scales + slot * (C::kScaleBytes / 4);
+                const float* f = scales + (slot + 1) * kTile;
 #pragma unroll
                 for (int n = 0; n < NB; ++n) {
                     const float v0 = lg2(f[16 * n]), v1 = lg2(f[16 * n + 8]);
@@ -688,11 +654,9 @@ __device__ void compute_role(const PagedAttnParams& p, uint8_t* smem, uint64_t* 
                     }
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(&empty[slot]);
+            if (lane == 0) mbar_arrive(&empty[slot + 1]);
         }
-        tiles += q.tb - q.ta;
-        if (C::kLater && !ok) return false;
-        // ---- the warp's results into the buffer, once nobody reads the ones before any more
+        // ---- the group's warps' results meet: rows 0-7, then rows 8-15
 #pragma unroll
         for (int x = 0; x < NT; ++x)
 #pragma unroll
@@ -709,17 +673,12 @@ __device__ void compute_role(const PagedAttnParams& p, uint8_t* smem, uint64_t* 
                 l[x][e] += __shfl_xor_sync(0xffffffffu, l[x][e], 4);
                 l[x][e] += __shfl_xor_sync(0xffffffffu, l[x][e], 8);
                 l[x][e] += __shfl_xor_sync(0xffffffffu, l[x][e], 16);
-                if (C::kLater && x == 0 && e == 0 && sets > 0) {
-                    ok = __all_sync(0xffffffffu, mbar_wait(freed, (sets - 1) & 1u, wc));
-                    if (!ok) break;
-                }
                 if (r8 == 0) {
                     sm[warp * kRows + 8 * x + 2 * c4 + e] = m[x][e];
                     sms[warp * kRows + 8 * x + 2 * c4 + e] = ms[x][e];
                     sl[warp * kRows + 8 * x + 2 * c4 + e] = l[x][e];
                 }
             }
-        if (C::kLater && !ok) return false;
         if (lane == 0) sbad[warp] = 0;
         __syncwarp();
         if (bad_v) sbad[warp] = 1;
@@ -737,18 +696,14 @@ __device__ void compute_role(const PagedAttnParams& p, uint8_t* smem, uint64_t* 
                         dst[e * C::kOStride + 16 * i + 8 + r8] = o[i][x][2 + e];
                     }
                 }
-            if (C::kLater) {
-                __syncwarp();
-                if (lane == 0) mbar_arrive(ready);
-                ++sets;
-            } else if (!(ok = join(q, x))) {
-                return false;
-            }
+            // (a warp that gave up still comes here, so that none waits for it)
+            if (!named_bar_and(kBar + grp, C::kGroupWarps * 32, ok)) return false;
+            join_rows<D, E4M3, NT>(p, smem, q, place, x);
+            named_bar_sync(kBar + grp, C::kGroupWarps * 32);  // the buffer is free again
         }
-        if (C::kLater) due = q;
+        place = 2 * share + 1;
         return true;
     });
-    if (C::kLater && ok && due.n > 0) join(due, 0);
 }
 
 template <int D, bool E4M3, int NT>
@@ -760,7 +715,6 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, NT>::kThreads, 1)
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     __shared__ __align__(8) uint64_t full[C::kSlots];
     __shared__ __align__(8) uint64_t empty[C::kSlots];
-    __shared__ __align__(8) uint64_t ready, freed;  // the warps' results: all in the buffer, all joined
     __shared__ int scratch[C::kThreads / 32];
     __shared__ int abort_flag;
     int* pre = reinterpret_cast<int*>(smem + C::kPreOff);
@@ -770,55 +724,91 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, NT>::kThreads, 1)
             mbar_init(&full[s], E4M3 ? 1 + 32 : 1);  // the tile's bytes, and every lane's scales
             mbar_init(&empty[s], C::kGroupWarps);
         }
-        mbar_init(&ready, C::kWarps);
-        mbar_init(&freed, C::kWarps);
         abort_flag = 0;
         fence_mbar_init();
     }
     const long long W = static_cast<long long>(share_tiles<C::kThreads>(p, pre, scratch)) * p.kv.hkv;
-    // the first W % grid blocks take one tile more: blocks without any are the last ones
-    const long long each = W / gridDim.x, more = W % gridDim.x, x = blockIdx.x;
-    const long long w0 = x * each + min(x, more), w1 = w0 + each + (x < more ? 1 : 0);
-    PagedPartial* parts = static_cast<PagedPartial*>(p.workspace) + 2 * blockIdx.x;
-    if (threadIdx.x < 2) parts[threadIdx.x].b = -1;  // until a cut pair says otherwise
+    // Every group has a share; the first W % shares take one tile more, those without any are the last
+    // ones, so share i is group i / grid's of block i % grid: a few tiles go to as many SMs.
+    const int warp = threadIdx.x / 32;
+    const bool loads = warp >= C::kWarps;
+    const int grp = loads ? warp - C::kWarps : warp / C::kGroupWarps, share = grp * gridDim.x + blockIdx.x;
+    const int slot0 = grp * C::kGroupSlots;
+    const long long each = W / (C::kGroups * gridDim.x), more = W % (C::kGroups * gridDim.x);
+    const long long w0 = share * each + min(static_cast<long long>(share), more), w1 = w0 + each + (share < more ? 1 : 0);
+    PagedPartial* parts = static_cast<PagedPartial*>(p.workspace);
+    if (loads && (threadIdx.x & 31) < 2) parts[2 * share + (threadIdx.x & 31)].b = -1;  // until a cut pair says otherwise
     __syncthreads();
     const WaitCtl wc{&abort_flag, p.err, p.timeout_ns};
-    if (threadIdx.x / 32 >= C::kWarps)
-        load_role<D, E4M3, NT>(p, &tk, &tv, smem_u32(smem), smem_u32(smem) + C::kScaleOff, full, empty, pre, w0, w1, wc);
+    if (loads)
+        load_role<D, E4M3, NT>(p, &tk, &tv, smem_u32(smem) + slot0 * C::kSlotBytes, smem_u32(smem) + C::kScaleOff + slot0 * C::kScaleBytes,
+                               full + slot0, empty + slot0, pre, w0, w1, wc);
     else
-        compute_role<D, E4M3, NT>(p, smem, full, empty, &ready, &freed, pre, w0, w1, wc);
+        compute_role<D, E4M3, NT>(p, smem, full + slot0, empty + slot0, pre, share, w0, w1, wc);
 }
 
-// Joins the parts of pairs that were cut.  Block (x, r): if a pair begins in block x of the first
-// kernel and goes on in block x + 1, row r of that pair.
+// Joins the parts of pairs that were cut.  Block (x, r): if a pair begins in share x and goes on in share
+// x + 1, row r of that pair.
 template <int D, bool E4M3>
 __global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__ PagedAttnParams p, int shares) {
     constexpr int kSub = 8;
     __shared__ float so[kSub][D], sl[kSub];
-    __shared__ int hdr[2 * kPagedMaxShares][2];  // pair (sequence and head, -1: none), and whether it begins there
     wait_primary();
     const PagedPartial* parts = static_cast<const PagedPartial*>(p.workspace);
-    for (int i = threadIdx.x; i < 2 * shares; i += 256) {
-        const int b = parts[i].b;
-        hdr[i][0] = b < 0 ? -1 : b * p.kv.hkv + parts[i].h;
-        hdr[i][1] = b < 0 ? 0 : parts[i].begins;
+    const int x = blockIdx.x, r = blockIdx.y, warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+    const int i0 = parts[2 * x + 1].b >= 0 ? 2 * x + 1 : 2 * x;  // the pair of x that goes on: its last cut part
+    const int b = parts[i0].b, h = parts[i0].h;
+    if (b < 0 || !parts[i0].begins) return;
+    int n = 1;  // parts: i0, then the first of every share up to x + n - 1
+    while (x + n < shares) {
+        const int y = x + n + lane;
+        const PagedPartial* q = parts + 2 * y;
+        const bool on = y < shares && q->b == b && q->h == h && !q->begins;
+        const uint32_t v = __ballot_sync(0xffffffffu, on);
+        n += v == 0xffffffffu ? 32 : __ffs(~v) - 1;
+        if (v != 0xffffffffu) break;
     }
-    __syncthreads();
-    const int x = blockIdx.x, r = blockIdx.y;
-    // the pair of x that begins in x and goes on: its last cut part
-    const int i0 = hdr[2 * x + 1][0] >= 0 ? 2 * x + 1 : 2 * x;
-    const int pair = hdr[i0][0];
-    if (pair < 0 || !hdr[i0][1]) return;
-    int x1 = x + 1;  // parts: i0, then the first of every block up to x1
-    while (x1 < shares && hdr[2 * x1][0] == pair && !hdr[2 * x1][1]) ++x1;
-    const int b = pair / p.kv.hkv, h = pair - b * p.kv.hkv;
     const PagedSeq s = paged_seq(p.kv, b);
+    const int R = min(s.T, p.max_q) * p.g;
+    auto part = [&](int k) { return parts + (k == 0 ? i0 : 2 * (x + k)); };
+    if (gridDim.y == 1) {
+        // a row a warp, a part a lane for the weights; the launch says so where pairs have few parts on average
+        for (int r = warp; r < R; r += kSub) {
+            float M = -INFINITY, Ms = -INFINITY;
+            for (int k = lane; k < n; k += 32) {
+                M = fmaxf(M, part(k)->m[r]);
+                Ms = fmaxf(Ms, part(k)->ms[r]);
+            }
+#pragma unroll
+            for (int o = 16; o; o >>= 1) {
+                M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+                Ms = fmaxf(Ms, __shfl_xor_sync(0xffffffffu, Ms, o));
+            }
+            float l = 0.f, acc[4] = {};
+#pragma unroll 8
+            for (int k = 0; k < n; ++k) {
+                const PagedPartial* q = part(k);
+                const float f = paged_weight(q->m[r], M);
+                l = paged_add_weighted(l, paged_weight(q->ms[r], Ms), q->l[r]);
+                if (4 * lane < D) {
+                    const float4 v = *reinterpret_cast<const float4*>(&q->o[r * kPagedMaxD + 4 * lane]);
+                    acc[0] = fmaf(f, v.x, acc[0]);
+                    acc[1] = fmaf(f, v.y, acc[1]);
+                    acc[2] = fmaf(f, v.z, acc[2]);
+                    acc[3] = fmaf(f, v.w, acc[3]);
+                }
+            }
+            const int t = r / p.g, head = h * p.g + r - t * p.g, tok = s.q0 + t;
+            if (4 * lane < D) paged_store4(p, tok, head, 4 * lane, acc, out_factor<E4M3>(M, Ms, l));
+            if (lane == 0) p.lse[tok * p.l_ts + head * p.l_hs] = l == 0.f ? -INFINITY : (Ms + log2f(l)) * kLn2;
+        }
+        return;
+    }
     const int t = r / p.g;
-    if (t >= min(s.T, p.max_q)) return;
-    const int n = x1 - x, warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+    if (r >= R) return;
     float M = -INFINITY, Ms = -INFINITY;
     for (int k = lane; k < n; k += 32) {
-        const PagedPartial* q = parts + (k == 0 ? i0 : 2 * (x + k));
+        const PagedPartial* q = part(k);
         M = fmaxf(M, q->m[r]);
         Ms = fmaxf(Ms, q->ms[r]);
     }
@@ -830,7 +820,7 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__
     float l = 0.f, acc[4] = {};
 #pragma unroll 4
     for (int k = warp; k < n; k += kSub) {
-        const PagedPartial* q = parts + (k == 0 ? i0 : 2 * (x + k));
+        const PagedPartial* q = part(k);
         const float f = paged_weight(q->m[r], M);
         l = paged_add_weighted(l, paged_weight(q->ms[r], Ms), q->l[r]);
         if (4 * lane < D) {
@@ -861,8 +851,10 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__
 }
 
 template <int D, bool E4M3, int NT>
-int launch_t(const PagedAttnParams& p, const PagedMaps& m, int shares, cudaStream_t stream) {
+int launch_t(const PagedAttnParams& p, const PagedMaps& m, int blocks, cudaStream_t stream) {
     using C = Cfg<D, E4M3, NT>;
+    const int shares = blocks * C::kGroups;
+    static_assert(C::kGroups <= kPagedMaxGroups, "room for their results");
     auto kern = paged_decode_kernel<D, E4M3, NT>;
     const int bytes = C::kFixedBytes + 4 * (p.kv.batch + 1);
     static std::atomic<unsigned long long> ready{0};
@@ -871,10 +863,11 @@ int launch_t(const PagedAttnParams& p, const PagedMaps& m, int shares, cudaStrea
                                         C::kFixedBytes + 4 * (kPagedMaxBatch + 1)) == cudaSuccess;
         }))
         return -4;
-    kern<<<shares, C::kThreads, bytes, stream>>>(p, m.k, m.v);
+    kern<<<blocks, C::kThreads, bytes, stream>>>(p, m.k, m.v);
     if (cudaGetLastError() != cudaSuccess) return -4;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(shares, p.max_q * p.g);
+    // fewer than 8 parts a pair on average: one block for all rows of a pair is quicker than one for each
+    cfg.gridDim = dim3(shares, 8LL * p.kv.batch * p.kv.hkv >= shares ? 1 : p.max_q * p.g);
     cfg.blockDim = dim3(256);
     cfg.stream = stream;
     cudaLaunchAttribute at[1];
@@ -887,14 +880,14 @@ int launch_t(const PagedAttnParams& p, const PagedMaps& m, int shares, cudaStrea
 
 }  // namespace
 
-int launch_paged_decode(const PagedAttnParams& p, const PagedMaps& m, int shares, cudaStream_t stream) {
+int launch_paged_decode(const PagedAttnParams& p, const PagedMaps& m, int blocks, cudaStream_t stream) {
     const bool one = p.max_q * p.g <= 8;
     if (p.kv.d == 128) {
-        if (p.kv.e4m3) return one ? launch_t<128, true, 1>(p, m, shares, stream) : launch_t<128, true, 2>(p, m, shares, stream);
-        return one ? launch_t<128, false, 1>(p, m, shares, stream) : launch_t<128, false, 2>(p, m, shares, stream);
+        if (p.kv.e4m3) return one ? launch_t<128, true, 1>(p, m, blocks, stream) : launch_t<128, true, 2>(p, m, blocks, stream);
+        return one ? launch_t<128, false, 1>(p, m, blocks, stream) : launch_t<128, false, 2>(p, m, blocks, stream);
     }
-    if (p.kv.e4m3) return one ? launch_t<64, true, 1>(p, m, shares, stream) : launch_t<64, true, 2>(p, m, shares, stream);
-    return one ? launch_t<64, false, 1>(p, m, shares, stream) : launch_t<64, false, 2>(p, m, shares, stream);
+    if (p.kv.e4m3) return one ? launch_t<64, true, 1>(p, m, blocks, stream) : launch_t<64, true, 2>(p, m, blocks, stream);
+    return one ? launch_t<64, false, 1>(p, m, blocks, stream) : launch_t<64, false, 2>(p, m, blocks, stream);
 }
 
 }  // namespace ra
