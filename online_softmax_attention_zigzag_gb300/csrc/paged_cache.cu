@@ -14,11 +14,11 @@
 // thread, and are bound by HBM once there is enough to move.  The place of a token hangs on four
 // loads one after the other (its sequence, that one's rows and length, the page), so:
 //   * small calls: a thread a piece, which finds its place itself while its rows are on their
-//     way; a decoding step of 64 tokens (8 heads, d = 128, e4m3) takes 2.7 us, 17.5k tokens of d = 64
-//     13.3 us (5.4 TB/s); with a block's shared list of places 3.9 and 17 us.
+//     way; a decoding step of 64 tokens (8 heads, d = 128, e4m3) takes 2.8 us, 17.5k tokens of d = 64
+//     13.8 us (5.2 TB/s); with a block's shared list of places 3.9 and 17 us.
 //   * large calls (more than eight waves of full SMs): a block finds the places of its tokens
 //     once, in shared memory, and every thread moves four pieces with all loads in flight: 32k
-//     tokens into e4m3 37.7 us (5.4 TB/s; a piece a thread 45 us), 131072 out of it 127 us
+//     tokens into e4m3 38 us (5.4 TB/s; a piece a thread 45 us), 131072 out of it 127 us
 //     (6.4 TB/s; 143 us).
 #include <cuda_bf16.h>
 

@@ -24,12 +24,21 @@
 //   * e4m3: eight warps expand codes into the bf16 tiles: exponent and mantissa bits moved into
 //     place are the value times 2^-120, exact for subnormal codes too, and one packed
 //     multiplication by 2^120 * scale finishes it, exact for scales that are powers of two.
+//   * long contexts: the tensor cores' sums are moved to memory every 512 tiles (fold_o).
 //
 //   * calls whose items all have one unit (at most 128 rows a sequence and KV head) have no partner
 //     whose softmax would overlap its products: the scores then alternate between the two units' S
 //     columns, S(j + 2) is issued behind P V(j), and the softmax goes from tile to tile without
 //     waiting for either; half the warps have nothing to do, and the other unit's Q makes room for
 //     e4m3 tiles on their way.
+//
+// What it takes, 64 query and 8 KV heads, d = 128 (the products' floor is the measured 1912 TFLOP/s):
+//     4096 tokens behind 28672, bf16: 2.55 ms, 1615 TFLOP/s, as the ring kernel's in a long loop: bound by
+//     each unit's chain of S, softmax, P V
+//     1024 tokens behind 15360: bf16 343 us (1550), e4m3 397 us (1340): there the expanding warps, 0.5 us
+//     each for V and K and 0.4 us for their scales' addresses, take as long as the two softmaxes
+//     16 x 8 tokens of 1k - 33k keys (one unit): bf16 171 us (5.8 TB/s), e4m3 180 us
+// Short items pay about 9 us each for their first and last tiles and their epilogue.
 //
 // Warps: 0-7 softmax (four a unit), 8 and 9 issue the units' MMAs, 10 loads, 11 lists the block's
 // parts; bf16: 12-15 look values over; e4m3: 12-19 expand and look over.  TMEM as in the ring kernel: S_x at
