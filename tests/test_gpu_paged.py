@@ -611,3 +611,31 @@ def test_outputs_on_16_byte_boundaries(ra, e4m3, out_dtype, d):
         assert ra.sync_status() == ra.RA_OK
         _check_all(B, q, out, lse)
         assert torch.isnan(buf[step:].view(B.total, hq, d + gap)[:, :, d:]).all() and torch.isnan(buf[:step]).all()
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("n", [1, 2])
+def test_one_long_sequence_among_short_ones(ra, e4m3, n):
+    """Its pair lies in most of the shares while the others share theirs: one part joined of two, one of hundreds."""
+    hq, hkv, d = 8, 1, 128
+    g = torch.Generator().manual_seed(95)
+    short = [int(x) for x in torch.randint(n, 300, (90,), generator=g)]
+    B = Batch([(n, x) for x in short[:45]] + [(n, 60001)] + [(n, x) for x in short[45:]], hkv=hkv, d=d, page=32, e4m3=e4m3,
+              device=dev(), seed=96)
+    q = _randn((B.total, hq, d), 97, d ** -0.5).to(dev())
+    o, l = _attend(ra, B, q, torch.float32)
+    assert ra.sync_status() == ra.RA_OK
+    # (few rows in bf16: P is two bf16 halves; in e4m3 fp16, 2^-11; the bound of one bf16 half covers both)
+    _check_all(B, q, o, l)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("n,hq,hkv,L", [(14, 8, 2, 15041), (40, 8, 1, 50000), (300, 4, 1, 20000), (17, 128, 1, 4000)])
+def test_few_long_items(ra, e4m3, n, hq, hkv, L):
+    """Fewer items than blocks: shares of several tiles, blocks without any, an item in dozens of parts."""
+    d = 128
+    B = Batch([(n, L)], hkv=hkv, d=d, page=64, e4m3=e4m3, device=dev(), seed=98)
+    q = _randn((n, hq, d), 99, d ** -0.5).to(dev())
+    o, l = _attend(ra, B, q)
+    assert ra.sync_status() == ra.RA_OK
+    _check_all(B, q, o, l)
