@@ -60,12 +60,15 @@ constexpr float kF16Up = 6.0f;            // p' is kept 2^6 times larger: at mos
 template <int D, bool E4M3, int NT>
 struct Cfg {
     static constexpr int kSlotBytes = kTile * D * (E4M3 ? 1 : 2);
+    // In 8 bits four groups of two warps, with 64 keys of a tile each (two groups with twice the tiles: 32 x 16k keys
+    // 171 us instead of 174, 512 short sequences 95 instead of 76, d = 64 130 instead of 103); in bf16 two groups
+    // of four (d = 64 with four: 165 us instead of 160; d = 128 has slots for two).
     static constexpr int kGroups = E4M3 ? 4 : 2;
-    static constexpr int kDepth = D == 128 ? 1 : 2;        // tiles of a group in shared memory: 128 KB in all
-    static constexpr int kGroupSlots = 2 * kDepth;         // a K and a V tile each
+    static constexpr int kDepth = D == 128 ? 1 : 2;           // tiles of a group in shared memory, 128 KB in all
+    static constexpr int kGroupSlots = 2 * kDepth;            // a K and a V slot each
     static constexpr int kSlots = kGroups * kGroupSlots;
-    static constexpr int kWarps = 8;                             // that compute
-    static constexpr int kThreads = (kWarps + kGroups) * 32;     // and one that loads for every group
+    static constexpr int kWarps = 8;                          // that compute
+    static constexpr int kThreads = (kWarps + kGroups) * 32;  // and one that loads for every group
     static constexpr int kGroupWarps = kWarps / kGroups;
     static constexpr int kKeys = kTile / kGroupWarps;  // of a tile, for a warp
     static constexpr int kOStride = D + 4;             // keeps the fragments' stores off each other's banks
