@@ -426,8 +426,9 @@ int ringattn_cache_read(const ra_paged_kv* kv, void* k_out, void* v_out, ra_stre
  * max_q: at least the largest n_b (host knowledge: it picks the kernel and bounds the work; rows
  *     of a sequence at and behind max_q are not written).
  * Sums, maxima and the running output are fp32; the probabilities are rounded to 16 bits for
- * their product with V.  (The tensor cores truncate their sums: over a million keys of equal weight
- * and values of one sign out may be 5e-4 of itself low.)
+ * their product with V.  (The tensor cores truncate their sums, which end after 32768 keys, or 65536
+ * where a sequence and KV head has more than 16 rows, and are added up rounded to nearest: with values of one
+ * sign out may be 1e-4, or 5e-4, of itself low, however many keys there are.)
  * workspace: DEVICE, at least ringattn_paged_workspace_bytes(total, batch, Hq, Hkv, d, max_q)
  *     bytes, 256-byte aligned; its contents do not matter before or after.  Calls that may
  *     overlap on the GPU, captured ones among them, need one each.

@@ -30,8 +30,8 @@
 //     32 x 16k keys of d = 64, e4m3              129 us, now 103; bf16 165 and 160 (6.6 TB/s)
 //     one sequence of 777 keys                  13.0 us, now 11.4
 // (Boxes that no row sees, behind sinks and before windows, cost nothing: windows 76 us with them, 75 without.)
-// A warp's sums run over its keys of a whole share, and the tensor cores truncate: equal weights over
-// 2^20 keys in one share come out 4.5e-4 low in bf16, 2.4e-5 in e4m3.
+// The tensor cores truncate every addend of a sum, always towards zero, so a warp's sums end after kFold tiles at
+// the latest: a longer part of a share goes in stretches, which are added up in fp32, rounded to nearest.
 // bf16 cache: P goes into its product as two bf16 halves (p = hi + lo, 16 significant bits): the
 // second product costs nothing here, the loads take longer.
 // e4m3 cache: codes become fp16 (one instruction for two, exact), q is brought to fp16's range by
@@ -54,6 +54,10 @@ constexpr int kBar = 1;                   // named barrier of the computing warp
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kRescale = 8.0f;          // the running max moves when it is exceeded by more (log2)
+// Tiles of a stretch.  With unequal weights and values of one sign 2^22 keys in one sum came out 0.7 % low in
+// bf16 and 1.4 % in e4m3; in stretches of 256 tiles 0.005 % and 0.007 %, however many there are.  (Shares of
+// ordinary calls are shorter: 8 x 128k keys in 8 bits are 108 tiles.)
+constexpr int kFold = 256;
 constexpr float kF16Up = 6.0f;            // p' is kept 2^6 times larger: at most 2^(8 + 6 + 1) in fp16
 
 // NT: 8 query rows each
@@ -270,10 +274,11 @@ __device__ __forceinline__ float bf16_add_nonfinite(float acc, uint16_t bits) {
     return (bits & 0x7f80u) == 0x7f80u ? acc + __uint_as_float(static_cast<uint32_t>(bits) << 16) : acc;
 }
 
-// Joins the group's warps' results for part q: rows 8 round .. + 8 of the pair, in turn.  Into the
-// outputs, or, if others have tiles of the pair too, into the workspace.
+// Joins the group's warps' results for tiles [ta, tb) of part q, which is all of it or a stretch: rows 8 round .. + 8 of
+// the pair, in turn.  Into the outputs, or, if others have tiles of the pair too or more stretches
+// follow, into the workspace, where the stretches before this one are.
 template <int D, bool E4M3, int NT>
-__device__ __forceinline__ void join_rows(const PagedAttnParams& p, const uint8_t* smem, Part q, int slot, int round) {
+__device__ __forceinline__ void join_rows(const PagedAttnParams& p, const uint8_t* smem, Part q, int ta, int tb, int slot, int round) {
     using C = Cfg<D, E4M3, NT>;
     constexpr int kWarps = C::kGroupWarps;
     const PagedKV& kv = p.kv;
@@ -285,7 +290,7 @@ __device__ __forceinline__ void join_rows(const PagedAttnParams& p, const uint8_
     const int* sbad = reinterpret_cast<const int*>(smem + C::kMlOff) + 3 * C::kWarps * kRows + w0;
     const PagedSeq s = paged_seq(kv, q.b);
     const int T = min(s.T, p.max_q), R = T * p.g;
-    const bool cut = q.ta > 0 || q.tb < q.n;
+    const bool cut = q.ta > 0 || q.tb < q.n, keep = cut || tb < q.tb, more = ta > q.ta;
     PagedPartial* part = static_cast<PagedPartial*>(p.workspace) + slot;
     if (cut && warp == 0 && lane == 0) {
         part->b = q.b;
@@ -301,7 +306,13 @@ __device__ __forceinline__ void join_rows(const PagedAttnParams& p, const uint8_
             M = fmaxf(M, sm[w * kRows + r]);
             Ms = fmaxf(Ms, sms[w * kRows + r]);
         }
-        float f[kWarps], L = 0.f;
+        float f[kWarps], L = 0.f, f0 = 0.f;
+        if (more) {
+            M = fmaxf(M, part->m[r]);
+            Ms = fmaxf(Ms, part->ms[r]);
+            f0 = paged_weight(part->m[r], M);
+            L = paged_add_weighted(L, paged_weight(part->ms[r], Ms), part->l[r]);
+        }
         bool any_bad = false;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
@@ -312,6 +323,13 @@ __device__ __forceinline__ void join_rows(const PagedAttnParams& p, const uint8_
         const int t = r / p.g, head = q.h * p.g + r - t * p.g, tok = s.q0 + t;
         for (int d = 4 * lane; d < D; d += 128) {
             float acc[4] = {};
+            if (more) {
+                const float4 v = *reinterpret_cast<const float4*>(&part->o[r * kPagedMaxD + d]);
+                acc[0] = f0 * v.x;
+                acc[1] = f0 * v.y;
+                acc[2] = f0 * v.z;
+                acc[3] = f0 * v.w;
+            }
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) {
                 const float4 v = *reinterpret_cast<const float4*>(so + (w * 8 + row8) * C::kOStride + d);
@@ -324,7 +342,7 @@ __device__ __forceinline__ void join_rows(const PagedAttnParams& p, const uint8_
                 const Tiles kt = key_tiles(p, s);
                 const int see_lo = s.base + T - p.window;
                 const int i = s.base + t, rhi = p.causal ? i + 1 : s.L, rlo = p.window > 0 ? i - p.window + 1 : 0;
-                for (int tt = q.ta; tt < q.tb; ++tt) {
+                for (int tt = ta; tt < tb; ++tt) {
                     const int j0 = (tt < kt.ns ? tt : kt.lo + tt - kt.ns) * kTile;
                     if (j0 + kTile <= (p.causal ? s.base + 1 : s.L) && (p.window == 0 || j0 >= see_lo || j0 + kTile <= p.sinks))
                         continue;  // its values went into the product as they are
@@ -339,11 +357,12 @@ __device__ __forceinline__ void join_rows(const PagedAttnParams& p, const uint8_
                     }
                 }
             }
-            if (cut) *reinterpret_cast<float4*>(&part->o[r * kPagedMaxD + d]) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+            if (keep) *reinterpret_cast<float4*>(&part->o[r * kPagedMaxD + d]) = make_float4(acc[0], acc[1], acc[2], acc[3]);
             else paged_store4(p, tok, head, d, acc, out_factor<E4M3>(M, Ms, L));
         }
+        __syncwarp();  // all lanes have what the stretches before left
         if (lane == 0) {
-            if (cut) {
+            if (keep) {
                 part->m[r] = M;
                 part->ms[r] = Ms;
                 part->l[r] = L;
@@ -372,7 +391,7 @@ __device__ void compute_role(const PagedAttnParams& p, uint8_t* smem, uint64_t* 
     uint32_t done = 0;  // tiles so far
     bool ok = true;
     int place = 2 * share;  // for a part that is cut: the first one's, then the others'
-    for_each_part(p, pre, w0, w1, [&](const Part& q) -> bool {
+    auto stretch = [&](const Part& q, int ta, int tb) -> bool {  // tiles [ta, tb) of part q
         const PagedSeq s = paged_seq(kv, q.b);
         const Tiles kt = key_tiles(p, s);
         const int T = min(s.T, p.max_q), R = T * p.g;
@@ -438,7 +457,7 @@ __device__ void compute_role(const PagedAttnParams& p, uint8_t* smem, uint64_t* 
             }
         bool bad_v = false;  // a value that is no number, in a tile that not every row sees whole
         const int see_lo = s.base + T - p.window;  // the window of the last row begins here
-        for (int t = q.ta; t < q.tb; ++t, ++done) {
+        for (int t = ta; t < tb; ++t, ++done) {
             const int j0 = (t < kt.ns ? t : kt.lo + t - kt.ns) * kTile;
             // does every row see every key of the tile?
             const bool whole = j0 + kTile <= (p.causal ? s.base + 1 : s.L) &&
@@ -705,9 +724,14 @@ __device__ void compute_role(const PagedAttnParams& p, uint8_t* smem, uint64_t* 
                 }
             // (a warp that gave up still comes here, so that none waits for it)
             if (!named_bar_and(kBar + grp, C::kGroupWarps * 32, ok)) return false;
-            join_rows<D, E4M3, NT>(p, smem, q, place, x);
+            join_rows<D, E4M3, NT>(p, smem, q, ta, tb, place, x);
             named_bar_sync(kBar + grp, C::kGroupWarps * 32);  // the buffer is free again
         }
+        return true;
+    };
+    for_each_part(p, pre, w0, w1, [&](const Part& q) -> bool {
+        for (int ta = q.ta; ta < q.tb; ta += kFold)
+            if (!stretch(q, ta, min(q.tb, ta + kFold))) return false;
         place = 2 * share + 1;
         return true;
     });
