@@ -421,7 +421,8 @@ int ringattn_cache_read(const ra_paged_kv* kv, void* k_out, void* v_out, ra_stre
  *     causal = 0:  all of them (window must be 0).
  * kv head h / (Hq / Hkv); no 1/sqrt(d) scale.  The keys must have been appended, the new
  * tokens' own among them.  A row that sees no key gets out = 0, lse = -inf.  What a row does
- * not see does not touch it, infinities and NaN in K or V included.  (out, lse) of calls over
+ * not see does not touch it, infinities and NaN in K or V included; an infinite v that it sees (bf16, with a
+ * weight of at least 2^-113 of its largest) makes that element of out the infinity, as in the definition.  (out, lse) of calls over
  * disjoint keys combine with ringattn_merge when out is fp32.
  * max_q: at least the largest n_b (host knowledge: it picks the kernel and bounds the work; rows
  *     of a sequence at and behind max_q are not written).

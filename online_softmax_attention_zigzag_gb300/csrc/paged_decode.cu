@@ -32,8 +32,10 @@
 // (Boxes that no row sees, behind sinks and before windows, cost nothing: windows 76 us with them, 75 without.)
 // The tensor cores truncate every addend of a sum, always towards zero, so a warp's sums end after kFold tiles at
 // the latest: a longer part of a share goes in stretches, which are added up in fp32, rounded to nearest.
-// bf16 cache: P goes into its product as two bf16 halves (p = hi + lo, 16 significant bits): the
-// second product costs nothing here, the loads take longer.
+// bf16 cache: P goes into its product as two bf16 halves (p = hi + lo to 2^-15): the second product costs
+// nothing here, the loads take longer.  hi is p cut off and lo a trifle above the rest, so that both are above
+// zero where p is, and an infinite v makes out that infinity: infinity * 0, and infinities of both
+// signs where lo is negative, would be no numbers.
 // e4m3 cache: codes become fp16 (one instruction for two, exact), q is brought to fp16's range by
 // a power of two per row (elements below 2^-28 of the row's largest lose bits), the K scale
 // multiplies the score, and the V scale enters the exponent: with v_j = 2^(a_j) u_j,
@@ -54,6 +56,7 @@ constexpr int kBar = 1;                   // named barrier of the computing warp
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kRescale = 8.0f;          // the running max moves when it is exceeded by more (log2)
+constexpr float kAbove = 1.f + 0x1p-20f;  // keeps p - hi above zero where hi is p (2^-20 of p, far below lo's rounding)
 // Tiles of a stretch.  With unequal weights and values of one sign 2^22 keys in one sum came out 0.7 % low in
 // bf16 and 1.4 % in e4m3; in stretches of 256 tiles 0.005 % and 0.007 %, however many there are.  (Shares of
 // ordinary calls are shorter: 8 x 128k keys in 8 bits are 108 tiles.)
@@ -609,9 +612,10 @@ __device__ void compute_role(const PagedAttnParams& p, uint8_t* smem, uint64_t* 
                         } else {
                             l[z][0] += a;
                             l[z][1] += b;
-                            const uint32_t w = pack_bf16x2(a, b);
-                            pa[n][z][h] = transpose8(w);
-                            pb[n][z][h] = transpose8(pack_bf16x2(a - __uint_as_float(w << 16), b - __uint_as_float(w & 0xffff0000u)));
+                            const uint32_t ua = __float_as_uint(a), ub = __float_as_uint(b);
+                            pa[n][z][h] = transpose8(__byte_perm(ua, ub, 0x7632));
+                            pb[n][z][h] = transpose8(pack_bf16x2(fmaf(a, kAbove, -__uint_as_float(ua & 0xffff0000u)),
+                                                                 fmaf(b, kAbove, -__uint_as_float(ub & 0xffff0000u))));
                         }
                     }
             }
