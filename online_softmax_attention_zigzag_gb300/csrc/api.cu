@@ -831,6 +831,7 @@ int ringattn_cache_append(const void* k_new, const void* v_new, long long k_toke
     if (static_cast<long long>(p.kv.total) * p.kv.hkv > INT_MAX) return RA_ERR_UNSUPPORTED;
     DeviceInfo* dev = nullptr;
     if ((st = device_info(&dev)) != RA_OK) return st;
+    p.err = dev->err;
     p.k_in = k_new;
     p.v_in = v_new;
     p.k_ts = k_token_stride;
@@ -849,6 +850,7 @@ int ringattn_cache_read(const ra_paged_kv* kv, void* k_out, void* v_out, ra_stre
     if (static_cast<long long>(p.kv.total) * p.kv.hkv > INT_MAX) return RA_ERR_UNSUPPORTED;
     DeviceInfo* dev = nullptr;
     if ((st = device_info(&dev)) != RA_OK) return st;
+    p.err = dev->err;
     p.k_out = k_out;
     p.v_out = v_out;
     return ra::launch_cache_read(p, dev->sms, reinterpret_cast<cudaStream_t>(stream));

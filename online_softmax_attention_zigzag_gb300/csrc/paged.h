@@ -8,6 +8,7 @@
 #include <atomic>
 
 #include "fastdiv.h"
+#include "internal.h"
 
 namespace ra {
 
@@ -22,6 +23,17 @@ bool once_a_device(std::atomic<unsigned long long>& done, F&& f) {
     done.fetch_or(bit, std::memory_order_release);
     return true;
 }
+
+// Sites of the check build (internal.h): every index that the paged kernels derive from the batch's arrays
+// and their own division of the work.
+enum PagedCheckSite : int {
+    kSitePagedToken = 51,  // a row of the caller's k, v or q, and of cache_read's output
+    kSitePagedPlace = 52,  // a row of the pool and its scale
+    kSitePagedBox = 53,    // a TMA box of the pool
+    kSitePagedShare = 54,  // a block's or group's part of the work
+    kSitePagedPartial = 55,  // its place among the partial results
+    kSitePagedOut = 56       // a row of out and lse
+};
 
 constexpr int kPagedMaxBatch = 4096;  // RINGATTN_PAGED_MAX_BATCH
 constexpr int kPagedTile = 128;       // keys of a tile
@@ -69,6 +81,7 @@ struct PagedCopyParams {  // append: token-major rows in; read: [Hkv, total, d] 
     long long k_ts, k_hs, v_ts, v_hs;  // token and head strides of k_in, v_in
     void* k_out;
     void* v_out;
+    int* err;    // device error word (check build)
     int tokens;  // of a block (set by the launcher, with the two divisions)
     FastDiv by_heads, by_tokens;
 };
@@ -139,6 +152,14 @@ __device__ __forceinline__ int paged_checked(const PagedKV& kv, int entry) {
     return (entry >= 0 && entry < kv.n_pages) ? entry : -1;
 }
 
+// What the check build asks of an index: row `row` of page pg and head h; rows of one page; a row of a call's tokens.
+__device__ __forceinline__ bool paged_place_ok(const PagedKV& kv, int pg, int h, int row, int rows = 1) {
+    return pg >= 0 && pg < kv.n_pages && h >= 0 && h < kv.hkv && row >= 0 && row + rows <= kv.page;
+}
+__device__ __forceinline__ bool paged_row_ok(const PagedKV& kv, int heads, long long t, int h) {
+    return t >= 0 && t < kv.total && h >= 0 && h < heads;
+}
+
 // The sequence whose rows hold row t (cu[b] <= t < cu[b + 1]), -1 if none does.  cu may be in
 // shared memory.
 __device__ __forceinline__ int paged_find(const int* cu, int batch, int t) {
@@ -167,6 +188,7 @@ __device__ __forceinline__ float paged_add_weighted(float sum, float w, float x)
 // Four elements of an output row, times inv, in the caller's type.
 __device__ __forceinline__ void paged_store4(const PagedAttnParams& p, int tok, int head, int d, const float (&x)[4],
                                              float inv) {
+    if (!RA_CHECKED(paged_row_ok(p.kv, p.hq, tok, head) && d >= 0 && d + 4 <= p.kv.d, p.err, kSitePagedOut)) return;
     const long long at = tok * p.o_ts + head * p.o_hs + d;
     if (p.out_f32) {
         *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) =
@@ -177,6 +199,12 @@ __device__ __forceinline__ void paged_store4(const PagedAttnParams& p, int tok, 
         asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w.y) : "f"(x[3] * inv), "f"(x[2] * inv));
         *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at) = w;
     }
+}
+
+// lse of an output row: M + log2 l, in natural units; no key at all has l = 0.
+__device__ __forceinline__ void paged_store_lse(const PagedAttnParams& p, int tok, int head, float M, float l) {
+    if (!RA_CHECKED(paged_row_ok(p.kv, p.hq, tok, head), p.err, kSitePagedOut)) return;
+    p.lse[tok * p.l_ts + head * p.l_hs] = l == 0.f ? -INFINITY : (M + log2f(l)) * 0.69314718055994531f;
 }
 #endif
 

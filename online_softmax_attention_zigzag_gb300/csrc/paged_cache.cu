@@ -151,6 +151,8 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
             tl[u] = static_cast<int>(fdiv(static_cast<unsigned>(r), p.by_heads));
             h[u] = r - tl[u] * kv.hkv;
             const long long t = t0 + tl[u];
+            xk[u] = xv[u] = make_uint4(0, 0, 0, 0);
+            if (!RA_CHECKED(paged_row_ok(kv, kv.hkv, t, h[u]), p.err, kSitePagedToken)) continue;
             xk[u] = ld_stream(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.k_in) + t * p.k_ts + h[u] * p.k_hs) + part);
             xv[u] = ld_stream(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.v_in) + t * p.v_ts + h[u] * p.v_hs) + part);
         }
@@ -168,6 +170,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
                     row = w.row[tl[u]];
                 }
             }
+            if (pg >= 0 && !RA_CHECKED(paged_place_ok(kv, pg, h[u], row), p.err, kSitePagedPlace)) pg = -1;
             const long long at = static_cast<long long>(h[u]) * kv.page + row;  // row inside the page
             if (E4M3) {
                 float sk, sv;
@@ -225,8 +228,9 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const __grid_constant__ 
                 pg = w.page[tl];
                 row = w.row[tl];
             }
+            if (!RA_CHECKED(paged_row_ok(kv, kv.hkv, t0 + tl, h), p.err, kSitePagedToken)) continue;
             to[u] = (static_cast<long long>(h) * kv.total + t0 + tl) * LPR + part;
-            if (pg < 0) continue;
+            if (pg < 0 || !RA_CHECKED(paged_place_ok(kv, pg, h, row), p.err, kSitePagedPlace)) continue;
             const long long at = static_cast<long long>(h) * kv.page + row;
             if (E4M3) {
                 ck[u] = ld_stream(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(kv.k) + pg * kv.k_ps + at * (8 * LPR)) + part);

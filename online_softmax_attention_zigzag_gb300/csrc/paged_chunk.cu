@@ -54,7 +54,6 @@ namespace {
 constexpr int kTile = kPagedTile;
 constexpr int kMmaWarp = 8, kLoadWarp = 10, kExpandWarp = 12;  // (11 lists)
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kRescaleLog2 = 8.0f;
 constexpr int kPBar = 1;                   // named barriers kPBar + x: unit x's P is written
 constexpr int kPBarThreads = 4 * 32 + 32;  // its softmax warps and its issuer
@@ -346,6 +345,10 @@ __device__ __forceinline__ void for_each_part(const PagedAttnParams& p, F&& f) {
             q.h = it.h;
             q.ta = static_cast<int>(skip);
             q.tb = round < rounds ? q.c.n : static_cast<int>(min(static_cast<long long>(q.c.n), q.ta + (w1 - w)));
+            if (!RA_CHECKED(it.b >= 0 && it.b < B && it.h >= 0 && it.h < H && it.e >= plan.base[it.b] && it.e < plan.base[it.b + 1] &&
+                                q.c.ta < q.c.tb && q.ta >= 0 && q.ta < q.tb && q.tb <= q.c.n,
+                            p.err, kSitePagedShare))
+                return;
             if (!f(q)) return;
             ++q.k;
             if (round < rounds) break;
@@ -445,9 +448,10 @@ __device__ void load_role(const PagedAttnParams& p, const CUtensorMap* tq, const
             ++qit[x];
             if (lane == 0) {
                 mbar_arrive_expect_tx(&b.q_full[x], q_bytes);
+                int tok = q.c.s.q0 + q.c.ta + x * p.unit_tokens;
+                if (!RA_CHECKED(paged_row_ok(kv, p.hq, tok, q.h * p.g + p.g - 1), p.err, kSitePagedToken)) tok = 0;
                 for (int i = 0; i < C::kBoxes; ++i)
-                    tma_load_3d(smem + x * C::kTileBytes + i * C::kBoxBytes, tq, &b.q_full[x], i * 64, q.h * p.g,
-                                q.c.s.q0 + q.c.ta + x * p.unit_tokens, stream);
+                    tma_load_3d(smem + x * C::kTileBytes + i * C::kBoxBytes, tq, &b.q_full[x], i * 64, q.h * p.g, tok, stream);
             }
             __syncwarp();
         }
@@ -465,7 +469,9 @@ __device__ void load_role(const PagedAttnParams& p, const CUtensorMap* tq, const
         };
         look(q.ta);
         for (int t = q.ta; t < q.tb + ahead; ++t) {
-            const int pg = paged_checked(kv, entry), y = q.h * kv.page + row;
+            int pg = paged_checked(kv, entry);
+            if (pg >= 0 && !RA_CHECKED(paged_place_ok(kv, pg, q.h, row, rows), p.err, kSitePagedBox)) pg = -1;
+            const int y = q.h * kv.page + row;
             if (t + 1 < q.tb) look(t + 1);
             const bool has_v = t >= q.ta + ahead, has_k = t < q.tb;
             if (ahead == 1) {
@@ -667,7 +673,8 @@ __device__ void expand_role(const PagedAttnParams& p, uint32_t smem, Bars& b, co
             if (t < q.tb && pos < q.c.hi) entry = paged_entry(kv, q.c.b, pos, row);
         };
         auto fetch = [&]() {
-            const int pg = paged_checked(kv, entry);
+            int pg = paged_checked(kv, entry);
+            if (pg >= 0 && !RA_CHECKED(paged_place_ok(kv, pg, q.h, row), p.err, kSitePagedPlace)) pg = -1;
             const long long at = static_cast<long long>(q.h) * kv.page + row;
             ks = pg >= 0 ? __ldg(kv.k_scale + pg * kv.ks_ps + at) : 0.f;
             vs = pg >= 0 ? __ldg(kv.v_scale + pg * kv.vs_ps + at) : 0.f;
@@ -897,7 +904,7 @@ __device__ __noinline__ void add_sick(const PagedAttnParams& p, const Chunk& c, 
             if (j < lo && j >= p.sinks) continue;
             int r;
             const int pg = paged_page(p.kv, c.b, j, r);
-            if (pg < 0) continue;
+            if (pg < 0 || !RA_CHECKED(paged_place_ok(p.kv, pg, h, r), p.err, kSitePagedPlace)) continue;
             const long long at = static_cast<long long>(h) * p.kv.page + r;
             if constexpr (E4M3) {
                 if (fabsf(__ldg(p.kv.v_scale + pg * p.kv.vs_ps + at)) < INFINITY) continue;
@@ -1089,10 +1096,11 @@ __device__ void softmax_role(const PagedAttnParams& p, int x, Bars& b, const Par
         ++iit;
         tc_fence_after();
         const bool cut = q.ta > 0 || q.tb < q.c.n;
-        const bool live = row < p.unit_tokens * p.g && t_row < q.c.tb;
         const bool sick = poison[q.k % kPoison] == q.k + 1;
         const float inv = lr == 0.f ? 0.f : 1.f / lr;
         const int tok = q.c.s.q0 + t_row, head = q.h * p.g + row - tok_in * p.g;
+        const bool live = row < p.unit_tokens * p.g && t_row < q.c.tb && RA_CHECKED(paged_row_ok(p.kv, p.hq, tok, head), p.err, kSitePagedOut) &&
+                          RA_CHECKED(q.slot == 0 || q.slot == 1, p.err, kSitePagedPartial);
         PagedChunkPartial* part = static_cast<PagedChunkPartial*>(p.workspace) + 2 * blockIdx.x + q.slot;
         const int r2 = x * kTile + row;
         if (!cut && !sick && !p.out_f32 && q.tb - q.ta <= kFold) {  // the usual end, with all loads in flight at once
@@ -1111,7 +1119,7 @@ __device__ void softmax_role(const PagedAttnParams& p, int x, Bars& b, const Par
                         w[i] = pack_bf16x2(__uint_as_float(o[c][2 * i]) * inv, __uint_as_float(o[c][2 * i + 1]) * inv);
                     store_row(static_cast<uint16_t*>(p.out) + tok * p.o_ts + head * p.o_hs + c * 32, w, p.out_wide);
                 }
-                p.lse[tok * p.l_ts + head * p.l_hs] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+                paged_store_lse(p, tok, head, m, l);
             }
             return true;
         }
@@ -1169,14 +1177,14 @@ __device__ void softmax_role(const PagedAttnParams& p, int x, Bars& b, const Par
                 part->l[r2] = l;
                 part->lr[r2] = lr;
             }
-            if (x == 0 && row == 0) {
+            if (x == 0 && row == 0 && live) {
                 part->b = q.c.b;
                 part->pair = q.c.pair;
                 part->h = q.h;
                 part->begins = q.ta == 0;
             }
         } else if (live) {
-            p.lse[tok * p.l_ts + head * p.l_hs] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+            paged_store_lse(p, tok, head, m, l);
         }
         return true;
     });
@@ -1279,6 +1287,7 @@ __global__ void __launch_bounds__(kJoinRows * D / 4) paged_chunk_join_kernel(con
     const PagedChunkPartial* p0 = parts + 2 * x + (parts[2 * x + 1].b >= 0 ? 1 : 0);
     const int b = p0->b, pair = p0->pair, h = p0->h;
     if (b < 0 || !p0->begins) return;
+    if (!RA_CHECKED(b < p.kv.batch && pair >= 0 && h >= 0 && h < p.kv.hkv, p.err, kSitePagedPartial)) return;
     const Chunk c = make_chunk(p, b, pair, paged_seq(p.kv, b));
     int n = 1;  // parts: p0, then the first ones of the blocks up to x + n - 1 (that have a filling)
     while (x + n < shares) {
@@ -1324,7 +1333,7 @@ __global__ void __launch_bounds__(kJoinRows * D / 4) paged_chunk_join_kernel(con
     if (ru >= rows || t >= c.tb) return;
     const int tok = c.s.q0 + t, head = h * p.g + ru % p.g;
     paged_store4(p, tok, head, 4 * col, acc, lr == 0.f ? 0.f : 1.f / lr);
-    if (col == 0) p.lse[tok * p.l_ts + head * p.l_hs] = l == 0.f ? -INFINITY : (M + log2f(l)) * kLn2;
+    if (col == 0) paged_store_lse(p, tok, head, M, l);
 }
 
 template <class... Args>

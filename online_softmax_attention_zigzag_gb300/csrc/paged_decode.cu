@@ -54,7 +54,6 @@ constexpr int kTile = kPagedTile;         // keys of a tile
 constexpr int kRows = 16;
 constexpr int kBar = 1;                   // named barrier of the computing warps
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kRescale = 8.0f;          // the running max moves when it is exceeded by more (log2)
 constexpr float kAbove = 1.f + 0x1p-20f;  // keeps p - hi above zero where hi is p (2^-20 of p, far below lo's rounding)
 // Tiles of a stretch.  With unequal weights and values of one sign 2^22 keys in one sum came out 0.7 % low in
@@ -162,6 +161,8 @@ __device__ __forceinline__ void for_each_part(const PagedAttnParams& p, const in
     long long w = w0;
     while (true) {
         q.tb = static_cast<int>(min(static_cast<long long>(q.n), q.ta + (w1 - w)));
+        if (!RA_CHECKED(q.b >= 0 && q.b < p.kv.batch && q.h >= 0 && q.h < H && q.ta >= 0 && q.ta < q.tb && q.tb <= q.n, p.err, kSitePagedShare))
+            return;
         if (!f(q)) return;
         w += q.tb - q.ta;
         if (w >= w1) return;
@@ -194,6 +195,7 @@ __device__ void load_role(const PagedAttnParams& p, const CUtensorMap* tk, const
         // q on its way to L1 for the warps that compute, who come here later
         for (int i = lane; i < min(s.T, p.max_q) * p.g * (D / 32); i += 32) {
             const int r = i / (D / 32), t = r / p.g;
+            if (!RA_CHECKED(paged_row_ok(kv, p.hq, s.q0 + t, q.h * p.g + r - t * p.g), p.err, kSitePagedToken)) continue;
             const uint16_t* src = static_cast<const uint16_t*>(p.q) + (s.q0 + t) * p.q_ts + (q.h * p.g + r - t * p.g) * p.q_hs;
             asm volatile("prefetch.global.L1 [%0];" ::"l"(src + (i % (D / 32)) * 32));
         }
@@ -208,7 +210,9 @@ __device__ void load_role(const PagedAttnParams& p, const CUtensorMap* tk, const
         };
         look(q.ta);
         for (int t = q.ta; t < q.tb; ++t, ++n) {
-            const int pg = paged_checked(kv, entry), y = q.h * kv.page + row;
+            int pg = paged_checked(kv, entry);
+            if (pg >= 0 && !RA_CHECKED(paged_place_ok(kv, pg, q.h, row, rows), p.err, kSitePagedBox)) pg = -1;
+            const int y = q.h * kv.page + row;
             if (t + 1 < q.tb) look(t + 1);
 #pragma unroll
             for (half = 0; half < 2; ++half) {  // K, then V
@@ -232,8 +236,8 @@ __device__ void load_role(const PagedAttnParams& p, const CUtensorMap* tk, const
                     const int of = __shfl_sync(0xffffffffu, pg, (4 * lane) >> log_rows);
                     const int at = __shfl_sync(0xffffffffu, y, (4 * lane) >> log_rows) + ((4 * lane) & (rows - 1));
                     const float* src = half ? kv.v_scale : kv.k_scale;
-                    copy16_async(scales + slot * C::kScaleBytes + lane * 16, of >= 0 ? src + of * (half ? kv.vs_ps : kv.ks_ps) + at : src,
-                                 of >= 0);
+                    const bool on = of >= 0 && RA_CHECKED(paged_place_ok(kv, of, q.h, at - q.h * kv.page, 4), p.err, kSitePagedPlace);
+                    copy16_async(scales + slot * C::kScaleBytes + lane * 16, on ? src + of * (half ? kv.vs_ps : kv.ks_ps) + at : src, on);
                     copies_arrive(&full[slot]);
                 }
             }
@@ -294,6 +298,7 @@ __device__ __forceinline__ void join_rows(const PagedAttnParams& p, const uint8_
     const PagedSeq s = paged_seq(kv, q.b);
     const int T = min(s.T, p.max_q), R = T * p.g;
     const bool cut = q.ta > 0 || q.tb < q.n, keep = cut || tb < q.tb, more = ta > q.ta;
+    if (!RA_CHECKED(slot >= 0 && slot < 2 * C::kGroups * static_cast<int>(gridDim.x) && R <= kRows, p.err, kSitePagedPartial)) return;
     PagedPartial* part = static_cast<PagedPartial*>(p.workspace) + slot;
     if (cut && warp == 0 && lane == 0) {
         part->b = q.b;
@@ -353,7 +358,7 @@ __device__ __forceinline__ void join_rows(const PagedAttnParams& p, const uint8_
                         if (p.window > 0 && j < rlo && j >= p.sinks) continue;
                         int in;
                         const int pg = paged_page(kv, q.b, j, in);
-                        if (pg < 0) continue;
+                        if (pg < 0 || !RA_CHECKED(paged_place_ok(kv, pg, q.h, in), p.err, kSitePagedPlace)) continue;
                         const uint16_t* v = static_cast<const uint16_t*>(kv.v) + pg * kv.v_ps + (static_cast<long long>(q.h) * kv.page + in) * D + d;
 #pragma unroll
                         for (int e = 0; e < 4; ++e) acc[e] = bf16_add_nonfinite(acc[e], v[e]);
@@ -370,7 +375,7 @@ __device__ __forceinline__ void join_rows(const PagedAttnParams& p, const uint8_
                 part->ms[r] = Ms;
                 part->l[r] = L;
             } else {
-                p.lse[tok * p.l_ts + head * p.l_hs] = L == 0.f ? -INFINITY : (Ms + log2f(L)) * kLn2;
+                paged_store_lse(p, tok, head, Ms, L);
             }
         }
     }
@@ -406,7 +411,7 @@ __device__ void compute_role(const PagedAttnParams& p, uint8_t* smem, uint64_t* 
         for (int x = 0; x < NT; ++x) {
             const int r = 8 * x + r8, t = r / p.g;
             const uint16_t* src = static_cast<const uint16_t*>(p.q) + (s.q0 + t) * p.q_ts + (q.h * p.g + r - t * p.g) * p.q_hs;
-            const bool live = r < R;
+            const bool live = r < R && RA_CHECKED(paged_row_ok(kv, p.hq, s.q0 + t, q.h * p.g + r - t * p.g), p.err, kSitePagedToken);
             if constexpr (E4M3) {
                 uint2 w[D / 16];
                 uint32_t m = 0;
@@ -794,6 +799,7 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__
     const int i0 = parts[2 * x + 1].b >= 0 ? 2 * x + 1 : 2 * x;  // the pair of x that goes on: its last cut part
     const int b = parts[i0].b, h = parts[i0].h;
     if (b < 0 || !parts[i0].begins) return;
+    if (!RA_CHECKED(b < p.kv.batch && h >= 0 && h < p.kv.hkv, p.err, kSitePagedPartial)) return;
     int n = 1;  // parts: i0, then the first of every share up to x + n - 1
     while (x + n < shares) {
         const int y = x + n + lane;
@@ -835,7 +841,7 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__
             }
             const int t = r / p.g, head = h * p.g + r - t * p.g, tok = s.q0 + t;
             if (4 * lane < D) paged_store4(p, tok, head, 4 * lane, acc, out_factor<E4M3>(M, Ms, l));
-            if (lane == 0) p.lse[tok * p.l_ts + head * p.l_hs] = l == 0.f ? -INFINITY : (Ms + log2f(l)) * kLn2;
+            if (lane == 0) paged_store_lse(p, tok, head, Ms, l);
         }
         return;
     }
@@ -882,7 +888,7 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__
             for (int e = 0; e < 4; ++e) v[e] += so[w][4 * lane + e];
         paged_store4(p, tok, head, 4 * lane, v, out_factor<E4M3>(M, Ms, l));
     }
-    if (lane == 0) p.lse[tok * p.l_ts + head * p.l_hs] = l == 0.f ? -INFINITY : (Ms + log2f(l)) * kLn2;
+    if (lane == 0) paged_store_lse(p, tok, head, Ms, l);
 }
 
 template <int D, bool E4M3, int NT>
