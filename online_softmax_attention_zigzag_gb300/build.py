@@ -12,6 +12,7 @@ loads it when RINGATTN_CHECK=1).
 from __future__ import annotations
 
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -43,12 +44,29 @@ def _run(cmd):
     return r.returncode, r.stdout
 
 
+def check_registers(src: str, text: str, log: str) -> None:
+    """A kernel that hands registers from some warps to others counts on what it starts with (a constant
+    ``kStartRegs`` of its source, for e4m3 and for bf16): more or fewer, and the library would refuse every call of
+    it.  Compares with what ptxas said (``-Xptxas -v``) and raises where they differ."""
+    want = re.search(r"kStartRegs = E4M3 \? (\d+) : (\d+)", text)
+    if not want:
+        return
+    used = re.findall(r"Compiling entry function '\w*paged_chunk_kernelILi\d+ELb([01])E.*?Used (\d+) registers", log, re.S)
+    if len(used) != 8:
+        raise RuntimeError(f"{src}: registers of {len(used)} kernels found, 8 expected")
+    for e4m3, n in used:
+        w = want.group(1 if e4m3 == "1" else 2)
+        if n != w:
+            raise RuntimeError(f"{src}: this compiler gives paged_chunk_kernel ({'e4m3' if e4m3 == '1' else 'bf16'}) {n} registers, "
+                               f"its split counts on {w} (kStartRegs)")
+
+
 def _objects(nvcc, variant, extra):
     """(source, command, object) for every translation unit of one library variant."""
     jobs = []
     for src in SOURCES:
         obj = os.path.join(BUILD, variant, src.replace(".cu", ".o"))
-        jobs.append((src, [nvcc, *ARCH, *FLAGS, *extra, "-c", os.path.join(CSRC, src), "-o", obj], obj))
+        jobs.append((src, [nvcc, *ARCH, *FLAGS, *extra, "-Xptxas", "-v", "-c", os.path.join(CSRC, src), "-o", obj], obj))
     return jobs
 
 
@@ -56,17 +74,19 @@ def build(verbose: bool = False) -> str:
     """Compile libringattn.so and the check build libringattn_check.so (-DRA_CHECK: index
     checks that record RA_ERR_BOUNDS), all translation units of both in parallel."""
     nvcc = _nvcc()
-    extra = ["-Xptxas", "-v"] if verbose else []
     variants = {"release": (LIB, []), "check": (LIB_CHECK, ["-DRA_CHECK"])}
     jobs = {}
     for name, (_, defs) in variants.items():
         os.makedirs(os.path.join(BUILD, name), exist_ok=True)
-        jobs[name] = _objects(nvcc, name, [*defs, *extra])
+        jobs[name] = _objects(nvcc, name, defs)
     flat = [j for js in jobs.values() for j in js]
     with ThreadPoolExecutor(max_workers=len(flat)) as ex:
         results = list(ex.map(lambda j: (j[0], *_run(j[1])), flat))
     failed = False
     for src, rc, out in results:
+        if rc == 0:
+            with open(os.path.join(CSRC, src)) as f:
+                check_registers(src, f.read(), out)
         if rc != 0 or verbose:
             sys.stdout.write(f"== {src} (rc={rc})\n{out}")
         failed |= rc != 0

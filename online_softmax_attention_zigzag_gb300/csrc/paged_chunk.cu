@@ -1358,7 +1358,7 @@ int launch_t(const PagedAttnParams& p, const PagedMaps& m, int shares, cudaStrea
     static std::atomic<unsigned long long> ready{0};
     if (!once_a_device(ready, [&] {
             if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes) != cudaSuccess) return false;
-            // the register split adds up only if the block starts with as many as it counts on
+            // the register split adds up only if the block starts with as many as it counts on (the build has checked it)
             cudaFuncAttributes a;
             return cudaFuncGetAttributes(&a, kern) == cudaSuccess && a.numRegs == C::kStartRegs;
         }))
