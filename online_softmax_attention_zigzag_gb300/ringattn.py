@@ -419,6 +419,13 @@ def _paged(k_cache, v_cache, k_scale, v_scale, block_table, cu, kv_len, total: i
                              t0 if batch > 1 else max_pages, n, page, h, d, e4m3, batch, max_pages, total)
 
 
+def _ints(**numbers) -> None:
+    """ctypes drops the upper bits of a number that no C int holds; these calls refuse it."""
+    for name, x in numbers.items():
+        if not -2 ** 31 <= x < 2 ** 31:
+            raise ValueError(f"{name} must be a 32-bit number, got {x}")
+
+
 def _raw_stream(stream, dev: int) -> int:
     """As :func:`_stream`, without making a Stream object for the current one."""
     return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
@@ -459,6 +466,7 @@ def cache_read(k_cache, v_cache, k_out, v_out, block_table, cu, kv_len, *, k_sca
 
 def paged_workspace_bytes(total: int, batch: int, Hq: int, Hkv: int, d: int, max_q: int) -> int:
     """ringattn_paged_workspace_bytes (host only)."""
+    _ints(total=total, batch=batch, Hq=Hq, Hkv=Hkv, d=d, max_q=max_q)
     n = ctypes.c_longlong(0)
     _check("ringattn_paged_workspace_bytes", lib().ringattn_paged_workspace_bytes(
         total, batch, Hq, Hkv, d, max_q, ctypes.byref(n)))
@@ -472,6 +480,8 @@ def fwd_paged(q, k_cache, v_cache, out, lse, block_table, cu, kv_len, workspace,
     strides).  With window > 0 a row at position i sees j in (i - window, i] and the first
     ``sinks`` positions.  max_q: at least the most rows of one sequence; workspace: a CUDA uint8
     tensor of at least :func:`paged_workspace_bytes`.  The cache as for :func:`cache_append`."""
+    if (max_q | causal | window | sinks) >> 31:
+        _ints(max_q=max_q, causal=causal, window=window, sinks=sinks)
     dev = torch.cuda.current_device()
     f32 = out.dtype is torch.float32
     qp, q0, q1 = _rows(q, "q", torch.bfloat16, dev)
