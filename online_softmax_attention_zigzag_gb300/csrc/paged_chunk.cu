@@ -1096,11 +1096,12 @@ __device__ void softmax_role(const PagedAttnParams& p, int x, Bars& b, const Par
         ++iit;
         tc_fence_after();
         const bool cut = q.ta > 0 || q.tb < q.c.n;
+        const bool live = row < p.unit_tokens * p.g && t_row < q.c.tb &&
+                          RA_CHECKED(paged_row_ok(p.kv, p.hq, q.c.s.q0 + t_row, q.h * p.g + row - tok_in * p.g), p.err, kSitePagedOut) &&
+                          RA_CHECKED(q.slot == 0 || q.slot == 1, p.err, kSitePagedPartial);
         const bool sick = poison[q.k % kPoison] == q.k + 1;
         const float inv = lr == 0.f ? 0.f : 1.f / lr;
         const int tok = q.c.s.q0 + t_row, head = q.h * p.g + row - tok_in * p.g;
-        const bool live = row < p.unit_tokens * p.g && t_row < q.c.tb && RA_CHECKED(paged_row_ok(p.kv, p.hq, tok, head), p.err, kSitePagedOut) &&
-                          RA_CHECKED(q.slot == 0 || q.slot == 1, p.err, kSitePagedPartial);
         PagedChunkPartial* part = static_cast<PagedChunkPartial*>(p.workspace) + 2 * blockIdx.x + q.slot;
         const int r2 = x * kTile + row;
         if (!cut && !sick && !p.out_f32 && q.tb - q.ta <= kFold) {  // the usual end, with all loads in flight at once
