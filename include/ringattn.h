@@ -344,7 +344,9 @@ int ringattn_merge(float* o_run, float* lse_run, const float* o_part, const floa
  *   contiguous.  An e4m3 pool has one fp32 scale a row: k_scale, v_scale [n_pages, Hkv,
  *   page_size], pages k_scale_page_stride (v_scale_page_stride) apart; a row's value is code *
  *   scale.  ringattn_cache_append writes scales that are powers of two, which every reader
- *   applies exactly; with other positive scales the reader's products round to bf16.  The NaN
+ *   applies exactly.  With other positive scales ringattn_cache_read rounds the product to bf16 once,
+ *   ringattn_fwd_paged uses them in fp32 up to 16 rows of a sequence and KV head, and above that rounds
+ *   the scale to bf16 and then the product.  The NaN
  *   codes 0x7f and 0xff are not used (a row that has no scale, because it held an infinity
  *   or a NaN, is zeros with the scale NaN, and reads as NaN); what they read as in a pool
  *   written by other means is unspecified.
