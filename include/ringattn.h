@@ -417,7 +417,7 @@ int ringattn_cache_read(const ra_paged_kv* kv, void* k_out, void* v_out, ra_stre
  * ringattn_fwd_paged -- attention of the batch's rows over their sequences' kept keys:
  * q [total, Hq, d] bf16 (strides as k_new's), out [total, Hq, d] bf16 (out_f32 = 0) or fp32
  * (1), lse [total, Hq] fp32, natural log; token and head strides in elements, out rows
- * adjacent elements (out strides as k_new's; lse strides at least 1).  Row t of sequence b, at position
+ * adjacent elements (out strides as k_new's; lse strides at least 1; no two rows of out or lse overlap).  Row t of sequence b, at position
  * i = kv_len[b] - n_b + t, sees the keys j < kv_len[b] with
  *     causal = 1:  j <= i, and with window > 0 also (j > i - window or j < sinks)
  *     causal = 0:  all of them (window must be 0).

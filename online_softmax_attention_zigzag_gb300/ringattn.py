@@ -419,6 +419,17 @@ def _paged(k_cache, v_cache, k_scale, v_scale, block_table, cu, kv_len, total: i
                              t0 if batch > 1 else max_pages, n, page, h, d, e4m3, batch, max_pages, total)
 
 
+def _check_rows(fn: str, code: int, **rows) -> None:
+    """As :func:`_check`; rows that the library does not take are refused by name."""
+    if code == RA_ERR_INVALID_ARG:
+        for name, t in rows.items():
+            p, s0, s1 = _rows(t, name, t.dtype, t.get_device())
+            if p % 16 or any(s % 8 or not t.shape[2] <= s < 2 ** 32 for s in (s0, s1)):
+                raise ValueError(f"{name}: token and head strides must be multiples of 8 elements, at least d and below 2^32, and the "
+                                 f"first element on a 16-byte boundary; got strides {s0} and {s1}, address {p:#x}")
+    _check(fn, code)
+
+
 def _ints(**numbers) -> None:
     """ctypes drops the upper bits of a number that no C int holds; these calls refuse it."""
     for name, x in numbers.items():
@@ -434,7 +445,7 @@ def _raw_stream(stream, dev: int) -> int:
 def cache_append(k_new, v_new, k_cache, v_cache, block_table, cu, kv_len, *, k_scale=None, v_scale=None,
                  stream=None) -> None:
     """ringattn_cache_append: store the rows of new tokens, k_new and v_new [total, Hkv, d] bf16
-    (any token and head strides), at their positions in the pages of k_cache and v_cache
+    (token and head strides multiples of 8, at least d), at their positions in the pages of k_cache and v_cache
     [n_pages, Hkv, page_size, d], bf16 or float8_e4m3fn (then with k_scale, v_scale [n_pages, Hkv,
     page_size] fp32).  block_table [batch, max_pages], cu [batch + 1] and kv_len [batch] are
     int32; kv_len counts the new tokens."""
@@ -445,8 +456,8 @@ def cache_append(k_new, v_new, k_cache, v_cache, block_table, cu, kv_len, *, k_s
     h, d, kv = _paged(k_cache, v_cache, k_scale, v_scale, block_table, cu, kv_len, total, dev)
     if k_new.shape != (total, h, d) or v_new.shape != (total, h, d):
         raise ValueError("k_new and v_new must be [total, Hkv, d] with the cache's Hkv and d")
-    _check("ringattn_cache_append", (_lib or lib()).ringattn_cache_append(kp, vp, k0, k1, v0, v1, kv,
-                                                                          _raw_stream(stream, dev)))
+    _check_rows("ringattn_cache_append", (_lib or lib()).ringattn_cache_append(
+        kp, vp, k0, k1, v0, v1, kv, _raw_stream(stream, dev)), k_new=k_new, v_new=v_new)
 
 
 def cache_read(k_cache, v_cache, k_out, v_out, block_table, cu, kv_len, *, k_scale=None, v_scale=None,
@@ -475,9 +486,9 @@ def paged_workspace_bytes(total: int, batch: int, Hq: int, Hkv: int, d: int, max
 
 def fwd_paged(q, k_cache, v_cache, out, lse, block_table, cu, kv_len, workspace, *, max_q, causal=1, window=0,
               sinks=0, k_scale=None, v_scale=None, stream=None) -> None:
-    """ringattn_fwd_paged: attention of q [total, Hq, d] bf16 (any token and head strides) over the
-    cached keys of its sequences -> out [total, Hq, d] bf16 or fp32, lse [total, Hq] fp32 (any
-    strides).  With window > 0 a row at position i sees j in (i - window, i] and the first
+    """ringattn_fwd_paged: attention of q [total, Hq, d] bf16 over the cached keys of its sequences ->
+    out [total, Hq, d] bf16 or fp32 (q's and out's token and head strides multiples of 8, at least d),
+    lse [total, Hq] fp32 (any strides from 1 up); rows of out and lse do not overlap.  With window > 0 a row at position i sees j in (i - window, i] and the first
     ``sinks`` positions.  max_q: at least the most rows of one sequence; workspace: a CUDA uint8
     tensor of at least :func:`paged_workspace_bytes`.  The cache as for :func:`cache_append`."""
     if (max_q | causal | window | sinks) >> 31:
@@ -495,9 +506,9 @@ def fwd_paged(q, k_cache, v_cache, out, lse, block_table, cu, kv_len, workspace,
     l0, l1 = lse.stride()
     if workspace.dtype is not torch.uint8 or workspace.get_device() != dev or workspace.stride() != (1,):
         _strided(workspace, "workspace", torch.uint8, dev, 1)
-    _check("ringattn_fwd_paged", (_lib or lib()).ringattn_fwd_paged(
+    _check_rows("ringattn_fwd_paged", (_lib or lib()).ringattn_fwd_paged(
         qp, q0, q1, kv, op, o0, o1, f32, lse.data_ptr(), l0 if total > 1 else max(1, Hq), l1 if Hq > 1 else 1, Hq, max_q,
-        causal, window, sinks, workspace.data_ptr(), workspace.shape[0], _raw_stream(stream, dev)))
+        causal, window, sinks, workspace.data_ptr(), workspace.shape[0], _raw_stream(stream, dev)), q=q, out=out)
 
 
 def rank_work(S: int, c: int, causal: int, layout: int, tile: int = 128):
