@@ -428,12 +428,19 @@ int ringattn_cache_read(const ra_paged_kv* kv, void* k_out, void* v_out, ra_stre
  * disjoint keys combine with ringattn_merge when out is fp32.
  * max_q: at least the largest n_b (host knowledge: it picks the kernel and bounds the work; rows
  *     of a sequence at and behind max_q are not written).
- * Sums, maxima and the running output are fp32; the probabilities are rounded to 16 bits for
- * their product with V.  (The tensor cores truncate their sums, which end after 32768 keys, or 65536
+ * Sums, maxima and the running output are fp32.  For its product with V a probability is rounded, by the rows of a
+ * sequence and KV head (max_q * Hq / Hkv):
+ *     up to 16, bf16 cache   to 2^-15 of itself (two bf16 halves)
+ *     up to 16, e4m3 cache   to 2^-11, times V's scale, as fp16: contributions below 2^-20 of a row's largest may lose
+ *                            bits, those below 2^-31 vanish; q is fp16 too, times a power of two a
+ *                            row, so that elements below 2^-28 of the row's largest lose bits
+ *     above 16               to bf16, 2^-8 (and the sum that out is divided by is that of the rounded ones)
+ * (The tensor cores truncate their sums, which end after 32768 keys, or 65536
  * where a sequence and KV head has more than 16 rows, and are added up rounded to nearest: with values of one
  * sign out may be 1e-4, or 5e-4, of itself low, however many keys there are.)
  * workspace: DEVICE, at least ringattn_paged_workspace_bytes(total, batch, Hq, Hkv, d, max_q)
- *     bytes, 256-byte aligned; its contents do not matter before or after.  Calls that may
+ *     bytes (10.7 MB up to 16 rows, 43 MB and 8 bytes an item above, whatever the lengths), 256-byte
+ *     aligned; its contents do not matter before or after.  Calls that may
  *     overlap on the GPU, captured ones among them, need one each.
  * Requires Hq % Hkv == 0, Hq / Hkv <= 128, total * Hq below 2^31 (else RA_ERR_UNSUPPORTED),
  * 16-byte aligned q and out.

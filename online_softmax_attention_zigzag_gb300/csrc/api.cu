@@ -635,8 +635,9 @@ int encode_pool(CUtensorMap* map, const void* base, long long page_stride, const
 }
 
 // Rows of a sequence and KV head decide the kernel: up to 16 the few-row one, which 16-row matrix
-// instructions serve; a chunk item fills 256 rows and does 17 at the cost of 128, which the loads
-// still hide.
+// instructions serve; a chunk item fills 256 rows and does 17 at the cost of 128.  In bf16 the loads hide most
+// of that (16 x 8 tokens, 64 rows a KV head: 170 us, 146 for their bytes), in e4m3 the expansion of the codes
+// does not fit behind half as many bytes (174 us, 75).
 bool paged_few(int total, int g, int max_q) {
     return static_cast<long long>(max_q < total ? max_q : total) * g <= ra::kPagedFewRows;
 }

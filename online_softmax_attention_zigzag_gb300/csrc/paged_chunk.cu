@@ -33,11 +33,12 @@
 //     e4m3 tiles on their way.
 //
 // What it takes, 64 query and 8 KV heads, d = 128 (the products' floor is the measured 1912 TFLOP/s):
-//     4096 tokens behind 28672, bf16: 2.55 ms, 1615 TFLOP/s, as the ring kernel's in a long loop: bound by
+//     4096 tokens behind 28672, bf16: 2.56 ms, 1610 TFLOP/s, as the ring kernel's in a long loop: bound by
 //     each unit's chain of S, softmax, P V
-//     1024 tokens behind 15360: bf16 343 us (1550), e4m3 397 us (1340): there the expanding warps, 0.5 us
-//     each for V and K and 0.4 us for their scales' addresses, take as long as the two softmaxes
-//     16 x 8 tokens of 1k - 33k keys (one unit): bf16 171 us (5.8 TB/s), e4m3 180 us
+//     1024 tokens behind 15360: bf16 342 - 353 us (1560 - 1510), e4m3 394 us (1350), d = 64 265 and 330: in
+//     e4m3 the expanding warps, 0.5 us each for V and K and 0.4 us for their scales' addresses, take as
+//     long as the two softmaxes
+//     16 x 8 tokens of 1k - 33k keys (one unit): bf16 170 us (5.8 TB/s), e4m3 174 us (2.9 TB/s: the expansion again)
 // Short items pay about 9 us each for their first and last tiles and their epilogue.
 //
 // Warps: 0-7 softmax (four a unit), 8 and 9 issue the units' MMAs, 10 loads, 11 lists the block's

@@ -23,13 +23,14 @@
 // What a tile takes is a chain of latencies (copy, barrier, S, max, exponentials, P V), and so is what
 // a pair takes (q, the meeting, the output): groups hide them behind one another.  One group of eight
 // warps with the same 128 KB of slots, and four that took one line's tiles in turn, were slower:
-//     64 x 16k keys of 8 heads, bf16             323 us, now 310 (6.6 TB/s)
-//     8 x 128k keys, e4m3                        293 us, now 288 (6.8 TB/s)
-//     48 windows of 4096 of 3k - 32k keys, e4m3   78 us, now  75
-//     512 x 20 - 300 keys, e4m3                  181 us, now  76; bf16 173 and 125
-//     32 x 16k keys of d = 64, e4m3              129 us, now 103; bf16 165 and 160 (6.6 TB/s)
-//     one sequence of 777 keys                  13.0 us, now 11.4
-// (Boxes that no row sees, behind sinks and before windows, cost nothing: windows 76 us with them, 75 without.)
+//     64 x 16k keys of 8 heads, bf16             323 us, now 313 (6.5 TB/s)
+//     8 x 128k keys, e4m3                        293 us, now 280 (7.0 TB/s)
+//     48 windows of 4096 of 3k - 32k keys, e4m3   78 us, now  74
+//     512 x 20 - 300 keys, e4m3                  181 us, now  76; bf16 173 and 127
+//     32 x 16k keys of d = 64, e4m3              129 us, now  99; bf16 165 and 162 (6.6 TB/s)
+//     one sequence of 777 keys                  13.0 us, now 11.7
+// (Boxes that no row sees, behind sinks and before windows, are not loaded: windows 77.3 us with them, 76.0 without; in
+// bf16 139.1 and 136.5.)
 // The tensor cores truncate every addend of a sum, always towards zero, so a warp's sums end after kFold tiles at
 // the latest: a longer part of a share goes in stretches, which are added up in fp32, rounded to nearest.
 // bf16 cache: P goes into its product as two bf16 halves (p = hi + lo to 2^-15): the second product costs
@@ -907,7 +908,9 @@ int launch_t(const PagedAttnParams& p, const PagedMaps& m, int blocks, cudaStrea
     kern<<<blocks, C::kThreads, bytes, stream>>>(p, m.k, m.v);
     if (cudaGetLastError() != cudaSuccess) return -4;
     cudaLaunchConfig_t cfg = {};
-    // fewer than 8 parts a pair on average: one block for all rows of a pair is quicker than one for each
+    // Fewer than 8 parts a pair on average: one block for all rows of a pair; else one for each row.  (All rows against
+    // a row a block: 64 x 16k keys of 8 heads 314 and 319 us, 48 windows in e4m3 76 and 84, one
+    // sequence of 128k keys 102 and 94, in e4m3 77 and 59; near the border level: 6 x 16k 73 and 73.)
     cfg.gridDim = dim3(shares, 8LL * p.kv.batch * p.kv.hkv >= shares ? 1 : p.max_q * p.g);
     cfg.blockDim = dim3(256);
     cfg.stream = stream;
