@@ -5,7 +5,9 @@ import math
 import pytest
 import torch
 
+from oracle import paged as opaged
 from tests.gpu_util import dev
+from tests.paged_util import Batch, check
 
 pytestmark = pytest.mark.gpu
 
@@ -54,3 +56,37 @@ def test_millions_of_keys(ra, e4m3, n, std, d):
         want = torch.logsumexp(x, 1) + math.log(L // page)
         off = (lse[rows].double().reshape(-1) - want).abs().max().item()
         assert off <= 2.0 ** -16 + 2.0 ** -22 * want.abs().max().item()
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("n,window,sinks", [(1, 0, 0), (2, 0, 0), (1, 60000, 200), (2, 50000, 1000)])
+def test_stretches_whose_maximum_grows(ra, e4m3, n, window, sinks):
+    """A part of 547 tiles for a group (the same pages for all its sequences), so three stretches, with scores that grow
+    along the keys, or shrink; the sequence of another group in two parts; an infinite value in the first stretch."""
+    hq, d, L = 8, 128, 70000
+    B = 4 * torch.cuda.get_device_properties(0).multi_processor_count + 1  # (one more than groups: some parts are cut)
+    for grow in (True, False):
+        S = Batch([(n, L)], hkv=1, d=d, page=512, e4m3=e4m3, device=dev(), seed=82, fill=False)
+        ramp = torch.arange(L)[:, None, None] / L
+        S.k[0] = (S.k[0].float() * (0.5 + 3.5 * (ramp if grow else 1 - ramp))).to(torch.bfloat16)
+        at = 150 if window else 20000  # (a sink)
+        if not e4m3:
+            S.v[0][at, 0, 9] = float("inf")
+        S.fill()
+        q = (torch.randn((B * n, hq, d), generator=torch.Generator().manual_seed(83)) * 0.3).to(torch.bfloat16)
+        out, lse = torch.empty((B * n, hq, d), device=dev()), torch.empty((B * n, hq), device=dev())
+        cu = torch.arange(0, B * n + 1, n, dtype=torch.int32, device=dev())
+        ws = torch.full((ra.paged_workspace_bytes(B * n, B, hq, 1, d, n),), 255, dtype=torch.uint8, device=dev())
+        ra.fwd_paged(q.to(dev()), S.k_cache, S.v_cache, out, lse, S.dtable.expand(B, -1).contiguous(), cu, S.dlen.expand(B).contiguous(),
+                     ws, max_q=n, window=window, sinks=sinks, **S.kw())
+        assert ra.sync_status() == ra.RA_OK
+        k, v = S.kept(0)
+        if not e4m3:
+            v[at, 0, 9] = 0.0
+        keep = [c for c in range(d) if c != 9]
+        for b in (0, B - 1):
+            rows = slice(b * n, (b + 1) * n)
+            ref = opaged.attention(q[rows].double().numpy(), k, v, True, window, sinks)
+            check(out[rows][..., keep], lse[rows], [x[..., keep] if x.ndim == 3 else x for x in ref], d, False, f"sequence {b}, {grow}")
+            if not e4m3:
+                assert torch.isposinf(out[rows][..., 9]).all()
