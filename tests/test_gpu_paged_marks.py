@@ -120,9 +120,9 @@ def test_a_coarser_probability_would_show(e4m3):
     kept = p if not e4m3 else x.to(torch.float16).double().numpy()
     lse = torch.from_numpy(ref[1])
 
-    def judge(p2):
+    def hold(p2):
         check(torch.from_numpy(p2 @ v[:, 0] / p.sum(1, keepdims=True))[None], lse, ref, d, False, p_eps=P_EPS[e4m3])
 
-    judge(kept)
+    hold(kept)
     with pytest.raises(AssertionError):
-        judge(cut)
+        hold(cut)
