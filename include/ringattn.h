@@ -455,6 +455,107 @@ int ringattn_fwd_paged(const void* q, long long q_token_stride, long long q_head
 int ringattn_paged_workspace_bytes(int total, int batch, int Hq, int Hkv, int d, int max_q, long long* bytes);
 
 /*
+ * ringattn_cache_weights -- the attention weight that the cached positions have had from this call's
+ * rows, added to what they had before: what ringattn_cache_evict chooses by.
+ *     weights[j] = (j < base ? decay * weights[j] : 0) + sum of exp(q . k_j - lse)
+ * over the rows of the sequence that see j and the query heads of the KV head, for every position j <
+ * kv_len[b] and KV head; base = kv_len[b] - n_b, so that the positions of the call's own rows start
+ * from nothing, whatever their places held.  Call it once for the rows of every step, with the q and
+ * the lse of that step's ringattn_fwd_paged, after it.  To weigh a prompt by its last rows alone, give
+ * those rows (cu, with kv_len as it is) and decay = 0.
+ * weights: [n_pages, Hkv, page_size] fp32 beside the pool's k and v; pages weights_page_stride apart
+ *     (a multiple of 4, at least Hkv * page_size, at most 2^36), 16-byte aligned.
+ * decay: in [0, 1]; 1 adds up, 0 does not read what was there.
+ * q, kv, Hq, max_q, causal, window, sinks, workspace: as for ringattn_fwd_paged; lse [total, Hq] fp32 as it
+ *     left it (any lse does: a key's weight is exp(q . k - lse)); a row whose lse is -inf adds nothing.
+ *     V is not read.  kv->v has to be given all the same.
+ * Positions that no row sees (behind a window) are scaled by decay; those of a sequence without rows
+ * stay as they are.  Scores and sums are fp32; no atomics: the same call gives the same bits.  With
+ * e4m3 a scale that is no power of two is used in fp32.
+ * Requires what ringattn_fwd_paged requires.
+ */
+int ringattn_cache_weights(const void* q, long long q_token_stride, long long q_head_stride, const float* lse,
+                           long long lse_token_stride, long long lse_head_stride, const ra_paged_kv* kv,
+                           float* weights, long long weights_page_stride, float decay, int Hq, int max_q, int causal,
+                           int window, int sinks, void* workspace, long long workspace_bytes, ra_stream_t stream);
+
+/*
+ * ringattn_cache_evict -- of every sequence's kv_len[b] positions n = min(keep[b], kv_len[b]) stay, chosen for
+ * every KV head on its own: the first `sinks` and the last `recent` before all others, then those of
+ * the largest weight (a NaN counts as larger than any number); of equal ones the lower position.  K, V, their scales and the weights of the i-th
+ * of them, in order of position, move to position i; what lies behind position n - 1 is left as it
+ * was, and the pages that only it uses are the caller's again.  Positions are then places in the cache and no longer
+ * places in the text: the rotation of new rows takes its own positions (ringattn_qk_norm_rope),
+ * attention over the packed cache needs no change (windows, `sinks` and `recent` count what is kept).
+ * kv: as for ringattn_cache_append, without rows: cu and total are not used (cu may be NULL).  No two
+ *     (sequence, position) pairs of the batch may have the same page and row, and pages that a sequence
+ *     outside the batch uses too would change under it.
+ * weights: as for ringattn_cache_weights; read, and packed as K and V are.
+ * keep: [batch] int32, device; taken as at least 0 and at most max_keep.
+ * kv_len_out: [batch] int32, device: n.  May be kv->kv_len.
+ * kept: [batch, Hkv, max_keep] int32, device, contiguous: where the i-th position was; -1 from n on.
+ * A page of the table outside [0, n_pages) reads as weight 0 and zeros, and what would move there is dropped.
+ * Requires max_keep at most 2^30, batch * Hkv below 2^31 (else RA_ERR_UNSUPPORTED); 4-byte aligned keep, kv_len_out, kept.
+ */
+int ringattn_cache_evict(const ra_paged_kv* kv, float* weights, long long weights_page_stride, const int* keep,
+                         int max_keep, int sinks, int recent, int* kv_len_out, int* kept, ra_stream_t stream);
+
+/*
+ * ringattn_qk_norm_rope -- what comes before attention: every head's query and key row x [d] normed by
+ * its root mean square, weighted, turned by its position, and q scaled (attention here applies no
+ * 1/sqrt(d)):
+ *     y = w * x / sqrt(mean(x^2) + eps);  then for j < rot/2 the pair (a, b) of y becomes
+ *     (a cos - b sin, b cos + a sin), with cos = cos_sin[position, j], sin = cos_sin[position, rot/2 + j];
+ *     q's rows are multiplied by q_scale.
+ * Pairs are (j, j + rot/2), or (2j, 2j + 1) with interleaved = 1; elements from rot on are not turned.
+ * Arithmetic is fp32 (a row whose squares add up to more than fp32 holds, |x| from about 2^60 on, has r = 0), rounded once.
+ */
+typedef struct {
+    void* q; /* [total, Hq, d] */
+    void* k; /* [total, Hkv, d] */
+    /* elements; multiples of 8, at least d, below 2^32: slices of a fused projection, token-major or head-major rows */
+    long long q_token_stride, q_head_stride, k_token_stride, k_head_stride;
+    int dtype; /* 0: bf16; 1: fp32, where a call takes it */
+} ra_qk_rows;
+typedef struct {
+    const void* q_weight; /* [d], device; NULL: ones */
+    const void* k_weight;
+    const float* cos_sin; /* [n_pos, rot], device: rot/2 cosines, then rot/2 sines; NULL only with rot = 0 */
+    const int* position;  /* [total], device: each token's row of cos_sin */
+    int total, Hq, Hkv, d, rot, n_pos;
+    int weight_f32;  /* 0: both weights are bf16, 1: fp32 */
+    int interleaved; /* 0, 1 */
+    float eps, q_scale;
+} ra_qk_norm;
+/*
+ * in, out: bf16.  Rows of out may be those of in (same strides); otherwise the outputs overlap nothing.
+ * A token whose position is outside [0, n_pos) belongs to nobody (a padded batch): nothing is written for it.
+ * Requires d in {64, 128}; rot a multiple of 16, at most d; total at most 2^30, Hq + Hkv at most 65536 (else
+ * RA_ERR_UNSUPPORTED); eps >= 0 and q_scale finite; 16-byte aligned rows, weights and cos_sin.  total = 0 is
+ * valid: nothing to do.
+ */
+int ringattn_qk_norm_rope(const ra_qk_rows* in, const ra_qk_rows* out, const ra_qk_norm* norm, ra_stream_t stream);
+
+/*
+ * ringattn_qk_norm_rope_bwd -- gradients of ringattn_qk_norm_rope.  With g = q_scale * (dout turned back),
+ * r = 1 / sqrt(mean(x^2) + eps) and u = w * g:
+ *     dw = sum over rows of g * x * r,   din = r * (u - x * r^2 * mean(u * x)).
+ * in: the rows that went in, bf16.  dout: gradients of the rows that came out, bf16 or fp32 (as
+ * ringattn_bwd_natural gives them, head-major).  din: bf16 or fp32; its rows may be those of dout (same
+ * type and strides).  dq_weight, dk_weight: [d] fp32, overwritten; either may be NULL.  Tokens whose position is
+ * outside the table have no part in the sums, and nothing is written for them.
+ * workspace: DEVICE, at least ringattn_qk_norm_rope_workspace_bytes bytes (1 MB at most up to 8192 heads), 256-byte aligned; NULL if
+ *     neither weight gradient is asked for.  Calls that may overlap need one each.
+ * The weights' gradients are added up in fp32 in an order that depends on the sizes and the GPU's number of SMs alone.
+ */
+int ringattn_qk_norm_rope_bwd(const ra_qk_rows* in, const ra_qk_rows* dout, const ra_qk_rows* din, float* dq_weight,
+                              float* dk_weight, const ra_qk_norm* norm, void* workspace, long long workspace_bytes,
+                              ra_stream_t stream);
+
+/* ringattn_qk_norm_rope_workspace_bytes -- host only.  See ringattn_qk_norm_rope_bwd. */
+int ringattn_qk_norm_rope_workspace_bytes(int total, int Hq, int Hkv, int d, long long* bytes);
+
+/*
  * ringattn_permute -- move rows between natural and rank-major order.
  * src, dst: [H, S, row_bytes] bytes, distinct buffers.  inverse = 0: natural ->
  * rank-major; 1: rank-major -> natural.  row_bytes >= 1 (2*d for bf16 Q/K/V, 4*d

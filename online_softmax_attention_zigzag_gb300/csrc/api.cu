@@ -17,6 +17,8 @@
 #include "ringattn.h"
 #include "internal.h"
 #include "paged.h"
+#include "cache_weights.h"
+#include "qk_norm.h"
 
 namespace {
 
@@ -683,14 +685,14 @@ int encode_paged(const ra::PagedAttnParams& p, ra::PagedMaps* m) {
     return RA_OK;
 }
 
-// Checks that concern the pool and the batch alone.
-int make_paged(const ra_paged_kv* a, ra::PagedKV* kv) {
+// Checks that concern the pool and the batch alone.  A call without token rows leaves cu and total alone.
+int make_paged(const ra_paged_kv* a, ra::PagedKV* kv, bool rows_too = true) {
     if (!a || a->n_pages < 1 || a->page_size < 1 || a->Hkv < 1 || a->d < 1 || a->batch < 1 || a->max_pages < 1 ||
-        a->total < 0 || (a->dtype != 0 && a->dtype != 1))
+        (a->dtype != 0 && a->dtype != 1) || (rows_too && (a->total < 0 || !a->cu)))
         return RA_ERR_INVALID_ARG;
-    if (!a->k || !a->v || a->k == a->v || !a->block_table || !a->cu || !a->kv_len || !aligned16(a->k) || !aligned16(a->v))
+    if (!a->k || !a->v || a->k == a->v || !a->block_table || !a->kv_len || !aligned16(a->k) || !aligned16(a->v))
         return RA_ERR_INVALID_ARG;
-    if (((reinterpret_cast<uintptr_t>(a->block_table) | reinterpret_cast<uintptr_t>(a->cu) |
+    if (((reinterpret_cast<uintptr_t>(a->block_table) | (rows_too ? reinterpret_cast<uintptr_t>(a->cu) : 0) |
           reinterpret_cast<uintptr_t>(a->kv_len)) & 3u) != 0)
         return RA_ERR_INVALID_ARG;
     const bool scaled = a->dtype == 1;
@@ -698,7 +700,8 @@ int make_paged(const ra_paged_kv* a, ra::PagedKV* kv) {
     if (a->d != 64 && a->d != 128) return RA_ERR_UNSUPPORTED;
     if (a->page_size % 16 != 0 || a->page_size > 65536 || a->batch > RINGATTN_PAGED_MAX_BATCH) return RA_ERR_UNSUPPORTED;
     // positions, and differences of two of them, are 32-bit numbers
-    if (static_cast<long long>(a->max_pages) * a->page_size > (1LL << 30) || a->total > (1 << 30)) return RA_ERR_UNSUPPORTED;
+    if (static_cast<long long>(a->max_pages) * a->page_size > (1LL << 30) || (rows_too && a->total > (1 << 30)))
+        return RA_ERR_UNSUPPORTED;
     const long long rows = static_cast<long long>(a->Hkv) * a->page_size;  // of one page
     if (rows > (1LL << 30)) return RA_ERR_UNSUPPORTED;
     const int unit = scaled ? 16 : 8;  // elements of 16 bytes
@@ -722,7 +725,7 @@ int make_paged(const ra_paged_kv* a, ra::PagedKV* kv) {
     kv->ks_ps = a->k_scale_page_stride;
     kv->vs_ps = a->v_scale_page_stride;
     kv->table = a->block_table;
-    kv->cu = a->cu;
+    kv->cu = rows_too ? a->cu : nullptr;
     kv->len = a->kv_len;
     kv->table_stride = a->table_stride;
     kv->n_pages = a->n_pages;
@@ -732,9 +735,67 @@ int make_paged(const ra_paged_kv* a, ra::PagedKV* kv) {
     kv->e4m3 = a->dtype;
     kv->batch = a->batch;
     kv->max_pages = a->max_pages;
-    kv->total = a->total;
+    kv->total = rows_too ? a->total : 0;
     kv->by_page = ra::make_fastdiv(static_cast<unsigned>(a->page_size));
     return RA_OK;
+}
+
+// The weights of a pool's positions: one fp32 a page, KV head and row.
+int check_weights(const float* w, long long page_stride, const ra::PagedKV& kv) {
+    if (!w || !aligned16(w) || page_stride < static_cast<long long>(kv.hkv) * kv.page || page_stride % 4 != 0)
+        return RA_ERR_INVALID_ARG;
+    return page_stride > (1LL << 36) ? RA_ERR_UNSUPPORTED : RA_OK;
+}
+
+// ------------------------------------------------------------------ norm and rotation of q and k
+int check_rows(const ra_qk_rows* a, int d, bool may_f32, ra::NormRows* r) {
+    if (!a || (a->dtype != 0 && !(may_f32 && a->dtype == 1))) return RA_ERR_INVALID_ARG;
+    const void* const p[2] = {a->q, a->k};
+    const long long ts[2] = {a->q_token_stride, a->k_token_stride}, hs[2] = {a->q_head_stride, a->k_head_stride};
+    for (int i = 0; i < 2; ++i) {
+        if (!p[i] || !aligned16(p[i]) || !row_strides_ok(ts[i], hs[i], d)) return RA_ERR_INVALID_ARG;
+        r->p[i] = const_cast<void*>(p[i]);
+        r->ts[i] = ts[i];
+        r->hs[i] = hs[i];
+    }
+    return RA_OK;
+}
+
+// Checks that concern neither rows nor workspace.
+int make_norm(const ra_qk_norm* a, ra::NormParams* p) {
+    if (!a || a->total < 0 || a->Hq < 1 || a->Hkv < 1 || a->d < 1 || a->rot < 0 || a->rot > a->d || a->n_pos < 1 ||
+        (a->weight_f32 != 0 && a->weight_f32 != 1) || (a->interleaved != 0 && a->interleaved != 1))
+        return RA_ERR_INVALID_ARG;
+    if (!(a->eps >= 0.f) || a->eps > 3.0e38f || !(a->q_scale >= -3.4e38f && a->q_scale <= 3.4e38f)) return RA_ERR_INVALID_ARG;
+    if (a->d != 64 && a->d != 128) return RA_ERR_UNSUPPORTED;
+    if (a->rot % 16 != 0 || a->total > (1 << 30) || static_cast<long long>(a->Hq) + a->Hkv > 65536) return RA_ERR_UNSUPPORTED;
+    if (!aligned16(a->q_weight) || !aligned16(a->k_weight)) return RA_ERR_INVALID_ARG;
+    if (a->total > 0 && (!a->position || (reinterpret_cast<uintptr_t>(a->position) & 3u) != 0 || !aligned16(a->cos_sin) ||
+                         (a->rot > 0 && !a->cos_sin)))
+        return RA_ERR_INVALID_ARG;
+    p->w[0] = a->q_weight;
+    p->w[1] = a->k_weight;
+    p->cos_sin = a->cos_sin;
+    p->position = a->position;
+    p->total = a->total;
+    p->heads[0] = a->Hq;
+    p->heads[1] = a->Hkv;
+    for (int i = 0; i < 2; ++i) p->groups[i] = (p->heads[i] + ra::kNormHeads - 1) / ra::kNormHeads;
+    p->d = a->d;
+    p->rot = a->rot;
+    p->n_pos = a->n_pos;
+    p->w_f32 = a->weight_f32;
+    p->interleaved = a->interleaved;
+    p->eps = a->eps;
+    p->scale[0] = a->q_scale;
+    p->scale[1] = 1.f;
+    return RA_OK;
+}
+
+// Sums of the backward pass's blocks, on a GPU of at most kNormMaxSms.
+long long norm_workspace(int total, int groups, int d) {
+    const long long blocks = static_cast<long long>(groups) * ra::norm_blocks(total, groups, d, ra::kNormMaxSms * ra::kNormBlocksPerSm);
+    return (std::max(blocks, 1LL) * d * 4 + 255) / 256 * 256;
 }
 
 }  // namespace
@@ -914,6 +975,124 @@ int ringattn_fwd_paged(const void* q, long long q_token_stride, long long q_head
     const int shares = dev->sms < ra::kPagedMaxShares ? dev->sms : ra::kPagedMaxShares;
     return paged_few(p.kv.total, p.g, max_q) ? ra::launch_paged_decode(p, maps, shares, cs)
                                              : ra::launch_paged_chunk(p, maps, shares, cs);
+}
+
+int ringattn_cache_weights(const void* q, long long q_token_stride, long long q_head_stride, const float* lse,
+                           long long lse_token_stride, long long lse_head_stride, const ra_paged_kv* kv, float* weights,
+                           long long weights_page_stride, float decay, int Hq, int max_q, int causal, int window, int sinks,
+                           void* workspace, long long workspace_bytes, ra_stream_t stream) {
+    NvtxRange nvtx("ringattn_cache_weights");
+    ra::WeightsParams p = {};
+    int st = make_paged(kv, &p.kv);
+    if (st != RA_OK) return st;
+    if (Hq < 1 || Hq % p.kv.hkv != 0 || max_q < 1 || (causal != 0 && causal != 1)) return RA_ERR_INVALID_ARG;
+    if (window < 0 || sinks < 0 || (window > 0 && causal == 0) || !(decay >= 0.f && decay <= 1.f)) return RA_ERR_INVALID_ARG;
+    if (p.kv.total == 0) return RA_OK;
+    if (!q || !lse || !workspace || !aligned16(q)) return RA_ERR_INVALID_ARG;
+    if ((reinterpret_cast<uintptr_t>(lse) & 3u) != 0 || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+        return RA_ERR_INVALID_ARG;
+    if (!row_strides_ok(q_token_stride, q_head_stride, p.kv.d) || lse_token_stride < 1 || lse_head_stride < 1)
+        return RA_ERR_INVALID_ARG;
+    if ((st = check_weights(weights, weights_page_stride, p.kv)) != RA_OK) return st;
+    p.g = Hq / p.kv.hkv;
+    if (p.g > 128 || static_cast<long long>(p.kv.total) * Hq > INT_MAX) return RA_ERR_UNSUPPORTED;
+    if (workspace_bytes < paged_workspace(p.kv.total, p.kv.batch, p.g, max_q, nullptr)) return RA_ERR_INVALID_ARG;
+    DeviceInfo* dev = nullptr;
+    if ((st = device_info(&dev)) != RA_OK) return st;
+    p.q = q;
+    p.lse = lse;
+    p.w = weights;
+    p.q_ts = q_token_stride;
+    p.q_hs = q_head_stride;
+    p.l_ts = lse_token_stride;
+    p.l_hs = lse_head_stride;
+    p.w_ps = weights_page_stride;
+    p.decay = decay;
+    p.hq = Hq;
+    p.max_q = max_q < p.kv.total ? max_q : p.kv.total;
+    p.causal = causal;
+    p.window = std::min(window, 1 << 30);
+    p.sinks = std::min(sinks, 1 << 30);
+    p.by_g = ra::make_fastdiv(static_cast<unsigned>(p.g));
+    p.err = dev->err;
+    return ra::launch_cache_weights(p, dev->sms, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int ringattn_cache_evict(const ra_paged_kv* kv, float* weights, long long weights_page_stride, const int* keep, int max_keep,
+                         int sinks, int recent, int* kv_len_out, int* kept, ra_stream_t stream) {
+    NvtxRange nvtx("ringattn_cache_evict");
+    ra::EvictParams p = {};
+    int st = make_paged(kv, &p.kv, false);
+    if (st != RA_OK) return st;
+    if (max_keep < 1 || sinks < 0 || recent < 0) return RA_ERR_INVALID_ARG;
+    if (!keep || !kv_len_out || !kept || ((reinterpret_cast<uintptr_t>(keep) | reinterpret_cast<uintptr_t>(kv_len_out) |
+                                           reinterpret_cast<uintptr_t>(kept)) & 3u) != 0)
+        return RA_ERR_INVALID_ARG;
+    if ((st = check_weights(weights, weights_page_stride, p.kv)) != RA_OK) return st;
+    if (max_keep > (1 << 30) || static_cast<long long>(p.kv.batch) * p.kv.hkv > INT_MAX) return RA_ERR_UNSUPPORTED;
+    DeviceInfo* dev = nullptr;
+    if ((st = device_info(&dev)) != RA_OK) return st;
+    p.w = weights;
+    p.w_ps = weights_page_stride;
+    p.keep = keep;
+    p.len_out = kv_len_out;
+    p.kept = kept;
+    p.max_keep = max_keep;
+    p.sinks = std::min(sinks, 1 << 30);
+    p.recent = std::min(recent, 1 << 30);
+    p.err = dev->err;
+    return ra::launch_cache_evict(p, dev->sms, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int ringattn_qk_norm_rope(const ra_qk_rows* in, const ra_qk_rows* out, const ra_qk_norm* norm, ra_stream_t stream) {
+    NvtxRange nvtx("ringattn_qk_norm_rope");
+    ra::NormParams p = {};
+    int st = make_norm(norm, &p);
+    if (st != RA_OK || p.total == 0) return st;
+    if ((st = check_rows(in, p.d, false, &p.x)) != RA_OK || (st = check_rows(out, p.d, false, &p.y)) != RA_OK) return st;
+    DeviceInfo* dev = nullptr;
+    if ((st = device_info(&dev)) != RA_OK) return st;
+    p.err = dev->err;
+    return ra::launch_qk_norm_rope(p, dev->sms, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int ringattn_qk_norm_rope_workspace_bytes(int total, int Hq, int Hkv, int d, long long* bytes) {
+    if (!bytes || total < 0 || Hq < 1 || Hkv < 1 || (d != 64 && d != 128)) return RA_ERR_INVALID_ARG;
+    if (static_cast<long long>(Hq) + Hkv > 65536) return RA_ERR_UNSUPPORTED;
+    *bytes = norm_workspace(total, (Hq + ra::kNormHeads - 1) / ra::kNormHeads + (Hkv + ra::kNormHeads - 1) / ra::kNormHeads, d);
+    return RA_OK;
+}
+
+int ringattn_qk_norm_rope_bwd(const ra_qk_rows* in, const ra_qk_rows* dout, const ra_qk_rows* din, float* dq_weight,
+                              float* dk_weight, const ra_qk_norm* norm, void* workspace, long long workspace_bytes,
+                              ra_stream_t stream) {
+    NvtxRange nvtx("ringattn_qk_norm_rope_bwd");
+    ra::NormParams p = {};
+    int st = make_norm(norm, &p);
+    if (st != RA_OK) return st;
+    if (((reinterpret_cast<uintptr_t>(dq_weight) | reinterpret_cast<uintptr_t>(dk_weight)) & 3u) != 0) return RA_ERR_INVALID_ARG;
+    if (dq_weight && dq_weight == dk_weight) return RA_ERR_INVALID_ARG;
+    if (p.total > 0) {
+        if ((st = check_rows(in, p.d, false, &p.x)) != RA_OK || (st = check_rows(dout, p.d, true, &p.y)) != RA_OK ||
+            (st = check_rows(din, p.d, true, &p.g)) != RA_OK)
+            return st;
+    } else if (!dq_weight && !dk_weight) {
+        return RA_OK;
+    }
+    if (dq_weight || dk_weight) {
+        if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 ||
+            workspace_bytes < norm_workspace(p.total, p.groups[0] + p.groups[1], p.d))
+            return RA_ERR_INVALID_ARG;
+    }
+    DeviceInfo* dev = nullptr;
+    if ((st = device_info(&dev)) != RA_OK) return st;
+    if (dev->sms > ra::kNormMaxSms) return RA_ERR_UNSUPPORTED;
+    p.dw[0] = dq_weight;
+    p.dw[1] = dk_weight;
+    p.partial = static_cast<float*>(workspace);
+    p.err = dev->err;
+    return ra::launch_qk_norm_rope_bwd(p, dout && dout->dtype == 1, din && din->dtype == 1, dev->sms,
+                                       reinterpret_cast<cudaStream_t>(stream));
 }
 
 int ringattn_rank_work(int S, int c, int causal, int layout, int tile, long long* units, long long* pairs,

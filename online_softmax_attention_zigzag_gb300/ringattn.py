@@ -38,6 +38,8 @@ EXPORTS = (
     "ringattn_fwd_host", "ringattn_host_workspace_bytes", "ringattn_relayout", "ringattn_ulysses_fwd",
     "ringattn_bwd", "ringattn_bwd_natural",
     "ringattn_cache_append", "ringattn_cache_read", "ringattn_fwd_paged", "ringattn_paged_workspace_bytes",
+    "ringattn_cache_weights", "ringattn_cache_evict",
+    "ringattn_qk_norm_rope", "ringattn_qk_norm_rope_bwd", "ringattn_qk_norm_rope_workspace_bytes",
 )
 
 # Longest sequence ringattn_fwd_docmask_noalloc takes (its static scratch, int32 [S]).
@@ -56,7 +58,7 @@ class RingAttnError(RuntimeError):
 
 _lib = None
 
-_P, _I, _LL = ctypes.c_void_p, ctypes.c_int, ctypes.c_longlong
+_P, _I, _LL, _F = ctypes.c_void_p, ctypes.c_int, ctypes.c_longlong, ctypes.c_float
 _ATTN = [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I]
 
 
@@ -98,6 +100,11 @@ def lib() -> ctypes.CDLL:
             "ringattn_cache_read": [_P, _P, _P, _P],
             "ringattn_fwd_paged": [_P, _LL, _LL, _P, _P, _LL, _LL, _I, _P, _LL, _LL, _I, _I, _I, _I, _I, _P, _LL, _P],
             "ringattn_paged_workspace_bytes": [_I, _I, _I, _I, _I, _I, _P],
+            "ringattn_cache_weights": [_P, _LL, _LL, _P, _LL, _LL, _P, _P, _LL, _F, _I, _I, _I, _I, _I, _P, _LL, _P],
+            "ringattn_cache_evict": [_P, _P, _LL, _P, _I, _I, _I, _P, _P, _P],
+            "ringattn_qk_norm_rope": [_P, _P, _P, _P],
+            "ringattn_qk_norm_rope_bwd": [_P, _P, _P, _P, _P, _P, _P, _LL, _P],
+            "ringattn_qk_norm_rope_workspace_bytes": [_I, _I, _I, _I, _P],
             "ringattn_rank_work": [_I, _I, _I, _I, _I, _P, _P, _P],
             "ringattn_sync_status": [_P],
             "ringattn_selftest_timeout": [_LL, _P],
@@ -377,18 +384,18 @@ _pack_paged = struct.Struct("7P5q8i").pack
 def _paged(k_cache, v_cache, k_scale, v_scale, block_table, cu, kv_len, total: int, dev: int):
     """(Hkv, d, ra_paged_kv as bytes): the library's description of a paged cache and the batch
     that uses it.  These calls run once a layer and token: what is right passes a few combined
-    tests, and only what is not goes on to the one that says why."""
+    tests, and only what is not goes on to the one that says why.  cu None: a call without token rows."""
     e4m3 = k_cache.dtype is torch.float8_e4m3fn
     dtype = torch.float8_e4m3fn if e4m3 else torch.bfloat16
     i32 = torch.int32
     shape = k_cache.shape
-    if not (k_cache.get_device() == v_cache.get_device() == block_table.get_device() == cu.get_device()
-            == kv_len.get_device() == dev and k_cache.dtype is dtype and v_cache.dtype is dtype
-            and block_table.dtype is i32 and cu.dtype is i32 and kv_len.dtype is i32
-            and len(shape) == 4 and v_cache.shape == shape and block_table.dim() == 2):
+    if not (k_cache.get_device() == v_cache.get_device() == block_table.get_device() == kv_len.get_device() == dev
+            and k_cache.dtype is dtype and v_cache.dtype is dtype and block_table.dtype is i32 and kv_len.dtype is i32
+            and (cu is None or (cu.dtype is i32 and cu.get_device() == dev)) and len(shape) == 4 and v_cache.shape == shape and block_table.dim() == 2):
         for t, name, dt, dim in ((k_cache, "k_cache", dtype, 4), (v_cache, "v_cache", dtype, 4),
                                  (block_table, "block_table", i32, 2), (cu, "cu", i32, 1), (kv_len, "kv_len", i32, 1)):
-            _strided(t, name, dt, dev, dim)
+            if t is not None or name != "cu":
+                _strided(t, name, dt, dev, dim)
         raise ValueError("k_cache and v_cache must have the same shape [n_pages, Hkv, page_size, d]")
     n, h, page, d = shape
     rows = h * page
@@ -410,12 +417,12 @@ def _paged(k_cache, v_cache, k_scale, v_scale, block_table, cu, kv_len, total: i
             raise ValueError("each page of k_scale and v_scale must be contiguous")
     batch, max_pages = block_table.shape
     t0, t1 = block_table.stride()
-    if cu.shape != (batch + 1,) or kv_len.shape != (batch,):
+    if (cu is not None and cu.shape != (batch + 1,)) or kv_len.shape != (batch,):
         raise ValueError("block_table must be [batch, max_pages], cu [batch + 1] and kv_len [batch]")
-    if (t1 != 1 and max_pages > 1) or not cu.is_contiguous() or not kv_len.is_contiguous():
+    if (t1 != 1 and max_pages > 1) or (cu is not None and not cu.is_contiguous()) or not kv_len.is_contiguous():
         raise ValueError("cu, kv_len and the rows of block_table must be contiguous")
-    return h, d, _pack_paged(k_cache.data_ptr(), v_cache.data_ptr(), ksp, vsp, block_table.data_ptr(), cu.data_ptr(),
-                             kv_len.data_ptr(), k0 if n > 1 else rows * d, v0 if n > 1 else rows * d, ks0, vs0,
+    return h, d, _pack_paged(k_cache.data_ptr(), v_cache.data_ptr(), ksp, vsp, block_table.data_ptr(),
+                             0 if cu is None else cu.data_ptr(), kv_len.data_ptr(), k0 if n > 1 else rows * d, v0 if n > 1 else rows * d, ks0, vs0,
                              t0 if batch > 1 else max_pages, n, page, h, d, e4m3, batch, max_pages, total)
 
 
@@ -509,6 +516,162 @@ def fwd_paged(q, k_cache, v_cache, out, lse, block_table, cu, kv_len, workspace,
     _check_rows("ringattn_fwd_paged", (_lib or lib()).ringattn_fwd_paged(
         qp, q0, q1, kv, op, o0, o1, f32, lse.data_ptr(), l0 if total > 1 else max(1, Hq), l1 if Hq > 1 else 1, Hq, max_q,
         causal, window, sinks, workspace.data_ptr(), workspace.shape[0], _raw_stream(stream, dev)), q=q, out=out)
+
+
+def _weights(weights, k_cache, dev: int):
+    """(address, page stride) of the weights beside a cache, [n_pages, Hkv, page_size] fp32."""
+    n, h, page = k_cache.shape[:3]
+    p, s0, s1 = _rows(weights, "weights", torch.float32, dev)
+    if weights.shape != (n, h, page):
+        raise ValueError("weights must be [n_pages, Hkv, page_size] with the cache's sizes")
+    if s1 != page:
+        raise ValueError("each page of weights must be contiguous")
+    return p, s0
+
+
+def cache_weights(q, lse, k_cache, v_cache, weights, block_table, cu, kv_len, workspace, *, max_q, decay=1.0, causal=1,
+                  window=0, sinks=0, k_scale=None, v_scale=None, stream=None) -> None:
+    """ringattn_cache_weights: add to weights [n_pages, Hkv, page_size] fp32 what every cached position gets of the
+    attention of q [total, Hq, d] bf16, whose lse [total, Hq] fp32 (any strides from 1 up) :func:`fwd_paged` has
+    left: decay times what was there (nothing, for the positions of q's own rows) plus the sum of exp(q.k - lse)
+    over the rows that see the position and the heads of the KV head.  The other arguments as for
+    :func:`fwd_paged`, whose workspace will do."""
+    if (max_q | causal | window | sinks) >> 31:
+        _ints(max_q=max_q, causal=causal, window=window, sinks=sinks)
+    dev = torch.cuda.current_device()
+    qp, q0, q1 = _rows(q, "q", torch.bfloat16, dev)
+    total, Hq, d = q.shape
+    _, kd, kv = _paged(k_cache, v_cache, k_scale, v_scale, block_table, cu, kv_len, total, dev)
+    if d != kd:
+        raise ValueError("q must be [total, Hq, d] with the cache's d")
+    if lse.get_device() != dev or lse.dtype is not torch.float32 or lse.shape != (total, Hq):
+        raise ValueError("lse must be a fp32 [total, Hq] tensor on the current device")
+    l0, l1 = lse.stride()
+    wp, w0 = _weights(weights, k_cache, dev)
+    if workspace.dtype is not torch.uint8 or workspace.get_device() != dev or workspace.stride() != (1,):
+        _strided(workspace, "workspace", torch.uint8, dev, 1)
+    _check_rows("ringattn_cache_weights", (_lib or lib()).ringattn_cache_weights(
+        qp, q0, q1, lse.data_ptr(), l0 if total > 1 else max(1, Hq), l1 if Hq > 1 else 1, kv, wp, w0, decay, Hq, max_q,
+        causal, window, sinks, workspace.data_ptr(), workspace.shape[0], _raw_stream(stream, dev)), q=q)
+
+
+def cache_evict(k_cache, v_cache, weights, block_table, kv_len, keep, kv_len_out, kept, *, sinks=0, recent=0,
+                k_scale=None, v_scale=None, stream=None) -> None:
+    """ringattn_cache_evict: of every sequence's positions keep[b] stay for each KV head (the first ``sinks``, the last
+    ``recent``, then those of the largest weight) and move to the front of its pages, in order, with their scales
+    and weights.  keep and kv_len_out [batch] int32 (kv_len_out may be kv_len); kept [batch, Hkv, max_keep] int32
+    receives where each of them was (-1 behind the last).  The cache as for :func:`cache_append`, weights as for
+    :func:`cache_weights`."""
+    if (sinks | recent) >> 31:
+        _ints(sinks=sinks, recent=recent)
+    dev = torch.cuda.current_device()
+    h, _, kv = _paged(k_cache, v_cache, k_scale, v_scale, block_table, None, kv_len, 0, dev)
+    wp, w0 = _weights(weights, k_cache, dev)
+    batch = block_table.shape[0]
+    for t, name, dim in ((keep, "keep", 1), (kv_len_out, "kv_len_out", 1), (kept, "kept", 3)):
+        _strided(t, name, torch.int32, dev, dim)
+        if t.shape[0] != batch or not t.is_contiguous():
+            raise ValueError("keep and kv_len_out must be [batch], kept [batch, Hkv, max_keep], contiguous")
+    if kept.shape[1] != h:
+        raise ValueError("kept must be [batch, Hkv, max_keep] with the cache's Hkv")
+    _check("ringattn_cache_evict", (_lib or lib()).ringattn_cache_evict(
+        kv, wp, w0, keep.data_ptr(), kept.shape[2], sinks, recent, kv_len_out.data_ptr(), kept.data_ptr(),
+        _raw_stream(stream, dev)))
+
+
+# ra_qk_rows and ra_qk_norm, fields in order
+_pack_qk_rows = struct.Struct("2P4qi4x").pack
+_pack_qk_norm = struct.Struct("4P8i2f").pack
+
+
+def _qk_rows(q, k, names, shapes, dtypes, dev: int):
+    """ra_qk_rows as bytes; q and k of the shapes given, both of one of the types."""
+    dt = q.dtype
+    if dt not in dtypes:
+        raise ValueError(f"{names[0]} must be {' or '.join(str(x) for x in dtypes)}, got {dt}")
+    qp, q0, q1 = _rows(q, names[0], dt, dev)
+    kp, k0, k1 = _rows(k, names[1], dt, dev)
+    if q.shape != shapes[0] or k.shape != shapes[1]:
+        raise ValueError(f"{names[0]} must be {list(shapes[0])} and {names[1]} {list(shapes[1])}")
+    return _pack_qk_rows(qp, kp, q0, q1, k0, k1, dt is torch.float32)
+
+
+_BF16 = (torch.bfloat16,)
+_BF16_F32 = (torch.bfloat16, torch.float32)
+
+
+def _qk_norm(q, k, position, cos_sin, q_weight, k_weight, eps, q_scale, interleaved, dev: int):
+    """(shapes of q and k, ra_qk_norm as bytes)."""
+    if q.dim() != 3 or k.dim() != 3 or q.shape[0] != k.shape[0] or q.shape[2] != k.shape[2]:
+        raise ValueError("q must be [total, Hq, d] and k [total, Hkv, d]")
+    total, hq, d = q.shape
+    f32 = torch.float32
+    wp, wt = [0, 0], None
+    for i, w in enumerate((q_weight, k_weight)):
+        if w is None:
+            continue
+        if wt is None:
+            wt = w.dtype
+        if w.dtype is not wt or wt not in _BF16_F32 or w.get_device() != dev or w.shape != (d,) or not w.is_contiguous():
+            raise ValueError("q_weight and k_weight must be [d] on the current device, contiguous, both bf16 or both fp32")
+        wp[i] = w.data_ptr()
+    if position.get_device() != dev or position.dtype is not torch.int32 or position.shape != (total,) or not position.is_contiguous():
+        raise ValueError("position must be a contiguous int32 [total] tensor on the current device")
+    if cos_sin.get_device() != dev or cos_sin.dtype is not f32 or cos_sin.dim() != 2 or not cos_sin.is_contiguous():
+        raise ValueError("cos_sin must be a contiguous fp32 [n_pos, rot] tensor on the current device")
+    n_pos, rot = cos_sin.shape
+    if n_pos >= 2 ** 31:
+        raise ValueError("cos_sin must have fewer than 2^31 rows")
+    return (q.shape, k.shape), _pack_qk_norm(wp[0], wp[1], cos_sin.data_ptr(), position.data_ptr(), total, hq, k.shape[1], d, rot,
+                                             n_pos, wt is f32, interleaved, eps, q_scale)
+
+
+def qk_norm_rope(q, k, q_out, k_out, position, cos_sin, *, q_weight=None, k_weight=None, eps=1e-6, q_scale=1.0, interleaved=0,
+                 stream=None) -> None:
+    """ringattn_qk_norm_rope: every head's row of q [total, Hq, d] and k [total, Hkv, d] bf16 (token and head strides
+    multiples of 8, at least d) normed by its root mean square, times the weight [d] (bf16 or fp32; None: ones), and turned by
+    cos_sin[position] ([n_pos, rot] fp32: rot / 2 cosines, then rot / 2 sines; position int32 [total]); q's rows also times
+    ``q_scale``.  q_out and k_out like q and k, in any such strides: [H, total, d] transposed is the ring's order; they may be
+    q and k.  interleaved: pairs (2 j, 2 j + 1) instead of (j, j + rot / 2).  Tokens whose position is outside the
+    table are left out."""
+    dev = torch.cuda.current_device()
+    shapes, norm = _qk_norm(q, k, position, cos_sin, q_weight, k_weight, eps, q_scale, interleaved, dev)
+    _check_rows("ringattn_qk_norm_rope", (_lib or lib()).ringattn_qk_norm_rope(
+        _qk_rows(q, k, ("q", "k"), shapes, _BF16, dev), _qk_rows(q_out, k_out, ("q_out", "k_out"), shapes, _BF16, dev), norm,
+        _raw_stream(stream, dev)), q=q, k=k, q_out=q_out, k_out=k_out)
+
+
+def qk_norm_rope_workspace_bytes(total: int, Hq: int, Hkv: int, d: int) -> int:
+    """ringattn_qk_norm_rope_workspace_bytes (host only)."""
+    _ints(total=total, Hq=Hq, Hkv=Hkv, d=d)
+    n = ctypes.c_longlong(0)
+    _check("ringattn_qk_norm_rope_workspace_bytes", lib().ringattn_qk_norm_rope_workspace_bytes(total, Hq, Hkv, d, ctypes.byref(n)))
+    return n.value
+
+
+def qk_norm_rope_bwd(q, k, dq_out, dk_out, dq, dk, position, cos_sin, workspace=None, *, q_weight=None, k_weight=None,
+                     dq_weight=None, dk_weight=None, eps=1e-6, q_scale=1.0, interleaved=0, stream=None) -> None:
+    """ringattn_qk_norm_rope_bwd: gradients of :func:`qk_norm_rope`.  q, k: what went in; dq_out, dk_out: gradients of
+    what came out, bf16 or fp32 (as :func:`attention_backward` gives them, transposed); dq, dk: of q and k, bf16 or fp32
+    (they may be dq_out and dk_out); dq_weight, dk_weight: [d] fp32, overwritten, or None.  workspace: a CUDA uint8
+    tensor of at least :func:`qk_norm_rope_workspace_bytes`, needed for the weights' gradients.  The other arguments as there."""
+    dev = torch.cuda.current_device()
+    shapes, norm = _qk_norm(q, k, position, cos_sin, q_weight, k_weight, eps, q_scale, interleaved, dev)
+    dw = []
+    for w in (dq_weight, dk_weight):
+        if w is not None and (w.get_device() != dev or w.dtype is not torch.float32 or w.shape != (q.shape[2],) or not w.is_contiguous()):
+            raise ValueError("dq_weight and dk_weight must be contiguous fp32 [d] tensors on the current device")
+        dw.append(0 if w is None else w.data_ptr())
+    if workspace is None:
+        if dw != [0, 0]:
+            raise ValueError("the weights' gradients need a workspace")
+        ws = size = 0
+    else:
+        ws, size = _strided(workspace, "workspace", torch.uint8, dev, 1), workspace.shape[0]
+    _check_rows("ringattn_qk_norm_rope_bwd", (_lib or lib()).ringattn_qk_norm_rope_bwd(
+        _qk_rows(q, k, ("q", "k"), shapes, _BF16, dev), _qk_rows(dq_out, dk_out, ("dq_out", "dk_out"), shapes, _BF16_F32, dev),
+        _qk_rows(dq, dk, ("dq", "dk"), shapes, _BF16_F32, dev), dw[0], dw[1], norm, ws, size, _raw_stream(stream, dev)),
+        q=q, k=k, dq_out=dq_out, dk_out=dk_out, dq=dq, dk=dk)
 
 
 def rank_work(S: int, c: int, causal: int, layout: int, tile: int = 128):
