@@ -644,6 +644,11 @@ bool paged_few(int total, int g, int max_q) {
     return static_cast<long long>(max_q < total ? max_q : total) * g <= ra::kPagedFewRows;
 }
 
+// (ringattn_cache_weights takes the same workspace)
+static_assert(sizeof(ra::WeightsSpace) <= 2 * ra::kPagedMaxShares * ra::kPagedMaxGroups * sizeof(ra::PagedPartial) &&
+                  sizeof(ra::WeightsSpace) <= 2 * ra::kPagedMaxShares * sizeof(ra::PagedChunkPartial),
+              "workspace");
+
 // Bytes of the workspace: two partial results a block, and for chunks the list of items (a
 // 64-bit count a pair of units and a block, an index a sequence).
 long long paged_workspace(int total, int batch, int g, int max_q, ra::PagedAttnParams* p) {
@@ -666,23 +671,27 @@ long long paged_workspace(int total, int batch, int g, int max_q, ra::PagedAttnP
     return (n + 255) / 256 * 256;
 }
 
+// q as [total, Hq, d], boxes of a unit's tokens x the heads of a KV head x 64 (P: a call's parameters)
+template <class P>
+int encode_q(CUtensorMap* map, const P& p) {
+    const ra::PagedKV& kv = p.kv;
+    cuuint64_t dims[3] = {static_cast<cuuint64_t>(kv.d), static_cast<cuuint64_t>(p.hq), static_cast<cuuint64_t>(kv.total)};
+    cuuint64_t strides[2] = {static_cast<cuuint64_t>(p.q_hs) * 2, static_cast<cuuint64_t>(p.q_ts) * 2};
+    cuuint32_t box[3] = {64, static_cast<cuuint32_t>(p.g), static_cast<cuuint32_t>(p.unit_tokens)};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(p.q), dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+               ? RA_OK
+               : RA_ERR_CUDA;
+}
+
 int encode_paged(const ra::PagedAttnParams& p, ra::PagedMaps* m) {
     const ra::PagedKV& kv = p.kv;
     int st;
     if ((st = encode_pool(&m->k, kv.k, kv.k_ps, kv, p.box_rows)) != RA_OK) return st;
     if ((st = encode_pool(&m->v, kv.v, kv.v_ps, kv, p.box_rows)) != RA_OK) return st;
-    if (p.unit_tokens > 0) {  // q as [total, Hq, d], boxes of a unit's tokens x the heads of a KV head x 64
-        cuuint64_t dims[3] = {static_cast<cuuint64_t>(kv.d), static_cast<cuuint64_t>(p.hq), static_cast<cuuint64_t>(kv.total)};
-        cuuint64_t strides[2] = {static_cast<cuuint64_t>(p.q_hs) * 2, static_cast<cuuint64_t>(p.q_ts) * 2};
-        cuuint32_t box[3] = {64, static_cast<cuuint32_t>(p.g), static_cast<cuuint32_t>(p.unit_tokens)};
-        cuuint32_t estr[3] = {1, 1, 1};
-        return g_encode(&m->q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(p.q), dims, strides, box, estr,
-                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
-                   ? RA_OK
-                   : RA_ERR_CUDA;
-    }
-    return RA_OK;
+    return p.unit_tokens > 0 ? encode_q(&m->q, p) : RA_OK;
 }
 
 // Checks that concern the pool and the batch alone.  A call without token rows leaves cu and total alone.
@@ -1014,8 +1023,18 @@ int ringattn_cache_weights(const void* q, long long q_token_stride, long long q_
     p.window = std::min(window, 1 << 30);
     p.sinks = std::min(sinks, 1 << 30);
     p.by_g = ra::make_fastdiv(static_cast<unsigned>(p.g));
+    p.space = static_cast<ra::WeightsSpace*>(workspace);
+    p.timeout_ns = wait_timeout_ns();
     p.err = dev->err;
-    return ra::launch_cache_weights(p, dev->sms, reinterpret_cast<cudaStream_t>(stream));
+    cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+    if (static_cast<long long>(p.max_q) * p.g <= ra::kWeightsFewRows) return ra::launch_cache_weights_few(p, dev->sms, cs);
+    while ((2 << p.unit_log) * p.g <= 128) ++p.unit_log;
+    p.unit_tokens = 1 << p.unit_log;
+    p.box_rows = std::gcd(p.kv.page, ra::kPagedTile);
+    CUtensorMap tk = {}, tq = {};
+    if ((st = get_encoder()) != RA_OK || (st = encode_q(&tq, p)) != RA_OK) return st;
+    if (!p.kv.e4m3 && (st = encode_pool(&tk, p.kv.k, p.kv.k_ps, p.kv, p.box_rows)) != RA_OK) return st;
+    return ra::launch_cache_weights_chunk(p, tk, tq, std::min(dev->sms, ra::kPagedMaxShares), cs);
 }
 
 int ringattn_cache_evict(const ra_paged_kv* kv, float* weights, long long weights_page_stride, const int* keep, int max_keep,

@@ -19,92 +19,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr float kLog2e = 1.4426950408889634f;
-
-// What the rows of one sequence see.  Positions are taken 16 at a time ("groups"): the visible ones first, then those
-// whose weight only fades (or starts at zero).
-struct Seen {
-    PagedSeq s;
-    int T;               // rows that count
-    int lo, sink_end;    // groups [0, sink_end) and [lo, hi) are seen by some row
-    int hi, end;         // [hi, end): behind the last row's position
-    int fades;           // groups [sink_end, lo) have to be scaled
-};
-
-__device__ __forceinline__ Seen look(const WeightsParams& p, int b) {
-    Seen r;
-    r.s = paged_seq(p.kv, b);
-    r.T = min(r.s.T, p.max_q);
-    r.lo = r.sink_end = r.hi = r.end = r.fades = 0;
-    if (r.T <= 0 || r.s.L <= 0) return r;
-    const int keys = p.causal ? max(0, min(r.s.L, r.s.base + r.T)) : r.s.L;
-    r.hi = (keys + kWeightsGroup - 1) / kWeightsGroup;
-    r.end = (r.s.L + kWeightsGroup - 1) / kWeightsGroup;
-    if (p.window > 0) {
-        r.lo = min(max(0, r.s.base - p.window + 1) / kWeightsGroup, r.hi);
-        r.sink_end = min((min(p.sinks, keys) + kWeightsGroup - 1) / kWeightsGroup, r.lo);
-        r.fades = p.decay != 1.f;
-    }
-    return r;
-}
-__device__ __forceinline__ int seen_groups(const Seen& r) { return r.sink_end + r.hi - r.lo; }
-__device__ __forceinline__ int other_groups(const Seen& r) { return (r.fades ? r.lo - r.sink_end : 0) + r.end - r.hi; }
-
-// Sums up to every sequence of groups times KV heads, in shared memory: seen[batch + 1], other[batch + 1].
-__device__ void count_groups(const WeightsParams& p, long long* seen, long long* other) {
-    __shared__ long long part[2][kWarps];
-    const int n = p.kv.batch, each = (n + kThreads - 1) / kThreads;
-    const int b0 = min(n, static_cast<int>(threadIdx.x) * each), b1 = min(n, b0 + each);
-    long long a = 0, o = 0;
-    for (int b = b0; b < b1; ++b) {
-        const Seen r = look(p, b);
-        seen[b] = a;
-        other[b] = o;
-        a += static_cast<long long>(seen_groups(r)) * p.kv.hkv;
-        o += static_cast<long long>(other_groups(r)) * p.kv.hkv;
-    }
-    // inclusive sums over the warp's lanes, then over the warps
-    const long long a0 = a, o0 = o;
-#pragma unroll
-    for (int d = 1; d < 32; d *= 2) {
-        const long long x = __shfl_up_sync(0xffffffffu, a, d), y = __shfl_up_sync(0xffffffffu, o, d);
-        if (threadIdx.x % 32 >= d) {
-            a += x;
-            o += y;
-        }
-    }
-    if (threadIdx.x % 32 == 31) {
-        part[0][threadIdx.x / 32] = a;
-        part[1][threadIdx.x / 32] = o;
-    }
-    __syncthreads();
-    for (int w = 0; w < static_cast<int>(threadIdx.x) / 32; ++w) {
-        a += part[0][w];
-        o += part[1][w];
-    }
-    if (threadIdx.x == kThreads - 1) {
-        seen[n] = a;
-        other[n] = o;
-    }
-    a -= a0;
-    o -= o0;
-    for (int b = b0; b < b1; ++b) {
-        seen[b] += a;
-        other[b] += o;
-    }
-    __syncthreads();
-}
-
-// The sequence whose groups hold number i of a list (sums[b] <= i < sums[b + 1]).
-__device__ __forceinline__ int find_group(const long long* sums, int batch, long long i) {
-    int lo = 0, hi = batch;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (sums[mid] <= i) lo = mid;
-        else hi = mid;
-    }
-    return lo;
-}
+constexpr float kLog2e = kWeightsLog2e;
 
 __device__ __forceinline__ uint4 ldg128(const void* p) {
     uint4 x;
@@ -115,18 +30,6 @@ __device__ __forceinline__ uint4 ldg128_stream(const void* p) {
     uint4 x;
     asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "l"(p));
     return x;
-}
-
-// Four e4m3 codes as two pairs of bf16, exact: an e4m3 number's bits, moved to where bf16 has its own, are the number
-// times 2^-120 (a subnormal code becomes a subnormal bf16 number).
-__device__ __forceinline__ uint32_t e4m3_bf16(uint32_t spread) {  // codes in bits 8..15 and 24..31
-    uint32_t x = ((spread >> 4) & 0x07f007f0u) | (spread & 0x80008000u), r;
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(0x7b807b80u));  // 2^120
-    return r;
-}
-__device__ __forceinline__ void expand4(uint32_t codes, uint32_t& a, uint32_t& b) {
-    a = e4m3_bf16(__byte_perm(codes, 0, 0x1404));
-    b = e4m3_bf16(__byte_perm(codes, 0, 0x3424));
 }
 
 // Columns 2 * (lane % 4) and the next one of a block of 8 query rows: what their scores are compared with.
@@ -179,7 +82,11 @@ __global__ void __launch_bounds__(kThreads) weights_kernel(const __grid_constant
     const PagedKV& kv = p.kv;
     long long* seen = sums;
     long long* other = sums + kv.batch + 1;
-    count_groups(p, seen, other);
+    sum_up<kThreads>(kv.batch, seen, other, [&](int b, long long& x, long long& y) {
+        const Seen r = look<kWeightsGroup>(p, b);
+        x = static_cast<long long>(seen_groups(r)) * kv.hkv;
+        y = static_cast<long long>(other_groups(r)) * kv.hkv;
+    });
     const int lane = threadIdx.x % 32, quad = lane / 4;
     const long long warp = blockIdx.x * static_cast<long long>(kWarps) + threadIdx.x / 32, warps = gridDim.x * static_cast<long long>(kWarps);
 
@@ -188,8 +95,8 @@ __global__ void __launch_bounds__(kThreads) weights_kernel(const __grid_constant
     const long long i_end = n * (warp + 1) / warps;
     while (i < i_end) {
         // one (sequence, KV head) after the other
-        const int b = find_group(seen, kv.batch, i);
-        const Seen r = look(p, b);
+        const int b = find_sequence(seen, kv.batch, i);
+        const Seen r = look<kWeightsGroup>(p, b);
         const int each = seen_groups(r);
         const int h = static_cast<int>((i - seen[b]) / each);
         int u = static_cast<int>((i - seen[b]) - static_cast<long long>(h) * each);
@@ -227,7 +134,7 @@ __global__ void __launch_bounds__(kThreads) weights_kernel(const __grid_constant
 #pragma unroll
             for (int m = 0; m < 2; ++m) {
                 const int j = j0 + quad + 8 * m;
-                if (j < r.s.base && p.decay != 0.f) old[m] = p.decay * wp[8 * m];
+                old[m] = faded(p, r, j, wp + 8 * m);
             }
             // whether some row does not see some of these keys
             const bool whole = (p.causal ? j0 + kWeightsGroup <= r.s.base + 1 : j0 + kWeightsGroup <= r.s.L) &&
@@ -290,17 +197,16 @@ __global__ void __launch_bounds__(kThreads) weights_kernel(const __grid_constant
     // positions that nobody sees: half a warp 16 of them
     const long long others = other[kv.batch];
     for (long long o = (others * warp / warps) + lane / 16; o < others * (warp + 1) / warps; o += 2) {
-        const int b = find_group(other, kv.batch, o);
-        const Seen r = look(p, b);
+        const int b = find_sequence(other, kv.batch, o);
+        const Seen r = look<kWeightsGroup>(p, b);
         const int each = other_groups(r);
         const int h = static_cast<int>((o - other[b]) / each), u = static_cast<int>((o - other[b]) - static_cast<long long>(h) * each);
-        const int gap = r.fades ? r.lo - r.sink_end : 0;
-        const int j0 = (u < gap ? r.sink_end + u : r.hi + u - gap) * kWeightsGroup, j = j0 + lane % 16;
+        const int j0 = other_group(r, u) * kWeightsGroup, j = j0 + lane % 16;
         int row;
         const int pg = paged_page(kv, b, j0, row);
         if (pg < 0 || j >= r.s.L || !RA_CHECKED(paged_place_ok(kv, pg, h, row, kWeightsGroup), p.err, kSiteWeightsPlace)) continue;
         float* wp = p.w + pg * p.w_ps + static_cast<long long>(h) * kv.page + row + lane % 16;
-        *wp = j < r.s.base && p.decay != 0.f ? p.decay * *wp : 0.f;
+        *wp = faded(p, r, j, wp);
     }
 }
 
@@ -319,13 +225,12 @@ int go(const WeightsParams& p, int sms, cudaStream_t stream) {
 
 template <int D, bool E4M3>
 int go_cols(const WeightsParams& p, int sms, cudaStream_t stream) {
-    const long long cols = static_cast<long long>(p.max_q) * p.g;
-    return cols <= 8 ? go<D, E4M3, 1>(p, sms, stream) : cols <= 16 ? go<D, E4M3, 2>(p, sms, stream) : go<D, E4M3, 0>(p, sms, stream);
+    return p.max_q * p.g <= 8 ? go<D, E4M3, 1>(p, sms, stream) : go<D, E4M3, 2>(p, sms, stream);
 }
 
 }  // namespace
 
-int launch_cache_weights(const WeightsParams& p, int sms, cudaStream_t stream) {
+int launch_cache_weights_few(const WeightsParams& p, int sms, cudaStream_t stream) {
     if (p.kv.d == 128) return p.kv.e4m3 ? go_cols<128, true>(p, sms, stream) : go_cols<128, false>(p, sms, stream);
     return p.kv.e4m3 ? go_cols<64, true>(p, sms, stream) : go_cols<64, false>(p, sms, stream);
 }

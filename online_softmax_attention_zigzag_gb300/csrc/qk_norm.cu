@@ -199,7 +199,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_bwd_kernel(const __grid_con
     using QY = typename Quad<DY32>::T;
     using QX = typename Quad<DX32>::T;
     constexpr int kTokens = kNormThreads / LPR;
-    __shared__ float sums[kTokens][8 * LPR];
+    __shared__ alignas(16) float sums[kTokens][8 * LPR];
     const int lane = threadIdx.x % LPR, slot = threadIdx.x / LPR;
     const Part part = block_part(p);
     const Pieces at = pieces(lane, p.rot, 8 * LPR);
