@@ -5,15 +5,19 @@
 // exp(s - lse) in a register.  No maximum, no exchange between threads, no second product: a unit of 128 x 128
 // scores costs 512 cycles of MMA, and as much of the exponential unit at 32 a cycle.
 //
-// An item is 256 keys of a (sequence, KV head), two tiles that stay in shared memory, and the units (128 query rows: a power of
-// two of tokens, all heads of the group) that see some of them; with one tile an SM would have to take in 64 bytes of q a
-// cycle, with two it is 32.  All units of all items form one list, sequence by sequence, head by head, pair of
+// An item is 256 keys of a (sequence, KV head), two tiles, and the units (128 query rows: a power of two of tokens, all heads
+// of the group) that see some of them.  The tiles lie in tensor memory as the products' A operands while q streams by: with both
+// operands in shared memory the MMAs alone read the 128 bytes a cycle that it gives, and q's copies (32 of them a cycle for two
+// tiles) and the loads of lse have to wait.  A thread adds up the same columns of both tiles, so that lse is loaded once for the
+// two: with one tile a thread those loads (16 bytes for each of 32 lanes, however equal) took as long as the MMAs.
+// All units of all items form one list, sequence by sequence, head by head, pair of
 // tiles by pair; a block takes an equal stretch of it.  How many units see a pair is a clamped linear function of the pair,
 // so that sums over pairs have closed forms and every role finds its way through the list by itself.  An item that the
 // stretches cut leaves partial sums, which a second kernel adds up in the blocks' order.
 //
-// Warps: 0-3 the sums of the first tile, 4-7 of the second, 8 issues the MMAs, 9 loads q and lse, 10-13 K (bf16: one of them
-// page boxes by TMA; e4m3: all four expand codes).  TMEM: four accumulators of 128 columns, in turn.
+// Warps: 0-15 the sums, four for every 32 columns; they also bring K from shared into tensor memory, out of its codes in
+// e4m3.  16 and 17 issue the tiles' MMAs, 18 loads q and lse, 19 K (page boxes).  TMEM: three accumulators of 128 columns in
+// turn, the two tiles of K behind them.
 #include <cuda_bf16.h>
 
 #include <cstddef>
@@ -25,25 +29,39 @@ namespace ra {
 namespace {
 
 constexpr int kTile = kPagedTile;
-constexpr int kMmaWarp = 8, kQWarp = 9, kKWarp = 10;
-constexpr int kThreads = 14 * 32;
-constexpr int kKSlots = 3, kQSlots = 3, kBiasSlots = 8, kAccs = 4;
+constexpr int kSumWarps = 16, kMmaWarp = 16, kQWarp = 18, kKWarp = 19;
+constexpr int kHalf = kTile / 2;  // columns of a warp's share of a unit
+constexpr int kSlots = 6;     // tiles of K and of q in shared memory (WeightsParams says how many of each)
+constexpr int kBiasSlots = 8, kAccs = 2, kItems = 4;  // (accumulators of each tile)
+constexpr int kAhead = 4;     // units whose lse the loader asks for at once
 constexpr uint32_t kTmemCols = 512;
 
-template <int D>
+template <int D, bool E4M3>
 struct Cfg {
+    static constexpr int kThreads = (E4M3 ? 23 : 20) * 32;
     static constexpr int kTileBytes = kTile * D * 2;
     static constexpr int kBoxBytes = kTile * 128;  // 64 columns of a tile
     static constexpr int kBoxes = D / 64;
-    static constexpr int kQOff = kKSlots * kTileBytes;
-    static constexpr int kSumsOff = kQOff + kQSlots * kTileBytes;
+    static constexpr int kSumsOff = kSlots * kTileBytes;
 };
 
+// One item of a block's stretch, as its loader hands it to the others.
+struct Item {
+    int b, h, pair;
+    int u0, u1;        // units; none: no more items
+    int begins, ends;  // whether the first and the last unit that see the pair are among them
+    int T, base, L, keys;
+};
+__device__ __forceinline__ int tiles_of(int pair, int keys) { return pair * kWeightsPair + kTile < keys ? 2 : 1; }
+
 struct Shared {
-    uint64_t k_full[kKSlots], k_empty[kKSlots], q_full[kQSlots], q_empty[kQSlots], bias_full[kBiasSlots], bias_empty[kBiasSlots],
-        acc_full[kAccs], acc_empty[kAccs], drain;
-    alignas(16) float bias[kBiasSlots][kTile];  // -lse in powers of two of a unit's rows; -inf: adds nothing
-    int care[kBiasSlots];           // some row of the unit adds nothing
+    uint64_t item_full[kItems], item_empty[kItems];
+    uint64_t k_full[kSlots], k_empty[kSlots], q_full[kSlots], q_empty[kSlots], bias_full[kBiasSlots], bias_empty[kBiasSlots],
+        acc_full[2][kAccs], acc_empty[2][kAccs], half_full[2], half_empty[2], drain[2];
+    Item item[kItems];
+    float half[2][kTile];  // what the second half of the columns gives a tile's keys
+    alignas(16) float bias[kBiasSlots][kTile];  // -lse in powers of two of a unit's rows; -inf: adds nothing; NaN: no row
+    int care[kBiasSlots];                       // some row of the unit adds nothing
     uint32_t tmem;
     int abort_flag;
 };
@@ -158,7 +176,6 @@ __device__ bool walk_next(const WeightsParams& p, Walk& w) {
     walk_item(w, -1);
     return true;
 }
-__device__ __forceinline__ int tiles_of(const Walk& w) { return w.pair * kWeightsPair + kTile < w.r.keys ? 2 : 1; }
 
 // ------------------------------------------------------------------ loading
 // A slot of a ring: waits until it is free.
@@ -172,73 +189,97 @@ __device__ __forceinline__ void drain_ring(uint64_t* full, uint32_t issued, uint
     }
 }
 
-template <int D>
+template <int D, bool E4M3>
 __device__ void q_role(const WeightsParams& p, const CUtensorMap* tq, uint32_t smem, Shared& sh, const long long* sums, const WaitCtl& wc) {
-    using C = Cfg<D>;
+    using C = Cfg<D, E4M3>;
     const int lane = threadIdx.x % 32;
     const uint32_t bytes = static_cast<uint32_t>(p.unit_tokens * p.g) * 128u * C::kBoxes;
     const uint64_t keep = make_policy_evict_last();
+    const uint32_t q_slots = kSlots - p.k_slots, q_base = smem + p.k_slots * C::kTileBytes;
     uint32_t n = 0;
     Walk w;
     bool ok = true;
     for (bool more = walk_begin(p, sums, w); more && ok; more = walk_next(p, w)) {
-        for (int u = w.u0; u < w.u1; ++u, ++n) {
-            const int t0 = u << p.unit_log, cols = min(p.unit_tokens, w.r.T - t0) * p.g;
-            // the unit's lse, asked for before the wait for its place
-            float x[4];
-            bool care = false;
+        for (int ub = w.u0; ub < w.u1 && ok; ub += kAhead) {
+            // lse of the next units, all asked for at once: one unit's at a time took longer than its MMAs
+            float x[kAhead][4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int c = lane + 32 * i;
-                x[i] = -INFINITY;
-                if (c >= cols) continue;
-                const int t = static_cast<int>(fdiv(static_cast<unsigned>(c), p.by_g)), head = w.h * p.g + c - t * p.g;
-                const long long row = w.r.s.q0 + t0 + t;
-                if (!RA_CHECKED(paged_row_ok(p.kv, p.hq, row, head), p.err, kSiteWeightsRow)) continue;
-                const float lse = __ldg(p.lse + row * p.l_ts + head * p.l_hs);
-                x[i] = lse == -INFINITY ? -INFINITY : -lse * kWeightsLog2e;
-                care |= x[i] == -INFINITY;
+            for (int k = 0; k < kAhead; ++k) {
+                const int t0 = (ub + k) << p.unit_log, cols = ub + k < w.u1 ? min(p.unit_tokens, w.r.T - t0) * p.g : 0;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int c = lane + 32 * i;
+                    x[k][i] = NAN;
+                    if (c >= cols) continue;
+                    const int t = static_cast<int>(fdiv(static_cast<unsigned>(c), p.by_g)), head = w.h * p.g + c - t * p.g;
+                    const long long row = w.r.s.q0 + t0 + t;
+                    if (RA_CHECKED(paged_row_ok(p.kv, p.hq, row, head), p.err, kSiteWeightsRow)) x[k][i] = __ldg(p.lse + row * p.l_ts + head * p.l_hs);
+                }
             }
-            care = __any_sync(0xffffffffu, care);
-            ok = take(sh.q_empty, n, kQSlots, wc);
-            if (!ok) break;
-            if (lane == 0) {
-                const uint32_t s = n % kQSlots;
-                mbar_arrive_expect_tx(&sh.q_full[s], bytes);
-                int tok = w.r.s.q0 + t0;
-                if (!RA_CHECKED(paged_row_ok(p.kv, p.hq, tok, w.h * p.g + p.g - 1), p.err, kSiteWeightsRow)) tok = 0;
-                for (int i = 0; i < C::kBoxes; ++i)
-                    tma_load_3d(smem + C::kQOff + s * C::kTileBytes + i * C::kBoxBytes, tq, &sh.q_full[s], i * 64, w.h * p.g, tok, keep);
-            }
-            __syncwarp();
-            ok = take(sh.bias_empty, n, kBiasSlots, wc);
-            if (!ok) {
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                if (ub + k >= w.u1) break;
+                ok = take(sh.q_empty, n, q_slots, wc);
+                if (!ok) break;
+                const int t0 = (ub + k) << p.unit_log;
+                if (lane == 0) {
+                    const uint32_t s = n % q_slots;
+                    mbar_arrive_expect_tx(&sh.q_full[s], bytes);
+                    int tok = w.r.s.q0 + t0;
+                    if (!RA_CHECKED(paged_row_ok(p.kv, p.hq, tok, w.h * p.g + p.g - 1), p.err, kSiteWeightsRow)) tok = 0;
+                    for (int i = 0; i < C::kBoxes; ++i)
+                        tma_load_3d(q_base + s * C::kTileBytes + i * C::kBoxBytes, tq, &sh.q_full[s], i * 64, w.h * p.g, tok, keep);
+                }
+                __syncwarp();
+                ok = take(sh.bias_empty, n, kBiasSlots, wc);
+                const uint32_t s = n % kBiasSlots;
                 ++n;
-                break;
-            }
-            const uint32_t s = n % kBiasSlots;
+                if (!ok) break;
+                bool care = false;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) sh.bias[s][lane + 32 * i] = x[i];
-            if (lane == 0) sh.care[s] = care;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.bias_full[s]);
+                for (int i = 0; i < 4; ++i) {
+                    const bool none = x[k][i] == -INFINITY;
+                    sh.bias[s][lane + 32 * i] = none ? -INFINITY : -x[k][i] * kWeightsLog2e;
+                    care |= none;
+                }
+                care = __any_sync(0xffffffffu, care);
+                if (lane == 0) sh.care[s] = care;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.bias_full[s]);
+            }
         }
     }
-    if (!ok && lane == 0) drain_ring(sh.q_full, n, kQSlots, wc);  // copies in flight land before the block ends
+    if (!ok && lane == 0) drain_ring(sh.q_full, n, q_slots, wc);  // copies in flight land before the block ends
+}
+
+// Hands an item on to the warps that issue and add up (null: no more).
+__device__ __forceinline__ bool publish(Shared& sh, uint32_t n, const Walk* w, const WaitCtl& wc) {
+    if (!take(sh.item_empty, n, kItems, wc)) return false;
+    if (threadIdx.x % 32 == 0) {
+        Item& it = sh.item[n % kItems];
+        if (w) it = Item{w->b, w->h, w->pair, w->u0, w->u1, w->u0 == w->first, w->u1 == w->last + 1, w->r.T, w->r.s.base, w->r.s.L, w->r.keys};
+        else it.u0 = it.u1 = 0;
+        mbar_arrive(&sh.item_full[n % kItems]);
+    }
+    __syncwarp();
+    return true;
 }
 
 // bf16: one warp, a lane a box of rows of one page.
 template <int D>
 __device__ void k_role(const WeightsParams& p, const CUtensorMap* tk, uint32_t smem, Shared& sh, const long long* sums, const WaitCtl& wc) {
-    using C = Cfg<D>;
+    using C = Cfg<D, false>;
     const PagedKV& kv = p.kv;
     const int lane = threadIdx.x % 32, rows = p.box_rows, boxes = kTile / rows;
     const uint64_t policy = make_policy_evict_first();
-    uint32_t n = 0;
+    const uint32_t slots = p.k_slots;
+    uint32_t n = 0, ni = 0;
     Walk w;
-    bool ok = true;
-    for (bool more = walk_begin(p, sums, w); more && ok; more = walk_next(p, w)) {
-        const int tiles = tiles_of(w);
+    bool more = walk_begin(p, sums, w), ok = true;
+    for (; ok; ++ni) {
+        ok = publish(sh, ni, more ? &w : nullptr, wc);
+        if (!ok || !more) break;
+        const int tiles = tiles_of(w.pair, w.r.keys);
         int pg[2], y[2];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
@@ -250,10 +291,10 @@ __device__ void k_role(const WeightsParams& p, const CUtensorMap* tk, uint32_t s
         }
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-            if (k >= tiles) continue;
-            ok = take(sh.k_empty, n, kKSlots, wc);
-            if (!ok) break;
-            const uint32_t s = n % kKSlots;
+            if (k >= tiles || !ok) continue;
+            ok = take(sh.k_empty, n, slots, wc);
+            if (!ok) continue;
+            const uint32_t s = n % slots;
             ++n;
             if (lane == 0) mbar_arrive_expect_tx(&sh.k_full[s], C::kTileBytes);
             __syncwarp();
@@ -261,21 +302,25 @@ __device__ void k_role(const WeightsParams& p, const CUtensorMap* tk, uint32_t s
                 for (int i = 0; i < C::kBoxes; ++i)  // (no page: zeros)
                     tma_load_3d(smem + s * C::kTileBytes + i * C::kBoxBytes + lane * rows * 128, tk, &sh.k_full[s], i * 64, y[k], pg[k], policy);
         }
+        more = walk_next(p, w);
     }
-    if (!ok && lane == 0) drain_ring(sh.k_full, n, kKSlots, wc);
+    if (!ok && lane == 0) drain_ring(sh.k_full, n, slots, wc);
 }
 
-// e4m3: four warps expand codes, a thread one 16-byte piece of D / 16 rows at a time.  The scales stay with the keys' sums.
+// e4m3: four warps expand codes, a thread one 16-byte piece of D / 16 rows.  The scales stay with the keys' sums.
 template <int D>
 __device__ void expand_role(const WeightsParams& p, uint32_t smem, Shared& sh, const long long* sums, const WaitCtl& wc) {
-    using C = Cfg<D>;
+    using C = Cfg<D, true>;
     constexpr int kPieces = D / 16, kRows = 128 / kPieces, kLoads = kTile / kRows;
     const PagedKV& kv = p.kv;
     const int i0 = threadIdx.x - kKWarp * 32, piece = i0 % kPieces, r0 = i0 / kPieces;
-    uint32_t n = 0;
+    const uint32_t slots = p.k_slots;
+    uint32_t n = 0, ni = 0;
     Walk w;
-    for (bool more = walk_begin(p, sums, w); more; more = walk_next(p, w)) {
-        const int tiles = tiles_of(w);
+    for (bool more = walk_begin(p, sums, w);; more = walk_next(p, w), ++ni) {
+        if (i0 < 32 && !publish(sh, ni, more ? &w : nullptr, wc)) return;
+        if (!more) return;
+        const int tiles = tiles_of(w.pair, w.r.keys);
         for (int k = 0; k < tiles; ++k, ++n) {
             uint4 x[kLoads];
 #pragma unroll
@@ -289,8 +334,8 @@ __device__ void expand_role(const WeightsParams& p, uint32_t smem, Shared& sh, c
                 x[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(kv.k) + pg * kv.k_ps +
                                                             (static_cast<long long>(w.h) * kv.page + row) * D) + piece);
             }
-            if (!take(sh.k_empty, n, kKSlots, wc)) return;
-            const uint32_t stage = smem + (n % kKSlots) * C::kTileBytes + (piece / 4) * C::kBoxBytes;
+            if (!take(sh.k_empty, n, slots, wc)) return;
+            const uint32_t stage = smem + (n % slots) * C::kTileBytes + (piece / 4) * C::kBoxBytes;
 #pragma unroll
             for (int i = 0; i < kLoads; ++i) {
                 const int r = i * kRows + r0;
@@ -304,8 +349,23 @@ __device__ void expand_role(const WeightsParams& p, uint32_t smem, Shared& sh, c
                 sts128(at + (((c + 1) ^ (r & 7)) << 4), y[4], y[5], y[6], y[7]);
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            mbar_arrive(&sh.k_full[n % kKSlots]);
+            mbar_arrive(&sh.k_full[n % slots]);
         }
+    }
+}
+
+// Item after item, until there are none (true) or a wait has run out: f(item) returns whether all went well.  Every warp of the
+// takers takes every item.
+template <class F>
+__device__ __forceinline__ bool take_items(Shared& sh, const WaitCtl& wc, F&& f) {
+    for (uint32_t n = 0;; ++n) {
+        const uint32_t s = n % kItems;
+        if (!mbar_wait_w(&sh.item_full[s], (n / kItems) & 1u, wc)) return false;
+        const volatile Item& it = sh.item[s];
+        if (it.u0 == it.u1) return true;
+        if (!f(it)) return false;
+        __syncwarp();
+        if (threadIdx.x % 32 == 0) mbar_arrive(&sh.item_empty[s]);
     }
 }
 
@@ -321,42 +381,48 @@ __device__ __forceinline__ void issue_scores(uint32_t d_tmem, uint32_t k_base, u
     }
 }
 
-template <int D>
-__device__ void mma_role(const WeightsParams& p, uint32_t smem, Shared& sh, const long long* sums, uint32_t tmem, const WaitCtl& wc) {
-    using C = Cfg<D>;
+// One warp a tile: each of an issuer's waits takes 100 to 300 cycles even where its barrier has long completed.
+template <int D, bool E4M3>
+__device__ void mma_role(const WeightsParams& p, int tile, uint32_t smem, Shared& sh, uint32_t tmem, const WaitCtl& wc) {
+    using C = Cfg<D, E4M3>;
+    const uint32_t k_slots = p.k_slots, q_slots = kSlots - k_slots, q_base = smem + k_slots * C::kTileBytes;
     uint32_t nk = 0, nq = 0, na = 0;
-    Walk w;
-    bool ok = true;
-    for (bool more = walk_begin(p, sums, w); more && ok; more = walk_next(p, w)) {
-        const int tiles = tiles_of(w);
-        for (int k = 0; k < tiles && ok; ++k) ok = mbar_wait_w(&sh.k_full[(nk + k) % kKSlots], ((nk + k) / kKSlots) & 1u, wc);
-        for (int u = w.u0; u < w.u1 && ok; ++u, ++nq) {
-            const int cols = min(p.unit_tokens, w.r.T - (u << p.unit_log)) * p.g;
-            const uint32_t idesc = idesc_bf16(kTile, 16, 0) + (static_cast<uint32_t>((cols - 1) / 16 * 2) << 17);  // N: cols, in sixteens
-            ok = mbar_wait_w(&sh.q_full[nq % kQSlots], (nq / kQSlots) & 1u, wc);
-            for (int k = 0; k < tiles && ok; ++k, ++na) {
-                ok = mbar_wait_w(&sh.acc_empty[na % kAccs], ((na / kAccs) & 1u) ^ 1u, wc);
-                if (!ok) break;
-                tc_fence_after();
-                issue_scores<D>(tmem + (na % kAccs) * kTile, smem + ((nk + k) % kKSlots) * C::kTileBytes,
-                                smem + C::kQOff + (nq % kQSlots) * C::kTileBytes, idesc);
-                mma_commit_e(&sh.acc_full[na % kAccs]);
-            }
-            if (ok) mma_commit_e(&sh.q_empty[nq % kQSlots]);
-        }
-        if (ok)
-            for (int k = 0; k < tiles; ++k) mma_commit_e(&sh.k_empty[(nk + k) % kKSlots]);
+    const bool ok = take_items(sh, wc, [&](const volatile Item& it) -> bool {
+        const int tiles = tiles_of(it.pair, it.keys), u1 = it.u1, T = it.T;
+        const bool on = tile < tiles;
+        const uint32_t slot = (nk + tile) % k_slots;
+        // (both tiles: an issuer that does not look at a slot's every round could take one for the next but one)
+        for (int k = 0; k < tiles; ++k)
+            if (!mbar_wait_w(&sh.k_full[(nk + k) % k_slots], ((nk + k) / k_slots) & 1u, wc)) return false;
         nk += tiles;
-    }
+        for (int u = it.u0; u < u1; ++u, ++nq) {
+            const int cols = min(p.unit_tokens, T - (u << p.unit_log)) * p.g;
+            const uint32_t idesc = idesc_bf16(kTile, 16, 0) + (static_cast<uint32_t>((cols - 1) / 16 * 2) << 17);  // N: cols, in sixteens
+            const uint32_t qs = nq % q_slots;
+            if (on) {
+                const uint32_t acc = na % kAccs;
+                if (!mbar_wait2_w(&sh.q_full[qs], (nq / q_slots) & 1u, &sh.acc_empty[tile][acc], ((na / kAccs) & 1u) ^ 1u, wc)) return false;
+                ++na;
+                tc_fence_after();
+                issue_scores<D>(tmem + (tile * kAccs + acc) * kTile, smem + slot * C::kTileBytes, q_base + qs * C::kTileBytes, idesc);
+                mma_commit_e(&sh.acc_full[tile][acc]);
+            } else if (!mbar_wait_w(&sh.q_full[qs], (nq / q_slots) & 1u, wc)) {
+                return false;
+            }
+            mma_commit_e(&sh.q_empty[qs]);
+        }
+        for (int k = 0; k < tiles; ++k) mma_commit_e(&sh.k_empty[(nk - tiles + k) % k_slots]);
+        return true;
+    });
     if (!ok) {  // every MMA that was issued must finish before TMEM is released
-        mma_commit_e(&sh.drain);
-        drain_wait(&sh.drain, 0, wc.timeout_ns);
+        mma_commit_e(&sh.drain[tile]);
+        drain_wait(&sh.drain[tile], 0, wc.timeout_ns);
     }
 }
 
 // ------------------------------------------------------------------ the keys' sums
-// Adds up 32 columns from c on; all of them are seen.
-__device__ __forceinline__ void add_block(const uint32_t (&s)[32], const float* bias, float mul, float (&sum)[4]) {
+// Adds up 32 columns; all of them are seen.
+__device__ __forceinline__ void add_block(const uint32_t* s, const float* bias, float mul, float (&sum)[4]) {
 #pragma unroll
     for (int i = 0; i < 32; i += 4) {
         const float4 m = *reinterpret_cast<const float4*>(bias + i);
@@ -368,7 +434,7 @@ __device__ __forceinline__ void add_block(const uint32_t (&s)[32], const float* 
     }
 }
 // Those among [from, to) whose row adds something.
-__device__ __forceinline__ void add_some(const uint32_t (&s)[32], const float* bias, float mul, int from, int to, float (&sum)[4]) {
+__device__ __forceinline__ void add_some(const uint32_t* s, const float* bias, float mul, int from, int to, float (&sum)[4]) {
 #pragma unroll
     for (int i = 0; i < 32; ++i) {
         const float m = bias[i], x = ex2(fmaf(__uint_as_float(s[i]), mul, m));
@@ -376,125 +442,140 @@ __device__ __forceinline__ void add_some(const uint32_t (&s)[32], const float* b
     }
 }
 
-template <bool E4M3>
-__device__ void sum_role(const WeightsParams& p, int tile, Shared& sh, const long long* sums, uint32_t tmem, const WaitCtl& wc) {
+// Four warps: columns [64 half, 64 half + 64) of tile `tile`, a key a thread.
+template <int D, bool E4M3>
+__device__ void sum_role(const WeightsParams& p, int tile, int half, Shared& sh, uint32_t tmem, const WaitCtl& wc) {
     const PagedKV& kv = p.kv;
-    const int r = threadIdx.x % kTile, lane = threadIdx.x % 32;
-    const uint32_t lanes = static_cast<uint32_t>(threadIdx.x / 32 % 4 * 32) << 16;
-    uint32_t nq = 0, na = 0;
-    Walk w;
-    for (bool more = walk_begin(p, sums, w); more; more = walk_next(p, w)) {
-        const int tiles = tiles_of(w);
-        const int j0 = w.pair * kWeightsPair + tile * kTile, j = j0 + r;
-        // where the key's weight is, what it was, and its scale: used after the last unit, and from the first one on
+    const int r = threadIdx.x % kTile, lane = threadIdx.x % 32, c0 = half * kHalf;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(threadIdx.x / 32 % 4 * 32) << 16) + tile * kAccs * kTile + c0;
+    uint32_t nq = 0, na = 0, item = 0;
+    take_items(sh, wc, [&](const volatile Item& it) -> bool {
+        const int T = it.T, u1 = it.u1, base = it.base, j = it.pair * kWeightsPair + tile * kTile + r;
+        const bool on = tile < tiles_of(it.pair, it.keys), whole_item = it.begins && it.ends;
+        // where the key's weight is, what it was, and its scale
         float* wp = nullptr;
-        float old = 0.f, mul = kWeightsLog2e;
-        if (j < w.r.s.L) {
+        float old = 0.f, mul = kWeightsLog2e, total = 0.f;
+        if (j < it.L) {
             int row;
-            const int pg = paged_page(kv, w.b, j, row);
-            if (pg >= 0 && RA_CHECKED(paged_place_ok(kv, pg, w.h, row), p.err, kSiteWeightsPlace)) {
-                const long long at = static_cast<long long>(w.h) * kv.page + row;
+            const int h = it.h, pg = paged_page(kv, it.b, j, row);
+            if (pg >= 0 && RA_CHECKED(paged_place_ok(kv, pg, h, row), p.err, kSiteWeightsPlace)) {
+                const long long at = static_cast<long long>(h) * kv.page + row;
                 wp = p.w + pg * p.w_ps + at;
-                if (E4M3 && j < w.r.keys) mul *= __ldg(kv.k_scale + pg * kv.ks_ps + at);
+                if (E4M3 && j < it.keys) mul *= __ldg(kv.k_scale + pg * kv.ks_ps + at);
+                if (half == 0 && whole_item && j < base && p.decay != 0.f) old = p.decay * *wp;
             }
         }
-        const bool whole_item = w.u0 == w.first && w.u1 == w.last + 1;
-        if (wp && whole_item) old = faded(p, w.r, j, wp);
         // tokens that see the key
-        const int t_from = p.causal ? max(0, j - w.r.s.base) : 0;
-        auto before = [&](int key) { return static_cast<int>(min(static_cast<long long>(w.r.T), static_cast<long long>(key) - w.r.s.base + p.window)); };
-        const int t_to = p.window > 0 && j >= p.sinks ? before(j) : w.r.T;
-        // and those that see the whole tile (positions behind the last included: they are not written)
-        const int all_from = p.causal ? max(0, j0 + kTile - 1 - w.r.s.base) : 0;
-        const int all_to = p.window > 0 && j0 + kTile > p.sinks ? before(max(j0, p.sinks)) : w.r.T;
-        float total = 0.f;
-        for (int u = w.u0; u < w.u1; ++u, ++nq, na += tiles) {
+        const int t_from = p.causal ? max(0, j - base) : 0;
+        const int t_to = p.window > 0 && j >= p.sinks ? static_cast<int>(min(static_cast<long long>(T), static_cast<long long>(j) - base + p.window)) : T;
+        for (int u = it.u0; u < u1; ++u, ++nq) {
             const uint32_t slot = nq % kBiasSlots;
-            if (!mbar_wait_w(&sh.bias_full[slot], (nq / kBiasSlots) & 1u, wc)) return;
-            if (tile < tiles) {
-                const int t0 = u << p.unit_log, t1 = min(t0 + p.unit_tokens, w.r.T), cols = (t1 - t0) * p.g;
-                const bool whole = t0 >= all_from && t1 <= all_to && !sh.care[slot];
-                const int from = min(max(t_from - t0, 0), p.unit_tokens) * p.g, to = max(min(t_to, t1) - t0, 0) * p.g;
-                const uint32_t acc = (na + tile) % kAccs;
-                if (!mbar_wait_w(&sh.acc_full[acc], ((na + tile) / kAccs) & 1u, wc)) return;
+            if (!mbar_wait_w(&sh.bias_full[slot], (nq / kBiasSlots) & 1u, wc)) return false;
+            if (on) {
+                const int t0 = u << p.unit_log, t1 = min(t0 + p.unit_tokens, T);
+                // the unit's rows that see the key, and whether all rows see all the warp's keys
+                const int from = min(max(t_from - t0, 0), p.unit_tokens) * p.g - c0, to = max(min(t_to, t1) - t0, 0) * p.g - c0;
+                const bool all = __all_sync(0xffffffffu, from <= 0 && to >= kHalf) && !sh.care[slot];
+                const uint32_t acc = na % kAccs;
+                if (!mbar_wait_w(&sh.acc_full[tile][acc], (na / kAccs) & 1u, wc)) return false;
+                ++na;
                 tc_fence_after();
-                const uint32_t at = tmem + lanes + acc * kTile;
-                const float* bias = sh.bias[slot];
+                const uint32_t at = lanes + acc * kTile;
+                const float* bias = sh.bias[slot] + c0;
                 float sum[4] = {0.f, 0.f, 0.f, 0.f};
-                if (whole && cols == kTile) {
-                    uint32_t a[32], b[32];
-                    tmem_ld32(at, a);
+                if (all) {
+                    // the scores leave tensor memory at once, so that the next product can begin
+                    uint32_t x[2][32];
+                    tmem_ld32(at, x[0]);
+                    tmem_ld32(at + 32, x[1]);
                     tmem_wait_ld();
-                    tmem_ld32(at + 32, b);
-                    add_block(a, bias, mul, sum);
-                    tmem_wait_ld();
-                    tmem_ld32(at + 64, a);
-                    add_block(b, bias + 32, mul, sum);
-                    tmem_wait_ld();
-                    tmem_ld32(at + 96, b);
-                    add_block(a, bias + 64, mul, sum);
-                    tmem_wait_ld();
-                    add_block(b, bias + 96, mul, sum);
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sh.acc_empty[tile][acc]);
+                    add_block(x[0], bias, mul, sum);
+                    add_block(x[1], bias + 32, mul, sum);
                 } else {
-                    for (int c = 0; c < cols; c += 32) {
-                        uint32_t a[32];
-                        tmem_ld32(at + c, a);
+#pragma unroll 1
+                    for (int c = 0; c < kHalf; c += 32) {
+                        // (a block of columns that sees none of the warp's keys, or all)
+                        if (__all_sync(0xffffffffu, from >= c + 32 || to <= c || from >= to)) continue;
+                        uint32_t x[32];
+                        tmem_ld32(at + c, x);
                         tmem_wait_ld();
-                        if (whole && c + 32 <= cols) add_block(a, bias + c, mul, sum);
-                        else add_some(a, bias + c, mul, from - c, to - c, sum);
+                        if (__all_sync(0xffffffffu, from <= c && to >= c + 32) && !sh.care[slot]) add_block(x, bias + c, mul, sum);
+                        else add_some(x, bias + c, mul, from - c, to - c, sum);
                     }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sh.acc_empty[tile][acc]);
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sh.acc_empty[acc]);
                 total += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-            } else {
-                __syncwarp();
             }
+            __syncwarp();
             if (lane == 0) mbar_arrive(&sh.bias_empty[slot]);
         }
+        // the halves together
+        const uint32_t round = item++ & 1u;
+        if (half == 1) {
+            if (!mbar_wait_w(&sh.half_empty[tile], round ^ 1u, wc)) return false;
+            sh.half[tile][r] = total;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.half_full[tile]);
+            return true;
+        }
+        if (!mbar_wait_w(&sh.half_full[tile], round, wc)) return false;
+        total += sh.half[tile][r];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.half_empty[tile]);
         if (whole_item) {
             if (wp) *wp = old + total;
         } else {
-            WeightsPartial& part = p.space->part[blockIdx.x][w.u0 == w.first];
-            part.sum[tile * kTile + r] = total;
+            WeightsPartial& rest = p.space->part[blockIdx.x][it.begins];
+            rest.sum[tile * kTile + r] = total;
             if (threadIdx.x == 0) {
-                part.h = w.h;
-                part.pair = w.pair;
-                part.ends = w.u1 == w.last + 1;
-                part.b = w.b;
+                rest.h = it.h;
+                rest.pair = it.pair;
+                rest.ends = it.ends;
+                rest.b = it.b;
             }
         }
-    }
+        return true;
+    });
 }
 
 template <int D, bool E4M3>
-__global__ void __launch_bounds__(kThreads, 1) weights_chunk_kernel(const __grid_constant__ WeightsParams p, const __grid_constant__ CUtensorMap tk,
+__global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1) weights_chunk_kernel(const __grid_constant__ WeightsParams p, const __grid_constant__ CUtensorMap tk,
                                                                     const __grid_constant__ CUtensorMap tq) {
-    using C = Cfg<D>;
+    using C = Cfg<D, E4M3>;
     extern __shared__ uint8_t raw[];
     __shared__ Shared sh;
     static_assert(offsetof(Shared, bias) % 16 == 0 && alignof(Shared) >= 16, "bias is read four at a time");
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~static_cast<uintptr_t>(1023));
     const int warp = threadIdx.x / 32;
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kKSlots; ++i) {
+        for (int i = 0; i < kSlots; ++i) {
             mbar_init(&sh.k_full[i], E4M3 ? 128 : 1);
-            mbar_init(&sh.k_empty[i], 1);
-        }
-        for (int i = 0; i < kQSlots; ++i) {
+            mbar_init(&sh.k_empty[i], 2);
             mbar_init(&sh.q_full[i], 1);
-            mbar_init(&sh.q_empty[i], 1);
+            mbar_init(&sh.q_empty[i], 2);
         }
         for (int i = 0; i < kBiasSlots; ++i) {
             mbar_init(&sh.bias_full[i], 1);
-            mbar_init(&sh.bias_empty[i], 8);
+            mbar_init(&sh.bias_empty[i], kSumWarps);
         }
-        for (int i = 0; i < kAccs; ++i) {
-            mbar_init(&sh.acc_full[i], 1);
-            mbar_init(&sh.acc_empty[i], 4);
+        for (int i = 0; i < kItems; ++i) {
+            mbar_init(&sh.item_full[i], 1);
+            mbar_init(&sh.item_empty[i], kSumWarps + 2);
         }
-        mbar_init(&sh.drain, 1);
+        for (int i = 0; i < 2; ++i) {
+            for (int k = 0; k < kAccs; ++k) {
+                mbar_init(&sh.acc_full[i][k], 1);
+                mbar_init(&sh.acc_empty[i][k], 8);
+            }
+            mbar_init(&sh.half_full[i], 4);
+            mbar_init(&sh.half_empty[i], 4);
+            mbar_init(&sh.drain[i], 1);
+        }
         sh.abort_flag = 0;
         p.space->part[blockIdx.x][0].b = p.space->part[blockIdx.x][1].b = -1;
         fence_mbar_init();
@@ -506,7 +587,7 @@ __global__ void __launch_bounds__(kThreads, 1) weights_chunk_kernel(const __grid
     long long* sums = p.kv.batch <= kWeightsSumsShared ? reinterpret_cast<long long*>(smem + C::kSumsOff) : p.space->sums[blockIdx.x];
     // (the counts of pairs that nobody sees lie where tiles will: only their sum is kept)
     long long* others = p.kv.batch <= kWeightsSumsShared ? sums + kWeightsSumsShared + 1 : reinterpret_cast<long long*>(smem);
-    sum_up<kThreads>(p.kv.batch, sums, others, [&](int b, long long& x, long long& y) {
+    sum_up<C::kThreads>(p.kv.batch, sums, others, [&](int b, long long& x, long long& y) {
         const Seen r = look<kWeightsPair>(p, b);
         x = seen_units(r, units_of(p, r)) * p.kv.hkv;
         y = static_cast<long long>(other_groups(r)) * p.kv.hkv;
@@ -519,17 +600,11 @@ __global__ void __launch_bounds__(kThreads, 1) weights_chunk_kernel(const __grid
     launch_dependents();
     const uint32_t tmem = sh.tmem, base = smem_u32(smem);
     const WaitCtl wc{&sh.abort_flag, p.err, p.timeout_ns};
-    if (warp < 8) {
-        sum_role<E4M3>(p, warp / 4, sh, sums, tmem, wc);
-    } else if (warp == kMmaWarp) {
-        mma_role<D>(p, base, sh, sums, tmem, wc);
-    } else if (warp == kQWarp) {
-        q_role<D>(p, &tq, base, sh, sums, wc);
-    } else if (E4M3) {
-        expand_role<D>(p, base, sh, sums, wc);
-    } else if (warp == kKWarp) {
-        k_role<D>(p, &tk, base, sh, sums, wc);
-    }
+    if (warp < kSumWarps) sum_role<D, E4M3>(p, warp / 8, warp / 4 % 2, sh, tmem, wc);
+    else if (warp < kQWarp) mma_role<D, E4M3>(p, warp - kMmaWarp, base, sh, tmem, wc);
+    else if (warp == kQWarp) q_role<D, E4M3>(p, &tq, base, sh, sums, wc);
+    else if (E4M3) expand_role<D>(p, base, sh, sums, wc);
+    else k_role<D>(p, &tk, base, sh, sums, wc);
     __syncwarp();
     tc_fence_before();
     __syncthreads();
@@ -587,7 +662,7 @@ __global__ void __launch_bounds__(kWeightsPair) weights_join_kernel(const __grid
 
 template <int D, bool E4M3>
 int launch_t(const WeightsParams& p, const CUtensorMap& tk, const CUtensorMap& tq, int shares, cudaStream_t stream) {
-    using C = Cfg<D>;
+    using C = Cfg<D, E4M3>;
     constexpr int kSmem = C::kSumsOff + 16 * (kWeightsSumsShared + 1) + 1024;
     const auto kernel = weights_chunk_kernel<D, E4M3>;
     static std::atomic<unsigned long long> done{0};
@@ -596,7 +671,7 @@ int launch_t(const WeightsParams& p, const CUtensorMap& tk, const CUtensorMap& t
                    cudaFuncSetAttribute(weights_join_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 16 * (kPagedMaxBatch + 1)) == cudaSuccess;
         }))
         return -4;
-    kernel<<<shares, kThreads, kSmem, stream>>>(p, tk, tq);
+    kernel<<<shares, C::kThreads, kSmem, stream>>>(p, tk, tq);
     if (cudaGetLastError() != cudaSuccess) return -4;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(shares);
