@@ -1049,7 +1049,7 @@ int ringattn_cache_evict(const ra_paged_kv* kv, float* weights, long long weight
                                            reinterpret_cast<uintptr_t>(kept)) & 3u) != 0)
         return RA_ERR_INVALID_ARG;
     if ((st = check_weights(weights, weights_page_stride, p.kv)) != RA_OK) return st;
-    if (max_keep > (1 << 30) || static_cast<long long>(p.kv.batch) * p.kv.hkv > INT_MAX) return RA_ERR_UNSUPPORTED;
+    if (max_keep > (1 << 30) || static_cast<long long>(p.kv.batch) * p.kv.hkv > INT_MAX / 8) return RA_ERR_UNSUPPORTED;
     DeviceInfo* dev = nullptr;
     if ((st = device_info(&dev)) != RA_OK) return st;
     p.w = weights;
