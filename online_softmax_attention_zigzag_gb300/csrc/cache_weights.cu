@@ -8,7 +8,8 @@
 //
 // Few-row kernel: a warp takes 16 keys of one page at a time, straight from global memory into mma.sync fragments.  The
 // order of the d elements in the product is free as long as K and q agree, so that a lane's fragments of two steps of
-// 16 are 16 neighbouring bytes of a row.
+// 16 are 16 neighbouring bytes of a row.  Bound by HBM: one token each of 64 sequences of up to 16k keys (64 query heads, 8 KV heads,
+// d = 128, bf16) 188 us, 6.4 TB/s; of 8 sequences of up to 128k keys in e4m3 190 us, 5.8 TB/s.
 #include <cuda_bf16.h>
 
 #include "cache_weights.h"
@@ -35,12 +36,14 @@ __device__ __forceinline__ uint4 ldg128_stream(const void* p) {
 // Columns 2 * (lane % 4) and the next one of a block of 8 query rows: what their scores are compared with.
 struct Column {
     float bias;    // lse in powers of two; +inf: adds nothing
+    float mul;     // what a product is multiplied by for a score in powers of two, but for the key's scale
     int end, from;  // sees j < end, and j >= from or j < sinks
 };
 
 __device__ __forceinline__ Column column(const WeightsParams& p, const Seen& r, int h, int c) {
     Column x;
     x.bias = INFINITY;
+    x.mul = kLog2e;
     x.end = 0;
     x.from = 0;
     if (c >= r.T * p.g) return x;
@@ -55,9 +58,11 @@ __device__ __forceinline__ Column column(const WeightsParams& p, const Seen& r, 
 }
 
 // q's fragments of a block of 8 query rows, column lane / 4: words 4 s .. 4 s + 3 are the 8 elements that go with the
-// lane's 8 of the keys, in pairs two steps' b0 and b1.  16 bytes of a key are 8 elements in bf16, 16 in e4m3.
+// lane's 8 of the keys, in pairs two steps' b0 and b1.  16 bytes of a key are 8 elements in bf16, 16 in e4m3.  For e4m3 they
+// become fp16, as the codes do (exactly, in one instruction for two of them): times a power of two that brings the row's largest
+// finite element to 2^14 .. 2^15, so that elements below 2^-28 of it lose bits.  Returns what undoes that.
 template <int D, bool E4M3>
-__device__ __forceinline__ void load_q(const WeightsParams& p, const Seen& r, int h, int c, uint32_t (&f)[D / 8]) {
+__device__ __forceinline__ float load_q(const WeightsParams& p, const Seen& r, int h, int c, uint32_t (&f)[D / 8]) {
     const bool on = c < r.T * p.g;
     const int t = on ? static_cast<int>(fdiv(static_cast<unsigned>(c), p.by_g)) : 0, head = h * p.g + (on ? c - t * p.g : 0);
     const long long row = r.s.q0 + t;
@@ -72,13 +77,48 @@ __device__ __forceinline__ void load_q(const WeightsParams& p, const Seen& r, in
         f[4 * s + 2] = x.z;
         f[4 * s + 3] = x.w;
     }
+    if (!E4M3) return 1.f;
+    int top = 0;  // largest biased exponent of a finite element
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) {
+        const int lo = (f[i] >> 7) & 0xff, hi = (f[i] >> 23) & 0xff;
+        top = max(top, max(lo == 0xff ? 0 : lo, hi == 0xff ? 0 : hi));
+    }
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    const int up = min(141 - top, 126);  // (rows below 2^-112: what fp32 can undo)
+    const float a = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) f[i] = pack_f16x2(__uint_as_float(f[i] << 16) * a, __uint_as_float(f[i] & 0xffff0000u) * a);
+    return __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
 }
 
-// NB > 0: all query rows of a sequence and KV head fit into NB blocks of 8 columns, which stay in registers.
+// Four e4m3 codes as two pairs of fp16, exact.
+__device__ __forceinline__ void codes_f16(uint32_t codes, uint32_t& a, uint32_t& b) {
+    a = e4m3x2_f16x2(codes & 0xffffu);
+    b = e4m3x2_f16x2(codes >> 16);
+}
+
+// A group of 16 keys: a lane's pieces of rows lane / 4 and lane / 4 + 8, their scales, weights and where those are.
+template <int D, bool E4M3>
+struct Keys {
+    static constexpr int kPieces = E4M3 ? D / 64 : D / 32;
+    uint4 k[2][kPieces];
+    float mul[2], old[2];
+    float* w;  // null: no page
+    int j0;
+};
+
+// Blocks of an SM, which share its registers.  bf16 keeps the loads of 16 warps in flight (64 x 16k tokens: 188 us with two, 195
+// with three).  In e4m3 a warp has half as many bytes in flight and turns codes into fp16 meanwhile: 8 x 128k take 190 us with
+// three, 236 with two, 222 with four, which spill; loading a group ahead, or two at a time, left no registers for the third: 243, 236.
+template <bool E4M3>
+constexpr int blocks_per_sm() { return E4M3 ? 3 : 2; }
+
+// All query rows of a sequence and KV head fit into NB blocks of 8 columns, which stay in registers.
 template <int D, bool E4M3, int NB>
-__global__ void __launch_bounds__(kThreads) weights_kernel(const __grid_constant__ WeightsParams p) {
+__global__ void __launch_bounds__(kThreads, blocks_per_sm<E4M3>()) weights_kernel(const __grid_constant__ WeightsParams p) {
     extern __shared__ long long sums[];
-    constexpr int kBlocks = NB > 0 ? NB : 1;
     const PagedKV& kv = p.kv;
     long long* seen = sums;
     long long* other = sums + kv.batch + 1;
@@ -102,95 +142,105 @@ __global__ void __launch_bounds__(kThreads) weights_kernel(const __grid_constant
         int u = static_cast<int>((i - seen[b]) - static_cast<long long>(h) * each);
         const int u_end = static_cast<int>(min(static_cast<long long>(each), u + (i_end - i)));
         i += u_end - u;
-        const int cols = r.T * p.g;
-        uint32_t qf[kBlocks][D / 8];
-        Column col[kBlocks][2];
-        if (NB > 0) {
+        uint32_t qf[NB][D / 8];
+        Column col[NB][2];
 #pragma unroll
-            for (int c = 0; c < NB; ++c) {
-                load_q<D, E4M3>(p, r, h, 8 * c + quad, qf[c]);
-                col[c][0] = column(p, r, h, 8 * c + 2 * (lane % 4));
-                col[c][1] = column(p, r, h, 8 * c + 2 * (lane % 4) + 1);
+        for (int c = 0; c < NB; ++c) {
+            const float undo = load_q<D, E4M3>(p, r, h, 8 * c + quad, qf[c]);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                col[c][e] = column(p, r, h, 8 * c + 2 * (lane % 4) + e);
+                if (E4M3) col[c][e].mul *= __shfl_sync(0xffffffffu, undo, 4 * (2 * (lane % 4) + e));
             }
         }
-        for (; u < u_end; ++u) {
-            const int j0 = (u < r.sink_end ? u : u - r.sink_end + r.lo) * kWeightsGroup;
-            int row;
-            const int pg = paged_page(kv, b, j0, row);
-            if (pg < 0 || !RA_CHECKED(paged_place_ok(kv, pg, h, row, kWeightsGroup), p.err, kSiteWeightsPlace)) continue;
-            const long long place = static_cast<long long>(h) * kv.page + row;
-            uint4 k[2][E4M3 ? D / 64 : D / 32];
-            float mul[2] = {kLog2e, kLog2e};
+        // groups follow one another on a page: its place is looked up once
+        int left = 0;  // groups of the page that are still to come
+        const char* kp = nullptr;
+        const float* sp = nullptr;
+        float* wp = nullptr;
+        auto fetch = [&](int at, Keys<D, E4M3>& f) {
+            f.j0 = (at < r.sink_end ? at : at - r.sink_end + r.lo) * kWeightsGroup;
+            if (left == 0 || at == r.sink_end) {
+                int row;
+                const int pg = paged_page(kv, b, f.j0, row);
+                left = (kv.page - row) / kWeightsGroup;
+                wp = nullptr;
+                if (pg >= 0 && RA_CHECKED(paged_place_ok(kv, pg, h, row, left * kWeightsGroup), p.err, kSiteWeightsPlace)) {
+                    const long long place = static_cast<long long>(h) * kv.page + row + quad;
+                    wp = p.w + pg * p.w_ps + place;
+                    kp = static_cast<const char*>(kv.k) + (pg * kv.k_ps + place * D) * (E4M3 ? 1 : 2) + 16 * (lane % 4);
+                    if (E4M3) sp = kv.k_scale + pg * kv.ks_ps + place;
+                }
+            }
+            --left;
+            f.w = wp;
+            if (!wp) return;
 #pragma unroll
             for (int m = 0; m < 2; ++m) {
-                const char* at = static_cast<const char*>(kv.k) +
-                                 (pg * kv.k_ps + (place + quad + 8 * m) * D) * (E4M3 ? 1 : 2) + 16 * (lane % 4);
 #pragma unroll
-                for (int s = 0; s < (E4M3 ? D / 64 : D / 32); ++s) k[m][s] = ldg128_stream(at + 64 * s);
-                if (E4M3) mul[m] = __ldg(kv.k_scale + pg * kv.ks_ps + place + quad + 8 * m) * kLog2e;
+                for (int s = 0; s < Keys<D, E4M3>::kPieces; ++s) f.k[m][s] = ldg128_stream(kp + 8 * m * D * (E4M3 ? 1 : 2) + 64 * s);
+                f.mul[m] = E4M3 ? __ldg(sp + 8 * m) : 1.f;
+                f.old[m] = faded(p, r, f.j0 + quad + 8 * m, wp + 8 * m);
             }
-            float* wp = p.w + pg * p.w_ps + place + quad;
-            float old[2] = {0.f, 0.f};
-#pragma unroll
-            for (int m = 0; m < 2; ++m) {
-                const int j = j0 + quad + 8 * m;
-                old[m] = faded(p, r, j, wp + 8 * m);
-            }
+            kp += kWeightsGroup * D * (E4M3 ? 1 : 2);
+            if (E4M3) sp += kWeightsGroup;
+            wp += kWeightsGroup;
+        };
+        auto use = [&](const Keys<D, E4M3>& f) {
+            if (!f.w) return;
+            const int j0 = f.j0;
             // whether some row does not see some of these keys
             const bool whole = (p.causal ? j0 + kWeightsGroup <= r.s.base + 1 : j0 + kWeightsGroup <= r.s.L) &&
                                (p.window <= 0 || j0 + kWeightsGroup <= p.sinks || j0 > r.s.base + r.T - 1 - p.window);
-            float sum[2] = {0.f, 0.f};
-            for (int c0 = 0; c0 < cols; c0 += 8 * kBlocks) {
-                if (NB == 0) {
-                    load_q<D, E4M3>(p, r, h, c0 + quad, qf[0]);
-                    col[0][0] = column(p, r, h, c0 + 2 * (lane % 4));
-                    col[0][1] = column(p, r, h, c0 + 2 * (lane % 4) + 1);
+            float sum[2] = {0.f, 0.f}, x[NB][4];
+#pragma unroll
+            for (int c = 0; c < NB; ++c)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[c][e] = 0.f;
+#pragma unroll
+            for (int s = 0; s < D / 32; ++s) {
+                uint4 ka, kb;
+                if (E4M3) {
+                    const uint4 ca = f.k[0][s / 2], cb = f.k[1][s / 2];
+                    codes_f16(s % 2 ? ca.z : ca.x, ka.x, ka.y);
+                    codes_f16(s % 2 ? ca.w : ca.y, ka.z, ka.w);
+                    codes_f16(s % 2 ? cb.z : cb.x, kb.x, kb.y);
+                    codes_f16(s % 2 ? cb.w : cb.y, kb.z, kb.w);
+                } else {
+                    ka = f.k[0][s];
+                    kb = f.k[1][s];
                 }
-                float x[kBlocks][4];
+                const uint32_t a0[4] = {ka.x, kb.x, ka.y, kb.y}, a1[4] = {ka.z, kb.z, ka.w, kb.w};
 #pragma unroll
-                for (int c = 0; c < kBlocks; ++c)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) x[c][e] = 0.f;
-#pragma unroll
-                for (int s = 0; s < D / 32; ++s) {
-                    uint4 ka, kb;
-                    if (E4M3) {
-                        const uint4 ca = k[0][s / 2], cb = k[1][s / 2];
-                        expand4(s % 2 ? ca.z : ca.x, ka.x, ka.y);
-                        expand4(s % 2 ? ca.w : ca.y, ka.z, ka.w);
-                        expand4(s % 2 ? cb.z : cb.x, kb.x, kb.y);
-                        expand4(s % 2 ? cb.w : cb.y, kb.z, kb.w);
-                    } else {
-                        ka = k[0][s];
-                        kb = k[1][s];
-                    }
-                    const uint32_t a0[4] = {ka.x, kb.x, ka.y, kb.y}, a1[4] = {ka.z, kb.z, ka.w, kb.w};
-#pragma unroll
-                    for (int c = 0; c < kBlocks; ++c) {
-                        mma16816<false>(x[c], a0, qf[c][4 * s], qf[c][4 * s + 1]);
-                        mma16816<false>(x[c], a1, qf[c][4 * s + 2], qf[c][4 * s + 3]);
-                    }
+                for (int c = 0; c < NB; ++c) {
+                    mma16816<E4M3>(x[c], a0, qf[c][4 * s], qf[c][4 * s + 1]);
+                    mma16816<E4M3>(x[c], a1, qf[c][4 * s + 2], qf[c][4 * s + 3]);
                 }
-#pragma unroll
-                for (int c = 0; c < kBlocks; ++c)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const Column& y = col[c][e % 2];
-                        bool on = y.bias != INFINITY;
-                        if (!whole) {
-                            const int j = j0 + quad + 8 * (e / 2);
-                            on = on && j < y.end && (j >= y.from || j < p.sinks);
-                        }
-                        const float pr = ex2(fmaf(x[c][e], mul[e / 2], -y.bias));
-                        sum[e / 2] += on ? pr : 0.f;
-                    }
             }
+#pragma unroll
+            for (int c = 0; c < NB; ++c)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const Column& y = col[c][e % 2];
+                    bool on = y.bias != INFINITY;
+                    if (!whole) {
+                        const int j = j0 + quad + 8 * (e / 2);
+                        on = on && j < y.end && (j >= y.from || j < p.sinks);
+                    }
+                    const float pr = ex2(fmaf(x[c][e], E4M3 ? f.mul[e / 2] * y.mul : kLog2e, -y.bias));
+                    sum[e / 2] += on ? pr : 0.f;
+                }
 #pragma unroll
             for (int m = 0; m < 2; ++m) {
                 sum[m] += __shfl_xor_sync(0xffffffffu, sum[m], 1);
                 sum[m] += __shfl_xor_sync(0xffffffffu, sum[m], 2);
-                if (lane % 4 == 0 && j0 + quad + 8 * m < r.s.L) wp[8 * m] = old[m] + sum[m];
+                if (lane % 4 == 0 && j0 + quad + 8 * m < r.s.L) f.w[8 * m] = f.old[m] + sum[m];
             }
+        };
+        for (; u < u_end; ++u) {
+            Keys<D, E4M3> f;
+            fetch(u, f);
+            use(f);
         }
     }
 
@@ -219,7 +269,7 @@ int go(const WeightsParams& p, int sms, cudaStream_t stream) {
             return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 16 * (kPagedMaxBatch + 1)) == cudaSuccess;
         }))
         return -4;
-    kernel<<<2 * sms, kThreads, 16 * (p.kv.batch + 1), stream>>>(p);
+    kernel<<<blocks_per_sm<E4M3>() * sms, kThreads, 16 * (p.kv.batch + 1), stream>>>(p);
     return cudaGetLastError() == cudaSuccess ? 0 : -4;
 }
 
