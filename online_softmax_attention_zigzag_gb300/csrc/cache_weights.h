@@ -15,7 +15,7 @@ enum WeightsCheckSite : int {
 
 constexpr int kWeightsGroup = 16;  // keys that a warp of the few-row kernel takes at a time, all on one page
 constexpr int kWeightsPair = 256;  // keys of an item of the chunk kernel: two tiles
-constexpr int kWeightsSumsShared = 1024;  // batches up to this keep the chunk kernel's sums in shared memory
+constexpr int kWeightsSumsShared = 256;  // batches up to this keep the chunk kernel's sums in shared memory
 
 // What a block of the chunk kernel leaves of an item whose query rows others have too.
 struct WeightsPartial {

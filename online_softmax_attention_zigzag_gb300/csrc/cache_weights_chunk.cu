@@ -20,8 +20,6 @@
 // turn, the two tiles of K behind them.
 #include <cuda_bf16.h>
 
-#include <cstddef>
-
 #include "cache_weights.h"
 #include "ptx_paged.cuh"
 
@@ -32,7 +30,9 @@ constexpr int kTile = kPagedTile;
 constexpr int kSumWarps = 16, kMmaWarp = 16, kQWarp = 18, kKWarp = 19;
 constexpr int kHalf = kTile / 2;  // columns of a warp's share of a unit
 constexpr int kSlots = 6;     // tiles of K and of q in shared memory (WeightsParams says how many of each)
-constexpr int kBiasSlots = 8, kAccs = 2, kItems = 4;  // (accumulators of each tile)
+constexpr int kAccs = 2, kItems = 4;  // (accumulators of each tile)
+constexpr int kBiasBytes = kTile * 32;  // a step of 16 of a product's operand
+constexpr int kTilesOff = kSlots * kBiasBytes;
 constexpr int kAhead = 4;     // units whose lse the loader asks for at once
 constexpr uint32_t kTmemCols = 512;
 
@@ -42,7 +42,7 @@ struct Cfg {
     static constexpr int kTileBytes = kTile * D * 2;
     static constexpr int kBoxBytes = kTile * 128;  // 64 columns of a tile
     static constexpr int kBoxes = D / 64;
-    static constexpr int kSumsOff = kSlots * kTileBytes;
+    static constexpr int kSumsOff = kTilesOff + kSlots * kTileBytes;
 };
 
 // One item of a block's stretch, as its loader hands it to the others.
@@ -56,12 +56,10 @@ __device__ __forceinline__ int tiles_of(int pair, int keys) { return pair * kWei
 
 struct Shared {
     uint64_t item_full[kItems], item_empty[kItems];
-    uint64_t k_full[kSlots], k_empty[kSlots], q_full[kSlots], q_empty[kSlots], bias_full[kBiasSlots], bias_empty[kBiasSlots],
+    uint64_t k_full[kSlots], k_empty[kSlots], q_full[kSlots], q_empty[kSlots],
         acc_full[2][kAccs], acc_empty[2][kAccs], half_full[2], half_empty[2], drain[2];
     Item item[kItems];
     float half[2][kTile];  // what the second half of the columns gives a tile's keys
-    alignas(16) float bias[kBiasSlots][kTile];  // -lse in powers of two of a unit's rows; -inf: adds nothing; NaN: no row
-    int care[kBiasSlots];                       // some row of the unit adds nothing
     uint32_t tmem;
     int abort_flag;
 };
@@ -189,13 +187,43 @@ __device__ __forceinline__ void drain_ring(uint64_t* full, uint32_t issued, uint
     }
 }
 
+// A number as three bf16 parts, each the rest rounded: 24 bits of it.
+__device__ __forceinline__ void split3(float x, uint32_t (&part)[3]) {
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+        part[i] = pack_bf16x2(x, 0.f) & 0xffffu;
+        x -= __uint_as_float(part[i] << 16);
+    }
+}
+// Row r of an operand's last step, 16 elements without swizzle: 8 rows x 16 bytes lie together, then the next 8 rows; the other
+// 8 elements 2048 bytes on.
+constexpr uint32_t kBiasStep = 2048;
+__device__ __forceinline__ uint32_t bias_row(uint32_t at, int r) { return at + (r / 8) * 128 + (r % 8) * 16; }
+// K's: 1 / scale, in parts each three times over.  With q's (-lse in parts, over and over) the step adds -lse / scale to a score.
+__device__ __forceinline__ void store_k_bias(uint32_t at, int r, float inv_scale) {
+    uint32_t a[3];
+    split3(inv_scale, a);
+    sts128(bias_row(at, r), a[0] | (a[0] << 16), a[0] | (a[1] << 16), a[1] | (a[1] << 16), a[2] | (a[2] << 16));
+    sts128(bias_row(at + kBiasStep, r), a[2], 0, 0, 0);
+}
+__device__ __forceinline__ void store_q_bias(uint32_t at, int r, float x) {
+    uint32_t b[3];
+    split3(x, b);
+    sts128(bias_row(at, r), b[0] | (b[1] << 16), b[2] | (b[0] << 16), b[1] | (b[2] << 16), b[0] | (b[1] << 16));
+    sts128(bias_row(at + kBiasStep, r), b[2], 0, 0, 0);
+}
+__device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+// Inverse scales and lse stay within 2^60, so that no product of their parts leaves fp32: a score of a row with a smaller scale is
+// nothing anyhow, and where lse is beyond, fp32 scores are whole trillions apart.
+__device__ __forceinline__ float held_scale(float scale) { return scale < 0x1p-60f ? 0x1p-60f : scale; }
+
 template <int D, bool E4M3>
 __device__ void q_role(const WeightsParams& p, const CUtensorMap* tq, uint32_t smem, Shared& sh, const long long* sums, const WaitCtl& wc) {
     using C = Cfg<D, E4M3>;
     const int lane = threadIdx.x % 32;
     const uint32_t bytes = static_cast<uint32_t>(p.unit_tokens * p.g) * 128u * C::kBoxes;
     const uint64_t keep = make_policy_evict_last();
-    const uint32_t q_slots = kSlots - p.k_slots, q_base = smem + p.k_slots * C::kTileBytes;
+    const uint32_t q_slots = kSlots - p.k_slots, q_base = smem + kTilesOff + p.k_slots * C::kTileBytes, b_base = smem + p.k_slots * kBiasBytes;
     uint32_t n = 0;
     Walk w;
     bool ok = true;
@@ -209,7 +237,7 @@ __device__ void q_role(const WeightsParams& p, const CUtensorMap* tq, uint32_t s
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int c = lane + 32 * i;
-                    x[k][i] = NAN;
+                    x[k][i] = 0.f;
                     if (c >= cols) continue;
                     const int t = static_cast<int>(fdiv(static_cast<unsigned>(c), p.by_g)), head = w.h * p.g + c - t * p.g;
                     const long long row = w.r.s.q0 + t0 + t;
@@ -231,21 +259,15 @@ __device__ void q_role(const WeightsParams& p, const CUtensorMap* tq, uint32_t s
                         tma_load_3d(q_base + s * C::kTileBytes + i * C::kBoxBytes, tq, &sh.q_full[s], i * 64, w.h * p.g, tok, keep);
                 }
                 __syncwarp();
-                ok = take(sh.bias_empty, n, kBiasSlots, wc);
-                const uint32_t s = n % kBiasSlots;
-                ++n;
-                if (!ok) break;
-                bool care = false;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const bool none = x[k][i] == -INFINITY;
-                    sh.bias[s][lane + 32 * i] = none ? -INFINITY : -x[k][i] * kWeightsLog2e;
-                    care |= none;
+                    const float v = x[k][i] == -INFINITY ? -0x1p60f : -x[k][i];  // (a row whose lse is -inf adds nothing)
+                    store_q_bias(b_base + (n % q_slots) * kBiasBytes, lane + 32 * i, v < -0x1p60f ? -0x1p60f : v > 0x1p60f ? 0x1p60f : v);
                 }
-                care = __any_sync(0xffffffffu, care);
-                if (lane == 0) sh.care[s] = care;
+                fence_async_shared();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&sh.bias_full[s]);
+                if (lane == 0) mbar_arrive(&sh.q_full[n % q_slots]);
+                ++n;
             }
         }
     }
@@ -300,7 +322,7 @@ __device__ void k_role(const WeightsParams& p, const CUtensorMap* tk, uint32_t s
             __syncwarp();
             if (lane < boxes)
                 for (int i = 0; i < C::kBoxes; ++i)  // (no page: zeros)
-                    tma_load_3d(smem + s * C::kTileBytes + i * C::kBoxBytes + lane * rows * 128, tk, &sh.k_full[s], i * 64, y[k], pg[k], policy);
+                    tma_load_3d(smem + kTilesOff + s * C::kTileBytes + i * C::kBoxBytes + lane * rows * 128, tk, &sh.k_full[s], i * 64, y[k], pg[k], policy);
         }
         more = walk_next(p, w);
     }
@@ -334,8 +356,17 @@ __device__ void expand_role(const WeightsParams& p, uint32_t smem, Shared& sh, c
                 x[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(kv.k) + pg * kv.k_ps +
                                                             (static_cast<long long>(w.h) * kv.page + row) * D) + piece);
             }
+            float scale = 1.f;  // of row i0
+            {
+                const int pos = w.pair * kWeightsPair + k * kTile + i0;
+                int row;
+                const int pg = pos < w.r.keys ? paged_page(kv, w.b, pos, row) : -1;
+                if (pg >= 0 && RA_CHECKED(paged_place_ok(kv, pg, w.h, row), p.err, kSiteWeightsPlace))
+                    scale = held_scale(__ldg(kv.k_scale + pg * kv.ks_ps + static_cast<long long>(w.h) * kv.page + row));
+            }
             if (!take(sh.k_empty, n, slots, wc)) return;
-            const uint32_t stage = smem + (n % slots) * C::kTileBytes + (piece / 4) * C::kBoxBytes;
+            store_k_bias(smem + (n % slots) * kBiasBytes, i0, 1.f / scale);
+            const uint32_t stage = smem + kTilesOff + (n % slots) * C::kTileBytes + (piece / 4) * C::kBoxBytes;
 #pragma unroll
             for (int i = 0; i < kLoads; ++i) {
                 const int r = i * kRows + r0;
@@ -348,7 +379,7 @@ __device__ void expand_role(const WeightsParams& p, uint32_t smem, Shared& sh, c
                 sts128(at + ((c ^ (r & 7)) << 4), y[0], y[1], y[2], y[3]);
                 sts128(at + (((c + 1) ^ (r & 7)) << 4), y[4], y[5], y[6], y[7]);
             }
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            fence_async_shared();
             mbar_arrive(&sh.k_full[n % slots]);
         }
     }
@@ -370,22 +401,32 @@ __device__ __forceinline__ bool take_items(Shared& sh, const WaitCtl& wc, F&& f)
 }
 
 // ------------------------------------------------------------------ MMA
-// S = K Q^T of a tile: 128 keys x n query rows.
+// Shared-memory matrix descriptor of a K-major operand without swizzle: `lbo` bytes to the next 16 bytes of a row, `sbo` to the
+// next 8 rows.
+__device__ __forceinline__ uint64_t sdesc_plain(uint32_t addr, uint32_t lbo, uint32_t sbo) {
+    return static_cast<uint64_t>((addr >> 4) & 0x3fffu) | static_cast<uint64_t>((lbo >> 4) & 0x3fffu) << 16 |
+           static_cast<uint64_t>((sbo >> 4) & 0x3fffu) << 32 | 1ull << 46;
+}
+
+// S = K Q^T - lse / scale of a tile: 128 keys x n query rows.
 template <int D>
-__device__ __forceinline__ void issue_scores(uint32_t d_tmem, uint32_t k_base, uint32_t q_base, uint32_t idesc) {
+__device__ __forceinline__ void issue_scores(uint32_t d_tmem, uint32_t k_base, uint32_t q_base, uint32_t k_bias, uint32_t q_bias, uint32_t idesc) {
     const uint64_t kd = sdesc_sw128(k_base, 16, 1024), qd = sdesc_sw128(q_base, 16, 1024);
 #pragma unroll
     for (int kk = 0; kk < D / 16; ++kk) {
         const uint32_t off = (kk / 4) * (kTile * 128 >> 4) + (kk % 4) * (32 >> 4);
         mma_ss_e(d_tmem, desc_add(kd, off), desc_add(qd, off), idesc, kk > 0 ? 1u : 0u);
     }
+    // last, so that the sums before are rounded at their own size
+    mma_ss_e(d_tmem, sdesc_plain(k_bias, kBiasStep, 128), sdesc_plain(q_bias, kBiasStep, 128), idesc, 1u);
 }
 
 // One warp a tile: each of an issuer's waits takes 100 to 300 cycles even where its barrier has long completed.
 template <int D, bool E4M3>
 __device__ void mma_role(const WeightsParams& p, int tile, uint32_t smem, Shared& sh, uint32_t tmem, const WaitCtl& wc) {
     using C = Cfg<D, E4M3>;
-    const uint32_t k_slots = p.k_slots, q_slots = kSlots - k_slots, q_base = smem + k_slots * C::kTileBytes;
+    const uint32_t k_slots = p.k_slots, q_slots = kSlots - k_slots, q_base = smem + kTilesOff + k_slots * C::kTileBytes,
+                   b_base = smem + k_slots * kBiasBytes;
     uint32_t nk = 0, nq = 0, na = 0;
     const bool ok = take_items(sh, wc, [&](const volatile Item& it) -> bool {
         const int tiles = tiles_of(it.pair, it.keys), u1 = it.u1, T = it.T;
@@ -404,7 +445,8 @@ __device__ void mma_role(const WeightsParams& p, int tile, uint32_t smem, Shared
                 if (!mbar_wait2_w(&sh.q_full[qs], (nq / q_slots) & 1u, &sh.acc_empty[tile][acc], ((na / kAccs) & 1u) ^ 1u, wc)) return false;
                 ++na;
                 tc_fence_after();
-                issue_scores<D>(tmem + (tile * kAccs + acc) * kTile, smem + slot * C::kTileBytes, q_base + qs * C::kTileBytes, idesc);
+                issue_scores<D>(tmem + (tile * kAccs + acc) * kTile, smem + kTilesOff + slot * C::kTileBytes, q_base + qs * C::kTileBytes,
+                                smem + (E4M3 ? slot * kBiasBytes : 0), b_base + qs * kBiasBytes, idesc);
                 mma_commit_e(&sh.acc_full[tile][acc]);
             } else if (!mbar_wait_w(&sh.q_full[qs], (nq / q_slots) & 1u, wc)) {
                 return false;
@@ -421,24 +463,23 @@ __device__ void mma_role(const WeightsParams& p, int tile, uint32_t smem, Shared
 }
 
 // ------------------------------------------------------------------ the keys' sums
-// Adds up 32 columns; all of them are seen.
-__device__ __forceinline__ void add_block(const uint32_t* s, const float* bias, float mul, float (&sum)[4]) {
+// Adds up 32 columns; all of them are seen.  (s: scores less lse; mul: their scale, to powers of two)
+__device__ __forceinline__ void add_block(const uint32_t (&s)[32], float mul, float (&sum)[4]) {
 #pragma unroll
     for (int i = 0; i < 32; i += 4) {
-        const float4 m = *reinterpret_cast<const float4*>(bias + i);
         float x[4];
-        ffma2(x[0], x[1], __uint_as_float(s[i]), __uint_as_float(s[i + 1]), mul, mul, m.x, m.y);
-        ffma2(x[2], x[3], __uint_as_float(s[i + 2]), __uint_as_float(s[i + 3]), mul, mul, m.z, m.w);
+        fmul2(x[0], x[1], __uint_as_float(s[i]), __uint_as_float(s[i + 1]), mul, mul);
+        fmul2(x[2], x[3], __uint_as_float(s[i + 2]), __uint_as_float(s[i + 3]), mul, mul);
         fadd2(sum[0], sum[1], sum[0], sum[1], ex2(x[0]), ex2(x[1]));
         fadd2(sum[2], sum[3], sum[2], sum[3], ex2(x[2]), ex2(x[3]));
     }
 }
-// Those among [from, to) whose row adds something.
-__device__ __forceinline__ void add_some(const uint32_t* s, const float* bias, float mul, int from, int to, float (&sum)[4]) {
+// Those among [from, to).
+__device__ __forceinline__ void add_some(const uint32_t (&s)[32], float mul, int from, int to, float (&sum)[4]) {
 #pragma unroll
     for (int i = 0; i < 32; ++i) {
-        const float m = bias[i], x = ex2(fmaf(__uint_as_float(s[i]), mul, m));
-        sum[i & 3] += i >= from && i < to && m != -INFINITY ? x : 0.f;
+        const float x = ex2(__uint_as_float(s[i]) * mul);
+        sum[i & 3] += i >= from && i < to ? x : 0.f;
     }
 }
 
@@ -448,7 +489,7 @@ __device__ void sum_role(const WeightsParams& p, int tile, int half, Shared& sh,
     const PagedKV& kv = p.kv;
     const int r = threadIdx.x % kTile, lane = threadIdx.x % 32, c0 = half * kHalf;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(threadIdx.x / 32 % 4 * 32) << 16) + tile * kAccs * kTile + c0;
-    uint32_t nq = 0, na = 0, item = 0;
+    uint32_t na = 0, item = 0;
     take_items(sh, wc, [&](const volatile Item& it) -> bool {
         const int T = it.T, u1 = it.u1, base = it.base, j = it.pair * kWeightsPair + tile * kTile + r;
         const bool on = tile < tiles_of(it.pair, it.keys), whole_item = it.begins && it.ends;
@@ -461,58 +502,50 @@ __device__ void sum_role(const WeightsParams& p, int tile, int half, Shared& sh,
             if (pg >= 0 && RA_CHECKED(paged_place_ok(kv, pg, h, row), p.err, kSiteWeightsPlace)) {
                 const long long at = static_cast<long long>(h) * kv.page + row;
                 wp = p.w + pg * p.w_ps + at;
-                if (E4M3 && j < it.keys) mul *= __ldg(kv.k_scale + pg * kv.ks_ps + at);
+                if (E4M3 && j < it.keys) mul *= held_scale(__ldg(kv.k_scale + pg * kv.ks_ps + at));
                 if (half == 0 && whole_item && j < base && p.decay != 0.f) old = p.decay * *wp;
             }
         }
         // tokens that see the key
         const int t_from = p.causal ? max(0, j - base) : 0;
         const int t_to = p.window > 0 && j >= p.sinks ? static_cast<int>(min(static_cast<long long>(T), static_cast<long long>(j) - base + p.window)) : T;
-        for (int u = it.u0; u < u1; ++u, ++nq) {
-            const uint32_t slot = nq % kBiasSlots;
-            if (!mbar_wait_w(&sh.bias_full[slot], (nq / kBiasSlots) & 1u, wc)) return false;
-            if (on) {
-                const int t0 = u << p.unit_log, t1 = min(t0 + p.unit_tokens, T);
-                // the unit's rows that see the key, and whether all rows see all the warp's keys
-                const int from = min(max(t_from - t0, 0), p.unit_tokens) * p.g - c0, to = max(min(t_to, t1) - t0, 0) * p.g - c0;
-                const bool all = __all_sync(0xffffffffu, from <= 0 && to >= kHalf) && !sh.care[slot];
-                const uint32_t acc = na % kAccs;
-                if (!mbar_wait_w(&sh.acc_full[tile][acc], (na / kAccs) & 1u, wc)) return false;
-                ++na;
-                tc_fence_after();
-                const uint32_t at = lanes + acc * kTile;
-                const float* bias = sh.bias[slot] + c0;
-                float sum[4] = {0.f, 0.f, 0.f, 0.f};
-                if (all) {
-                    // the scores leave tensor memory at once, so that the next product can begin
-                    uint32_t x[2][32];
-                    tmem_ld32(at, x[0]);
-                    tmem_ld32(at + 32, x[1]);
-                    tmem_wait_ld();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&sh.acc_empty[tile][acc]);
-                    add_block(x[0], bias, mul, sum);
-                    add_block(x[1], bias + 32, mul, sum);
-                } else {
+        for (int u = it.u0; u < u1 && on; ++u, ++na) {
+            const int t0 = u << p.unit_log, t1 = min(t0 + p.unit_tokens, T);
+            // the share's rows that see the key, and whether all rows see all the warp's keys
+            const int from = min(max(t_from - t0, 0), p.unit_tokens) * p.g - c0, to = max(min(t_to, t1) - t0, 0) * p.g - c0;
+            const bool all = __all_sync(0xffffffffu, from <= 0 && to >= kHalf);
+            const uint32_t acc = na % kAccs;
+            if (!mbar_wait_w(&sh.acc_full[tile][acc], (na / kAccs) & 1u, wc)) return false;
+            tc_fence_after();
+            const uint32_t at = lanes + acc * kTile;
+            float sum[4] = {0.f, 0.f, 0.f, 0.f};
+            if (all) {
+                // the scores leave tensor memory at once, so that the next product can begin
+                uint32_t x[2][32];
+                tmem_ld32(at, x[0]);
+                tmem_ld32(at + 32, x[1]);
+                tmem_wait_ld();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.acc_empty[tile][acc]);
+                add_block(x[0], mul, sum);
+                add_block(x[1], mul, sum);
+            } else {
 #pragma unroll 1
-                    for (int c = 0; c < kHalf; c += 32) {
-                        // (a block of columns that sees none of the warp's keys, or all)
-                        if (__all_sync(0xffffffffu, from >= c + 32 || to <= c || from >= to)) continue;
-                        uint32_t x[32];
-                        tmem_ld32(at + c, x);
-                        tmem_wait_ld();
-                        if (__all_sync(0xffffffffu, from <= c && to >= c + 32) && !sh.care[slot]) add_block(x, bias + c, mul, sum);
-                        else add_some(x, bias + c, mul, from - c, to - c, sum);
-                    }
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&sh.acc_empty[tile][acc]);
+                for (int c = 0; c < kHalf; c += 32) {
+                    // (a block of columns that sees none of the warp's keys, or all)
+                    if (__all_sync(0xffffffffu, from >= c + 32 || to <= c || from >= to)) continue;
+                    uint32_t x[32];
+                    tmem_ld32(at + c, x);
+                    tmem_wait_ld();
+                    if (__all_sync(0xffffffffu, from <= c && to >= c + 32)) add_block(x, mul, sum);
+                    else add_some(x, mul, from - c, to - c, sum);
                 }
-                total += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.acc_empty[tile][acc]);
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.bias_empty[slot]);
+            total += (sum[0] + sum[1]) + (sum[2] + sum[3]);
         }
         // the halves together
         const uint32_t round = item++ & 1u;
@@ -549,19 +582,14 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1) weights_chunk_kerne
     using C = Cfg<D, E4M3>;
     extern __shared__ uint8_t raw[];
     __shared__ Shared sh;
-    static_assert(offsetof(Shared, bias) % 16 == 0 && alignof(Shared) >= 16, "bias is read four at a time");
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~static_cast<uintptr_t>(1023));
     const int warp = threadIdx.x / 32;
     if (threadIdx.x == 0) {
         for (int i = 0; i < kSlots; ++i) {
             mbar_init(&sh.k_full[i], E4M3 ? 128 : 1);
             mbar_init(&sh.k_empty[i], 2);
-            mbar_init(&sh.q_full[i], 1);
+            mbar_init(&sh.q_full[i], 2);  // q, and -lse
             mbar_init(&sh.q_empty[i], 2);
-        }
-        for (int i = 0; i < kBiasSlots; ++i) {
-            mbar_init(&sh.bias_full[i], 1);
-            mbar_init(&sh.bias_empty[i], kSumWarps);
         }
         for (int i = 0; i < kItems; ++i) {
             mbar_init(&sh.item_full[i], 1);
@@ -593,7 +621,9 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1) weights_chunk_kerne
         y = static_cast<long long>(other_groups(r)) * p.kv.hkv;
     });
     if (blockIdx.x == 0 && threadIdx.x == 0) p.space->others = others[p.kv.batch];
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncthreads();  // (others may lie where the tiles will)
+    if (!E4M3 && threadIdx.x < kTile) store_k_bias(smem_u32(smem), threadIdx.x, 1.f);
+    fence_async_shared();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
