@@ -51,6 +51,7 @@ struct Item {
     int u0, u1;        // units; none: no more items
     int begins, ends;  // whether the first and the last unit that see the pair are among them
     int T, base, L, keys;
+    float scale[kWeightsPair];  // e4m3: of the keys, as held_scale gives them
 };
 __device__ __forceinline__ int tiles_of(int pair, int keys) { return pair * kWeightsPair + kTile < keys ? 2 : 1; }
 
@@ -73,11 +74,13 @@ struct Units {
     int step_log;  // units' worth of tokens of a pair: 256 / unit_tokens
     int first0, last0;  // first(p) = max(0, first0 + p step), last(p) = min(n - 1, last0 + p step)
     int whole;     // pairs below this are seen by the last unit (sinks; all without a window)
+    int extra;
 };
 __device__ __forceinline__ Units units_of(const WeightsParams& p, const Seen& r) {
     Units u;
     u.n = (r.T + p.unit_tokens - 1) >> p.unit_log;
     u.step_log = 8 - p.unit_log;
+    u.extra = p.item_units;
     // (floor of a token's number by a unit's tokens; a pair's 256 keys are a multiple of those)
     u.first0 = p.causal ? (-r.s.base) >> p.unit_log : INT_MIN / 2;
     u.last0 = static_cast<int>(min((kWeightsPair - 2ll - r.s.base + p.window) >> p.unit_log, 1ll << 30));
@@ -90,7 +93,7 @@ __device__ __forceinline__ int first_unit(const Units& u, int p) {
 __device__ __forceinline__ int last_unit(const Units& u, int p) {
     return p < u.whole ? u.n - 1 : static_cast<int>(min(static_cast<long long>(u.n - 1), u.last0 + (static_cast<long long>(p) << u.step_log)));
 }
-// Units of the pairs [a, b), all of them seen.
+// Units of the pairs [a, b), all of them seen, with what each pair costs beside.
 __device__ long long count_units(const Units& u, int a, int b) {
     if (b <= a) return 0;
     const long long step = 1ll << u.step_log;
@@ -103,18 +106,19 @@ __device__ long long count_units(const Units& u, int a, int b) {
     const long long w = min(max(u.whole, a), b);  // [a, w): the last unit
     const long long l = max(w, from(u.last0 - static_cast<long long>(u.n - 1)));
     const long long lasts = (w - a + b - l) * static_cast<long long>(u.n - 1) + step * (tri(l) - tri(w)) + u.last0 * (l - w);
-    return lasts - firsts + (b - a);
+    return lasts - firsts + (1ll + u.extra) * (b - a);
 }
 __device__ __forceinline__ long long seen_units(const Seen& r, const Units& u) {
     return count_units(u, 0, r.sink_end) + count_units(u, r.lo, r.hi);
 }
 
-// A block's stretch, item by item: units [u0, u1) of pair `pair`, of [first, last].
+// A block's stretch, item by item: units [u0, u1) of pair `pair`, of [first, last].  An item takes `extra` places of the list
+// before its units: who gets those alone does nothing for it.
 struct Walk {
     const long long* sums;
     long long at, end;
-    int b, h, pair, u0, u1, first, last;
-    long long each;  // units of the sequence and head
+    int b, h, pair, v0, u0, u1, first, last;
+    long long each;  // places of the sequence and head
     Seen r;
     Units u;
 };
@@ -125,11 +129,14 @@ __device__ void walk_sequence(const WeightsParams& p, Walk& w) {
     w.u = units_of(p, w.r);
     w.each = seen_units(w.r, w.u);
 }
-__device__ __forceinline__ void walk_item(Walk& w, int u0) {
+// The pair's units from place `skip` of it on; false if the stretch ends before the first.
+__device__ __forceinline__ bool walk_item(Walk& w, long long skip) {
     w.first = first_unit(w.u, w.pair);
     w.last = last_unit(w.u, w.pair);
-    w.u0 = u0 < 0 ? w.first : u0;
-    w.u1 = static_cast<int>(min(static_cast<long long>(w.last + 1), w.u0 + (w.end - w.at)));
+    w.v0 = w.first - w.u.extra + static_cast<int>(skip);
+    w.u0 = max(w.first, w.v0);
+    w.u1 = static_cast<int>(min(static_cast<long long>(w.last + 1), w.v0 + (w.end - w.at)));
+    return w.u1 > w.first;
 }
 // The first item; false if there is none.
 __device__ bool walk_begin(const WeightsParams& p, const long long* sums, Walk& w) {
@@ -156,12 +163,11 @@ __device__ bool walk_begin(const WeightsParams& p, const long long* sums, Walk& 
         else hi = mid;
     }
     w.pair = lo;
-    walk_item(w, first_unit(w.u, lo) + static_cast<int>(rest - count_units(w.u, from, lo)));
-    return true;
+    return walk_item(w, rest - count_units(w.u, from, lo));
 }
 // The next one.
 __device__ bool walk_next(const WeightsParams& p, Walk& w) {
-    w.at += w.u1 - w.u0;
+    w.at += w.u1 - w.v0;
     if (w.at >= w.end) return false;
     if (++w.pair == w.r.sink_end) w.pair = w.r.lo;
     if (w.pair >= w.r.hi) {
@@ -171,8 +177,7 @@ __device__ bool walk_next(const WeightsParams& p, Walk& w) {
         }
         w.pair = w.r.sink_end > 0 ? 0 : w.r.lo;
     }
-    walk_item(w, -1);
-    return true;
+    return walk_item(w, 0);
 }
 
 // ------------------------------------------------------------------ loading
@@ -225,7 +230,7 @@ __device__ void q_role(const WeightsParams& p, const CUtensorMap* tq, uint32_t s
     const uint64_t keep = make_policy_evict_last();
     const uint32_t q_slots = kSlots - p.k_slots, q_base = smem + kTilesOff + p.k_slots * C::kTileBytes, b_base = smem + p.k_slots * kBiasBytes;
     uint32_t n = 0;
-    Walk w;
+    Walk w = {};
     bool ok = true;
     for (bool more = walk_begin(p, sums, w); more && ok; more = walk_next(p, w)) {
         for (int ub = w.u0; ub < w.u1 && ok; ub += kAhead) {
@@ -274,17 +279,23 @@ __device__ void q_role(const WeightsParams& p, const CUtensorMap* tq, uint32_t s
     if (!ok && lane == 0) drain_ring(sh.q_full, n, q_slots, wc);  // copies in flight land before the block ends
 }
 
-// Hands an item on to the warps that issue and add up (null: no more).
-__device__ __forceinline__ bool publish(Shared& sh, uint32_t n, const Walk* w, const WaitCtl& wc) {
-    if (!take(sh.item_empty, n, kItems, wc)) return false;
-    if (threadIdx.x % 32 == 0) {
-        Item& it = sh.item[n % kItems];
-        if (w) it = Item{w->b, w->h, w->pair, w->u0, w->u1, w->u0 == w->first, w->u1 == w->last + 1, w->r.T, w->r.s.base, w->r.s.L, w->r.keys};
-        else it.u0 = it.u1 = 0;
-        mbar_arrive(&sh.item_full[n % kItems]);
+// Hands an item on to the warps that issue and add up (null: no more); one warp of the loaders.
+__device__ __forceinline__ void describe(Item& it, const Walk* w) {
+    if (!w) {
+        it.u0 = it.u1 = 0;
+        return;
     }
-    __syncwarp();
-    return true;
+    it.b = w->b;
+    it.h = w->h;
+    it.pair = w->pair;
+    it.u0 = w->u0;
+    it.u1 = w->u1;
+    it.begins = w->u0 == w->first;
+    it.ends = w->u1 == w->last + 1;
+    it.T = w->r.T;
+    it.base = w->r.s.base;
+    it.L = w->r.s.L;
+    it.keys = w->r.keys;
 }
 
 // bf16: one warp, a lane a box of rows of one page.
@@ -299,8 +310,14 @@ __device__ void k_role(const WeightsParams& p, const CUtensorMap* tk, uint32_t s
     Walk w;
     bool more = walk_begin(p, sums, w), ok = true;
     for (; ok; ++ni) {
-        ok = publish(sh, ni, more ? &w : nullptr, wc);
-        if (!ok || !more) break;
+        ok = take(sh.item_empty, ni, kItems, wc);
+        if (!ok) break;
+        if (lane == 0) {
+            describe(sh.item[ni % kItems], more ? &w : nullptr);
+            mbar_arrive(&sh.item_full[ni % kItems]);
+        }
+        __syncwarp();
+        if (!more) break;
         const int tiles = tiles_of(w.pair, w.r.keys);
         int pg[2], y[2];
 #pragma unroll
@@ -329,7 +346,8 @@ __device__ void k_role(const WeightsParams& p, const CUtensorMap* tk, uint32_t s
     if (!ok && lane == 0) drain_ring(sh.k_full, n, slots, wc);
 }
 
-// e4m3: four warps expand codes, a thread one 16-byte piece of D / 16 rows.  The scales stay with the keys' sums.
+// e4m3: four warps expand codes, a thread one 16-byte piece of D / 16 rows.  The codes of a tile are on their way while the tile
+// before is expanded.  The scales go along with the item.
 template <int D>
 __device__ void expand_role(const WeightsParams& p, uint32_t smem, Shared& sh, const long long* sums, const WaitCtl& wc) {
     using C = Cfg<D, true>;
@@ -337,51 +355,86 @@ __device__ void expand_role(const WeightsParams& p, uint32_t smem, Shared& sh, c
     const PagedKV& kv = p.kv;
     const int i0 = threadIdx.x - kKWarp * 32, piece = i0 % kPieces, r0 = i0 / kPieces;
     const uint32_t slots = p.k_slots;
-    uint32_t n = 0, ni = 0;
-    Walk w;
-    for (bool more = walk_begin(p, sums, w);; more = walk_next(p, w), ++ni) {
-        if (i0 < 32 && !publish(sh, ni, more ? &w : nullptr, wc)) return;
-        if (!more) return;
-        const int tiles = tiles_of(w.pair, w.r.keys);
-        for (int k = 0; k < tiles; ++k, ++n) {
-            uint4 x[kLoads];
+    uint32_t n = 0;
+    Walk w = {};
+    // the pages of a pair's 16 groups of 16 rows, a lane one of them: looked up once for all, an item ahead
+    constexpr int kGroups = kWeightsPair / 16;
+    int entry = -1, entry_row = 0;
+    auto look_up = [&]() {
+        const int pos = w.pair * kWeightsPair + 16 * (i0 % 32);
+        entry = -1;
+        if (i0 % 32 < kGroups && pos < w.r.keys) entry = paged_entry(kv, w.b, pos, entry_row);
+    };
+    auto load = [&](int k, uint4 (&x)[kLoads], float& scale) {
+        int pg = paged_checked(kv, entry);
+        if (pg >= 0 && !RA_CHECKED(paged_place_ok(kv, pg, w.h, entry_row, 16), p.err, kSiteWeightsPlace)) pg = -1;
+        const int pos0 = w.pair * kWeightsPair + k * kTile, base = w.h * kv.page;
+        auto place = [&](int row, int& page) {  // of row `row` of the tile
+            page = __shfl_sync(0xffffffffu, pg, k * (kTile / 16) + row / 16);
+            const int at = base + __shfl_sync(0xffffffffu, entry_row, k * (kTile / 16) + row / 16) + row % 16;
+            if (pos0 + row >= w.r.keys) page = -1;
+            return at;
+        };
+        int page, at = place(i0, page);
+        scale = page >= 0 ? __ldg(kv.k_scale + page * kv.ks_ps + at) : 1.f;
 #pragma unroll
-            for (int i = 0; i < kLoads; ++i) {
-                const int pos = w.pair * kWeightsPair + k * kTile + i * kRows + r0;
-                x[i] = make_uint4(0, 0, 0, 0);
-                if (pos >= w.r.keys) continue;
-                int row;
-                const int pg = paged_page(kv, w.b, pos, row);
-                if (pg < 0 || !RA_CHECKED(paged_place_ok(kv, pg, w.h, row), p.err, kSiteWeightsPlace)) continue;
-                x[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(kv.k) + pg * kv.k_ps +
-                                                            (static_cast<long long>(w.h) * kv.page + row) * D) + piece);
-            }
-            float scale = 1.f;  // of row i0
-            {
-                const int pos = w.pair * kWeightsPair + k * kTile + i0;
-                int row;
-                const int pg = pos < w.r.keys ? paged_page(kv, w.b, pos, row) : -1;
-                if (pg >= 0 && RA_CHECKED(paged_place_ok(kv, pg, w.h, row), p.err, kSiteWeightsPlace))
-                    scale = held_scale(__ldg(kv.k_scale + pg * kv.ks_ps + static_cast<long long>(w.h) * kv.page + row));
-            }
-            if (!take(sh.k_empty, n, slots, wc)) return;
-            store_k_bias(smem + (n % slots) * kBiasBytes, i0, 1.f / scale);
-            const uint32_t stage = smem + kTilesOff + (n % slots) * C::kTileBytes + (piece / 4) * C::kBoxBytes;
-#pragma unroll
-            for (int i = 0; i < kLoads; ++i) {
-                const int r = i * kRows + r0;
-                uint32_t y[8];
-                expand4(x[i].x, y[0], y[1]);
-                expand4(x[i].y, y[2], y[3]);
-                expand4(x[i].z, y[4], y[5]);
-                expand4(x[i].w, y[6], y[7]);
-                const uint32_t at = stage + r * 128, c = 2 * (piece % 4);
-                sts128(at + ((c ^ (r & 7)) << 4), y[0], y[1], y[2], y[3]);
-                sts128(at + (((c + 1) ^ (r & 7)) << 4), y[4], y[5], y[6], y[7]);
-            }
-            fence_async_shared();
-            mbar_arrive(&sh.k_full[n % slots]);
+        for (int i = 0; i < kLoads; ++i) {
+            at = place(i * kRows + r0, page);
+            x[i] = make_uint4(0, 0, 0, 0);
+            if (page >= 0) x[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(kv.k) + page * kv.k_ps + static_cast<long long>(at) * D) + piece);
         }
+    };
+    auto expand = [&](const uint4 (&x)[kLoads], float scale) -> bool {
+        if (!take(sh.k_empty, n, slots, wc)) return false;
+        store_k_bias(smem + (n % slots) * kBiasBytes, i0, 1.f / scale);
+        const uint32_t stage = smem + kTilesOff + (n % slots) * C::kTileBytes + (piece / 4) * C::kBoxBytes;
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const int r = i * kRows + r0;
+            uint32_t y[8];
+            expand4(x[i].x, y[0], y[1]);
+            expand4(x[i].y, y[2], y[3]);
+            expand4(x[i].z, y[4], y[5]);
+            expand4(x[i].w, y[6], y[7]);
+            const uint32_t at = stage + r * 128, c = 2 * (piece % 4);
+            sts128(at + ((c ^ (r & 7)) << 4), y[0], y[1], y[2], y[3]);
+            sts128(at + (((c + 1) ^ (r & 7)) << 4), y[4], y[5], y[6], y[7]);
+        }
+        fence_async_shared();
+        mbar_arrive(&sh.k_full[n % slots]);
+        ++n;
+        return true;
+    };
+    uint4 x0[kLoads];
+    float s0 = 1.f, s1 = 1.f;
+    bool more = walk_begin(p, sums, w);
+    if (more) {
+        look_up();
+        load(0, x0, s0);
+    }
+    for (uint32_t ni = 0;; ++ni) {
+        if (!take(sh.item_empty, ni, kItems, wc)) return;
+        Item& it = sh.item[ni % kItems];
+        if (!more) {
+            if (i0 == 0) describe(it, nullptr);
+            __syncwarp();
+            if (i0 % 32 == 0) mbar_arrive(&sh.item_full[ni % kItems]);
+            return;
+        }
+        const bool two = tiles_of(w.pair, w.r.keys) == 2;
+        s0 = held_scale(s0);
+        if (!expand(x0, s0)) return;
+        if (two) load(1, x0, s1);
+        s1 = held_scale(s1);
+        it.scale[i0] = s0;
+        it.scale[kTile + i0] = s1;
+        if (i0 == 0) describe(it, &w);
+        __syncwarp();
+        if (i0 % 32 == 0) mbar_arrive(&sh.item_full[ni % kItems]);
+        more = walk_next(p, w);
+        if (more) look_up();
+        if (two && !expand(x0, s1)) return;
+        if (more) load(0, x0, s0);
     }
 }
 
@@ -493,17 +546,16 @@ __device__ void sum_role(const WeightsParams& p, int tile, int half, Shared& sh,
     take_items(sh, wc, [&](const volatile Item& it) -> bool {
         const int T = it.T, u1 = it.u1, base = it.base, j = it.pair * kWeightsPair + tile * kTile + r;
         const bool on = tile < tiles_of(it.pair, it.keys), whole_item = it.begins && it.ends;
-        // where the key's weight is, what it was, and its scale
+        // where the key's weight is, and what it was: asked for now, used after the last unit
         float* wp = nullptr;
-        float old = 0.f, mul = kWeightsLog2e, total = 0.f;
-        if (j < it.L) {
+        float old = 0.f, total = 0.f;
+        const float mul = E4M3 ? kWeightsLog2e * it.scale[tile * kTile + r] : kWeightsLog2e;
+        if (half == 0 && j < it.L) {
             int row;
             const int h = it.h, pg = paged_page(kv, it.b, j, row);
             if (pg >= 0 && RA_CHECKED(paged_place_ok(kv, pg, h, row), p.err, kSiteWeightsPlace)) {
-                const long long at = static_cast<long long>(h) * kv.page + row;
-                wp = p.w + pg * p.w_ps + at;
-                if (E4M3 && j < it.keys) mul *= held_scale(__ldg(kv.k_scale + pg * kv.ks_ps + at));
-                if (half == 0 && whole_item && j < base && p.decay != 0.f) old = p.decay * *wp;
+                wp = p.w + pg * p.w_ps + static_cast<long long>(h) * kv.page + row;
+                if (whole_item && j < base && p.decay != 0.f) old = *wp;
             }
         }
         // tokens that see the key
@@ -561,7 +613,7 @@ __device__ void sum_role(const WeightsParams& p, int tile, int half, Shared& sh,
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.half_empty[tile]);
         if (whole_item) {
-            if (wp) *wp = old + total;
+            if (wp) *wp = (old != 0.f ? p.decay * old : 0.f) + total;
         } else {
             WeightsPartial& rest = p.space->part[blockIdx.x][it.begins];
             rest.sum[tile * kTile + r] = total;
@@ -592,7 +644,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1) weights_chunk_kerne
             mbar_init(&sh.q_empty[i], 2);
         }
         for (int i = 0; i < kItems; ++i) {
-            mbar_init(&sh.item_full[i], 1);
+            mbar_init(&sh.item_full[i], E4M3 ? 4 : 1);
             mbar_init(&sh.item_empty[i], kSumWarps + 2);
         }
         for (int i = 0; i < 2; ++i) {
