@@ -22,11 +22,12 @@ namespace cg = cooperative_groups;
 
 constexpr int kCluster = 8;  // most blocks of a (sequence, KV head)
 constexpr int kSelThreads = 1024;
+constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kKeys = 16;  // neighbouring positions of a thread, all on one page
 constexpr int kChunk = kKeys * kSelThreads;
 constexpr int kDigit = 11;  // bits; 32 = 11 + 11 + 10
 constexpr int kBins = 1 << kDigit;
-constexpr int kList = 3840;  // keys with the first digit in question that a block lists
+constexpr int kList = 5119;  // keys with the first digit in question that a block lists
 
 __device__ __forceinline__ uint32_t order(float w) {
     const uint32_t u = __float_as_uint(w);
@@ -45,18 +46,23 @@ __device__ __forceinline__ Sequence sequence(const EvictParams& p, int b) {
     return s;
 }
 
-// The order of positions [j0, j0 + 16), 0 from `end` on (below all others).
+// The order of positions [j0, j0 + kKeys), 0 from `end` on (below all others).
 __device__ __forceinline__ void load_keys(const EvictParams& p, int b, int h, int L, int j0, int end, uint32_t (&key)[kKeys]) {
 #pragma unroll
     for (int e = 0; e < kKeys; ++e) key[e] = 0u;
     if (j0 >= end) return;
-    int row;
-    const int pg = paged_page(p.kv, b, j0, row);
-    const bool ok = pg >= 0 && RA_CHECKED(paged_place_ok(p.kv, pg, h, row, kKeys), p.err, kSiteEvictPlace);
-    const float4* w = reinterpret_cast<const float4*>(p.w + (ok ? pg * p.w_ps + static_cast<long long>(h) * p.kv.page + row : 0));
+    const float4* w[kKeys / 16];
+    bool ok[kKeys / 16];
+#pragma unroll
+    for (int g = 0; g < kKeys / 16; ++g) {
+        int row = 0;
+        const int pg = j0 + 16 * g < end ? paged_page(p.kv, b, j0 + 16 * g, row) : -1;
+        ok[g] = pg >= 0 && RA_CHECKED(paged_place_ok(p.kv, pg, h, row, 16), p.err, kSiteEvictPlace);
+        w[g] = reinterpret_cast<const float4*>(p.w + (ok[g] ? pg * p.w_ps + static_cast<long long>(h) * p.kv.page + row : 0));
+    }
     float4 x[kKeys / 4];
 #pragma unroll
-    for (int i = 0; i < kKeys / 4; ++i) x[i] = ok ? w[i] : make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = 0; i < kKeys / 4; ++i) x[i] = ok[i / 4] ? w[i / 4][i % 4] : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int e = 0; e < kKeys; ++e) {
         const int j = j0 + e;
@@ -80,7 +86,7 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t x, uint32_t* sm, uint32_
     const uint32_t s = warp_scan(x);
     if (lane == 31) sm[warp] = s;
     __syncthreads();
-    const uint32_t w = warp_scan(sm[lane]);
+    const uint32_t w = warp_scan(lane < kSelWarps ? sm[lane] : 0u);
     const uint32_t before = __shfl_sync(0xffffffffu, w, (warp + 31) % 32);
     total = __shfl_sync(0xffffffffu, w, 31);
     __syncthreads();
@@ -95,10 +101,16 @@ __device__ __forceinline__ int find_lane(uint32_t count, uint32_t& need) {
 }
 
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_constant__ EvictParams p) {
-    __shared__ alignas(16) uint32_t hist[3][kBins];  // of this block
-    __shared__ alignas(16) uint32_t all[kBins], coarse[32];  // of the cluster; coarse: 64 bins each, the largest first
-    __shared__ uint32_t list[kList], listed;
-    __shared__ uint32_t sm[32], counts[2];
+    // this block's counts, the cluster's, the keys that are left; at the end the positions that stay
+    struct Counts {
+        uint32_t hist[3][kBins], list[kList + 1];  // (the last place of the list: for those that are not)
+    };
+    __shared__ alignas(16) Counts counts;
+    // sums of 64 bins each, the largest first: this block's, the cluster's, and the cluster's counts of the 64 in question
+    __shared__ alignas(8) uint32_t coarse[3][32], all_coarse[3][32], fine[3][64];
+    __shared__ uint32_t sm[kSelWarps], listed, stretch[2];
+    auto& hist = counts.hist;
+    auto& list = counts.list;
     cg::cluster_group cluster = cg::this_cluster();
     const int rank = static_cast<int>(cluster.block_rank()), ranks = static_cast<int>(cluster.num_blocks());
     const int head = blockIdx.x / ranks, b = head / p.kv.hkv, h = head - b * p.kv.hkv;
@@ -121,6 +133,8 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
     auto load = [&](int c) { load_keys(p, b, h, s.L, begin + c * kChunk + kKeys * static_cast<int>(threadIdx.x), end, key); };
     load(0);
     if (threadIdx.x == 0) listed = 0;
+    if (threadIdx.x < 96) (&all_coarse[0][0])[threadIdx.x] = 0;
+    if (threadIdx.x < 192) (&fine[0][0])[threadIdx.x] = 0;
     for (int i = threadIdx.x; i < 3 * kBins / 4; i += kSelThreads) reinterpret_cast<uint4*>(&hist[0][0])[i] = make_uint4(0, 0, 0, 0);
     __syncthreads();
     auto together = [&]() {
@@ -145,13 +159,13 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
                 uint32_t at = 0;
                 if (lane == 31 && to > 0) at = atomicAdd(&listed, to);
                 at = __shfl_sync(0xffffffffu, at, 31) + to - n;
-                if (n > 0) {
+                if (__any_sync(0xffffffffu, n > 0)) {
 #pragma unroll
-                    for (int e = 0; e < kKeys; ++e)
-                        if (key[e] != 0u && (key[e] & mask) == prefix) {
-                            if (at < kList) list[at] = key[e];
-                            ++at;
-                        }
+                    for (int e = 0; e < kKeys; ++e) {  // (without branches: sixteen of them took 5000 cycles)
+                        const bool on = key[e] != 0u && (key[e] & mask) == prefix;
+                        list[on ? min(at, static_cast<uint32_t>(kList)) : kList] = key[e];
+                        at += on;
+                    }
                 }
             }
             __syncthreads();
@@ -164,11 +178,17 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
             for (int c = 0; c < chunks; ++c) {
                 if (chunks > 1 && (c > 0 || pass > 0)) load(c);
                 // (weights that are all the same, zeros above all: additions to one place wait for each other)
-                bool same = true;
+                bool same = true, whole = pass == 0;
 #pragma unroll
-                for (int e = 1; e < kKeys; ++e) same = same && key[e] == key[0];
+                for (int e = 0; e < kKeys; ++e) {
+                    same = same && key[e] == key[0];
+                    whole = whole && key[e] != 0u;
+                }
                 if (same) {
                     if (key[0] != 0u && (key[0] & mask) == prefix) atomicAdd(&hist[pass][(key[0] >> shift) & digit], static_cast<uint32_t>(kKeys));
+                } else if (whole) {
+#pragma unroll
+                    for (int e = 0; e < kKeys; ++e) atomicAdd(&hist[0][key[e] >> 21], 1u);
                 } else {
 #pragma unroll
                     for (int e = 0; e < kKeys; ++e)
@@ -176,38 +196,36 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
                 }
             }
         }
-        together();
-        // warp w: 64 bins of all blocks, the largest of them first; two a lane
-        const int at = kBins - 2 - 2 * static_cast<int>(threadIdx.x);
-        uint2 x = *reinterpret_cast<const uint2*>(&hist[pass][at]);
-        if (ranks > 1) {
-            uint2 y[kCluster];
-#pragma unroll
-            for (int r = 0; r < kCluster; ++r)
-                if (r < ranks) y[r] = *reinterpret_cast<const uint2*>(cluster.map_shared_rank(&hist[pass][at], r));
-            x = make_uint2(0, 0);
-#pragma unroll
-            for (int r = 0; r < kCluster; ++r)
-                if (r < ranks) {
-                    x.x += y[r].x;
-                    x.y += y[r].y;
-                }
-        }
-        *reinterpret_cast<uint2*>(&all[at]) = x;
-        const uint32_t sum = __reduce_add_sync(0xffffffffu, x.x + x.y);
-        if (lane == 0) coarse[warp] = sum;
         __syncthreads();
-        // every warp for itself: which of the 32, which pair of bins, which of the two
-        const int c = find_lane(coarse[lane], need);
-        const uint2 y = *reinterpret_cast<const uint2*>(&all[kBins - 2 - 2 * (32 * c + lane)]);
-        const int l = find_lane(y.x + y.y, need);
-        const uint32_t upper = __shfl_sync(0xffffffffu, y.y, l), lower = __shfl_sync(0xffffffffu, y.x, l);
-        const bool in_upper = need <= upper;
-        if (!in_upper) need -= upper;
-        const int bin = kBins - 1 - 2 * (32 * c + l) - (in_upper ? 0 : 1);
+        static_assert(kBins == 2 * kSelThreads && kSelWarps == 32, "64 bins a warp");
+        const uint2 x = *reinterpret_cast<const uint2*>(&hist[pass][kBins - 2 - 2 * static_cast<int>(threadIdx.x)]);
+        const uint32_t sum = __reduce_add_sync(0xffffffffu, x.x + x.y);
+        if (lane == 0) coarse[pass][warp] = sum;
+        together();
+        // of the other blocks' counts only what is needed: first the sums, then the 64 in question (all 2048 of eight blocks took
+        // 4500 cycles, three times over)
+        if (warp < ranks) atomicAdd(&all_coarse[pass][lane], ranks > 1 ? *cluster.map_shared_rank(&coarse[pass][lane], warp) : coarse[pass][lane]);
+        __syncthreads();
+        const int c = find_lane(all_coarse[pass][lane], need);
+        if (warp < ranks) {
+            const uint32_t* y = &hist[pass][kBins - 2 - 2 * (32 * c + lane)];
+            const uint2 z = *reinterpret_cast<const uint2*>(ranks > 1 ? cluster.map_shared_rank(const_cast<uint32_t*>(y), warp) : y);
+            atomicAdd(&fine[pass][2 * lane], z.y);
+            atomicAdd(&fine[pass][2 * lane + 1], z.x);
+        }
+        __syncthreads();
+        const uint2 z = *reinterpret_cast<const uint2*>(&fine[pass][2 * lane]);
+        const int l = find_lane(z.x + z.y, need);
+        uint32_t count = __shfl_sync(0xffffffffu, z.x, l);
+        int bin = kBins - 1 - 2 * (32 * c + l);
+        if (need > count) {
+            need -= count;
+            count = __shfl_sync(0xffffffffu, z.y, l);
+            --bin;
+        }
         prefix |= static_cast<uint32_t>(bin) << shift;
         mask |= digit << shift;
-        if (need == (in_upper ? upper : lower)) {  // the whole bin stays: no need to look into it
+        if (need == count) {  // the whole bin stays: no need to look into it
             prefix -= 1u;
             need = 0;
             break;
@@ -233,35 +251,55 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
     }
     if (ranks > 1) {
         if (threadIdx.x == 0) {
-            counts[0] = above;
-            counts[1] = equal;
+            stretch[0] = above;
+            stretch[1] = equal;
         }
         cluster.sync();
         above = equal = 0;
-        for (int r = 0; r < rank; ++r) {
-            const uint32_t* x = cluster.map_shared_rank(counts, r);
-            above += x[0];
-            equal += x[1];
-        }
+        uint32_t x[kCluster][2];
+#pragma unroll
+        for (int r = 0; r < kCluster; ++r)
+            if (r < rank) {
+                x[r][0] = *cluster.map_shared_rank(&stretch[0], r);
+                x[r][1] = *cluster.map_shared_rank(&stretch[1], r);
+            }
+#pragma unroll
+        for (int r = 0; r < kCluster; ++r)
+            if (r < rank) {
+                above += x[r][0];
+                equal += x[r][1];
+            }
         cluster.barrier_arrive();  // (a block's shared memory has to be there while others read it)
     } else {
         above = equal = 0;
     }
-    // in order of position: everything above `prefix`, and the first `need` that equal it
+    // in order of position: everything above `prefix`, and the first `need` that equal it; through shared memory, as
+    // neighbours in the list come from threads far apart (written straight to it they took 5 us)
+    uint32_t* stage = &counts.hist[0][0];
+    constexpr uint32_t kStage = sizeof(Counts) / 4;
     for (int c = 0; c < chunks; ++c) {
         if (chunks > 1) {
             load(c);
             before = block_scan(tally(), sm, total);
         }
-        const uint32_t a = above + (before & 0xffffu), q = equal + (before >> 16);
-        uint32_t at = a + min(q, need);
-        const int j0 = begin + c * kChunk + kKeys * static_cast<int>(threadIdx.x);
-        uint32_t left = need - min(q, need);  // how many of the thread's equal ones stay
-        while (left < static_cast<uint32_t>(__popc(is_equal))) is_equal &= ~(1u << (31 - __clz(is_equal)));
-        // (no more than n: weights that another stream changes meanwhile are counted twice and need not agree)
-        for (uint32_t stays = is_above | is_equal; stays && at < static_cast<uint32_t>(s.n); stays &= stays - 1u, ++at) kept[at] = j0 + __ffs(stays) - 1;
+        const uint32_t a = above + (before & 0xffffu), q = equal + (before >> 16), from = above + min(equal, need);
         above += total & 0xffffu;
         equal += total >> 16;
+        const uint32_t stays_here = above + min(equal, need) - from;
+        uint32_t at = a + min(q, need) - from;
+        const int j0 = begin + c * kChunk + kKeys * static_cast<int>(threadIdx.x);
+        const uint32_t left = need - min(q, need);  // how many of the thread's equal ones stay
+        while (left < static_cast<uint32_t>(__popc(is_equal))) is_equal &= ~(1u << (31 - __clz(is_equal)));
+        uint32_t stays = is_above | is_equal;
+        // (no more than n: weights that another stream changes meanwhile are counted twice and need not agree)
+        if (stays_here <= kStage) {
+            for (; stays && at < kStage; stays &= stays - 1u, ++at) stage[at] = j0 + __ffs(stays) - 1;
+            __syncthreads();
+            for (uint32_t i = threadIdx.x; i < stays_here && from + i < static_cast<uint32_t>(s.n); i += kSelThreads) kept[from + i] = stage[i];
+            __syncthreads();
+        } else {
+            for (; stays && from + at < static_cast<uint32_t>(s.n); stays &= stays - 1u, ++at) kept[from + at] = j0 + __ffs(stays) - 1;
+        }
     }
     if (ranks > 1) cluster.barrier_wait();
 }
@@ -269,12 +307,13 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
 constexpr int kMoveThreads = 256;
 constexpr int kMoveUnroll = 8;
 
-// One tensor's rows of a sequence and head, PIECES pieces of type T a row: round by round, the cluster's blocks side by side.
-template <class T, int PIECES>
-__device__ __forceinline__ void move_rows(const EvictParams& p, const int* kept, int b, int h, int n, T* x, long long ps,
+// One tensor's rows of a sequence and head, PIECES pieces of type T a row, of which this block moves those from `slice` of
+// SLICES on: round by round, the cluster's blocks side by side.
+template <class T, int PIECES, int SLICES>
+__device__ __forceinline__ void move_rows(const EvictParams& p, const int* kept, int b, int h, int n, T* x, long long ps, int slice,
                                           const cg::cluster_group& cluster) {
-    constexpr int kRows = kMoveThreads / PIECES, kTile = kRows * kMoveUnroll;
-    const int piece = threadIdx.x % PIECES, r0 = threadIdx.x / PIECES;
+    constexpr int kLanes = PIECES / SLICES, kRows = kMoveThreads / kLanes, kTile = kRows * kMoveUnroll;
+    const int piece = slice * kLanes + threadIdx.x % kLanes, r0 = threadIdx.x / kLanes;
     const int round = kTile * static_cast<int>(cluster.num_blocks()), mine = kTile * static_cast<int>(cluster.block_rank()) + r0;
     T now[kMoveUnroll], next[kMoveUnroll];
     T* to_now[kMoveUnroll];
@@ -316,25 +355,25 @@ __device__ __forceinline__ void move_rows(const EvictParams& p, const int* kept,
     }
 }
 
-template <int D, bool E4M3>
+// blockIdx.y: slices of K, then of V, then the weights and scales.
+template <int D, bool E4M3, int SLICES>
 __global__ void __launch_bounds__(kMoveThreads, 2) evict_move_kernel(const __grid_constant__ EvictParams p) {
-    constexpr int kPieces = D * (E4M3 ? 1 : 2) / 16;
+    constexpr int es = E4M3 ? 1 : 2, kPieces = D * es / 16;
     const cg::cluster_group cluster = cg::this_cluster();
     const int head = blockIdx.x / cluster.num_blocks(), b = head / p.kv.hkv, h = head - b * p.kv.hkv;
     wait_primary();
     // (len_out may be kv's own lengths: what this block takes from them is the same before and after)
-    const int n = sequence(p, b).n;
+    const int n = sequence(p, b).n, y = blockIdx.y;
     const int* kept = p.kept + static_cast<long long>(head) * p.max_keep;
-    constexpr int es = E4M3 ? 1 : 2;
-    if (blockIdx.y == 0) {
-        move_rows<uint4, kPieces>(p, kept, b, h, n, static_cast<uint4*>(p.kv.k), p.kv.k_ps * es / 16, cluster);
-    } else if (blockIdx.y == 1) {
-        move_rows<uint4, kPieces>(p, kept, b, h, n, static_cast<uint4*>(p.kv.v), p.kv.v_ps * es / 16, cluster);
+    if (y < SLICES) {
+        move_rows<uint4, kPieces, SLICES>(p, kept, b, h, n, static_cast<uint4*>(p.kv.k), p.kv.k_ps * es / 16, y, cluster);
+    } else if (y < 2 * SLICES) {
+        move_rows<uint4, kPieces, SLICES>(p, kept, b, h, n, static_cast<uint4*>(p.kv.v), p.kv.v_ps * es / 16, y - SLICES, cluster);
     } else {
-        move_rows<float, 1>(p, kept, b, h, n, p.w, p.w_ps, cluster);
+        move_rows<float, 1, 1>(p, kept, b, h, n, p.w, p.w_ps, 0, cluster);
         if (E4M3) {
-            move_rows<float, 1>(p, kept, b, h, n, p.kv.k_scale, p.kv.ks_ps, cluster);
-            move_rows<float, 1>(p, kept, b, h, n, p.kv.v_scale, p.kv.vs_ps, cluster);
+            move_rows<float, 1, 1>(p, kept, b, h, n, p.kv.k_scale, p.kv.ks_ps, 0, cluster);
+            move_rows<float, 1, 1>(p, kept, b, h, n, p.kv.v_scale, p.kv.vs_ps, 0, cluster);
         }
         if (h == 0 && cluster.block_rank() == 0 && threadIdx.x == 0) p.len_out[b] = n;
     }
@@ -375,10 +414,21 @@ int launch_cache_evict(const EvictParams& p, int sms, cudaStream_t stream) {
     const int sel = cluster_of(heads, sms, most_len, 4096);
     if (launch_clusters(evict_select_kernel, dim3(static_cast<unsigned>(heads * sel)), kSelThreads, sel, false, stream, p) != cudaSuccess) return -4;
     const int mov = cluster_of(2 * heads, 4LL * sms, p.max_keep, 256);
-    const dim3 grid(static_cast<unsigned>(heads * mov), 3);
+    // few blocks: rows in two halves, each of which is packed by itself (8 heads of 128k in e4m3, 16k of them kept: __ us, __ whole)
+    const int slices = 2 * heads * mov <= sms ? 2 : 1;
+    const dim3 grid(static_cast<unsigned>(heads * mov), 2 * slices + 1);
     cudaError_t e;
-    if (p.kv.d == 128) e = p.kv.e4m3 ? launch_clusters(evict_move_kernel<128, true>, grid, kMoveThreads, mov, true, stream, p) : launch_clusters(evict_move_kernel<128, false>, grid, kMoveThreads, mov, true, stream, p);
-    else e = p.kv.e4m3 ? launch_clusters(evict_move_kernel<64, true>, grid, kMoveThreads, mov, true, stream, p) : launch_clusters(evict_move_kernel<64, false>, grid, kMoveThreads, mov, true, stream, p);
+#define RA_MOVE(D, E4M3)                                                                                                     \
+    e = slices == 2 ? launch_clusters(evict_move_kernel<D, E4M3, 2>, grid, kMoveThreads, mov, true, stream, p)                \
+                    : launch_clusters(evict_move_kernel<D, E4M3, 1>, grid, kMoveThreads, mov, true, stream, p)
+    if (p.kv.d == 128) {
+        if (p.kv.e4m3) RA_MOVE(128, true);
+        else RA_MOVE(128, false);
+    } else {
+        if (p.kv.e4m3) RA_MOVE(64, true);
+        else RA_MOVE(64, false);
+    }
+#undef RA_MOVE
     return e == cudaSuccess ? 0 : -4;
 }
 

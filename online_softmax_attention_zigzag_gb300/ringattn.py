@@ -587,13 +587,21 @@ _pack_qk_norm = struct.Struct("4P8i2f").pack
 def _qk_rows(q, k, names, shapes, dtypes, dev: int):
     """ra_qk_rows as bytes; q and k of the shapes given, both of one of the types."""
     dt = q.dtype
-    if dt not in dtypes:
-        raise ValueError(f"{names[0]} must be {' or '.join(str(x) for x in dtypes)}, got {dt}")
-    qp, q0, q1 = _rows(q, names[0], dt, dev)
-    kp, k0, k1 = _rows(k, names[1], dt, dev)
-    if q.shape != shapes[0] or k.shape != shapes[1]:
-        raise ValueError(f"{names[0]} must be {list(shapes[0])} and {names[1]} {list(shapes[1])}")
-    return _pack_qk_rows(qp, kp, q0, q1, k0, k1, dt is torch.float32)
+    sq, sk = shapes
+    q0, q1, q2 = q.stride() if q.shape == sq else (0, 0, 0)
+    k0, k1, k2 = k.stride() if k.shape == sk else (0, 0, 0)
+    if q2 != 1 or k2 != 1 or dt not in dtypes or k.dtype is not dt or q.get_device() != dev or k.get_device() != dev:
+        if dt not in dtypes:
+            raise ValueError(f"{names[0]} must be {' or '.join(str(x) for x in dtypes)}, got {dt}")
+        _rows(q, names[0], dt, dev)
+        _rows(k, names[1], dt, dev)
+        raise ValueError(f"{names[0]} must be {list(sq)} and {names[1]} {list(sk)}")
+    # (the stride of an axis of one entry means nothing)
+    n, hq, d = sq
+    hk = sk[1]
+    if n == 1:
+        q0, k0 = hq * d, hk * d
+    return _pack_qk_rows(q.data_ptr(), k.data_ptr(), q0, q1 if hq > 1 else d, k0, k1 if hk > 1 else d, dt is torch.float32)
 
 
 _BF16 = (torch.bfloat16,)
@@ -601,29 +609,34 @@ _BF16_F32 = (torch.bfloat16, torch.float32)
 
 
 def _qk_norm(q, k, position, cos_sin, q_weight, k_weight, eps, q_scale, interleaved, dev: int):
-    """(shapes of q and k, ra_qk_norm as bytes)."""
-    if q.dim() != 3 or k.dim() != 3 or q.shape[0] != k.shape[0] or q.shape[2] != k.shape[2]:
+    """((q's shape, k's shape), ra_qk_norm as bytes)."""
+    sq, sk, st = q.shape, k.shape, cos_sin.shape
+    if len(sq) != 3 or len(sk) != 3 or sq[0] != sk[0] or sq[2] != sk[2]:
         raise ValueError("q must be [total, Hq, d] and k [total, Hkv, d]")
-    total, hq, d = q.shape
+    total, hq, d = sq
     f32 = torch.float32
-    wp, wt = [0, 0], None
-    for i, w in enumerate((q_weight, k_weight)):
+    wq = wk = 0
+    wt = None
+    for w in (q_weight, k_weight):
         if w is None:
             continue
         if wt is None:
             wt = w.dtype
         if w.dtype is not wt or wt not in _BF16_F32 or w.get_device() != dev or w.shape != (d,) or not w.is_contiguous():
             raise ValueError("q_weight and k_weight must be [d] on the current device, contiguous, both bf16 or both fp32")
-        wp[i] = w.data_ptr()
-    if position.get_device() != dev or position.dtype is not torch.int32 or position.shape != (total,) or not position.is_contiguous():
+        if w is q_weight:
+            wq = w.data_ptr()
+        if w is k_weight:
+            wk = w.data_ptr()
+    if position.dtype is not torch.int32 or position.get_device() != dev or position.shape != (total,) or not position.is_contiguous():
         raise ValueError("position must be a contiguous int32 [total] tensor on the current device")
-    if cos_sin.get_device() != dev or cos_sin.dtype is not f32 or cos_sin.dim() != 2 or not cos_sin.is_contiguous():
+    if cos_sin.dtype is not f32 or cos_sin.get_device() != dev or len(st) != 2 or not cos_sin.is_contiguous():
         raise ValueError("cos_sin must be a contiguous fp32 [n_pos, rot] tensor on the current device")
-    n_pos, rot = cos_sin.shape
+    n_pos, rot = st
     if n_pos >= 2 ** 31:
         raise ValueError("cos_sin must have fewer than 2^31 rows")
-    return (q.shape, k.shape), _pack_qk_norm(wp[0], wp[1], cos_sin.data_ptr(), position.data_ptr(), total, hq, k.shape[1], d, rot,
-                                             n_pos, wt is f32, interleaved, eps, q_scale)
+    return (sq, sk), _pack_qk_norm(wq, wk, cos_sin.data_ptr(), position.data_ptr(), total, hq, sk[1], d, rot, n_pos, wt is f32,
+                                   interleaved, eps, q_scale)
 
 
 def qk_norm_rope(q, k, q_out, k_out, position, cos_sin, *, q_weight=None, k_weight=None, eps=1e-6, q_scale=1.0, interleaved=0,
