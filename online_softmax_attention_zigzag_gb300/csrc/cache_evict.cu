@@ -355,6 +355,48 @@ __device__ __forceinline__ void move_rows(const EvictParams& p, const int* kept,
     }
 }
 
+// The same for N tensors of one number a row, whose places are looked up once.
+struct Numbers {
+    float* x;
+    long long ps;
+};
+template <int N>
+__device__ __forceinline__ void move_numbers(const EvictParams& p, const int* kept, int b, int h, int n, const Numbers (&x)[N],
+                                             const cg::cluster_group& cluster) {
+    constexpr int kUnroll = N > 1 ? 4 : 8, kTile = kMoveThreads * kUnroll;
+    const int round = kTile * static_cast<int>(cluster.num_blocks()), mine = kTile * static_cast<int>(cluster.block_rank()) + static_cast<int>(threadIdx.x);
+    for (long long base = 0; base < n; base += round) {
+        float v[N][kUnroll];
+        float* to[N][kUnroll];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            const long long i = base + mine + u * kMoveThreads;
+            const int j = i < n ? __ldcg(kept + i) : -1;
+            int row, from_row;
+            int dst = -1, src = -1;
+            if (j >= 0 && j != static_cast<int>(i) && RA_CHECKED(j > i && j < p.kv.max_pages * p.kv.page, p.err, kSiteEvictKept)) {
+                dst = paged_page(p.kv, b, static_cast<int>(i), row);
+                src = paged_page(p.kv, b, j, from_row);
+                if (dst >= 0 && !RA_CHECKED(paged_place_ok(p.kv, dst, h, row), p.err, kSiteEvictPlace)) dst = -1;
+                if (src >= 0 && !RA_CHECKED(paged_place_ok(p.kv, src, h, from_row), p.err, kSiteEvictPlace)) src = -1;
+            }
+#pragma unroll
+            for (int k = 0; k < N; ++k) {
+                v[k][u] = src >= 0 ? x[k].x[src * x[k].ps + static_cast<long long>(h) * p.kv.page + from_row] : 0.f;
+                to[k][u] = dst >= 0 ? x[k].x + dst * x[k].ps + static_cast<long long>(h) * p.kv.page + row : nullptr;
+            }
+        }
+        if (cluster.num_blocks() > 1) cluster.sync();
+        else __syncthreads();
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u)
+                if (to[k][u]) *to[k][u] = v[k][u];
+        // (what is written now lies before what the next round reads)
+    }
+}
+
 // blockIdx.y: slices of K, then of V, then the weights and scales.
 template <int D, bool E4M3, int SLICES>
 __global__ void __launch_bounds__(kMoveThreads, 2) evict_move_kernel(const __grid_constant__ EvictParams p) {
@@ -370,10 +412,12 @@ __global__ void __launch_bounds__(kMoveThreads, 2) evict_move_kernel(const __gri
     } else if (y < 2 * SLICES) {
         move_rows<uint4, kPieces, SLICES>(p, kept, b, h, n, static_cast<uint4*>(p.kv.v), p.kv.v_ps * es / 16, y - SLICES, cluster);
     } else {
-        move_rows<float, 1, 1>(p, kept, b, h, n, p.w, p.w_ps, 0, cluster);
-        if (E4M3) {
-            move_rows<float, 1, 1>(p, kept, b, h, n, p.kv.k_scale, p.kv.ks_ps, 0, cluster);
-            move_rows<float, 1, 1>(p, kept, b, h, n, p.kv.v_scale, p.kv.vs_ps, 0, cluster);
+        if constexpr (E4M3) {
+            const Numbers x[3] = {{p.w, p.w_ps}, {p.kv.k_scale, p.kv.ks_ps}, {p.kv.v_scale, p.kv.vs_ps}};
+            move_numbers<3>(p, kept, b, h, n, x, cluster);
+        } else {
+            const Numbers x[1] = {{p.w, p.w_ps}};
+            move_numbers<1>(p, kept, b, h, n, x, cluster);
         }
         if (h == 0 && cluster.block_rank() == 0 && threadIdx.x == 0) p.len_out[b] = n;
     }
