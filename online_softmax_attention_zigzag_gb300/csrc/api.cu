@@ -1027,7 +1027,7 @@ int ringattn_cache_weights(const void* q, long long q_token_stride, long long q_
     p.timeout_ns = wait_timeout_ns();
     p.err = dev->err;
     cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-    if (static_cast<long long>(p.max_q) * p.g <= ra::kWeightsFewRows) return ra::launch_cache_weights_few(p, dev->sms, cs);
+    if (ra::weights_few(static_cast<long long>(p.max_q) * p.g, p.kv.d, p.kv.e4m3)) return ra::launch_cache_weights_few(p, dev->sms, cs);
     while ((2 << p.unit_log) * p.g <= 128) ++p.unit_log;
     p.unit_tokens = 1 << p.unit_log;
     p.box_rows = std::gcd(p.kv.page, ra::kPagedTile);

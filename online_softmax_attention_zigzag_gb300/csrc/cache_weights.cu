@@ -99,6 +99,25 @@ __device__ __forceinline__ void codes_f16(uint32_t codes, uint32_t& a, uint32_t&
     b = e4m3x2_f16x2(codes >> 16);
 }
 
+// Positions that nobody sees: half a warp 16 of them.  other: their groups, summed up over the sequences.
+__device__ void fade_others(const WeightsParams& p, const long long* other, long long warp, long long warps) {
+    const PagedKV& kv = p.kv;
+    const int lane = threadIdx.x % 32;
+    const long long others = other[kv.batch];
+    for (long long o = (others * warp / warps) + lane / 16; o < others * (warp + 1) / warps; o += 2) {
+        const int b = find_sequence(other, kv.batch, o);
+        const Seen r = look<kWeightsGroup>(p, b);
+        const int each = other_groups(r);
+        const int h = static_cast<int>((o - other[b]) / each), u = static_cast<int>((o - other[b]) - static_cast<long long>(h) * each);
+        const int j0 = other_group(r, u) * kWeightsGroup, j = j0 + lane % 16;
+        int row;
+        const int pg = paged_page(kv, b, j0, row);
+        if (pg < 0 || j >= r.s.L || !RA_CHECKED(paged_place_ok(kv, pg, h, row, kWeightsGroup), p.err, kSiteWeightsPlace)) continue;
+        float* wp = p.w + pg * p.w_ps + static_cast<long long>(h) * kv.page + row + lane % 16;
+        *wp = faded(p, r, j, wp);
+    }
+}
+
 // A group of 16 keys: a lane's pieces of rows lane / 4 and lane / 4 + 8, their scales, weights and where those are.
 template <int D, bool E4M3>
 struct Keys {
@@ -244,38 +263,139 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<E4M3>()) weights_kerne
         }
     }
 
-    // positions that nobody sees: half a warp 16 of them
-    const long long others = other[kv.batch];
-    for (long long o = (others * warp / warps) + lane / 16; o < others * (warp + 1) / warps; o += 2) {
-        const int b = find_sequence(other, kv.batch, o);
-        const Seen r = look<kWeightsGroup>(p, b);
-        const int each = other_groups(r);
-        const int h = static_cast<int>((o - other[b]) / each), u = static_cast<int>((o - other[b]) - static_cast<long long>(h) * each);
-        const int j0 = other_group(r, u) * kWeightsGroup, j = j0 + lane % 16;
-        int row;
-        const int pg = paged_page(kv, b, j0, row);
-        if (pg < 0 || j >= r.s.L || !RA_CHECKED(paged_place_ok(kv, pg, h, row, kWeightsGroup), p.err, kSiteWeightsPlace)) continue;
-        float* wp = p.w + pg * p.w_ps + static_cast<long long>(h) * kv.page + row + lane % 16;
-        *wp = faded(p, r, j, wp);
-    }
+    fade_others(p, other, warp, warps);
 }
 
-template <int D, bool E4M3, int NB>
-int go(const WeightsParams& p, int sms, cudaStream_t stream) {
-    static std::atomic<unsigned long long> done{0};
-    const auto kernel = weights_kernel<D, E4M3, NB>;
+// More rows of a sequence and KV head, up to kWeightsWideRows: too many for registers.  A block takes a stretch of groups, its
+// warps every eighth, with q's fragments in shared memory as the lanes take them (16 bytes a lane, no conflicts), and so is what a
+// column's scores are compared with.  K is read once whatever the rows are, in e4m3 turned into fp16 once.
+constexpr int kWideBlocks = 3;  // an SM (two: 32 rows of bf16 156 us for 134, 64 rows of e4m3 156 for 140)
+
+struct WideColumn {
+    float bias, mul;
+    int end, from;
+};
+
+template <int D, bool E4M3>
+__global__ void __launch_bounds__(kThreads, kWideBlocks) weights_wide_kernel(const __grid_constant__ WeightsParams p) {
+    constexpr int kSteps = D / 32;  // pairs of steps of 16
+    extern __shared__ long long sums[];
+    __shared__ uint4 qs[kWeightsWideRows / 8][kSteps][32];
+    __shared__ WideColumn cs[kWeightsWideRows];
+    const PagedKV& kv = p.kv;
+    long long* seen = sums;
+    long long* other = sums + kv.batch + 1;
+    sum_up<kThreads>(kv.batch, seen, other, [&](int b, long long& x, long long& y) {
+        const Seen r = look<kWeightsGroup>(p, b);
+        x = static_cast<long long>(seen_groups(r)) * kv.hkv;
+        y = static_cast<long long>(other_groups(r)) * kv.hkv;
+    });
+    const int lane = threadIdx.x % 32, quad = lane / 4, warp = threadIdx.x / 32;
+    const long long n = seen[kv.batch];
+    long long i = n * blockIdx.x / gridDim.x;
+    const long long i_end = n * (blockIdx.x + 1) / gridDim.x;
+    while (i < i_end) {
+        const int b = find_sequence(seen, kv.batch, i);
+        const Seen r = look<kWeightsGroup>(p, b);
+        const int each = seen_groups(r);
+        const int h = static_cast<int>((i - seen[b]) / each);
+        const int u0 = static_cast<int>((i - seen[b]) - static_cast<long long>(h) * each);
+        const int u_end = static_cast<int>(min(static_cast<long long>(each), u0 + (i_end - i)));
+        i += u_end - u0;
+        const int blocks = (r.T * p.g + 7) / 8;  // of 8 columns
+        __syncthreads();  // everybody is done with the columns before
+        for (int c = warp; c < blocks; c += kWarps) {
+            uint32_t f[D / 8];
+            const float undo = load_q<D, E4M3>(p, r, h, 8 * c + quad, f);
+#pragma unroll
+            for (int s = 0; s < kSteps; ++s) qs[c][s][lane] = make_uint4(f[4 * s], f[4 * s + 1], f[4 * s + 2], f[4 * s + 3]);
+            if (lane % 4 == 0) {
+                const Column x = column(p, r, h, 8 * c + quad);
+                cs[8 * c + quad] = WideColumn{x.bias, E4M3 ? x.mul * undo : x.mul, x.end, x.from};
+            }
+        }
+        __syncthreads();
+        for (int u = u0 + warp; u < u_end; u += kWarps) {
+            const int j0 = (u < r.sink_end ? u : u - r.sink_end + r.lo) * kWeightsGroup;
+            int row;
+            const int pg = paged_page(kv, b, j0, row);
+            if (pg < 0 || !RA_CHECKED(paged_place_ok(kv, pg, h, row, kWeightsGroup), p.err, kSiteWeightsPlace)) continue;
+            const long long place = static_cast<long long>(h) * kv.page + row + quad;
+            float* wp = p.w + pg * p.w_ps + place;
+            uint4 k[2][kSteps];
+            float mul[2], old[2], sum[2] = {0.f, 0.f};
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                const char* at = static_cast<const char*>(kv.k) + (pg * kv.k_ps + (place + 8 * m) * D) * (E4M3 ? 1 : 2) + 16 * (lane % 4);
+                if (E4M3) {
+#pragma unroll
+                    for (int s = 0; s < kSteps / 2; ++s) {
+                        const uint4 x = ldg128_stream(at + 64 * s);
+                        codes_f16(x.x, k[m][2 * s].x, k[m][2 * s].y);
+                        codes_f16(x.y, k[m][2 * s].z, k[m][2 * s].w);
+                        codes_f16(x.z, k[m][2 * s + 1].x, k[m][2 * s + 1].y);
+                        codes_f16(x.w, k[m][2 * s + 1].z, k[m][2 * s + 1].w);
+                    }
+                } else {
+#pragma unroll
+                    for (int s = 0; s < kSteps; ++s) k[m][s] = ldg128_stream(at + 64 * s);
+                }
+                mul[m] = E4M3 ? __ldg(kv.k_scale + pg * kv.ks_ps + place + 8 * m) : 1.f;
+                old[m] = faded(p, r, j0 + quad + 8 * m, wp + 8 * m);
+            }
+            const bool whole = (p.causal ? j0 + kWeightsGroup <= r.s.base + 1 : j0 + kWeightsGroup <= r.s.L) &&
+                               (p.window <= 0 || j0 + kWeightsGroup <= p.sinks || j0 > r.s.base + r.T - 1 - p.window);
+#pragma unroll 2
+            for (int c = 0; c < blocks; ++c) {
+                float x[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int s = 0; s < kSteps; ++s) {
+                    const uint4 q = qs[c][s][lane];
+                    const uint32_t a0[4] = {k[0][s].x, k[1][s].x, k[0][s].y, k[1][s].y}, a1[4] = {k[0][s].z, k[1][s].z, k[0][s].w, k[1][s].w};
+                    mma16816<E4M3>(x, a0, q.x, q.y);
+                    mma16816<E4M3>(x, a1, q.z, q.w);
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const WideColumn& y = cs[8 * c + 2 * (lane % 4) + e % 2];
+                    bool on = y.bias != INFINITY;
+                    if (!whole) {
+                        const int j = j0 + quad + 8 * (e / 2);
+                        on = on && j < y.end && (j >= y.from || j < p.sinks);
+                    }
+                    const float pr = ex2(fmaf(x[e], E4M3 ? mul[e / 2] * y.mul : kLog2e, -y.bias));
+                    sum[e / 2] += on ? pr : 0.f;
+                }
+            }
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                sum[m] += __shfl_xor_sync(0xffffffffu, sum[m], 1);
+                sum[m] += __shfl_xor_sync(0xffffffffu, sum[m], 2);
+                if (lane % 4 == 0 && j0 + quad + 8 * m < r.s.L) wp[8 * m] = old[m] + sum[m];
+            }
+        }
+    }
+    fade_others(p, other, blockIdx.x * static_cast<long long>(kWarps) + warp, gridDim.x * static_cast<long long>(kWarps));
+}
+
+template <class K>
+int go(K kernel, std::atomic<unsigned long long>& done, const WeightsParams& p, int blocks, cudaStream_t stream) {
     // (sums of up to RINGATTN_PAGED_MAX_BATCH sequences)
     if (!once_a_device(done, [&] {
             return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 16 * (kPagedMaxBatch + 1)) == cudaSuccess;
         }))
         return -4;
-    kernel<<<blocks_per_sm<E4M3>() * sms, kThreads, 16 * (p.kv.batch + 1), stream>>>(p);
+    kernel<<<blocks, kThreads, 16 * (p.kv.batch + 1), stream>>>(p);
     return cudaGetLastError() == cudaSuccess ? 0 : -4;
 }
 
 template <int D, bool E4M3>
 int go_cols(const WeightsParams& p, int sms, cudaStream_t stream) {
-    return p.max_q * p.g <= 8 ? go<D, E4M3, 1>(p, sms, stream) : go<D, E4M3, 2>(p, sms, stream);
+    static std::atomic<unsigned long long> done[3];
+    const int cols = p.max_q * p.g, blocks = blocks_per_sm<E4M3>() * sms;
+    if (cols <= 8) return go(weights_kernel<D, E4M3, 1>, done[0], p, blocks, stream);
+    if (cols <= 16) return go(weights_kernel<D, E4M3, 2>, done[1], p, blocks, stream);
+    return go(weights_wide_kernel<D, E4M3>, done[2], p, kWideBlocks * sms, stream);
 }
 
 }  // namespace

@@ -61,13 +61,19 @@ struct EvictParams {
     int* err;
 };
 
-// few rows: at most kWeightsFewRows rows of a sequence and KV head
+// weights_few
 int launch_cache_weights_few(const WeightsParams& p, int sms, cudaStream_t stream);
 // any number, g <= 128; maps of K's pool and of q in boxes of a unit's tokens
 int launch_cache_weights_chunk(const WeightsParams& p, const CUtensorMap& tk, const CUtensorMap& tq, int shares, cudaStream_t stream);
 int launch_cache_evict(const EvictParams& p, int sms, cudaStream_t stream);
 
-constexpr int kWeightsFewRows = 16;
+// Most rows of a sequence and KV head that the kernels on mma.sync take.  What they do grows with the rows, while the chunk
+// kernel does a tile of 128 keys at the cost of 128 rows; in bf16 both wait for K's bytes for long, in e4m3 the chunk kernel waits
+// for its four warps that expand codes.  16 sequences of 1k to 32k keys, 8 KV heads, us with these and with the chunk kernel:
+//   bf16, d = 128: 24 rows 104, 151; 32 rows 134, 156.  d = 64: 24 rows 75, 140; 60 rows 136, 163
+//   e4m3, d = 128: 24 rows 107, 513; 64 rows 140, 376; 128 rows 300, 483.  d = 64: 24 rows 71, 229; 60 rows 97, 193
+constexpr int kWeightsWideRows = 128;
+inline bool weights_few(long long rows, int d, bool e4m3) { return rows <= (e4m3 ? kWeightsWideRows : 4096 / d); }
 
 #ifdef __CUDACC__
 constexpr float kWeightsLog2e = 1.4426950408889634f;
