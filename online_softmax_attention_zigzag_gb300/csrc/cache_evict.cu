@@ -27,6 +27,7 @@ constexpr int kKeys = 16;  // neighbouring positions of a thread, all on one pag
 constexpr int kChunk = kKeys * kSelThreads;
 constexpr int kDigit = 11;  // bits; 32 = 11 + 11 + 10
 constexpr int kBins = 1 << kDigit;
+constexpr int kDirect = 512;  // and up to which they are ranked one against the other
 constexpr int kList = 5119;  // keys with the first digit in question that a block lists
 
 __device__ __forceinline__ uint32_t order(float w) {
@@ -170,6 +171,24 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
             }
             __syncthreads();
             use_list = listed <= kList;
+            if (ranks == 1 && listed <= kDirect) {
+                // so few that each is ranked against all: a warp one after the other (two digits more would take 4 us)
+                for (uint32_t i = warp; i < listed; i += kSelWarps) {
+                    const uint32_t mine = list[i];
+                    uint32_t both = 0;  // above in the low half, equal in the high one
+                    for (uint32_t j = lane; j < listed; j += 32) both += list[j] > mine ? 1u : list[j] == mine ? 0x10000u : 0u;
+                    both = __reduce_add_sync(0xffffffffu, both);
+                    const uint32_t more = both & 0xffffu, as_much = both >> 16;
+                    if (more < need && need <= more + as_much && lane == 0) {  // (equal ones all write the same)
+                        stretch[0] = mine;
+                        stretch[1] = need - more;
+                    }
+                }
+                __syncthreads();
+                prefix = stretch[0];
+                need = stretch[1];
+                break;
+            }
         }
         if (use_list) {
             for (uint32_t i = threadIdx.x; i < listed; i += kSelThreads)
