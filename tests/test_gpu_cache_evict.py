@@ -181,6 +181,36 @@ def test_long_ones(ra, e4m3, L, keep):
         assert torch.equal(got, want)
 
 
+@pytest.mark.parametrize("L,keep,heads", [(17000, 900, 160), (40000, 20000, 1), (140000, 70001, 1), (30000, 1, 3), (5000, 4999, 200)])
+@pytest.mark.parametrize("kind", ["ties", "zeros", "near"])
+def test_long_ones_whose_weights_are_alike(ra, L, keep, heads, kind):
+    """More equal ones than a block lists, stretches of several parts, thousands of keys whose first digits agree."""
+    d, page = 64, 128
+    g = torch.Generator(device=dev()).manual_seed(L + keep)
+    pages = -(-L // page)
+    table = torch.randperm(pages, generator=g, device=dev()).to(torch.int32)[None]
+    k, v = (torch.zeros((pages, heads, page, d), device=dev(), dtype=torch.uint8).view(torch.float8_e4m3fn) for _ in range(2))
+    sc = [torch.rand((pages, heads, page), generator=g, device=dev()) for _ in range(2)]
+    w = torch.rand((pages, heads, page), generator=g, device=dev())
+    if kind == "ties":
+        w = (w * 4).floor()
+    elif kind == "zeros":
+        w = w * (w > 0.9)
+    else:
+        w = 1.0 + w * 1e-3
+    t = table[0].long()
+    x = w[t].transpose(0, 1).reshape(heads, -1)[:, :L]
+    order = torch.sort(x, dim=1, descending=True, stable=True)[1][:, :keep].sort(1)[0]
+    want = [s[t].transpose(0, 1).reshape(heads, -1)[:, :L].gather(1, order) for s in (w, *sc)]
+    ln, kp = (torch.tensor([y], dtype=torch.int32, device=dev()) for y in (L, keep))
+    kept = torch.empty((1, heads, keep), dtype=torch.int32, device=dev())
+    ra.cache_evict(k, v, w, table, ln, kp, ln, kept, k_scale=sc[0], v_scale=sc[1])
+    assert ra.sync_status() == ra.RA_OK
+    assert int(ln) == keep and torch.equal(kept[0].long(), order)
+    for s, y in zip((w, *sc), want):
+        assert torch.equal(s[t].transpose(0, 1).reshape(heads, -1)[:, :keep], y)
+
+
 def test_many_heads_and_sequences(ra):
     Run([(37 * b) % 90 for b in range(300)], [(11 * b) % 50 for b in range(300)], hkv=5, seed=10).check(ra, 1, 2)
 

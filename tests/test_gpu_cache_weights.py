@@ -274,6 +274,78 @@ def test_captured_and_on_another_stream(ra, n):
     assert ra.sync_status() == ra.RA_OK
 
 
+@pytest.mark.parametrize("n", [1, 2, 9, 40, 300])
+@pytest.mark.parametrize("g", [1, 3, 7, 9, 33, 100, 128])
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_query_heads_of_a_kv_head(ra, n, g, e4m3):
+    """Units of the chunk kernel that 128 rows do not fill, head-major q."""
+    r = Run([(n, n + 390), (1, 200), (n, n)], hq=2 * g, hkv=2, d=64, page=48, e4m3=e4m3, seed=g, decay=0.5)
+    q = r.q.transpose(0, 1).contiguous().to(dev()).transpose(0, 1)
+    r.call(ra, q=q)
+    assert ra.sync_status() == ra.RA_OK
+    r.check()
+
+
+@pytest.mark.parametrize("n", [1, 5, 40, 200])
+@pytest.mark.parametrize("batch", [40, 600])
+def test_batches_of_all_sizes(ra, n, batch):
+    """Sequences with and without rows, more of them than one part of shared memory holds."""
+    seqs = [(n if b % 7 == 0 else b % 3, (61 * b) % 300 + 1) for b in range(batch)]
+    seqs = [(min(a, L), L) for a, L in seqs]
+    r = Run(seqs, hq=4, hkv=1, d=64, page=16, seed=n, window=100, sinks=3, decay=0.5)
+    r.call(ra)
+    assert ra.sync_status() == ra.RA_OK
+    r.check()
+
+
+@pytest.mark.parametrize("n", [1, 7, 60, 200])
+@pytest.mark.parametrize("max_q", [1, 5, 33, 150])
+def test_rows_behind_max_q_do_not_count(ra, n, max_q):
+    seqs = [(n, 300), (min(n, 3), 100)]
+    r = Run(seqs, hq=8, hkv=2, d=64, seed=16, max_q=max_q)
+    lse = r.lse.clone()
+    for b in range(2):
+        r.lse[int(r.B.cu[b]) + max_q:int(r.B.cu[b + 1])] = -float("inf")
+    r.call(ra, lse=lse.to(dev()))
+    assert ra.sync_status() == ra.RA_OK
+    r.check()
+
+
+@pytest.mark.parametrize("n", [1, 6, 60, 200])
+def test_rows_of_zeros_and_of_very_different_sizes(ra, n):
+    """e4m3 scales from 2^-120 (rows of zeros) to 2^40; keys that some lse makes large weights of."""
+    r = Run([(n, 300)], hq=8, hkv=2, d=128, e4m3=True, seed=17, std=0.0)
+    k = r.B.k[0]
+    k[10:40] = 0.0
+    k[50:60] *= 2.0 ** -70
+    k[60:70] *= 2.0 ** 40
+    k[70] = 2.0 ** -133
+    r.B.fill()
+    r.q = (torch.randn(r.q.shape, generator=torch.Generator().manual_seed(18)) * 2.0 ** -40).to(torch.bfloat16)
+    r.lse = torch.randn(r.lse.shape, generator=torch.Generator().manual_seed(19)) * 5
+    r.call(ra)
+    assert ra.sync_status() == ra.RA_OK
+    r.check()
+
+
+@pytest.mark.parametrize("n", [1, 6, 60, 200])
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_lse_of_every_size(ra, n, e4m3):
+    """Far from the scores: weights of nothing and of infinity, as the definition has them in fp32."""
+    r = Run([(n, 300)], hq=8, hkv=2, d=64, e4m3=e4m3, seed=20)
+    for at, x in ((0, 1e4), (1, 1e9), (2, 3e38), (3, float("inf")), (4, 200.0)):
+        r.lse[:, at] = x  # heads of the first KV head and the first of the second add nothing
+    r.call(ra)
+    assert ra.sync_status() == ra.RA_OK
+    r.check()
+    r.w.copy_(r.before)
+    r.lse[:, 7] = -1e5
+    r.call(ra)
+    pg, row = r.B.places(0)
+    w = r.w[pg, :, row]
+    assert torch.isinf(w[:300 - n + 1, 1]).all() and not torch.isinf(w[:, 0]).any()
+
+
 def test_many_sequences(ra):
     """More of them than threads, as many as a call takes, most without rows."""
     seqs = [(1, 1 + (7 * b) % 40) if b % 5 == 0 else (0, 3) for b in range(4096)]
