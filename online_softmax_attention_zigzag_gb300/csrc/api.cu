@@ -803,7 +803,7 @@ int make_norm(const ra_qk_norm* a, ra::NormParams* p) {
 
 // Sums of the backward pass's blocks, on a GPU of at most kNormMaxSms.
 long long norm_workspace(int total, int groups, int d) {
-    const long long blocks = static_cast<long long>(groups) * ra::norm_blocks(total, groups, d, ra::kNormMaxSms * ra::kNormBlocksPerSm);
+    const long long blocks = static_cast<long long>(groups) * ra::norm_blocks(total, groups, d, ra::kNormMaxSms * ra::kNormBwdBlocksPerSm);
     return (std::max(blocks, 1LL) * d * 4 + 255) / 256 * 256;
 }
 
@@ -1031,8 +1031,7 @@ int ringattn_cache_weights(const void* q, long long q_token_stride, long long q_
     while ((2 << p.unit_log) * p.g <= 128) ++p.unit_log;
     p.unit_tokens = 1 << p.unit_log;
     p.box_rows = std::gcd(p.kv.page, ra::kPagedTile);
-    p.k_slots = p.max_q <= 2 * p.unit_tokens ? 4 : 3;
-    p.item_units = 8;
+    p.item_units = p.kv.e4m3 ? 8 : 3;
     CUtensorMap tk = {}, tq = {};
     if ((st = get_encoder()) != RA_OK || (st = encode_q(&tq, p)) != RA_OK) return st;
     if (!p.kv.e4m3 && (st = encode_pool(&tk, p.kv.k, p.kv.k_ps, p.kv, p.box_rows)) != RA_OK) return st;

@@ -43,7 +43,6 @@ struct WeightsParams {
     // chunk kernel: tokens of a unit of at most 128 query rows (a power of two, and its exponent), rows of a TMA box of
     // the pool, scratch
     int unit_tokens, unit_log, box_rows;
-    int k_slots;     // of the tiles in shared memory, those of K
     int item_units;  // what an item costs beside its units, in units
     WeightsSpace* space;
     unsigned long long timeout_ns;

@@ -29,7 +29,10 @@ namespace {
 constexpr int kTile = kPagedTile;
 constexpr int kSumWarps = 16, kMmaWarp = 16, kQWarp = 18, kKWarp = 19;
 constexpr int kHalf = kTile / 2;  // columns of a warp's share of a unit
-constexpr int kSlots = 6;     // tiles of K and of q in shared memory (WeightsParams says how many of each)
+// Tiles of K and of q in shared memory, six in all.  Four of K are an item ahead; a third of q gains nothing where items are
+// long (4096 rows of 32k: 1364 us either way), and two of K the less the shorter they are (16 x 32 rows of 1k to 32k keys: 136
+// us with four, 148 with three, 168 with two).
+constexpr uint32_t kKSlots = 4, kQSlots = 2, kSlots = kKSlots + kQSlots;
 constexpr int kAccs = 2, kItems = 4;  // (accumulators of each tile)
 constexpr int kBiasBytes = kTile * 32;  // a step of 16 of a product's operand
 constexpr int kTilesOff = kSlots * kBiasBytes;
@@ -57,7 +60,7 @@ __device__ __forceinline__ int tiles_of(int pair, int keys) { return pair * kWei
 
 struct Shared {
     uint64_t item_full[kItems], item_empty[kItems];
-    uint64_t k_full[kSlots], k_empty[kSlots], q_full[kSlots], q_empty[kSlots],
+    uint64_t k_full[kKSlots], k_empty[kKSlots], q_full[kQSlots], q_empty[kQSlots],
         acc_full[2][kAccs], acc_empty[2][kAccs], half_full[2], half_empty[2], drain[2];
     Item item[kItems];
     float half[2][kTile];  // what the second half of the columns gives a tile's keys
@@ -228,7 +231,7 @@ __device__ void q_role(const WeightsParams& p, const CUtensorMap* tq, uint32_t s
     const int lane = threadIdx.x % 32;
     const uint32_t bytes = static_cast<uint32_t>(p.unit_tokens * p.g) * 128u * C::kBoxes;
     const uint64_t keep = make_policy_evict_last();
-    const uint32_t q_slots = kSlots - p.k_slots, q_base = smem + kTilesOff + p.k_slots * C::kTileBytes, b_base = smem + p.k_slots * kBiasBytes;
+    const uint32_t q_base = smem + kTilesOff + kKSlots * C::kTileBytes, b_base = smem + kKSlots * kBiasBytes;
     uint32_t n = 0;
     Walk w = {};
     bool ok = true;
@@ -252,11 +255,11 @@ __device__ void q_role(const WeightsParams& p, const CUtensorMap* tq, uint32_t s
 #pragma unroll
             for (int k = 0; k < kAhead; ++k) {
                 if (ub + k >= w.u1) break;
-                ok = take(sh.q_empty, n, q_slots, wc);
+                ok = take(sh.q_empty, n, kQSlots, wc);
                 if (!ok) break;
                 const int t0 = (ub + k) << p.unit_log;
                 if (lane == 0) {
-                    const uint32_t s = n % q_slots;
+                    const uint32_t s = n % kQSlots;
                     mbar_arrive_expect_tx(&sh.q_full[s], bytes);
                     int tok = w.r.s.q0 + t0;
                     if (!RA_CHECKED(paged_row_ok(p.kv, p.hq, tok, w.h * p.g + p.g - 1), p.err, kSiteWeightsRow)) tok = 0;
@@ -267,16 +270,16 @@ __device__ void q_role(const WeightsParams& p, const CUtensorMap* tq, uint32_t s
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const float v = x[k][i] == -INFINITY ? -0x1p60f : -x[k][i];  // (a row whose lse is -inf adds nothing)
-                    store_q_bias(b_base + (n % q_slots) * kBiasBytes, lane + 32 * i, v < -0x1p60f ? -0x1p60f : v > 0x1p60f ? 0x1p60f : v);
+                    store_q_bias(b_base + (n % kQSlots) * kBiasBytes, lane + 32 * i, v < -0x1p60f ? -0x1p60f : v > 0x1p60f ? 0x1p60f : v);
                 }
                 fence_async_shared();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&sh.q_full[n % q_slots]);
+                if (lane == 0) mbar_arrive(&sh.q_full[n % kQSlots]);
                 ++n;
             }
         }
     }
-    if (!ok && lane == 0) drain_ring(sh.q_full, n, q_slots, wc);  // copies in flight land before the block ends
+    if (!ok && lane == 0) drain_ring(sh.q_full, n, kQSlots, wc);  // copies in flight land before the block ends
 }
 
 // Hands an item on to the warps that issue and add up (null: no more); one warp of the loaders.
@@ -305,7 +308,6 @@ __device__ void k_role(const WeightsParams& p, const CUtensorMap* tk, uint32_t s
     const PagedKV& kv = p.kv;
     const int lane = threadIdx.x % 32, rows = p.box_rows, boxes = kTile / rows;
     const uint64_t policy = make_policy_evict_first();
-    const uint32_t slots = p.k_slots;
     uint32_t n = 0, ni = 0;
     Walk w;
     bool more = walk_begin(p, sums, w), ok = true;
@@ -331,9 +333,9 @@ __device__ void k_role(const WeightsParams& p, const CUtensorMap* tk, uint32_t s
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
             if (k >= tiles || !ok) continue;
-            ok = take(sh.k_empty, n, slots, wc);
+            ok = take(sh.k_empty, n, kKSlots, wc);
             if (!ok) continue;
-            const uint32_t s = n % slots;
+            const uint32_t s = n % kKSlots;
             ++n;
             if (lane == 0) mbar_arrive_expect_tx(&sh.k_full[s], C::kTileBytes);
             __syncwarp();
@@ -343,7 +345,7 @@ __device__ void k_role(const WeightsParams& p, const CUtensorMap* tk, uint32_t s
         }
         more = walk_next(p, w);
     }
-    if (!ok && lane == 0) drain_ring(sh.k_full, n, slots, wc);
+    if (!ok && lane == 0) drain_ring(sh.k_full, n, kKSlots, wc);
 }
 
 // e4m3: four warps expand codes, a thread one 16-byte piece of D / 16 rows.  The codes of a tile are on their way while the tile
@@ -354,7 +356,6 @@ __device__ void expand_role(const WeightsParams& p, uint32_t smem, Shared& sh, c
     constexpr int kPieces = D / 16, kRows = 128 / kPieces, kLoads = kTile / kRows;
     const PagedKV& kv = p.kv;
     const int i0 = threadIdx.x - kKWarp * 32, piece = i0 % kPieces, r0 = i0 / kPieces;
-    const uint32_t slots = p.k_slots;
     uint32_t n = 0;
     Walk w = {};
     // the pages of a pair's 16 groups of 16 rows, a lane one of them: looked up once for all, an item ahead
@@ -385,9 +386,9 @@ __device__ void expand_role(const WeightsParams& p, uint32_t smem, Shared& sh, c
         }
     };
     auto expand = [&](const uint4 (&x)[kLoads], float scale) -> bool {
-        if (!take(sh.k_empty, n, slots, wc)) return false;
-        store_k_bias(smem + (n % slots) * kBiasBytes, i0, 1.f / scale);
-        const uint32_t stage = smem + kTilesOff + (n % slots) * C::kTileBytes + (piece / 4) * C::kBoxBytes;
+        if (!take(sh.k_empty, n, kKSlots, wc)) return false;
+        store_k_bias(smem + (n % kKSlots) * kBiasBytes, i0, 1.f / scale);
+        const uint32_t stage = smem + kTilesOff + (n % kKSlots) * C::kTileBytes + (piece / 4) * C::kBoxBytes;
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
             const int r = i * kRows + r0;
@@ -401,7 +402,7 @@ __device__ void expand_role(const WeightsParams& p, uint32_t smem, Shared& sh, c
             sts128(at + (((c + 1) ^ (r & 7)) << 4), y[4], y[5], y[6], y[7]);
         }
         fence_async_shared();
-        mbar_arrive(&sh.k_full[n % slots]);
+        mbar_arrive(&sh.k_full[n % kKSlots]);
         ++n;
         return true;
     };
@@ -478,35 +479,34 @@ __device__ __forceinline__ void issue_scores(uint32_t d_tmem, uint32_t k_base, u
 template <int D, bool E4M3>
 __device__ void mma_role(const WeightsParams& p, int tile, uint32_t smem, Shared& sh, uint32_t tmem, const WaitCtl& wc) {
     using C = Cfg<D, E4M3>;
-    const uint32_t k_slots = p.k_slots, q_slots = kSlots - k_slots, q_base = smem + kTilesOff + k_slots * C::kTileBytes,
-                   b_base = smem + k_slots * kBiasBytes;
+    const uint32_t q_base = smem + kTilesOff + kKSlots * C::kTileBytes, b_base = smem + kKSlots * kBiasBytes;
     uint32_t nk = 0, nq = 0, na = 0;
     const bool ok = take_items(sh, wc, [&](const volatile Item& it) -> bool {
         const int tiles = tiles_of(it.pair, it.keys), u1 = it.u1, T = it.T;
         const bool on = tile < tiles;
-        const uint32_t slot = (nk + tile) % k_slots;
+        const uint32_t slot = (nk + tile) % kKSlots;
         // (both tiles: an issuer that does not look at a slot's every round could take one for the next but one)
         for (int k = 0; k < tiles; ++k)
-            if (!mbar_wait_w(&sh.k_full[(nk + k) % k_slots], ((nk + k) / k_slots) & 1u, wc)) return false;
+            if (!mbar_wait_w(&sh.k_full[(nk + k) % kKSlots], ((nk + k) / kKSlots) & 1u, wc)) return false;
         nk += tiles;
         for (int u = it.u0; u < u1; ++u, ++nq) {
             const int cols = min(p.unit_tokens, T - (u << p.unit_log)) * p.g;
             const uint32_t idesc = idesc_bf16(kTile, 16, 0) + (static_cast<uint32_t>((cols - 1) / 16 * 2) << 17);  // N: cols, in sixteens
-            const uint32_t qs = nq % q_slots;
+            const uint32_t qs = nq % kQSlots;
             if (on) {
                 const uint32_t acc = na % kAccs;
-                if (!mbar_wait2_w(&sh.q_full[qs], (nq / q_slots) & 1u, &sh.acc_empty[tile][acc], ((na / kAccs) & 1u) ^ 1u, wc)) return false;
+                if (!mbar_wait2_w(&sh.q_full[qs], (nq / kQSlots) & 1u, &sh.acc_empty[tile][acc], ((na / kAccs) & 1u) ^ 1u, wc)) return false;
                 ++na;
                 tc_fence_after();
                 issue_scores<D>(tmem + (tile * kAccs + acc) * kTile, smem + kTilesOff + slot * C::kTileBytes, q_base + qs * C::kTileBytes,
                                 smem + (E4M3 ? slot * kBiasBytes : 0), b_base + qs * kBiasBytes, idesc);
                 mma_commit_e(&sh.acc_full[tile][acc]);
-            } else if (!mbar_wait_w(&sh.q_full[qs], (nq / q_slots) & 1u, wc)) {
+            } else if (!mbar_wait_w(&sh.q_full[qs], (nq / kQSlots) & 1u, wc)) {
                 return false;
             }
             mma_commit_e(&sh.q_empty[qs]);
         }
-        for (int k = 0; k < tiles; ++k) mma_commit_e(&sh.k_empty[(nk - tiles + k) % k_slots]);
+        for (int k = 0; k < tiles; ++k) mma_commit_e(&sh.k_empty[(nk - tiles + k) % kKSlots]);
         return true;
     });
     if (!ok) {  // every MMA that was issued must finish before TMEM is released
@@ -637,9 +637,11 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1) weights_chunk_kerne
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~static_cast<uintptr_t>(1023));
     const int warp = threadIdx.x / 32;
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kSlots; ++i) {
+        for (uint32_t i = 0; i < kKSlots; ++i) {
             mbar_init(&sh.k_full[i], E4M3 ? 128 : 1);
             mbar_init(&sh.k_empty[i], 2);
+        }
+        for (uint32_t i = 0; i < kQSlots; ++i) {
             mbar_init(&sh.q_full[i], 2);  // q, and -lse
             mbar_init(&sh.q_empty[i], 2);
         }
