@@ -15,7 +15,7 @@ enum WeightsCheckSite : int {
 
 constexpr int kWeightsGroup = 16;  // keys that a warp of the few-row kernel takes at a time, all on one page
 constexpr int kWeightsPair = 256;  // keys of an item of the chunk kernel: two tiles
-constexpr int kWeightsSumsShared = 256;  // batches up to this keep the chunk kernel's sums in shared memory
+constexpr int kWeightsSumsShared = 224;  // batches up to this keep the chunk kernel's sums in shared memory (what its tiles leave)
 
 // What a block of the chunk kernel leaves of an item whose query rows others have too.
 struct WeightsPartial {
@@ -68,11 +68,11 @@ int launch_cache_evict(const EvictParams& p, int sms, cudaStream_t stream);
 
 // Most rows of a sequence and KV head that the kernels on mma.sync take.  What they do grows with the rows, while the chunk
 // kernel does a tile of 128 keys at the cost of 128 rows; in bf16 both wait for K's bytes for long, in e4m3 the chunk kernel waits
-// for its four warps that expand codes.  16 sequences of 1k to 32k keys, 8 KV heads, us with these and with the chunk kernel:
-//   bf16, d = 128: 24 rows 104, 151; 32 rows 134, 156.  d = 64: 24 rows 75, 140; 60 rows 136, 163
-//   e4m3, d = 128: 24 rows 107, 513; 64 rows 140, 376; 128 rows 300, 483.  d = 64: 24 rows 71, 229; 60 rows 97, 193
-constexpr int kWeightsWideRows = 128;
-inline bool weights_few(long long rows, int d, bool e4m3) { return rows <= (e4m3 ? kWeightsWideRows : 4096 / d); }
+// for the warps that expand codes.  16 sequences of 1k to 32k keys, 8 KV heads, us with these and with the chunk kernel:
+//   bf16, d = 128: 24 rows 105, 109; 32 rows 134, 112.  d = 64: 24 rows 72, 90; 32 rows 74, 68
+//   e4m3, d = 128: 64 rows 141, 191; 80 rows 199, 293; 96 rows 198, 200; 128 rows 300, 255.  d = 64: 80 rows 144, 179; 96 rows 164, 146
+constexpr int kWeightsWideRows = 80;
+inline bool weights_few(long long rows, bool e4m3) { return rows <= (e4m3 ? kWeightsWideRows : 24); }
 
 #ifdef __CUDACC__
 constexpr float kWeightsLog2e = 1.4426950408889634f;
