@@ -9,6 +9,11 @@
 //
 // The i-th of the positions that stay is at i or behind it, and they move in order, so packing works in place: what a cluster
 // has read of a round of rows before it writes them, it does not need again, and the rows behind lie behind.
+//
+// 16 sequences of 4k to 16k positions, 8 KV heads, 2k kept, bf16: 65 us, 4.2 TB/s of what it has to read and write.  Selecting is a
+// chain of latencies (three digits and a list, each with two exchanges in the cluster); packing takes 50, as long as a plain
+// gather of such rows, 256 bytes one in eight.  One sequence of 128k in e4m3, 16k kept: 46 us, selecting 20, then rounds that
+// wait for the cluster.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
@@ -324,53 +329,87 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
 }
 
 constexpr int kMoveThreads = 256;
-constexpr int kMoveUnroll = 8;
+// Blocks of an SM, and rounds in shared memory.  The first case above and the second, us: 3 of 4 65, 46; 4 of 3 74, 46; 2 of 6 67, 55;
+// through registers, a round ahead, 109, 54.
+constexpr int kMoveBlocks = 3;
+constexpr int kMoveStages = 4;
+constexpr int kMoveUnroll = 4;  // pieces of 16 bytes of a thread and round, at most
 
-// One tensor's rows of a sequence and head, PIECES pieces of type T a row, of which this block moves those from `slice` of
-// SLICES on: round by round, the cluster's blocks side by side.
-template <class T, int PIECES, int SLICES>
-__device__ __forceinline__ void move_rows(const EvictParams& p, const int* kept, int b, int h, int n, T* x, long long ps, int slice,
-                                          const cg::cluster_group& cluster) {
-    constexpr int kLanes = PIECES / SLICES, kRows = kMoveThreads / kLanes, kTile = kRows * kMoveUnroll;
-    const int piece = slice * kLanes + threadIdx.x % kLanes, r0 = threadIdx.x / kLanes;
-    const int round = kTile * static_cast<int>(cluster.num_blocks()), mine = kTile * static_cast<int>(cluster.block_rank()) + r0;
-    T now[kMoveUnroll], next[kMoveUnroll];
-    T* to_now[kMoveUnroll];
-    T* to_next[kMoveUnroll];
-    auto load = [&](long long base, T (&v)[kMoveUnroll], T* (&to)[kMoveUnroll]) {
-        int j[kMoveUnroll];
-#pragma unroll
-        for (int u = 0; u < kMoveUnroll; ++u) {
-            const long long i = base + mine + u * kRows;
-            j[u] = i < n ? __ldcg(kept + i) : -1;
-        }
-#pragma unroll
-        for (int u = 0; u < kMoveUnroll; ++u) {
-            const int i = static_cast<int>(base) + mine + u * kRows;
-            to[u] = nullptr;
-            v[u] = T{};
-            if (j[u] < 0 || j[u] == i) continue;  // (none, or it stays where it is)
+struct MoveShared {
+    uint4 piece[kMoveStages][kMoveUnroll][kMoveThreads];
+    long long to[kMoveStages][kMoveThreads];  // where a round's rows go, a warp's 32 together; -1: nowhere
+};
+
+// One tensor's rows of a sequence and head, PIECES pieces of 16 bytes a row, of which this block moves those from `slice` of
+// SLICES on: round by round, the cluster's blocks side by side, a few rounds on their way to shared memory while one is written.  A
+// thread writes the pieces that it has loaded.  Where rows lie and go is found by a lane a row, for 32 of a warp's rows at once.
+template <int PIECES, int SLICES>
+__device__ __forceinline__ void move_rows(const EvictParams& p, const int* kept, int b, int h, int n, uint4* x, long long ps, int slice,
+                                          MoveShared& sh, const cg::cluster_group& cluster) {
+    constexpr int kLanes = PIECES / SLICES;    // of a row
+    constexpr int kRows = 32 / kLanes;         // of a warp and step
+    constexpr int kSteps = kLanes < 4 ? kLanes : kMoveUnroll;  // of a round
+    constexpr int kRound = kSteps * kRows, kRounds = 32 / kRound;  // of a warp's rows; of a look-up
+    static_assert(kRound * kRounds == 32, "32 rows a look-up");
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, piece = slice * kLanes + lane % kLanes;
+    const int block = kRound * kMoveThreads / 32, ranks = static_cast<int>(cluster.num_blocks());
+    const int mine = block * static_cast<int>(cluster.block_rank()) + warp * kRound;
+    const long long all = (static_cast<long long>(n) + static_cast<long long>(block) * ranks - 1) / (static_cast<long long>(block) * ranks);
+    const int rounds = static_cast<int>(all);
+    // the lane's row of the look-up that begins with round `r`
+    auto row_of = [&](int r) { return static_cast<long long>(r + lane / kRound) * block * ranks + mine + lane % kRound; };
+    auto kept_at = [&](int r) {
+        const long long i = row_of(r);
+        return i < n ? __ldcg(kept + i) : -1;
+    };
+    long long from = -1, to = -1;  // of this look-up's rows; from -1: zeros, to -1: nowhere
+    int j = kept_at(0);
+    auto look_up = [&](int r) {
+        const int i = static_cast<int>(row_of(r));
+        from = to = -1;
+        if (j >= 0 && j != i) {  // (it stays where it is)
             int row;
             int pg = paged_page(p.kv, b, i, row);
             if (pg >= 0 && RA_CHECKED(paged_place_ok(p.kv, pg, h, row), p.err, kSiteEvictPlace))
-                to[u] = x + pg * ps + (static_cast<long long>(h) * p.kv.page + row) * PIECES + piece;
-            if (!RA_CHECKED(j[u] > i && j[u] < p.kv.max_pages * p.kv.page, p.err, kSiteEvictKept)) continue;
-            pg = paged_page(p.kv, b, j[u], row);
-            if (pg >= 0 && RA_CHECKED(paged_place_ok(p.kv, pg, h, row), p.err, kSiteEvictPlace))
-                v[u] = x[pg * ps + (static_cast<long long>(h) * p.kv.page + row) * PIECES + piece];
+                to = pg * ps + (static_cast<long long>(h) * p.kv.page + row) * PIECES;
+            if (RA_CHECKED(j > i && j < p.kv.max_pages * p.kv.page, p.err, kSiteEvictKept)) {
+                pg = paged_page(p.kv, b, j, row);
+                if (pg >= 0 && RA_CHECKED(paged_place_ok(p.kv, pg, h, row), p.err, kSiteEvictPlace))
+                    from = pg * ps + (static_cast<long long>(h) * p.kv.page + row) * PIECES;
+            }
         }
+        j = kept_at(r + kRounds);
     };
-    load(0, now, to_now);
-    for (long long base = 0; base < n; base += round) {
-        load(base + round, next, to_next);
-        if (cluster.num_blocks() > 1) cluster.sync();  // everything up to the next round has been read
-        else __syncthreads();
+    auto load = [&](int r) {
+        if (r < rounds) {
+            if (r % kRounds == 0) look_up(r);
+            const int s = r % kMoveStages, first = r % kRounds * kRound;
 #pragma unroll
-        for (int u = 0; u < kMoveUnroll; ++u) {
-            if (to_now[u]) *to_now[u] = now[u];
-            now[u] = next[u];
-            to_now[u] = to_next[u];
+            for (int u = 0; u < kSteps; ++u) {
+                const int of = first + u * kRows + lane / kLanes;
+                const long long f = __shfl_sync(0xffffffffu, from, of), t = __shfl_sync(0xffffffffu, to, of);
+                if (t >= 0) copy16_async(smem_u32(&sh.piece[s][u][threadIdx.x]), x + max(f, 0ll) + piece, f >= 0);
+            }
+            if (lane / kRound == r % kRounds) sh.to[s][warp * 32 + lane % kRound] = to;
         }
+        copies_commit();
+    };
+#pragma unroll 1
+    for (int r = 0; r < kMoveStages - 1; ++r) load(r);
+#pragma unroll 1
+    for (int r = 0; r < rounds; ++r) {
+        copies_wait<kMoveStages - 2>();
+        // everything up to this round has been read
+        if (ranks > 1) cluster.sync();
+        else __syncthreads();
+        const int s = r % kMoveStages;
+#pragma unroll
+        for (int u = 0; u < kSteps; ++u) {
+            const long long t = sh.to[s][warp * 32 + u * kRows + lane / kLanes];
+            if (t >= 0) x[t + piece] = sh.piece[s][u][threadIdx.x];
+        }
+        __syncwarp();
+        load(r + kMoveStages - 1);
     }
 }
 
@@ -418,7 +457,9 @@ __device__ __forceinline__ void move_numbers(const EvictParams& p, const int* ke
 
 // blockIdx.y: slices of K, then of V, then the weights and scales.
 template <int D, bool E4M3, int SLICES>
-__global__ void __launch_bounds__(kMoveThreads, 2) evict_move_kernel(const __grid_constant__ EvictParams p) {
+__global__ void __launch_bounds__(kMoveThreads, kMoveBlocks) evict_move_kernel(const __grid_constant__ EvictParams p) {
+    extern __shared__ uint4 raw[];
+    MoveShared& sh = *reinterpret_cast<MoveShared*>(raw);
     constexpr int es = E4M3 ? 1 : 2, kPieces = D * es / 16;
     const cg::cluster_group cluster = cg::this_cluster();
     const int head = blockIdx.x / cluster.num_blocks(), b = head / p.kv.hkv, h = head - b * p.kv.hkv;
@@ -427,9 +468,9 @@ __global__ void __launch_bounds__(kMoveThreads, 2) evict_move_kernel(const __gri
     const int n = sequence(p, b).n, y = blockIdx.y;
     const int* kept = p.kept + static_cast<long long>(head) * p.max_keep;
     if (y < SLICES) {
-        move_rows<uint4, kPieces, SLICES>(p, kept, b, h, n, static_cast<uint4*>(p.kv.k), p.kv.k_ps * es / 16, y, cluster);
+        move_rows<kPieces, SLICES>(p, kept, b, h, n, static_cast<uint4*>(p.kv.k), p.kv.k_ps * es / 16, y, sh, cluster);
     } else if (y < 2 * SLICES) {
-        move_rows<uint4, kPieces, SLICES>(p, kept, b, h, n, static_cast<uint4*>(p.kv.v), p.kv.v_ps * es / 16, y - SLICES, cluster);
+        move_rows<kPieces, SLICES>(p, kept, b, h, n, static_cast<uint4*>(p.kv.v), p.kv.v_ps * es / 16, y - SLICES, sh, cluster);
     } else {
         if constexpr (E4M3) {
             const Numbers x[3] = {{p.w, p.w_ps}, {p.kv.k_scale, p.kv.ks_ps}, {p.kv.v_scale, p.kv.vs_ps}};
@@ -453,10 +494,11 @@ int cluster_of(long long heads, long long most, long long rows, int least) {
 }
 
 template <class... Args>
-cudaError_t launch_clusters(void (*kern)(Args...), dim3 grid, int threads, int cluster, bool dependent, cudaStream_t stream, Args... args) {
+cudaError_t launch_clusters(void (*kern)(Args...), dim3 grid, int threads, int smem, int cluster, bool dependent, cudaStream_t stream, Args... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute at[2] = {};
     at[0].id = cudaLaunchAttributeClusterDimension;
@@ -469,21 +511,31 @@ cudaError_t launch_clusters(void (*kern)(Args...), dim3 grid, int threads, int c
     cfg.numAttrs = (cluster > 1 ? 1 : 0) + (dependent ? 1 : 0);
     return cudaLaunchKernelEx(&cfg, kern, args...);
 }
+
+template <int D, bool E4M3, int SLICES>
+cudaError_t launch_move(const EvictParams& p, dim3 grid, int cluster, cudaStream_t stream) {
+    const auto kernel = evict_move_kernel<D, E4M3, SLICES>;
+    constexpr int kSmem = sizeof(MoveShared);
+    static std::atomic<unsigned long long> done{0};
+    if (!once_a_device(done, [&] { return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) == cudaSuccess; }))
+        return cudaErrorUnknown;
+    return launch_clusters(kernel, grid, kMoveThreads, kSmem, cluster, true, stream, p);
+}
 }  // namespace
 
 int launch_cache_evict(const EvictParams& p, int sms, cudaStream_t stream) {
     const long long heads = static_cast<long long>(p.kv.batch) * p.kv.hkv;
     const long long most_len = static_cast<long long>(p.kv.max_pages) * p.kv.page;
     const int sel = cluster_of(heads, sms, most_len, 4096);
-    if (launch_clusters(evict_select_kernel, dim3(static_cast<unsigned>(heads * sel)), kSelThreads, sel, false, stream, p) != cudaSuccess) return -4;
-    const int mov = cluster_of(2 * heads, 4LL * sms, p.max_keep, 256);
-    // few blocks: rows in two halves, each of which is packed by itself (8 heads of 128k in e4m3, 16k of them kept: __ us, __ whole)
+    if (launch_clusters(evict_select_kernel, dim3(static_cast<unsigned>(heads * sel)), kSelThreads, 0, sel, false, stream, p) != cudaSuccess) return -4;
+    // (a cluster's blocks wait for one another every round: 128 heads, two blocks each, 87 us, one 65)
+    const int mov = cluster_of(2 * heads, 2LL * sms, p.max_keep, 256);
+    // few blocks: rows in two halves, each of which is packed by itself (8 heads of 128k in e4m3, 16k of them kept: 46 us, 55 whole;
+    // 128 heads 75, 65)
     const int slices = 2 * heads * mov <= sms ? 2 : 1;
     const dim3 grid(static_cast<unsigned>(heads * mov), 2 * slices + 1);
     cudaError_t e;
-#define RA_MOVE(D, E4M3)                                                                                                     \
-    e = slices == 2 ? launch_clusters(evict_move_kernel<D, E4M3, 2>, grid, kMoveThreads, mov, true, stream, p)                \
-                    : launch_clusters(evict_move_kernel<D, E4M3, 1>, grid, kMoveThreads, mov, true, stream, p)
+#define RA_MOVE(D, E4M3) e = slices == 2 ? launch_move<D, E4M3, 2>(p, grid, mov, stream) : launch_move<D, E4M3, 1>(p, grid, mov, stream)
     if (p.kv.d == 128) {
         if (p.kv.e4m3) RA_MOVE(128, true);
         else RA_MOVE(128, false);
