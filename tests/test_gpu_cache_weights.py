@@ -397,3 +397,53 @@ def test_long_ones_against_torch_in_64_bits(ra, n, L, hq, hkv, e4m3, window):
     rel = (d + 16) * 2.0 ** -23 * size + 2.0 ** -22 * 8 + 2.0 ** -20 + (n * hq / hkv + 16) * 2.0 ** -24
     worst = float(((got - want).abs() / (rel * want.abs() + 1e-37)).max())
     assert worst <= 1.0, f"off by {worst:.3g} of its bound"
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("page,hq,hkv,d,seqs", [
+    (16, 16, 2, 64, [(16, 1500), (17, 900), (16, 300), (33, 1100)]),     # one unit of 128 rows, two, one, three
+    (128, 8, 4, 128, [(64, 3000), (65, 2000), (64, 128), (64, 70)]),     # the same with all pairs of two tiles, then one tile
+    (48, 32, 2, 128, [(8, 6000), (24, 3000), (16, 257), (9, 255)]),
+    (256, 6, 1, 64, [(21, 5000), (22, 5000), (43, 129), (84, 2100)]),    # units of 126 rows
+])
+@pytest.mark.parametrize("window", [0, 700])
+def test_few_units_see_every_pair_of_tiles(ra, page, hq, hkv, d, seqs, window, e4m3):
+    r = Run(seqs, hq=hq, hkv=hkv, d=d, page=page, e4m3=e4m3, seed=23, decay=0.5, window=window, sinks=4 if window else 0)
+    r.call(ra)
+    assert ra.sync_status() == ra.RA_OK
+    r.check()
+
+
+@pytest.mark.parametrize("batch", [223, 224, 225, 257])
+def test_batches_whose_shares_leave_shared_memory(ra, batch):
+    seqs = [(14 + b % 5, 14 + b % 5 + 37 * (b % 11)) for b in range(batch)]
+    r = Run(seqs, hq=8, hkv=1, d=64, page=16, seed=24)
+    r.call(ra)
+    assert ra.sync_status() == ra.RA_OK
+    r.check()
+
+
+@pytest.mark.parametrize("n", [1, 30, 300])
+def test_two_calls_at_once(ra, n):
+    """Batches, pools and workspaces of their own on two streams, again and again."""
+    runs = [Run([(n, n + 2000), (n, n + 90)], hq=8, hkv=2, d=64, page=16, e4m3=s == 1, seed=25 + s) for s in range(2)]
+    want = []
+    for r in runs:
+        r.call(ra)
+        torch.cuda.synchronize()
+        want.append(r.w.clone())
+    args = [(r.ws(ra), r.q.to(dev()), r.lse.to(dev())) for r in runs]
+    streams = [torch.cuda.Stream() for _ in runs]
+    torch.cuda.synchronize()
+    for r in runs:
+        r.w.copy_(r.before)
+    torch.cuda.synchronize()
+    for k in range(6):
+        for r, s, (ws, q, lse) in zip(runs, streams, args):
+            with torch.cuda.stream(s):
+                r.w.copy_(r.before)
+                r.call(ra, stream=s, ws=ws, q=q, lse=lse)
+    torch.cuda.synchronize()
+    assert ra.sync_status() == ra.RA_OK
+    for r, w in zip(runs, want):
+        assert torch.equal(torch.nan_to_num(r.w, nan=-1.0), torch.nan_to_num(w, nan=-1.0))
