@@ -33,6 +33,10 @@ numpy).  Each function names the passage it follows:
   rotation").
 * :mod:`oracle.paged` -- a paged K/V cache (bf16 or e4m3 rows) and the attention
   of a sequence's last rows over it.
+* :mod:`oracle.qk_norm` -- the norm and the rotation of query and key rows, and
+  their gradients.
+* :mod:`oracle.evict` -- the attention weight that cached positions have had, and
+  which of them stay.
 * :mod:`oracle.backward` -- the exact gradient of that attention with respect
   to q, k and v, and the ring's backward (KV blocks travel with their dK, dV
   accumulators); the pages give only the forward, so the gradient is the
