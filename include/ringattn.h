@@ -470,8 +470,12 @@ int ringattn_paged_workspace_bytes(int total, int batch, int Hq, int Hkv, int d,
  *     left it (any lse does: a key's weight is exp(q . k - lse)); a row whose lse is -inf adds nothing.
  *     V is not read.  kv->v has to be given all the same.
  * Positions that no row sees (behind a window) are scaled by decay; those of a sequence without rows
- * stay as they are.  Scores and sums are fp32; no atomics: the same call gives the same bits.  With
- * e4m3 a scale that is no power of two is used in fp32.
+ * stay as they are.  No two (sequence, position) pairs of the batch may have the same page and row: a
+ * prefix that two sequences share has one place for its weights, and both would write it.
+ * Scores and sums are fp32; no atomics: the same call gives the same bits.  In e4m3, with up to 80 rows of a sequence
+ * and KV head (max_q * Hq / Hkv), elements of q below 2^-28 of their row's largest lose bits, and with more rows a scale
+ * below 2^-60 counts as 2^-60; with more rows than those (24 in bf16) an lse beyond 2^60 either way counts as 2^60.  A scale that
+ * is no power of two is used in fp32.
  * Requires what ringattn_fwd_paged requires.
  */
 int ringattn_cache_weights(const void* q, long long q_token_stride, long long q_head_stride, const float* lse,
@@ -495,7 +499,7 @@ int ringattn_cache_weights(const void* q, long long q_token_stride, long long q_
  * kv_len_out: [batch] int32, device: n.  May be kv->kv_len.
  * kept: [batch, Hkv, max_keep] int32, device, contiguous: where the i-th position was; -1 from n on.
  * A page of the table outside [0, n_pages) reads as weight 0 and zeros, and what would move there is dropped.
- * Requires max_keep at most 2^30, batch * Hkv below 2^31 (else RA_ERR_UNSUPPORTED); 4-byte aligned keep, kv_len_out, kept.
+ * Requires max_keep at most 2^30, batch * Hkv below 2^28 (else RA_ERR_UNSUPPORTED); 4-byte aligned keep, kv_len_out, kept.
  */
 int ringattn_cache_evict(const ra_paged_kv* kv, float* weights, long long weights_page_stride, const int* keep,
                          int max_keep, int sinks, int recent, int* kv_len_out, int* kept, ra_stream_t stream);
@@ -509,6 +513,7 @@ int ringattn_cache_evict(const ra_paged_kv* kv, float* weights, long long weight
  *     q's rows are multiplied by q_scale.
  * Pairs are (j, j + rot/2), or (2j, 2j + 1) with interleaved = 1; elements from rot on are not turned.
  * Arithmetic is fp32 (a row whose squares add up to more than fp32 holds, |x| from about 2^60 on, has r = 0), rounded once.
+ * With eps = 0 a row of zeros is 0 / 0: NaN.
  */
 typedef struct {
     void* q; /* [total, Hq, d] */
