@@ -12,8 +12,8 @@
 //
 // 16 sequences of 4k to 16k positions, 8 KV heads, 2k kept, bf16: 65 us, 4.2 TB/s of what it has to read and write.  Selecting is a
 // chain of latencies (three digits and a list, each with two exchanges in the cluster); packing takes 50, as long as a plain
-// gather of such rows, 256 bytes one in eight.  One sequence of 128k in e4m3, 16k kept: 46 us, selecting 20, then rounds that
-// wait for the cluster.
+// gather of such rows, 256 bytes one in eight.  One sequence of 128k in e4m3, 16k kept: 46 us, selecting 20, then rounds in which
+// blocks of a cluster wait for each other; 64k kept in bf16 142, 3.9 TB/s.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
@@ -26,10 +26,7 @@ namespace {
 namespace cg = cooperative_groups;
 
 constexpr int kCluster = 8;  // most blocks of a (sequence, KV head)
-constexpr int kSelThreads = 1024;
-constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kKeys = 16;  // neighbouring positions of a thread, all on one page
-constexpr int kChunk = kKeys * kSelThreads;
 constexpr int kDigit = 11;  // bits; 32 = 11 + 11 + 10
 constexpr int kBins = 1 << kDigit;
 constexpr int kDirect = 512;  // and up to which they are ranked one against the other
@@ -87,12 +84,13 @@ __device__ __forceinline__ uint32_t warp_scan(uint32_t x) {
     return x;
 }
 // Exclusive sums over the block; `total` gets the sum of all.
+template <int THREADS>
 __device__ __forceinline__ uint32_t block_scan(uint32_t x, uint32_t* sm, uint32_t& total) {
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     const uint32_t s = warp_scan(x);
     if (lane == 31) sm[warp] = s;
     __syncthreads();
-    const uint32_t w = warp_scan(lane < kSelWarps ? sm[lane] : 0u);
+    const uint32_t w = warp_scan(lane < THREADS / 32 ? sm[lane] : 0u);
     const uint32_t before = __shfl_sync(0xffffffffu, w, (warp + 31) % 32);
     total = __shfl_sync(0xffffffffu, w, 31);
     __syncthreads();
@@ -106,7 +104,9 @@ __device__ __forceinline__ int find_lane(uint32_t count, uint32_t& need) {
     return at;
 }
 
-__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_constant__ EvictParams p) {
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) evict_select_kernel(const __grid_constant__ EvictParams p) {
+    constexpr int kWarps = THREADS / 32, kChunk = kKeys * THREADS;
     // this block's counts, the cluster's, the keys that are left; at the end the positions that stay
     struct Counts {
         uint32_t hist[3][kBins], list[kList + 1];  // (the last place of the list: for those that are not)
@@ -114,7 +114,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
     __shared__ alignas(16) Counts counts;
     // sums of 64 bins each, the largest first: this block's, the cluster's, and the cluster's counts of the 64 in question
     __shared__ alignas(8) uint32_t coarse[3][32], all_coarse[3][32], fine[3][64];
-    __shared__ uint32_t sm[kSelWarps], listed, stretch[2];
+    __shared__ uint32_t sm[kWarps], listed, stretch[2];
     auto& hist = counts.hist;
     auto& list = counts.list;
     cg::cluster_group cluster = cg::this_cluster();
@@ -124,7 +124,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
     const Sequence s = sequence(p, b);
     launch_dependents();
     int* kept = p.kept + static_cast<long long>(head) * p.max_keep;
-    const int first = rank * kSelThreads + threadIdx.x, step = ranks * kSelThreads;
+    const int first = rank * THREADS + threadIdx.x, step = ranks * THREADS;
     for (int i = s.n + first; i < p.max_keep; i += step) kept[i] = -1;
     if (s.n == s.L) {
         for (int i = first; i < s.n; i += step) kept[i] = i;
@@ -141,7 +141,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
     if (threadIdx.x == 0) listed = 0;
     if (threadIdx.x < 96) (&all_coarse[0][0])[threadIdx.x] = 0;
     if (threadIdx.x < 192) (&fine[0][0])[threadIdx.x] = 0;
-    for (int i = threadIdx.x; i < 3 * kBins / 4; i += kSelThreads) reinterpret_cast<uint4*>(&hist[0][0])[i] = make_uint4(0, 0, 0, 0);
+    for (int i = threadIdx.x; i < 3 * kBins / 4; i += THREADS) reinterpret_cast<uint4*>(&hist[0][0])[i] = make_uint4(0, 0, 0, 0);
     __syncthreads();
     auto together = [&]() {
         if (ranks > 1) cluster.sync();
@@ -178,7 +178,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
             use_list = listed <= kList;
             if (ranks == 1 && listed <= kDirect) {
                 // so few that each is ranked against all: a warp one after the other (two digits more would take 4 us)
-                for (uint32_t i = warp; i < listed; i += kSelWarps) {
+                for (uint32_t i = warp; i < listed; i += kWarps) {
                     const uint32_t mine = list[i];
                     uint32_t both = 0;  // above in the low half, equal in the high one
                     for (uint32_t j = lane; j < listed; j += 32) both += list[j] > mine ? 1u : list[j] == mine ? 0x10000u : 0u;
@@ -196,7 +196,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
             }
         }
         if (use_list) {
-            for (uint32_t i = threadIdx.x; i < listed; i += kSelThreads)
+            for (uint32_t i = threadIdx.x; i < listed; i += THREADS)
                 if ((list[i] & mask) == prefix) atomicAdd(&hist[pass][(list[i] >> shift) & digit], 1u);
         } else {
             for (int c = 0; c < chunks; ++c) {
@@ -221,10 +221,17 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
             }
         }
         __syncthreads();
-        static_assert(kBins == 2 * kSelThreads && kSelWarps == 32, "64 bins a warp");
-        const uint2 x = *reinterpret_cast<const uint2*>(&hist[pass][kBins - 2 - 2 * static_cast<int>(threadIdx.x)]);
-        const uint32_t sum = __reduce_add_sync(0xffffffffu, x.x + x.y);
-        if (lane == 0) coarse[pass][warp] = sum;
+        constexpr int kBinsEach = kBins / THREADS, kLanes = 64 / kBinsEach;  // of a thread; threads that have 64 together
+        static_assert(kBins == 32 * 64 && kLanes <= 32, "32 sums of 64 bins");
+        uint32_t sum = 0;
+#pragma unroll
+        for (int e = 0; e < kBinsEach; e += 2) {
+            const uint2 x = *reinterpret_cast<const uint2*>(&hist[pass][kBins - kBinsEach * (static_cast<int>(threadIdx.x) + 1) + e]);
+            sum += x.x + x.y;
+        }
+#pragma unroll
+        for (int d = 1; d < kLanes; d *= 2) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        if (lane % kLanes == 0) coarse[pass][threadIdx.x / kLanes] = sum;
         together();
         // of the other blocks' counts only what is needed: first the sums, then the 64 in question (all 2048 of eight blocks took
         // 4500 cycles, three times over)
@@ -269,7 +276,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
     uint32_t above = 0, equal = 0, total, before = 0;
     for (int c = 0; c < chunks; ++c) {
         if (chunks > 1) load(c);
-        before = block_scan(tally(), sm, total);
+        before = block_scan<THREADS>(tally(), sm, total);
         above += total & 0xffffu;
         equal += total >> 16;
     }
@@ -304,7 +311,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
     for (int c = 0; c < chunks; ++c) {
         if (chunks > 1) {
             load(c);
-            before = block_scan(tally(), sm, total);
+            before = block_scan<THREADS>(tally(), sm, total);
         }
         const uint32_t a = above + (before & 0xffffu), q = equal + (before >> 16), from = above + min(equal, need);
         above += total & 0xffffu;
@@ -319,7 +326,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
         if (stays_here <= kStage) {
             for (; stays && at < kStage; stays &= stays - 1u, ++at) stage[at] = j0 + __ffs(stays) - 1;
             __syncthreads();
-            for (uint32_t i = threadIdx.x; i < stays_here && from + i < static_cast<uint32_t>(s.n); i += kSelThreads) kept[from + i] = stage[i];
+            for (uint32_t i = threadIdx.x; i < stays_here && from + i < static_cast<uint32_t>(s.n); i += THREADS) kept[from + i] = stage[i];
             __syncthreads();
         } else {
             for (; stays && from + at < static_cast<uint32_t>(s.n); stays &= stays - 1u, ++at) kept[from + at] = j0 + __ffs(stays) - 1;
@@ -396,12 +403,22 @@ __device__ __forceinline__ void move_rows(const EvictParams& p, const int* kept,
     };
 #pragma unroll 1
     for (int r = 0; r < kMoveStages - 1; ++r) load(r);
+    if (ranks > 1) {
+        copies_wait<kMoveStages - 2>();
+        cluster.barrier_arrive();
+    }
 #pragma unroll 1
     for (int r = 0; r < rounds; ++r) {
-        copies_wait<kMoveStages - 2>();
-        // everything up to this round has been read
-        if (ranks > 1) cluster.sync();
-        else __syncthreads();
+        // everything up to this round has been read; that the next one has, a cluster's block says before it writes this one (128k
+        // positions to 64k in bf16 187 us with a barrier a round in one piece, 142 so)
+        if (ranks > 1) {
+            cluster.barrier_wait();
+            copies_wait<kMoveStages - 3>();
+            cluster.barrier_arrive();
+        } else {
+            copies_wait<kMoveStages - 2>();
+            __syncthreads();
+        }
         const int s = r % kMoveStages;
 #pragma unroll
         for (int u = 0; u < kSteps; ++u) {
@@ -411,6 +428,7 @@ __device__ __forceinline__ void move_rows(const EvictParams& p, const int* kept,
         __syncwarp();
         load(r + kMoveStages - 1);
     }
+    if (ranks > 1) cluster.barrier_wait();
 }
 
 // The same for N tensors of one number a row, whose places are looked up once.
@@ -527,7 +545,13 @@ int launch_cache_evict(const EvictParams& p, int sms, cudaStream_t stream) {
     const long long heads = static_cast<long long>(p.kv.batch) * p.kv.hkv;
     const long long most_len = static_cast<long long>(p.kv.max_pages) * p.kv.page;
     const int sel = cluster_of(heads, sms, most_len, 4096);
-    if (launch_clusters(evict_select_kernel, dim3(static_cast<unsigned>(heads * sel)), kSelThreads, 0, sel, false, stream, p) != cudaSuccess) return -4;
+    const dim3 sel_grid(static_cast<unsigned>(heads * sel));
+    // Blocks of half the threads, two an SM, where there are many, or where a stretch is no longer than their 8192 keys (512 heads of 8k
+    // 236 us, 220 so; 8 heads of 32k 54, 50; but 128 heads of 16k, with one block each, 68, 82).
+    const bool half = heads > sms || most_len <= 8192LL * sel;
+    if ((half ? launch_clusters(evict_select_kernel<512>, sel_grid, 512, 0, sel, false, stream, p)
+             : launch_clusters(evict_select_kernel<1024>, sel_grid, 1024, 0, sel, false, stream, p)) != cudaSuccess)
+        return -4;
     // (a cluster's blocks wait for one another every round: 128 heads, two blocks each, 87 us, one 65)
     const int mov = cluster_of(2 * heads, 2LL * sms, p.max_keep, 256);
     // few blocks: rows in two halves, each of which is packed by itself (8 heads of 128k in e4m3, 16k of them kept: 46 us, 55 whole;

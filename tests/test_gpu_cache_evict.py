@@ -279,3 +279,12 @@ def test_captured_and_on_another_stream(ra):
         for x, y in zip(r.pools(), pools):
             assert torch.equal(torch.nan_to_num(x.float()), torch.nan_to_num(y.float())), how
     assert ra.sync_status() == ra.RA_OK
+
+
+@pytest.mark.parametrize("hkv,lens,keep", [(160, [8192, 1], [700, 1]), (153, [8193], [4000]), (152, [16400], [300]), (80, [20000, 5000], [64, 2500])])
+@pytest.mark.parametrize("kind", ["all kinds", "few values"])
+def test_more_heads_than_the_gpu_has_sms(ra, hkv, lens, keep, kind):
+    g = torch.Generator().manual_seed(31)
+    r = Run(lens, keep, hkv=hkv, d=64, page=16, seed=31,
+            weights=lambda b, L: torch.rand((L, hkv), generator=g) if kind == "all kinds" else torch.randint(0, 3, (L, hkv), generator=g).float())
+    r.check(ra, sinks=3, recent=20)

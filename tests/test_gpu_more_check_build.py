@@ -80,6 +80,7 @@ def test_weights(libs, e4m3, hq, hkv, d, page, seqs, kw):
     (3, 64, 48, [131, 1700, 20], [64, 900, 0]),
     (2, 128, 64, [40000, 9000], [20000, 10]),
     (40, 64, 16, [900] * 8, [300] * 8),  # a block a head
+    (160, 64, 16, [9000], [500]),
 ])
 def test_evict(libs, e4m3, hkv, d, page, lens, keep):
     def run(ra):
