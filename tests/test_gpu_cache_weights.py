@@ -447,3 +447,31 @@ def test_two_calls_at_once(ra, n):
     assert ra.sync_status() == ra.RA_OK
     for r, w in zip(runs, want):
         assert torch.equal(torch.nan_to_num(r.w, nan=-1.0), torch.nan_to_num(w, nan=-1.0))
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("n", [1, 40, 300])
+def test_pages_far_apart(ra, e4m3, n):
+    """Pages whose places pass 32 bits, in elements and in bytes: weights and eviction give what they give with pages side by side."""
+    r = Run([(n, n + 200), (min(n, 7), 150)], hq=8, hkv=2, d=64, page=64, e4m3=e4m3, seed=27)
+    pages = r.B.n_pages
+    near = [r.B.k_cache, r.B.v_cache, r.w] + ([r.B.k_scale, r.B.v_scale] if e4m3 else [])
+    apart = (2 ** 32 + 4096) // (pages - 1) // 64 * 64 + 64  # elements: the last page lies behind 2^32 of them
+    far = []
+    for x in near:
+        base = torch.empty(apart * (pages - 1) + x[0].numel(), dtype=x.dtype, device=dev())
+        y = base.as_strided(x.shape, (apart, *x.stride()[1:]))
+        y.view(torch.uint8 if e4m3 and x.element_size() == 1 else x.dtype).copy_(x.view(torch.uint8 if e4m3 and x.element_size() == 1 else x.dtype))
+        far.append(y)
+    keep, lens = (torch.tensor(v, dtype=torch.int32, device=dev()) for v in ((70, 60), (0, 0)))
+    res = []
+    for pools in (near, far):
+        kw = dict(k_scale=pools[3], v_scale=pools[4]) if e4m3 else {}
+        ra.cache_weights(r.q.to(dev()), r.lse.to(dev()), *pools[:3], *r.B.args(), r.ws(ra), max_q=r.max_q, **kw)
+        kept = torch.empty((2, 2, 70), dtype=torch.int32, device=dev())
+        ra.cache_evict(*pools[:3], r.B.dtable, r.B.dlen, keep, lens, kept, sinks=1, recent=5, **kw)
+        torch.cuda.synchronize()
+        assert ra.sync_status() == ra.RA_OK
+        res.append([kept] + [x.contiguous().view({1: torch.uint8, 2: torch.int16, 4: torch.int32}[x.element_size()]) for x in pools])
+    for a, b in zip(*res):
+        assert torch.equal(a, b)
