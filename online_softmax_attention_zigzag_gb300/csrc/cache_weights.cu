@@ -269,7 +269,9 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<E4M3>()) weights_kerne
 // More rows of a sequence and KV head, up to kWeightsWideRows: too many for registers.  A block takes a stretch of groups, its
 // warps every eighth, with q's fragments in shared memory as the lanes take them (16 bytes a lane, no conflicts), and so is what a
 // column's scores are compared with.  K is read once whatever the rows are, in e4m3 turned into fp16 once.
-constexpr int kWideBlocks = 3;  // an SM (two: 64 rows of e4m3 156 us for 140)
+// Blocks of an SM.  24 and 64 rows of e4m3 take 107 and 140 us so; with four 122 and 145; with two, and two groups a warp, which halves
+// the reads of q from shared memory, 134 and 166.
+constexpr int kWideBlocks = 3;
 
 struct WideColumn {
     float bias, mul;

@@ -35,9 +35,9 @@ namespace {
 constexpr int kTile = kPagedTile;
 constexpr int kSumWarps = 16, kMmaWarp = 16, kQWarp = 18, kKWarp = 19, kExpandWarp = 20;
 constexpr int kHalf = kTile / 2;  // columns of a warp's share of a unit
-// Tiles of q, and in e4m3 of codes, in shared memory.  Of K four, an item ahead (16 x 32 rows of 1k to 32k keys: 136 us with four,
-// 148 with three, 168 with two); in e4m3 three and two of codes (two and four: the same).  A third tile of q gains nothing where
-// items are long: 1364 us for 4096 rows of 32k either way.
+// Tiles of q, and in e4m3 of codes, in shared memory.  Of K four in bf16, an item ahead; in e4m3 three and two of codes (two and
+// four: the same).  A third tile of q in place of one of K gains little where items are long, and loses more where they are not:
+// 4096 rows of 32k 1337 us for 1346, 16 x 32 rows of 1k to 32k keys 147 for 123, in e4m3 276 for 253.
 constexpr uint32_t kQSlots = 2, kRawSlots = 2;
 constexpr int kAccs = 2, kItems = 4;  // (accumulators of each tile)
 constexpr int kBiasBytes = kTile * 32;  // a step of 16 of a product's operand
@@ -603,7 +603,8 @@ __device__ void sum_role(const WeightsParams& p, int tile, int half, Shared& sh,
             const uint32_t at = lanes + acc * kTile;
             float sum[4] = {0.f, 0.f, 0.f, 0.f};
             if (all) {
-                // the scores leave tensor memory at once, so that the next product can begin
+                // The scores leave tensor memory at once, so that the next product can begin.  (In two halves, the next unit's first
+                // one on its way under this one's second, they held it longer: 4096 rows of 32k 1559 us for 1350.)
                 uint32_t x[2][32];
                 tmem_ld32(at, x[0]);
                 tmem_ld32(at + 32, x[1]);
