@@ -20,9 +20,10 @@
 // of 128 columns a tile.
 //
 // 4096 rows on 32k keys, 64 query heads, 8 KV heads, d = 128, bf16: 1350 us in ten calls (1456 in long runs, at the power limit),
-// 1.53 PFLOP/s of its 2.06 TFLOP; the products alone 1222, without the exponentials 1252.  lse from shared memory 1860.  12
+// 1.53 PFLOP/s of its 2.06 TFLOP; copies of it at 1364: the products alone 1222, without the exponentials 1252.  lse from shared
+// memory 1860.  12
 // sequences of up to 1023 rows behind up to 9000 keys in e4m3, a window of 2500: 127 us.  Items are short there, and what an item
-// costs beside its units (finding it, its pages, two tiles of codes) is what bounds it: 16 sequences of 32 rows 123 us in bf16, 263
+// costs beside its units (finding it, its pages, two tiles of codes) is what bounds it: 16 sequences of 32 rows 123 us in bf16, 253
 // in e4m3, where expanding an item's codes takes longer than its two units.
 #include <cuda_bf16.h>
 
