@@ -467,7 +467,8 @@ int ringattn_paged_workspace_bytes(int total, int batch, int Hq, int Hkv, int d,
  *     (a multiple of 4, at least Hkv * page_size, at most 2^36), 16-byte aligned.
  * decay: in [0, 1]; 1 adds up, 0 does not read what was there.
  * q, kv, Hq, max_q, causal, window, sinks, workspace: as for ringattn_fwd_paged; lse [total, Hq] fp32 as it
- *     left it (any lse does: a key's weight is exp(q . k - lse)); a row whose lse is -inf adds nothing.
+ *     left it (any lse does: a key's weight is exp(q . k - lse)); a row whose lse is -inf adds nothing, whatever it
+ *     and the keys hold.
  *     V is not read.  kv->v has to be given all the same.
  * Positions that no row sees (behind a window) are scaled by decay; those of a sequence without rows
  * stay as they are.  No two (sequence, position) pairs of the batch may have the same page and row: a

@@ -26,6 +26,7 @@
 // costs beside its units (finding it, its pages, two tiles of codes) is what bounds it: 16 sequences of 32 rows 123 us in bf16, 253
 // in e4m3, where expanding an item's codes takes longer than its two units.
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 
 #include "cache_weights.h"
 #include "ptx_paged.cuh"
@@ -65,13 +66,14 @@ struct Item {
     int T, base, L, keys;
     int page[2][8], row[2][8];  // of the tiles' boxes; page < 0: none
     float scale[kWeightsPair];  // e4m3: of the keys, as held_scale gives them
+    int q0;                     // the sequence's first row
 };
 __device__ __forceinline__ int tiles_of(int pair, int keys) { return pair * kWeightsPair + kTile < keys ? 2 : 1; }
 
 struct Shared {
     uint64_t item_full[kItems], item_empty[kItems];
     uint64_t item_raw[kItems], raw_full[kRawSlots], raw_empty[kRawSlots];  // e4m3
-    uint64_t k_full[4], k_empty[4], q_full[kQSlots], q_empty[kQSlots],
+    uint64_t k_full[4], k_empty[4], q_full[kQSlots], q_empty[kQSlots], q_landed,
         acc_full[2][kAccs], acc_empty[2][kAccs], half_full[2], half_empty[2], drain[2];
     Item item[kItems];
     float half[2][kTile];  // what the second half of the columns gives a tile's keys
@@ -244,8 +246,24 @@ __device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy
 // nothing anyhow, and where lse is beyond, fp32 scores are whole trillions apart.
 __device__ __forceinline__ float held_scale(float scale) { return scale < 0x1p-60f ? 0x1p-60f : scale; }
 
+// Zeros in place of rows of q (lane + 32 i for bit i of `out`), once the unit has landed; false if it has not in time.
+template <int BOXES>
+__device__ __noinline__ bool leave_out(uint32_t tile, Shared& sh, uint32_t landed, uint32_t out, int* err, uint64_t timeout_ns) {
+    const WaitCtl wc{&sh.abort_flag, err, timeout_ns};
+    if (!__all_sync(0xffffffffu, mbar_wait(&sh.q_landed, landed & 1u, wc, 32))) {
+        drain_wait(&sh.q_landed, landed & 1u, timeout_ns);
+        return false;
+    }
+    for (int i = 0; i < 4; ++i)
+        for (int k = 0; k < BOXES * 8 && (out >> i & 1u); ++k)
+            sts128(tile + k / 8 * (kTile * 128) + (threadIdx.x % 32 + 32 * i) * 128 + k % 8 * 16, 0, 0, 0, 0);
+    return true;
+}
+
 // One warp.  The next unit's lse is on its way while a unit is handed on (8 rows of 16 sequences 123 us without, 108 so), and a slot that
 // holds the unit already, where only a few see each pair, is handed on as it is (32 rows 140 us without, 123).
+// A row whose lse is -inf adds nothing: with zeros in place of its q, and -2^60 for -lse, its weights are 0 whatever it holds (but for
+// keys that hold no numbers: `again`).
 template <int D, bool E4M3>
 __device__ void q_role(const WeightsParams& p, const CUtensorMap* tq, uint32_t smem, Shared& sh, const long long* sums, const WaitCtl& wc) {
     using C = Cfg<D, E4M3>;
@@ -278,7 +296,7 @@ __device__ void q_role(const WeightsParams& p, const CUtensorMap* tq, uint32_t s
     };
     Walk w = {};
     bool more = walk_begin(p, sums, w), ok = true;
-    uint32_t n = 0;
+    uint32_t n = 0, landed = 0;
     Unit now = {}, held[2] = {{-1, 0, 0, 0, 0}, {-1, 0, 0, 0, 0}};  // held: what the slots hold, the next one's first
     float x[4];
     if (more) {
@@ -295,17 +313,26 @@ __device__ void q_role(const WeightsParams& p, const CUtensorMap* tq, uint32_t s
         if (!ok) break;
         const uint32_t s = n % kQSlots;
         if (held[0].b != now.b || held[0].h != now.h || held[0].u != now.u) {
+            uint32_t out = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) out |= x[i] == -INFINITY ? 1u << i : 0u;
+            uint64_t* bar = __any_sync(0xffffffffu, out != 0u) ? &sh.q_landed : &sh.q_full[s];
             if (lane == 0) {
-                mbar_arrive_expect_tx(&sh.q_full[s], bytes);
+                mbar_arrive_expect_tx(bar, bytes);
                 int tok = now.q0 + (now.u << p.unit_log);
                 if (!RA_CHECKED(paged_row_ok(p.kv, p.hq, tok, now.h * p.g + p.g - 1), p.err, kSiteWeightsRow)) tok = 0;
                 for (int i = 0; i < C::kBoxes; ++i)
-                    tma_load_3d(q_base + s * C::kTileBytes + i * C::kBoxBytes, tq, &sh.q_full[s], i * 64, now.h * p.g, tok, keep);
+                    tma_load_3d(q_base + s * C::kTileBytes + i * C::kBoxBytes, tq, bar, i * 64, now.h * p.g, tok, keep);
             }
             __syncwarp();
+            if (bar == &sh.q_landed) {
+                ok = leave_out<C::kBoxes>(q_base + s * C::kTileBytes, sh, landed++, out, p.err, p.timeout_ns);
+                if (!ok) break;
+                if (lane == 0) mbar_arrive(&sh.q_full[s]);
+            }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const float v = x[i] == -INFINITY ? -0x1p60f : -x[i];  // (a row whose lse is -inf adds nothing)
+                const float v = x[i] == -INFINITY ? -0x1p60f : -x[i];
                 store_q_bias<E4M3>(b_base + s * kBiasBytes, lane + 32 * i, v < -0x1p60f ? -0x1p60f : v > 0x1p60f ? 0x1p60f : v);
             }
             fence_async_shared();
@@ -337,6 +364,7 @@ __device__ __forceinline__ void describe(Item& it, const Walk* w) {
     it.u1 = w->u1;
     it.begins = w->u0 == w->first;
     it.ends = w->u1 == w->last + 1;
+    it.q0 = w->r.s.q0;
     it.T = w->r.T;
     it.base = w->r.s.base;
     it.L = w->r.s.L;
@@ -570,6 +598,62 @@ __device__ __forceinline__ void add_some(const uint32_t (&s)[32], float mul, int
     }
 }
 
+// A key that holds an infinity or a NaN makes NaN of a row of zeros as well, so that its sum may be NaN because of rows that add nothing.
+// The sums of such keys, one after the other, once more from where q and K lie, a row of the item's units a lane; the others stay.
+// (Out of line, looked for once an item: calls without any take as long in bf16 as without this, 1 % more in e4m3, and 5 % more where
+// an item has few units, 16 sequences of 32 rows 131 us, 138.  Told by a flag from q's loader, unit by unit, 4 %, and 16 % in mixed batches.)
+template <int D, bool E4M3>
+__device__ __noinline__ float again(const WeightsParams& p, const volatile Item& it, int tile, float total) {
+    const int r = threadIdx.x % kTile, lane = threadIdx.x % 32, box_log = 31 - __clz(p.box_rows), T = it.T, q0 = it.q0, h = it.h;
+    const int j = it.pair * kWeightsPair + tile * kTile + r, t_from = p.causal ? max(0, j - it.base) : 0;
+    const int t_to = p.window > 0 && j >= p.sinks ? static_cast<int>(min(static_cast<long long>(T), static_cast<long long>(j) - it.base + p.window)) : T;
+    const float mul = E4M3 ? kWeightsLog2e * it.scale[tile * kTile + r] : kWeightsLog2e;
+    const char* key = static_cast<const char*>(p.kv.k);
+    bool numbers = true;
+    const int pg = it.page[tile][r >> box_log], row = it.row[tile][r >> box_log] + (r & (p.box_rows - 1));
+    if (total != total && j < it.L && pg >= 0 && RA_CHECKED(paged_place_ok(p.kv, pg, h, row - h * p.kv.page), p.err, kSiteWeightsPlace)) {
+        key += (pg * p.kv.k_ps + static_cast<long long>(row) * D) * (E4M3 ? 1 : 2);
+        if (E4M3) numbers = fabsf(mul) < INFINITY;
+        else
+            for (int e = 0; e < D; ++e) numbers = numbers && (reinterpret_cast<const uint16_t*>(key)[e] & 0x7f80u) != 0x7f80u;
+    }
+    for (uint32_t bad = __ballot_sync(0xffffffffu, !numbers); bad; bad &= bad - 1u) {
+        const int of = __ffs(bad) - 1, from = __shfl_sync(0xffffffffu, t_from, of), to = __shfl_sync(0xffffffffu, t_to, of);
+        const char* k = reinterpret_cast<const char*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(key), of));
+        const float scale = __shfl_sync(0xffffffffu, mul, of);
+        float sum = 0.f;
+        for (int u = it.u0; u < it.u1; ++u) {
+            for (int c = lane; c < kTile; c += 32) {
+                const int in_unit = static_cast<int>(fdiv(static_cast<unsigned>(c), p.by_g)), t = (u << p.unit_log) + in_unit, head = h * p.g + c - in_unit * p.g;
+                if (in_unit >= p.unit_tokens || t < from || t >= to || !RA_CHECKED(paged_row_ok(p.kv, p.hq, q0 + t, head), p.err, kSiteWeightsRow)) continue;
+                const float lse = __ldg(p.lse + (q0 + t) * p.l_ts + head * p.l_hs);
+                if (lse == -INFINITY) continue;
+                const uint32_t* q = reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(p.q) + (q0 + t) * p.q_ts + head * p.q_hs);
+                float s = 0.f;
+                for (int e = 0; e < D / 2; ++e) {
+                    const uint32_t a = __ldg(q + e);
+                    float2 b;
+                    if (E4M3) {
+                        const uint32_t w = e4m3x2_f16x2(reinterpret_cast<const uint16_t*>(k)[e]);
+                        b = __half22float2(*reinterpret_cast<const __half2*>(&w));
+                    } else {
+                        const uint32_t w = reinterpret_cast<const uint32_t*>(k)[e];
+                        b = make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+                    }
+                    s = fmaf(__uint_as_float(a << 16), b.x, s);
+                    s = fmaf(__uint_as_float(a & 0xffff0000u), b.y, s);
+                }
+                sum += ex2(fmaf(s, scale, -lse * kWeightsLog2e));
+            }
+            if (__any_sync(0xffffffffu, sum != sum)) break;
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (lane == of) total = sum;
+    }
+    return total;
+}
+
 // Four warps: columns [64 half, 64 half + 64) of tile `tile`, a key a thread.
 template <int D, bool E4M3>
 __device__ void sum_role(const WeightsParams& p, int tile, int half, Shared& sh, uint32_t tmem, const WaitCtl& wc) {
@@ -645,6 +729,7 @@ __device__ void sum_role(const WeightsParams& p, int tile, int half, Shared& sh,
         total += sh.half[tile][r];
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.half_empty[tile]);
+        if (__any_sync(0xffffffffu, total != total)) total = again<D, E4M3>(p, it, tile, total);
         if (whole_item) {
             if (wp) *wp = (old != 0.f ? p.decay * old : 0.f) + total;
         } else {
@@ -680,6 +765,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1) weights_chunk_kerne
             mbar_init(&sh.q_full[i], 2);  // q, and -lse
             mbar_init(&sh.q_empty[i], 2);
         }
+        mbar_init(&sh.q_landed, 1);
         for (uint32_t i = 0; i < kRawSlots; ++i) {
             mbar_init(&sh.raw_full[i], 1);
             mbar_init(&sh.raw_empty[i], 4);
