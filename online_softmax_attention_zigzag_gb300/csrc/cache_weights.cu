@@ -35,14 +35,14 @@ __device__ __forceinline__ uint4 ldg128_stream(const void* p) {
 
 // Columns 2 * (lane % 4) and the next one of a block of 8 query rows: what their scores are compared with.
 struct Column {
-    float bias;    // lse in powers of two; +inf: adds nothing
+    float bias;    // lse in powers of two; -inf: adds nothing
     float mul;     // what a product is multiplied by for a score in powers of two, but for the key's scale
     int end, from;  // sees j < end, and j >= from or j < sinks
 };
 
 __device__ __forceinline__ Column column(const WeightsParams& p, const Seen& r, int h, int c) {
     Column x;
-    x.bias = INFINITY;
+    x.bias = -INFINITY;
     x.mul = kLog2e;
     x.end = 0;
     x.from = 0;
@@ -51,7 +51,7 @@ __device__ __forceinline__ Column column(const WeightsParams& p, const Seen& r, 
     const long long row = r.s.q0 + t;
     if (!RA_CHECKED(paged_row_ok(p.kv, p.hq, row, head), p.err, kSiteWeightsRow)) return x;
     const float lse = __ldg(p.lse + row * p.l_ts + head * p.l_hs);
-    x.bias = lse == -INFINITY ? INFINITY : lse * kLog2e;
+    x.bias = lse < -0x1p127f && lse > -INFINITY ? -0x1p127f : lse * kLog2e;  // (no other lse becomes -inf)
     x.end = p.causal ? min(r.s.L, r.s.base + t + 1) : r.s.L;
     x.from = p.window > 0 ? r.s.base + t - p.window + 1 : 0;
     return x;
@@ -241,7 +241,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<E4M3>()) weights_kerne
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const Column& y = col[c][e % 2];
-                    bool on = y.bias != INFINITY;
+                    bool on = y.bias != -INFINITY;
                     if (!whole) {
                         const int j = j0 + quad + 8 * (e / 2);
                         on = on && j < y.end && (j >= y.from || j < p.sinks);
@@ -360,7 +360,7 @@ __global__ void __launch_bounds__(kThreads, kWideBlocks) weights_wide_kernel(con
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const WideColumn& y = cs[8 * c + 2 * (lane % 4) + e % 2];
-                    bool on = y.bias != INFINITY;
+                    bool on = y.bias != -INFINITY;
                     if (!whole) {
                         const int j = j0 + quad + 8 * (e / 2);
                         on = on && j < y.end && (j >= y.from || j < p.sinks);
