@@ -513,8 +513,8 @@ int ringattn_cache_evict(const ra_paged_kv* kv, float* weights, long long weight
  *     (a cos - b sin, b cos + a sin), with cos = cos_sin[position, j], sin = cos_sin[position, rot/2 + j];
  *     q's rows are multiplied by q_scale.
  * Pairs are (j, j + rot/2), or (2j, 2j + 1) with interleaved = 1; elements from rot on are not turned.
- * Arithmetic is fp32 (a row whose squares add up to more than fp32 holds, |x| from about 2^60 on, has r = 0), rounded once.
- * With eps = 0 a row of zeros is 0 / 0: NaN.
+ * Arithmetic is fp32, rounded once.  With an eps below 2^-60 rows of every size are normed, however small or large (a row of zeros is
+ * 0 / 0 with eps = 0: NaN); from 2^-60 on, a row whose squares add up to more than fp32 holds, |x| from about 2^60 on, has r = 0.
  */
 typedef struct {
     void* q; /* [total, Hq, d] */

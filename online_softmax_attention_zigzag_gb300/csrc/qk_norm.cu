@@ -130,6 +130,33 @@ __device__ __forceinline__ float row_sum(float x) {
     return x;
 }
 
+// Rows whose mean(x^2) + eps is out of 2^-60 .. 2^60 (or NaN): their squares, or the sum of them, may leave fp32's normal numbers.  They are
+// left for a second look (FAR), in kernels of their own for an eps so small that it does not cover rows whose squares vanish: the look
+// costs the backward pass 8 to 11 us of 32k tokens' 346 to 458 (64 query and 8 KV heads, d = 128), the forward pass 2 of 203.
+constexpr float kFar = 0x1p-60f;
+__device__ __forceinline__ bool far_out(float mean) { return !(mean >= kFar && mean <= 0x1p60f); }
+// Such a row's x times a power of two `a` that brings the larger of its largest element and sqrt(eps) to about 1, and
+// 1 / sqrt(mean + eps) of that, so that x r is what it was.  A warp's lanes run together.
+template <int LPR>
+__device__ __forceinline__ float bring_in(float (&x)[8], float eps, float& a) {
+    uint32_t top = eps > 0.f ? ((__float_as_uint(eps) >> 23) + 127u) >> 1 : 0u;  // a biased exponent
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t e = __float_as_uint(x[i]) >> 23 & 0xffu;
+        top = max(top, e == 0xffu ? 0u : e);
+    }
+#pragma unroll
+    for (int o = 1; o < LPR; o *= 2) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    a = __uint_as_float(max(254u - top, 1u) << 23);
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        x[i] *= a;
+        ss = fmaf(x[i], x[i], ss);
+    }
+    return rsqrtf(fmaf(row_sum<LPR>(ss), 1.f / (8 * LPR), eps * a * a));
+}
+
 // What a block's threads do: blockIdx.y is a group of heads of q or of k, and a row's lanes take tokens
 // blocks_x * kNormThreads / LPR apart.
 struct Part {
@@ -143,7 +170,7 @@ __device__ __forceinline__ Part block_part(const NormParams& p) {
     return s;
 }
 
-template <int LPR, bool INTER>
+template <int LPR, bool INTER, bool FAR>
 __global__ void __launch_bounds__(kNormThreads) norm_kernel(const __grid_constant__ NormParams p) {
     constexpr int kTokens = kNormThreads / LPR;
     const int lane = threadIdx.x % LPR, slot = threadIdx.x / LPR;
@@ -175,15 +202,8 @@ __global__ void __launch_bounds__(kNormThreads) norm_kernel(const __grid_constan
             c[i] *= w[i] * p.scale[part.kind];
         }
         uint16_t* dst = static_cast<uint16_t*>(p.y.p[part.kind]) + t * p.y.ts[part.kind] + part.h0 * p.y.hs[part.kind];
-#pragma unroll
-        for (int h = 0; h < kNormHeads; ++h) {
-            float x[8], z[8], ss = 0.f;
-            unpack4(raw[h][0], x);
-            unpack4(raw[h][1], x + 4);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
-            const float r = rsqrtf(fmaf(row_sum<LPR>(ss), inv_d, p.eps));
-            if (!on || h >= part.heads || !RA_CHECKED(part.h0 + h < p.heads[part.kind], p.err, kSiteNormRow)) continue;
+        auto store = [&](int h, const float (&x)[8], float r) {
+            float z[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) z[i] = r * fmaf(x[i], c[i], at.turned ? x[pair_of<INTER>(i)] * s[i] : 0.f);
 #pragma unroll
@@ -192,11 +212,37 @@ __global__ void __launch_bounds__(kNormThreads) norm_kernel(const __grid_constan
                 pack4(z + 4 * k, o);
                 *reinterpret_cast<uint2*>(dst + h * p.y.hs[part.kind] + at.at[k]) = o;
             }
+        };
+        uint32_t later = 0;  // heads whose rows are far out
+#pragma unroll
+        for (int h = 0; h < kNormHeads; ++h) {
+            float x[8], ss = 0.f;
+            unpack4(raw[h][0], x);
+            unpack4(raw[h][1], x + 4);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
+            const float mean = fmaf(row_sum<LPR>(ss), inv_d, p.eps);
+            if (!on || h >= part.heads || !RA_CHECKED(part.h0 + h < p.heads[part.kind], p.err, kSiteNormRow)) continue;
+            if (FAR && far_out(mean)) later |= 1u << h;
+            else store(h, x, rsqrtf(mean));
+        }
+        if (FAR && __any_sync(0xffffffffu, later != 0u)) {
+#pragma unroll 1
+            for (int h = 0; h < part.heads; ++h) {
+                const bool mine = later >> h & 1u;
+                float x[8] = {}, a;
+                if (mine) {
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) unpack4(*reinterpret_cast<const uint2*>(src + h * p.x.hs[part.kind] + at.at[k]), x + 4 * k);
+                }
+                const float r = bring_in<LPR>(x, p.eps, a);
+                if (mine) store(h, x, r);
+            }
         }
     }
 }
 
-template <int LPR, bool INTER, bool DY32, bool DX32>
+template <int LPR, bool INTER, bool DY32, bool DX32, bool FAR>
 __global__ void __launch_bounds__(kNormThreads) norm_bwd_kernel(const __grid_constant__ NormParams p) {
     using QY = typename Quad<DY32>::T;
     using QX = typename Quad<DX32>::T;
@@ -228,6 +274,9 @@ __global__ void __launch_bounds__(kNormThreads) norm_bwd_kernel(const __grid_con
                     grad[h][k] = *reinterpret_cast<const QY*>(dy + h * p.y.hs[part.kind] + at.at[k]);
                 }
             }
+        // (the loads stay before the arithmetic, which the compiler otherwise mixes with them for the second look's sake: bf16 gradients
+        // 367 us, 357 so)
+        if (FAR) asm volatile("" ::: "memory");
         const int pos = __ldg(p.position + t);
         const bool on = t0 + slot < p.total && pos >= 0 && pos < p.n_pos;
         float c[8], s[8];
@@ -239,6 +288,22 @@ __global__ void __launch_bounds__(kNormThreads) norm_bwd_kernel(const __grid_con
         }
         typename Quad<DX32>::E* dst =
             static_cast<typename Quad<DX32>::E*>(p.g.p[part.kind]) + t * p.g.ts[part.kind] + part.h0 * p.g.hs[part.kind];
+        // u: dout; then dout turned back, g, and u
+        auto turn_back = [&](float (&u)[8], float (&g)[8]) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) g[i] = fmaf(u[i], c[i], at.turned ? u[pair_of<INTER>(i)] * s[i] : 0.f);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) u[i] = g[i] * w[i];
+        };
+        auto store = [&](int h, const float (&x)[8]) {
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                QX o;
+                pack4(x + 4 * k, o);
+                *reinterpret_cast<QX*>(dst + h * p.g.hs[part.kind] + at.at[k]) = o;
+            }
+        };
+        uint32_t later = 0;  // heads whose rows are far out
 #pragma unroll
         for (int h = 0; h < kNormHeads; ++h) {
             float x[8], g[8], u[8], ss = 0.f, ux = 0.f;
@@ -246,27 +311,48 @@ __global__ void __launch_bounds__(kNormThreads) norm_bwd_kernel(const __grid_con
             unpack4(raw[h][1], x + 4);
             unpack4(grad[h][0], u);
             unpack4(grad[h][1], u + 4);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) g[i] = fmaf(u[i], c[i], at.turned ? u[pair_of<INTER>(i)] * s[i] : 0.f);
+            turn_back(u, g);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                u[i] = g[i] * w[i];
                 ss = fmaf(x[i], x[i], ss);
                 ux = fmaf(u[i], x[i], ux);
             }
-            const float r = rsqrtf(fmaf(row_sum<LPR>(ss), inv_d, p.eps));
+            const float mean = fmaf(row_sum<LPR>(ss), inv_d, p.eps), r = rsqrtf(mean);
             const float m = row_sum<LPR>(ux) * inv_d * r * r;
-            if (!on || h >= part.heads || !RA_CHECKED(part.h0 + h < p.heads[part.kind], p.err, kSiteNormRow)) continue;
+            const bool far = FAR && far_out(mean), here = on && h < part.heads && RA_CHECKED(part.h0 + h < p.heads[part.kind], p.err, kSiteNormRow);
+            if (here && far) later |= 1u << h;
+            if (!here || far) continue;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 dw[i] = fmaf(g[i], x[i] * r, dw[i]);
                 u[i] = r * fmaf(-m, x[i], u[i]);
             }
+            store(h, u);
+        }
+        if (FAR && __any_sync(0xffffffffu, later != 0u)) {
+#pragma unroll 1
+            for (int h = 0; h < part.heads; ++h) {
+                const bool mine = later >> h & 1u;
+                float x[8] = {}, g[8], u[8] = {}, ux = 0.f, a;
+                if (mine) {
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                QX o;
-                pack4(u + 4 * k, o);
-                *reinterpret_cast<QX*>(dst + h * p.g.hs[part.kind] + at.at[k]) = o;
+                    for (int k = 0; k < 2; ++k) {
+                        unpack4(*reinterpret_cast<const uint2*>(src + h * p.x.hs[part.kind] + at.at[k]), x + 4 * k);
+                        unpack4(*reinterpret_cast<const QY*>(dy + h * p.y.hs[part.kind] + at.at[k]), u + 4 * k);
+                    }
+                }
+                turn_back(u, g);
+                const float r = bring_in<LPR>(x, p.eps, a);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) ux = fmaf(u[i], x[i], ux);
+                const float m = row_sum<LPR>(ux) * inv_d * r * r;
+                if (!mine) continue;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    dw[i] = fmaf(g[i], x[i] * r, dw[i]);
+                    u[i] = r * fmaf(-m, x[i], u[i]) * a;  // (r of x is a times that of a x, which may be more than fp32 holds)
+                }
+                store(h, u);
             }
         }
     }
@@ -307,14 +393,19 @@ __global__ void __launch_bounds__(256) norm_dw_kernel(const __grid_constant__ No
     }
 }
 
-template <int LPR, bool INTER>
+template <int LPR, bool INTER, bool FAR>
+void go(const NormParams& p, dim3 grid, cudaStream_t s) {
+    norm_kernel<LPR, INTER, FAR><<<grid, kNormThreads, 0, s>>>(p);
+}
+
+template <int LPR, bool INTER, bool FAR>
 void go_bwd(const NormParams& p, dim3 grid, bool dy_f32, bool dx_f32, cudaStream_t s) {
     if (dy_f32) {
-        if (dx_f32) norm_bwd_kernel<LPR, INTER, true, true><<<grid, kNormThreads, 0, s>>>(p);
-        else norm_bwd_kernel<LPR, INTER, true, false><<<grid, kNormThreads, 0, s>>>(p);
+        if (dx_f32) norm_bwd_kernel<LPR, INTER, true, true, FAR><<<grid, kNormThreads, 0, s>>>(p);
+        else norm_bwd_kernel<LPR, INTER, true, false, FAR><<<grid, kNormThreads, 0, s>>>(p);
     } else {
-        if (dx_f32) norm_bwd_kernel<LPR, INTER, false, true><<<grid, kNormThreads, 0, s>>>(p);
-        else norm_bwd_kernel<LPR, INTER, false, false><<<grid, kNormThreads, 0, s>>>(p);
+        if (dx_f32) norm_bwd_kernel<LPR, INTER, false, true, FAR><<<grid, kNormThreads, 0, s>>>(p);
+        else norm_bwd_kernel<LPR, INTER, false, false, FAR><<<grid, kNormThreads, 0, s>>>(p);
     }
 }
 
@@ -331,13 +422,11 @@ int launch_qk_norm_rope(NormParams p, int sms, cudaStream_t stream) {
     const int groups = p.groups[0] + p.groups[1];
     p.blocks_x = norm_blocks(p.total, groups, p.d, sms * kNormBlocksPerSm);
     const dim3 grid(p.blocks_x, groups);
-    if (p.d == 128) {
-        if (p.interleaved) norm_kernel<16, true><<<grid, kNormThreads, 0, stream>>>(p);
-        else norm_kernel<16, false><<<grid, kNormThreads, 0, stream>>>(p);
-    } else {
-        if (p.interleaved) norm_kernel<8, true><<<grid, kNormThreads, 0, stream>>>(p);
-        else norm_kernel<8, false><<<grid, kNormThreads, 0, stream>>>(p);
-    }
+    const bool far = p.eps < kFar;
+#define RA_GO(LPR, INTER) far ? go<LPR, INTER, true>(p, grid, stream) : go<LPR, INTER, false>(p, grid, stream)
+    if (p.d == 128) p.interleaved ? (RA_GO(16, true)) : (RA_GO(16, false));
+    else p.interleaved ? (RA_GO(8, true)) : (RA_GO(8, false));
+#undef RA_GO
     return cudaGetLastError() == cudaSuccess ? 0 : -4;
 }
 
@@ -345,14 +434,15 @@ int launch_qk_norm_rope_bwd(NormParams p, bool dy_f32, bool dx_f32, int sms, cud
     const int groups = p.groups[0] + p.groups[1];
     p.blocks_x = norm_blocks(p.total, groups, p.d, sms * kNormBwdBlocksPerSm);
     const dim3 grid(p.blocks_x, groups);
+    const bool far = p.eps < kFar;
+#define RA_GO(LPR, INTER) far ? go_bwd<LPR, INTER, true>(p, grid, dy_f32, dx_f32, stream) : go_bwd<LPR, INTER, false>(p, grid, dy_f32, dx_f32, stream)
     if (p.total == 0) {  // (no rows: the weights' gradients are sums of nothing)
     } else if (p.d == 128) {
-        if (p.interleaved) go_bwd<16, true>(p, grid, dy_f32, dx_f32, stream);
-        else go_bwd<16, false>(p, grid, dy_f32, dx_f32, stream);
+        p.interleaved ? (RA_GO(16, true)) : (RA_GO(16, false));
     } else {
-        if (p.interleaved) go_bwd<8, true>(p, grid, dy_f32, dx_f32, stream);
-        else go_bwd<8, false>(p, grid, dy_f32, dx_f32, stream);
+        p.interleaved ? (RA_GO(8, true)) : (RA_GO(8, false));
     }
+#undef RA_GO
     if (cudaGetLastError() != cudaSuccess) return -4;
     if (!p.dw[0] && !p.dw[1]) return 0;
     cudaLaunchConfig_t cfg = {};
