@@ -562,8 +562,9 @@ def cache_evict(k_cache, v_cache, weights, block_table, kv_len, keep, kv_len_out
     and weights.  keep and kv_len_out [batch] int32 (kv_len_out may be kv_len); kept [batch, Hkv, max_keep] int32
     receives where each of them was (-1 behind the last).  The cache as for :func:`cache_append`, weights as for
     :func:`cache_weights`."""
-    if (sinks | recent) >> 31:
-        _ints(sinks=sinks, recent=recent)
+    max_keep = kept.shape[-1] if kept.dim() else 0
+    if (sinks | recent | max_keep) >> 31:
+        _ints(sinks=sinks, recent=recent, max_keep=max_keep)
     dev = torch.cuda.current_device()
     h, _, kv = _paged(k_cache, v_cache, k_scale, v_scale, block_table, None, kv_len, 0, dev)
     wp, w0 = _weights(weights, k_cache, dev)
@@ -572,11 +573,8 @@ def cache_evict(k_cache, v_cache, weights, block_table, kv_len, keep, kv_len_out
         _strided(t, name, torch.int32, dev, dim)
         if t.shape[0] != batch or not t.is_contiguous():
             raise ValueError("keep and kv_len_out must be [batch], kept [batch, Hkv, max_keep], contiguous")
-    _, heads, max_keep = kept.shape
-    if heads != h:
+    if kept.shape[1] != h:
         raise ValueError("kept must be [batch, Hkv, max_keep] with the cache's Hkv")
-    if max_keep >> 31:
-        _ints(max_keep=max_keep)
     _check("ringattn_cache_evict", (_lib or lib()).ringattn_cache_evict(
         kv, wp, w0, keep.data_ptr(), max_keep, sinks, recent, kv_len_out.data_ptr(), kept.data_ptr(),
         _raw_stream(stream, dev)))
@@ -638,12 +636,10 @@ def _qk_norm(q, k, position, cos_sin, q_weight, k_weight, eps, q_scale, interlea
     n_pos, rot = st
     if n_pos >= 2 ** 31:
         raise ValueError("cos_sin must have fewer than 2^31 rows")
-    try:
-        return (sq, sk), _pack_qk_norm(wq, wk, cos_sin.data_ptr(), position.data_ptr(), total, hq, sk[1], d, rot, n_pos, wt is f32,
-                                       interleaved, eps, q_scale)
-    except (struct.error, OverflowError):
+    if interleaved >> 31:
         _ints(interleaved=interleaved)
-        raise ValueError(f"eps and q_scale must be fp32 numbers, got {eps} and {q_scale}") from None
+    return (sq, sk), _pack_qk_norm(wq, wk, cos_sin.data_ptr(), position.data_ptr(), total, hq, sk[1], d, rot, n_pos, wt is f32,
+                                   interleaved, eps, q_scale)
 
 
 def qk_norm_rope(q, k, q_out, k_out, position, cos_sin, *, q_weight=None, k_weight=None, eps=1e-6, q_scale=1.0, interleaved=0,
