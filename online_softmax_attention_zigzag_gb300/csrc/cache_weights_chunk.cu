@@ -246,26 +246,13 @@ __device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy
 // nothing anyhow, and where lse is beyond, fp32 scores are whole trillions apart.
 __device__ __forceinline__ float held_scale(float scale) { return scale < 0x1p-60f ? 0x1p-60f : scale; }
 
-// Zeros in place of rows of q (lane + 32 i for bit i of `out`), once the unit has landed; false if it has not in time.
-template <int BOXES>
-__device__ __noinline__ bool leave_out(uint32_t tile, Shared& sh, uint32_t landed, uint32_t out, int* err, uint64_t timeout_ns) {
-    const WaitCtl wc{&sh.abort_flag, err, timeout_ns};
-    if (!__all_sync(0xffffffffu, mbar_wait(&sh.q_landed, landed & 1u, wc, 32))) {
-        drain_wait(&sh.q_landed, landed & 1u, timeout_ns);
-        return false;
-    }
-    for (int i = 0; i < 4; ++i)
-        for (int k = 0; k < BOXES * 8 && (out >> i & 1u); ++k)
-            sts128(tile + k / 8 * (kTile * 128) + (threadIdx.x % 32 + 32 * i) * 128 + k % 8 * 16, 0, 0, 0, 0);
-    return true;
-}
-
 // One warp.  The next unit's lse is on its way while a unit is handed on (8 rows of 16 sequences 123 us without, 108 so), and a slot that
 // holds the unit already, where only a few see each pair, is handed on as it is (32 rows 140 us without, 123).
 // A row whose lse is -inf adds nothing: with zeros in place of its q, and -2^60 for -lse, its weights are 0 whatever it holds (but for
-// keys that hold no numbers: `again`).
-template <int D, bool E4M3>
-__device__ void q_role(const WeightsParams& p, const CUtensorMap* tq, uint32_t smem, Shared& sh, const long long* sums, const WaitCtl& wc) {
+// keys that hold no numbers: `again`).  The loop that sees to such rows (OUT) goes on from unit `first`, where the one that does not
+// has come to one and returns false: in one loop 16 sequences of 32 rows in e4m3, none of them such a row, took 270 us, 254 so.
+template <int D, bool E4M3, bool OUT>
+__device__ __forceinline__ bool q_units(const WeightsParams& p, const CUtensorMap* tq, uint32_t smem, Shared& sh, const long long* sums, const WaitCtl& wc, uint32_t& first) {
     using C = Cfg<D, E4M3>;
     const int lane = threadIdx.x % 32;
     const uint32_t bytes = static_cast<uint32_t>(p.unit_tokens * p.g) * 128u * C::kBoxes;
@@ -298,25 +285,30 @@ __device__ void q_role(const WeightsParams& p, const CUtensorMap* tq, uint32_t s
     bool more = walk_begin(p, sums, w), ok = true;
     uint32_t n = 0, landed = 0;
     Unit now = {}, held[2] = {{-1, 0, 0, 0, 0}, {-1, 0, 0, 0, 0}};  // held: what the slots hold, the next one's first
+    auto after = [&](const Unit& a) {
+        if (a.u + 1 < w.u1) return unit(w, a.u + 1);
+        more = walk_next(p, w);
+        return more ? unit(w, w.u0) : a;
+    };
     float x[4];
-    if (more) {
-        now = unit(w, w.u0);
-        load(now, x);
-    }
+    if (more) now = unit(w, w.u0);
+    if (OUT)
+        for (; n < first && more; ++n) now = after(now);
+    if (more) load(now, x);
     while (more) {
-        Unit next = now;
         float y[4];
-        if (now.u + 1 < w.u1) next = unit(w, now.u + 1);
-        else if ((more = walk_next(p, w))) next = unit(w, w.u0);
+        const Unit next = after(now);
         if (more) load(next, y);
         ok = take(sh.q_empty, n, kQSlots, wc);
         if (!ok) break;
         const uint32_t s = n % kQSlots;
         if (held[0].b != now.b || held[0].h != now.h || held[0].u != now.u) {
-            uint32_t out = 0;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) out |= x[i] == -INFINITY ? 1u << i : 0u;
-            uint64_t* bar = __any_sync(0xffffffffu, out != 0u) ? &sh.q_landed : &sh.q_full[s];
+            const bool out = __any_sync(0xffffffffu, x[0] == -INFINITY || x[1] == -INFINITY || x[2] == -INFINITY || x[3] == -INFINITY);
+            if (!OUT && out) {
+                first = n;
+                return false;
+            }
+            uint64_t* bar = OUT && out ? &sh.q_landed : &sh.q_full[s];
             if (lane == 0) {
                 mbar_arrive_expect_tx(bar, bytes);
                 int tok = now.q0 + (now.u << p.unit_log);
@@ -325,10 +317,17 @@ __device__ void q_role(const WeightsParams& p, const CUtensorMap* tq, uint32_t s
                     tma_load_3d(q_base + s * C::kTileBytes + i * C::kBoxBytes, tq, bar, i * 64, now.h * p.g, tok, keep);
             }
             __syncwarp();
-            if (bar == &sh.q_landed) {
-                ok = leave_out<C::kBoxes>(q_base + s * C::kTileBytes, sh, landed++, out, p.err, p.timeout_ns);
-                if (!ok) break;
-                if (lane == 0) mbar_arrive(&sh.q_full[s]);
+            if (OUT && out) {
+                ok = __all_sync(0xffffffffu, mbar_wait(&sh.q_landed, landed & 1u, wc, 32));
+                if (!ok) {
+                    drain_wait(&sh.q_landed, landed & 1u, wc.timeout_ns);
+                    break;
+                }
+                ++landed;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    for (int k = 0; k < C::kBoxes * 8 && x[i] == -INFINITY; ++k)
+                        sts128(q_base + s * C::kTileBytes + k / 8 * C::kBoxBytes + (lane + 32 * i) * 128 + k % 8 * 16, 0, 0, 0, 0);
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -337,6 +336,7 @@ __device__ void q_role(const WeightsParams& p, const CUtensorMap* tq, uint32_t s
             }
             fence_async_shared();
             __syncwarp();
+            if (OUT && out && lane == 0) mbar_arrive(&sh.q_full[s]);
         } else if (lane == 0) {
             mbar_arrive(&sh.q_full[s]);
         }
@@ -349,6 +349,16 @@ __device__ void q_role(const WeightsParams& p, const CUtensorMap* tq, uint32_t s
         for (int i = 0; i < 4; ++i) x[i] = y[i];
     }
     if (!ok && lane == 0) drain_ring(sh.q_full, n, kQSlots, wc);  // copies in flight land before the block ends
+    return true;
+}
+template <int D, bool E4M3>
+__device__ __noinline__ void q_units_out(const WeightsParams& p, const CUtensorMap* tq, uint32_t smem, Shared& sh, const long long* sums, uint32_t first) {
+    q_units<D, E4M3, true>(p, tq, smem, sh, sums, WaitCtl{&sh.abort_flag, p.err, p.timeout_ns}, first);
+}
+template <int D, bool E4M3>
+__device__ void q_role(const WeightsParams& p, const CUtensorMap* tq, uint32_t smem, Shared& sh, const long long* sums, const WaitCtl& wc) {
+    uint32_t first = 0;
+    if (!q_units<D, E4M3, false>(p, tq, smem, sh, sums, wc, first)) q_units_out<D, E4M3>(p, tq, smem, sh, sums, first);
 }
 
 // Hands an item on to the warps that issue and add up (null: no more); one warp of the loaders.
@@ -600,8 +610,8 @@ __device__ __forceinline__ void add_some(const uint32_t (&s)[32], float mul, int
 
 // A key that holds an infinity or a NaN makes NaN of a row of zeros as well, so that its sum may be NaN because of rows that add nothing.
 // The sums of such keys, one after the other, once more from where q and K lie, a row of the item's units a lane; the others stay.
-// (Out of line, looked for once an item: calls without any take as long in bf16 as without this, 1 % more in e4m3, and 5 % more where
-// an item has few units, 16 sequences of 32 rows 131 us, 138.  Told by a flag from q's loader, unit by unit, 4 %, and 16 % in mixed batches.)
+// (Out of line, and looked for once an item: the times of calls without any stay within 1 %, but for items of few units in e4m3, 16
+// sequences of 32 rows 248 us, 254.  Told by a flag from q's loader, unit by unit, 4 % everywhere and 16 % in mixed batches.)
 template <int D, bool E4M3>
 __device__ __noinline__ float again(const WeightsParams& p, const volatile Item& it, int tile, float total) {
     const int r = threadIdx.x % kTile, lane = threadIdx.x % 32, box_log = 31 - __clz(p.box_rows), T = it.T, q0 = it.q0, h = it.h;
