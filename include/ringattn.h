@@ -466,7 +466,8 @@ int ringattn_paged_workspace_bytes(int total, int batch, int Hq, int Hkv, int d,
  * weights: [n_pages, Hkv, page_size] fp32 beside the pool's k and v; pages weights_page_stride apart
  *     (a multiple of 4, at least Hkv * page_size, at most 2^36), 16-byte aligned.
  * decay: in [0, 1]; 1 adds up, 0 does not read what was there.
- * q, kv, Hq, max_q, causal, window, sinks, workspace: as for ringattn_fwd_paged; lse [total, Hq] fp32 as it
+ * q, kv, Hq, max_q, causal, window, sinks, workspace: as for ringattn_fwd_paged (max_q picks one kernel for the whole batch: single
+ *     tokens and a long chunk are faster in two calls); lse [total, Hq] fp32 as it
  *     left it (any lse does: a key's weight is exp(q . k - lse)); a row whose lse is -inf adds nothing, whatever it
  *     and the keys hold.
  *     V is not read.  kv->v has to be given all the same.

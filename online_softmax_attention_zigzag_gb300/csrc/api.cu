@@ -1031,7 +1031,7 @@ int ringattn_cache_weights(const void* q, long long q_token_stride, long long q_
     while ((2 << p.unit_log) * p.g <= 128) ++p.unit_log;
     p.unit_tokens = 1 << p.unit_log;
     p.box_rows = std::gcd(p.kv.page, ra::kPagedTile);
-    // what an item costs beside its units, in units: 12 sequences of 1 to 2048 rows in e4m3 228 us with none, 153 with one, 127 with
+    // what an item costs beside its units, in units: 12 sequences of 1 to 1023 rows in e4m3 228 us with none, 153 with one, 127 with
     // two, 131 with three; 8 prompts of 500 to 900 rows in bf16 52, 52, 50, 52
     p.item_units = 2;
     CUtensorMap tk = {}, tq = {};

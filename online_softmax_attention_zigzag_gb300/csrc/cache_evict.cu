@@ -10,10 +10,10 @@
 // The i-th of the positions that stay is at i or behind it, and they move in order, so packing works in place: what a cluster
 // has read of a round of rows before it writes them, it does not need again, and the rows behind lie behind.
 //
-// 16 sequences of 4k to 16k positions, 8 KV heads, 2k kept, bf16: 65 us, 4.2 TB/s of what it has to read and write.  Selecting is a
-// chain of latencies (three digits and a list, each with two exchanges in the cluster); packing takes 50, as long as a plain
-// gather of such rows, 256 bytes one in eight.  One sequence of 128k in e4m3, 16k kept: 46 us, selecting 20, then rounds in which
-// blocks of a cluster wait for each other; 64k kept in bf16 142, 3.9 TB/s.
+// 16 sequences of 4k to 16k positions, 8 KV heads, 2k kept, bf16: 68 us out of a flushed L2 (64 without), 4.1 TB/s of what it has to
+// read and write.  Selecting is a chain of latencies (three digits and a list, each with two exchanges in the cluster); packing takes
+// 46, about what a plain gather of such rows does, 256 bytes one in eight.  One sequence of 128k in e4m3, 16k kept: 46 us,
+// selecting 19, then rounds in which blocks of a cluster wait for each other; 64k kept in bf16 144, 3.8 TB/s.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
@@ -29,8 +29,8 @@ constexpr int kCluster = 8;  // most blocks of a (sequence, KV head)
 constexpr int kKeys = 16;  // neighbouring positions of a thread, all on one page
 constexpr int kDigit = 11;  // bits; 32 = 11 + 11 + 10
 constexpr int kBins = 1 << kDigit;
-constexpr int kDirect = 512;  // and up to which they are ranked one against the other
-constexpr int kList = 5119;  // keys with the first digit in question that a block lists
+constexpr int kDirect = 512;  // as many keys that are left after the first digit are ranked one against the other
+constexpr int kList = 5119;  // as many keys with the first digit in question a block lists
 
 __device__ __forceinline__ uint32_t order(float w) {
     const uint32_t u = __float_as_uint(w);
@@ -504,7 +504,9 @@ __global__ void __launch_bounds__(kMoveThreads, kMoveBlocks) evict_move_kernel(c
 }  // namespace
 
 namespace {
-// Blocks of a cluster: a power of two, so many that `heads` clusters come to about `most` blocks, and each has work.
+// Blocks of a cluster: a power of two, so many that `heads` clusters come to about `most` blocks, and each has work: by the most
+// that there may be, since the lengths are on the device.  A table much longer than its sequences costs them some exchanges: one
+// of 700 positions, or five of up to 700, 21 us with a table for 128k, 17 with one of their size.
 int cluster_of(long long heads, long long most, long long rows, int least) {
     int n = 1;
     while (n < kCluster && 2 * n * heads <= most && rows > static_cast<long long>(n) * least) n *= 2;

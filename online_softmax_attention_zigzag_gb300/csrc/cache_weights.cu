@@ -131,6 +131,8 @@ struct Keys {
 // Blocks of an SM, which share its registers.  bf16 keeps the loads of 16 warps in flight (64 x 16k tokens: 188 us with two, 195
 // with three).  In e4m3 a warp has half as many bytes in flight and turns codes into fp16 meanwhile: 8 x 128k take 190 us with
 // three, 236 with two, 222 with four, which spill; loading a group ahead, or two at a time, left no registers for the third: 243, 236.
+// All that was measured with one block of columns.  Two of them (9 to 16 rows) spill with three as well, 244 bytes a thread at d = 128:
+// 8 sequences of 100k to 128k with two tokens of 8 heads take 265 us for a floor of 158, 64 of up to 16k 148 for 84.
 template <bool E4M3>
 constexpr int blocks_per_sm() { return E4M3 ? 3 : 2; }
 
